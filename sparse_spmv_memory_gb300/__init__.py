@@ -12,7 +12,8 @@ must exist: build it with ``__graft_entry__.build()`` or
 The operation (SparseDecoding, aimodeling.com article, "The Kernel Is the
 Other Half of the Answer"): y = W x for one token, with W kept N:M-sparse
 (2:4, 4:8, 8:16, 16:32) and stored as compact fp16 values plus one 32-bit
-mask word per 32 input columns.
+mask word per 32 input columns.  ``decode`` adds the operators around those
+products in a step of speculative decoding (``include/nm_decode.h``).
 """
 from __future__ import annotations
 
@@ -31,6 +32,8 @@ __all__ = [
     "nm_spmv_swiglu", "nm_spmm_prefill", "nm_spmm_prefill_variant_count",
     "nm_spmm_prefill_workspace_bytes", "nm_spmm_prefill_plan", "nm_wait_timeouts",
     "nm_prefill_stall_selftest",
+    "nm_rope_inv_freq", "nm_rope_append", "nm_cache_read", "nm_tree_attention",
+    "nm_tree_attention_workspace_bytes", "nm_tree_verify",
 ]
 
 NM_OK = 0
@@ -111,6 +114,7 @@ def _declare(L: ctypes.CDLL) -> ctypes.CDLL:
         f = getattr(L, name)
         f.argtypes = args
         f.restype = res
+    decode.declare(L)
     return L
 
 
@@ -473,3 +477,10 @@ def nm_check_masks_noalloc(masks, cols: int, stream=None) -> int:
     if r < 0:
         raise NMError(-r, "nm_check_masks_noalloc")
     return r
+
+
+# The operators around the products in a step of speculative decoding.
+from . import decode  # noqa: E402
+from .decode import (  # noqa: E402
+    nm_cache_read, nm_rope_append, nm_rope_inv_freq, nm_tree_attention,
+    nm_tree_attention_workspace_bytes, nm_tree_verify)

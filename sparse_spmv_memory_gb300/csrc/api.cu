@@ -13,16 +13,11 @@
 namespace nmk {
 
 // ---- per-device attributes, queried once ------------------------------------
-struct DeviceInfo {
-  int sms;
-  int smem_optin;  // bytes of dynamic shared memory a block may opt into
-};
-
 static constexpr int kMaxDevices = 64;
 static DeviceInfo g_info[kMaxDevices];
 static std::atomic<int> g_info_ready[kMaxDevices];
 
-static cudaError_t device_info(DeviceInfo* out) {
+cudaError_t device_info(DeviceInfo* out) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;

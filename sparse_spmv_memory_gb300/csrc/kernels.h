@@ -201,6 +201,13 @@ inline cudaError_t launch_kernel(Kernel kernel, int grid, int block, size_t smem
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// Per-device attributes, queried once (api.cu).
+struct DeviceInfo {
+  int sms;
+  int smem_optin;  // bytes of dynamic shared memory a block may opt into
+};
+cudaError_t device_info(DeviceInfo* out);
+
 // Sets the dynamic shared memory limit of `func` to the device maximum once
 // per device.
 cudaError_t ensure_max_smem(const void* func, int* done_flags, int max_devices);

@@ -1,0 +1,619 @@
+"""GPU parity of the speculative-decoding operators (nm_rope_append,
+nm_cache_read, nm_tree_attention, nm_tree_verify) against 64-bit references."""
+from __future__ import annotations
+
+import random
+
+import numpy as np
+import pytest
+
+import decode_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+KINDS = ["fp16", "e4m3", "int8"]
+NAN = float("nan")
+
+
+@pytest.fixture(scope="module")
+def nm():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from sparse_spmv_memory_gb300 import _build
+    _build.build()
+    import sparse_spmv_memory_gb300 as m
+    m.lib()
+    return m
+
+
+def cuda(*ts):
+    out = tuple(None if t is None else t.cuda() for t in ts)
+    return out if len(out) > 1 else out[0]
+
+
+def within(got, want, tol, what):
+    got = got.double().cpu()
+    inf = torch.isinf(want)
+    assert torch.equal(got[inf], want[inf]), f"{what}: infinities differ"
+    err = (got - want).abs()
+    bad = ~(err <= tol) & ~inf
+    assert not bad.any(), (f"{what}: {int(bad.sum())} of {bad.numel()} beyond tolerance, worst ratio "
+                           f"{float((err / tol)[bad].max()):.3g}, first {bad.nonzero()[0].tolist()}")
+
+
+# ---- attention ---------------------------------------------------------------------
+def tree_masks(n, rnd):
+    seen = []
+    for i in range(n):
+        seen.append((seen[rnd.randrange(i)] if i else 0) | (1 << i))
+    return seen
+
+
+def signed(masks):
+    return torch.tensor([m - (1 << 64) if m >> 63 else m for m in masks], dtype=torch.int64)
+
+
+class Batch:
+    """Inputs of one attention call on the CPU, and the call."""
+
+    def __init__(self, kind, ctx, nodes, q_heads, kv_heads, dim, page, seed=1, masks="tree",
+                 q_scale=2.0, spread=1.0, spoil=True):
+        gen, rnd = torch.Generator().manual_seed(seed), random.Random(seed)
+        self.ctx, self.nodes, self.page = ctx, nodes, page
+        need = [max(1, -(-(c + n) // page)) for c, n in zip(ctx, nodes)]
+        pages = sum(need) + 2
+        order = torch.randperm(pages, generator=gen).to(torch.int32)
+        self.table = torch.full((len(ctx), max(need)), -1, dtype=torch.int32)
+        at = 0
+        for s, m in enumerate(need):
+            self.table[s, :m] = order[at:at + m]
+            at += m
+        self.k, self.v, self.ks, self.vs = ref.random_cache(kind, pages, kv_heads, page, dim, gen,
+                                                            spread)
+        self.start = [sum(nodes[:s]) for s in range(len(nodes) + 1)]
+        self.masks = None if masks is None else [m for n in nodes for m in tree_masks(n, rnd)]
+        T = sum(nodes)
+        self.q = (torch.randn((T, q_heads, dim), generator=gen) * q_scale).half()
+        self.scale = dim ** -0.5
+        self.clean = (self.k.clone(), self.v.clone())
+        if spoil:  # whatever lies behind the sequences' ends is never used
+            for s in range(len(ctx)):
+                end = ctx[s] + nodes[s]
+                for j in range(end, need[s] * page):
+                    self.set_row(s, j, NAN)
+
+    def place(self, s, j):
+        return int(self.table[s, j // self.page]), j % self.page
+
+    def set_row(self, s, j, x, head=slice(None), which="kv"):
+        p, o = self.place(s, j)
+        for name in which:
+            cache, scale = (self.k, self.ks) if name == "k" else (self.v, self.vs)
+            if scale is None:
+                cache[p, head, o] = x
+            else:
+                scale[p, head, o] = x
+
+    def run(self, nm, **kw):
+        k, v, ks, vs = cuda(self.k, self.v, self.ks, self.vs)
+        mask = None if self.masks is None else signed(self.masks).cuda()
+        return nm.nm_tree_attention(
+            self.q.cuda(), k, v, self.table.cuda(),
+            torch.tensor(self.ctx, dtype=torch.int32).cuda(),
+            torch.tensor(self.start, dtype=torch.int32).cuda(), max(1, max(self.nodes)),
+            tree_mask=mask, k_scale=ks, v_scale=vs, scale=self.scale, **kw)
+
+    def want(self):
+        def clean(x, scale):  # the reference never reads spoilt rows either, but 0 * nan would
+            return x if scale is not None else torch.nan_to_num(x, 0.0)
+        ks = None if self.ks is None else torch.nan_to_num(self.ks, 0.0)
+        vs = None if self.vs is None else torch.nan_to_num(self.vs, 0.0)
+        return ref.attention(self.q, clean(self.k, ks), clean(self.v, vs), ks, vs, self.table,
+                             self.ctx, self.start, self.masks, self.scale)
+
+    def check(self, nm, what, **kw):
+        out, lse = self.run(nm, **kw)
+        torch.cuda.synchronize()
+        o, l, to, tl = self.want()
+        within(lse, l, tl, what + " lse")
+        within(out, o, to, what + " out")
+        return out, lse
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("ctx,nodes", [
+    ([0], [1]), ([1], [1]), ([7], [1]), ([500], [1]), ([129], [2]), ([63, 64, 65], [3, 1, 5]),
+    ([0, 1000, 17], [8, 8, 8]), ([256, 0, 300, 5], [16, 33, 1, 20]), ([1500], [64]),
+    ([40] * 9, [4] * 9), ([3000, 2], [7, 1])])
+def test_attention_lengths(nm, kind, ctx, nodes):
+    Batch(kind, ctx, nodes, 16, 4, 128, 16).check(nm, f"{kind} ctx {ctx} nodes {nodes}")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("q_heads,kv_heads,dim", [(1, 1, 64), (7, 1, 64), (28, 4, 64), (8, 8, 128),
+                                                  (5, 5, 64), (32, 8, 128), (24, 2, 128),
+                                                  (64, 1, 128), (40, 8, 64)])
+@pytest.mark.parametrize("nodes", [1, 5, 17])
+def test_attention_heads(nm, kind, q_heads, kv_heads, dim, nodes):
+    Batch(kind, [211, 34], [nodes, max(1, nodes - 2)], q_heads, kv_heads, dim, 32, seed=3).check(
+        nm, f"{kind} {q_heads}/{kv_heads}x{dim} nodes {nodes}")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("page", [8, 64, 128, 1024])
+@pytest.mark.parametrize("nodes", [2, 40])
+def test_attention_pages_and_causal(nm, kind, page, nodes):
+    """Pages that end inside any tile, one larger than the context; no mask."""
+    Batch(kind, [333, 129], [nodes, 1], 8, 2, 128, page, seed=5, masks=None).check(
+        nm, f"{kind} page {page}")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("nodes", [3, 24])
+def test_attention_rows_that_see_nothing(nm, kind, nodes):
+    b = Batch(kind, [0, 70, 0], [nodes, nodes, 1], 16, 2, 64, 16, seed=7)
+    for t in (0, nodes, nodes + 1, 2 * nodes):  # no bits at all
+        b.masks[t] = 0
+    out, lse = b.check(nm, f"{kind} empty rows")
+    assert torch.isinf(lse[0]).all() and (out[0] == 0).all()
+    assert torch.isinf(lse[2 * nodes]).all() and (out[2 * nodes] == 0).all()
+    assert torch.isfinite(lse[nodes]).all()  # it sees its context
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("nodes", [6, 30])
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("bad", [NAN, float("inf")])
+def test_attention_spoilt_node(nm, kind, nodes, which, bad):
+    """A non-finite row of one node reaches the nodes that see it and no others."""
+    b = Batch(kind, [90], [nodes], 8, 2, 128, 16, seed=9)
+    want, wl, to, tl = b.want()
+    j = 3
+    b.set_row(0, 90 + j, bad, which=which)
+    out, lse = b.run(nm)
+    seen = torch.tensor([bool((m >> j) & 1) for m in b.masks])
+    assert seen.any() and not seen.all()
+    within(out[~seen], want[~seen], to[~seen], "nodes that do not see it")
+    within(lse[~seen], wl[~seen], tl[~seen], "lse of nodes that do not see it")
+    if bad != bad or which == "v" or kind == "fp16":  # codes times an infinite scale: the score may
+        assert not torch.isfinite(out[seen]).all(-1).any()  # be -inf, which rightly weighs nothing
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("nodes", [4, 32])
+def test_attention_large_scores_and_outliers(nm, kind, nodes):
+    """Scores of several hundred (all weight on few rows) and values whose rows
+    differ by orders of magnitude."""
+    b = Batch(kind, [400], [nodes], 8, 2, 128, 32, seed=11, q_scale=60.0)
+    factor = 10.0 ** (torch.arange(b.v.shape[0] * 32).view(-1, 1, 32) % 7 - 4).float()
+    if b.vs is None:
+        b.v = (b.v.float() * factor[..., None]).half()
+    else:
+        b.vs = b.vs * factor
+    b.check(nm, f"{kind} large scores")
+    b = Batch(kind, [400], [nodes], 8, 2, 128, 32, seed=12)
+    b.scale = 0.0  # every row weighs the same
+    b.check(nm, f"{kind} scale 0")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("nodes", [1, 20])
+def test_attention_absent_pages(nm, kind, nodes):
+    """Entries out of range, and positions beyond the table, are seen by no node."""
+    b = Batch(kind, [200, 100], [nodes, nodes], 8, 2, 64, 16, seed=13, spoil=False)
+    b.table[0, 2], b.table[0, 5], b.table[1, 0] = -1, b.k.shape[0], 2 ** 31 - 1
+    b.check(nm, f"{kind} absent pages")
+    b.table = b.table[:, :4].contiguous()
+    b.check(nm, f"{kind} short table")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("nodes", [3, 18])
+def test_attention_strides(nm, kind, nodes):
+    """q and out inside wider rows, k and v pages interleaved in one buffer, a
+    table that is part of a wider one."""
+    b = Batch(kind, [150, 77], [nodes, 2], 8, 2, 128, 16, seed=15)
+    T = sum(b.nodes)
+    both = torch.stack([b.k.view(torch.uint8 if b.ks is not None else torch.float16),
+                        b.v.view(torch.uint8 if b.ks is not None else torch.float16)], 1).cuda()
+    both = both.view(b.k.dtype)
+    ks = vs = None
+    if b.ks is not None:
+        sc = torch.stack([b.ks, b.vs], 1).cuda()
+        ks, vs = sc[:, 0], sc[:, 1]
+    wide_q = torch.full((T, 12 * 128), 7.0, dtype=torch.float16, device="cuda")
+    wide_q[:, :8 * 128] = b.q.view(T, -1).cuda()
+    wide_o = torch.full((T, 10 * 128), 7.0, dtype=torch.float16, device="cuda")
+    wide_t = torch.full((2, b.table.shape[1] + 5), 10 ** 6, dtype=torch.int32, device="cuda")
+    wide_t[:, :b.table.shape[1]] = b.table.cuda()
+    out, lse = nm.nm_tree_attention(
+        wide_q[:, :8 * 128].unflatten(1, (8, 128)), both[:, 0], both[:, 1],
+        wide_t[:, :b.table.shape[1]], torch.tensor(b.ctx, dtype=torch.int32).cuda(),
+        torch.tensor(b.start, dtype=torch.int32).cuda(), max(b.nodes),
+        tree_mask=signed(b.masks).cuda(), k_scale=ks, v_scale=vs,
+        out=wide_o[:, :8 * 128].unflatten(1, (8, 128)))
+    o, l, to, tl = b.want()
+    within(out, o, to, "strided out")
+    within(lse, l, tl, "strided lse")
+    assert (wide_o[:, 8 * 128:] == 7).all()
+
+
+def test_attention_ragged_bounds(nm):
+    """Nodes beyond max_nodes are not computed, sequences without nodes and
+    tokens outside q_start are left alone."""
+    b = Batch("fp16", [50, 60, 70], [3, 0, 9], 8, 2, 64, 16, seed=17)
+    T = sum(b.nodes)
+    out = torch.full((T, 8, 64), 5.0, dtype=torch.float16, device="cuda")
+    lse = torch.full((T, 8), 5.0, device="cuda")
+    k, v = cuda(b.k, b.v)
+    nm.nm_tree_attention(b.q.cuda(), k, v, b.table.cuda(),
+                         torch.tensor(b.ctx, dtype=torch.int32).cuda(),
+                         torch.tensor(b.start, dtype=torch.int32).cuda(), 4,
+                         tree_mask=signed(b.masks).cuda(), out=out, lse=lse)
+    # with max_nodes 4 the third sequence's nodes are its first four only
+    b.nodes[2] = 4
+    b.start = [0, 3, 3, 7]
+    b.q, keep = b.q[:7], b.masks
+    b.masks = [m & 15 for m in keep[:7]]
+    o, l, to, tl = b.want()
+    within(out[:7], o, to, "first nodes")
+    within(lse[:7], l, tl, "first nodes' lse")
+    assert (out[7:] == 5).all() and (lse[7:] == 5).all()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("nodes", [1, 4, 32])
+def test_attention_workspace_and_repeats(nm, kind, nodes):
+    """The same bits every time, through one workspace that other calls used in
+    between, on a stream of its own."""
+    b = Batch(kind, [5000, 30], [nodes, nodes], 8, 1, 128, 64, seed=19)
+    c = Batch(kind, [100] * 20, [2] * 20, 8, 1, 128, 64, seed=20)
+    need = max(nm.nm_tree_attention_workspace_bytes(2, 8, 1, 128, nodes),
+               nm.nm_tree_attention_workspace_bytes(20, 8, 1, 128, 2))
+    ws = torch.zeros(max(need, 16), dtype=torch.uint8, device="cuda")
+    first = b.check(nm, "first", workspace=ws)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        c.run(nm, workspace=ws)
+        second = b.run(nm, workspace=ws)
+    side.synchronize()
+    assert torch.equal(first[0], second[0]) and torch.equal(first[1], second[1])
+
+
+def test_attention_long_offsets(nm):
+    """A cache whose byte and element offsets pass 2^32: the sequence's pages lie
+    at both of its ends."""
+    dim, heads, page = 128, 8, 64
+    pages = (1 << 32) // (heads * page * dim) + 50
+    k = torch.zeros((pages, heads, page, dim), dtype=torch.int8, device="cuda")
+    v = torch.zeros_like(k)
+    ks = torch.zeros((pages, heads, page), device="cuda")
+    vs = torch.zeros_like(ks)
+    b = Batch("int8", [380], [6], 16, heads, dim, page, seed=21)
+    far = torch.tensor([pages - 1 - 3 * i if i % 2 == 0 else i for i in range(b.k.shape[0])])
+    for a, c in ((k, b.k), (v, b.v), (ks, b.ks), (vs, b.vs)):
+        a[far.cuda()] = c.cuda()
+    table = torch.where(b.table >= 0, far[b.table.clamp_min(0).long()].to(torch.int32), -1)
+    out, lse = nm.nm_tree_attention(b.q.cuda(), k, v, table.cuda(),
+                                    torch.tensor(b.ctx, dtype=torch.int32).cuda(),
+                                    torch.tensor(b.start, dtype=torch.int32).cuda(), 6,
+                                    tree_mask=signed(b.masks).cuda(), k_scale=ks, v_scale=vs)
+    o, l, to, tl = b.want()
+    within(out, o, to, "far pages out")
+    within(lse, l, tl, "far pages lse")
+    # and the same rows read back
+    slots = (far[:4, None] * page + torch.arange(page)).reshape(-1).cuda()
+    rk, rv = nm.nm_cache_read(k, v, slots, k_scale=ks, v_scale=vs)
+    want = (b.k[:4].float() * b.ks[:4, ..., None]).half().transpose(1, 2).reshape(-1, heads, dim)
+    ok = ~torch.isnan(want)
+    assert torch.equal(rk.cpu()[ok], want[ok])
+
+
+def test_attention_graph(nm):
+    """The call replays from a CUDA graph on new contents of its buffers."""
+    b = Batch("fp16", [700], [4], 32, 8, 128, 16, seed=23)
+    k, v, q = cuda(b.k, b.v, b.q)
+    args = (k, v, b.table.cuda(), torch.tensor(b.ctx, dtype=torch.int32).cuda(),
+            torch.tensor(b.start, dtype=torch.int32).cuda(), 4)
+    mask = signed(b.masks).cuda()
+    ws = torch.zeros(max(16, nm.nm_tree_attention_workspace_bytes(1, 32, 8, 128, 4)),
+                     dtype=torch.uint8, device="cuda")
+    out, lse = torch.empty_like(q), torch.empty((4, 32), device="cuda")
+    nm.nm_tree_attention(q, *args, tree_mask=mask, workspace=ws, out=out, lse=lse)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        nm.nm_tree_attention(q, *args, tree_mask=mask, workspace=ws, out=out, lse=lse)
+    b.q = (b.q.float() * -0.7).half()
+    q.copy_(b.q)
+    for _ in range(3):
+        out.zero_()
+        g.replay()
+    torch.cuda.synchronize()
+    o, l, to, tl = b.want()
+    within(out, o, to, "replayed out")
+    within(lse, l, tl, "replayed lse")
+
+
+# ---- rotary positions, cache write and read ------------------------------------------
+def append_case(kind, tokens, q_heads, kv_heads, dim, page, seed, top=5000):
+    gen = torch.Generator().manual_seed(seed)
+    pages = -(-tokens // page) + 3
+    x = torch.randn((tokens, q_heads + 2 * kv_heads, dim), generator=gen)
+    x[..., 1] *= 15
+    pos = torch.randint(0, top, (tokens,), generator=gen).to(torch.int32)
+    slots = torch.randperm(pages * page, generator=gen)[:tokens].contiguous()
+    shape = (pages, kv_heads, page, dim)
+    k, v = (torch.zeros(shape, dtype=ref.DTYPES[kind], device="cuda") for _ in range(2))
+    ks = vs = None
+    if kind != "fp16":
+        ks, vs = (torch.zeros(shape[:3], device="cuda") for _ in range(2))
+    return x.half(), pos, slots, k, v, ks, vs
+
+
+def check_append(nm, kind, x, pos, slots, caches, freq, interleaved, mscale, q):
+    """q, and the cache's rows: the rotation's fp32 error is at most 2^-21 (|a| +
+    |b|) (cos and sin to 2^-22, two products and a sum); q and fp16 rows are
+    rounded once; a code lies within half a step (and the fp32 error of x /
+    scale, 2^-21 max|x|) of its value, or a neighbour where that is a tie."""
+    k, v, ks, vs = caches
+    H, page = k.shape[1], k.shape[2]
+    Q = x.shape[1] - 2 * H
+    y, size = ref.rotate(x[:, :Q + H], pos, freq, interleaved, mscale)
+    if q is not None:
+        within(q, y[:, :Q], 2.0 ** -11 * y[:, :Q].abs() + 2.0 ** -21 * size[:, :Q] + 2.0 ** -25, "q")
+    for cache, scale, row, sz, name in ((k, ks, y[:, Q:], size[:, Q:], "k"),
+                                        (v, vs, x[:, Q + H:].double(), x[:, Q + H:].double().abs(), "v")):
+        pg, off = slots // page, slots % page
+        got = cache.cpu().view(torch.uint8 if scale is not None else torch.float16)[pg, :, off]
+        got = got.view(cache.dtype).float().double()
+        eps = 2.0 ** -21 * sz
+        if scale is None:
+            within(got, row, 2.0 ** -11 * row.abs() + eps + 2.0 ** -25, name)
+            continue
+        sc = scale.cpu()[pg, :, off].double()
+        s = row.abs().amax(-1) / ref.CODE_MAX[kind]
+        worst = eps.amax(-1)
+        within(sc, s, 2.0 ** -22 * s + worst / ref.CODE_MAX[kind] + 1e-45, name + " scale")
+        tol = ref.code_step(row, s, kind) / 2 * (1 + 2.0 ** -20) + eps + 2.0 ** -20 * row.abs() \
+            + worst[..., None] / 100 + 1e-45
+        within(got * sc[..., None], row, tol, name + " codes")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dim,rot", [(128, 128), (128, 64), (128, 36), (64, 64), (64, 20), (64, 0),
+                                     (128, 2)])
+def test_append_layouts(nm, kind, interleaved, dim, rot):
+    x, pos, slots, *caches = append_case(kind, 37, 6, 2, dim, 16, seed=rot + dim)
+    freq = nm.nm_rope_inv_freq(rot, 10000.0)
+    q = nm.nm_rope_append(x.view(37, -1).cuda(), caches[0], caches[1], pos.cuda(), slots.cuda(),
+                          freq, 6, k_scale=caches[2], v_scale=caches[3], interleaved=interleaved,
+                          mscale=1.25)
+    check_append(nm, kind, x, pos, slots, caches, freq.cpu(), interleaved,
+                 1.25 if rot else 1.0, q)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("tokens,q_heads,kv_heads,dim", [(1, 32, 8, 128), (1, 1, 1, 64), (3, 28, 4, 64),
+                                                         (700, 8, 1, 128), (64, 64, 8, 128)])
+def test_append_sizes(nm, kind, tokens, q_heads, kv_heads, dim):
+    x, pos, slots, *caches = append_case(kind, tokens, q_heads, kv_heads, dim, 64, seed=tokens,
+                                         top=131072)
+    freq = nm.nm_rope_inv_freq(dim, 500000.0, "banded", 8.0)
+    q = nm.nm_rope_append(x.view(tokens, -1).cuda(), caches[0], caches[1], pos.cuda(),
+                          slots.cuda(), freq, q_heads, k_scale=caches[2], v_scale=caches[3])
+    check_append(nm, kind, x, pos, slots, caches, freq.cpu(), False, 1.0, q)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_append_again_commits_the_same_rows(nm, kind):
+    """Rows appended again to other slots are the same bits; without q; slots out
+    of range are not written; qkv inside wider rows."""
+    x, pos, slots, k, v, ks, vs = append_case(kind, 9, 4, 2, 128, 16, seed=3)
+    freq = nm.nm_rope_inv_freq(128)
+    wide = torch.zeros((9, 9 * 128), dtype=torch.float16, device="cuda")
+    wide[:, :8 * 128] = x.view(9, -1).cuda()
+    q = nm.nm_rope_append(wide[:, :8 * 128], k, v, pos.cuda(), slots.cuda(), freq, 4, k_scale=ks,
+                          v_scale=vs)
+    before = [t.clone() for t in (k, v, ks, vs) if t is not None]
+    first = nm.nm_cache_read(k, v, slots.cuda(), ks, vs)
+    out = slots.clone()
+    out[0], out[1], out[2] = -1, k.shape[0] * 16, 1 << 60
+    none = nm.nm_rope_append(wide[:, :8 * 128], k, v, pos.cuda(), out.cuda(), freq, 4, k_scale=ks,
+                             v_scale=vs, want_q=False)
+    assert none is None
+    for a, b in zip(before, [t for t in (k, v, ks, vs) if t is not None]):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    free = [i for i in range(k.shape[0] * 16) if i not in set(slots.tolist())][:3]
+    dst = torch.tensor(free, device="cuda")
+    nm.nm_rope_append(wide[4:7, :8 * 128], k, v, pos[4:7].cuda().contiguous(), dst, freq, 4,
+                      k_scale=ks, v_scale=vs, want_q=False)
+    again = nm.nm_cache_read(k, v, dst, ks, vs)
+    assert torch.equal(again[0], first[0][4:7]) and torch.equal(again[1], first[1][4:7])
+    assert q.shape == (9, 4, 128)
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+def test_append_zero_and_non_finite_rows(nm, kind):
+    x, pos, slots, k, v, ks, vs = append_case(kind, 4, 2, 1, 64, 8, seed=5)
+    x[0, 3] = 0                      # token 0's values
+    x[1, 3, 5] = float("inf")
+    x[2, 3, 6] = NAN
+    x[3, 3] = 0
+    x[3, 3, 0] = 6e-8                # the smallest subnormal
+    nm.nm_rope_append(x.view(4, -1).cuda(), k, v, pos.cuda(), slots.cuda(),
+                      nm.nm_rope_inv_freq(64), 2, k_scale=ks, v_scale=vs)
+    rk, rv = nm.nm_cache_read(k, v, slots.cuda(), ks, vs)
+    assert (rv[0] == 0).all()
+    assert torch.isnan(rv[1]).all() and torch.isnan(rv[2]).all()
+    assert torch.equal(rv[3].cpu(), x[3, 3:4])
+    assert torch.isfinite(rk).all()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rows,heads,dim,page", [(1, 1, 64, 8), (77, 8, 128, 16), (1000, 3, 64, 128)])
+def test_read_bits(nm, kind, rows, heads, dim, page):
+    """code * scale in fp32, rounded once: the same bits as the CPU's."""
+    gen = torch.Generator().manual_seed(rows)
+    pages = -(-rows // page) + 2
+    k, v, ks, vs = ref.random_cache(kind, pages, heads, page, dim, gen, 3.0)
+    slots = torch.randint(0, pages * page, (rows,), generator=gen)
+    if rows > 5:
+        slots[3], slots[5] = -7, pages * page
+    gk, gv = nm.nm_cache_read(*cuda(k, v, slots), *(cuda(ks, vs)))
+    for got, c, s in ((gk, k, ks), (gv, v, vs)):
+        x = c.float() if s is None else c.float() * s[..., None]
+        ok = (slots >= 0) & (slots < pages * page)
+        at = torch.where(ok, slots, 0)
+        want = torch.where(ok[:, None, None], x[at // page, :, at % page], 0.0).half()
+        assert torch.equal(got.cpu(), want)
+
+
+# ---- verification --------------------------------------------------------------------
+def verify_case(seed, seqs, nodes, vocab, drafted, temperature, fp32, closeness=0.7, fan=3):
+    """Inputs of a walk whose decisions all lie 1e-4 off their boundaries: fp32
+    sums of the vocabulary are good to a few 1e-6."""
+    while True:
+        rng, rnd = np.random.default_rng(seed), random.Random(seed)
+        n = [max(1, nodes - rnd.randrange(3)) for _ in range(seqs)]
+        start = np.concatenate([[0], np.cumsum(n)]).astype(np.int32)
+        N = int(start[-1])
+        logits = (rng.standard_normal((N, vocab)) * 2.5).astype(np.float32 if fp32 else np.float16)
+        guess = logits.astype(np.float64) + rng.standard_normal((N, vocab)) * closeness
+        q = np.exp(guess - guess.max(1, keepdims=True))
+        q = (q / q.sum(1, keepdims=True)).astype(np.float32)
+        parents, ids = np.full(N, -1, np.int32), np.zeros(N, np.int32)
+        for s in range(seqs):
+            kids = [0] * n[s]
+            for i in range(1, n[s]):
+                p = rnd.choice([j for j in range(i) if kids[j] < fan])
+                parents[start[s] + i] = p
+                row = start[s] + p
+                if drafted:
+                    ids[start[s] + i] = rng.choice(vocab, p=q[row].astype(np.float64)
+                                                   / q[row].astype(np.float64).sum())
+                else:
+                    ids[start[s] + i] = np.argsort(-guess[row], kind="stable")[min(kids[p], vocab - 1)]
+                kids[p] += 1
+        accept = rng.random(N).astype(np.float32)
+        race = np.maximum(rng.exponential(size=(seqs, vocab)), 1e-30).astype(np.float32)
+        want = ref.verify(logits, ids, parents, start, accept, race, q if drafted else None,
+                          temperature, nodes)
+        if want[3] > 1e-4:
+            return logits, ids, parents, start, accept, race, q if drafted else None, want[:3]
+        seed += 1000
+
+
+def run_verify(nm, case, nodes, temperature, **kw):
+    logits, ids, parents, start, accept, race, q = (None if a is None else torch.from_numpy(a).cuda()
+                                                    for a in case[:7])
+    return nm.nm_tree_verify(logits, ids, parents, start, nodes, draft=q, accept=accept, race=race,
+                             temperature=temperature, **kw)
+
+
+def same(got, want):
+    for g, w, what in zip(got, want, ("path", "count", "token")):
+        assert np.array_equal(g.cpu().numpy(), w), what
+
+
+@pytest.mark.parametrize("fp32", [False, True])
+@pytest.mark.parametrize("drafted", [True, False])
+@pytest.mark.parametrize("temperature", [0.0, 0.7, 1.0])
+@pytest.mark.parametrize("seqs,nodes,vocab", [(1, 1, 1), (1, 2, 5), (3, 7, 33), (5, 20, 1000),
+                                              (2, 64, 32000), (17, 5, 4097)])
+def test_verify_walks(nm, fp32, drafted, temperature, seqs, nodes, vocab):
+    case = verify_case(seqs * 100 + nodes, seqs, nodes, vocab, drafted, temperature, fp32)
+    same(run_verify(nm, case, nodes, temperature), case[7])
+
+
+@pytest.mark.parametrize("drafted", [True, False])
+def test_verify_far_draft_and_repeated_children(nm, drafted):
+    """A draft far from the target (most children rejected, several a node) and
+    children with equal tokens."""
+    for seed in range(6):
+        case = list(verify_case(seed, 4, 24, 300, drafted, 1.0, True, closeness=4.0, fan=8))
+        same(run_verify(nm, case, 24, 1.0), case[7])
+
+
+def test_verify_forbidden_tokens_and_bad_rows(nm):
+    """Logits of -inf have no weight; a row that is all -inf, or has NaN or +inf,
+    ends the walk with token -1; nodes with bad parents or tokens are never
+    visited; a sequence without nodes."""
+    V = 100
+    logits = torch.full((6, V), float("-inf"))
+    logits[0, 7] = 0.0                    # token 7 for certain
+    logits[1, 50] = NAN                   # sequence 0, node 1
+    logits[2, 3] = 1.0                    # sequence 1, node 0: token 3
+    logits[4] = 0.0
+    logits[4, 9] = float("inf")           # sequence 3, node 0
+    ids = torch.tensor([0, 7, 0, 3, 0, 5], dtype=torch.int32)
+    par = torch.tensor([-1, 0, -1, 5, -1, 0], dtype=torch.int32)
+    start = torch.tensor([0, 2, 4, 4, 6], dtype=torch.int32)
+    for temperature in (1.0, 0.0):
+        path, count, token = nm.nm_tree_verify(
+            *cuda(logits, ids, par, start), 2, accept=torch.full((6,), 0.5).cuda(),
+            race=torch.ones((4, V)).cuda(), temperature=temperature)
+        assert path.tolist() == [[0, 1], [0, -1], [-1, -1], [0, -1]]
+        assert count.tolist() == [2, 1, 0, 1]
+        assert token.tolist() == [-1, 3, -1, -1]
+    ids[1] = V  # out of the vocabulary
+    path, count, token = nm.nm_tree_verify(
+        *cuda(logits, ids, par, start), 2, accept=torch.full((6,), 0.5).cuda(),
+        race=torch.ones((4, V)).cuda())
+    assert path[0].tolist() == [0, -1] and int(token[0]) == 7
+
+
+@pytest.mark.parametrize("temperature", [0.0, 1.0])
+def test_verify_ties_take_the_lowest_index(nm, temperature):
+    V = 5000
+    logits = torch.zeros((1, V))
+    logits[0, 1234] = logits[0, 1111] = logits[0, 4999] = 3.0
+    path, count, token = nm.nm_tree_verify(
+        logits.cuda(), torch.zeros(1, dtype=torch.int32).cuda(),
+        torch.full((1,), -1, dtype=torch.int32).cuda(), torch.tensor([0, 1], dtype=torch.int32).cuda(),
+        1, accept=torch.zeros(1).cuda(), race=torch.ones((1, V)).cuda(), temperature=temperature)
+    assert int(token[0]) == 1111
+
+
+@pytest.mark.parametrize("fp32", [False, True])
+def test_verify_strides(nm, fp32):
+    """Rows inside wider ones, at odd element offsets (no vector loads)."""
+    case = verify_case(77, 3, 9, 1001, True, 0.9, fp32)
+    logits, ids, parents, start, accept, race, q = (torch.from_numpy(a).cuda() for a in case[:7])
+
+    def inside(t):
+        w = torch.full((t.shape[0], t.shape[1] + 6), NAN, dtype=t.dtype, device="cuda")
+        w[:, 1:1 + t.shape[1]] = t
+        return w[:, 1:1 + t.shape[1]]
+    got = nm.nm_tree_verify(inside(logits), ids, parents, start, 9, draft=inside(q), accept=accept,
+                            race=inside(race), temperature=0.9)
+    same(got, case[7])
+
+
+@pytest.mark.parametrize("drafted", [True, False])
+def test_verify_keeps_the_targets_distribution(nm, drafted):
+    """Over many sequences the first kept token is distributed as the target's:
+    each frequency within 5 standard deviations."""
+    rng = np.random.default_rng(5)
+    S, V = 40000, 6
+    p = np.array([0.35, 0.25, 0.2, 0.1, 0.07, 0.03])
+    q = np.array([0.05, 0.4, 0.1, 0.3, 0.1, 0.05])
+    logits = np.tile(np.log(p).astype(np.float32), (3 * S, 1))
+    kids = rng.choice(V, size=(S, 2), p=q) if drafted else np.tile([1, 3], (S, 1))
+    ids = np.zeros((S, 3), np.int32)
+    ids[:, 1:] = kids
+    parents = np.tile(np.array([-1, 0, 0], np.int32), S)
+    start = np.arange(0, 3 * S + 1, 3, dtype=np.int32)
+    draft = np.tile(q.astype(np.float32), (3 * S, 1)) if drafted else None
+    case = (logits, ids.reshape(-1), parents, start, rng.random(3 * S).astype(np.float32),
+            np.maximum(rng.exponential(size=(S, V)), 1e-30).astype(np.float32), draft)
+    path, count, token = run_verify(nm, case, 3, 1.0)
+    path, count, token = path.cpu().numpy(), count.cpu().numpy(), token.cpu().numpy()
+    kept = np.where(count > 1, ids[np.arange(S), np.maximum(path[:, 1], 0)], token)
+    f = np.bincount(kept, minlength=V) / S
+    assert (np.abs(f - p) < 5 * np.sqrt(p * (1 - p) / S)).all(), (f, p)
+    assert 0.2 < (count > 1).mean() < 0.95
