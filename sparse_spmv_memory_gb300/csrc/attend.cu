@@ -1,16 +1,18 @@
 // attend.cu -- attention of drafted nodes over a paged cache
-// (nm_tree_attention).
+// (nm_tree_attention), for few query rows per key head; attend_wide.cu has the
+// kernel for many.
 //
 // For a node's query q and the rows (k_j, v_j) that it sees,
-//   o = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q.k_j - m),
+//   o = sum_j p_j v_j / sum_j p_j,  p_j = 2^(s_j - m),  s_j = scale log2(e) q.k_j,
 // with m the largest score so far: a new maximum m' scales what was summed by
-// exp(m - m'), so one pass over the cache does, and parts with their own m
-// join by the same rule.
+// 2^(m - m'), so one pass over the cache does, and parts with their own m join
+// by the same rule.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "attend.cuh"
 #include "decode.h"
 #include "device.cuh"
 #include "kernels.h"
@@ -18,111 +20,542 @@
 namespace nmk {
 namespace {
 
-template <int TYPE>
-__device__ __forceinline__ float code_value(const uint8_t* base, int64_t at) {
-  if (TYPE == kCacheFp16) return __half2float(reinterpret_cast<const __half*>(base)[at]);
-  if (TYPE == kCacheInt8) return (float)(int8_t)base[at];
-  return __half2float(__half(__nv_cvt_fp8_to_halfraw(base[at], __NV_E4M3)));
+// ---- loads and conversions -----------------------------------------------------
+template <int WORDS>  // 2, 4 or 8 words; zeros where !on
+__device__ __forceinline__ void load_words(const uint8_t* at, bool on, uint32_t* r) {
+#pragma unroll
+  for (int i = 0; i < WORDS; ++i) r[i] = 0;
+  if (!on) return;
+  if (WORDS == 8) {
+    uint32_t v[8];
+    ld_stream_v8(reinterpret_cast<const uint32_t*>(at), v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = v[i];
+  } else if (WORDS == 4) {
+    const uint4 v = ld_stream_v4(at);
+    r[0] = v.x, r[1] = v.y, r[2] = v.z, r[3] = v.w;
+  } else {
+    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];"
+                 : "=r"(r[0]), "=r"(r[1])
+                 : "l"(at));
+  }
 }
 
-// One block per token and query head; a warp takes every 8th position, its
-// lanes share the head's elements.
-template <int D, int TYPE>
-__global__ void __launch_bounds__(256) attend_kernel(AttendParams p) {
-  constexpr int E = D / 32, NW = 8;
-  __shared__ float so[NW][D], sm[NW], sl[NW];
+__device__ __forceinline__ uint32_t byte_perm(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
+  return r;
+}
+
+// Two codes in the low 16 bits -> two fp16, exactly (e4m3, NaN included).
+__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t two) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(r) : "r"(two));
+  return r;
+}
+
+// Four codes of a word -> two words of two fp16.  int8: the byte with its sign
+// bit flipped under 0x64 is the fp16 1024 + 128 + code.
+template <int TYPE>
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if (TYPE == kCacheE4m3) {
+    lo = e4m3x2_to_half2(w);
+    hi = e4m3x2_to_half2(w >> 16);
+  } else {
+    const uint32_t u = w ^ 0x80808080u;
+    const __half2 off = __half2half2(__ushort_as_half(0x6480));  // 1152
+    uint32_t a = byte_perm(u, 0x64646464u, 0x4140), b = byte_perm(u, 0x64646464u, 0x4342);
+    __half2 x = __hsub2(*reinterpret_cast<__half2*>(&a), off);
+    __half2 y = __hsub2(*reinterpret_cast<__half2*>(&b), off);
+    lo = *reinterpret_cast<uint32_t*>(&x);
+    hi = *reinterpret_cast<uint32_t*>(&y);
+  }
+}
+
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Halves of w that are infinite or NaN: bit 0, bit 1.
+__device__ __forceinline__ uint32_t bad_halves(uint32_t w) {
+  return ((w & 0x7C00u) == 0x7C00u ? 1u : 0u) | ((w & 0x7C000000u) == 0x7C000000u ? 2u : 0u);
+}
+
+// ---- the kernel for few rows ------------------------------------------------------
+// mma.sync.m16n8k16 with the query rows as A (16 at a time), a head's rows of K
+// as B for the scores, and of V as B for the sums.  K and V come from HBM
+// straight into the registers the MMA reads them from, 32 bytes a lane: the
+// order of a product's k index is free as long as A and B agree, and so is the
+// order of the output's columns.  Lane 4g + q
+//   - of K holds of row g (per 8 positions) the elements that the k slots of q
+//     are given to: any 4 per MMA, so whole 16- to 32-byte pieces of the row;
+//   - of V holds of the rows 2q, 2q+1, 2q+8, 2q+9 the piece g of the row: its
+//     column t of MMA n-tile t.  Two rows' halves are paired by byte permutes.
+// No shared memory, no barrier, until a block's warps join their sums.  A warp
+// takes every NW-th unit of the block's part.
+template <int D, int TYPE, int MT>
+struct Narrow {
+  static constexpr bool F16 = TYPE == kCacheFp16;
+  static constexpr int NG = F16 || MT > 1 ? 2 : 4;      // groups of 8 positions in a unit
+  static constexpr int UK = 8 * NG;           // positions of a unit
+  static constexpr int KS = D / 16;           // MMA k steps of a score
+  static constexpr int NT = D / 8;            // n-tiles of an output row
+  static constexpr int KW = D * (F16 ? 2 : 1) / 16;  // words of K a lane holds per group
+  static constexpr int VW = D * (F16 ? 2 : 1) / 32;  // words of V a lane holds per row
+  // the element of k step ks, MMA slots 2q, 2q+1, 2q+8, 2q+9: four from here
+  static __device__ __forceinline__ int k_elem(int ks, int q) {
+    return F16 ? (ks >> 2) * 64 + 16 * q + 4 * (ks & 3) : (D / 4) * q + 4 * ks;
+  }
+};
+
+template <int D, int TYPE, int MT, int NW>
+__global__ void __launch_bounds__(NW * 32, 1) attend_narrow_kernel(AttendParams p) {
+  using N = Narrow<D, TYPE, MT>;
+  constexpr bool F16 = N::F16;
+  constexpr int ROWS = 16 * MT, NTH = NW * 32, PITCH = D + 4;
+  using Sched = Schedule<ROWS, N::UK, NTH>;
+  extern __shared__ __align__(16) uint8_t dyn[];
+  float* so = reinterpret_cast<float*>(dyn);                     // [NW][ROWS][PITCH]
+  __shared__ uint4 sq[MT][N::KS][32];                            // A fragments of the queries
+  __shared__ uint64_t smask[ROWS];
+  __shared__ float sm[NW][ROWS], sl[NW][ROWS], sf[NW][ROWS];
+  __shared__ float row_m[ROWS], row_l[ROWS];
+  __shared__ int64_t buf[NTH + 1];
   pdl_launch_dependents();
   pdl_wait_previous();
-  const int t = blockIdx.x, hq = blockIdx.y;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int s = 0;
-  while (s < p.seqs && !(p.q_start[s] <= t && t < p.q_start[s + 1])) ++s;
-  if (s == p.seqs) return;
-  const int first = max(p.q_start[s], 0);
-  const int node = t - first;
-  const int n = min(min(p.q_start[s + 1], p.tokens) - first, p.max_nodes);
-  if (node >= n) return;
-  const int ctx = max(p.ctx_len[s], 0);
-  const uint64_t seen = p.tree_mask ? p.tree_mask[t] : (2ull << node) - 1ull;
-  const int kh = hq / (p.q_heads / p.c.kv_heads);
-  float q[E], o[E], m = -INFINITY, l = 0.0f;
+  Sched sched;
+  if (!sched.init(p, NW, buf)) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const int G = p.q_heads / p.c.kv_heads;
+  const float cs = p.scale * kLog2e;
+  int* counters = reinterpret_cast<int*>(p.workspace);
+  float* slots = reinterpret_cast<float*>(
+      p.workspace + attend_counter_bytes((int64_t)p.seqs * p.c.kv_heads * sched.rt_max));
+
+  Span w;
+  SeqInfo si;
+  while (sched.next(p, w, si)) {
+    const int rows = min(ROWS, si.n * G - w.rt * ROWS);
+    __syncthreads();  // the shared arrays of the last item are free
+    for (int i = threadIdx.x; i < MT * N::KS * 32; i += NTH) {
+      const int mt = i / (N::KS * 32), ks = i / 32 % N::KS, ln = i % 32;
+      const int e = N::k_elem(ks, ln & 3);
+      uint2 v[2];
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = __half2float(p.q[(int64_t)t * p.ldq + (int64_t)hq * D + lane + 32 * e]) * p.scale;
-    o[e] = 0.0f;
-  }
-  for (int64_t j = warp; j < (int64_t)ctx + n; j += NW) {
-    if (j >= ctx && !((seen >> (j - ctx)) & 1)) continue;
-    const int64_t ti = j >> p.c.page_shift;
-    if (ti >= p.table_cols) continue;
-    const int64_t page = p.table[(int64_t)s * p.ld_table + ti];
-    if (page < 0 || page >= p.c.pages) continue;
-    const int64_t in_page = ((int64_t)kh << p.c.page_shift) + (j & ((1 << p.c.page_shift) - 1));
-    const int64_t at = page * p.c.page_stride + in_page * D;
-    const int64_t sat = page * p.c.scale_page_stride + in_page;
-    float d = 0.0f;
+      for (int k = 0; k < 2; ++k) {
+        const int r = 16 * mt + (ln >> 2) + 8 * k, rr = w.rt * ROWS + r;
+        v[k] = make_uint2(0, 0);
+        if (r < rows)
+          v[k] = *reinterpret_cast<const uint2*>(p.q + (int64_t)(si.first + rr / G) * p.ldq +
+                                                 (int64_t)(w.h * G + rr % G) * D + e);
+      }
+      sq[mt][ks][ln] = make_uint4(v[0].x, v[1].x, v[0].y, v[1].y);
+    }
+    for (int r = threadIdx.x; r < ROWS; r += NTH) {
+      const int node = (w.rt * ROWS + r) / G;
+      smask[r] = r >= rows ? 0ull : p.tree_mask ? p.tree_mask[si.first + node] : (2ull << node) - 1ull;
+    }
+    __syncthreads();
+
+    float o[MT][N::NT][4], m[MT][2], l[MT][2];
 #pragma unroll
-    for (int e = 0; e < E; ++e) d += q[e] * code_value<TYPE>(p.c.k, at + lane + 32 * e);
-    d = warp_sum(d);
-    if (TYPE != kCacheFp16) d *= p.c.k_scale[sat];
-    const float m2 = fmaxf(m, d);
-    const float base = m2 == -INFINITY ? 0.0f : m2;
-    const float keep = expf(m - base), w = expf(d - base);
-    m = m2;
-    l = l * keep + w;
-    const float wv = TYPE == kCacheFp16 ? w : w * p.c.v_scale[sat];
+    for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-      o[e] = o[e] * keep + wv * code_value<TYPE>(p.c.v, at + lane + 32 * e);
-  }
+      for (int t = 0; t < N::NT; ++t)
 #pragma unroll
-  for (int e = 0; e < E; ++e) so[warp][lane + 32 * e] = o[e];
-  if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
+        for (int i = 0; i < 4; ++i) o[mt][t][i] = 0.0f;
+      m[mt][0] = m[mt][1] = -INFINITY;
+      l[mt][0] = l[mt][1] = 0.0f;
+    }
+    const int32_t* table = p.table + (int64_t)w.s * p.ld_table;
+    uint32_t kr[N::NG][N::KW], vr[N::NG][2][N::VW];
+    float ksc[N::NG][2], vsc[N::NG][2];
+    RowAt at[N::NG];
+
+    auto find = [&](int u) {
+#pragma unroll
+      for (int c = 0; c < N::NG; ++c) {
+        const int64_t pos = (int64_t)u * N::UK + 8 * c;
+        at[c] = pos < si.len ? group_at<D>(p, table, w.h, pos) : RowAt{-1, -1};
+      }
+    };
+    auto load_k = [&](int u) {
+#pragma unroll
+      for (int c = 0; c < N::NG; ++c) {
+        const int64_t pos = (int64_t)u * N::UK + 8 * c;
+        const bool on = at[c].code >= 0 && pos + g < si.len;
+        const uint8_t* base = p.c.k + (at[c].code + g * D) * (F16 ? 2 : 1);
+        constexpr int PIECE = N::KW > 8 ? 8 : N::KW;  // words of a load
+#pragma unroll
+        for (int i = 0; i < N::KW / PIECE; ++i)
+          load_words<PIECE>(base + (i * 4 + q) * PIECE * 4, on, &kr[c][i * PIECE]);
+        if (!F16) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const bool son = at[c].code >= 0 && pos + 2 * q + i < si.len;
+            ksc[c][i] = son ? p.c.k_scale[at[c].scale + 2 * q + i] : 0.0f;
+            vsc[c][i] = son ? p.c.v_scale[at[c].scale + 2 * q + i] : 0.0f;
+          }
+        }
+      }
+    };
+    auto load_v = [&](int u) {
+#pragma unroll
+      for (int c = 0; c < N::NG; ++c) {
+        const int64_t pos = (int64_t)u * N::UK + 8 * c;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = 2 * q + i;
+          const bool on = at[c].code >= 0 && pos + r < si.len;
+          load_words<N::VW>(p.c.v + (at[c].code + r * D) * (F16 ? 2 : 1) + g * N::VW * 4, on, vr[c][i]);
+        }
+      }
+    };
+
+    int u = w.u0 + warp;
+    if (u < w.u1) {
+      find(u);
+      load_k(u);
+      load_v(u);
+    }
+    for (; u < w.u1; u += NW) {
+      const int64_t pos0 = (int64_t)u * N::UK;
+      uint32_t there = 0;
+#pragma unroll
+      for (int c = 0; c < N::NG; ++c) there |= at[c].code >= 0 ? 1u << c : 0u;
+      // ---- scores: row g (i = 0, 1) and g + 8 (2, 3) of positions 8c + 2q, + 1
+      float s[MT][N::NG][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int c = 0; c < N::NG; ++c)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[mt][c][i] = 0.0f;
+#pragma unroll
+      for (int ks = 0; ks < N::KS; ++ks) {
+        uint32_t b[N::NG][2];
+#pragma unroll
+        for (int c = 0; c < N::NG; ++c) {
+          if (F16) {
+            b[c][0] = kr[c][2 * ks];
+            b[c][1] = kr[c][2 * ks + 1];
+          } else {
+            widen4<TYPE>(kr[c][ks], b[c][0], b[c][1]);
+          }
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          const uint4 f = sq[mt][ks][lane];
+          const uint32_t a[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+          for (int c = 0; c < N::NG; ++c) mma16816(s[mt][c], a, b[c][0], b[c][1]);
+        }
+      }
+      float vs[N::NG][2], lv[N::NG][2];
+#pragma unroll
+      for (int c = 0; c < N::NG; ++c)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float f = F16 ? cs : cs * ksc[c][i];
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            s[mt][c][i] *= f;
+            s[mt][c][2 + i] *= f;
+          }
+          if (!F16) {
+            vs[c][i] = vsc[c][i];
+            lv[c][i] = fmaxf(log2_fast(vsc[c][i]), -40.0f);
+          }
+        }
+      if (u + NW < w.u1) {
+        find(u + NW);
+        load_k(u + NW);
+      }
+      // ---- masks: the last units have the nodes, or end
+      const bool edge = pos0 + N::UK > si.ctx || there != (1u << N::NG) - 1u;
+      uint32_t seen[MT][2];  // bit 2c + i: row sees position 8c + 2q + i
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) seen[mt][0] = seen[mt][1] = ~0u;
+      if (edge) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint64_t bits = smask[16 * mt + g + 8 * k];
+            uint32_t see = 0;
+#pragma unroll
+            for (int c = 0; c < N::NG; ++c)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int64_t pos = pos0 + 8 * c + 2 * q + i, j = pos - si.ctx;
+                const bool on = ((there >> c) & 1u) && pos < si.len &&
+                                (j < 0 || ((bits >> (j & 63)) & 1ull));
+                see |= on ? 1u << (2 * c + i) : 0u;
+                if (!on) s[mt][c][2 * k + i] = -INFINITY;
+              }
+            seen[mt][k] = see;
+          }
+      }
+      // ---- weights
+      uint32_t a[MT][N::NG / 2][4];
+      float keep[MT][2];
+      bool grew = false;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float top = m[mt][k];
+#pragma unroll
+          for (int c = 0; c < N::NG; ++c)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              top = fmaxf(top, F16 ? s[mt][c][2 * k + i] : s[mt][c][2 * k + i] + lv[c][i]);
+          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+          keep[mt][k] = m[mt][k] == -INFINITY ? 0.0f : exp2_fast(m[mt][k] - top);
+          grew |= top != m[mt][k];
+          l[mt][k] *= keep[mt][k];
+          m[mt][k] = top;
+          const float base = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+          for (int c = 0; c < N::NG; ++c) {
+            float e[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              e[i] = exp2_fast(s[mt][c][2 * k + i] - base);
+              l[mt][k] += e[i];
+              if (!F16) e[i] = (seen[mt][k] >> (2 * c + i)) & 1u ? e[i] * vs[c][i] : 0.0f;
+            }
+            a[mt][c / 2][(c & 1) * 2 + k] = pack_half2(e[0], e[1]);
+          }
+        }
+      if (__any_sync(0xFFFFFFFFu, grew)) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int t = 0; t < N::NT; ++t) {
+              o[mt][t][2 * k] *= keep[mt][k];
+              o[mt][t][2 * k + 1] *= keep[mt][k];
+            }
+      }
+      // ---- sums
+      uint32_t bad = 0;  // bit 2c + i: the value row of position 8c + 2q + i is not finite
+#pragma unroll
+      for (int c2 = 0; c2 < N::NG / 2; ++c2) {
+#pragma unroll
+        for (int j = 0; j < N::VW; ++j) {
+          // b[x][y]: rows (2q, 2q+1) of group 2 c2 + y, columns of n-tile x
+          uint32_t b[4][2];
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const uint32_t r0 = vr[2 * c2 + y][0][j], r1 = vr[2 * c2 + y][1][j];
+            if (F16) {
+              b[0][y] = byte_perm(r0, r1, 0x5410);
+              b[1][y] = byte_perm(r0, r1, 0x7632);
+            } else {
+              widen4<TYPE>(byte_perm(r0, r1, 0x5140), b[0][y], b[1][y]);
+              widen4<TYPE>(byte_perm(r0, r1, 0x7362), b[2][y], b[3][y]);
+            }
+            if (edge) {
+#pragma unroll
+              for (int x = 0; x < (F16 ? 2 : 4); ++x) {
+                const uint32_t h = bad_halves(b[x][y]);
+                if (h) {
+                  bad |= h << (2 * (2 * c2 + y));
+                  b[x][y] &= (h & 1u ? 0u : 0xFFFFu) | (h & 2u ? 0u : 0xFFFF0000u);
+                }
+              }
+            }
+          }
+#pragma unroll
+          for (int x = 0; x < (F16 ? 2 : 4); ++x)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+              mma16816(o[mt][j * (F16 ? 2 : 4) + x], a[mt][c2], b[x][0], b[x][1]);
+        }
+      }
+      if (u + NW < w.u1) load_v(u + NW);
+      if (edge) {
+        // a value row with an infinity or NaN entered as zeros there, so that
+        // only the rows that see it are spoilt
+        bad |= __shfl_xor_sync(0xFFFFFFFFu, bad, 4);
+        bad |= __shfl_xor_sync(0xFFFFFFFFu, bad, 8);
+        bad |= __shfl_xor_sync(0xFFFFFFFFu, bad, 16);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            uint32_t hit = bad & seen[mt][k];
+            hit |= __shfl_xor_sync(0xFFFFFFFFu, hit, 1);
+            hit |= __shfl_xor_sync(0xFFFFFFFFu, hit, 2);
+            if (hit) {
+#pragma unroll
+              for (int t = 0; t < N::NT; ++t)
+                o[mt][t][2 * k] = o[mt][t][2 * k + 1] = __uint_as_float(0x7FC00000u);
+            }
+          }
+      }
+    }
+
+    // ---- join the warps: every warp's sums, maxima and weights to shared memory
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float sum = l[mt][k];
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+        const int r = 16 * mt + g + 8 * k;
+        if (q == 0) {
+          sm[warp][r] = m[mt][k];
+          sl[warp][r] = sum;
+        }
+        float* dst = so + ((size_t)warp * ROWS + r) * PITCH;
+        // n-tile t, columns 2q, 2q+1 are elements (D/8) 2q + t and (D/8)(2q+1) + t
+#pragma unroll
+        for (int t = 0; t < N::NT; ++t) {
+          dst[(D / 8) * 2 * q + t] = o[mt][t][2 * k];
+          dst[(D / 8) * (2 * q + 1) + t] = o[mt][t][2 * k + 1];
+        }
+      }
+    __syncthreads();
+    for (int r = threadIdx.x; r < ROWS; r += NTH) {
+      float M = -INFINITY, tot = 0.0f;
+      for (int x = 0; x < NW; ++x) M = fmaxf(M, sm[x][r]);
+      const float base = M == -INFINITY ? 0.0f : M;
+      for (int x = 0; x < NW; ++x) {
+        const float f = exp2_fast(sm[x][r] - base);
+        sf[x][r] = f;
+        tot += sl[x][r] * f;
+      }
+      row_m[r] = M;
+      row_l[r] = tot;
+    }
+    __syncthreads();
+    const bool whole = w.u0 == 0 && w.u1 == w.nu;
+    float* slot = slots + ((size_t)blockIdx.x * 2 + (w.start + w.u0 == sched.begin ? 0 : 1)) *
+                              attend_slot_floats(ROWS, D);
+    for (int i = threadIdx.x; i < rows * (D / 4); i += NTH) {
+      const int r = i / (D / 4), d = i % (D / 4) * 4;
+      float4 x = make_float4(0, 0, 0, 0);
+#pragma unroll
+      for (int y = 0; y < NW; ++y) {
+        const float4 v = *reinterpret_cast<const float4*>(so + ((size_t)y * ROWS + r) * PITCH + d);
+        const float f = sf[y][r];
+        x.x += v.x * f, x.y += v.y * f, x.z += v.z * f, x.w += v.w * f;
+      }
+      if (whole) {
+        const float inv = row_l[r] == 0.0f ? 0.0f : 1.0f / row_l[r];
+        const int rr = w.rt * ROWS + r;
+        __half* dst = p.out + (int64_t)(si.first + rr / G) * p.ldo + (int64_t)(w.h * G + rr % G) * D + d;
+        *reinterpret_cast<uint2*>(dst) =
+            make_uint2(pack_half2(x.x * inv, x.y * inv), pack_half2(x.z * inv, x.w * inv));
+      } else {
+        *reinterpret_cast<float4*>(slot + (size_t)r * D + d) = x;
+      }
+    }
+    for (int r = threadIdx.x; r < rows; r += NTH) {
+      if (whole) {
+        const int rr = w.rt * ROWS + r;
+        if (p.lse)
+          p.lse[(int64_t)(si.first + rr / G) * p.q_heads + w.h * G + rr % G] =
+              row_l[r] == 0.0f ? -INFINITY : (row_m[r] + log2f(row_l[r])) * kLn2;
+      } else {
+        slot[(size_t)ROWS * D + r] = row_m[r];
+        slot[(size_t)ROWS * D + ROWS + r] = row_l[r];
+      }
+    }
+    if (whole) continue;
+
+    // ---- join the blocks: the last one to store its part adds all of them
+    const int64_t b0 = sched.block_of(w.start), b1 = sched.block_of(w.start + w.nu - 1);
+    if (!last_of_item(counters + w.item, (int)(b1 - b0 + 1))) continue;
+    auto part = [&](int64_t b) {
+      return slots + ((size_t)b * 2 + (sched.block_begin(b) >= w.start ? 0 : 1)) *
+                         attend_slot_floats(ROWS, D);
+    };
+    for (int i = threadIdx.x; i < rows * (D / 4); i += NTH) {
+      const int r = i / (D / 4), d = i % (D / 4) * 4;
+      float M = -INFINITY;
+      for (int64_t b = b0; b <= b1; ++b) M = fmaxf(M, __ldcg(part(b) + (size_t)ROWS * D + r));
+      const float base = M == -INFINITY ? 0.0f : M;
+      float4 x = make_float4(0, 0, 0, 0);
+      float tot = 0.0f;
+      for (int64_t b = b0; b <= b1; ++b) {
+        const float* sp = part(b);
+        const float f = exp2_fast(__ldcg(sp + (size_t)ROWS * D + r) - base);
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(sp + (size_t)r * D + d));
+        tot += __ldcg(sp + (size_t)ROWS * D + ROWS + r) * f;
+        x.x += v.x * f, x.y += v.y * f, x.z += v.z * f, x.w += v.w * f;
+      }
+      const float inv = tot == 0.0f ? 0.0f : 1.0f / tot;
+      const int rr = w.rt * ROWS + r;
+      const int64_t t = si.first + rr / G;
+      const int hq = w.h * G + rr % G;
+      *reinterpret_cast<uint2*>(p.out + t * p.ldo + (int64_t)hq * D + d) =
+          make_uint2(pack_half2(x.x * inv, x.y * inv), pack_half2(x.z * inv, x.w * inv));
+      if (d == 0 && p.lse) p.lse[t * p.q_heads + hq] = tot == 0.0f ? -INFINITY : (M + log2f(tot)) * kLn2;
+    }
   }
-  __syncthreads();
-  float M = -INFINITY, tot = 0.0f;
-  for (int w = 0; w < NW; ++w) M = fmaxf(M, sm[w]);
-  const float base = M == -INFINITY ? 0.0f : M;
-  for (int w = 0; w < NW; ++w) tot += sl[w] * expf(sm[w] - base);
-  if (threadIdx.x < D) {
-    float x = 0.0f;
-    for (int w = 0; w < NW; ++w) x += so[w][threadIdx.x] * expf(sm[w] - base);
-    const bool none = tot == 0.0f;
-    p.out[(int64_t)t * p.ldo + (int64_t)hq * D + threadIdx.x] = __float2half_rn(none ? 0.0f : x / tot);
-    if (threadIdx.x == 0 && p.lse) p.lse[(int64_t)t * p.q_heads + hq] = none ? -INFINITY : M + logf(tot);
+}
+
+constexpr int narrow_warps(int) { return 8; }
+
+template <int D, int TYPE, int MT>
+cudaError_t narrow_one(const AttendParams& p, int sms, cudaStream_t stream) {
+  constexpr int NW = narrow_warps(MT);
+  constexpr size_t smem = (size_t)NW * 16 * MT * (D + 4) * sizeof(float);
+  auto* k = attend_narrow_kernel<D, TYPE, MT, NW>;
+  static int done[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !__atomic_load_n(&done[dev], __ATOMIC_ACQUIRE)) {
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) __atomic_store_n(&done[dev], 1, __ATOMIC_RELEASE);
   }
+  return launch_kernel(k, sms, NW * 32, smem, stream, kFlagPdl, p);
+}
+
+template <int D, int TYPE>
+cudaError_t narrow_mt(const AttendParams& p, int sms, cudaStream_t stream) {
+  const int rows = p.max_nodes * (p.q_heads / p.c.kv_heads);
+  return rows > 16 ? narrow_one<D, TYPE, 2>(p, sms, stream) : narrow_one<D, TYPE, 1>(p, sms, stream);
 }
 
 }  // namespace
 
-size_t attend_workspace_bytes(int64_t, int, int, int, int, int) { return 0; }
-
-template <int D, int TYPE>
-static cudaError_t attend_one(const AttendParams& p, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)p.tokens, (unsigned)p.q_heads);
-  cfg.blockDim = dim3(256);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attend_kernel<D, TYPE>, p);
+size_t attend_workspace_bytes(int64_t seqs, int q_heads, int kv_heads, int head_dim, int max_nodes,
+                              int sms) {
+  const int rows = max_nodes * (q_heads / kv_heads);
+  const int tile = rows > 16 ? 32 : 16;
+  return attend_counter_bytes(seqs * kv_heads * ((rows + tile - 1) / tile)) +
+         (size_t)sms * 2 * attend_slot_floats(tile, head_dim) * sizeof(float);
 }
 
 cudaError_t launch_attend(const AttendParams& p, int head_dim, int type, int sms,
                           cudaStream_t stream) {
   if (head_dim == 128) {
-    if (type == kCacheFp16) return attend_one<128, kCacheFp16>(p, stream);
-    if (type == kCacheE4m3) return attend_one<128, kCacheE4m3>(p, stream);
-    return attend_one<128, kCacheInt8>(p, stream);
+    if (type == kCacheFp16) return narrow_mt<128, kCacheFp16>(p, sms, stream);
+    if (type == kCacheE4m3) return narrow_mt<128, kCacheE4m3>(p, sms, stream);
+    return narrow_mt<128, kCacheInt8>(p, sms, stream);
   }
-  if (type == kCacheFp16) return attend_one<64, kCacheFp16>(p, stream);
-  if (type == kCacheE4m3) return attend_one<64, kCacheE4m3>(p, stream);
-  return attend_one<64, kCacheInt8>(p, stream);
+  if (type == kCacheFp16) return narrow_mt<64, kCacheFp16>(p, sms, stream);
+  if (type == kCacheE4m3) return narrow_mt<64, kCacheE4m3>(p, sms, stream);
+  return narrow_mt<64, kCacheInt8>(p, sms, stream);
 }
 
 }  // namespace nmk

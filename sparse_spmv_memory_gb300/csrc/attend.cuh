@@ -1,0 +1,221 @@
+// attend.cuh -- what the attention kernels share: the split of the work over
+// the blocks, the addresses of cache rows, and the joining of partial sums.
+//
+// Work split.  An item is a sequence, a key head and a tile of query rows (row
+// r of a sequence and key head is node r / G, query head h G + r % G, G query
+// heads sharing the key head).  An item's positions are cut into units; the
+// units of all items, one after the other, are cut evenly over the blocks
+// (lengths are known on the device only, and the longest sequence must not
+// decide).  So a block has some items whole, and at its range's two ends parts
+// of items.  A part is stored as unnormalised sums with their maxima in the
+// block's slot, and the block that completes an item's count of parts joins
+// them in block order: the result does not depend on which block that is.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include "decode.h"
+#include "device.cuh"
+
+namespace nmk {
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float exp2_fast(float x) {  // 2^x, 2^-22 relative, 0 for -inf
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float log2_fast(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// A sequence's rows and positions.
+struct SeqInfo {
+  int first;    // its first token
+  int n;        // nodes
+  int64_t ctx;  // context positions
+  int64_t len;  // positions that can be seen by some node
+};
+
+__device__ __forceinline__ SeqInfo seq_info(const AttendParams& p, int s) {
+  SeqInfo i;
+  i.first = max(p.q_start[s], 0);
+  i.n = max(0, min(min(p.q_start[s + 1], p.tokens) - i.first, p.max_nodes));
+  i.ctx = max(p.ctx_len[s], 0);
+  i.len = min(i.ctx + i.n, p.table_cols << p.c.page_shift);
+  return i;
+}
+
+struct Span {        // a part of an item that a block has: units u0 .. u1 - 1 of nu
+  int s, h, rt;      // sequence, key head, row tile
+  int u0, u1, nu;
+  int64_t start;     // the item's first unit among all units
+  int64_t item;      // its number among all items, counting row tiles to RT_MAX each
+};
+
+// The block's range of units, and the walk over its items.
+//   ROWS: rows of a tile;  UK: positions of a unit;  NT: threads of the block;
+//   min_units: units worth a block.
+template <int ROWS, int UK, int NT>
+struct Schedule {
+  int64_t total, begin, end;  // units of all items; of this block
+  int64_t blocks;             // blocks that have units
+  int64_t at;                 // where the walk is
+  int s;
+  int64_t s_start;            // first unit of sequence s
+  int rt_max;
+
+  __device__ __forceinline__ int64_t block_begin(int64_t b) const {
+    return total / blocks * b + total % blocks * b / blocks;
+  }
+  // The block that has unit u: the largest b with floor(b total / blocks) <= u.
+  __device__ __forceinline__ int64_t block_of(int64_t u) const {
+    return ((u + 1) * blocks - 1) / total;
+  }
+  static __device__ __forceinline__ int units_of(const SeqInfo& i) {
+    return (int)((i.len + UK - 1) / UK);
+  }
+  __device__ __forceinline__ int tiles_of(const AttendParams& p, const SeqInfo& i) const {
+    return (i.n * (p.q_heads / p.c.kv_heads) + ROWS - 1) / ROWS;
+  }
+
+  // All threads of the block; buf: NT + 1 words of shared memory.
+  __device__ __forceinline__ bool init(const AttendParams& p, int min_units, int64_t* buf) {
+    rt_max = (p.max_nodes * (p.q_heads / p.c.kv_heads) + ROWS - 1) / ROWS;
+    const int chunks = (p.seqs + NT - 1) / NT;
+    total = 0;
+    for (int c = 0; c < chunks; ++c) total += scan(p, c, buf);
+    blocks = min((int64_t)gridDim.x, (total + min_units - 1) / min_units);
+    if (blocks < 1) blocks = 1;
+    if (blockIdx.x >= blocks) return false;
+    begin = block_begin(blockIdx.x);
+    end = block_begin(blockIdx.x + 1);
+    if (begin >= end) return false;
+    at = begin;
+    __shared__ int found;
+    __shared__ int64_t found_start;
+    int64_t before = 0;
+    for (int c = 0; c < chunks; ++c) {
+      const int64_t sum = chunks > 1 ? scan(p, c, buf) : total;
+      if (begin < before + sum) {
+        const int i = threadIdx.x;
+        if (before + buf[i] <= begin && begin < before + buf[i + 1]) {
+          found = c * NT + i;
+          found_start = before + buf[i];
+        }
+        break;
+      }
+      before += sum;
+    }
+    __syncthreads();
+    s = found;
+    s_start = found_start;
+    return true;
+  }
+
+  // buf[i]: units of the chunk's sequences before its i-th; the chunk's sum.
+  __device__ __forceinline__ int64_t scan(const AttendParams& p, int c, int64_t* buf) {
+    const int i = c * NT + threadIdx.x;
+    int64_t v = 0;
+    if (i < p.seqs) {
+      const SeqInfo q = seq_info(p, i);
+      v = (int64_t)units_of(q) * tiles_of(p, q) * p.c.kv_heads;
+    }
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+      if (lane >= o) x += y;
+    }
+    __shared__ int64_t sums[NT / 32];
+    __syncthreads();
+    if (lane == 31) sums[warp] = x;
+    __syncthreads();
+    int64_t base = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) {
+      if (w < warp) base += sums[w];
+      all += sums[w];
+    }
+    buf[threadIdx.x] = base + x - v;
+    if (threadIdx.x == NT - 1) buf[NT] = all;
+    __syncthreads();
+    return all;
+  }
+
+  // The next part of an item; false when the range is done.
+  __device__ __forceinline__ bool next(const AttendParams& p, Span& w, SeqInfo& q) {
+    if (at >= end) return false;
+    int64_t per;
+    for (;;) {
+      q = seq_info(p, s);
+      per = (int64_t)units_of(q) * tiles_of(p, q) * p.c.kv_heads;
+      if (at < s_start + per) break;
+      s_start += per;
+      ++s;
+    }
+    const int nu = units_of(q), tiles = tiles_of(p, q);
+    const int in = (int)((at - s_start) / nu);  // item of the sequence
+    w.s = s;
+    w.h = in / tiles;
+    w.rt = in % tiles;
+    w.nu = nu;
+    w.start = s_start + (int64_t)in * nu;
+    w.u0 = (int)(at - w.start);
+    w.u1 = (int)min((int64_t)nu, end - w.start);
+    w.item = ((int64_t)s * p.c.kv_heads + w.h) * rt_max + w.rt;
+    at = w.start + w.u1;
+    return true;
+  }
+};
+
+// Workspace: a counter per item, then two slots per block of ROWS rows x (D
+// sums, maximum, sum of weights).
+__host__ __device__ constexpr size_t attend_counter_bytes(int64_t items) { return (size_t)(items + 3) / 4 * 16; }
+__host__ __device__ constexpr size_t attend_slot_floats(int rows, int d) { return (size_t)rows * (d + 2); }
+
+// Where a head's rows of positions g .. g + 7 (g a multiple of 8) begin: pages
+// hold whole groups of 8.  Negative: absent.
+struct RowAt {
+  int64_t code;   // element
+  int64_t scale;
+};
+template <int D>
+__device__ __forceinline__ RowAt group_at(const AttendParams& p, const int32_t* table, int h,
+                                          int64_t g) {
+  RowAt r{-1, -1};
+  const int64_t t = g >> p.c.page_shift;
+  if (t < p.table_cols) {
+    const int64_t page = table[t];
+    if (page >= 0 && page < p.c.pages) {
+      const int64_t in = ((int64_t)h << p.c.page_shift) + (g & ((1 << p.c.page_shift) - 1));
+      r.code = page * p.c.page_stride + in * D;
+      r.scale = page * p.c.scale_page_stride + in;
+    }
+  }
+  return r;
+}
+
+// Joins an item's parts when this block's is the last of them (all threads;
+// the block's own part is stored).  Returns false if another block will.
+__device__ __forceinline__ bool last_of_item(int* counter, int parts) {
+  __shared__ int last;
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    last = atomicAdd(counter, 1) == parts - 1;
+    if (last) *counter = 0;  // ready for the next call
+  }
+  __syncthreads();
+  const bool l = last;
+  if (l) __threadfence();
+  return l;
+}
+
+}  // namespace nmk
