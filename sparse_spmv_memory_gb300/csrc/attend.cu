@@ -130,11 +130,10 @@ __global__ void __launch_bounds__(NW * 32, 1) attend_narrow_kernel(AttendParams 
   __shared__ uint64_t smask[ROWS];
   __shared__ float sm[NW][ROWS], sl[NW][ROWS], sf[NW][ROWS];
   __shared__ float row_m[ROWS], row_l[ROWS];
-  __shared__ int64_t buf[NTH + 1];
   pdl_launch_dependents();
   pdl_wait_previous();
   Sched sched;
-  if (!sched.init(p, NW, buf)) return;
+  if (!sched.init(p, NW)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   const int G = p.q_heads / p.c.kv_heads;
   const float cs = p.scale * kLog2e;
@@ -181,13 +180,19 @@ __global__ void __launch_bounds__(NW * 32, 1) attend_narrow_kernel(AttendParams 
     uint32_t kr[N::NG][N::KW], vr[N::NG][2][N::VW];
     float ksc[N::NG][2], vsc[N::NG][2];
     RowAt at[N::NG];
+    int32_t entry[N::NG];  // table entries of the unit after the one being loaded
 
-    auto find = [&](int u) {
+    auto look_up = [&](int u) {
 #pragma unroll
       for (int c = 0; c < N::NG; ++c) {
         const int64_t pos = (int64_t)u * N::UK + 8 * c;
-        at[c] = pos < si.len ? group_at<D>(p, table, w.h, pos) : RowAt{-1, -1};
+        entry[c] = u < w.u1 && pos < si.len ? table[pos >> p.c.page_shift] : -1;
       }
+    };
+    auto find = [&](int u) {
+#pragma unroll
+      for (int c = 0; c < N::NG; ++c)
+        at[c] = group_at<D>(p, entry[c], w.h, (int64_t)u * N::UK + 8 * c);
     };
     auto load_k = [&](int u) {
 #pragma unroll
@@ -224,9 +229,11 @@ __global__ void __launch_bounds__(NW * 32, 1) attend_narrow_kernel(AttendParams 
 
     int u = w.u0 + warp;
     if (u < w.u1) {
+      look_up(u);
       find(u);
       load_k(u);
       load_v(u);
+      look_up(u + NW);
     }
     for (; u < w.u1; u += NW) {
       const int64_t pos0 = (int64_t)u * N::UK;
@@ -280,6 +287,7 @@ __global__ void __launch_bounds__(NW * 32, 1) attend_narrow_kernel(AttendParams 
       if (u + NW < w.u1) {
         find(u + NW);
         load_k(u + NW);
+        look_up(u + 2 * NW);
       }
       // ---- masks: the last units have the nodes, or end
       const bool edge = pos0 + N::UK > si.ctx || there != (1u << N::NG) - 1u;
@@ -445,8 +453,7 @@ __global__ void __launch_bounds__(NW * 32, 1) attend_narrow_kernel(AttendParams 
     }
     __syncthreads();
     const bool whole = w.u0 == 0 && w.u1 == w.nu;
-    float* slot = slots + ((size_t)blockIdx.x * 2 + (w.start + w.u0 == sched.begin ? 0 : 1)) *
-                              attend_slot_floats(ROWS, D);
+    float* slot = slots + part_slot(blockIdx.x, sched.per, w.start) * attend_slot_floats(ROWS, D);
     for (int i = threadIdx.x; i < rows * (D / 4); i += NTH) {
       const int r = i / (D / 4), d = i % (D / 4) * 4;
       float4 x = make_float4(0, 0, 0, 0);
@@ -481,32 +488,46 @@ __global__ void __launch_bounds__(NW * 32, 1) attend_narrow_kernel(AttendParams 
 
     // ---- join the blocks: the last one to store its part adds all of them
     const int64_t b0 = sched.block_of(w.start), b1 = sched.block_of(w.start + w.nu - 1);
-    if (!last_of_item(counters + w.item, (int)(b1 - b0 + 1))) continue;
-    auto part = [&](int64_t b) {
-      return slots + ((size_t)b * 2 + (sched.block_begin(b) >= w.start ? 0 : 1)) *
-                         attend_slot_floats(ROWS, D);
-    };
+    const int parts = (int)(b1 - b0 + 1);
+    if (!last_of_item(counters + w.item, parts)) continue;
+    float* factor = so;  // [parts][ROWS]
+    for (int r = threadIdx.x; r < rows; r += NTH) {
+      float M = -INFINITY, tot = 0.0f;
+      for (int y = 0; y < parts; ++y) {
+        const float* sp = slots + part_slot(b0 + y, sched.per, w.start) * attend_slot_floats(ROWS, D);
+        const float m1 = __ldcg(sp + (size_t)ROWS * D + r);
+        factor[y * ROWS + r] = m1;
+        M = fmaxf(M, m1);
+      }
+      const float base = M == -INFINITY ? 0.0f : M;
+      for (int y = 0; y < parts; ++y) {
+        const float* sp = slots + part_slot(b0 + y, sched.per, w.start) * attend_slot_floats(ROWS, D);
+        const float f = exp2_fast(factor[y * ROWS + r] - base);
+        factor[y * ROWS + r] = f;
+        tot += __ldcg(sp + (size_t)ROWS * D + ROWS + r) * f;
+      }
+      row_l[r] = tot == 0.0f ? 0.0f : 1.0f / tot;
+      const int rr = w.rt * ROWS + r;
+      if (p.lse)
+        p.lse[(int64_t)(si.first + rr / G) * p.q_heads + w.h * G + rr % G] =
+            tot == 0.0f ? -INFINITY : (M + log2f(tot)) * kLn2;
+    }
+    __syncthreads();
     for (int i = threadIdx.x; i < rows * (D / 4); i += NTH) {
       const int r = i / (D / 4), d = i % (D / 4) * 4;
-      float M = -INFINITY;
-      for (int64_t b = b0; b <= b1; ++b) M = fmaxf(M, __ldcg(part(b) + (size_t)ROWS * D + r));
-      const float base = M == -INFINITY ? 0.0f : M;
       float4 x = make_float4(0, 0, 0, 0);
-      float tot = 0.0f;
-      for (int64_t b = b0; b <= b1; ++b) {
-        const float* sp = part(b);
-        const float f = exp2_fast(__ldcg(sp + (size_t)ROWS * D + r) - base);
+#pragma unroll 8
+      for (int y = 0; y < parts; ++y) {
+        const float* sp = slots + part_slot(b0 + y, sched.per, w.start) * attend_slot_floats(ROWS, D);
         const float4 v = __ldcg(reinterpret_cast<const float4*>(sp + (size_t)r * D + d));
-        tot += __ldcg(sp + (size_t)ROWS * D + ROWS + r) * f;
+        const float f = factor[y * ROWS + r];
         x.x += v.x * f, x.y += v.y * f, x.z += v.z * f, x.w += v.w * f;
       }
-      const float inv = tot == 0.0f ? 0.0f : 1.0f / tot;
+      const float inv = row_l[r];
       const int rr = w.rt * ROWS + r;
-      const int64_t t = si.first + rr / G;
-      const int hq = w.h * G + rr % G;
-      *reinterpret_cast<uint2*>(p.out + t * p.ldo + (int64_t)hq * D + d) =
+      *reinterpret_cast<uint2*>(p.out + (int64_t)(si.first + rr / G) * p.ldo +
+                                (int64_t)(w.h * G + rr % G) * D + d) =
           make_uint2(pack_half2(x.x * inv, x.y * inv), pack_half2(x.z * inv, x.w * inv));
-      if (d == 0 && p.lse) p.lse[t * p.q_heads + hq] = tot == 0.0f ? -INFINITY : (M + log2f(tot)) * kLn2;
     }
   }
 }

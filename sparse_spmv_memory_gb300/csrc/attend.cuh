@@ -58,59 +58,94 @@ struct Span {        // a part of an item that a block has: units u0 .. u1 - 1 o
   int64_t item;      // its number among all items, counting row tiles to RT_MAX each
 };
 
+// a / b for 0 <= a, 0 < b: a 64-bit division is some hundred instructions, and
+// in nearly every call both numbers fit 32 bits.
+__device__ __forceinline__ int64_t div_units(int64_t a, int64_t b) {
+  if ((((uint64_t)a | (uint64_t)b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
+
 // The block's range of units, and the walk over its items.
 //   ROWS: rows of a tile;  UK: positions of a unit;  NT: threads of the block;
 //   min_units: units worth a block.
 template <int ROWS, int UK, int NT>
 struct Schedule {
-  int64_t total, begin, end;  // units of all items; of this block
-  int64_t blocks;             // blocks that have units
-  int64_t at;                 // where the walk is
+  int64_t per;         // units of a block (the last one's may be fewer)
+  int64_t begin, end;  // this block's
+  int64_t at;          // where the walk is
+  int64_t s_start;     // first unit of sequence s
   int s;
-  int64_t s_start;            // first unit of sequence s
   int rt_max;
 
-  __device__ __forceinline__ int64_t block_begin(int64_t b) const {
-    return total / blocks * b + total % blocks * b / blocks;
-  }
-  // The block that has unit u: the largest b with floor(b total / blocks) <= u.
-  __device__ __forceinline__ int64_t block_of(int64_t u) const {
-    return ((u + 1) * blocks - 1) / total;
-  }
+  __device__ __forceinline__ int64_t block_of(int64_t u) const { return div_units(u, per); }
   static __device__ __forceinline__ int units_of(const SeqInfo& i) {
     return (int)((i.len + UK - 1) / UK);
   }
   __device__ __forceinline__ int tiles_of(const AttendParams& p, const SeqInfo& i) const {
     return (i.n * (p.q_heads / p.c.kv_heads) + ROWS - 1) / ROWS;
   }
+  __device__ __forceinline__ int64_t seq_units(const AttendParams& p, int i) const {
+    if (i >= p.seqs) return 0;
+    const SeqInfo q = seq_info(p, i);
+    return (int64_t)units_of(q) * tiles_of(p, q) * p.c.kv_heads;
+  }
+  __device__ __forceinline__ bool take(int64_t total, int min_units) {
+    per = max(div_units(total + gridDim.x - 1, gridDim.x), (int64_t)min_units);
+    begin = at = per * blockIdx.x;
+    end = min(begin + per, total);
+    return begin < end;
+  }
 
-  // All threads of the block; buf: NT + 1 words of shared memory.
-  __device__ __forceinline__ bool init(const AttendParams& p, int min_units, int64_t* buf) {
+  // All threads of the block; false: nothing to do.
+  __device__ __forceinline__ bool init(const AttendParams& p, int min_units) {
     rt_max = (p.max_nodes * (p.q_heads / p.c.kv_heads) + ROWS - 1) / ROWS;
-    const int chunks = (p.seqs + NT - 1) / NT;
-    total = 0;
-    for (int c = 0; c < chunks; ++c) total += scan(p, c, buf);
-    blocks = min((int64_t)gridDim.x, (total + min_units - 1) / min_units);
-    if (blocks < 1) blocks = 1;
-    if (blockIdx.x >= blocks) return false;
-    begin = block_begin(blockIdx.x);
-    end = block_begin(blockIdx.x + 1);
-    if (begin >= end) return false;
-    at = begin;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (p.seqs <= 32) {  // every warp by itself: no barrier
+      const int64_t v = seq_units(p, lane);
+      int64_t x = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (!take(__shfl_sync(0xFFFFFFFFu, x, 31), min_units)) return false;
+      const uint32_t mine = __ballot_sync(0xFFFFFFFFu, x > begin);
+      s = __ffs(mine) - 1;
+      s_start = __shfl_sync(0xFFFFFFFFu, x - v, s);
+      return true;
+    }
+    __shared__ int64_t sums[NT / 32];
     __shared__ int found;
     __shared__ int64_t found_start;
-    int64_t before = 0;
-    for (int c = 0; c < chunks; ++c) {
-      const int64_t sum = chunks > 1 ? scan(p, c, buf) : total;
-      if (begin < before + sum) {
-        const int i = threadIdx.x;
-        if (before + buf[i] <= begin && begin < before + buf[i + 1]) {
-          found = c * NT + i;
-          found_start = before + buf[i];
+    int64_t mine = 0;
+    for (int i = threadIdx.x; i < p.seqs; i += NT) mine += seq_units(p, i);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, o);
+    if (lane == 0) sums[warp] = mine;
+    __syncthreads();
+    int64_t total = 0;
+    for (int w = 0; w < NT / 32; ++w) total += sums[w];
+    if (!take(total, min_units)) return false;
+    if (warp == 0) {  // the sequence that has unit `begin`
+      int64_t before = 0;
+      for (int c = 0; c < p.seqs; c += 32) {
+        const int64_t v = seq_units(p, c + lane);
+        int64_t x = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+          if (lane >= o) x += y;
         }
-        break;
+        const uint32_t past = __ballot_sync(0xFFFFFFFFu, before + x > begin);
+        if (past) {
+          if (lane == __ffs(past) - 1) {
+            found = c + lane;
+            found_start = before + x - v;
+          }
+          break;
+        }
+        before += __shfl_sync(0xFFFFFFFFu, x, 31);
       }
-      before += sum;
     }
     __syncthreads();
     s = found;
@@ -118,50 +153,20 @@ struct Schedule {
     return true;
   }
 
-  // buf[i]: units of the chunk's sequences before its i-th; the chunk's sum.
-  __device__ __forceinline__ int64_t scan(const AttendParams& p, int c, int64_t* buf) {
-    const int i = c * NT + threadIdx.x;
-    int64_t v = 0;
-    if (i < p.seqs) {
-      const SeqInfo q = seq_info(p, i);
-      v = (int64_t)units_of(q) * tiles_of(p, q) * p.c.kv_heads;
-    }
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t x = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
-      if (lane >= o) x += y;
-    }
-    __shared__ int64_t sums[NT / 32];
-    __syncthreads();
-    if (lane == 31) sums[warp] = x;
-    __syncthreads();
-    int64_t base = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < NT / 32; ++w) {
-      if (w < warp) base += sums[w];
-      all += sums[w];
-    }
-    buf[threadIdx.x] = base + x - v;
-    if (threadIdx.x == NT - 1) buf[NT] = all;
-    __syncthreads();
-    return all;
-  }
-
   // The next part of an item; false when the range is done.
   __device__ __forceinline__ bool next(const AttendParams& p, Span& w, SeqInfo& q) {
     if (at >= end) return false;
-    int64_t per;
+    int nu, tiles;
     for (;;) {
       q = seq_info(p, s);
-      per = (int64_t)units_of(q) * tiles_of(p, q) * p.c.kv_heads;
-      if (at < s_start + per) break;
-      s_start += per;
+      nu = units_of(q);
+      tiles = tiles_of(p, q);
+      const int64_t all = (int64_t)nu * tiles * p.c.kv_heads;
+      if (at < s_start + all) break;
+      s_start += all;
       ++s;
     }
-    const int nu = units_of(q), tiles = tiles_of(p, q);
-    const int in = (int)((at - s_start) / nu);  // item of the sequence
+    const int in = (int)div_units(at - s_start, nu);  // item of the sequence
     w.s = s;
     w.h = in / tiles;
     w.rt = in % tiles;
@@ -180,24 +185,25 @@ struct Schedule {
 __host__ __device__ constexpr size_t attend_counter_bytes(int64_t items) { return (size_t)(items + 3) / 4 * 16; }
 __host__ __device__ constexpr size_t attend_slot_floats(int rows, int d) { return (size_t)rows * (d + 2); }
 
+// The slot that block b has an item's part in: its first where its range begins
+// inside the item (or with it), else its second.
+__device__ __forceinline__ int64_t part_slot(int64_t b, int64_t per, int64_t item_start) {
+  return b * 2 + (b * per >= item_start ? 0 : 1);
+}
+
 // Where a head's rows of positions g .. g + 7 (g a multiple of 8) begin: pages
 // hold whole groups of 8.  Negative: absent.
 struct RowAt {
   int64_t code;   // element
   int64_t scale;
 };
-template <int D>
-__device__ __forceinline__ RowAt group_at(const AttendParams& p, const int32_t* table, int h,
-                                          int64_t g) {
+template <int D>  // page: the table's entry for them
+__device__ __forceinline__ RowAt group_at(const AttendParams& p, int64_t page, int h, int64_t g) {
   RowAt r{-1, -1};
-  const int64_t t = g >> p.c.page_shift;
-  if (t < p.table_cols) {
-    const int64_t page = table[t];
-    if (page >= 0 && page < p.c.pages) {
-      const int64_t in = ((int64_t)h << p.c.page_shift) + (g & ((1 << p.c.page_shift) - 1));
-      r.code = page * p.c.page_stride + in * D;
-      r.scale = page * p.c.scale_page_stride + in;
-    }
+  if (page >= 0 && page < p.c.pages) {
+    const int64_t in = ((int64_t)h << p.c.page_shift) + (g & ((1 << p.c.page_shift) - 1));
+    r.code = page * p.c.page_stride + in * D;
+    r.scale = page * p.c.scale_page_stride + in;
   }
   return r;
 }
