@@ -8,6 +8,7 @@
 #include <atomic>
 
 #include "../../include/nm_spmv.h"
+#include "decode.h"
 #include "kernels.h"
 
 namespace nmk {
@@ -731,8 +732,11 @@ int nm_prefill_stall_selftest(const void* values, const uint32_t* masks, int64_t
 }
 
 int64_t nm_wait_timeouts(int reset) {
-  unsigned long long n = 0;
-  return read_wait_timeouts(&n, reset) == cudaSuccess ? (int64_t)n : -NM_ERR_CUDA;
+  unsigned long long n = 0, m = 0;
+  if (read_wait_timeouts(&n, reset) != cudaSuccess ||
+      read_attend_wait_timeouts(&m, reset) != cudaSuccess)
+    return -NM_ERR_CUDA;
+  return (int64_t)(n + m);
 }
 
 int64_t nm_check_masks(const uint32_t* masks, int64_t rows, int64_t cols, void* stream) {

@@ -8,7 +8,6 @@
 // 2^(m - m'), so one pass over the cache does, and parts with their own m join
 // by the same rule.
 #include <cuda_fp16.h>
-#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -16,6 +15,7 @@
 #include "decode.h"
 #include "device.cuh"
 #include "kernels.h"
+#include "widen.cuh"
 
 namespace nmk {
 namespace {
@@ -41,37 +41,6 @@ __device__ __forceinline__ void load_words(const uint8_t* at, bool on, uint32_t*
   }
 }
 
-__device__ __forceinline__ uint32_t byte_perm(uint32_t a, uint32_t b, uint32_t sel) {
-  uint32_t r;
-  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
-  return r;
-}
-
-// Two codes in the low 16 bits -> two fp16, exactly (e4m3, NaN included).
-__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t two) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(r) : "r"(two));
-  return r;
-}
-
-// Four codes of a word -> two words of two fp16.  int8: the byte with its sign
-// bit flipped under 0x64 is the fp16 1024 + 128 + code.
-template <int TYPE>
-__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  if (TYPE == kCacheE4m3) {
-    lo = e4m3x2_to_half2(w);
-    hi = e4m3x2_to_half2(w >> 16);
-  } else {
-    const uint32_t u = w ^ 0x80808080u;
-    const __half2 off = __half2half2(__ushort_as_half(0x6480));  // 1152
-    uint32_t a = byte_perm(u, 0x64646464u, 0x4140), b = byte_perm(u, 0x64646464u, 0x4342);
-    __half2 x = __hsub2(*reinterpret_cast<__half2*>(&a), off);
-    __half2 y = __hsub2(*reinterpret_cast<__half2*>(&b), off);
-    lo = *reinterpret_cast<uint32_t*>(&x);
-    hi = *reinterpret_cast<uint32_t*>(&y);
-  }
-}
-
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
   asm volatile(
@@ -84,11 +53,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// Halves of w that are infinite or NaN: bit 0, bit 1.
-__device__ __forceinline__ uint32_t bad_halves(uint32_t w) {
-  return ((w & 0x7C00u) == 0x7C00u ? 1u : 0u) | ((w & 0x7C000000u) == 0x7C000000u ? 2u : 0u);
 }
 
 // ---- the kernel for few rows ------------------------------------------------------
@@ -559,9 +523,14 @@ cudaError_t narrow_mt(const AttendParams& p, int sms, cudaStream_t stream) {
 
 }  // namespace
 
+// Rows of a sequence and key head from which the tcgen05 kernel takes over.
+constexpr int kWideRows = 33;
+
 size_t attend_workspace_bytes(int64_t seqs, int q_heads, int kv_heads, int head_dim, int max_nodes,
                               int sms) {
   const int rows = max_nodes * (q_heads / kv_heads);
+  if (rows >= kWideRows)
+    return attend_wide_workspace_bytes(seqs * kv_heads * ((rows + 127) / 128), head_dim, sms);
   const int tile = rows > 16 ? 32 : 16;
   return attend_counter_bytes(seqs * kv_heads * ((rows + tile - 1) / tile)) +
          (size_t)sms * 2 * attend_slot_floats(tile, head_dim) * sizeof(float);
@@ -569,6 +538,8 @@ size_t attend_workspace_bytes(int64_t seqs, int q_heads, int kv_heads, int head_
 
 cudaError_t launch_attend(const AttendParams& p, int head_dim, int type, int sms,
                           cudaStream_t stream) {
+  if (p.max_nodes * (p.q_heads / p.c.kv_heads) >= kWideRows)
+    return launch_attend_wide(p, head_dim, type, sms, stream);
   if (head_dim == 128) {
     if (type == kCacheFp16) return narrow_mt<128, kCacheFp16>(p, sms, stream);
     if (type == kCacheE4m3) return narrow_mt<128, kCacheE4m3>(p, sms, stream);

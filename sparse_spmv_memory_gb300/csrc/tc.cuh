@@ -8,16 +8,17 @@
 namespace nmk {
 
 // Number of mbarrier waits that gave up (see mbar_wait); read and reset by
-// nm_wait_timeouts().  Zero in every correct run.  Defined here because one
-// translation unit (prefill.cu) includes this header.
-__device__ unsigned long long g_wait_timeouts = 0;
+// nm_wait_timeouts().  Zero in every correct run.  Each translation unit that
+// includes this header (prefill.cu, attend_wide.cu) has a counter and a flag of
+// its own; nm_wait_timeouts adds the counters and clears the flags.
+static __device__ unsigned long long g_wait_timeouts = 0;
 
 // Set by the first wait that gives up; every later abortable wait (in any
 // block, and in later launches until nm_wait_timeouts(1) clears it) gives up
 // at once, and new blocks return before allocating anything, so one lost
 // arrival ends the whole launch after one wait limit instead of one limit per
 // wait per block.
-__device__ unsigned int g_wait_abort = 0;
+static __device__ unsigned int g_wait_abort = 0;
 
 __device__ __forceinline__ bool wait_aborted() {
   return *(volatile unsigned int*)&g_wait_abort != 0u;
@@ -65,6 +66,19 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(done)
       : "r"(bar), "r"(parity), "r"(kSuspendNs)
+      : "memory");
+  return done != 0;
+}
+
+// One test of the barrier phase, without suspending.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
       : "memory");
   return done != 0;
 }
@@ -183,6 +197,33 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(uint32_t M, uint32_t N) {
   return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
+// Shared-memory matrix descriptor of a tile whose 128-byte rows (64 fp16) have
+// the 128-byte swizzle, 8-row groups 1024 bytes apart.  A K-major operand's
+// rows run along K and `lbo` is unused; an MN-major one's run along M or N, a
+// group of 8 rows is 8 steps of K, and the next 64 of M or N begin `lbo` bytes on.
+__device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr, uint32_t lbo) {
+  uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1u << 46;
+  d |= (uint64_t)2u << 61;
+  return d;
+}
+
+// The bit of the instruction descriptor that makes B MN-major.
+constexpr uint32_t kIdescBMajorMN = 1u << 16;
+
+// D[tmem] (+)= A[tmem] * B[smem]^T: A's row m in lane m, two fp16 of K a column.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                           uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 // D[tmem] (+)= A[smem] * B[smem]^T, issued by one thread.
 __device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                         uint32_t idesc, uint32_t accumulate) {
@@ -213,6 +254,41 @@ __device__ __forceinline__ void tmem_ld_32(uint32_t taddr, uint32_t (&v)[32]) {
         "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
       : "r"(taddr)
       : "memory");
+}
+
+// 16 and 32 columns of this warp's 32 TMEM lanes, stored.
+__device__ __forceinline__ void tmem_st_16(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_32(uint32_t taddr, const uint32_t (&v)[32]) {
+  tmem_st_16(taddr, v);
+  tmem_st_16(taddr + 16, v + 16);
+}
+
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// 16-byte asynchronous copy global -> shared; src_bytes = 0 writes zeros.
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, uint32_t src_bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(src_bytes)
+               : "memory");
+}
+
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void cp_async_wait_group() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ void tmem_ld_wait() {
