@@ -530,7 +530,7 @@ size_t attend_workspace_bytes(int64_t seqs, int q_heads, int kv_heads, int head_
                               int sms) {
   const int rows = max_nodes * (q_heads / kv_heads);
   if (rows >= kWideRows)
-    return attend_wide_workspace_bytes(seqs * kv_heads * ((rows + 127) / 128), head_dim, sms);
+    return attend_wide_workspace_bytes(seqs, kv_heads, rows, head_dim, sms);
   const int tile = rows > 16 ? 32 : 16;
   return attend_counter_bytes(seqs * kv_heads * ((rows + tile - 1) / tile)) +
          (size_t)sms * 2 * attend_slot_floats(tile, head_dim) * sizeof(float);

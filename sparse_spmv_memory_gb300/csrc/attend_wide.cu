@@ -1,13 +1,14 @@
 // attend_wide.cu -- nm_tree_attention for many query rows per key head: 128
 // rows at a time on tcgen05.
 //
-// A block has 128 query rows in shared memory and walks the positions in tiles
-// of 128.  Two streams take the tiles in turn, each with a score tile, sums and
-// running maxima of its own, so that one's softmax runs while the tensor core
-// works for the other; they join at the item's end (attend.cu has the rule).
+// A block walks the positions in tiles of 128.  Two streams, each with a score
+// tile, sums and running maxima of its own, keep the tensor core and the
+// softmax busy at the same time: with more than 128 rows (PAIR) they are two
+// row tiles that share every K and V tile, with fewer they take the tiles of
+// one row tile in turn and join at the item's end (attend.cu has the rule).
 //   loaders  bring K and V tiles into a ring of stages of fp16, 128-byte
-//            swizzled rows: cp.async for an fp16 cache; codes go through a raw
-//            ring (every thread copies, widens and stores pieces of its own).
+//            swizzled rows: TMA boxes of whole pages for an fp16 cache; codes
+//            come by bulk copies into a raw ring and are widened by the warps.
 //   MMA      one thread: S = Q K^T into TMEM; O += P V with P from TMEM and V
 //            as the MN-major operand (its rows are the reduction's).
 //   softmax  two warpgroups, a query row per thread: scores from TMEM, weights
@@ -18,15 +19,18 @@
 // 2^(s_j + log2 v_j - m), v_j the row's scale, and the sum of weights adds
 // w_j / v_j; a key's scale multiplies its score.  So codes enter the MMA
 // exactly and a weight is rounded once.
+#include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+#include <string.h>
 
 #include "attend.cuh"
 #include "decode.h"
 #include "device.cuh"
 #include "kernels.h"
 #include "tc.cuh"
+#include "tmap.h"
 #include "widen.cuh"
 
 namespace nmk {
@@ -34,44 +38,60 @@ namespace {
 
 constexpr int kRows = 128, kKeys = 128;
 constexpr int kSoftWarps = 8, kMmaWarp = 8, kLoadWarp = 9;
-constexpr int kMeta = 8;    // tiles whose scales are kept (see Wide)
+constexpr int kMeta = 8;    // tiles whose scales and pages are kept
 constexpr int kBad = 16;    // items whose spoilt nodes are kept
 constexpr float kGrow = 8.0f;
-constexpr float kTinyScale = 7.888609052210118e-31f;  // 2^-100: a zero scale counts as this
+constexpr float kTinyScale = 7.888609052210118e-31f;  // 2^-100: a smaller scale counts as this
 
-template <int D, int TYPE>
+// A slot of a tile (item) is written again kMeta (kBad) tiles (items) on.  A
+// loader is at most NS + RS <= 10 positions of the ring ahead of the MMAs, and
+// a tile's softmax is over when its V tile is consumed: 13 positions before
+// the slot's next K tile at least; an item takes two positions or more.
+template <int D, int TYPE, bool PAIR>
 struct Wide {
   static constexpr bool F16 = TYPE == kCacheFp16;
-  static constexpr int LW = F16 ? 4 : 8;  // loader warps
+  static constexpr int LW = F16 ? 3 : 7;  // loader warps: 384 or 512 threads
   static constexpr int THREADS = 32 * (kLoadWarp + LW);
+  static constexpr int QT = PAIR ? 2 : 1;     // row tiles of an item
   static constexpr int TILE = kKeys * D * 2;  // bytes of a stage
   static constexpr int HALF = kKeys * 128;    // 64 elements of every row
-  // K and V tiles in the order of their use; at most 8 (a slot of kMeta is
-  // written again 8 tiles on, when at least the tile 4 before was consumed)
-  static constexpr int NS = F16 ? (D == 128 ? 5 : 8) : (D == 128 ? 3 : 6);
-  static constexpr int LAG = 3;               // fp16: positions copied ahead of their announcement
-  static constexpr int RS = F16 ? 0 : 4;      // raw tiles in flight
+  static constexpr int NS = F16 ? (D == 128 ? (PAIR ? 4 : 5) : 8) : (D == 128 ? 3 : 6);
+  static constexpr int RS = F16 ? 0 : (D == 128 ? (PAIR ? 2 : 4) : 4);  // raw tiles
   static constexpr int RAW = kKeys * D;
   static constexpr int Q_OFF = 0;
-  static constexpr int ST_OFF = Q_OFF + kRows * D * 2;
+  static constexpr int ST_OFF = Q_OFF + QT * kRows * D * 2;
   static constexpr int RAW_OFF = ST_OFF + NS * TILE;
-  static constexpr int SC_OFF = RAW_OFF + RS * RAW;  // 8-bit: raw k, raw v, k', log2 v, 1 / v
-  static constexpr int BYTES = SC_OFF + (F16 ? 0 : 5 * kMeta * kKeys * 4);
+  static constexpr int SC_OFF = RAW_OFF + RS * RAW;  // 8-bit: k scale', log2 v, 1 / v
+  static constexpr int BYTES = SC_OFF + (F16 ? 0 : 3 * kMeta * kKeys * 4);
   static constexpr int SMEM = BYTES + 1024;   // room to align the base
   static_assert(SMEM <= 227 * 1024 - 4096, "static shared memory needs room too");
-  static_assert(NS <= 8 && (!F16 || LAG < NS), "see above");
+  static_assert(NS + RS <= 10 && NS <= 8, "see above");
 };
 
 // TMEM columns.
 constexpr uint32_t kS0 = 0, kS1 = 128, kO0 = 256, kO1 = 384, kTmemCols = 512;
 
-template <int D, int TYPE>
-__global__ void __launch_bounds__(Wide<D, TYPE>::THREADS, 1) attend_wide_kernel(AttendParams p) {
-  using W = Wide<D, TYPE>;
+__device__ __forceinline__ uint32_t half2_of(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ void sts_v4(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+
+template <int D, int TYPE, bool PAIR>
+__global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
+    attend_wide_kernel(const __grid_constant__ AttendParams p, const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_v) {
+  using W = Wide<D, TYPE, PAIR>;
   constexpr bool F16 = W::F16;
-  using Sched = Schedule<kRows, kKeys, W::THREADS>;
+  constexpr int RS = F16 ? 1 : W::RS;
+  constexpr int IROWS = W::QT * kRows;  // rows of an item
+  using Sched = Schedule<IROWS, kKeys, W::THREADS>;
   extern __shared__ uint8_t raw_smem[];
-  __shared__ uint64_t bar_mem[2 * W::NS + 8];
+  __shared__ uint64_t bar_mem[2 * W::NS + 8 + 2 * RS];
   __shared__ uint32_t tmem_slot, s_last;
   __shared__ uint32_t there_of[kMeta];
   __shared__ uint32_t bad_of[kBad][2];
@@ -87,6 +107,8 @@ __global__ void __launch_bounds__(Wide<D, TYPE>::THREADS, 1) attend_wide_kernel(
   auto pfull = [&](int b) { return bars + 8u * (2 * W::NS + 2 + b); };  // weights ready
   auto ofull = [&](int b) { return bars + 8u * (2 * W::NS + 4 + b); };  // sums ready
   const uint32_t qfull = bars + 8u * (2 * W::NS + 6), soft = bars + 8u * (2 * W::NS + 7);
+  auto rfull = [&](int s) { return bars + 8u * (2 * W::NS + 8 + s); };        // raw tile landed
+  auto rfree = [&](int s) { return bars + 8u * (2 * W::NS + 8 + RS + s); };   // ... and read
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_launch_dependents();
@@ -100,6 +122,10 @@ __global__ void __launch_bounds__(Wide<D, TYPE>::THREADS, 1) attend_wide_kernel(
       mbar_init(full(s), W::LW);
       mbar_init(empty(s), 1);
     }
+    for (int s = 0; s < RS; ++s) {
+      mbar_init(rfull(s), 1);
+      mbar_init(rfree(s), W::LW);
+    }
     for (int b = 0; b < 2; ++b) {
       mbar_init(sfull(b), 1);
       mbar_init(pfull(b), 4);
@@ -108,6 +134,10 @@ __global__ void __launch_bounds__(Wide<D, TYPE>::THREADS, 1) attend_wide_kernel(
     mbar_init(qfull, kSoftWarps);
     mbar_init(soft, kSoftWarps);
     fence_mbar_init();
+    if (F16) {
+      prefetch_tmap(&tm_k);
+      prefetch_tmap(&tm_v);
+    }
   }
   if (threadIdx.x < kBad * 2) bad_of[threadIdx.x / 2][threadIdx.x % 2] = 0;
   if (warp == kMmaWarp) {
@@ -126,216 +156,270 @@ __global__ void __launch_bounds__(Wide<D, TYPE>::THREADS, 1) attend_wide_kernel(
 
   if (warp >= kLoadWarp) {
     // ---- loaders ---------------------------------------------------------------
-    const int lw = warp - kLoadWarp;
-    int c = 0, said = 0;  // positions of the ring issued and announced
-    int tile_no = 0, item_no = 0;
+    const int lw = warp - kLoadWarp, lt = lw * 32 + lane;
+    constexpr int LT = W::LW * 32;
+    const int page_rows = min(1 << p.c.page_shift, kKeys);  // rows of a box
+    const int boxes = kKeys / page_rows;                    // of a tile
+    int c = 0;  // positions of the ring so far
+    int item_no = 0;
     bool ok = true;
-    auto announce = [&](int upto) {
-      for (; said < upto; ++said) {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(full(said % W::NS));
+    struct Tile {     // what the ring's position c holds
+      int64_t pos0;   // its first position
+      RowAt at;       // lane l < 16: its l-th group of 8 rows,
+      int page, row;  // in this page at this row (of all heads')
+      uint32_t there; // groups that are there
+      int left;       // rows before the sequence's end
+      bool edge;      // has nodes, or absent rows
+      int node0;      // node number of its first row (far below 0: none near)
+      int bad, meta;  // slots
+    };
+    auto note = [&](const Tile& t, bool first) {  // a K tile's slots (one warp)
+      if (lane == 0) {
+        there_of[t.meta] = t.there;
+        if (first)
+          bad_of[(item_no + kBad / 2) % kBad][0] = bad_of[(item_no + kBad / 2) % kBad][1] = 0;
       }
     };
-    auto acquire = [&](int pos) {  // the stage of ring position pos
-      if (pos < W::NS) return true;
-      return wait_warp(empty(pos % W::NS), (pos / W::NS - 1) & 1);
+    // Clears halves that are not finite in a node's value row and notes the node:
+    // an infinity or NaN must not meet a weight of 0.
+    auto clean = [&](uint32_t* h, int words, int node, int slot) {
+      uint32_t any = 0;
+      for (int y = 0; y < words; ++y) {
+        const uint32_t b = bad_halves(h[y]);
+        any |= b;
+        h[y] &= (b & 1u ? 0u : 0xFFFFu) | (b & 2u ? 0u : 0xFFFF0000u);
+      }
+      if (any) atomicOr(&bad_of[slot][(node >> 5) & 1], 1u << (node & 31));
     };
-    struct Raw {  // what a raw tile is (8-bit)
-      int v, edge, node0, bad, meta;
-    };
-    Raw ring[F16 ? 1 : W::RS];
 
-    // 8-bit: widen the pieces that this thread copied for position pos.
-    auto convert = [&](int pos, const Raw& t) {
-      if (!acquire(pos)) return false;
-      const uint32_t dst = sT + (pos % W::NS) * W::TILE;
-      const uint32_t src = base + W::RAW_OFF + (pos % (F16 ? 1 : W::RS)) * W::RAW;
-      constexpr int PR = D / 16;  // pieces of a row
-      const int lt = lw * 32 + lane;
+    // fp16: the ring's next position is K (v false) or V of tile t.
+    auto emit16 = [&](bool v, const Tile& t, bool first) {
+      const int st = c % W::NS;
+      if (c >= W::NS && !wait_warp(empty(st), (c / W::NS - 1) & 1)) return false;
+      const uint32_t dst = sT + st * W::TILE;
+      if (!v && lw == 0) note(t, first);
+      if (v && t.edge) {  // absent rows are zeros, nodes' rows are looked at
+        constexpr int PR = D / 8;
+        for (int id0 = 0; id0 < kKeys * PR; id0 += LT) {
+          const int id = id0 + lt, r = min(id / PR, kKeys - 1), ch = id % PR;
+          const int64_t code = __shfl_sync(0xFFFFFFFFu, t.at.code, r >> 3);
+          if (id >= kKeys * PR) continue;
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if (code >= 0 && r < t.left) x = ld_stream_v4(p.c.v + (code + (r & 7) * D + ch * 8) * 2);
+          uint32_t h[4] = {x.x, x.y, x.z, x.w};
+          if (t.node0 + r >= 0) clean(h, 4, t.node0 + r, t.bad);
+          sts_v4(dst + (ch >> 3) * W::HALF + r * 128 + (((ch & 7) ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full(st));
+      } else {
+        if (lw == 0) {
+          // box l: the page rows of group l * page_rows / 8, for lane l < boxes
+          const int group = (lane * page_rows >> 3) & 15;
+          const int page = __shfl_sync(0xFFFFFFFFu, t.page, group), row = __shfl_sync(0xFFFFFFFFu, t.row, group);
+          const bool on = lane < boxes && ((t.there >> group) & 1u);
+          const int have = __popc(__ballot_sync(0xFFFFFFFFu, on));
+          if (lane == 0) mbar_arrive_expect_tx(full(st), have * page_rows * D * 2);
+          __syncwarp();
+          if (on) {
 #pragma unroll
-      for (int i = 0; i < kKeys * PR / (W::LW * 32); ++i) {
-        const int id = lt + i * W::LW * 32, r = id / PR, ch = id % PR;
+            for (int hf = 0; hf < D / 64; ++hf)
+              tma_load_3d(dst + hf * W::HALF + lane * page_rows * 128, v ? &tm_v : &tm_k, hf * 64, row,
+                          page, full(st));
+          }
+        } else if (lane == 0) {
+          mbar_arrive(full(st));
+        }
+        __syncwarp();
+      }
+      ++c;
+      return true;
+    };
+
+    // 8-bit: raw position rc is K or V of tile t: bulk copies of page pieces.
+    auto fetch8 = [&](int rc, bool v, const Tile& t) {
+      if (lw != 0) return true;
+      const int st = rc % RS;
+      if (rc >= RS && !wait_warp(rfree(st), (rc / RS - 1) & 1)) return false;
+      const int64_t code = __shfl_sync(0xFFFFFFFFu, t.at.code, (lane * page_rows >> 3) & 15);
+      const bool on = lane < boxes && code >= 0;
+      const int have = __popc(__ballot_sync(0xFFFFFFFFu, on));
+      if (lane == 0) mbar_arrive_expect_tx(rfull(st), have * page_rows * D);
+      __syncwarp();
+      if (on)
+        bulk_load(base + W::RAW_OFF + st * W::RAW + lane * page_rows * D, (v ? p.c.v : p.c.k) + code,
+                  page_rows * D, rfull(st));
+      __syncwarp();
+      return true;
+    };
+    float sc_k = 0.0f, sc_v = 0.0f;  // thread lt < 128: the next tile's scales of row lt
+    auto load_scales = [&](const Tile& t) {
+      const int r = lt & (kKeys - 1);
+      const int64_t at = __shfl_sync(0xFFFFFFFFu, t.at.scale, r >> 3);
+      const bool on = lt < kKeys && at >= 0 && r < t.left;
+      sc_k = on ? p.c.k_scale[at + (r & 7)] : 0.0f;
+      sc_v = on ? p.c.v_scale[at + (r & 7)] : 0.0f;
+    };
+    // Widens the raw tile of position c into its stage.
+    auto emit8 = [&](bool v, const Tile& t, bool first) {
+      const int st = c % W::NS, rs = c % RS;
+      if (!wait_warp(rfull(rs), (c / RS) & 1)) return false;
+      if (c >= W::NS && !wait_warp(empty(st), (c / W::NS - 1) & 1)) return false;
+      const uint32_t dst = sT + st * W::TILE, src = base + W::RAW_OFF + rs * W::RAW;
+      if (!v && lw == 0) note(t, first);
+      constexpr int PR = D / 16;  // pieces of a row
+#pragma unroll 2
+      for (int id = lt; id < kKeys * PR; id += LT) {
+        const int r = id / PR, ch = id % PR;
         uint32_t w[4], h[8];
         asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                      : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
                      : "r"(src + id * 16));
+        if (v && t.edge) {
+          const bool on = r < t.left && ((t.there >> (r >> 3)) & 1u);
+          if (!on) w[0] = w[1] = w[2] = w[3] = 0;
+        }
 #pragma unroll
         for (int k = 0; k < 4; ++k) widen4<F16 ? kCacheE4m3 : TYPE>(w[k], h[2 * k], h[2 * k + 1]);
-        if (TYPE == kCacheE4m3 && t.v && t.edge && t.node0 + r >= 0) {
-          uint32_t any = 0;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const uint32_t b = bad_halves(h[k]);
-            any |= b;
-            h[k] &= (b & 1u ? 0u : 0xFFFFu) | (b & 2u ? 0u : 0xFFFF0000u);
-          }
-          if (any) atomicOr(&bad_of[t.bad][((t.node0 + r) >> 5) & 1], 1u << ((t.node0 + r) & 31));
+        if (v && t.edge) {
+          if (TYPE == kCacheE4m3 && t.node0 + r >= 0) clean(h, 8, t.node0 + r, t.bad);
         }
         const uint32_t at = dst + (ch >> 2) * W::HALF + r * 128;
         const uint32_t c0 = (ch & 3) * 2;
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + (((c0 + k) ^ (r & 7)) << 4)),
-                       "r"(h[4 * k]), "r"(h[4 * k + 1]), "r"(h[4 * k + 2]), "r"(h[4 * k + 3])
-                       : "memory");
+        sts_v4(at + ((c0 ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
+        sts_v4(at + (((c0 + 1) ^ (r & 7)) << 4), h[4], h[5], h[6], h[7]);
       }
-      if (!t.v) {  // the tile's scales: k' = k scale log2(e), log2 v, 1 / v
-        const int r = lt & (kKeys - 1);
-        const float x = scales[(lt < kKeys ? 0 : kMeta * kKeys) + t.meta * kKeys + r];
-        if (lt < kKeys) {
-          scales[2 * kMeta * kKeys + t.meta * kKeys + r] = x * cs;
-        } else {
-          float lv = log2f(x), rv = 1.0f / x;
-          if (x < kTinyScale) lv = -100.0f, rv = 1.0f / kTinyScale;
-          const int j = t.node0 + r;
-          if (t.edge && j >= 0 && !(x < INFINITY)) {  // a node's row with a scale that is not finite
-            lv = 0.0f, rv = 1.0f;
-            atomicOr(&bad_of[t.bad][(j >> 5) & 1], 1u << (j & 31));
-          }
-          scales[3 * kMeta * kKeys + t.meta * kKeys + r] = lv;
-          scales[4 * kMeta * kKeys + t.meta * kKeys + r] = rv;
+      if (!v && lt < kKeys) {  // the tile's scales: k scale log2(e), log2 v, 1 / v
+        float lv = log2f(sc_v), rv = 1.0f / sc_v;
+        if (sc_v < kTinyScale) lv = -100.0f, rv = 1.0f / kTinyScale;
+        const int j = t.node0 + lt;
+        if (t.edge && j >= 0 && !(sc_v < INFINITY)) {  // a node's row whose scale is not finite
+          lv = 0.0f, rv = 1.0f;
+          atomicOr(&bad_of[t.bad][(j >> 5) & 1], 1u << (j & 31));
         }
+        float* f = scales + t.meta * kKeys + lt;
+        f[0] = sc_k * cs;
+        f[kMeta * kKeys] = lv;
+        f[2 * kMeta * kKeys] = rv;
       }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(full(st));
+        mbar_arrive(rfree(rs));
+      }
+      ++c;
       return true;
     };
 
-    Span w;
-    SeqInfo si;
-    while (ok && sched.next(p, w, si)) {
-      const int32_t* table = p.table + (int64_t)w.s * p.ld_table;
-      const int n = w.u1 - w.u0;
-      const int bad_slot = item_no % kBad;
-      auto look_up = [&](int i) {  // lane l: the page of the tile's l-th group of 8
-        const int64_t pos = (int64_t)(w.u0 + i) * kKeys + 8 * lane;
-        return i < n && lane < 16 && pos < si.len ? table[pos >> p.c.page_shift] : -1;
-      };
-      // Position c of the ring: K (v false) or V of tile i, whose groups of
-      // rows begin at `at`.
-      auto emit = [&](bool v, int i, const RowAt& at) {
-        const int64_t pos0 = (int64_t)(w.u0 + i) * kKeys;
-        const bool edge = pos0 + kKeys > si.ctx;
-        const int left = (int)min((int64_t)kKeys, si.len - pos0);  // rows that are there
-        const uint8_t* from = v ? p.c.v : p.c.k;
-        if (F16) {
-          if (c >= W::NS && !__all_sync(0xFFFFFFFFu, mbar_test(empty(c % W::NS), (c / W::NS - 1) & 1))) {
-            cp_async_wait_group<0>();  // what has landed is announced before this warp waits
-            announce(c);
-          }
-          if (!acquire(c)) return false;
-          if (!v && lw == 0 && lane == 0) {
-            if (i == 0) bad_of[(item_no + kBad / 2) % kBad][0] = bad_of[(item_no + kBad / 2) % kBad][1] = 0;
-          }
-          if (!v && lw == 0) {
-            const uint32_t there = __ballot_sync(0xFFFFFFFFu, lane < 16 && at.code >= 0) & 0xFFFFu;
-            if (lane == 0) there_of[tile_no % kMeta] = there;
-          }
-          const uint32_t dst = sT + (c % W::NS) * W::TILE;
-          constexpr int PR = D / 8, PI = 32 / PR;  // pieces of a row, rows of an instruction
-          const bool slow = v && edge;
-#pragma unroll 4
-          for (int k = 0; k < 32 / PI; ++k) {
-            const int r = lw * 32 + k * PI + lane / PR, ch = lane % PR;
-            const int64_t code = __shfl_sync(0xFFFFFFFFu, at.code, r >> 3);
-            const bool on = code >= 0 && r < left;
-            const uint8_t* src = from + ((on ? code : 0) + (r & 7) * D + ch * 8) * 2;
-            const uint32_t to = dst + (ch >> 3) * W::HALF + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
-            if (!slow) {
-              cp_async_16(to, src, on ? 16u : 0u);
-            } else {  // value rows of nodes: an infinity or NaN must not meet a weight of 0
-              uint4 x = make_uint4(0, 0, 0, 0);
-              if (on) x = ld_stream_v4(src);
-              uint32_t h[4] = {x.x, x.y, x.z, x.w}, any = 0;
-              const int64_t j = pos0 + r - si.ctx;
-              if (j >= 0) {
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                  const uint32_t b = bad_halves(h[y]);
-                  any |= b;
-                  h[y] &= (b & 1u ? 0u : 0xFFFFu) | (b & 2u ? 0u : 0xFFFF0000u);
-                }
-                if (any) atomicOr(&bad_of[bad_slot][((int)j >> 5) & 1], 1u << ((int)j & 31));
-              }
-              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(h[0]), "r"(h[1]),
-                           "r"(h[2]), "r"(h[3])
-                           : "memory");
-            }
-          }
-          cp_async_commit();
-          ++c;
-          if (c - said > W::LAG) {
-            cp_async_wait_group<W::LAG>();
-            announce(c - W::LAG);
-          }
-        } else {
-          constexpr int RS = F16 ? 1 : W::RS;
-          if (c >= RS) {  // the raw slot's last tile goes first
-            cp_async_wait_group<RS - 1>();
-            if (!convert(c - RS, ring[c % RS])) return false;
-            announce(c - RS + 1);
-          }
-          if (!v && lw == 0) {
-            const uint32_t there = __ballot_sync(0xFFFFFFFFu, lane < 16 && at.code >= 0) & 0xFFFFu;
-            if (lane == 0) {
-              there_of[tile_no % kMeta] = there;
-              if (i == 0)
-                bad_of[(item_no + kBad / 2) % kBad][0] = bad_of[(item_no + kBad / 2) % kBad][1] = 0;
-            }
-          }
-          const uint32_t dst = base + W::RAW_OFF + (c % RS) * W::RAW;
-          constexpr int PR = D / 16;
-          const int lt = lw * 32 + lane;
-#pragma unroll
-          for (int k = 0; k < kKeys * PR / (W::LW * 32); ++k) {
-            const int id = lt + k * W::LW * 32, r = id / PR, ch = id % PR;
-            const int64_t code = __shfl_sync(0xFFFFFFFFu, at.code, r >> 3);
-            const bool on = code >= 0 && r < left;
-            cp_async_16(dst + id * 16, from + (on ? code : 0) + (r & 7) * D + ch * 16, on ? 16u : 0u);
-          }
-          if (!v) {
-            const int r = lt & (kKeys - 1);
-            const int64_t sc = __shfl_sync(0xFFFFFFFFu, at.scale, r >> 3);
-            const bool on = sc >= 0 && r < left;
-            const float* f = (lt < kKeys ? p.c.k_scale : p.c.v_scale) + (on ? sc : 0) + (r & 7);
-            cp_async_4(smem_addr(scales + (lt < kKeys ? 0 : kMeta * kKeys) +
-                                 (tile_no % kMeta) * kKeys + r),
-                       on ? f : p.c.k_scale, on ? 4u : 0u);
-          }
-          cp_async_commit();
-          ring[c % RS] = Raw{v ? 1 : 0, edge ? 1 : 0, (int)max(pos0 - si.ctx, (int64_t)-(1 << 20)),
-                             bad_slot, tile_no % kMeta};
-          ++c;
-        }
-        if (!v) ++tile_no;
+    // The positions of the ring in order: K0, V0, K1, V1, ... for PAIR, else
+    // K0, K1, V0, K2, V1, ..., as the MMA thread takes them.  `Walk` yields them
+    // one by one; the 8-bit loaders run two of them, one a raw ring ahead.
+    struct Walk {
+      Sched sched;
+      Span w;
+      SeqInfo si;
+      int i, n;       // next K tile
+      int vi;         // next V tile
+      int32_t entry;  // the next K tile's page, of the lane's group
+      Tile k, last;   // tiles whose V is still to come: k the newer
+      int tiles, items;
+      bool open;
+    };
+    auto look_up = [&](const Walk& x, int i) {
+      const int64_t pos = (int64_t)(x.w.u0 + i) * kKeys + 8 * lane;
+      return i < x.n && lane < 16 && pos < x.si.len
+                 ? p.table[(int64_t)x.w.s * p.ld_table + (pos >> p.c.page_shift)]
+                 : -1;
+    };
+    auto start = [&](Walk& x) {
+      x.open = x.sched.next(p, x.w, x.si);
+      if (!x.open) return;
+      x.n = x.w.u1 - x.w.u0;
+      x.i = x.vi = 0;
+      x.entry = look_up(x, 0);
+    };
+    // The next position: false when there is none.  first: an item's first.
+    auto step = [&](Walk& x, bool& v, bool& first) {
+      if (x.open && x.i == x.n && x.vi == x.n) {
+        ++x.items;
+        start(x);
+      }
+      if (!x.open) return false;
+      const int lead = PAIR ? 0 : 1;
+      v = x.i == x.n || x.i - x.vi > lead;
+      first = !v && x.i == 0;
+      if (v) {
+        ++x.vi;
         return true;
-      };
-      // K0, K1, V0, K2, V1, ...: the order in which the MMA thread takes them
-      int32_t entry = look_up(0);
-      RowAt now{-1, -1}, last{-1, -1};
-      for (int i = 0; i <= n && ok; ++i) {
-        if (i < n) {
-          now = group_at<D>(p, entry, w.h, (int64_t)(w.u0 + i) * kKeys + 8 * (lane & 15));
-          entry = look_up(i + 1);
-          ok = emit(false, i, now);
-        }
-        if (ok && i > 0) ok = emit(true, i - 1, last);
-        last = now;
       }
-      ++item_no;
-    }
-    if (F16) {
-      cp_async_wait_group<0>();
-      if (ok) announce(c);
+      x.last = x.k;
+      Tile& t = x.k;
+      t.pos0 = (int64_t)(x.w.u0 + x.i) * kKeys;
+      t.at = group_at<D>(p, x.entry, x.w.h, t.pos0 + 8 * (lane & 15));
+      t.page = x.entry;
+      t.row = (x.w.h << p.c.page_shift) + (int)((t.pos0 + 8 * (lane & 15)) & ((1 << p.c.page_shift) - 1));
+      t.there = __ballot_sync(0xFFFFFFFFu, lane < 16 && t.at.code >= 0);
+      t.left = (int)min((int64_t)kKeys, x.si.len - t.pos0);
+      t.edge = t.pos0 + kKeys > x.si.ctx || t.there != 0xFFFFu;
+      t.node0 = (int)max(t.pos0 - x.si.ctx, (int64_t)-(1 << 20));
+      t.bad = x.items % kBad;
+      t.meta = x.tiles++ % kMeta;
+      ++x.i;
+      x.entry = look_up(x, x.i);
+      return true;
+    };
+    // which tile a V position belongs to: the newest K tile, or the one before
+    auto v_tile = [&](const Walk& x) -> const Tile& { return x.vi == x.i ? x.k : x.last; };
+
+    Walk x;
+    x.sched = sched;
+    x.tiles = x.items = 0;
+    start(x);
+    bool v, first;
+    if constexpr (F16) {
+      while (ok && step(x, v, first)) {
+        item_no = x.items;
+        ok = emit16(v, v ? v_tile(x) : x.k, first);
+      }
     } else {
-      constexpr int RS = F16 ? 1 : W::RS;
-      cp_async_wait_group<0>();
-      for (int pos = max(0, c - RS); ok && pos < c; ++pos) {
-        ok = convert(pos, ring[pos % RS]);
-        if (ok) announce(pos + 1);
+      Walk y = x;  // fetches RS positions ahead
+      int fc = 0;
+      bool more = true, fv, ff;
+      for (; ok && more && fc < RS; ++fc) {
+        more = step(y, fv, ff);
+        if (!more) break;
+        ok = fetch8(fc, fv, fv ? v_tile(y) : y.k);
+      }
+      while (ok && step(x, v, first)) {
+        item_no = x.items;
+        if (first) load_scales(x.k);
+        ok = emit8(v, v ? v_tile(x) : x.k, first);
+        if (!ok) break;
+        if (!v && x.i < x.n) {  // the next K tile's scales
+          Tile t = x.k;
+          t.pos0 += kKeys;
+          t.at = group_at<D>(p, x.entry, x.w.h, t.pos0 + 8 * (lane & 15));
+          t.left = (int)min((int64_t)kKeys, x.si.len - t.pos0);
+          load_scales(t);
+        }
+        if (more) {
+          more = step(y, fv, ff);
+          if (more) ok = fetch8(fc++, fv, fv ? v_tile(y) : y.k);
+        }
       }
     }
-    // every release of a stage has landed before the block ends
-    for (int pos = max(0, c - W::NS); ok && pos < c; ++pos) ok = wait_warp(empty(pos % W::NS), (pos / W::NS) & 1);
+    // Before the block ends its copies have landed and every release of a stage
+    // has arrived.
+    if (!F16 && !ok && lw == 0) {  // raw tiles that nobody waited for
+      for (int s = 0; s < RS; ++s) mbar_wait(rfull(s), (c / RS) & 1, 100000000ull, false);
+    }
+    for (int pos = max(0, c - W::NS); pos < c; ++pos) {
+      if (F16) mbar_wait(full(pos % W::NS), (pos / W::NS) & 1, kWaitLimitNs, ok);
+      if (ok) ok = wait_warp(empty(pos % W::NS), (pos / W::NS) & 1);
+    }
+    __syncwarp();
   } else if (warp == kMmaWarp) {
     // ---- MMA issuer ----------------------------------------------------------------
     if (lane == 0) {
@@ -345,47 +429,80 @@ __global__ void __launch_bounds__(Wide<D, TYPE>::THREADS, 1) attend_wide_kernel(
       bool ok = true;
       Span w;
       SeqInfo si;
-      auto scores = [&](int i) {
-        const int st = c % W::NS;
-        if (!mbar_wait(full(st), (c / W::NS) & 1)) return false;
-        fence_proxy_async_smem();
+      auto ready = [&](int pos) {
+        if (!mbar_wait(full(pos % W::NS), (pos / W::NS) & 1)) return false;
         tc_fence_after_sync();
-        const uint32_t d = tmem + ((i & 1) ? kS1 : kS0), b = sT + st * W::TILE;
+        return true;
+      };
+      auto scores = [&](int pos, int b) {  // stream b, the K tile of ring position pos
+        const uint32_t d = tmem + (b ? kS1 : kS0), k = sT + pos % W::NS * W::TILE;
+        const uint32_t q = sQ + (PAIR && b ? kRows * D * 2 : 0);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           const uint32_t off = (ks >> 2) * W::HALF + (ks & 3) * 32;
-          mma_f16(d, smem_desc_sw128(sQ + off, 16), smem_desc_sw128(b + off, 16), id_s, ks != 0);
+          mma_f16(d, smem_desc_sw128(q + off, 16), smem_desc_sw128(k + off, 16), id_s, ks != 0);
         }
-        mma_commit(empty(st));
-        mma_commit(sfull(i & 1));
-        ++c;
+        mma_commit(sfull(b));
+      };
+      auto sums = [&](int pos, int b, bool add) {
+        if (!mbar_wait(pfull(b), np[b]++ & 1)) return false;
+        tc_fence_after_sync();
+        const uint32_t d = tmem + (b ? kO1 : kO0), a = tmem + (b ? kS1 : kS0);
+        const uint32_t v = sT + pos % W::NS * W::TILE;
+#pragma unroll
+        for (int ks = 0; ks < kKeys / 16; ++ks)
+          mma_f16_ts(d, a + ks * 8, smem_desc_sw128(v + ks * 2048, W::HALF), id_o, add || ks != 0);
+        mma_commit(ofull(b));
         return true;
       };
       while (ok && sched.next(p, w, si)) {
         const int n = w.u1 - w.u0;
         if (!mbar_wait(qfull, items & 1)) break;
-        fence_proxy_async_smem();
         ++items;
-        ok = scores(0);
-        for (int i = 0; i < n && ok; ++i) {
-          if (i + 1 < n && !scores(i + 1)) {
-            ok = false;
-            break;
-          }
-          const int st = c % W::NS, b = i & 1;
-          ok = mbar_wait(full(st), (c / W::NS) & 1) && mbar_wait(pfull(b), np[b] & 1);
+        if (PAIR) {
+          const bool two = si.n * G - w.rt * IROWS > kRows;
+          ok = ready(c);
           if (!ok) break;
-          ++np[b];
-          fence_proxy_async_smem();
-          tc_fence_after_sync();
-          const uint32_t d = tmem + (b ? kO1 : kO0), a = tmem + (b ? kS1 : kS0);
-#pragma unroll
-          for (int ks = 0; ks < kKeys / 16; ++ks)
-            mma_f16_ts(d, a + ks * 8, smem_desc_sw128(sT + st * W::TILE + ks * 2048, W::HALF), id_o,
-                       i > 1 || ks != 0);
-          mma_commit(empty(st));
-          mma_commit(ofull(b));
+          scores(c, 0);
+          if (two) scores(c, 1);
+          mma_commit(empty(c % W::NS));
           ++c;
+          for (int i = 0; i < n; ++i) {
+            const int cv = c, ck = c + 1;
+            const bool more = i + 1 < n;
+            ok = ready(cv) && sums(cv, 0, i > 0);
+            if (ok && more) {
+              ok = ready(ck);
+              if (ok) scores(ck, 0);
+            }
+            if (ok && two) ok = sums(cv, 1, i > 0);
+            if (!ok) break;
+            mma_commit(empty(cv % W::NS));
+            if (more) {
+              if (two) scores(ck, 1);
+              mma_commit(empty(ck % W::NS));
+            }
+            c += more ? 2 : 1;
+          }
+        } else {
+          ok = ready(c);
+          if (!ok) break;
+          scores(c, 0);
+          mma_commit(empty(c % W::NS));
+          ++c;
+          for (int i = 0; i < n; ++i) {
+            if (i + 1 < n) {
+              ok = ready(c);
+              if (!ok) break;
+              scores(c, (i + 1) & 1);
+              mma_commit(empty(c % W::NS));
+              ++c;
+            }
+            ok = ready(c) && sums(c, i & 1, i > 1);
+            if (!ok) break;
+            mma_commit(empty(c % W::NS));
+            ++c;
+          }
         }
       }
     }
@@ -395,6 +512,7 @@ __global__ void __launch_bounds__(Wide<D, TYPE>::THREADS, 1) attend_wide_kernel(
     const int b = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t tlane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t tS = tlane + (b ? kS1 : kS0), tO = tlane + (b ? kO1 : kO0);
+    const int step = PAIR ? 1 : 2, off0 = PAIR ? 0 : b;  // tiles of this stream
     int tile_no = 0, item_no = 0, ns = 0, no = 0, phase = 0;
     auto soft_sync = [&]() {  // all softmax warps
       __syncwarp();
@@ -409,36 +527,41 @@ __global__ void __launch_bounds__(Wide<D, TYPE>::THREADS, 1) attend_wide_kernel(
     SeqInfo si;
     while (ok && sched.next(p, w, si)) {
       const int n = w.u1 - w.u0;
-      const int rows = min(kRows, si.n * G - w.rt * kRows);
+      const int r0 = w.rt * IROWS + (PAIR ? b * kRows : 0);  // the stream's first row
+      const int rows = max(0, min(kRows, si.n * G - r0));
       // queries: every score product of the last item is done
-      for (int id = threadIdx.x; id < kRows * (D / 8); id += kSoftWarps * 32) {
-        const int r = id / (D / 8), ch = id % (D / 8), rr = w.rt * kRows + r;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (r < rows)
-          x = *reinterpret_cast<const uint4*>(p.q + (int64_t)(si.first + rr / G) * p.ldq +
-                                              (int64_t)(w.h * G + rr % G) * D + ch * 8);
+      {
+        const int t0 = PAIR ? threadIdx.x & 127 : threadIdx.x;
+        const uint32_t q = sQ + (PAIR && b ? kRows * D * 2 : 0);
         const uint32_t sg = p.scale < 0.0f ? 0x80008000u : 0u;
-        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
-                         sQ + (ch >> 3) * W::HALF + r * 128 + (((ch & 7) ^ (r & 7)) << 4)),
-                     "r"(x.x ^ sg), "r"(x.y ^ sg), "r"(x.z ^ sg), "r"(x.w ^ sg)
-                     : "memory");
+        for (int id = t0; id < kRows * (D / 8); id += PAIR ? 128 : 256) {
+          const int r = id / (D / 8), ch = id % (D / 8), rr = r0 + r;
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if (r < rows)
+            x = *reinterpret_cast<const uint4*>(p.q + (int64_t)(si.first + rr / G) * p.ldq +
+                                                (int64_t)(w.h * G + rr % G) * D + ch * 8);
+          sts_v4(q + (ch >> 3) * W::HALF + r * 128 + (((ch & 7) ^ (r & 7)) << 4), x.x ^ sg, x.y ^ sg,
+                 x.z ^ sg, x.w ^ sg);
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(qfull);
 
-      const int rr = w.rt * kRows + row, node = rr / G;
+      const int rr = r0 + row, node = rr / G;
       const bool mine = row < rows;
       const uint64_t bits = !mine ? 0ull
                             : p.tree_mask ? p.tree_mask[si.first + node]
                                           : (2ull << node) - 1ull;
       const bool idle = (warp & 3) * 32 >= rows;  // a warp without rows
       float m = -INFINITY, l = 0.0f;
-      for (int i = b; i < n; i += 2) {
+      const int tiles = PAIR && rows == 0 ? 0 : (n - off0 + step - 1) / step;
+      for (int k = 0; k < tiles; ++k) {
+        const int i = off0 + k * step;
         ok = wait_warp(sfull(b), ns++ & 1);
         // (the sums up to here were issued before these scores: no further wait,
         // but every phase of a barrier is seen, so that its parity says which)
-        if (ok && i > b) ok = wait_warp(ofull(b), (no + (i - b) / 2 - 1) & 1);
+        if (ok && k > 0) ok = wait_warp(ofull(b), (no + k - 1) & 1);
         if (!ok) break;
         if (!idle) {
           tc_fence_after_sync();
@@ -446,54 +569,62 @@ __global__ void __launch_bounds__(Wide<D, TYPE>::THREADS, 1) attend_wide_kernel(
           const int64_t pos0 = (int64_t)(w.u0 + i) * kKeys;
           const uint32_t there = *(volatile uint32_t*)&there_of[slot];
           const bool edge = pos0 + kKeys > si.ctx || there != 0xFFFFu;
-          const float* ksc = scales + 2 * kMeta * kKeys + slot * kKeys;
-          const float* lvs = ksc + kMeta * kKeys;
-          const float* rvs = lvs + kMeta * kKeys;
-          // what the row sees of an edge tile: position x of it in bit x
-          uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
-          if (edge) {
-            const int64_t k0 = pos0 - si.ctx;  // node number of position 0
+          const float4* ksc = reinterpret_cast<const float4*>(scales + slot * kKeys);
+          const float4* lvs = ksc + kMeta * kKeys / 4;
+          const float4* rvs = lvs + kMeta * kKeys / 4;
+          // what the row sees of positions 32 y .. of an edge tile
+          auto sees = [&](int y) {
+            const int64_t f = pos0 - si.ctx + 32 * y;  // node number of the first
+            uint32_t x;
+            if (f <= -32) x = ~0u;
+            else if (f >= 64) x = 0u;
+            else if (f >= 0) x = (uint32_t)(bits >> f);
+            else x = (uint32_t)((bits << -f) | ((1ull << -f) - 1ull));
+            uint32_t g = there >> (4 * y);
+            g = (g & 1u ? 0xFFu : 0u) | (g & 2u ? 0xFF00u : 0u) | (g & 4u ? 0xFF0000u : 0u) |
+                (g & 8u ? 0xFF000000u : 0u);
+            x &= g;
+            const int64_t rest = si.len - pos0 - 32 * y;
+            if (rest < 32) x &= rest <= 0 ? 0u : (1u << rest) - 1u;
+            return x;
+          };
+          // exponents (powers of 2) of 32 positions, in place
+          auto exponents = [&](uint32_t (&v)[32], int y) {
+            if (F16) {
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const int64_t f = k0 + 32 * y;
-              uint32_t x;
-              if (f <= -32) x = ~0u;
-              else if (f >= 64) x = 0u;
-              else if (f >= 0) x = (uint32_t)(bits >> f);
-              else x = (uint32_t)((bits << -f) | ((1ull << -f) - 1ull));
-              uint32_t g = there >> (4 * y);
-              g = (g & 1u ? 0xFFu : 0u) | (g & 2u ? 0xFF00u : 0u) | (g & 4u ? 0xFF0000u : 0u) |
-                  (g & 8u ? 0xFF000000u : 0u);
-              x &= g;
-              const int64_t rest = si.len - pos0 - 32 * y;
-              if (rest < 32) x &= rest <= 0 ? 0u : (1u << rest) - 1u;
-              see[y] = x;
+              for (int x = 0; x < 32; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * cs);
+            } else {
+#pragma unroll
+              for (int x = 0; x < 32; x += 4) {
+                const float4 a = ksc[8 * y + x / 4], d = lvs[8 * y + x / 4];
+                v[x] = __float_as_uint(fmaf(__uint_as_float(v[x]), a.x, d.x));
+                v[x + 1] = __float_as_uint(fmaf(__uint_as_float(v[x + 1]), a.y, d.y));
+                v[x + 2] = __float_as_uint(fmaf(__uint_as_float(v[x + 2]), a.z, d.z));
+                v[x + 3] = __float_as_uint(fmaf(__uint_as_float(v[x + 3]), a.w, d.w));
+              }
             }
-          }
-          // the exponent of position x of chunk y, in powers of 2
-          auto exponent = [&](float s, int y, int x) {
-            const float t = F16 ? s * cs : fmaf(s, ksc[32 * y + x], lvs[32 * y + x]);
-            return edge && !((see[y] >> x) & 1u) ? -INFINITY : t;
+            if (edge) {
+              const uint32_t see = sees(y);
+#pragma unroll
+              for (int x = 0; x < 32; ++x)
+                if (!((see >> x) & 1u)) v[x] = 0xFF800000u;  // -inf
+            }
           };
           float top = -INFINITY;
-#pragma unroll
+#pragma unroll 1
           for (int y = 0; y < 4; ++y) {
             uint32_t v[32];
             tmem_ld_32(tS + 32 * y, v);
             tmem_ld_wait();
-            if (F16 && !edge) {
-              float t = __uint_as_float(v[0]);
+            exponents(v, y);
+            float t[4] = {top, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-              for (int x = 1; x < 32; ++x) t = fmaxf(t, __uint_as_float(v[x]));
-              top = fmaxf(top, t * cs);
-            } else {
-#pragma unroll
-              for (int x = 0; x < 32; ++x) top = fmaxf(top, exponent(__uint_as_float(v[x]), y, x));
-            }
+            for (int x = 0; x < 32; ++x) t[x & 3] = fmaxf(t[x & 3], __uint_as_float(v[x]));
+            top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
           }
           const bool grow = top > m + kGrow || (m == -INFINITY && top > -INFINITY);
           const float m2 = grow ? top : m;
-          if (i > b && __any_sync(0xFFFFFFFFu, grow)) {  // there are sums so far
+          if (k > 0 && __any_sync(0xFFFFFFFFu, grow)) {  // there are sums so far
             const float keep = !grow ? 1.0f : m == -INFINITY ? 0.0f : exp2_fast(m - m2);
 #pragma unroll 1
             for (int y = 0; y < D; y += 32) {
@@ -508,108 +639,113 @@ __global__ void __launch_bounds__(Wide<D, TYPE>::THREADS, 1) attend_wide_kernel(
           }
           m = m2;
           const float off = m == -INFINITY ? 0.0f : m;
-          float sum[2] = {0.0f, 0.0f};
-#pragma unroll
+#pragma unroll 1
           for (int y = 0; y < 4; ++y) {
             uint32_t v[32], h[16];
             tmem_ld_32(tS + 32 * y, v);
             tmem_ld_wait();
+            exponents(v, y);
+            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int x = 0; x < 32; ++x) {
-              const float s = __uint_as_float(v[x]);
-              const float e = F16 && !edge ? exp2_fast(fmaf(s, cs, -off))
-                                           : exp2_fast(exponent(s, y, x) - off);
-              if (F16)
-                sum[x & 1] += e;
-              else
-                sum[x & 1] = fmaf(e, rvs[32 * y + x], sum[x & 1]);
-              v[x] = __float_as_uint(e);
-            }
+            for (int x = 0; x < 32; x += 4) {
+              float e[4];
 #pragma unroll
-            for (int x = 0; x < 16; ++x) {
-              const __half2 t = __floats2half2_rn(__uint_as_float(v[2 * x]), __uint_as_float(v[2 * x + 1]));
-              h[x] = *reinterpret_cast<const uint32_t*>(&t);
+              for (int z = 0; z < 4; ++z) e[z] = exp2_fast(__uint_as_float(v[x + z]) - off);
+              if (F16) {
+#pragma unroll
+                for (int z = 0; z < 4; ++z) sum[z] += e[z];
+              } else {
+                const float4 r = rvs[8 * y + x / 4];
+                sum[0] = fmaf(e[0], r.x, sum[0]);
+                sum[1] = fmaf(e[1], r.y, sum[1]);
+                sum[2] = fmaf(e[2], r.z, sum[2]);
+                sum[3] = fmaf(e[3], r.w, sum[3]);
+              }
+              h[x / 2] = half2_of(e[0], e[1]);
+              h[x / 2 + 1] = half2_of(e[2], e[3]);
             }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             tmem_st_16(tS + 16 * y, h);
           }
-          l += sum[0] + sum[1];
           tmem_st_wait();
         }
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(pfull(b));
       }
-      const int mine_tiles = (n - b + 1) / 2;
-      if (ok && mine_tiles > 0) ok = wait_warp(ofull(b), (no + mine_tiles - 1) & 1);
-      no += mine_tiles;
+      if (ok && tiles > 0) ok = wait_warp(ofull(b), (no + tiles - 1) & 1);
+      no += tiles;
       tile_no += n;
-      // ---- the streams join: columns of the first half here, of the second there
-      s_ml[b][row] = make_float2(m, l);
-      if (!ok || !soft_sync()) {
-        ok = false;
-        break;
+      // ---- the sums: PAIR: each stream has its rows; else the streams join,
+      // stream b writing the b-th half of the columns
+      float M = m, tot = l, fa = 1.0f, fb = 0.0f;
+      const bool both = !PAIR && n > 1;
+      if (!PAIR) {
+        s_ml[b][row] = make_float2(m, l);
+        if (!ok || !soft_sync()) {
+          ok = false;
+          break;
+        }
+        const float2 A = s_ml[0][row], B = s_ml[1][row];
+        M = fmaxf(A.x, B.x);
+        const float off = M == -INFINITY ? 0.0f : M;
+        fa = exp2_fast(A.x - off);
+        fb = both ? exp2_fast(B.x - off) : 0.0f;
+        tot = A.y * fa + (both ? B.y * fb : 0.0f);
       }
+      if (!ok) break;
       tc_fence_after_sync();
-      const float2 A = s_ml[0][row], B = s_ml[1][row];
-      const float M = fmaxf(A.x, B.x), off = M == -INFINITY ? 0.0f : M;
-      const float fa = exp2_fast(A.x - off), fb = n > 1 ? exp2_fast(B.x - off) : 0.0f;
-      const float tot = A.y * fa + (n > 1 ? B.y * fb : 0.0f);
       const uint64_t spoilt = *(volatile uint32_t*)&bad_of[item_no % kBad][0] |
                               (uint64_t)*(volatile uint32_t*)&bad_of[item_no % kBad][1] << 32;
       const float poison = bits & spoilt ? __uint_as_float(0x7FC00000u) : 0.0f;
       const bool whole = w.u0 == 0 && w.u1 == w.nu;
       const float inv = tot == 0.0f ? 0.0f : 1.0f / tot;
       float4* slot4 = reinterpret_cast<float4*>(
-          slots + part_slot(blockIdx.x, sched.per, w.start) * attend_slot_floats(kRows, D));
+          slots + part_slot(blockIdx.x, sched.per, w.start) * attend_slot_floats(IROWS, D));
+      const int srow = (PAIR ? b * kRows : 0) + row;  // row of the item
       __half* out = p.out + (int64_t)(si.first + node) * p.ldo + (int64_t)(w.h * G + rr % G) * D;
+      const int c0 = PAIR ? 0 : b * (D / 2), c1 = PAIR ? D : (b + 1) * (D / 2);
       if (!idle) {
 #pragma unroll 1
-        for (int y = 0; y < D / 2; y += 32) {
-          const int d0 = b * (D / 2) + y;
+        for (int d0 = c0; d0 < c1; d0 += 32) {
           uint32_t v[32], u[32];
-          tmem_ld_32(tlane + kO0 + d0, v);
-          if (n > 1) tmem_ld_32(tlane + kO1 + d0, u);
+          tmem_ld_32((PAIR ? tO : tlane + kO0) + d0, v);
+          if (both) tmem_ld_32(tlane + kO1 + d0, u);
           tmem_ld_wait();
           float x[32];
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
             x[k] = __uint_as_float(v[k]) * fa + poison;
-            if (n > 1) x[k] += __uint_as_float(u[k]) * fb;
+            if (both) x[k] += __uint_as_float(u[k]) * fb;
           }
           if (mine && whole) {
 #pragma unroll
-            for (int k = 0; k < 32; k += 8) {
-              uint32_t h[4];
-#pragma unroll
-              for (int z = 0; z < 4; ++z) {
-                const __half2 t = __floats2half2_rn(x[k + 2 * z] * inv, x[k + 2 * z + 1] * inv);
-                h[z] = *reinterpret_cast<const uint32_t*>(&t);
-              }
-              *reinterpret_cast<uint4*>(out + d0 + k) = make_uint4(h[0], h[1], h[2], h[3]);
-            }
+            for (int k = 0; k < 32; k += 8)
+              *reinterpret_cast<uint4*>(out + d0 + k) =
+                  make_uint4(half2_of(x[k] * inv, x[k + 1] * inv), half2_of(x[k + 2] * inv, x[k + 3] * inv),
+                             half2_of(x[k + 4] * inv, x[k + 5] * inv),
+                             half2_of(x[k + 6] * inv, x[k + 7] * inv));
           } else if (mine) {
 #pragma unroll
             for (int k = 0; k < 32; k += 4)
-              slot4[(d0 + k) / 4 * kRows + row] = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+              slot4[(d0 + k) / 4 * IROWS + srow] = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
           }
           __syncwarp();
         }
       }
-      if (mine && b == 0) {
-        if (whole) {
-          if (p.lse)
-            p.lse[(int64_t)(si.first + node) * p.q_heads + w.h * G + rr % G] =
-                tot == 0.0f ? -INFINITY : (M + log2f(tot)) * kLn2;
-        } else {
-          float* f = reinterpret_cast<float*>(slot4) + kRows * D;
-          f[row] = M;
-          f[kRows + row] = tot;
-        }
+      const bool writes = mine && (PAIR || b == 0);
+      if (writes && whole && p.lse)
+        p.lse[(int64_t)(si.first + node) * p.q_heads + w.h * G + rr % G] =
+            tot == 0.0f ? -INFINITY : (M + log2f(tot)) * kLn2;
+      if (writes && !whole) {
+        float* f = reinterpret_cast<float*>(slot4) + IROWS * D;
+        f[srow] = M;
+        f[IROWS + srow] = tot;
       }
       ++item_no;
       tc_fence_before_sync();
       if (whole) {
-        ok = soft_sync();  // nobody reads TMEM any more
+        if (!PAIR) ok = soft_sync();  // nobody reads the other stream's sums any more
         continue;
       }
       // ---- the blocks join: the last one to store its part adds all of them
@@ -627,46 +763,44 @@ __global__ void __launch_bounds__(Wide<D, TYPE>::THREADS, 1) attend_wide_kernel(
       if (!ok) break;
       if (!*(volatile uint32_t*)&s_last) continue;
       if (mine) {
-      __threadfence();
-      float M2 = -INFINITY, tot2 = 0.0f;
-      for (int64_t y = b0; y <= b1; ++y)
-        M2 = fmaxf(M2, __ldcg(slots + part_slot(y, sched.per, w.start) * attend_slot_floats(kRows, D) +
-                              kRows * D + row));
-      const float off2 = M2 == -INFINITY ? 0.0f : M2;
-      for (int64_t y = b0; y <= b1; ++y) {
-        const float* f = slots + part_slot(y, sched.per, w.start) * attend_slot_floats(kRows, D) + kRows * D;
-        tot2 += __ldcg(f + kRows + row) * exp2_fast(__ldcg(f + row) - off2);
-      }
-      const float inv2 = tot2 == 0.0f ? 0.0f : 1.0f / tot2;
-#pragma unroll 1
-      for (int d0 = b * (D / 2); d0 < (b + 1) * (D / 2); d0 += 16) {
-        float4 x[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) x[k] = make_float4(0, 0, 0, 0);
-#pragma unroll 2
+        __threadfence();
+        const float* part0 = slots + part_slot(b0, sched.per, w.start) * attend_slot_floats(IROWS, D);
+        auto part = [&](int64_t y) {  // after the first, an item's part begins its block's range
+          return y == b0 ? part0 : slots + (size_t)y * 2 * attend_slot_floats(IROWS, D);
+        };
+        float M2 = -INFINITY, tot2 = 0.0f;
+        for (int64_t y = b0; y <= b1; ++y) M2 = fmaxf(M2, __ldcg(part(y) + IROWS * D + srow));
+        const float off2 = M2 == -INFINITY ? 0.0f : M2;
         for (int64_t y = b0; y <= b1; ++y) {
-          const float* f = slots + part_slot(y, sched.per, w.start) * attend_slot_floats(kRows, D);
-          const float e = exp2_fast(__ldcg(f + kRows * D + row) - off2);
+          const float* f = part(y) + IROWS * D;
+          tot2 += __ldcg(f + IROWS + srow) * exp2_fast(__ldcg(f + srow) - off2);
+        }
+        const float inv2 = tot2 == 0.0f ? 0.0f : 1.0f / tot2;
+#pragma unroll 1
+        for (int d0 = c0; d0 < c1; d0 += 16) {
+          float4 x[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(f) + (d0 / 4 + k) * kRows + row);
-            x[k].x += v.x * e, x[k].y += v.y * e, x[k].z += v.z * e, x[k].w += v.w * e;
+          for (int k = 0; k < 4; ++k) x[k] = make_float4(0, 0, 0, 0);
+#pragma unroll 2
+          for (int64_t y = b0; y <= b1; ++y) {
+            const float* f = part(y);
+            const float e = exp2_fast(__ldcg(f + IROWS * D + srow) - off2);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(f) + (d0 / 4 + k) * IROWS + srow);
+              x[k].x += v.x * e, x[k].y += v.y * e, x[k].z += v.z * e, x[k].w += v.w * e;
+            }
           }
-        }
 #pragma unroll
-        for (int k = 0; k < 4; k += 2) {
-          const __half2 h0 = __floats2half2_rn(x[k].x * inv2, x[k].y * inv2);
-          const __half2 h1 = __floats2half2_rn(x[k].z * inv2, x[k].w * inv2);
-          const __half2 h2 = __floats2half2_rn(x[k + 1].x * inv2, x[k + 1].y * inv2);
-          const __half2 h3 = __floats2half2_rn(x[k + 1].z * inv2, x[k + 1].w * inv2);
-          *reinterpret_cast<uint4*>(out + d0 + 4 * k) =
-              make_uint4(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1),
-                         *reinterpret_cast<const uint32_t*>(&h2), *reinterpret_cast<const uint32_t*>(&h3));
+          for (int k = 0; k < 4; k += 2)
+            *reinterpret_cast<uint4*>(out + d0 + 4 * k) =
+                make_uint4(half2_of(x[k].x * inv2, x[k].y * inv2), half2_of(x[k].z * inv2, x[k].w * inv2),
+                           half2_of(x[k + 1].x * inv2, x[k + 1].y * inv2),
+                           half2_of(x[k + 1].z * inv2, x[k + 1].w * inv2));
         }
-      }
-      if (b == 0 && p.lse)
-        p.lse[(int64_t)(si.first + node) * p.q_heads + w.h * G + rr % G] =
-            tot2 == 0.0f ? -INFINITY : (M2 + log2f(tot2)) * kLn2;
+        if (writes && p.lse)
+          p.lse[(int64_t)(si.first + node) * p.q_heads + w.h * G + rr % G] =
+              tot2 == 0.0f ? -INFINITY : (M2 + log2f(tot2)) * kLn2;
       }
       __syncwarp();
     }
@@ -691,10 +825,21 @@ __global__ void __launch_bounds__(Wide<D, TYPE>::THREADS, 1) attend_wide_kernel(
   }
 }
 
-template <int D, int TYPE>
+// A cache's pages as {head_dim, kv_heads * page_size rows, pages}, in boxes of
+// 64 elements and the rows of a page (at most a tile's).
+bool encode_pages(CUtensorMap* m, const void* base, const CacheView& c, int head_dim) {
+  const int rows = 1 << c.page_shift;
+  const cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)c.kv_heads * rows, (cuuint64_t)c.pages};
+  const cuuint64_t strides[2] = {(cuuint64_t)head_dim * 2, (cuuint64_t)c.page_stride * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)(rows < kKeys ? rows : kKeys), 1};
+  return encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, base, 3, dims, strides, box,
+                      CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <int D, int TYPE, bool PAIR>
 cudaError_t wide_one(const AttendParams& p, int sms, cudaStream_t stream) {
-  using W = Wide<D, TYPE>;
-  auto* k = attend_wide_kernel<D, TYPE>;
+  using W = Wide<D, TYPE, PAIR>;
+  auto* k = attend_wide_kernel<D, TYPE, PAIR>;
   static int done[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -704,25 +849,40 @@ cudaError_t wide_one(const AttendParams& p, int sms, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     if (dev < 64) __atomic_store_n(&done[dev], 1, __ATOMIC_RELEASE);
   }
-  return launch_kernel(k, sms, W::THREADS, W::SMEM, stream, kFlagPdl, p);
+  CUtensorMap tk, tv;
+  if (TYPE == kCacheFp16) {
+    if (!encode_pages(&tk, p.c.k, p.c, D) || !encode_pages(&tv, p.c.v, p.c, D)) return cudaErrorInvalidValue;
+  } else {
+    memset(&tk, 0, sizeof(tk));
+    memset(&tv, 0, sizeof(tv));
+  }
+  return launch_kernel(k, sms, W::THREADS, W::SMEM, stream, kFlagPdl, p, tk, tv);
+}
+
+template <int D, int TYPE>
+cudaError_t wide_rows(const AttendParams& p, int sms, cudaStream_t stream) {
+  return p.max_nodes * (p.q_heads / p.c.kv_heads) > kRows ? wide_one<D, TYPE, true>(p, sms, stream)
+                                                           : wide_one<D, TYPE, false>(p, sms, stream);
 }
 
 }  // namespace
 
-size_t attend_wide_workspace_bytes(int64_t items, int head_dim, int sms) {
-  return attend_counter_bytes(items) + (size_t)sms * 2 * attend_slot_floats(kRows, head_dim) * sizeof(float);
+size_t attend_wide_workspace_bytes(int64_t seqs, int kv_heads, int rows, int head_dim, int sms) {
+  const int tile = rows > kRows ? 2 * kRows : kRows;
+  return attend_counter_bytes(seqs * kv_heads * ((rows + tile - 1) / tile)) +
+         (size_t)sms * 2 * attend_slot_floats(tile, head_dim) * sizeof(float);
 }
 
 cudaError_t launch_attend_wide(const AttendParams& p, int head_dim, int type, int sms,
                                cudaStream_t stream) {
   if (head_dim == 128) {
-    if (type == kCacheFp16) return wide_one<128, kCacheFp16>(p, sms, stream);
-    if (type == kCacheE4m3) return wide_one<128, kCacheE4m3>(p, sms, stream);
-    return wide_one<128, kCacheInt8>(p, sms, stream);
+    if (type == kCacheFp16) return wide_rows<128, kCacheFp16>(p, sms, stream);
+    if (type == kCacheE4m3) return wide_rows<128, kCacheE4m3>(p, sms, stream);
+    return wide_rows<128, kCacheInt8>(p, sms, stream);
   }
-  if (type == kCacheFp16) return wide_one<64, kCacheFp16>(p, sms, stream);
-  if (type == kCacheE4m3) return wide_one<64, kCacheE4m3>(p, sms, stream);
-  return wide_one<64, kCacheInt8>(p, sms, stream);
+  if (type == kCacheFp16) return wide_rows<64, kCacheFp16>(p, sms, stream);
+  if (type == kCacheE4m3) return wide_rows<64, kCacheE4m3>(p, sms, stream);
+  return wide_rows<64, kCacheInt8>(p, sms, stream);
 }
 
 cudaError_t read_attend_wait_timeouts(unsigned long long* count, int reset) {

@@ -71,7 +71,7 @@ cudaError_t launch_attend(const AttendParams& p, int head_dim, int type, int sms
                           cudaStream_t stream);
 
 // Many rows per key head (attend_wide.cu).
-size_t attend_wide_workspace_bytes(int64_t items, int head_dim, int sms);
+size_t attend_wide_workspace_bytes(int64_t seqs, int kv_heads, int rows, int head_dim, int sms);
 cudaError_t launch_attend_wide(const AttendParams& p, int head_dim, int type, int sms,
                                cudaStream_t stream);
 // Its bounded waits that gave up since the last reset.

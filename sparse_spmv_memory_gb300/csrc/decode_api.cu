@@ -40,8 +40,8 @@ int check_cache(const nm_cache* c, CacheView* v) {
     return NM_ERR_SHAPE;
   const int64_t per_page = c->kv_heads * ps;
   // a page's stride and the cache's last element stay far below 2^63
-  if (c->page_stride < per_page * c->head_dim || c->page_stride >= ((int64_t)1 << 40) ||
-      (scaled && (c->scale_page_stride < per_page || c->scale_page_stride >= ((int64_t)1 << 40))))
+  if (c->page_stride < per_page * c->head_dim || c->page_stride >= ((int64_t)1 << 38) ||
+      (scaled && (c->scale_page_stride < per_page || c->scale_page_stride >= ((int64_t)1 << 38))))
     return NM_ERR_SHAPE;
   if (!aligned(c->k, 32) || !aligned(c->v, 32) || c->page_stride * code_bytes(c->type) % 32 != 0 ||
       (scaled && (!aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))))
