@@ -50,13 +50,21 @@ constexpr float kTinyScale = 7.888609052210118e-31f;  // 2^-100: a smaller scale
 template <int D, int TYPE, bool PAIR>
 struct Wide {
   static constexpr bool F16 = TYPE == kCacheFp16;
-  static constexpr int LW = F16 ? 3 : 7;  // loader warps: 384 or 512 threads
+  // Loader warps (384 or 512 threads).  8-bit: one fetches, two groups of CW
+  // widen the even and the odd positions of the ring; NS and RS are even, so
+  // that a slot's barriers are always waited on by the same group.
+  static constexpr int LW = F16 ? 3 : 7, CW = 3;
   static constexpr int THREADS = 32 * (kLoadWarp + LW);
+  // Registers of a thread: the launch gives every warpgroup (65536 / THREADS,
+  // rounded down to 8) of them, the softmax warpgroups take some of the others'.
+  static constexpr int REGS = F16 ? 168 : 128, SOFT_REGS = F16 ? 200 : 168, OTHER_REGS = F16 ? 104 : 88;
+  static_assert(2 * SOFT_REGS + (THREADS / 128 - 2) * OTHER_REGS <= THREADS / 128 * REGS,
+                "the split fits the launch");
   static constexpr int QT = PAIR ? 2 : 1;     // row tiles of an item
   static constexpr int TILE = kKeys * D * 2;  // bytes of a stage
   static constexpr int HALF = kKeys * 128;    // 64 elements of every row
-  static constexpr int NS = F16 ? (D == 128 ? (PAIR ? 4 : 5) : 8) : (D == 128 ? 3 : 6);
-  static constexpr int RS = F16 ? 0 : (D == 128 ? (PAIR ? 2 : 4) : 4);  // raw tiles
+  static constexpr int NS = F16 ? (D == 128 ? (PAIR ? 4 : 5) : 8) : (D == 128 ? 2 : 4);
+  static constexpr int RS = F16 ? 0 : (D == 128 && PAIR ? 4 : 6);  // raw tiles
   static constexpr int RAW = kKeys * D;
   static constexpr int Q_OFF = 0;
   static constexpr int ST_OFF = Q_OFF + QT * kRows * D * 2;
@@ -66,6 +74,7 @@ struct Wide {
   static constexpr int SMEM = BYTES + 1024;   // room to align the base
   static_assert(SMEM <= 227 * 1024 - 4096, "static shared memory needs room too");
   static_assert(NS + RS <= 10 && NS <= 8, "see above");
+  static_assert(F16 || (NS % 2 == 0 && RS % 2 == 0 && LW == 1 + 2 * CW), "see above");
 };
 
 // TMEM columns.
@@ -74,6 +83,36 @@ constexpr uint32_t kS0 = 0, kS1 = 128, kO0 = 256, kO1 = 384, kTmemCols = 512;
 __device__ __forceinline__ uint32_t half2_of(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, w;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
 }
 
 __device__ __forceinline__ void sts_v4(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -112,19 +151,16 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_launch_dependents();
-  pdl_wait_previous();
   if (__syncthreads_or(threadIdx.x == 0 && wait_aborted())) return;
-  Sched sched;
-  if (!sched.init(p, 1)) return;
-
+  // what touches no caller's memory comes before the wait for the last kernel
   if (warp == 0 && lane == 0) {
     for (int s = 0; s < W::NS; ++s) {
-      mbar_init(full(s), W::LW);
+      mbar_init(full(s), F16 ? W::LW : W::CW);
       mbar_init(empty(s), 1);
     }
     for (int s = 0; s < RS; ++s) {
       mbar_init(rfull(s), 1);
-      mbar_init(rfree(s), W::LW);
+      mbar_init(rfree(s), W::CW);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(sfull(b), 1);
@@ -145,6 +181,9 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
     tmem_relinquish();
   }
   tc_fence_before_sync();
+  pdl_wait_previous();
+  Sched sched;
+  const bool work = sched.init(p, 1);
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = *(volatile uint32_t*)&tmem_slot;
@@ -154,8 +193,10 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
     return __all_sync(0xFFFFFFFFu, mbar_wait(bar, par)) != 0;
   };
 
-  if (warp >= kLoadWarp) {
+  if (!work) {
+  } else if (warp >= kLoadWarp) {
     // ---- loaders ---------------------------------------------------------------
+    regs_down<W::OTHER_REGS>();
     const int lw = warp - kLoadWarp, lt = lw * 32 + lane;
     constexpr int LT = W::LW * 32;
     const int page_rows = min(1 << p.c.page_shift, kKeys);  // rows of a box
@@ -237,12 +278,13 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
       return true;
     };
 
-    // 8-bit: raw position rc is K or V of tile t: bulk copies of page pieces.
-    auto fetch8 = [&](int rc, bool v, const Tile& t) {
-      if (lw != 0) return true;
-      const int st = rc % RS;
-      if (rc >= RS && !wait_warp(rfree(st), (rc / RS - 1) & 1)) return false;
-      const int64_t code = __shfl_sync(0xFFFFFFFFu, t.at.code, (lane * page_rows >> 3) & 15);
+    // 8-bit, the fetching warp: the raw ring's next position is K or V of tile t.
+    auto fetch8 = [&](bool v, const Tile& t, bool first) {
+      const int st = c % RS;
+      if (c >= RS && !wait_warp(rfree(st), (c / RS - 1) & 1)) return false;
+      if (!v) note(t, first);
+      const int group = (lane * page_rows >> 3) & 15;
+      const int64_t code = __shfl_sync(0xFFFFFFFFu, t.at.code, group);
       const bool on = lane < boxes && code >= 0;
       const int have = __popc(__ballot_sync(0xFFFFFFFFu, on));
       if (lane == 0) mbar_arrive_expect_tx(rfull(st), have * page_rows * D);
@@ -251,57 +293,64 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
         bulk_load(base + W::RAW_OFF + st * W::RAW + lane * page_rows * D, (v ? p.c.v : p.c.k) + code,
                   page_rows * D, rfull(st));
       __syncwarp();
+      ++c;
       return true;
     };
-    float sc_k = 0.0f, sc_v = 0.0f;  // thread lt < 128: the next tile's scales of row lt
-    auto load_scales = [&](const Tile& t) {
-      const int r = lt & (kKeys - 1);
-      const int64_t at = __shfl_sync(0xFFFFFFFFu, t.at.scale, r >> 3);
-      const bool on = lt < kKeys && at >= 0 && r < t.left;
-      sc_k = on ? p.c.k_scale[at + (r & 7)] : 0.0f;
-      sc_v = on ? p.c.v_scale[at + (r & 7)] : 0.0f;
-    };
-    // Widens the raw tile of position c into its stage.
-    auto emit8 = [&](bool v, const Tile& t, bool first) {
+    // 8-bit, a widening group (ct: thread of it): the raw tile of position c to
+    // its stage; with a K tile its scales: k scale log2(e), log2 v, 1 / v.
+    const int ct = lt - 32 - (lw > W::CW ? W::CW * 32 : 0);
+    constexpr int CT = W::CW * 32;
+    auto widen8 = [&](bool v, const Tile& t) {
       const int st = c % W::NS, rs = c % RS;
+      float sc[2][2];  // rows ct and ct + CT: k, v scale; in flight while the codes are waited for
+      if (!v) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = min(ct + i * CT, kKeys - 1);
+          const int64_t at = __shfl_sync(0xFFFFFFFFu, t.at.scale, r >> 3);
+          const bool on = at >= 0 && r < t.left;
+          sc[i][0] = on ? p.c.k_scale[at + (r & 7)] : 0.0f;
+          sc[i][1] = on ? p.c.v_scale[at + (r & 7)] : 0.0f;
+        }
+      }
       if (!wait_warp(rfull(rs), (c / RS) & 1)) return false;
       if (c >= W::NS && !wait_warp(empty(st), (c / W::NS - 1) & 1)) return false;
       const uint32_t dst = sT + st * W::TILE, src = base + W::RAW_OFF + rs * W::RAW;
-      if (!v && lw == 0) note(t, first);
       constexpr int PR = D / 16;  // pieces of a row
-#pragma unroll 2
-      for (int id = lt; id < kKeys * PR; id += LT) {
+      const bool look = v && t.edge;
+#pragma unroll 4
+      for (int id = ct; id < kKeys * PR; id += CT) {
         const int r = id / PR, ch = id % PR;
         uint32_t w[4], h[8];
         asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                      : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
                      : "r"(src + id * 16));
-        if (v && t.edge) {
-          const bool on = r < t.left && ((t.there >> (r >> 3)) & 1u);
-          if (!on) w[0] = w[1] = w[2] = w[3] = 0;
-        }
+        if (look && !(r < t.left && ((t.there >> (r >> 3)) & 1u))) w[0] = w[1] = w[2] = w[3] = 0;
 #pragma unroll
         for (int k = 0; k < 4; ++k) widen4<F16 ? kCacheE4m3 : TYPE>(w[k], h[2 * k], h[2 * k + 1]);
-        if (v && t.edge) {
-          if (TYPE == kCacheE4m3 && t.node0 + r >= 0) clean(h, 8, t.node0 + r, t.bad);
-        }
+        if (TYPE == kCacheE4m3 && look && t.node0 + r >= 0) clean(h, 8, t.node0 + r, t.bad);
         const uint32_t at = dst + (ch >> 2) * W::HALF + r * 128;
         const uint32_t c0 = (ch & 3) * 2;
         sts_v4(at + ((c0 ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
         sts_v4(at + (((c0 + 1) ^ (r & 7)) << 4), h[4], h[5], h[6], h[7]);
       }
-      if (!v && lt < kKeys) {  // the tile's scales: k scale log2(e), log2 v, 1 / v
-        float lv = log2f(sc_v), rv = 1.0f / sc_v;
-        if (sc_v < kTinyScale) lv = -100.0f, rv = 1.0f / kTinyScale;
-        const int j = t.node0 + lt;
-        if (t.edge && j >= 0 && !(sc_v < INFINITY)) {  // a node's row whose scale is not finite
-          lv = 0.0f, rv = 1.0f;
-          atomicOr(&bad_of[t.bad][(j >> 5) & 1], 1u << (j & 31));
+      if (!v) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = ct + i * CT, j = t.node0 + r;
+          if (r >= kKeys) continue;
+          const float x = sc[i][1];
+          float lv = log2f(x), rv = 1.0f / x;
+          if (x < kTinyScale) lv = -100.0f, rv = 1.0f / kTinyScale;
+          if (t.edge && j >= 0 && !(x < INFINITY)) {  // a node's row whose scale is not finite
+            lv = 0.0f, rv = 1.0f;
+            atomicOr(&bad_of[t.bad][(j >> 5) & 1], 1u << (j & 31));
+          }
+          float* f = scales + t.meta * kKeys + r;
+          f[0] = sc[i][0] * cs;
+          f[kMeta * kKeys] = lv;
+          f[2 * kMeta * kKeys] = rv;
         }
-        float* f = scales + t.meta * kKeys + lt;
-        f[0] = sc_k * cs;
-        f[kMeta * kKeys] = lv;
-        f[2 * kMeta * kKeys] = rv;
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -309,13 +358,12 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
         mbar_arrive(full(st));
         mbar_arrive(rfree(rs));
       }
-      ++c;
       return true;
     };
 
     // The positions of the ring in order: K0, V0, K1, V1, ... for PAIR, else
     // K0, K1, V0, K2, V1, ..., as the MMA thread takes them.  `Walk` yields them
-    // one by one; the 8-bit loaders run two of them, one a raw ring ahead.
+    // one by one.
     struct Walk {
       Sched sched;
       Span w;
@@ -383,132 +431,125 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
         item_no = x.items;
         ok = emit16(v, v ? v_tile(x) : x.k, first);
       }
-    } else {
-      Walk y = x;  // fetches RS positions ahead
-      int fc = 0;
-      bool more = true, fv, ff;
-      for (; ok && more && fc < RS; ++fc) {
-        more = step(y, fv, ff);
-        if (!more) break;
-        ok = fetch8(fc, fv, fv ? v_tile(y) : y.k);
-      }
+    } else if (lw == 0) {
       while (ok && step(x, v, first)) {
         item_no = x.items;
-        if (first) load_scales(x.k);
-        ok = emit8(v, v ? v_tile(x) : x.k, first);
-        if (!ok) break;
-        if (!v && x.i < x.n) {  // the next K tile's scales
-          Tile t = x.k;
-          t.pos0 += kKeys;
-          t.at = group_at<D>(p, x.entry, x.w.h, t.pos0 + 8 * (lane & 15));
-          t.left = (int)min((int64_t)kKeys, x.si.len - t.pos0);
-          load_scales(t);
-        }
-        if (more) {
-          more = step(y, fv, ff);
-          if (more) ok = fetch8(fc++, fv, fv ? v_tile(y) : y.k);
-        }
+        ok = fetch8(v, v ? v_tile(x) : x.k, first);
       }
+    } else {
+      for (; ok && step(x, v, first); ++c)
+        if ((c & 1) == (lw > W::CW ? 1 : 0)) ok = widen8(v, v ? v_tile(x) : x.k);
     }
     // Before the block ends its copies have landed and every release of a stage
     // has arrived.
-    if (!F16 && !ok && lw == 0) {  // raw tiles that nobody waited for
-      for (int s = 0; s < RS; ++s) mbar_wait(rfull(s), (c / RS) & 1, 100000000ull, false);
+    if (F16 || lw == 0) {
+      constexpr int NC = F16 ? W::NS : RS;
+      for (int pos = max(0, c - NC); pos < c; ++pos)
+        mbar_wait(F16 ? full(pos % W::NS) : rfull(pos % RS), (pos / NC) & 1, kWaitLimitNs, ok);
     }
-    for (int pos = max(0, c - W::NS); pos < c; ++pos) {
-      if (F16) mbar_wait(full(pos % W::NS), (pos / W::NS) & 1, kWaitLimitNs, ok);
-      if (ok) ok = wait_warp(empty(pos % W::NS), (pos / W::NS) & 1);
+    if (F16 || lw > 0) {
+      for (int pos = max(0, c - W::NS); ok && pos < c; ++pos)
+        if (F16 || (pos & 1) == (lw > W::CW ? 1 : 0))
+          ok = wait_warp(empty(pos % W::NS), (pos / W::NS) & 1);
     }
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // ---- MMA issuer ----------------------------------------------------------------
-    if (lane == 0) {
-      constexpr uint32_t id_s = idesc_f16_f32(kRows, kKeys);
-      constexpr uint32_t id_o = idesc_f16_f32(kRows, D) | kIdescBMajorMN;
-      int c = 0, items = 0, np[2] = {0, 0};
-      bool ok = true;
-      Span w;
-      SeqInfo si;
-      auto ready = [&](int pos) {
-        if (!mbar_wait(full(pos % W::NS), (pos / W::NS) & 1)) return false;
-        tc_fence_after_sync();
-        return true;
-      };
-      auto scores = [&](int pos, int b) {  // stream b, the K tile of ring position pos
-        const uint32_t d = tmem + (b ? kS1 : kS0), k = sT + pos % W::NS * W::TILE;
-        const uint32_t q = sQ + (PAIR && b ? kRows * D * 2 : 0);
+    // The warp walks together, one lane issues.
+    regs_down<W::OTHER_REGS>();
+    constexpr uint32_t id_s = idesc_f16_f32(kRows, kKeys);
+    constexpr uint32_t id_o = idesc_f16_f32(kRows, D) | kIdescBMajorMN;
+    const bool lead = elect_one();
+    const uint32_t q_lo = desc_sw128_lo(sQ, 16), k_lo = desc_sw128_lo(sT, 16),
+                   v_lo = desc_sw128_lo(sT, W::HALF);
+    int c = 0, items = 0, np[2] = {0, 0};
+    bool ok = true;
+    Span w;
+    SeqInfo si;
+    auto ready = [&](int pos) {
+      if (!wait_warp(full(pos % W::NS), (pos / W::NS) & 1)) return false;
+      tc_fence_after_sync();
+      return true;
+    };
+    auto scores = [&](int pos, int b) {  // stream b, the K tile of ring position pos
+      const uint32_t d = tmem + (b ? kS1 : kS0), k = k_lo + pos % W::NS * (W::TILE >> 4);
+      const uint32_t q = q_lo + (PAIR && b ? (kRows * D * 2) >> 4 : 0);
+      if (lead) {
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t off = (ks >> 2) * W::HALF + (ks & 3) * 32;
-          mma_f16(d, smem_desc_sw128(q + off, 16), smem_desc_sw128(k + off, 16), id_s, ks != 0);
+          const uint32_t off = ((ks >> 2) * W::HALF + (ks & 3) * 32) >> 4;
+          mma_f16(d, desc_of(q + off, kDescSw128Hi), desc_of(k + off, kDescSw128Hi), id_s, ks != 0);
         }
         mma_commit(sfull(b));
-      };
-      auto sums = [&](int pos, int b, bool add) {
-        if (!mbar_wait(pfull(b), np[b]++ & 1)) return false;
-        tc_fence_after_sync();
-        const uint32_t d = tmem + (b ? kO1 : kO0), a = tmem + (b ? kS1 : kS0);
-        const uint32_t v = sT + pos % W::NS * W::TILE;
+      }
+      __syncwarp();
+    };
+    auto sums = [&](int pos, int b, bool add) {
+      if (!wait_warp(pfull(b), np[b]++ & 1)) return false;
+      tc_fence_after_sync();
+      const uint32_t d = tmem + (b ? kO1 : kO0), a = tmem + (b ? kS1 : kS0);
+      const uint32_t v = v_lo + pos % W::NS * (W::TILE >> 4);
+      if (lead) {
 #pragma unroll
         for (int ks = 0; ks < kKeys / 16; ++ks)
-          mma_f16_ts(d, a + ks * 8, smem_desc_sw128(v + ks * 2048, W::HALF), id_o, add || ks != 0);
+          mma_f16_ts(d, a + ks * 8, desc_of(v + ks * (2048 >> 4), kDescSw128Hi), id_o,
+                     ks != 0 ? 1u : add ? 1u : 0u);
         mma_commit(ofull(b));
-        return true;
-      };
-      while (ok && sched.next(p, w, si)) {
-        const int n = w.u1 - w.u0;
-        if (!mbar_wait(qfull, items & 1)) break;
-        ++items;
+      }
+      __syncwarp();
+      return true;
+    };
+    auto release = [&](int pos) {
+      if (lead) mma_commit(empty(pos % W::NS));
+      __syncwarp();
+    };
+    while (ok && sched.next(p, w, si)) {
+      const int n = w.u1 - w.u0;
+      if (!wait_warp(qfull, items & 1)) break;
+      ++items;
+      const bool two = PAIR && si.n * G - w.rt * IROWS > kRows;
+      ok = ready(c);
+      if (!ok) break;
+      scores(c, 0);
+      if (two) scores(c, 1);
+      release(c);
+      ++c;
+      for (int i = 0; i < n; ++i) {
+        const bool more = i + 1 < n;
         if (PAIR) {
-          const bool two = si.n * G - w.rt * IROWS > kRows;
-          ok = ready(c);
-          if (!ok) break;
-          scores(c, 0);
-          if (two) scores(c, 1);
-          mma_commit(empty(c % W::NS));
-          ++c;
-          for (int i = 0; i < n; ++i) {
-            const int cv = c, ck = c + 1;
-            const bool more = i + 1 < n;
-            ok = ready(cv) && sums(cv, 0, i > 0);
-            if (ok && more) {
-              ok = ready(ck);
-              if (ok) scores(ck, 0);
-            }
-            if (ok && two) ok = sums(cv, 1, i > 0);
-            if (!ok) break;
-            mma_commit(empty(cv % W::NS));
-            if (more) {
-              if (two) scores(ck, 1);
-              mma_commit(empty(ck % W::NS));
-            }
-            c += more ? 2 : 1;
+          const int cv = c, ck = c + 1;
+          ok = ready(cv) && sums(cv, 0, i > 0);
+          if (ok && more) {
+            ok = ready(ck);
+            if (ok) scores(ck, 0);
           }
-        } else {
-          ok = ready(c);
+          if (ok && two) ok = sums(cv, 1, i > 0);
           if (!ok) break;
-          scores(c, 0);
-          mma_commit(empty(c % W::NS));
-          ++c;
-          for (int i = 0; i < n; ++i) {
-            if (i + 1 < n) {
-              ok = ready(c);
-              if (!ok) break;
-              scores(c, (i + 1) & 1);
-              mma_commit(empty(c % W::NS));
-              ++c;
-            }
-            ok = ready(c) && sums(c, i & 1, i > 1);
+          release(cv);
+          if (more) {
+            if (two) scores(ck, 1);
+            release(ck);
+          }
+          c += more ? 2 : 1;
+        } else {
+          if (more) {
+            ok = ready(c);
             if (!ok) break;
-            mma_commit(empty(c % W::NS));
+            scores(c, (i + 1) & 1);
+            release(c);
             ++c;
           }
+          ok = ready(c) && sums(c, i & 1, i > 1);
+          if (!ok) break;
+          release(c);
+          ++c;
         }
       }
     }
     __syncwarp();
   } else {
     // ---- softmax -------------------------------------------------------------------
+    regs_up<W::SOFT_REGS>();
     const int b = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t tlane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t tS = tlane + (b ? kS1 : kS0), tO = tlane + (b ? kO1 : kO0);
@@ -534,14 +575,24 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
         const int t0 = PAIR ? threadIdx.x & 127 : threadIdx.x;
         const uint32_t q = sQ + (PAIR && b ? kRows * D * 2 : 0);
         const uint32_t sg = p.scale < 0.0f ? 0x80008000u : 0u;
-        for (int id = t0; id < kRows * (D / 8); id += PAIR ? 128 : 256) {
-          const int r = id / (D / 8), ch = id % (D / 8), rr = r0 + r;
-          uint4 x = make_uint4(0, 0, 0, 0);
-          if (r < rows)
-            x = *reinterpret_cast<const uint4*>(p.q + (int64_t)(si.first + rr / G) * p.ldq +
-                                                (int64_t)(w.h * G + rr % G) * D + ch * 8);
-          sts_v4(q + (ch >> 3) * W::HALF + r * 128 + (((ch & 7) ^ (r & 7)) << 4), x.x ^ sg, x.y ^ sg,
-                 x.z ^ sg, x.w ^ sg);
+        constexpr int TH = PAIR ? 128 : 256, PER = kRows * (D / 8) / TH;
+        uint4 x[8];  // loads in flight
+#pragma unroll
+        for (int i0 = 0; i0 < PER; i0 += 8) {
+#pragma unroll
+          for (int i = 0; i < 8 && i0 + i < PER; ++i) {
+            const int id = t0 + (i0 + i) * TH, r = id / (D / 8), ch = id % (D / 8), rr = r0 + r;
+            x[i] = make_uint4(0, 0, 0, 0);
+            if (r < rows)
+              x[i] = ld_keep_v4(p.q + (int64_t)(si.first + rr / G) * p.ldq +
+                                (int64_t)(w.h * G + rr % G) * D + ch * 8);
+          }
+#pragma unroll
+          for (int i = 0; i < 8 && i0 + i < PER; ++i) {
+            const int id = t0 + (i0 + i) * TH, r = id / (D / 8), ch = id % (D / 8);
+            sts_v4(q + (ch >> 3) * W::HALF + r * 128 + (((ch & 7) ^ (r & 7)) << 4), x[i].x ^ sg,
+                   x[i].y ^ sg, x[i].z ^ sg, x[i].w ^ sg);
+          }
         }
       }
       fence_proxy_async_smem();
@@ -610,6 +661,55 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
                 if (!((see >> x) & 1u)) v[x] = 0xFF800000u;  // -inf
             }
           };
+          // Most tiles: no row's maximum moves.  Weights by the maximum so far,
+          // in one reading of the scores; kept only if no score exceeds it.
+          bool done = false;
+          if (k > 0 && !edge && __all_sync(0xFFFFFFFFu, m > -INFINITY)) {
+            uint32_t h[64];
+            float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+            float t[2] = {-INFINITY, -INFINITY};
+            const float2 mm = make_float2(-m, -m), cc = make_float2(cs, cs);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              uint32_t v[32];
+              tmem_ld_32(tS + 32 * y, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int x = 0; x < 32; x += 4) {
+                float2 e0 = make_float2(__uint_as_float(v[x]), __uint_as_float(v[x + 1]));
+                float2 e1 = make_float2(__uint_as_float(v[x + 2]), __uint_as_float(v[x + 3]));
+                if (F16) {
+                  e0 = fma2(e0, cc, mm);
+                  e1 = fma2(e1, cc, mm);
+                } else {
+                  const float4 a = ksc[8 * y + x / 4], d = lvs[8 * y + x / 4];
+                  e0 = add2(fma2(e0, make_float2(a.x, a.y), make_float2(d.x, d.y)), mm);
+                  e1 = add2(fma2(e1, make_float2(a.z, a.w), make_float2(d.z, d.w)), mm);
+                }
+                t[0] = fmaxf(fmaxf(t[0], e0.x), e0.y);
+                t[1] = fmaxf(fmaxf(t[1], e1.x), e1.y);
+                e0 = make_float2(exp2_fast(e0.x), exp2_fast(e0.y));
+                e1 = make_float2(exp2_fast(e1.x), exp2_fast(e1.y));
+                if (F16) {
+                  sum[0] = add2(sum[0], e0);
+                  sum[1] = add2(sum[1], e1);
+                } else {
+                  const float4 r = rvs[8 * y + x / 4];
+                  sum[0] = fma2(e0, make_float2(r.x, r.y), sum[0]);
+                  sum[1] = fma2(e1, make_float2(r.z, r.w), sum[1]);
+                }
+                h[16 * y + x / 2] = half2_of(e0.x, e0.y);
+                h[16 * y + x / 2 + 1] = half2_of(e1.x, e1.y);
+              }
+            }
+            done = __all_sync(0xFFFFFFFFu, fmaxf(t[0], t[1]) <= kGrow);
+            if (done) {
+#pragma unroll
+              for (int y = 0; y < 4; ++y) tmem_st_16(tS + 16 * y, h + 16 * y);
+              l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            }
+          }
+          if (!done) {
           float top = -INFINITY;
 #pragma unroll 1
           for (int y = 0; y < 4; ++y) {
@@ -666,6 +766,7 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
             }
             l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             tmem_st_16(tS + 16 * y, h);
+          }
           }
           tmem_st_wait();
         }
@@ -762,47 +863,59 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
       ok = soft_sync();
       if (!ok) break;
       if (!*(volatile uint32_t*)&s_last) continue;
-      if (mine) {
-        __threadfence();
-        const float* part0 = slots + part_slot(b0, sched.per, w.start) * attend_slot_floats(IROWS, D);
-        auto part = [&](int64_t y) {  // after the first, an item's part begins its block's range
-          return y == b0 ? part0 : slots + (size_t)y * 2 * attend_slot_floats(IROWS, D);
-        };
+      __threadfence();
+      float* part0 = slots + part_slot(b0, sched.per, w.start) * attend_slot_floats(IROWS, D);
+      auto part = [&](int y) {  // after the first, an item's part begins its block's range
+        return y == 0 ? part0 : slots + (size_t)(b0 + y) * 2 * attend_slot_floats(IROWS, D);
+      };
+      const int parts = (int)(b1 - b0) + 1;
+      if (mine && (PAIR || b == 0)) {
         float M2 = -INFINITY, tot2 = 0.0f;
-        for (int64_t y = b0; y <= b1; ++y) M2 = fmaxf(M2, __ldcg(part(y) + IROWS * D + srow));
-        const float off2 = M2 == -INFINITY ? 0.0f : M2;
-        for (int64_t y = b0; y <= b1; ++y) {
+#pragma unroll 8
+        for (int y = 0; y < parts; ++y) {
           const float* f = part(y) + IROWS * D;
-          tot2 += __ldcg(f + IROWS + srow) * exp2_fast(__ldcg(f + srow) - off2);
+          const float m1 = __ldcg(f + srow), l1 = __ldcg(f + IROWS + srow), m2 = fmaxf(M2, m1);
+          const float o = m2 == -INFINITY ? 0.0f : m2;
+          tot2 = tot2 * exp2_fast(M2 - o) + l1 * exp2_fast(m1 - o);
+          M2 = m2;
         }
-        const float inv2 = tot2 == 0.0f ? 0.0f : 1.0f / tot2;
-#pragma unroll 1
-        for (int d0 = c0; d0 < c1; d0 += 16) {
-          float4 x[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) x[k] = make_float4(0, 0, 0, 0);
-#pragma unroll 2
-          for (int64_t y = b0; y <= b1; ++y) {
-            const float* f = part(y);
-            const float e = exp2_fast(__ldcg(f + IROWS * D + srow) - off2);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(f) + (d0 / 4 + k) * IROWS + srow);
-              x[k].x += v.x * e, x[k].y += v.y * e, x[k].z += v.z * e, x[k].w += v.w * e;
-            }
-          }
-#pragma unroll
-          for (int k = 0; k < 4; k += 2)
-            *reinterpret_cast<uint4*>(out + d0 + 4 * k) =
-                make_uint4(half2_of(x[k].x * inv2, x[k].y * inv2), half2_of(x[k].z * inv2, x[k].w * inv2),
-                           half2_of(x[k + 1].x * inv2, x[k + 1].y * inv2),
-                           half2_of(x[k + 1].z * inv2, x[k + 1].w * inv2));
-        }
-        if (writes && p.lse)
+        s_ml[PAIR ? b : 0][row] =
+            make_float2(M2 == -INFINITY ? 0.0f : M2, tot2 == 0.0f ? 0.0f : 1.0f / tot2);
+        if (p.lse)
           p.lse[(int64_t)(si.first + node) * p.q_heads + w.h * G + rr % G] =
               tot2 == 0.0f ? -INFINITY : (M2 + log2f(tot2)) * kLn2;
       }
-      __syncwarp();
+      ok = soft_sync();
+      if (!ok) break;
+      // a warp takes 32 rows and 32 columns at a time: many loads in flight
+      const int all = min(IROWS, si.n * G - w.rt * IROWS), blocks32 = (all + 31) / 32;
+      for (int e = warp; e < blocks32 * (D / 32); e += kSoftWarps) {
+        const int r = e % blocks32 * 32 + lane, d4 = e / blocks32 * 8;
+        if (r < all) {
+          const float2 mi = s_ml[r / kRows][r % kRows];
+          float4 x[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) x[k] = make_float4(0, 0, 0, 0);
+#pragma unroll 2
+          for (int y = 0; y < parts; ++y) {
+            const float* f = part(y);
+            const float g = exp2_fast(__ldcg(f + IROWS * D + r) - mi.x) * mi.y;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(f) + (d4 + k) * IROWS + r);
+              x[k].x += v.x * g, x[k].y += v.y * g, x[k].z += v.z * g, x[k].w += v.w * g;
+            }
+          }
+          const int r2 = w.rt * IROWS + r;
+          __half* dst = p.out + (int64_t)(si.first + r2 / G) * p.ldo + (int64_t)(w.h * G + r2 % G) * D + 4 * d4;
+#pragma unroll
+          for (int k = 0; k < 8; k += 2)
+            *reinterpret_cast<uint4*>(dst + 4 * k) =
+                make_uint4(half2_of(x[k].x, x[k].y), half2_of(x[k].z, x[k].w),
+                           half2_of(x[k + 1].x, x[k + 1].y), half2_of(x[k + 1].z, x[k + 1].w));
+        }
+      }
+      ok = soft_sync();  // s_ml is free
     }
   }
 
@@ -816,6 +929,9 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
     if (lane == 0) {
       mbar_init(done, 1);
       fence_mbar_init();
+    }
+    __syncwarp();
+    if (elect_one()) {  // the lane that issued them
       mma_commit(done);
       mbar_wait(done, 0, kWaitLimitNs, false);
     }

@@ -209,13 +209,29 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(uint32_t M, uint32_t N) {
 // the 128-byte swizzle, 8-row groups 1024 bytes apart.  A K-major operand's
 // rows run along K and `lbo` is unused; an MN-major one's run along M or N, a
 // group of 8 rows is 8 steps of K, and the next 64 of M or N begin `lbo` bytes on.
-__device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr, uint32_t lbo) {
-  uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFFu);
-  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
-  d |= (uint64_t)(1024u >> 4) << 32;
-  d |= (uint64_t)1u << 46;
-  d |= (uint64_t)2u << 61;
+// In halves: the low word moves with the address (add
+// bytes / 16; shared memory's addresses stay within its 14 bits), the high one
+// is constant.  One thread issues many MMAs, and each instruction it needs for
+// a descriptor costs it several cycles.
+__device__ __forceinline__ uint32_t desc_sw128_lo(uint32_t saddr, uint32_t lbo) {
+  return ((saddr >> 4) & 0x3FFFu) | ((lbo >> 4) & 0x3FFFu) << 16;
+}
+constexpr uint32_t kDescSw128Hi = (1024u >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo, uint32_t hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
   return d;
+}
+
+// True in one lane of a whole warp, always the same one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
 }
 
 // The bit of the instruction descriptor that makes B MN-major.
