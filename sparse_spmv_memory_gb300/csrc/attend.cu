@@ -100,6 +100,7 @@ __global__ void __launch_bounds__(NW * 32, 1) attend_narrow_kernel(AttendParams 
   if (!sched.init(p, NW)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   const int G = p.q_heads / p.c.kv_heads;
+  const Heads heads(G);
   const float cs = p.scale * kLog2e;
   int* counters = reinterpret_cast<int*>(p.workspace);
   float* slots = reinterpret_cast<float*>(
@@ -119,13 +120,13 @@ __global__ void __launch_bounds__(NW * 32, 1) attend_narrow_kernel(AttendParams 
         const int r = 16 * mt + (ln >> 2) + 8 * k, rr = w.rt * ROWS + r;
         v[k] = make_uint2(0, 0);
         if (r < rows)
-          v[k] = *reinterpret_cast<const uint2*>(p.q + (int64_t)(si.first + rr / G) * p.ldq +
-                                                 (int64_t)(w.h * G + rr % G) * D + e);
+          v[k] = *reinterpret_cast<const uint2*>(p.q + (int64_t)(si.first + heads.node(rr)) * p.ldq +
+                                                 (w.h * G + heads.head(rr)) * D + e);
       }
       sq[mt][ks][ln] = make_uint4(v[0].x, v[1].x, v[0].y, v[1].y);
     }
     for (int r = threadIdx.x; r < ROWS; r += NTH) {
-      const int node = (w.rt * ROWS + r) / G;
+      const int node = heads.node(w.rt * ROWS + r);
       smask[r] = r >= rows ? 0ull : p.tree_mask ? p.tree_mask[si.first + node] : (2ull << node) - 1ull;
     }
     __syncthreads();
@@ -430,7 +431,7 @@ __global__ void __launch_bounds__(NW * 32, 1) attend_narrow_kernel(AttendParams 
       if (whole) {
         const float inv = row_l[r] == 0.0f ? 0.0f : 1.0f / row_l[r];
         const int rr = w.rt * ROWS + r;
-        __half* dst = p.out + (int64_t)(si.first + rr / G) * p.ldo + (int64_t)(w.h * G + rr % G) * D + d;
+        __half* dst = p.out + (int64_t)(si.first + heads.node(rr)) * p.ldo + (w.h * G + heads.head(rr)) * D + d;
         *reinterpret_cast<uint2*>(dst) =
             make_uint2(pack_half2(x.x * inv, x.y * inv), pack_half2(x.z * inv, x.w * inv));
       } else {
@@ -441,7 +442,7 @@ __global__ void __launch_bounds__(NW * 32, 1) attend_narrow_kernel(AttendParams 
       if (whole) {
         const int rr = w.rt * ROWS + r;
         if (p.lse)
-          p.lse[(int64_t)(si.first + rr / G) * p.q_heads + w.h * G + rr % G] =
+          p.lse[(int64_t)(si.first + heads.node(rr)) * p.q_heads + w.h * G + heads.head(rr)] =
               row_l[r] == 0.0f ? -INFINITY : (row_m[r] + log2f(row_l[r])) * kLn2;
       } else {
         slot[(size_t)ROWS * D + r] = row_m[r];
@@ -473,7 +474,7 @@ __global__ void __launch_bounds__(NW * 32, 1) attend_narrow_kernel(AttendParams 
       row_l[r] = tot == 0.0f ? 0.0f : 1.0f / tot;
       const int rr = w.rt * ROWS + r;
       if (p.lse)
-        p.lse[(int64_t)(si.first + rr / G) * p.q_heads + w.h * G + rr % G] =
+        p.lse[(int64_t)(si.first + heads.node(rr)) * p.q_heads + w.h * G + heads.head(rr)] =
             tot == 0.0f ? -INFINITY : (M + log2f(tot)) * kLn2;
     }
     __syncthreads();
@@ -489,8 +490,8 @@ __global__ void __launch_bounds__(NW * 32, 1) attend_narrow_kernel(AttendParams 
       }
       const float inv = row_l[r];
       const int rr = w.rt * ROWS + r;
-      *reinterpret_cast<uint2*>(p.out + (int64_t)(si.first + rr / G) * p.ldo +
-                                (int64_t)(w.h * G + rr % G) * D + d) =
+      *reinterpret_cast<uint2*>(p.out + (int64_t)(si.first + heads.node(rr)) * p.ldo +
+                                (w.h * G + heads.head(rr)) * D + d) =
           make_uint2(pack_half2(x.x * inv, x.y * inv), pack_half2(x.z * inv, x.w * inv));
     }
   }

@@ -34,6 +34,14 @@ __device__ __forceinline__ float log2_fast(float x) {
   return y;
 }
 
+// r / G for query rows (r < 2^13, 1 <= G <= 64) by a multiplication.
+struct Heads {
+  uint32_t g, inv;
+  __device__ __forceinline__ explicit Heads(int heads) : g(heads), inv(0xFFFFFFFFu / heads + 1u) {}
+  __device__ __forceinline__ int node(int r) const { return g == 1 ? r : (int)__umulhi(r, inv); }
+  __device__ __forceinline__ int head(int r) const { return r - node(r) * (int)g; }
+};
+
 // A sequence's rows and positions.
 struct SeqInfo {
   int first;    // its first token

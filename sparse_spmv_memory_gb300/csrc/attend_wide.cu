@@ -188,6 +188,7 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
   tc_fence_after_sync();
   const uint32_t tmem = *(volatile uint32_t*)&tmem_slot;
   const int G = p.q_heads / p.c.kv_heads;
+  const Heads heads(G);
   const float cs = fabsf(p.scale) * kLog2e;  // a negative scale's sign goes to the queries
   auto wait_warp = [&](uint32_t bar, uint32_t par) {
     return __all_sync(0xFFFFFFFFu, mbar_wait(bar, par)) != 0;
@@ -240,16 +241,25 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
       const uint32_t dst = sT + st * W::TILE;
       if (!v && lw == 0) note(t, first);
       if (v && t.edge) {  // absent rows are zeros, nodes' rows are looked at
-        constexpr int PR = D / 8;
-        for (int id0 = 0; id0 < kKeys * PR; id0 += LT) {
-          const int id = id0 + lt, r = min(id / PR, kKeys - 1), ch = id % PR;
-          const int64_t code = __shfl_sync(0xFFFFFFFFu, t.at.code, r >> 3);
-          if (id >= kKeys * PR) continue;
-          uint4 x = make_uint4(0, 0, 0, 0);
-          if (code >= 0 && r < t.left) x = ld_stream_v4(p.c.v + (code + (r & 7) * D + ch * 8) * 2);
-          uint32_t h[4] = {x.x, x.y, x.z, x.w};
-          if (t.node0 + r >= 0) clean(h, 4, t.node0 + r, t.bad);
-          sts_v4(dst + (ch >> 3) * W::HALF + r * 128 + (((ch & 7) ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
+        constexpr int PR = D / 8, B = 8;  // pieces of a row; loads in flight
+        for (int id0 = lt; id0 - lt < kKeys * PR; id0 += B * LT) {
+          uint4 x[B];
+#pragma unroll
+          for (int i = 0; i < B; ++i) {
+            const int id = id0 + i * LT, r = min(id / PR, kKeys - 1), ch = id % PR;
+            const int64_t code = __shfl_sync(0xFFFFFFFFu, t.at.code, r >> 3);
+            x[i] = make_uint4(0, 0, 0, 0);
+            if (id < kKeys * PR && code >= 0 && r < t.left)
+              x[i] = ld_stream_v4(p.c.v + (code + (r & 7) * D + ch * 8) * 2);
+          }
+#pragma unroll
+          for (int i = 0; i < B; ++i) {
+            const int id = id0 + i * LT, r = id / PR, ch = id % PR;
+            if (id >= kKeys * PR) continue;
+            uint32_t h[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            if (t.node0 + r >= 0) clean(h, 4, t.node0 + r, t.bad);
+            sts_v4(dst + (ch >> 3) * W::HALF + r * 128 + (((ch & 7) ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
+          }
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -576,30 +586,27 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
         const uint32_t q = sQ + (PAIR && b ? kRows * D * 2 : 0);
         const uint32_t sg = p.scale < 0.0f ? 0x80008000u : 0u;
         constexpr int TH = PAIR ? 128 : 256, PER = kRows * (D / 8) / TH;
-        uint4 x[8];  // loads in flight
+        uint4 x[PER];  // all loads in flight
 #pragma unroll
-        for (int i0 = 0; i0 < PER; i0 += 8) {
+        for (int i = 0; i < PER; ++i) {
+          const int id = t0 + i * TH, r = id / (D / 8), ch = id % (D / 8), rr = r0 + r;
+          x[i] = make_uint4(0, 0, 0, 0);
+          if (r < rows)
+            x[i] = ld_keep_v4(p.q + (int64_t)(si.first + heads.node(rr)) * p.ldq +
+                              (w.h * G + heads.head(rr)) * D + ch * 8);
+        }
 #pragma unroll
-          for (int i = 0; i < 8 && i0 + i < PER; ++i) {
-            const int id = t0 + (i0 + i) * TH, r = id / (D / 8), ch = id % (D / 8), rr = r0 + r;
-            x[i] = make_uint4(0, 0, 0, 0);
-            if (r < rows)
-              x[i] = ld_keep_v4(p.q + (int64_t)(si.first + rr / G) * p.ldq +
-                                (int64_t)(w.h * G + rr % G) * D + ch * 8);
-          }
-#pragma unroll
-          for (int i = 0; i < 8 && i0 + i < PER; ++i) {
-            const int id = t0 + (i0 + i) * TH, r = id / (D / 8), ch = id % (D / 8);
-            sts_v4(q + (ch >> 3) * W::HALF + r * 128 + (((ch & 7) ^ (r & 7)) << 4), x[i].x ^ sg,
-                   x[i].y ^ sg, x[i].z ^ sg, x[i].w ^ sg);
-          }
+        for (int i = 0; i < PER; ++i) {
+          const int id = t0 + i * TH, r = id / (D / 8), ch = id % (D / 8);
+          sts_v4(q + (ch >> 3) * W::HALF + r * 128 + (((ch & 7) ^ (r & 7)) << 4), x[i].x ^ sg,
+                 x[i].y ^ sg, x[i].z ^ sg, x[i].w ^ sg);
         }
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(qfull);
 
-      const int rr = r0 + row, node = rr / G;
+      const int rr = r0 + row, node = heads.node(rr), hq = w.h * G + heads.head(rr);
       const bool mine = row < rows;
       const uint64_t bits = !mine ? 0ull
                             : p.tree_mask ? p.tree_mask[si.first + node]
@@ -804,7 +811,7 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
       float4* slot4 = reinterpret_cast<float4*>(
           slots + part_slot(blockIdx.x, sched.per, w.start) * attend_slot_floats(IROWS, D));
       const int srow = (PAIR ? b * kRows : 0) + row;  // row of the item
-      __half* out = p.out + (int64_t)(si.first + node) * p.ldo + (int64_t)(w.h * G + rr % G) * D;
+      __half* out = p.out + (int64_t)(si.first + node) * p.ldo + (int64_t)hq * D;
       const int c0 = PAIR ? 0 : b * (D / 2), c1 = PAIR ? D : (b + 1) * (D / 2);
       if (!idle) {
 #pragma unroll 1
@@ -836,7 +843,7 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
       }
       const bool writes = mine && (PAIR || b == 0);
       if (writes && whole && p.lse)
-        p.lse[(int64_t)(si.first + node) * p.q_heads + w.h * G + rr % G] =
+        p.lse[(int64_t)(si.first + node) * p.q_heads + hq] =
             tot == 0.0f ? -INFINITY : (M + log2f(tot)) * kLn2;
       if (writes && !whole) {
         float* f = reinterpret_cast<float*>(slot4) + IROWS * D;
@@ -882,7 +889,7 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
         s_ml[PAIR ? b : 0][row] =
             make_float2(M2 == -INFINITY ? 0.0f : M2, tot2 == 0.0f ? 0.0f : 1.0f / tot2);
         if (p.lse)
-          p.lse[(int64_t)(si.first + node) * p.q_heads + w.h * G + rr % G] =
+          p.lse[(int64_t)(si.first + node) * p.q_heads + hq] =
               tot2 == 0.0f ? -INFINITY : (M2 + log2f(tot2)) * kLn2;
       }
       ok = soft_sync();
@@ -907,7 +914,8 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
             }
           }
           const int r2 = w.rt * IROWS + r;
-          __half* dst = p.out + (int64_t)(si.first + r2 / G) * p.ldo + (int64_t)(w.h * G + r2 % G) * D + 4 * d4;
+          __half* dst = p.out + (int64_t)(si.first + heads.node(r2)) * p.ldo +
+                        (w.h * G + heads.head(r2)) * D + 4 * d4;
 #pragma unroll
           for (int k = 0; k < 8; k += 2)
             *reinterpret_cast<uint4*>(dst + 4 * k) =
