@@ -1,5 +1,6 @@
 """Build step of the CUDA library: compiles csrc/*.cu for sm_103a with nvcc and
-links them into ``libnmspmv.so`` next to this file (in-tree, never installed).
+links them into ``libnmspmv.so`` next to this file (in-tree, never installed),
+and builds the compiled half of decode.py against it.
 
 The translation units are compiled in parallel; nothing is rebuilt when the
 library is newer than every source and header.
@@ -17,6 +18,9 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libnmspmv.so")
+# the compiled half of decode.py: tensors to arguments of the library's calls
+EXT_PATH = os.path.join(HERE, "_decode_ext.so")
+EXT_SOURCE = os.path.join(CSRC, "binding.cpp")
 
 SOURCES = ["api.cu", "spmv.cu", "spmm.cu", "spmm_b2.cu", "spmm_b4.cu", "spmm_b6.cu", "spmm_b8.cu",
            "spmm24.cu", "gemv.cu", "pack.cu", "check_noalloc.cu", "prefill.cu", "rope_cache.cu",
@@ -34,17 +38,40 @@ def nvcc() -> str:
 
 
 def _inputs() -> list[str]:
-    files = [os.path.join(CSRC, s) for s in SOURCES]
+    files = [os.path.join(CSRC, s) for s in SOURCES] + [EXT_SOURCE]
     files += glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
     files += glob.glob(os.path.join(INCLUDE, "*.h"))
     return files
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(EXT_PATH):
         return False
-    lib_t = os.path.getmtime(LIB_PATH)
-    return all(os.path.getmtime(f) <= lib_t for f in _inputs())
+    made = min(os.path.getmtime(LIB_PATH), os.path.getmtime(EXT_PATH))
+    return all(os.path.getmtime(f) <= made for f in _inputs())
+
+
+def _ext_command(out: str) -> tuple[list[str], list[str]]:
+    """(compile, link) commands of the binding for the running Python and PyTorch."""
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    obj = os.path.join(BUILD_DIR, "binding.o")
+    cxx = os.environ.get("CXX") or "g++"
+    compile_ = [cxx, "-std=c++17", "-O2", "-fPIC", "-Wall", f"-I{INCLUDE}",
+                "-isystem", os.path.join(root, "include"),
+                "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                "-isystem", os.path.join(cuda, "include"),
+                "-isystem", sysconfig.get_paths()["include"],
+                f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                "-c", EXT_SOURCE, "-o", obj]
+    link = [cxx, "-shared", "-o", out, obj, f"-L{HERE}", "-l:" + os.path.basename(LIB_PATH),
+            "-Wl,-rpath,$ORIGIN",
+            f"-L{os.path.join(root, 'lib')}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    return compile_, link
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
@@ -55,11 +82,14 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     exe = nvcc()
     extra = ["-Xptxas", "-v"] if ptxas_info else []
     procs = []
+    ext_tmp = EXT_PATH + ".tmp"
+    ext_compile, ext_link = _ext_command(ext_tmp)
     for src in SOURCES:
         obj = os.path.join(BUILD_DIR, src.replace(".cu", ".o"))
         cmd = [exe, *NVCC_FLAGS, *extra, "-c", os.path.join(CSRC, src), "-o", obj]
         procs.append((src, obj, subprocess.Popen(cmd, stdout=subprocess.PIPE,
                                                  stderr=subprocess.STDOUT, text=True)))
+    ext = subprocess.Popen(ext_compile, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
     objs, errors = [], []
     for src, obj, p in procs:
         out, _ = p.communicate()
@@ -68,14 +98,21 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         elif verbose or ptxas_info:
             sys.stdout.write(out)
         objs.append(obj)
+    out, _ = ext.communicate()
+    if ext.returncode != 0:
+        errors.append(f"--- {os.path.basename(EXT_SOURCE)} ---\n{out}")
     if errors:
-        raise RuntimeError("nvcc failed:\n" + "\n".join(errors))
+        raise RuntimeError("compilation failed:\n" + "\n".join(errors))
     tmp = LIB_PATH + ".tmp"
     cmd = [exe, *ARCH, "-shared", "-o", tmp, *objs]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError("link failed:\n" + res.stdout + res.stderr)
     os.replace(tmp, LIB_PATH)
+    res = subprocess.run(ext_link, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("link failed:\n" + res.stdout + res.stderr)
+    os.replace(ext_tmp, EXT_PATH)
     return LIB_PATH
 
 

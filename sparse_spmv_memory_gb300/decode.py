@@ -3,7 +3,8 @@
 and values into a paged cache, reading its rows back, attention of a tree of
 drafted tokens over the cache, and the verification of those tokens.
 
-As the rest of the binding this is marshalling only.  A cache is passed as its
+As the rest of the binding this is marshalling only, compiled (csrc/binding.cpp)
+because these calls take a few microseconds each.  A cache is passed as its
 tensors: ``k_cache`` and ``v_cache`` [pages][kv_heads][page_size][head_dim] of
 float16, float8_e4m3fn or int8 (the dtype names what it holds; any page stride,
 the inner three dimensions contiguous), and for the 8-bit types ``k_scale`` and
@@ -53,63 +54,22 @@ def declare(L) -> None:
         f.restype = res
 
 
-def _contiguous_after(t, first: int) -> bool:
-    """Whether the dimensions from ``first`` on are laid out densely."""
-    want = 1
-    for size, stride in zip(reversed(t.shape[first:]), reversed(t.stride()[first:])):
-        if size != 1 and stride != want:
-            return False
-        want *= size
-    return True
+_ext = None
 
 
-def _cache(k, v, k_scale, v_scale) -> _Cache:
-    torch = _nm._torch()
-    _nm._need_cuda(k, v, k_scale, v_scale)
-    types = {torch.float16: 0, torch.float8_e4m3fn: 1, torch.int8: 2}
-    if k.dtype not in types or v.dtype != k.dtype:
-        raise ValueError("k_cache and v_cache must both be float16, float8_e4m3fn or int8")
-    if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or \
-            not _contiguous_after(k, 1):
-        raise ValueError("k_cache and v_cache must be [pages][kv_heads][page_size][head_dim] of one "
-                         "shape and stride, contiguous but for the page stride")
-    scale_stride = 0
-    if k.dtype != torch.float16:
-        if k_scale is None or v_scale is None:
-            raise ValueError("an 8-bit cache needs k_scale and v_scale")
-        for s in (k_scale, v_scale):
-            if s.dtype != torch.float32 or s.shape != k.shape[:3] or \
-                    s.stride() != k_scale.stride() or not _contiguous_after(s, 1):
-                raise ValueError("k_scale and v_scale must be float32 [pages][kv_heads][page_size] "
-                                 "of one stride, contiguous but for the page stride")
-        scale_stride = k_scale.stride(0) if k.shape[0] > 1 else k.shape[1] * k.shape[2]
-    elif k_scale is not None or v_scale is not None:
-        raise ValueError("a float16 cache takes no scales")
-    pages, heads, page, dim = k.shape
-    stride = k.stride(0) if pages > 1 else heads * page * dim
-    return _Cache(k.data_ptr(), v.data_ptr(), _nm._ptr(k_scale), _nm._ptr(v_scale), pages, stride,
-                  scale_stride, heads, page, dim, types[k.dtype])
+def _calls():
+    """The compiled half of this module (csrc/binding.cpp)."""
+    global _ext
+    if _ext is None:
+        _nm._torch()  # its libraries are the binding's
+        _nm.lib()  # the library first: its absence is the clearer message
+        from . import _decode_ext
+        _ext = _decode_ext
+    return _ext
 
 
-def _vector(t, dtype, n, what):
-    """A contiguous device vector of ``n`` elements of ``dtype`` (or None)."""
-    if t is None:
-        return None
-    _nm._need_cuda(t)
-    if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous {dtype} tensor of {n} elements")
-    return t.data_ptr()
-
-
-def _heads(t, tokens, dim, what):
-    """(pointer, token stride) of fp16 [tokens][heads][dim] with dense heads."""
-    torch = _nm._torch()
-    _nm._need_cuda(t)
-    if t.dtype != torch.float16 or t.dim() != 3 or t.shape[0] != tokens or t.shape[2] != dim or \
-            not _contiguous_after(t, 1):
-        raise ValueError(f"{what} must be float16 [{tokens}][heads][{dim}], contiguous but for the "
-                         "token stride")
-    return t.data_ptr(), t.stride(0) if tokens > 1 else t.shape[1] * t.shape[2]
+def _given(stream):
+    return None if stream is None else _nm._stream(stream)
 
 
 def nm_rope_inv_freq(rot_dim: int, base: float = 10000.0, scaling: str | None = None,
@@ -137,49 +97,15 @@ def nm_rope_append(qkv, k_cache, v_cache, positions, slots, inv_freq, q_heads: i
     as long as the rotated part of a head.  Returns the rotated queries fp16
     [tokens][q_heads][head_dim] (``q`` if given; None with want_q=False, which
     skips them: the form that commits accepted tokens to their final slots)."""
-    torch = _nm._torch()
-    c = _cache(k_cache, v_cache, k_scale, v_scale)
-    _nm._need_cuda(qkv, inv_freq)
-    if qkv.dtype != torch.float16 or qkv.dim() != 2 or qkv.stride(1) != 1 or \
-            qkv.shape[1] != (q_heads + 2 * c.kv_heads) * c.head_dim:
-        raise ValueError("qkv must be float16 [tokens][(q_heads + 2 kv_heads) * head_dim] with unit "
-                         "column stride")
-    tokens = qkv.shape[0]
-    pos = _vector(positions, torch.int32, tokens, "positions")
-    slot = _vector(slots, torch.int64, tokens, "slots")
-    freq = _vector(inv_freq, torch.float32, inv_freq.numel(), "inv_freq")
-    if q is None and want_q:
-        q = torch.empty((tokens, q_heads, c.head_dim), dtype=torch.float16, device=qkv.device)
-    qp, ldq = (None, 0) if q is None else _heads(q, tokens, c.head_dim, "q")
-    if q is not None and q.shape[1] != q_heads:
-        raise ValueError("q must have q_heads heads")
-    _nm._check(_nm.lib().nm_rope_append(
-        qkv.data_ptr(), qkv.stride(0) if tokens > 1 else qkv.shape[1], tokens, q_heads, pos, slot,
-        freq, 2 * inv_freq.numel(), 1 if interleaved else 0, mscale, qp, ldq, ctypes.byref(c),
-        _nm._stream(stream)), "nm_rope_append")
-    return q
+    return _calls().rope_append(qkv, k_cache, v_cache, positions, slots, inv_freq, q_heads, k_scale,
+                                v_scale, interleaved, mscale, q, want_q, _given(stream))
 
 
 def nm_cache_read(k_cache, v_cache, slots, k_scale=None, v_scale=None, k=None, v=None,
                   stream=None):
     """Rows ``slots`` (int64; out of range: zeros) of the cache as fp16: (k, v),
     each [rows][kv_heads][head_dim]."""
-    torch = _nm._torch()
-    c = _cache(k_cache, v_cache, k_scale, v_scale)
-    rows = slots.numel()
-    slot = _vector(slots, torch.int64, rows, "slots")
-    shape = (rows, c.kv_heads, c.head_dim)
-    if k is None:
-        k = torch.empty(shape, dtype=torch.float16, device=slots.device)
-    if v is None:
-        v = torch.empty(shape, dtype=torch.float16, device=slots.device)
-    for t in (k, v):
-        _nm._need_cuda(t)
-        if t.dtype != torch.float16 or t.shape != shape or not t.is_contiguous():
-            raise ValueError("k and v must be contiguous float16 [rows][kv_heads][head_dim]")
-    _nm._check(_nm.lib().nm_cache_read(ctypes.byref(c), slot, rows, k.data_ptr(), v.data_ptr(),
-                                       _nm._stream(stream)), "nm_cache_read")
-    return k, v
+    return _calls().cache_read(k_cache, v_cache, slots, k_scale, v_scale, k, v, _given(stream))
 
 
 def nm_tree_attention_workspace_bytes(seqs: int, q_heads: int, kv_heads: int, head_dim: int,
@@ -202,39 +128,9 @@ def nm_tree_attention(q, k_cache, v_cache, block_table, ctx_len, q_start, max_no
     call leaves it ready); a zeroed one of
     nm_tree_attention_workspace_bytes(...) bytes is allocated when none is
     given."""
-    torch = _nm._torch()
-    c = _cache(k_cache, v_cache, k_scale, v_scale)
-    tokens, q_heads, dim = q.shape
-    qp, ldq = _heads(q, tokens, c.head_dim, "q")
-    seqs = ctx_len.numel()
-    ctx = _vector(ctx_len, torch.int32, seqs, "ctx_len")
-    start = _vector(q_start, torch.int32, seqs + 1, "q_start")
-    mask = _vector(tree_mask, torch.int64, tokens, "tree_mask")
-    _nm._need_cuda(block_table, workspace)
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or \
-            block_table.shape[0] != seqs or block_table.stride(1) != 1 and block_table.shape[1] != 1:
-        raise ValueError("block_table must be int32 [seqs][entries] with unit column stride")
-    if out is None:
-        out = torch.empty((tokens, q_heads, dim), dtype=torch.float16, device=q.device)
-    op, ldo = _heads(out, tokens, c.head_dim, "out")
-    if out.shape[1] != q_heads:
-        raise ValueError("out must have as many heads as q")
-    if lse is None:
-        lse = torch.empty((tokens, q_heads), dtype=torch.float32, device=q.device)
-    lp = _vector(lse, torch.float32, tokens * q_heads, "lse")
-    L = _nm.lib()
-    if workspace is None:
-        need = L.nm_tree_attention_workspace_bytes(seqs, q_heads, c.kv_heads, dim, max_nodes)
-        if need:
-            workspace = torch.zeros(need, dtype=torch.uint8, device=q.device)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    cols = block_table.shape[1]
-    _nm._check(L.nm_tree_attention(
-        qp, ldq, tokens, q_heads, seqs, start, max_nodes, ctypes.byref(c), block_table.data_ptr(),
-        block_table.stride(0) if seqs > 1 else cols, cols, ctx, mask,
-        dim ** -0.5 if scale is None else scale, op, ldo, lp, _nm._ptr(workspace), ws_bytes,
-        _nm._stream(stream)), "nm_tree_attention")
-    return out, lse
+    return _calls().tree_attention(q, k_cache, v_cache, block_table, ctx_len, q_start, max_nodes,
+                                   tree_mask, k_scale, v_scale, scale, out, lse, workspace,
+                                   _given(stream))
 
 
 def nm_tree_verify(logits, tokens, parents, node_start, max_nodes: int, draft=None, accept=None,
@@ -250,35 +146,5 @@ def nm_tree_verify(logits, tokens, parents, node_start, max_nodes: int, draft=No
     are the random numbers; temperature 0 takes the largest logit and neither.
     Returns (path int32 [seqs][max_nodes], the accepted nodes and then -1;
     count int32 [seqs]; token int32 [seqs], the next one)."""
-    torch = _nm._torch()
-    _nm._need_cuda(logits, draft, race)
-    if logits.dtype not in (torch.float16, torch.float32) or logits.dim() != 2 or \
-            logits.stride(1) != 1 and logits.shape[1] != 1:
-        raise ValueError("logits must be float16 or float32 [nodes][vocab] with unit column stride")
-    n, vocab = logits.shape
-    seqs = node_start.numel() - 1
-    ids = _vector(tokens, torch.int32, n, "tokens")
-    par = _vector(parents, torch.int32, n, "parents")
-    start = _vector(node_start, torch.int32, seqs + 1, "node_start")
-    acc = _vector(accept, torch.float32, n, "accept")
-    for t, rows, what in ((draft, n, "draft"), (race, seqs, "race")):
-        if t is not None and (t.dtype != torch.float32 or t.shape != (rows, vocab) or
-                              t.stride(1) != 1 and vocab != 1):
-            raise ValueError(f"{what} must be float32 [{rows}][{vocab}] with unit column stride")
-    if path is None:
-        path = torch.empty((seqs, max_nodes), dtype=torch.int32, device=logits.device)
-    if count is None:
-        count = torch.empty(seqs, dtype=torch.int32, device=logits.device)
-    if token is None:
-        token = torch.empty(seqs, dtype=torch.int32, device=logits.device)
-
-    def ld(t):
-        return 0 if t is None else t.stride(0) if t.shape[0] > 1 else vocab
-
-    _nm._check(_nm.lib().nm_tree_verify(
-        logits.data_ptr(), 1 if logits.dtype == torch.float32 else 0, ld(logits), vocab,
-        _nm._ptr(draft), ld(draft), ids, par, start, n, seqs, max_nodes, acc, _nm._ptr(race),
-        ld(race), temperature, _vector(path, torch.int32, seqs * max_nodes, "path"),
-        _vector(count, torch.int32, seqs, "count"), _vector(token, torch.int32, seqs, "token"),
-        _nm._stream(stream)), "nm_tree_verify")
-    return path, count, token
+    return _calls().tree_verify(logits, tokens, parents, node_start, max_nodes, draft, accept, race,
+                                temperature, path, count, token, _given(stream))
