@@ -73,6 +73,14 @@ __device__ __forceinline__ void load8(const __half* row, int g, int n, bool vec,
 __device__ __forceinline__ float one(const float* row, int i) { return row[i]; }
 __device__ __forceinline__ float one(const __half* row, int i) { return __half2float(row[i]); }
 
+// Asks for elements 8 g .. of a row to come to L2 (a thread of every 128 bytes).
+template <typename T>
+__device__ __forceinline__ void prefetch8(const T* row, int g, int n) {
+  constexpr int kSame = 128 / (8 * sizeof(T));
+  if ((threadIdx.x & (kSame - 1)) == 0 && g * 8 < n)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(row + (int64_t)g * 8));
+}
+
 // A weight and its index; the larger weight wins, the lower index of equals.
 // Index -1: none yet; -2: a row that must not be used, wins over all.
 struct Best {
@@ -165,19 +173,36 @@ __global__ void __launch_bounds__(kThreads, 1) verify_kernel(VerifyParams p, int
     }
     const bool greedy = p.temperature == 0.0f, drafted = p.draft != nullptr;
     const float scale = greedy ? 1.0f : kLog2 / p.temperature;
+    // a row on its way to L2: a child's while its parent is still looked at
+    auto fetch = [&](int node) {
+      const T* r = static_cast<const T*>(p.logits) + (int64_t)(first + node) * p.ld_logits;
+#pragma unroll
+      for (int k = 0; k < kHeld; ++k) prefetch8(r, gt + k * stride, V);
+      if (drafted) {
+        const float* d = p.draft + (int64_t)(first + node) * p.ld_draft;
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k) prefetch8(d, gt + k * stride, V);
+      }
+    };
     for (;;) {
       if (writer && lane == 0) path[len] = cur;
       ++len;
       const T* row = static_cast<const T*>(p.logits) + (int64_t)(first + cur) * p.ld_logits;
       const float* qrow = drafted ? p.draft + (int64_t)(first + cur) * p.ld_draft : nullptr;
-      const uint64_t kids = (uint64_t)__ballot_sync(0xFFFFFFFFu, par[0] == cur) |
-                            (uint64_t)__ballot_sync(0xFFFFFFFFu, par[1] == cur) << 32;
       float x[kHeld][8], q[kHeld][8];
 #pragma unroll
       for (int k = 0; k < kHeld; ++k) load8(row, gt + k * stride, V, vec_logits, -INFINITY, x[k]);
       if (drafted) {
 #pragma unroll
         for (int k = 0; k < kHeld; ++k) load8(qrow, gt + k * stride, V, vec_draft, 0.0f, q[k]);
+      }
+      const uint64_t kids = (uint64_t)__ballot_sync(0xFFFFFFFFu, par[0] == cur) |
+                            (uint64_t)__ballot_sync(0xFFFFFFFFu, par[1] == cur) << 32;
+      if (kids) fetch(__ffsll(kids) - 1);
+      if (len == 1 && !greedy) {
+        const float* race = p.race + (int64_t)s * p.ld_race;
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k) prefetch8(race, gt + k * stride, V);
       }
       float kx[2] = {0.0f, 0.0f}, kq[2] = {1.0f, 1.0f};  // the children's logits and draft
       if (!greedy) {
@@ -190,12 +215,13 @@ __global__ void __launch_bounds__(kThreads, 1) verify_kernel(VerifyParams p, int
       }
       int next = -1;
       if (greedy) {
-        Best t{0.0f, -1};
+        Best t{-INFINITY, -1};
+        bool bad = false;
         auto look = [&](const float (&v)[8], int g) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            if (!(v[i] < INFINITY)) t.i = -2;  // NaN or +infinity
-            if (t.i != -2 && v[i] > -INFINITY) t = better(t, Best{v[i], g * 8 + i});
+            bad |= !(v[i] < INFINITY);  // NaN or +infinity
+            if (v[i] > t.w) t = Best{v[i], g * 8 + i};  // ascending: the lowest of equals
           }
         };
 #pragma unroll
@@ -204,6 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1) verify_kernel(VerifyParams p, int
           load8(row, g, V, vec_logits, -INFINITY, x[0]);
           look(x[0], g);
         }
+        if (bad) t.i = -2;
         t = best_of(t);
         if (t.i >= 0) {
           token = t.i;
@@ -234,7 +261,10 @@ __global__ void __launch_bounds__(kThreads, 1) verify_kernel(VerifyParams p, int
 #pragma unroll
       for (int k = 0; k < kHeld; ++k)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum += exp2_fast((x[k][i] - m0) * scale);
+        for (int i = 0; i < 8; ++i) {
+          x[k][i] = exp2_fast((x[k][i] - m0) * scale);
+          sum += x[k][i];
+        }
       for (int g = gt + kHeld * stride; g < groups; g += stride) {
         load8(row, g, V, vec_logits, -INFINITY, y);
 #pragma unroll
@@ -250,10 +280,11 @@ __global__ void __launch_bounds__(kThreads, 1) verify_kernel(VerifyParams p, int
       if (!(S > 0.0f && S < INFINITY)) break;  // a NaN among the logits
       const float inv = 1.0f / S;
       auto prob = [&](float v) { return exp2_fast((v - M) * scale) * inv; };
+      const float mine = m == -INFINITY ? 0.0f : exp2_fast((m - M) * scale) * inv;
 #pragma unroll
       for (int k = 0; k < kHeld; ++k)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[k][i] = prob(x[k][i]);
+        for (int i = 0; i < 8; ++i) x[k][i] *= mine;
 
       float a = 1.0f, b = 0.0f;  // w = relu(a p - b q)
       float left = 1.0f;         // without draft: the sum of p over what is not rejected
@@ -264,11 +295,13 @@ __global__ void __launch_bounds__(kThreads, 1) verify_kernel(VerifyParams p, int
         const float uc = __shfl_sync(0xFFFFFFFFu, c < 32 ? u[0] : u[1], from);
         const float pt = prob(__shfl_sync(0xFFFFFFFFu, c < 32 ? kx[0] : kx[1], from));
         const float qt = __shfl_sync(0xFFFFFFFFu, c < 32 ? kq[0] : kq[1], from);
+        const uint64_t later = rest & (rest - 1);
         if (drafted) {
           if (uc * qt < fmaxf(a * pt - b * qt, 0.0f)) {
             next = c;
             break;
           }
+          if (later) fetch(__ffsll(later) - 1);
           float z = 0.0f;
 #pragma unroll
           for (int k = 0; k < kHeld; ++k)
@@ -307,27 +340,35 @@ __global__ void __launch_bounds__(kThreads, 1) verify_kernel(VerifyParams p, int
         continue;
       }
       // no child: the race over w
-      Best t{0.0f, -1};
+      Best t{-1.0f, -1};
       const float* race = p.race + (int64_t)s * p.ld_race;
-      auto run = [&](const float (&pr)[8], const float (&qr)[8], int g) {
-        if (g >= groups) return;
-        load8(race, g, V, vec_race, 1.0f, y);
+      if (drafted) {
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[k][i] = fmaxf(a * x[k][i] - b * q[k][i], 0.0f);
+      }
+#pragma unroll
+      for (int k = 0; k < kHeld; ++k) load8(race, gt + k * stride, V, vec_race, 1.0f, q[k]);
+      auto run = [&](const float (&w)[8], const float (&e)[8], int g) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          float w = pr[i];
-          if (drafted) w = fmaxf(a * w - b * qr[i], 0.0f);
-          for (int k = 0; k < gone; ++k)
-            if (s_gone[k] == g * 8 + i) w = 0.0f;
-          if (g * 8 + i < V) t = better(t, Best{w > 0.0f ? w / y[i] : 0.0f, g * 8 + i});
+          float r = w[i] > 0.0f ? __fdividef(w[i], e[i]) : 0.0f;
+          for (int k = 0; k < gone; ++k) r = s_gone[k] == g * 8 + i ? 0.0f : r;
+          if (r > t.w && g * 8 + i < V) t = Best{r, g * 8 + i};  // ascending: the lowest of equals
         }
       };
 #pragma unroll
       for (int k = 0; k < kHeld; ++k) run(x[k], q[k], gt + k * stride);
       for (int g = gt + kHeld * stride; g < groups; g += stride) {
         load8(row, g, V, vec_logits, -INFINITY, x[0]);
-        if (drafted) load8(qrow, g, V, vec_draft, 0.0f, q[0]);
+        load8(race, g, V, vec_race, 1.0f, q[0]);
+        if (drafted) load8(qrow, g, V, vec_draft, 0.0f, y);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[0][i] = prob(x[0][i]);
+        for (int i = 0; i < 8; ++i) {
+          x[0][i] = prob(x[0][i]);
+          if (drafted) x[0][i] = fmaxf(a * x[0][i] - b * y[i], 0.0f);
+        }
         run(x[0], q[0], g);
       }
       token = best_of(t).i;
@@ -351,12 +392,14 @@ bool rows_aligned(const void* p, int64_t ld, size_t size) {
 }
 
 template <typename T>
-cudaError_t verify_one(const VerifyParams& p, cudaStream_t stream) {
+cudaError_t verify_one(const VerifyParams& p, int sms, cudaStream_t stream) {
   auto* k = verify_kernel<T>;
-  // the fewest blocks whose threads hold a row; a longer vocabulary's rest is
-  // read again for every sum
+  // The fewest blocks whose threads hold a row (a longer vocabulary's rest is
+  // read again for every sum); more of them, down to 8 elements a thread, while
+  // all sequences' blocks have an SM each: a sum's 2^x then take less of its time.
   int cl = 1;
   while (cl < kMaxCluster && cl * kThreads * kHeld * 8 < p.vocab) cl *= 2;
+  while (cl < kMaxCluster && cl * kThreads * 8 < p.vocab && (int64_t)p.seqs * cl * 2 <= sms) cl *= 2;
   if (cl > 8) {
     static int done[64];
     int dev = 0;
@@ -386,8 +429,8 @@ cudaError_t verify_one(const VerifyParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_verify(const VerifyParams& p, int logits_fp32, int, cudaStream_t stream) {
-  return logits_fp32 ? verify_one<float>(p, stream) : verify_one<__half>(p, stream);
+cudaError_t launch_verify(const VerifyParams& p, int logits_fp32, int sms, cudaStream_t stream) {
+  return logits_fp32 ? verify_one<float>(p, sms, stream) : verify_one<__half>(p, sms, stream);
 }
 
 }  // namespace nmk
