@@ -732,11 +732,12 @@ int nm_prefill_stall_selftest(const void* values, const uint32_t* masks, int64_t
 }
 
 int64_t nm_wait_timeouts(int reset) {
-  unsigned long long n = 0, m = 0;
-  if (read_wait_timeouts(&n, reset) != cudaSuccess ||
-      read_attend_wait_timeouts(&m, reset) != cudaSuccess)
+  unsigned long long a = 0, b = 0, c = 0;
+  if (read_wait_timeouts(&a, reset) != cudaSuccess ||
+      read_attend_wait_timeouts(&b, reset) != cudaSuccess ||
+      read_verify_wait_timeouts(&c, reset) != cudaSuccess)
     return -NM_ERR_CUDA;
-  return (int64_t)(n + m);
+  return (int64_t)(a + b + c);
 }
 
 int64_t nm_check_masks(const uint32_t* masks, int64_t rows, int64_t cols, void* stream) {

@@ -1010,13 +1010,7 @@ cudaError_t launch_attend_wide(const AttendParams& p, int head_dim, int type, in
 }
 
 cudaError_t read_attend_wait_timeouts(unsigned long long* count, int reset) {
-  cudaError_t e = cudaMemcpyFromSymbol(count, g_wait_timeouts, sizeof(*count));
-  if (e != cudaSuccess || !reset) return e;
-  const unsigned long long zero = 0;
-  const unsigned int clear = 0;
-  e = cudaMemcpyToSymbol(g_wait_timeouts, &zero, sizeof(zero));
-  if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_wait_abort, &clear, sizeof(clear));
-  return e;
+  return read_local_wait_timeouts(count, reset);
 }
 
 }  // namespace nmk

@@ -93,5 +93,6 @@ struct VerifyParams {
   int32_t *path, *count, *token;
 };
 cudaError_t launch_verify(const VerifyParams& p, int logits_fp32, int sms, cudaStream_t stream);
+cudaError_t read_verify_wait_timeouts(unsigned long long* count, int reset);
 
 }  // namespace nmk

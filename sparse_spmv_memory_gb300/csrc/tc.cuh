@@ -3,6 +3,7 @@
 // tcgen05 MMA descriptors.
 #pragma once
 
+#include <cuda_runtime.h>
 #include <stdint.h>
 
 namespace nmk {
@@ -327,6 +328,17 @@ __device__ __forceinline__ void sts_u64(uint32_t saddr, uint32_t lo, uint32_t hi
 
 __device__ __forceinline__ void sts_u32(uint32_t saddr, uint32_t v) {
   asm volatile("st.shared.u32 [%0], %1;" ::"r"(saddr), "r"(v) : "memory");
+}
+
+// This translation unit's count; `reset` clears it and the flag (host side).
+static inline cudaError_t read_local_wait_timeouts(unsigned long long* count, int reset) {
+  cudaError_t e = cudaMemcpyFromSymbol(count, g_wait_timeouts, sizeof(*count));
+  if (e != cudaSuccess || !reset) return e;
+  const unsigned long long zero = 0;
+  const unsigned int clear = 0;
+  e = cudaMemcpyToSymbol(g_wait_timeouts, &zero, sizeof(zero));
+  if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_wait_abort, &clear, sizeof(clear));
+  return e;
 }
 
 }  // namespace nmk
