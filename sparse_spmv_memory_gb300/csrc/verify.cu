@@ -52,6 +52,27 @@ __device__ __forceinline__ uint4 load16_if(const void* at, bool on) {
   return v;
 }
 
+// One element's bits if `on` (0 else), and its value: the bits are asked for
+// where a conversion would wait for them.
+__device__ __forceinline__ uint32_t bits_if(const float* at, bool on) {
+  uint32_t v;
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\tmov.u32 %0, 0;\n\t@p ld.global.nc.u32 %0, [%1];\n\t}"
+               : "=&r"(v)
+               : "l"(at), "r"((uint32_t)on));
+  return v;
+}
+__device__ __forceinline__ uint32_t bits_if(const __half* at, bool on) {
+  uint16_t v;
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\tmov.u16 %0, 0;\n\t@p ld.global.nc.u16 %0, [%1];\n\t}"
+               : "=&h"(v)
+               : "l"(at), "r"((uint32_t)on));
+  return v;
+}
+template <typename T>
+__device__ __forceinline__ float value_of(uint32_t bits) {
+  return sizeof(T) == 2 ? __half2float(__ushort_as_half((uint16_t)bits)) : __uint_as_float(bits);
+}
+
 __device__ __forceinline__ float one(const float* row, int i) { return row[i]; }
 __device__ __forceinline__ float one(const __half* row, int i) { return __half2float(row[i]); }
 
@@ -290,14 +311,12 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(VerifyParams p, int
         if (!greedy) prefetch_groups<HELD>(race, gt, stride, V);
       }
       // everything that this node needs is asked for before any of it is used
-      float kx[2] = {0.0f, 0.0f}, kq[2] = {1.0f, 1.0f};  // the children's logits and draft
-      if (!greedy) {
+      uint32_t kx[2], kq[2];  // the children's logits and draft
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-          if (par[k] == cur) {
-            kx[k] = one(row, id[k]);
-            if (drafted) kq[k] = qrow[id[k]];
-          }
+      for (int k = 0; k < 2; ++k) {
+        const bool on = par[k] == cur && !greedy;
+        kx[k] = bits_if(row + (on ? id[k] : 0), on);
+        kq[k] = drafted ? bits_if(qrow + (on ? id[k] : 0), on) : 0x3F800000u;  // 1
       }
       float x[HELD][8];
       if (drafted) stage_draft(qrow);
@@ -382,8 +401,8 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(VerifyParams p, int
         const int c = __ffsll(rest) - 1, from = c & 31;
         const int t = __shfl_sync(0xFFFFFFFFu, c < 32 ? id[0] : id[1], from);
         const float uc = __shfl_sync(0xFFFFFFFFu, c < 32 ? u[0] : u[1], from);
-        const float pt = prob(__shfl_sync(0xFFFFFFFFu, c < 32 ? kx[0] : kx[1], from));
-        const float qt = __shfl_sync(0xFFFFFFFFu, c < 32 ? kq[0] : kq[1], from);
+        const float pt = prob(value_of<T>(__shfl_sync(0xFFFFFFFFu, c < 32 ? kx[0] : kx[1], from)));
+        const float qt = __uint_as_float(__shfl_sync(0xFFFFFFFFu, c < 32 ? kq[0] : kq[1], from));
         const uint64_t later = rest & (rest - 1);
         if (drafted) {
           if (uc * qt < fmaxf(a * pt - b * qt, 0.0f)) {
