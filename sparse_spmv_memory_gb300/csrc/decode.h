@@ -46,7 +46,8 @@ struct ReadParams {
   int rows;
   __half *k_out, *v_out;  // either may be null
 };
-cudaError_t launch_cache_read(const ReadParams& p, int head_dim, int type, cudaStream_t stream);
+cudaError_t launch_cache_read(const ReadParams& p, int head_dim, int type, int sms,
+                              cudaStream_t stream);
 
 // ---- attention over the cache (attend.cu) -------------------------------------
 struct AttendParams {

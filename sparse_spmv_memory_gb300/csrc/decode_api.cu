@@ -159,11 +159,13 @@ int nm_cache_read(const nm_cache* cache, const int64_t* slots, int64_t rows, voi
   if (overlap(k_out, out, v_out, out) || overlaps_cache(cache, k_out, k_out ? out : 0) ||
       overlaps_cache(cache, v_out, v_out ? out : 0))
     return NM_ERR_ALIAS;
+  int sms;
+  if (sm_count(&sms) != NM_OK) return NM_ERR_CUDA;
   p.slots = slots;
   p.rows = (int)rows;
   p.k_out = static_cast<__half*>(k_out);
   p.v_out = static_cast<__half*>(v_out);
-  return status(launch_cache_read(p, cache->head_dim, cache->type,
+  return status(launch_cache_read(p, cache->head_dim, cache->type, sms,
                                   static_cast<cudaStream_t>(stream)));
 }
 

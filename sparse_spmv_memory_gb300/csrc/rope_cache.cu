@@ -8,6 +8,7 @@
 #include "decode.h"
 #include "device.cuh"
 #include "kernels.h"
+#include "widen.cuh"
 
 namespace nmk {
 namespace {
@@ -63,149 +64,180 @@ __device__ __forceinline__ void turn_of(float p, float f, float m, float& c, flo
   s = m * fmaf(c0, e, s0 * d);
 }
 
-// A block takes one token and a part of its heads: its first threads put the
-// token's cos and sin in shared memory, then groups of D / 8 lanes take a head
-// each, 8 elements a lane.
+// A warp takes one token and 32 / (D / 8) heads at a time, 8 elements a lane, up
+// to `turns` times.  Its lanes compute the token's cos and sin once, two angles
+// each, and hand them round by shuffles; a pair's other half comes from the lane
+// that has it.  No shared memory, no barrier, the next turn's load in flight.
 template <int D, int TYPE>
-__global__ void __launch_bounds__(256) append_kernel(AppendParams p, int heads_per_block) {
-  constexpr int L = D / 8;           // lanes of a head
-  __shared__ float sc[D / 2], ss[D / 2];
+__global__ void __launch_bounds__(128) append_kernel(AppendParams p, int turns) {
+  constexpr int L = D / 8, HEADS = 32 / L;  // lanes of a head, heads of a turn
   pdl_launch_dependents();
   pdl_wait_previous();
   const int t = blockIdx.x;
-  const int half = p.rot_dim >> 1;
-  const float pos = (float)p.positions[t];
-  for (int i = threadIdx.x; i < half; i += blockDim.x) turn_of(pos, p.inv_freq[i], p.mscale, sc[i], ss[i]);
-  __syncthreads();
-  const int H = p.c.kv_heads;
-  const int h_first = p.q_out ? 0 : p.q_heads;
+  const int lane = threadIdx.x & 31, in = lane % L;
+  const int half = p.rot_dim >> 1, H = p.c.kv_heads;
   const int h_end = p.q_heads + 2 * H;
-  const int lane = threadIdx.x % L, group = threadIdx.x / L;
+  const int step = HEADS * 4 * gridDim.y;  // heads of a turn of all the token's warps
+  const int hw = (p.q_out ? 0 : p.q_heads) + (blockIdx.y * 4 + (threadIdx.x >> 5)) * HEADS;
+  if (hw >= h_end) return;  // the whole warp
+  const __half* row = p.qkv + (int64_t)t * p.ldqkv;
+  auto load = [&](int h) { return h < h_end ? ld_keep_v4(row + h * D + in * 8) : make_uint4(0, 0, 0, 0); };
+  uint4 raw = load(hw + lane / L);
   const int64_t slot = p.slots[t];
   const bool keep = slot >= 0 && slot < (p.c.pages << p.c.page_shift);
-  const __half* row = p.qkv + (int64_t)t * p.ldqkv;
-  const int h0 = h_first + blockIdx.y * heads_per_block;
-  const int h1 = min(h0 + heads_per_block, h_end);
-  // every group runs the same number of turns: the shuffles need whole warps
-  for (int hb = h0; hb < h1; hb += 256 / L) {
-    const int h = hb + group;
-    const bool on = h < h1 && (h < p.q_heads || keep);
-    float x[8];
-    uint4 raw = make_uint4(0, 0, 0, 0);
-    if (on) raw = ld_keep_v4(row + (int64_t)h * D + lane * 8);
-    unpack8(raw, x);
-    if (on && h < p.q_heads + H) {
-      if (p.interleaved) {
+  const int64_t page = slot >> p.c.page_shift, off = slot & ((1 << p.c.page_shift) - 1);
+
+  // angles 2 lane and 2 lane + 1, and from them the lane's own
+  float ac[2] = {1.0f, 1.0f}, as[2] = {0.0f, 0.0f}, c[8], s[8];
+  const float pos = (float)p.positions[t];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int k = lane * 4 + i;
-          if (k < half) {
-            const float a = x[2 * i], b = x[2 * i + 1];
-            x[2 * i] = a * sc[k] - b * ss[k];
-            x[2 * i + 1] = b * sc[k] + a * ss[k];
-          }
+  for (int k = 0; k < 2; ++k)
+    if (2 * lane + k < half) turn_of(pos, p.inv_freq[2 * lane + k], p.mscale, ac[k], as[k]);
+  const bool vec = (half & 7) == 0, turned = in * 8 < p.rot_dim;
+  const bool upper = in * 8 >= half;       // vec: the second of the pairs
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    // the angle of element i (interleaved: of elements 2i, 2i + 1 for i < 4)
+    const int e = in * 8 + i;
+    const int a = p.interleaved ? in * 4 + (i & 3) : e < half ? e : e - half;
+    const float c0 = __shfl_sync(0xFFFFFFFFu, ac[0], (a >> 1) & 31), c1 = __shfl_sync(0xFFFFFFFFu, ac[1], (a >> 1) & 31);
+    const float s0 = __shfl_sync(0xFFFFFFFFu, as[0], (a >> 1) & 31), s1 = __shfl_sync(0xFFFFFFFFu, as[1], (a >> 1) & 31);
+    c[i] = a & 1 ? c1 : c0;
+    s[i] = a & 1 ? s1 : s0;
+    if (!p.interleaved && e < half) s[i] = -s[i];  // a cos - b sin, b cos + a sin
+  }
+  const int other = lane - in + (upper ? in - (half >> 3) : in + (half >> 3));
+
+  for (int k = 0; k < turns; ++k) {
+    const int hk = hw + k * step;
+    if (hk >= h_end) break;  // the whole warp
+    const int h = hk + lane / L;
+    const uint4 now = raw;
+    if (k + 1 < turns) raw = load(h + step);
+    float x[8];
+    unpack8(now, x);
+    if (hk < p.q_heads + H && half > 0) {  // some of the warp's heads are rotated
+      const bool rot = h < p.q_heads + H;
+      if (p.interleaved) {
+        if (rot) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (in * 4 + i < half) {
+              const float a = x[2 * i], b = x[2 * i + 1];
+              x[2 * i] = a * c[i] - b * s[i];
+              x[2 * i + 1] = b * c[i] + a * s[i];
+            }
         }
-      } else if (lane * 8 < p.rot_dim) {
+      } else {
         float y[8];
-        if ((half & 7) == 0) {  // the partners are 8 neighbours too
-          const int other = lane * 8 < half ? lane * 8 + half : lane * 8 - half;
-          unpack8(ld_keep_v4(row + (int64_t)h * D + other), y);
+        if (vec) {
+          uint4 q;
+          q.x = __shfl_sync(0xFFFFFFFFu, now.x, other & 31);
+          q.y = __shfl_sync(0xFFFFFFFFu, now.y, other & 31);
+          q.z = __shfl_sync(0xFFFFFFFFu, now.z, other & 31);
+          q.w = __shfl_sync(0xFFFFFFFFu, now.w, other & 31);
+          unpack8(q, y);
         } else {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const int e = lane * 8 + i;
-            y[i] = e < p.rot_dim
-                       ? __half2float(row[(int64_t)h * D + (e < half ? e + half : e - half)])
-                       : 0.0f;
+            const int e = in * 8 + i;
+            y[i] = rot && e < p.rot_dim ? __half2float(row[h * D + (e < half ? e + half : e - half)]) : 0.0f;
           }
         }
+        if (rot && turned) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int e = lane * 8 + i;
-          if (e < half)
-            x[i] = x[i] * sc[e] - y[i] * ss[e];
-          else if (e < p.rot_dim)
-            x[i] = x[i] * sc[e - half] + y[i] * ss[e - half];
+          for (int i = 0; i < 8; ++i)
+            if (in * 8 + i < p.rot_dim) x[i] = x[i] * c[i] + y[i] * s[i];
         }
       }
     }
     // largest magnitude of the row, by its bits: a NaN ranks above infinity
     uint32_t top = 0;
-    if (TYPE != kCacheFp16) {
+    if (TYPE != kCacheFp16 && hk + HEADS > p.q_heads) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
 #pragma unroll
       for (int o = L / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
     }
-    if (!on) continue;
     if (h < p.q_heads) {
-      *reinterpret_cast<uint4*>(p.q_out + (int64_t)t * p.ldq + (int64_t)h * D + lane * 8) = pack8(x);
-      continue;
-    }
-    const bool is_v = h >= p.q_heads + H;
-    const int kh = h - p.q_heads - (is_v ? H : 0);
-    const int64_t page = slot >> p.c.page_shift;
-    const int64_t in_page = ((int64_t)kh << p.c.page_shift) + (slot & ((1 << p.c.page_shift) - 1));
-    const int64_t at = page * p.c.page_stride + in_page * D + lane * 8;
-    uint8_t* dst = is_v ? p.c.v : p.c.k;
-    if (TYPE == kCacheFp16) {
-      *reinterpret_cast<uint4*>(dst + at * 2) = pack8(x);
-    } else {
-      const float scale = top >= 0x7F800000u
-                              ? __uint_as_float(0x7FC00000u)
-                              : __fdiv_rn(__uint_as_float(top), TYPE == kCacheE4m3 ? 448.0f : 127.0f);
-      *reinterpret_cast<uint2*>(dst + at) = encode8<TYPE>(x, scale);
-      if (lane == 0) (is_v ? p.c.v_scale : p.c.k_scale)[page * p.c.scale_page_stride + in_page] = scale;
-    }
-  }
-}
-
-template <int TYPE>
-__device__ __forceinline__ void decode8(const uint8_t* at, float scale, float (&x)[8]) {
-  if (TYPE == kCacheFp16) {
-    unpack8(ld_stream_v4(at), x);
-    return;
-  }
-  const uint2 u = *reinterpret_cast<const uint2*>(at);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t b = ((i < 4 ? u.x : u.y) >> (8 * (i & 3))) & 0xFFu;
-    if (TYPE == kCacheE4m3) {
-      const __half_raw h = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)b, __NV_E4M3);
-      x[i] = __half2float(__half(h)) * scale;
-    } else {
-      x[i] = (float)(int8_t)b * scale;
+      *reinterpret_cast<uint4*>(p.q_out + (int64_t)t * p.ldq + h * D + in * 8) = pack8(x);
+    } else if (h < h_end && keep) {
+      const bool is_v = h >= p.q_heads + H;
+      const int kh = h - p.q_heads - (is_v ? H : 0);
+      const int64_t in_page = ((int64_t)kh << p.c.page_shift) + off;
+      const int64_t at = page * p.c.page_stride + in_page * D + in * 8;
+      uint8_t* dst = is_v ? p.c.v : p.c.k;
+      if (TYPE == kCacheFp16) {
+        *reinterpret_cast<uint4*>(dst + at * 2) = pack8(x);
+      } else {
+        const float scale = top >= 0x7F800000u
+                                ? __uint_as_float(0x7FC00000u)
+                                : __fdiv_rn(__uint_as_float(top), TYPE == kCacheE4m3 ? 448.0f : 127.0f);
+        *reinterpret_cast<uint2*>(dst + at) = encode8<TYPE>(x, scale);
+        if (in == 0) (is_v ? p.c.v_scale : p.c.k_scale)[page * p.c.scale_page_stride + in_page] = scale;
+      }
     }
   }
 }
 
-// A thread takes 8 elements of a row.
+// A warp takes a slot: its rows are one 16-byte piece a lane, 32 lanes at a time
+// over the heads, K and V side by side, and both outputs are contiguous.
 template <int D, int TYPE>
 __global__ void __launch_bounds__(256) read_kernel(ReadParams p) {
-  constexpr int L = D / 8;
+  constexpr bool F16 = TYPE == kCacheFp16;
+  constexpr int E = F16 ? 8 : 16;              // elements of a piece
+  constexpr int L = D / E, HEADS = 32 / L;     // lanes of a row, heads at a time
   pdl_launch_dependents();
   pdl_wait_previous();
-  const int64_t n = (int64_t)p.rows * p.c.kv_heads * L;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= n) return;
-  const int lane = (int)(i % L);
-  const int64_t rh = i / L;
-  const int h = (int)(rh % p.c.kv_heads);
-  const int64_t slot = p.slots[rh / p.c.kv_heads];
-  const bool is_v = blockIdx.y != 0;
-  __half* out = is_v ? p.v_out : p.k_out;
-  if (!out) return;
-  float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  if (slot >= 0 && slot < (p.c.pages << p.c.page_shift)) {
-    const int64_t page = slot >> p.c.page_shift;
-    const int64_t in_page = ((int64_t)h << p.c.page_shift) + (slot & ((1 << p.c.page_shift) - 1));
-    const float scale = TYPE == kCacheFp16 ? 1.0f
-                                           : (is_v ? p.c.v_scale : p.c.k_scale)
-                                                 [page * p.c.scale_page_stride + in_page];
-    const int64_t at = page * p.c.page_stride + in_page * D + lane * 8;
-    decode8<TYPE>((is_v ? p.c.v : p.c.k) + at * (TYPE == kCacheFp16 ? 2 : 1), scale, x);
+  const int lane = threadIdx.x & 31, piece = lane % L;
+  const int H = p.c.kv_heads;
+  const int warps = gridDim.x * 8;
+  for (int64_t r = blockIdx.x * 8 + (threadIdx.x >> 5); r < p.rows; r += warps) {
+    const int64_t slot = p.slots[r];
+    const bool there = slot >= 0 && slot < (p.c.pages << p.c.page_shift);
+    const int64_t page = slot >> p.c.page_shift, off = slot & ((1 << p.c.page_shift) - 1);
+#pragma unroll 2
+    for (int h = lane / L; h < H; h += HEADS) {
+      const int64_t in_page = ((int64_t)h << p.c.page_shift) + off;
+      const int64_t at = page * p.c.page_stride + in_page * D + piece * E;
+      const int64_t sat = page * p.c.scale_page_stride + in_page;
+      uint4 raw[2];
+      float scale[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        raw[k] = make_uint4(0, 0, 0, 0);
+        scale[k] = 0.0f;
+        if (there) {
+          raw[k] = ld_stream_v4((k ? p.c.v : p.c.k) + at * (F16 ? 2 : 1));
+          if (!F16) scale[k] = (k ? p.c.v_scale : p.c.k_scale)[sat];
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        __half* out = k ? p.v_out : p.k_out;
+        if (!out) continue;
+        uint4* dst = reinterpret_cast<uint4*>(out + (r * H + h) * D + piece * E);
+        if (F16) {
+          __stcs(dst, raw[k]);
+        } else {
+          const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+          uint32_t o[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t lo, hi;
+            widen4<F16 ? kCacheE4m3 : TYPE>(w[i], lo, hi);
+            const float2 a = half2_bits_to_float2(lo), b = half2_bits_to_float2(hi);
+            const __half2 x = __floats2half2_rn(a.x * scale[k], a.y * scale[k]);
+            const __half2 y = __floats2half2_rn(b.x * scale[k], b.y * scale[k]);
+            o[2 * i] = *reinterpret_cast<const uint32_t*>(&x);
+            o[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&y);
+          }
+          __stcs(dst, make_uint4(o[0], o[1], o[2], o[3]));
+          __stcs(dst + 1, make_uint4(o[4], o[5], o[6], o[7]));
+        }
+      }
+    }
   }
-  *reinterpret_cast<uint4*>(out + i * 8) = pack8(x);
 }
 
 }  // namespace
@@ -213,22 +245,22 @@ __global__ void __launch_bounds__(256) read_kernel(ReadParams p) {
 template <int D, int TYPE>
 static cudaError_t append_one(const AppendParams& p, int sms, cudaStream_t stream) {
   const int heads = (p.q_out ? p.q_heads : 0) + 2 * p.c.kv_heads;
-  constexpr int kPer = 256 / (D / 8);  // heads a block takes at a time
-  // Few tokens: a block per turn of heads; many: a block walks a token's heads.
-  const int turns = (heads + kPer - 1) / kPer;
-  int parts = turns;
-  while (parts > 1 && (int64_t)p.tokens * parts > 8 * sms) parts = (parts + 1) / 2;
-  const int per = (turns + parts - 1) / parts * kPer;
+  constexpr int kPer = 32 / (D / 8) * 4;  // heads of a block's turn
+  // As many turns as leave every SM 24 warps: the angles are worth more of them,
+  // a single token's latency one.
+  const int all = (heads + kPer - 1) / kPer;
+  int64_t turns = (int64_t)p.tokens * all / (6 * sms);
+  turns = turns < 1 ? 1 : turns > all ? all : turns;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)p.tokens, (unsigned)((heads + per - 1) / per));
-  cfg.blockDim = dim3(256);
+  cfg.gridDim = dim3((unsigned)p.tokens, (unsigned)((all + turns - 1) / turns));
+  cfg.blockDim = dim3(128);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, append_kernel<D, TYPE>, p, per);
+  return cudaLaunchKernelEx(&cfg, append_kernel<D, TYPE>, p, (int)turns);
 }
 
 cudaError_t launch_rope_append(const AppendParams& p, int head_dim, int type, int sms,
@@ -244,31 +276,23 @@ cudaError_t launch_rope_append(const AppendParams& p, int head_dim, int type, in
 }
 
 template <int D, int TYPE>
-static cudaError_t read_one(const ReadParams& p, cudaStream_t stream) {
-  const int64_t n = (int64_t)p.rows * p.c.kv_heads * (D / 8);
-  const int64_t blocks = (n + 255) / 256;
-  if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)blocks, 2);
-  cfg.blockDim = dim3(256);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, read_kernel<D, TYPE>, p);
+static cudaError_t read_one(const ReadParams& p, int sms, cudaStream_t stream) {
+  // eight blocks' warps fill an SM; a long read's warps take several rows each
+  const int64_t blocks = ((int64_t)p.rows + 7) / 8;
+  return launch_kernel(read_kernel<D, TYPE>, (int)(blocks < 8 * sms ? blocks : 8 * sms), 256, 0, stream,
+                       kFlagPdl, p);
 }
 
-cudaError_t launch_cache_read(const ReadParams& p, int head_dim, int type, cudaStream_t stream) {
+cudaError_t launch_cache_read(const ReadParams& p, int head_dim, int type, int sms,
+                              cudaStream_t stream) {
   if (head_dim == 128) {
-    if (type == kCacheFp16) return read_one<128, kCacheFp16>(p, stream);
-    if (type == kCacheE4m3) return read_one<128, kCacheE4m3>(p, stream);
-    return read_one<128, kCacheInt8>(p, stream);
+    if (type == kCacheFp16) return read_one<128, kCacheFp16>(p, sms, stream);
+    if (type == kCacheE4m3) return read_one<128, kCacheE4m3>(p, sms, stream);
+    return read_one<128, kCacheInt8>(p, sms, stream);
   }
-  if (type == kCacheFp16) return read_one<64, kCacheFp16>(p, stream);
-  if (type == kCacheE4m3) return read_one<64, kCacheE4m3>(p, stream);
-  return read_one<64, kCacheInt8>(p, stream);
+  if (type == kCacheFp16) return read_one<64, kCacheFp16>(p, sms, stream);
+  if (type == kCacheE4m3) return read_one<64, kCacheE4m3>(p, sms, stream);
+  return read_one<64, kCacheInt8>(p, sms, stream);
 }
 
 }  // namespace nmk
