@@ -456,43 +456,42 @@ __global__ void __launch_bounds__(NW * 32, 1) attend_narrow_kernel(AttendParams 
     const int parts = (int)(b1 - b0 + 1);
     if (!last_of_item(counters + w.item, parts)) continue;
     float* factor = so;  // [parts][ROWS]
+    auto part = [&](int y) {
+      return slots + part_slot(b0 + y, sched.per, w.start) * attend_slot_floats(ROWS, D);
+    };
     for (int r = threadIdx.x; r < rows; r += NTH) {
-      float M = -INFINITY, tot = 0.0f;
-      for (int y = 0; y < parts; ++y) {
-        const float* sp = slots + part_slot(b0 + y, sched.per, w.start) * attend_slot_floats(ROWS, D);
-        const float m1 = __ldcg(sp + (size_t)ROWS * D + r);
-        factor[y * ROWS + r] = m1;
-        M = fmaxf(M, m1);
-      }
-      const float base = M == -INFINITY ? 0.0f : M;
-      for (int y = 0; y < parts; ++y) {
-        const float* sp = slots + part_slot(b0 + y, sched.per, w.start) * attend_slot_floats(ROWS, D);
-        const float f = exp2_fast(factor[y * ROWS + r] - base);
-        factor[y * ROWS + r] = f;
-        tot += __ldcg(sp + (size_t)ROWS * D + ROWS + r) * f;
-      }
-      row_l[r] = tot == 0.0f ? 0.0f : 1.0f / tot;
+      const float2 ml = join_ml(parts, ROWS, [&](int y) { return part(y) + ROWS * D + r; });
+      row_m[r] = ml.x == -INFINITY ? 0.0f : ml.x;
+      row_l[r] = ml.y == 0.0f ? 0.0f : 1.0f / ml.y;
       const int rr = w.rt * ROWS + r;
       if (p.lse)
         p.lse[(int64_t)(si.first + heads.node(rr)) * p.q_heads + w.h * G + heads.head(rr)] =
-            tot == 0.0f ? -INFINITY : (M + log2f(tot)) * kLn2;
+            ml.y == 0.0f ? -INFINITY : (ml.x + log2f(ml.y)) * kLn2;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < parts * rows; i += NTH) {
+      const int y = i / rows, r = i % rows;
+      factor[y * ROWS + r] = exp2_fast(__ldcg(part(y) + ROWS * D + r) - row_m[r]) * row_l[r];
     }
     __syncthreads();
     for (int i = threadIdx.x; i < rows * (D / 4); i += NTH) {
       const int r = i / (D / 4), d = i % (D / 4) * 4;
       float4 x = make_float4(0, 0, 0, 0);
-#pragma unroll 8
-      for (int y = 0; y < parts; ++y) {
-        const float* sp = slots + part_slot(b0 + y, sched.per, w.start) * attend_slot_floats(ROWS, D);
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(sp + (size_t)r * D + d));
-        const float f = factor[y * ROWS + r];
-        x.x += v.x * f, x.y += v.y * f, x.z += v.z * f, x.w += v.w * f;
+      for (int y0 = 0; y0 < parts; y0 += 8) {
+        float4 v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          v[j] = __ldcg(reinterpret_cast<const float4*>(part(min(y0 + j, parts - 1)) + (size_t)r * D + d));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float f = y0 + j < parts ? factor[(y0 + j) * ROWS + r] : 0.0f;
+          x.x += v[j].x * f, x.y += v[j].y * f, x.z += v[j].z * f, x.w += v[j].w * f;
+        }
       }
-      const float inv = row_l[r];
       const int rr = w.rt * ROWS + r;
       *reinterpret_cast<uint2*>(p.out + (int64_t)(si.first + heads.node(rr)) * p.ldo +
                                 (w.h * G + heads.head(rr)) * D + d) =
-          make_uint2(pack_half2(x.x * inv, x.y * inv), pack_half2(x.z * inv, x.w * inv));
+          make_uint2(pack_half2(x.x, x.y), pack_half2(x.z, x.w));
     }
   }
 }

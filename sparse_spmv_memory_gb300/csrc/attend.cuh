@@ -199,6 +199,32 @@ __device__ __forceinline__ int64_t part_slot(int64_t b, int64_t per, int64_t ite
   return b * 2 + (b * per >= item_start ? 0 : 1);
 }
 
+// The maximum and the sum of weights of one row over an item's parts, `at(y)` its
+// part y's maximum and `lo` floats on its sum: eight parts' loads are issued
+// before the first is used (a plain loop waits for each).
+template <typename At>
+__device__ __forceinline__ float2 join_ml(int parts, int lo, At at) {
+  float M = -INFINITY, tot = 0.0f;
+  for (int y0 = 0; y0 < parts; y0 += 8) {
+    float m[8], l[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float* f = at(min(y0 + j, parts - 1));
+      m[j] = __ldcg(f);
+      l[j] = __ldcg(f + lo);
+    }
+    float m2 = M;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m2 = fmaxf(m2, m[j]);
+    const float o = m2 == -INFINITY ? 0.0f : m2;
+    tot *= exp2_fast(M - o);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) tot += y0 + j < parts ? l[j] * exp2_fast(m[j] - o) : 0.0f;
+    M = m2;
+  }
+  return make_float2(M, tot);
+}
+
 // Where a head's rows of positions g .. g + 7 (g a multiple of 8) begin: pages
 // hold whole groups of 8.  Negative: absent.
 struct RowAt {

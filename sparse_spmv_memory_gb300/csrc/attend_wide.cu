@@ -80,6 +80,9 @@ struct Wide {
 // TMEM columns.
 constexpr uint32_t kS0 = 0, kS1 = 128, kO0 = 256, kO1 = 384, kTmemCols = 512;
 
+// Workspace: 16 bytes for each item (where its parts are), then two slots a block.
+__host__ __device__ constexpr size_t join_head_bytes(int64_t items) { return (size_t)items * 16; }
+
 __device__ __forceinline__ uint32_t half2_of(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -131,7 +134,7 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
   using Sched = Schedule<IROWS, kKeys, W::THREADS>;
   extern __shared__ uint8_t raw_smem[];
   __shared__ uint64_t bar_mem[2 * W::NS + 8 + 2 * RS];
-  __shared__ uint32_t tmem_slot, s_last;
+  __shared__ uint32_t tmem_slot;
   __shared__ uint32_t there_of[kMeta];
   __shared__ uint32_t bad_of[kBad][2];
   __shared__ float2 s_ml[2][kRows];
@@ -570,9 +573,9 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
       if (lane == 0) mbar_arrive(soft);
       return wait_warp(soft, phase++ & 1);
     };
-    int* counters = reinterpret_cast<int*>(p.workspace);
+    int4* heads_of_items = reinterpret_cast<int4*>(p.workspace);
     float* slots = reinterpret_cast<float*>(
-        p.workspace + attend_counter_bytes((int64_t)p.seqs * p.c.kv_heads * sched.rt_max));
+        p.workspace + join_head_bytes((int64_t)p.seqs * p.c.kv_heads * sched.rt_max));
     bool ok = true;
     Span w;
     SeqInfo si;
@@ -850,80 +853,14 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
         f[srow] = M;
         f[IROWS + srow] = tot;
       }
+      // attend_join_kernel adds an item's parts: where they are
+      if (w.u0 == 0 && threadIdx.x == 0) {
+        const int64_t b0 = sched.block_of(w.start), b1 = sched.block_of(w.start + w.nu - 1);
+        heads_of_items[w.item] = make_int4((int)part_slot(b0, sched.per, w.start), (int)b0, (int)(b1 - b0) + 1, 0);
+      }
       ++item_no;
       tc_fence_before_sync();
-      if (whole) {
-        if (!PAIR) ok = soft_sync();  // nobody reads the other stream's sums any more
-        continue;
-      }
-      // ---- the blocks join: the last one to store its part adds all of them
-      const int64_t b0 = sched.block_of(w.start), b1 = sched.block_of(w.start + w.nu - 1);
-      __threadfence();
-      ok = soft_sync();
-      if (!ok) break;
-      if (threadIdx.x == 0) {
-        const bool last = atomicAdd(counters + w.item, 1) == (int)(b1 - b0);
-        if (last) counters[w.item] = 0;  // ready for the next call
-        __threadfence();
-        s_last = last;
-      }
-      ok = soft_sync();
-      if (!ok) break;
-      if (!*(volatile uint32_t*)&s_last) continue;
-      __threadfence();
-      float* part0 = slots + part_slot(b0, sched.per, w.start) * attend_slot_floats(IROWS, D);
-      auto part = [&](int y) {  // after the first, an item's part begins its block's range
-        return y == 0 ? part0 : slots + (size_t)(b0 + y) * 2 * attend_slot_floats(IROWS, D);
-      };
-      const int parts = (int)(b1 - b0) + 1;
-      if (mine && (PAIR || b == 0)) {
-        float M2 = -INFINITY, tot2 = 0.0f;
-#pragma unroll 8
-        for (int y = 0; y < parts; ++y) {
-          const float* f = part(y) + IROWS * D;
-          const float m1 = __ldcg(f + srow), l1 = __ldcg(f + IROWS + srow), m2 = fmaxf(M2, m1);
-          const float o = m2 == -INFINITY ? 0.0f : m2;
-          tot2 = tot2 * exp2_fast(M2 - o) + l1 * exp2_fast(m1 - o);
-          M2 = m2;
-        }
-        s_ml[PAIR ? b : 0][row] =
-            make_float2(M2 == -INFINITY ? 0.0f : M2, tot2 == 0.0f ? 0.0f : 1.0f / tot2);
-        if (p.lse)
-          p.lse[(int64_t)(si.first + node) * p.q_heads + hq] =
-              tot2 == 0.0f ? -INFINITY : (M2 + log2f(tot2)) * kLn2;
-      }
-      ok = soft_sync();
-      if (!ok) break;
-      // a warp takes 32 rows and 32 columns at a time: many loads in flight
-      const int all = min(IROWS, si.n * G - w.rt * IROWS), blocks32 = (all + 31) / 32;
-      for (int e = warp; e < blocks32 * (D / 32); e += kSoftWarps) {
-        const int r = e % blocks32 * 32 + lane, d4 = e / blocks32 * 8;
-        if (r < all) {
-          const float2 mi = s_ml[r / kRows][r % kRows];
-          float4 x[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) x[k] = make_float4(0, 0, 0, 0);
-#pragma unroll 2
-          for (int y = 0; y < parts; ++y) {
-            const float* f = part(y);
-            const float g = exp2_fast(__ldcg(f + IROWS * D + r) - mi.x) * mi.y;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(f) + (d4 + k) * IROWS + r);
-              x[k].x += v.x * g, x[k].y += v.y * g, x[k].z += v.z * g, x[k].w += v.w * g;
-            }
-          }
-          const int r2 = w.rt * IROWS + r;
-          __half* dst = p.out + (int64_t)(si.first + heads.node(r2)) * p.ldo +
-                        (w.h * G + heads.head(r2)) * D + 4 * d4;
-#pragma unroll
-          for (int k = 0; k < 8; k += 2)
-            *reinterpret_cast<uint4*>(dst + 4 * k) =
-                make_uint4(half2_of(x[k].x, x[k].y), half2_of(x[k].z, x[k].w),
-                           half2_of(x[k + 1].x, x[k + 1].y), half2_of(x[k + 1].z, x[k + 1].w));
-        }
-      }
-      ok = soft_sync();  // s_ml is free
+      if (!PAIR) ok = soft_sync();  // nobody reads the other stream's sums any more
     }
   }
 
@@ -947,6 +884,75 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
     tc_fence_after_sync();
     tmem_dealloc(tmem, kTmemCols);
   }
+}
+
+// Adds the parts of the items that several blocks had: a block takes 32 rows of
+// an item, a thread a row and 4 or 8 columns (warps side by side), every part's
+// loads in flight together.  A launch of its own: one block that added its item
+// in the kernel above had 10 to 40 us of it, a whole grid has 2 to 3.
+template <int D, int IROWS>
+__global__ void __launch_bounds__(256) attend_join_kernel(AttendParams p, int rt_max, int blocks) {
+  pdl_launch_dependents();
+  pdl_wait_previous();
+  const int G = p.q_heads / p.c.kv_heads;
+  const int item = blockIdx.x, s = item / (p.c.kv_heads * rt_max), h = item / rt_max % p.c.kv_heads,
+            rt = item % rt_max;
+  const SeqInfo si = seq_info(p, s);
+  const int rows = min(IROWS, si.n * G - rt * IROWS);
+  const int r = blockIdx.y * 32 + (threadIdx.x & 31), warp = threadIdx.x >> 5;
+  if ((int)blockIdx.y * 32 >= rows) return;
+  const int4 head = reinterpret_cast<const int4*>(p.workspace)[item];
+  const int parts = head.z;
+  // (an item without an entry, after a wait that gave up, reads in bounds)
+  if (parts < 2 || parts > blocks || (uint32_t)head.x >= 2u * blocks || head.y < 0 || head.y > blocks - parts ||
+      r >= rows)
+    return;
+  const float* slots = reinterpret_cast<const float*>(
+      p.workspace + join_head_bytes((int64_t)p.seqs * p.c.kv_heads * rt_max));
+  // after the first, an item's part begins its block's range
+  auto part = [&](int y) {
+    return slots + (size_t)(y == 0 ? head.x : (head.y + y) * 2) * attend_slot_floats(IROWS, D);
+  };
+  constexpr int C = D / 32, B = 16 / C;  // 16-byte columns of a thread, parts at a time
+  float4 x[C], v[B][C];
+  float pm[B];
+  auto fetch = [&](int y0) {
+#pragma unroll
+    for (int j = 0; j < B; ++j) {
+      const float* f = part(min(y0 + j, parts - 1));
+      pm[j] = __ldcg(f + IROWS * D + r);
+#pragma unroll
+      for (int k = 0; k < C; ++k)
+        v[j][k] = __ldcg(reinterpret_cast<const float4*>(f) + (warp * C + k) * IROWS + r);
+    }
+  };
+  fetch(0);
+  const float2 ml = join_ml(parts, IROWS, [&](int y) { return part(y) + IROWS * D + r; });
+  const float M = ml.x, tot = ml.y, off = M == -INFINITY ? 0.0f : M;
+#pragma unroll
+  for (int k = 0; k < C; ++k) x[k] = make_float4(0, 0, 0, 0);
+  for (int y0 = 0; y0 < parts; y0 += B) {
+    if (y0 > 0) fetch(y0);
+#pragma unroll
+    for (int j = 0; j < B; ++j) {
+      if (y0 + j >= parts) break;
+      const float g = exp2_fast(pm[j] - off);
+#pragma unroll
+      for (int k = 0; k < C; ++k)
+        x[k].x += v[j][k].x * g, x[k].y += v[j][k].y * g, x[k].z += v[j][k].z * g, x[k].w += v[j][k].w * g;
+    }
+  }
+  const float inv = tot == 0.0f ? 0.0f : 1.0f / tot;
+  const Heads heads(G);
+  const int rr = rt * IROWS + r, node = heads.node(rr), hq = h * G + heads.head(rr);
+  __half* dst = p.out + (int64_t)(si.first + node) * p.ldo + hq * D + warp * C * 4;
+#pragma unroll
+  for (int k = 0; k < C; k += 2)
+    *reinterpret_cast<uint4*>(dst + 4 * k) =
+        make_uint4(half2_of(x[k].x * inv, x[k].y * inv), half2_of(x[k].z * inv, x[k].w * inv),
+                   half2_of(x[k + 1].x * inv, x[k + 1].y * inv), half2_of(x[k + 1].z * inv, x[k + 1].w * inv));
+  if (warp == 0 && p.lse)
+    p.lse[(int64_t)(si.first + node) * p.q_heads + hq] = tot == 0.0f ? -INFINITY : (M + log2f(tot)) * kLn2;
 }
 
 // A cache's pages as {head_dim, kv_heads * page_size rows, pages}, in boxes of
@@ -980,7 +986,21 @@ cudaError_t wide_one(const AttendParams& p, int sms, cudaStream_t stream) {
     memset(&tk, 0, sizeof(tk));
     memset(&tv, 0, sizeof(tv));
   }
-  return launch_kernel(k, sms, W::THREADS, W::SMEM, stream, kFlagPdl, p, tk, tv);
+  e = launch_kernel(k, sms, W::THREADS, W::SMEM, stream, kFlagPdl, p, tk, tv);
+  if (e != cudaSuccess) return e;
+  constexpr int IROWS = W::QT * kRows;
+  const int rt_max = (p.max_nodes * (p.q_heads / p.c.kv_heads) + IROWS - 1) / IROWS;
+  cudaLaunchConfig_t cfg = {};
+  const int rows = p.max_nodes * (p.q_heads / p.c.kv_heads);
+  cfg.gridDim = dim3((unsigned)(p.seqs * p.c.kv_heads * rt_max), (unsigned)((rows < IROWS ? rows : IROWS) + 31) / 32);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attend_join_kernel<D, IROWS>, p, rt_max, sms);
 }
 
 template <int D, int TYPE>
@@ -993,7 +1013,7 @@ cudaError_t wide_rows(const AttendParams& p, int sms, cudaStream_t stream) {
 
 size_t attend_wide_workspace_bytes(int64_t seqs, int kv_heads, int rows, int head_dim, int sms) {
   const int tile = rows > kRows ? 2 * kRows : kRows;
-  return attend_counter_bytes(seqs * kv_heads * ((rows + tile - 1) / tile)) +
+  return join_head_bytes(seqs * kv_heads * ((rows + tile - 1) / tile)) +
          (size_t)sms * 2 * attend_slot_floats(tile, head_dim) * sizeof(float);
 }
 
