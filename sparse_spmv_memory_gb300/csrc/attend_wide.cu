@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
       mbar_init(pfull(b), 4);
       mbar_init(ofull(b), 1);
     }
-    mbar_init(qfull, kSoftWarps);
+    mbar_init(qfull, PAIR ? kSoftWarps : kSoftWarps / 2);
     mbar_init(soft, kSoftWarps);
     fence_mbar_init();
     if (F16) {
@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
   const uint32_t tmem = *(volatile uint32_t*)&tmem_slot;
   const int G = p.q_heads / p.c.kv_heads;
   const Heads heads(G);
-  const float cs = fabsf(p.scale) * kLog2e;  // a negative scale's sign goes to the queries
+  const float cs = p.scale * kLog2e;
   auto wait_warp = [&](uint32_t bar, uint32_t par) {
     return __all_sync(0xFFFFFFFFu, mbar_wait(bar, par)) != 0;
   };
@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
     const int page_rows = min(1 << p.c.page_shift, kKeys);  // rows of a box
     const int boxes = kKeys / page_rows;                    // of a tile
     int c = 0;  // positions of the ring so far
-    int item_no = 0;
+    int item_no = 0, looked = 0;
     bool ok = true;
     struct Tile {     // what the ring's position c holds
       int64_t pos0;   // its first position
@@ -243,50 +243,48 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
       if (c >= W::NS && !wait_warp(empty(st), (c / W::NS - 1) & 1)) return false;
       const uint32_t dst = sT + st * W::TILE;
       if (!v && lw == 0) note(t, first);
-      if (v && t.edge) {  // absent rows are zeros, nodes' rows are looked at
-        constexpr int PR = D / 8, B = 8;  // pieces of a row; loads in flight
-        for (int id0 = lt; id0 - lt < kKeys * PR; id0 += B * LT) {
-          uint4 x[B];
+      // box l: the page rows of group l * page_rows / 8, for lane l < boxes
+      const int group = (lane * page_rows >> 3) & 15;
+      const int page = __shfl_sync(0xFFFFFFFFu, t.page, group), row = __shfl_sync(0xFFFFFFFFu, t.row, group);
+      const bool on = lane < boxes && ((t.there >> group) & 1u);
+      const int have = __popc(__ballot_sync(0xFFFFFFFFu, on));
+      const bool look = v && t.edge;  // absent rows are to be zeros, nodes' rows are looked at
+      const uint32_t bar = look ? rfull(0) : full(st);
+      if (lw == 0) {
+        if (lane == 0 && (have || !look)) mbar_arrive_expect_tx(bar, have * page_rows * D * 2);
+        __syncwarp();
+        if (on) {
 #pragma unroll
-          for (int i = 0; i < B; ++i) {
-            const int id = id0 + i * LT, r = min(id / PR, kKeys - 1), ch = id % PR;
-            const int64_t code = __shfl_sync(0xFFFFFFFFu, t.at.code, r >> 3);
-            x[i] = make_uint4(0, 0, 0, 0);
-            if (id < kKeys * PR && code >= 0 && r < t.left)
-              x[i] = ld_stream_v4(p.c.v + (code + (r & 7) * D + ch * 8) * 2);
+          for (int hf = 0; hf < D / 64; ++hf)
+            tma_load_3d(dst + hf * W::HALF + lane * page_rows * 128, v ? &tm_v : &tm_k, hf * 64, row, page,
+                        bar);
+        }
+        __syncwarp();
+      } else if (!look && lane == 0) {
+        mbar_arrive(full(st));
+      }
+      if (look) {
+        if (have && !wait_warp(bar, looked++ & 1)) return false;
+        constexpr int PR = D / 8;
+        for (int id = lt; id < kKeys * PR; id += LT) {
+          const int r = id / PR, ch = id % PR;
+          const bool there = r < t.left && ((t.there >> (r >> 3)) & 1u);
+          if (there && t.node0 + r < 0) continue;
+          const uint32_t at = dst + (ch >> 3) * W::HALF + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+          uint32_t h[4] = {0, 0, 0, 0};
+          if (there) {
+            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+                         : "r"(at));
+            clean(h, 4, t.node0 + r, t.bad);
           }
-#pragma unroll
-          for (int i = 0; i < B; ++i) {
-            const int id = id0 + i * LT, r = id / PR, ch = id % PR;
-            if (id >= kKeys * PR) continue;
-            uint32_t h[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-            if (t.node0 + r >= 0) clean(h, 4, t.node0 + r, t.bad);
-            sts_v4(dst + (ch >> 3) * W::HALF + r * 128 + (((ch & 7) ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
-          }
+          sts_v4(at, h[0], h[1], h[2], h[3]);
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(full(st));
-      } else {
-        if (lw == 0) {
-          // box l: the page rows of group l * page_rows / 8, for lane l < boxes
-          const int group = (lane * page_rows >> 3) & 15;
-          const int page = __shfl_sync(0xFFFFFFFFu, t.page, group), row = __shfl_sync(0xFFFFFFFFu, t.row, group);
-          const bool on = lane < boxes && ((t.there >> group) & 1u);
-          const int have = __popc(__ballot_sync(0xFFFFFFFFu, on));
-          if (lane == 0) mbar_arrive_expect_tx(full(st), have * page_rows * D * 2);
-          __syncwarp();
-          if (on) {
-#pragma unroll
-            for (int hf = 0; hf < D / 64; ++hf)
-              tma_load_3d(dst + hf * W::HALF + lane * page_rows * 128, v ? &tm_v : &tm_k, hf * 64, row,
-                          page, full(st));
-          }
-        } else if (lane == 0) {
-          mbar_arrive(full(st));
-        }
-        __syncwarp();
       }
+      __syncwarp();
       ++c;
       return true;
     };
@@ -577,38 +575,40 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
     float* slots = reinterpret_cast<float*>(
         p.workspace + join_head_bytes((int64_t)p.seqs * p.c.kv_heads * sched.rt_max));
     bool ok = true;
-    Span w;
-    SeqInfo si;
-    while (ok && sched.next(p, w, si)) {
-      const int n = w.u1 - w.u0;
-      const int r0 = w.rt * IROWS + (PAIR ? b * kRows : 0);  // the stream's first row
-      const int rows = max(0, min(kRows, si.n * G - r0));
-      // queries: every score product of the last item is done
-      {
-        const int t0 = PAIR ? threadIdx.x & 127 : threadIdx.x;
-        const uint32_t q = sQ + (PAIR && b ? kRows * D * 2 : 0);
-        const uint32_t sg = p.scale < 0.0f ? 0x80008000u : 0u;
-        constexpr int TH = PAIR ? 128 : 256, PER = kRows * (D / 8) / TH;
-        uint4 x[PER];  // all loads in flight
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-          const int id = t0 + i * TH, r = id / (D / 8), ch = id % (D / 8), rr = r0 + r;
-          x[i] = make_uint4(0, 0, 0, 0);
-          if (r < rows)
-            x[i] = ld_keep_v4(p.q + (int64_t)(si.first + heads.node(rr)) * p.ldq +
-                              (w.h * G + heads.head(rr)) * D + ch * 8);
-        }
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-          const int id = t0 + i * TH, r = id / (D / 8), ch = id % (D / 8);
-          sts_v4(q + (ch >> 3) * W::HALF + r * 128 + (((ch & 7) ^ (r & 7)) << 4), x[i].x ^ sg,
-                 x[i].y ^ sg, x[i].z ^ sg, x[i].w ^ sg);
-        }
+    // An item's queries (of this stream's rows), by this warpgroup: asked for when
+    // the last product that reads the ones before is done, announced when they
+    // are there, so that the next item's scores are computed while this one ends.
+    auto ask_q = [&](const Span& w, const SeqInfo& si) {
+      const int r0 = w.rt * IROWS + (PAIR ? b * kRows : 0), rows = min(kRows, si.n * G - r0);
+      const uint32_t q = sQ + (PAIR && b ? kRows * D * 2 : 0);
+      const int t0 = threadIdx.x & 127;
+#pragma unroll 4
+      for (int i = 0; i < kRows * (D / 8) / 128; ++i) {
+        const int id = t0 + i * 128, r = id / (D / 8), ch = id % (D / 8), rr = min(r0 + r, r0 + rows - 1);
+        const bool on = r < rows;
+        const __half* src = p.q;
+        if (on) src += (int64_t)(si.first + heads.node(rr)) * p.ldq + (w.h * G + heads.head(rr)) * D + ch * 8;
+        cp_async_16(q + (ch >> 3) * W::HALF + r * 128 + (((ch & 7) ^ (r & 7)) << 4), src, on ? 16u : 0u);
       }
+    };
+    auto announce_q = [&]() {
+      cp_async_wait_all();
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(qfull);
-
+    };
+    Span w, w2;
+    SeqInfo si, si2;
+    bool have = sched.next(p, w, si);
+    if (have && (PAIR || b == 0)) {
+      ask_q(w, si);
+      announce_q();
+    }
+    for (; ok && have; w = w2, si = si2) {
+      const int n = w.u1 - w.u0;
+      have = sched.next(p, w2, si2);  // the next item
+      const int r0 = w.rt * IROWS + (PAIR ? b * kRows : 0);  // the stream's first row
+      const int rows = max(0, min(kRows, si.n * G - r0));
       const int rr = r0 + row, node = heads.node(rr), hq = w.h * G + heads.head(rr);
       const bool mine = row < rows;
       const uint64_t bits = !mine ? 0ull
@@ -617,6 +617,9 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
       const bool idle = (warp & 3) * 32 >= rows;  // a warp without rows
       float m = -INFINITY, l = 0.0f;
       const int tiles = PAIR && rows == 0 ? 0 : (n - off0 + step - 1) / step;
+      // this stream has the item's last scores (or reads none of its queries)
+      const bool asks = have && (PAIR || b == ((n - 1) & 1));
+      if (PAIR && asks && tiles == 0) ask_q(w2, si2);
       for (int k = 0; k < tiles; ++k) {
         const int i = off0 + k * step;
         ok = wait_warp(sfull(b), ns++ & 1);
@@ -624,6 +627,7 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
         // but every phase of a barrier is seen, so that its parity says which)
         if (ok && k > 0) ok = wait_warp(ofull(b), (no + k - 1) & 1);
         if (!ok) break;
+        if (asks && k == tiles - 1) ask_q(w2, si2);
         if (!idle) {
           tc_fence_after_sync();
           const int slot = (tile_no + i) % kMeta;
@@ -671,10 +675,19 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
                 if (!((see >> x) & 1u)) v[x] = 0xFF800000u;  // -inf
             }
           };
-          // Most tiles: no row's maximum moves.  Weights by the maximum so far,
-          // in one reading of the scores; kept only if no score exceeds it.
+          // Most tiles: no row's maximum moves.  Weights by the maximum so far
+          // (an item's first tile: of 32 positions), in one reading of the scores;
+          // kept only if no score exceeds it by too much.
           bool done = false;
-          if (k > 0 && !edge && __all_sync(0xFFFFFFFFu, m > -INFINITY)) {
+          if (k == 0) {
+            uint32_t v[32];
+            tmem_ld_32(tS, v);
+            tmem_ld_wait();
+            exponents(v, 0);
+#pragma unroll
+            for (int x = 0; x < 32; ++x) m = fmaxf(m, __uint_as_float(v[x]));
+          }
+          if (__all_sync(0xFFFFFFFFu, m > -INFINITY)) {
             uint32_t h[64];
             float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
             float t[2] = {-INFINITY, -INFINITY};
@@ -696,6 +709,19 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
                   e0 = add2(fma2(e0, make_float2(a.x, a.y), make_float2(d.x, d.y)), mm);
                   e1 = add2(fma2(e1, make_float2(a.z, a.w), make_float2(d.z, d.w)), mm);
                 }
+                v[x] = __float_as_uint(e0.x), v[x + 1] = __float_as_uint(e0.y);
+                v[x + 2] = __float_as_uint(e1.x), v[x + 3] = __float_as_uint(e1.y);
+              }
+              if (edge) {
+                const uint32_t see = sees(y);
+#pragma unroll
+                for (int x = 0; x < 32; ++x)
+                  if (!((see >> x) & 1u)) v[x] = 0xFF800000u;  // -inf
+              }
+#pragma unroll
+              for (int x = 0; x < 32; x += 4) {
+                float2 e0 = make_float2(__uint_as_float(v[x]), __uint_as_float(v[x + 1]));
+                float2 e1 = make_float2(__uint_as_float(v[x + 2]), __uint_as_float(v[x + 3]));
                 t[0] = fmaxf(fmaxf(t[0], e0.x), e0.y);
                 t[1] = fmaxf(fmaxf(t[1], e1.x), e1.y);
                 e0 = make_float2(exp2_fast(e0.x), exp2_fast(e0.y));
@@ -784,6 +810,7 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(pfull(b));
       }
+      if (ok && asks) announce_q();
       if (ok && tiles > 0) ok = wait_warp(ofull(b), (no + tiles - 1) & 1);
       no += tiles;
       tile_no += n;
