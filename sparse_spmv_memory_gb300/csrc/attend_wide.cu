@@ -12,9 +12,10 @@
 //   MMA      one thread: S = Q K^T into TMEM; O += P V with P from TMEM and V
 //            as the MN-major operand (its rows are the reduction's).
 //   softmax  two warpgroups, a query row per thread: scores from TMEM, weights
-//            back over them as fp16.  The maximum that scales a row moves only
-//            when a score exceeds it by 2^8 (fp16 weights reach 2^8 then, at the
-//            same relative rounding), so the sums in TMEM are seldom rescaled.
+//            back over them as fp16, 32 positions at a time.  The maximum that
+//            scales a row moves only when a score exceeds it by 2^8 (fp16 weights
+//            reach 2^8 then, at the same relative rounding), so the sums in TMEM
+//            are seldom rescaled.
 // With 8-bit caches the product with V takes codes: the weight of position j is
 // 2^(s_j + log2 v_j - m), v_j the row's scale, and the sum of weights adds
 // w_j / v_j; a key's scale multiplies its score.  So codes enter the MMA
@@ -105,6 +106,16 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
       "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
       : "=f"(d.x), "=f"(d.y)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, w;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
 
@@ -653,20 +664,27 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
             if (rest < 32) x &= rest <= 0 ? 0u : (1u << rest) - 1u;
             return x;
           };
-          // exponents (powers of 2) of 32 positions, in place
-          auto exponents = [&](uint32_t (&v)[32], int y) {
-            if (F16) {
+          // 32 positions at a time, in one reading of the scores.
+#pragma unroll 1
+          for (int y = 0; y < 4; ++y) {
+            uint32_t v[32], h[16];
+            tmem_ld_32(tS + 32 * y, v);
+            tmem_ld_wait();
+            // exponents, in powers of 2
 #pragma unroll
-              for (int x = 0; x < 32; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * cs);
-            } else {
-#pragma unroll
-              for (int x = 0; x < 32; x += 4) {
+            for (int x = 0; x < 32; x += 4) {
+              float2 e0 = make_float2(__uint_as_float(v[x]), __uint_as_float(v[x + 1]));
+              float2 e1 = make_float2(__uint_as_float(v[x + 2]), __uint_as_float(v[x + 3]));
+              if (F16) {
+                e0 = mul2(e0, make_float2(cs, cs));
+                e1 = mul2(e1, make_float2(cs, cs));
+              } else {
                 const float4 a = ksc[8 * y + x / 4], d = lvs[8 * y + x / 4];
-                v[x] = __float_as_uint(fmaf(__uint_as_float(v[x]), a.x, d.x));
-                v[x + 1] = __float_as_uint(fmaf(__uint_as_float(v[x + 1]), a.y, d.y));
-                v[x + 2] = __float_as_uint(fmaf(__uint_as_float(v[x + 2]), a.z, d.z));
-                v[x + 3] = __float_as_uint(fmaf(__uint_as_float(v[x + 3]), a.w, d.w));
+                e0 = fma2(e0, make_float2(a.x, a.y), make_float2(d.x, d.y));
+                e1 = fma2(e1, make_float2(a.z, a.w), make_float2(d.z, d.w));
               }
+              v[x] = __float_as_uint(e0.x), v[x + 1] = __float_as_uint(e0.y);
+              v[x + 2] = __float_as_uint(e1.x), v[x + 3] = __float_as_uint(e1.y);
             }
             if (edge) {
               const uint32_t see = sees(y);
@@ -674,135 +692,65 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
               for (int x = 0; x < 32; ++x)
                 if (!((see >> x) & 1u)) v[x] = 0xFF800000u;  // -inf
             }
-          };
-          // Most tiles: no row's maximum moves.  Weights by the maximum so far
-          // (an item's first tile: of 32 positions), in one reading of the scores;
-          // kept only if no score exceeds it by too much.
-          bool done = false;
-          if (k == 0) {
-            uint32_t v[32];
-            tmem_ld_32(tS, v);
-            tmem_ld_wait();
-            exponents(v, 0);
-#pragma unroll
-            for (int x = 0; x < 32; ++x) m = fmaxf(m, __uint_as_float(v[x]));
-          }
-          if (__all_sync(0xFFFFFFFFu, m > -INFINITY)) {
-            uint32_t h[64];
-            float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-            float t[2] = {-INFINITY, -INFINITY};
-            const float2 mm = make_float2(-m, -m), cc = make_float2(cs, cs);
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              uint32_t v[32];
-              tmem_ld_32(tS + 32 * y, v);
-              tmem_ld_wait();
-#pragma unroll
-              for (int x = 0; x < 32; x += 4) {
-                float2 e0 = make_float2(__uint_as_float(v[x]), __uint_as_float(v[x + 1]));
-                float2 e1 = make_float2(__uint_as_float(v[x + 2]), __uint_as_float(v[x + 3]));
-                if (F16) {
-                  e0 = fma2(e0, cc, mm);
-                  e1 = fma2(e1, cc, mm);
-                } else {
-                  const float4 a = ksc[8 * y + x / 4], d = lvs[8 * y + x / 4];
-                  e0 = add2(fma2(e0, make_float2(a.x, a.y), make_float2(d.x, d.y)), mm);
-                  e1 = add2(fma2(e1, make_float2(a.z, a.w), make_float2(d.z, d.w)), mm);
-                }
-                v[x] = __float_as_uint(e0.x), v[x + 1] = __float_as_uint(e0.y);
-                v[x + 2] = __float_as_uint(e1.x), v[x + 3] = __float_as_uint(e1.y);
-              }
-              if (edge) {
-                const uint32_t see = sees(y);
-#pragma unroll
-                for (int x = 0; x < 32; ++x)
-                  if (!((see >> x) & 1u)) v[x] = 0xFF800000u;  // -inf
-              }
-#pragma unroll
-              for (int x = 0; x < 32; x += 4) {
-                float2 e0 = make_float2(__uint_as_float(v[x]), __uint_as_float(v[x + 1]));
-                float2 e1 = make_float2(__uint_as_float(v[x + 2]), __uint_as_float(v[x + 3]));
-                t[0] = fmaxf(fmaxf(t[0], e0.x), e0.y);
-                t[1] = fmaxf(fmaxf(t[1], e1.x), e1.y);
-                e0 = make_float2(exp2_fast(e0.x), exp2_fast(e0.y));
-                e1 = make_float2(exp2_fast(e1.x), exp2_fast(e1.y));
-                if (F16) {
-                  sum[0] = add2(sum[0], e0);
-                  sum[1] = add2(sum[1], e1);
-                } else {
-                  const float4 r = rvs[8 * y + x / 4];
-                  sum[0] = fma2(e0, make_float2(r.x, r.y), sum[0]);
-                  sum[1] = fma2(e1, make_float2(r.z, r.w), sum[1]);
-                }
-                h[16 * y + x / 2] = half2_of(e0.x, e0.y);
-                h[16 * y + x / 2 + 1] = half2_of(e1.x, e1.y);
-              }
-            }
-            done = __all_sync(0xFFFFFFFFu, fmaxf(t[0], t[1]) <= kGrow);
-            if (done) {
-#pragma unroll
-              for (int y = 0; y < 4; ++y) tmem_st_16(tS + 16 * y, h + 16 * y);
-              l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-            }
-          }
-          if (!done) {
-          float top = -INFINITY;
-#pragma unroll 1
-          for (int y = 0; y < 4; ++y) {
-            uint32_t v[32];
-            tmem_ld_32(tS + 32 * y, v);
-            tmem_ld_wait();
-            exponents(v, y);
-            float t[4] = {top, -INFINITY, -INFINITY, -INFINITY};
+            float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
             for (int x = 0; x < 32; ++x) t[x & 3] = fmaxf(t[x & 3], __uint_as_float(v[x]));
-            top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
-          }
-          const bool grow = top > m + kGrow || (m == -INFINITY && top > -INFINITY);
-          const float m2 = grow ? top : m;
-          if (k > 0 && __any_sync(0xFFFFFFFFu, grow)) {  // there are sums so far
-            const float keep = !grow ? 1.0f : m == -INFINITY ? 0.0f : exp2_fast(m - m2);
+            const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+            const bool grow = top > m + kGrow || (m == -INFINITY && top > -INFINITY);
+            if (__any_sync(0xFFFFFFFFu, grow)) {
+              // seldom (but for an item's first positions): the sums so far, and
+              // the weights of this tile so far, move to the new maximum
+              const float keep = !grow ? 1.0f : m == -INFINITY ? 0.0f : exp2_fast(m - top);
+              if (k > 0) {
 #pragma unroll 1
-            for (int y = 0; y < D; y += 32) {
-              uint32_t v[32];
-              tmem_ld_32(tO + y, v);
-              tmem_ld_wait();
+                for (int d = 0; d < D; d += 32) {
+                  uint32_t o[32];
+                  tmem_ld_32(tO + d, o);
+                  tmem_ld_wait();
 #pragma unroll
-              for (int x = 0; x < 32; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * keep);
-              tmem_st_32(tO + y, v);
-            }
-            l *= keep;
-          }
-          m = m2;
-          const float off = m == -INFINITY ? 0.0f : m;
+                  for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * keep);
+                  tmem_st_32(tO + d, o);
+                }
+              }
 #pragma unroll 1
-          for (int y = 0; y < 4; ++y) {
-            uint32_t v[32], h[16];
-            tmem_ld_32(tS + 32 * y, v);
-            tmem_ld_wait();
-            exponents(v, y);
-            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+              for (int z = 0; z < y; z += 2) {  // two chunks' weights (one may be to come)
+                uint32_t o[32];
+                tmem_st_wait();
+                tmem_ld_32(tS + 16 * z, o);
+                tmem_ld_wait();
+                // (rounded a second time, in the few tiles where a maximum moves)
+#pragma unroll
+                for (int x = 0; x < 32; ++x) {
+                  const float2 f = half2_bits_to_float2(o[x]);
+                  o[x] = half2_of(f.x * keep, f.y * keep);
+                }
+                tmem_st_16(tS + 16 * z, o);
+                if (z + 1 < y) tmem_st_16(tS + 16 * z + 16, o + 16);
+              }
+              l *= keep;
+              if (grow) m = top;
+            }
+            const float off = m == -INFINITY ? 0.0f : -m;
+            float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
             for (int x = 0; x < 32; x += 4) {
-              float e[4];
-#pragma unroll
-              for (int z = 0; z < 4; ++z) e[z] = exp2_fast(__uint_as_float(v[x + z]) - off);
+              float2 e0 = add2(make_float2(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), make_float2(off, off));
+              float2 e1 = add2(make_float2(__uint_as_float(v[x + 2]), __uint_as_float(v[x + 3])), make_float2(off, off));
+              e0 = make_float2(exp2_fast(e0.x), exp2_fast(e0.y));
+              e1 = make_float2(exp2_fast(e1.x), exp2_fast(e1.y));
               if (F16) {
-#pragma unroll
-                for (int z = 0; z < 4; ++z) sum[z] += e[z];
+                sum[0] = add2(sum[0], e0);
+                sum[1] = add2(sum[1], e1);
               } else {
                 const float4 r = rvs[8 * y + x / 4];
-                sum[0] = fmaf(e[0], r.x, sum[0]);
-                sum[1] = fmaf(e[1], r.y, sum[1]);
-                sum[2] = fmaf(e[2], r.z, sum[2]);
-                sum[3] = fmaf(e[3], r.w, sum[3]);
+                sum[0] = fma2(e0, make_float2(r.x, r.y), sum[0]);
+                sum[1] = fma2(e1, make_float2(r.z, r.w), sum[1]);
               }
-              h[x / 2] = half2_of(e[0], e[1]);
-              h[x / 2 + 1] = half2_of(e[2], e[3]);
+              h[x / 2] = half2_of(e0.x, e0.y);
+              h[x / 2 + 1] = half2_of(e1.x, e1.y);
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             tmem_st_16(tS + 16 * y, h);
-          }
           }
           tmem_st_wait();
         }
