@@ -338,23 +338,39 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
       if (!wait_warp(rfull(rs), (c / RS) & 1)) return false;
       if (c >= W::NS && !wait_warp(empty(st), (c / W::NS - 1) & 1)) return false;
       const uint32_t dst = sT + st * W::TILE, src = base + W::RAW_OFF + rs * W::RAW;
-      constexpr int PR = D / 16;  // pieces of a row
+      // A thread's pieces: column piece ch of rows r0, r0 + STEP, ...; the swizzle of
+      // row r0 + i STEP differs from row r0's by at most the bit that STEP's
+      // multiple of 4 turns.
+      constexpr int PR = D / 16, STEP = CT / PR;  // pieces of a row
+      static_assert(STEP % 4 == 0, "see above");
+      const int ch = ct % PR, r0 = ct / PR;
+      const uint32_t from = src + ct * 16;
+      const uint32_t to = dst + (ch >> 2) * W::HALF + r0 * 128 + ((((ch & 3) * 2) ^ (r0 & 7)) << 4);
+      constexpr uint32_t kTurn = STEP % 8 ? 64u : 0u;
       const bool look = v && t.edge;
-#pragma unroll 4
-      for (int id = ct; id < kKeys * PR; id += CT) {
-        const int r = id / PR, ch = id % PR;
-        uint32_t w[4], h[8];
-        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                     : "r"(src + id * 16));
-        if (look && !(r < t.left && ((t.there >> (r >> 3)) & 1u))) w[0] = w[1] = w[2] = w[3] = 0;
+      constexpr int ALL = (kKeys + STEP - 1) / STEP, B = 4;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) widen4<F16 ? kCacheE4m3 : TYPE>(w[k], h[2 * k], h[2 * k + 1]);
-        if (TYPE == kCacheE4m3 && look && t.node0 + r >= 0) clean(h, 8, t.node0 + r, t.bad);
-        const uint32_t at = dst + (ch >> 2) * W::HALF + r * 128;
-        const uint32_t c0 = (ch & 3) * 2;
-        sts_v4(at + ((c0 ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
-        sts_v4(at + (((c0 + 1) ^ (r & 7)) << 4), h[4], h[5], h[6], h[7]);
+      for (int i0 = 0; i0 < ALL; i0 += B) {
+        uint32_t w[B][4];
+#pragma unroll
+        for (int i = 0; i < B; ++i)
+          if (i0 + i < ALL && r0 + (i0 + i) * STEP < kKeys)
+            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(w[i][0]), "=r"(w[i][1]), "=r"(w[i][2]), "=r"(w[i][3])
+                         : "r"(from + (i0 + i) * CT * 16));
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+          const int r = r0 + (i0 + i) * STEP;
+          if (i0 + i >= ALL || r >= kKeys) continue;
+          if (look && !(r < t.left && ((t.there >> (r >> 3)) & 1u))) w[i][0] = w[i][1] = w[i][2] = w[i][3] = 0;
+          uint32_t h[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) widen4<F16 ? kCacheE4m3 : TYPE>(w[i][k], h[2 * k], h[2 * k + 1]);
+          if (TYPE == kCacheE4m3 && look && t.node0 + r >= 0) clean(h, 8, t.node0 + r, t.bad);
+          const uint32_t at = (to + (i0 + i) * STEP * 128) ^ ((i0 + i) & 1 ? kTurn : 0u);
+          sts_v4(at, h[0], h[1], h[2], h[3]);
+          sts_v4(at ^ 16u, h[4], h[5], h[6], h[7]);
+        }
       }
       if (!v) {
 #pragma unroll
