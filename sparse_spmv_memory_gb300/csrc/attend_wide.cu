@@ -51,14 +51,14 @@ constexpr float kTinyScale = 7.888609052210118e-31f;  // 2^-100: a smaller scale
 template <int D, int TYPE, bool PAIR>
 struct Wide {
   static constexpr bool F16 = TYPE == kCacheFp16;
-  // Loader warps (384 or 512 threads).  8-bit: one fetches, two groups of CW
+  // Loader warps (384 or 640 threads).  8-bit: one fetches, two groups of CW
   // widen the even and the odd positions of the ring; NS and RS are even, so
   // that a slot's barriers are always waited on by the same group.
-  static constexpr int LW = F16 ? 3 : 7, CW = 3;
+  static constexpr int LW = F16 ? 3 : 11, CW = 5;
   static constexpr int THREADS = 32 * (kLoadWarp + LW);
   // Registers of a thread: the launch gives every warpgroup (65536 / THREADS,
   // rounded down to 8) of them, the softmax warpgroups take some of the others'.
-  static constexpr int REGS = F16 ? 168 : 128, SOFT_REGS = F16 ? 200 : 168, OTHER_REGS = F16 ? 104 : 88;
+  static constexpr int REGS = F16 ? 168 : 96, SOFT_REGS = F16 ? 200 : 144, OTHER_REGS = F16 ? 104 : 64;
   static_assert(2 * SOFT_REGS + (THREADS / 128 - 2) * OTHER_REGS <= THREADS / 128 * REGS,
                 "the split fits the launch");
   static constexpr int QT = PAIR ? 2 : 1;     // row tiles of an item
@@ -76,6 +76,13 @@ struct Wide {
   static_assert(SMEM <= 227 * 1024 - 4096, "static shared memory needs room too");
   static_assert(NS + RS <= 10 && NS <= 8, "see above");
   static_assert(F16 || (NS % 2 == 0 && RS % 2 == 0 && LW == 1 + 2 * CW), "see above");
+};
+
+struct RawTile {
+  int v, edge, stop;  // V (else K); has nodes or absent rows; none: the ring has ended
+  int left, node0;    // as Tile's below
+  uint32_t there;
+  int bad, meta;
 };
 
 // TMEM columns.
@@ -149,6 +156,9 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
   __shared__ uint32_t there_of[kMeta];
   __shared__ uint32_t bad_of[kBad][2];
   __shared__ float2 s_ml[2][kRows];
+  // 8-bit: what a raw tile is, for the groups that widen it
+  __shared__ RawTile raw_of[RS];
+  __shared__ int64_t raw_scales[RS][16];  // of its groups of 8 rows
   const uint32_t base = (smem_addr(raw_smem) + 1023u) & ~1023u;
   uint8_t* gbase = raw_smem + (base - smem_addr(raw_smem));
   const uint32_t sQ = base + W::Q_OFF, sT = base + W::ST_OFF;
@@ -300,42 +310,58 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
       return true;
     };
 
-    // 8-bit, the fetching warp: the raw ring's next position is K or V of tile t.
-    auto fetch8 = [&](bool v, const Tile& t, bool first) {
+    // 8-bit, the fetching warp: the raw ring's next position is K or V of tile t
+    // (null: there is none).
+    auto fetch8 = [&](bool v, const Tile* t, bool first) {
       const int st = c % RS;
       if (c >= RS && !wait_warp(rfree(st), (c / RS - 1) & 1)) return false;
-      if (!v) note(t, first);
+      ++c;
+      if (!t) {
+        if (lane == 0) {
+          raw_of[st].stop = 1;
+          mbar_arrive(rfull(st));
+        }
+        __syncwarp();
+        return true;
+      }
+      if (!v) note(*t, first);
       const int group = (lane * page_rows >> 3) & 15;
-      const int64_t code = __shfl_sync(0xFFFFFFFFu, t.at.code, group);
+      const int64_t code = __shfl_sync(0xFFFFFFFFu, t->at.code, group);
       const bool on = lane < boxes && code >= 0;
       const int have = __popc(__ballot_sync(0xFFFFFFFFu, on));
+      if (lane < 16) raw_scales[st][lane] = t->at.scale;
+      if (lane == 0) raw_of[st] = RawTile{v, t->edge, 0, t->left, t->node0, t->there, t->bad, t->meta};
+      __syncwarp();
       if (lane == 0) mbar_arrive_expect_tx(rfull(st), have * page_rows * D);
       __syncwarp();
       if (on)
         bulk_load(base + W::RAW_OFF + st * W::RAW + lane * page_rows * D, (v ? p.c.v : p.c.k) + code,
                   page_rows * D, rfull(st));
       __syncwarp();
-      ++c;
       return true;
     };
     // 8-bit, a widening group (ct: thread of it): the raw tile of position c to
     // its stage; with a K tile its scales: k scale log2(e), log2 v, 1 / v.
     const int ct = lt - 32 - (lw > W::CW ? W::CW * 32 : 0);
     constexpr int CT = W::CW * 32;
-    auto widen8 = [&](bool v, const Tile& t) {
+    bool stop = false;
+    auto widen8 = [&]() {
       const int st = c % W::NS, rs = c % RS;
-      float sc[2][2];  // rows ct and ct + CT: k, v scale; in flight while the codes are waited for
-      if (!v) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int r = min(ct + i * CT, kKeys - 1);
-          const int64_t at = __shfl_sync(0xFFFFFFFFu, t.at.scale, r >> 3);
-          const bool on = at >= 0 && r < t.left;
-          sc[i][0] = on ? p.c.k_scale[at + (r & 7)] : 0.0f;
-          sc[i][1] = on ? p.c.v_scale[at + (r & 7)] : 0.0f;
+      if (!wait_warp(rfull(rs), (c / RS) & 1)) return false;
+      const RawTile t = raw_of[rs];
+      if (t.stop) {
+        stop = true;
+        return true;
+      }
+      const bool v = t.v;
+      float sc[2] = {0.0f, 0.0f};  // row ct's k and v scale, in flight while the codes are widened
+      if (!v && ct < kKeys) {
+        const int64_t at = raw_scales[rs][ct >> 3];
+        if (at >= 0 && ct < t.left) {
+          sc[0] = p.c.k_scale[at + (ct & 7)];
+          sc[1] = p.c.v_scale[at + (ct & 7)];
         }
       }
-      if (!wait_warp(rfull(rs), (c / RS) & 1)) return false;
       if (c >= W::NS && !wait_warp(empty(st), (c / W::NS - 1) & 1)) return false;
       const uint32_t dst = sT + st * W::TILE, src = base + W::RAW_OFF + rs * W::RAW;
       // A thread's pieces: column piece ch of rows r0, r0 + STEP, ...; the swizzle of
@@ -372,23 +398,18 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
           sts_v4(at ^ 16u, h[4], h[5], h[6], h[7]);
         }
       }
-      if (!v) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int r = ct + i * CT, j = t.node0 + r;
-          if (r >= kKeys) continue;
-          const float x = sc[i][1];
-          float lv = log2f(x), rv = 1.0f / x;
-          if (x < kTinyScale) lv = -100.0f, rv = 1.0f / kTinyScale;
-          if (t.edge && j >= 0 && !(x < INFINITY)) {  // a node's row whose scale is not finite
-            lv = 0.0f, rv = 1.0f;
-            atomicOr(&bad_of[t.bad][(j >> 5) & 1], 1u << (j & 31));
-          }
-          float* f = scales + t.meta * kKeys + r;
-          f[0] = sc[i][0] * cs;
-          f[kMeta * kKeys] = lv;
-          f[2 * kMeta * kKeys] = rv;
+      if (!v && ct < kKeys) {
+        const int j = t.node0 + ct;
+        float lv = log2f(sc[1]), rv = 1.0f / sc[1];
+        if (sc[1] < kTinyScale) lv = -100.0f, rv = 1.0f / kTinyScale;
+        if (t.edge && j >= 0 && !(sc[1] < INFINITY)) {  // a node's row whose scale is not finite
+          lv = 0.0f, rv = 1.0f;
+          atomicOr(&bad_of[t.bad][(j >> 5) & 1], 1u << (j & 31));
         }
+        float* f = scales + t.meta * kKeys + ct;
+        f[0] = sc[0] * cs;
+        f[kMeta * kKeys] = lv;
+        f[2 * kMeta * kKeys] = rv;
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -459,36 +480,37 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
     // which tile a V position belongs to: the newest K tile, or the one before
     auto v_tile = [&](const Walk& x) -> const Tile& { return x.vi == x.i ? x.k : x.last; };
 
-    Walk x;
-    x.sched = sched;
-    x.tiles = x.items = 0;
-    start(x);
-    bool v, first;
-    if constexpr (F16) {
-      while (ok && step(x, v, first)) {
-        item_no = x.items;
-        ok = emit16(v, v ? v_tile(x) : x.k, first);
-      }
-    } else if (lw == 0) {
-      while (ok && step(x, v, first)) {
-        item_no = x.items;
-        ok = fetch8(v, v ? v_tile(x) : x.k, first);
-      }
-    } else {
-      for (; ok && step(x, v, first); ++c)
-        if ((c & 1) == (lw > W::CW ? 1 : 0)) ok = widen8(v, v ? v_tile(x) : x.k);
-    }
-    // Before the block ends its copies have landed and every release of a stage
-    // has arrived.
     if (F16 || lw == 0) {
+      Walk x;
+      x.sched = sched;
+      x.tiles = x.items = 0;
+      start(x);
+      bool v, first;
+      while (ok && step(x, v, first)) {
+        item_no = x.items;
+        if constexpr (F16)
+          ok = emit16(v, v ? v_tile(x) : x.k, first);
+        else
+          ok = fetch8(v, v ? &v_tile(x) : &x.k, first);
+      }
+      if (!F16)  // a last position for each group
+        for (int i = 0; i < 2 && ok; ++i) ok = fetch8(false, nullptr, false);
+      // Before the block ends its copies have landed ...
       constexpr int NC = F16 ? W::NS : RS;
       for (int pos = max(0, c - NC); pos < c; ++pos)
         mbar_wait(F16 ? full(pos % W::NS) : rfull(pos % RS), (pos / NC) & 1, kWaitLimitNs, ok);
-    }
-    if (F16 || lw > 0) {
-      for (int pos = max(0, c - W::NS); ok && pos < c; ++pos)
-        if (F16 || (pos & 1) == (lw > W::CW ? 1 : 0))
+      // ... and every release of a stage has arrived.
+      if (F16)
+        for (int pos = max(0, c - W::NS); ok && pos < c; ++pos)
           ok = wait_warp(empty(pos % W::NS), (pos / W::NS) & 1);
+    } else {
+      const int g = lw > W::CW ? 1 : 0;
+      for (c = g; ok; c += 2) {
+        ok = widen8();
+        if (stop) break;
+      }
+      for (int pos = max(g, c - W::NS); ok && pos < c; pos += 2)
+        ok = wait_warp(empty(pos % W::NS), (pos / W::NS) & 1);
     }
     __syncwarp();
   } else if (warp == kMmaWarp) {
