@@ -24,7 +24,8 @@ EXT_SOURCE = os.path.join(CSRC, "binding.cpp")
 
 SOURCES = ["api.cu", "spmv.cu", "spmm.cu", "spmm_b2.cu", "spmm_b4.cu", "spmm_b6.cu", "spmm_b8.cu",
            "spmm24.cu", "gemv.cu", "pack.cu", "check_noalloc.cu", "prefill.cu", "rope_cache.cu",
-           "attend.cu", "attend_wide.cu", "verify.cu", "decode_api.cu"]
+           "attend.cu", "attend_wide_fp16.cu", "attend_wide_e4m3.cu", "attend_wide_int8.cu",
+           "verify.cu", "decode_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-std=c++17", "-O3", *ARCH, "-lineinfo", "-Xcompiler", "-fPIC",
               "-Xcompiler", "-Wall", f"-I{INCLUDE}"]

@@ -732,12 +732,14 @@ int nm_prefill_stall_selftest(const void* values, const uint32_t* masks, int64_t
 }
 
 int64_t nm_wait_timeouts(int reset) {
-  unsigned long long a = 0, b = 0, c = 0;
-  if (read_wait_timeouts(&a, reset) != cudaSuccess ||
-      read_attend_wait_timeouts(&b, reset) != cudaSuccess ||
-      read_verify_wait_timeouts(&c, reset) != cudaSuccess)
+  unsigned long long n[5] = {0};
+  if (read_wait_timeouts(&n[0], reset) != cudaSuccess ||
+      read_attend_wait_timeouts<kCacheFp16>(&n[1], reset) != cudaSuccess ||
+      read_attend_wait_timeouts<kCacheE4m3>(&n[2], reset) != cudaSuccess ||
+      read_attend_wait_timeouts<kCacheInt8>(&n[3], reset) != cudaSuccess ||
+      read_verify_wait_timeouts(&n[4], reset) != cudaSuccess)
     return -NM_ERR_CUDA;
-  return (int64_t)(a + b + c);
+  return (int64_t)(n[0] + n[1] + n[2] + n[3] + n[4]);
 }
 
 int64_t nm_check_masks(const uint32_t* masks, int64_t rows, int64_t cols, void* stream) {

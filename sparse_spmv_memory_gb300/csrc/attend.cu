@@ -1,5 +1,5 @@
 // attend.cu -- attention of drafted nodes over a paged cache
-// (nm_tree_attention), for few query rows per key head; attend_wide.cu has the
+// (nm_tree_attention), for few query rows per key head; attend_wide.cuh has the
 // kernel for many.
 //
 // For a node's query q and the rows (k_j, v_j) that it sees,
@@ -524,13 +524,16 @@ cudaError_t narrow_mt(const AttendParams& p, int sms, cudaStream_t stream) {
 }  // namespace
 
 // Rows of a sequence and key head from which the tcgen05 kernel takes over.
-constexpr int kWideRows = 33;
+constexpr int kWideRows = 17;
 
 size_t attend_workspace_bytes(int64_t seqs, int q_heads, int kv_heads, int head_dim, int max_nodes,
                               int sms) {
   const int rows = max_nodes * (q_heads / kv_heads);
-  if (rows >= kWideRows)
-    return attend_wide_workspace_bytes(seqs, kv_heads, rows, head_dim, sms);
+  if (rows >= kWideRows) {
+    const int wide = wide_item_rows(wide_mode(rows));
+    return join_head_bytes(seqs * kv_heads * ((rows + wide - 1) / wide)) +
+           (size_t)sms * 2 * attend_slot_floats(wide, head_dim) * sizeof(float);
+  }
   const int tile = rows > 16 ? 32 : 16;
   return attend_counter_bytes(seqs * kv_heads * ((rows + tile - 1) / tile)) +
          (size_t)sms * 2 * attend_slot_floats(tile, head_dim) * sizeof(float);
@@ -539,7 +542,9 @@ size_t attend_workspace_bytes(int64_t seqs, int q_heads, int kv_heads, int head_
 cudaError_t launch_attend(const AttendParams& p, int head_dim, int type, int sms,
                           cudaStream_t stream) {
   if (p.max_nodes * (p.q_heads / p.c.kv_heads) >= kWideRows)
-    return launch_attend_wide(p, head_dim, type, sms, stream);
+    return type == kCacheFp16   ? launch_attend_wide<kCacheFp16>(p, head_dim, sms, stream)
+           : type == kCacheE4m3 ? launch_attend_wide<kCacheE4m3>(p, head_dim, sms, stream)
+                                : launch_attend_wide<kCacheInt8>(p, head_dim, sms, stream);
   if (head_dim == 128) {
     if (type == kCacheFp16) return narrow_mt<128, kCacheFp16>(p, sms, stream);
     if (type == kCacheE4m3) return narrow_mt<128, kCacheE4m3>(p, sms, stream);

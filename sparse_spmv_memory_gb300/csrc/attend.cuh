@@ -193,6 +193,15 @@ struct Schedule {
 __host__ __device__ constexpr size_t attend_counter_bytes(int64_t items) { return (size_t)(items + 3) / 4 * 16; }
 __host__ __device__ constexpr size_t attend_slot_floats(int rows, int d) { return (size_t)rows * (d + 2); }
 
+// The many-row kernel (attend_wide.cuh) by the rows of a sequence and key head:
+// 0: 256 rows of an item; 1, 2, 4: 128, 64, 32 rows in so many copies.
+__host__ __device__ constexpr int wide_mode(int rows) {
+  return rows <= 32 ? 4 : rows <= 64 ? 2 : rows <= 128 ? 1 : 0;
+}
+__host__ __device__ constexpr int wide_item_rows(int mode) { return mode == 0 ? 256 : 128 / mode; }
+// Its workspace: 16 bytes for each item (where its parts are), then two slots a block.
+__host__ __device__ constexpr size_t join_head_bytes(int64_t items) { return (size_t)items * 16; }
+
 // The slot that block b has an item's part in: its first where its range begins
 // inside the item (or with it), else its second.
 __device__ __forceinline__ int64_t part_slot(int64_t b, int64_t per, int64_t item_start) {

@@ -1,4 +1,4 @@
-// attend_wide.cu -- nm_tree_attention for many query rows per key head: 128
+// attend_wide.cuh -- nm_tree_attention for many query rows per key head: 128
 // rows at a time on tcgen05.
 //
 // A block walks the positions in tiles of 128.  Two streams, each with a score
@@ -16,10 +16,17 @@
 //            scales a row moves only when a score exceeds it by 2^8 (fp16 weights
 //            reach 2^8 then, at the same relative rounding), so the sums in TMEM
 //            are seldom rescaled.
+// With at most 64 (32) rows, the tile's 128 rows are two (four) copies of them,
+// and copy c weighs only the c-th half (quarter) of a tile's positions: a warp can
+// read no other lanes of TMEM than its own, so without copies half of the softmax
+// warps would have nothing to do and the others all of it.  The copies' sums join
+// like the streams'.
 // With 8-bit caches the product with V takes codes: the weight of position j is
 // 2^(s_j + log2 v_j - m), v_j the row's scale, and the sum of weights adds
 // w_j / v_j; a key's scale multiplies its score.  So codes enter the MMA
 // exactly and a weight is rounded once.
+#pragma once
+
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -41,6 +48,7 @@ constexpr int kRows = 128, kKeys = 128;
 constexpr int kSoftWarps = 8, kMmaWarp = 8, kLoadWarp = 9;
 constexpr int kMeta = 8;    // tiles whose scales and pages are kept
 constexpr int kBad = 16;    // items whose spoilt nodes are kept
+constexpr int kCopyPitch = 20;  // floats: 16 columns of a row, and its banks moved on by 20
 constexpr float kGrow = 8.0f;
 constexpr float kTinyScale = 7.888609052210118e-31f;  // 2^-100: a smaller scale counts as this
 
@@ -48,8 +56,10 @@ constexpr float kTinyScale = 7.888609052210118e-31f;  // 2^-100: a smaller scale
 // loader is at most NS + RS <= 10 positions of the ring ahead of the MMAs, and
 // a tile's softmax is over when its V tile is consumed: 13 positions before
 // the slot's next K tile at least; an item takes two positions or more.
-template <int D, int TYPE, bool PAIR>
+template <int D, int TYPE, int MODE>
 struct Wide {
+  static constexpr bool PAIR = MODE == 0;
+  static constexpr int SPLIT = PAIR ? 1 : MODE;
   static constexpr bool F16 = TYPE == kCacheFp16;
   // Loader warps (384 or 640 threads).  8-bit: one fetches, two groups of CW
   // widen the even and the odd positions of the ring; NS and RS are even, so
@@ -62,16 +72,18 @@ struct Wide {
   static_assert(2 * SOFT_REGS + (THREADS / 128 - 2) * OTHER_REGS <= THREADS / 128 * REGS,
                 "the split fits the launch");
   static constexpr int QT = PAIR ? 2 : 1;     // row tiles of an item
+  static constexpr int IROWS = QT * kRows / SPLIT;  // rows of an item
   static constexpr int TILE = kKeys * D * 2;  // bytes of a stage
   static constexpr int HALF = kKeys * 128;    // 64 elements of every row
   static constexpr int NS = F16 ? (D == 128 ? (PAIR ? 4 : 5) : 8) : (D == 128 ? 2 : 4);
-  static constexpr int RS = F16 ? 0 : (D == 128 && PAIR ? 4 : 6);  // raw tiles
+  static constexpr int RS = F16 ? 0 : (D == 128 && MODE != 1 ? 4 : 6);  // raw tiles
   static constexpr int RAW = kKeys * D;
   static constexpr int Q_OFF = 0;
   static constexpr int ST_OFF = Q_OFF + QT * kRows * D * 2;
   static constexpr int RAW_OFF = ST_OFF + NS * TILE;
   static constexpr int SC_OFF = RAW_OFF + RS * RAW;  // 8-bit: k scale', log2 v, 1 / v
-  static constexpr int BYTES = SC_OFF + (F16 ? 0 : 3 * kMeta * kKeys * 4);
+  static constexpr int CB_OFF = SC_OFF + (F16 ? 0 : 3 * kMeta * kKeys * 4);
+  static constexpr int BYTES = CB_OFF + (SPLIT > 1 ? 2 * kRows * kCopyPitch * 4 : 0);  // rows' copies added
   static constexpr int SMEM = BYTES + 1024;   // room to align the base
   static_assert(SMEM <= 227 * 1024 - 4096, "static shared memory needs room too");
   static_assert(NS + RS <= 10 && NS <= 8, "see above");
@@ -87,9 +99,6 @@ struct RawTile {
 
 // TMEM columns.
 constexpr uint32_t kS0 = 0, kS1 = 128, kO0 = 256, kO1 = 384, kTmemCols = 512;
-
-// Workspace: 16 bytes for each item (where its parts are), then two slots a block.
-__host__ __device__ constexpr size_t join_head_bytes(int64_t items) { return (size_t)items * 16; }
 
 __device__ __forceinline__ uint32_t half2_of(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
@@ -141,14 +150,14 @@ __device__ __forceinline__ void sts_v4(uint32_t at, uint32_t a, uint32_t b, uint
                : "memory");
 }
 
-template <int D, int TYPE, bool PAIR>
-__global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
+template <int D, int TYPE, int MODE>
+__global__ void __launch_bounds__(Wide<D, TYPE, MODE>::THREADS, 1)
     attend_wide_kernel(const __grid_constant__ AttendParams p, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v) {
-  using W = Wide<D, TYPE, PAIR>;
-  constexpr bool F16 = W::F16;
-  constexpr int RS = F16 ? 1 : W::RS;
-  constexpr int IROWS = W::QT * kRows;  // rows of an item
+  using W = Wide<D, TYPE, MODE>;
+  constexpr bool F16 = W::F16, PAIR = W::PAIR;
+  constexpr int RS = F16 ? 1 : W::RS, SPLIT = W::SPLIT;
+  constexpr int IROWS = W::IROWS;
   using Sched = Schedule<IROWS, kKeys, W::THREADS>;
   extern __shared__ uint8_t raw_smem[];
   __shared__ uint64_t bar_mem[2 * W::NS + 8 + 2 * RS];
@@ -156,6 +165,7 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
   __shared__ uint32_t there_of[kMeta];
   __shared__ uint32_t bad_of[kBad][2];
   __shared__ float2 s_ml[2][kRows];
+  __shared__ float s_inv[2][kRows];
   // 8-bit: what a raw tile is, for the groups that widen it
   __shared__ RawTile raw_of[RS];
   __shared__ int64_t raw_scales[RS][16];  // of its groups of 8 rows
@@ -611,6 +621,8 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
     // ---- softmax -------------------------------------------------------------------
     regs_up<W::SOFT_REGS>();
     const int b = warp >> 2, row = (warp & 3) * 32 + lane;
+    // the item's (PAIR: the stream's) row, and which of its copies
+    const int irow = PAIR ? row : row % IROWS, copy = PAIR ? 0 : row / IROWS;
     const uint32_t tlane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t tS = tlane + (b ? kS1 : kS0), tO = tlane + (b ? kO1 : kO0);
     const int step = PAIR ? 1 : 2, off0 = PAIR ? 0 : b;  // tiles of this stream
@@ -628,13 +640,13 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
     // the last product that reads the ones before is done, announced when they
     // are there, so that the next item's scores are computed while this one ends.
     auto ask_q = [&](const Span& w, const SeqInfo& si) {
-      const int r0 = w.rt * IROWS + (PAIR ? b * kRows : 0), rows = min(kRows, si.n * G - r0);
+      const int r0 = w.rt * IROWS + (PAIR ? b * kRows : 0), rows = min(PAIR ? kRows : IROWS, si.n * G - r0);
       const uint32_t q = sQ + (PAIR && b ? kRows * D * 2 : 0);
       const int t0 = threadIdx.x & 127;
 #pragma unroll 4
       for (int i = 0; i < kRows * (D / 8) / 128; ++i) {
-        const int id = t0 + i * 128, r = id / (D / 8), ch = id % (D / 8), rr = min(r0 + r, r0 + rows - 1);
-        const bool on = r < rows;
+        const int id = t0 + i * 128, r = id / (D / 8), ch = id % (D / 8), rr = r0 + (PAIR ? r : r % IROWS);
+        const bool on = (PAIR ? r : r % IROWS) < rows;
         const __half* src = p.q;
         if (on) src += (int64_t)(si.first + heads.node(rr)) * p.ldq + (w.h * G + heads.head(rr)) * D + ch * 8;
         cp_async_16(q + (ch >> 3) * W::HALF + r * 128 + (((ch & 7) ^ (r & 7)) << 4), src, on ? 16u : 0u);
@@ -657,13 +669,13 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
       const int n = w.u1 - w.u0;
       have = sched.next(p, w2, si2);  // the next item
       const int r0 = w.rt * IROWS + (PAIR ? b * kRows : 0);  // the stream's first row
-      const int rows = max(0, min(kRows, si.n * G - r0));
-      const int rr = r0 + row, node = heads.node(rr), hq = w.h * G + heads.head(rr);
-      const bool mine = row < rows;
+      const int rows = max(0, min(PAIR ? kRows : IROWS, si.n * G - r0));
+      const int rr = r0 + irow, node = heads.node(rr), hq = w.h * G + heads.head(rr);
+      const bool mine = irow < rows;
       const uint64_t bits = !mine ? 0ull
                             : p.tree_mask ? p.tree_mask[si.first + node]
                                           : (2ull << node) - 1ull;
-      const bool idle = (warp & 3) * 32 >= rows;  // a warp without rows
+      const bool idle = (PAIR ? (warp & 3) * 32 : (warp & 3) * 32 % IROWS) >= rows;  // a warp without rows
       float m = -INFINITY, l = 0.0f;
       const int tiles = PAIR && rows == 0 ? 0 : (n - off0 + step - 1) / step;
       // this stream has the item's last scores (or reads none of its queries)
@@ -703,8 +715,9 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
             return x;
           };
           // 32 positions at a time, in one reading of the scores.
+          const int y0 = copy * (4 / SPLIT), y1 = y0 + 4 / SPLIT;
 #pragma unroll 1
-          for (int y = 0; y < 4; ++y) {
+          for (int y = y0; y < y1; ++y) {
             uint32_t v[32], h[16];
             tmem_ld_32(tS + 32 * y, v);
             tmem_ld_wait();
@@ -751,7 +764,7 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
                 }
               }
 #pragma unroll 1
-              for (int z = 0; z < y; z += 2) {  // two chunks' weights (one may be to come)
+              for (int z = y0; z < y; z += 2) {  // two chunks' weights (one may be to come)
                 uint32_t o[32];
                 tmem_st_wait();
                 tmem_ld_32(tS + 16 * z, o);
@@ -790,6 +803,12 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
             l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             tmem_st_16(tS + 16 * y, h);
           }
+          if (SPLIT > 1) {  // no weight on the other copies' positions
+            const uint32_t zero[16] = {};
+#pragma unroll 1
+            for (int y = 0; y < 4; ++y)
+              if (y < y0 || y >= y1) tmem_st_16(tS + 16 * y, zero);
+          }
           tmem_st_wait();
         }
         tc_fence_before_sync();
@@ -810,12 +829,20 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
           ok = false;
           break;
         }
-        const float2 A = s_ml[0][row], B = s_ml[1][row];
-        M = fmaxf(A.x, B.x);
+        // (a stream without tiles has maximum -infinity and sum 0)
+        M = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < SPLIT; ++c)
+          M = fmaxf(M, fmaxf(s_ml[0][irow + c * IROWS].x, s_ml[1][irow + c * IROWS].x));
         const float off = M == -INFINITY ? 0.0f : M;
-        fa = exp2_fast(A.x - off);
-        fb = both ? exp2_fast(B.x - off) : 0.0f;
-        tot = A.y * fa + (both ? B.y * fb : 0.0f);
+        tot = 0.0f;
+#pragma unroll
+        for (int c = 0; c < SPLIT; ++c) {
+          const float2 A = s_ml[0][irow + c * IROWS], B = s_ml[1][irow + c * IROWS];
+          tot += A.y * exp2_fast(A.x - off) + B.y * exp2_fast(B.x - off);
+        }
+        fa = exp2_fast(s_ml[0][row].x - off);
+        fb = both ? exp2_fast(s_ml[1][row].x - off) : 0.0f;
       }
       if (!ok) break;
       tc_fence_after_sync();
@@ -826,10 +853,56 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
       const float inv = tot == 0.0f ? 0.0f : 1.0f / tot;
       float4* slot4 = reinterpret_cast<float4*>(
           slots + part_slot(blockIdx.x, sched.per, w.start) * attend_slot_floats(IROWS, D));
-      const int srow = (PAIR ? b * kRows : 0) + row;  // row of the item
+      const int srow = (PAIR ? b * kRows : 0) + irow;  // row of the item
       __half* out = p.out + (int64_t)(si.first + node) * p.ldo + (int64_t)hq * D;
       const int c0 = PAIR ? 0 : b * (D / 2), c1 = PAIR ? D : (b + 1) * (D / 2);
-      if (!idle) {
+      if (SPLIT > 1) {
+        // the copies' sums, 16 columns at a time through shared memory
+        float* cb = reinterpret_cast<float*>(gbase + W::CB_OFF) + b * kRows * kCopyPitch;
+#pragma unroll 1
+        for (int d0 = c0; d0 < c1 && ok; d0 += 16) {
+          uint32_t v[16], u[16];
+          if (!idle) {
+            tmem_ld_16(tlane + kO0 + d0, v);
+            if (both) tmem_ld_16(tlane + kO1 + d0, u);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 16; k += 4) {
+              float x[4];
+#pragma unroll
+              for (int z = 0; z < 4; ++z) {
+                x[z] = __uint_as_float(v[k + z]) * fa + poison;
+                if (both) x[z] += __uint_as_float(u[k + z]) * fb;
+              }
+              *reinterpret_cast<float4*>(cb + row * kCopyPitch + k) = make_float4(x[0], x[1], x[2], x[3]);
+            }
+          }
+          if (d0 == c0) s_inv[b][row] = inv;
+          ok = soft_sync();
+          if (!ok) break;
+          for (int id = threadIdx.x & 127; id < rows * 4; id += 128) {
+            const int r = id >> 2, c4 = id & 3;
+            float4 x = make_float4(0, 0, 0, 0);
+#pragma unroll
+            for (int c = 0; c < SPLIT; ++c) {
+              const float4 t = *reinterpret_cast<const float4*>(cb + (r + c * IROWS) * kCopyPitch + 4 * c4);
+              x.x += t.x, x.y += t.y, x.z += t.z, x.w += t.w;
+            }
+            const int d = d0 + 4 * c4;
+            if (whole) {
+              const int r2 = r0 + r;
+              const float iv = s_inv[b][r];
+              *reinterpret_cast<uint2*>(p.out + (int64_t)(si.first + heads.node(r2)) * p.ldo +
+                                        (w.h * G + heads.head(r2)) * D + d) =
+                  make_uint2(half2_of(x.x * iv, x.y * iv), half2_of(x.z * iv, x.w * iv));
+            } else {
+              slot4[d / 4 * IROWS + r] = x;
+            }
+          }
+          ok = soft_sync();
+        }
+        if (!ok) break;
+      } else if (!idle) {
 #pragma unroll 1
         for (int d0 = c0; d0 < c1; d0 += 32) {
           uint32_t v[32], u[32];
@@ -857,7 +930,7 @@ __global__ void __launch_bounds__(Wide<D, TYPE, PAIR>::THREADS, 1)
           __syncwarp();
         }
       }
-      const bool writes = mine && (PAIR || b == 0);
+      const bool writes = mine && (PAIR || (b == 0 && copy == 0));
       if (writes && whole && p.lse)
         p.lse[(int64_t)(si.first + node) * p.q_heads + hq] =
             tot == 0.0f ? -INFINITY : (M + log2f(tot)) * kLn2;
@@ -979,10 +1052,10 @@ bool encode_pages(CUtensorMap* m, const void* base, const CacheView& c, int head
                       CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int D, int TYPE, bool PAIR>
+template <int D, int TYPE, int MODE>
 cudaError_t wide_one(const AttendParams& p, int sms, cudaStream_t stream) {
-  using W = Wide<D, TYPE, PAIR>;
-  auto* k = attend_wide_kernel<D, TYPE, PAIR>;
+  using W = Wide<D, TYPE, MODE>;
+  auto* k = attend_wide_kernel<D, TYPE, MODE>;
   static int done[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1001,7 +1074,7 @@ cudaError_t wide_one(const AttendParams& p, int sms, cudaStream_t stream) {
   }
   e = launch_kernel(k, sms, W::THREADS, W::SMEM, stream, kFlagPdl, p, tk, tv);
   if (e != cudaSuccess) return e;
-  constexpr int IROWS = W::QT * kRows;
+  constexpr int IROWS = W::IROWS;
   const int rt_max = (p.max_nodes * (p.q_heads / p.c.kv_heads) + IROWS - 1) / IROWS;
   cudaLaunchConfig_t cfg = {};
   const int rows = p.max_nodes * (p.q_heads / p.c.kv_heads);
@@ -1018,30 +1091,23 @@ cudaError_t wide_one(const AttendParams& p, int sms, cudaStream_t stream) {
 
 template <int D, int TYPE>
 cudaError_t wide_rows(const AttendParams& p, int sms, cudaStream_t stream) {
-  return p.max_nodes * (p.q_heads / p.c.kv_heads) > kRows ? wide_one<D, TYPE, true>(p, sms, stream)
-                                                           : wide_one<D, TYPE, false>(p, sms, stream);
+  switch (wide_mode(p.max_nodes * (p.q_heads / p.c.kv_heads))) {
+    case 4: return wide_one<D, TYPE, 4>(p, sms, stream);
+    case 2: return wide_one<D, TYPE, 2>(p, sms, stream);
+    case 1: return wide_one<D, TYPE, 1>(p, sms, stream);
+    default: return wide_one<D, TYPE, 0>(p, sms, stream);
+  }
 }
 
 }  // namespace
 
-size_t attend_wide_workspace_bytes(int64_t seqs, int kv_heads, int rows, int head_dim, int sms) {
-  const int tile = rows > kRows ? 2 * kRows : kRows;
-  return join_head_bytes(seqs * kv_heads * ((rows + tile - 1) / tile)) +
-         (size_t)sms * 2 * attend_slot_floats(tile, head_dim) * sizeof(float);
+// One translation unit for each type (attend_wide_*.cu).
+template <int TYPE>
+cudaError_t launch_attend_wide(const AttendParams& p, int head_dim, int sms, cudaStream_t stream) {
+  return head_dim == 128 ? wide_rows<128, TYPE>(p, sms, stream) : wide_rows<64, TYPE>(p, sms, stream);
 }
 
-cudaError_t launch_attend_wide(const AttendParams& p, int head_dim, int type, int sms,
-                               cudaStream_t stream) {
-  if (head_dim == 128) {
-    if (type == kCacheFp16) return wide_rows<128, kCacheFp16>(p, sms, stream);
-    if (type == kCacheE4m3) return wide_rows<128, kCacheE4m3>(p, sms, stream);
-    return wide_rows<128, kCacheInt8>(p, sms, stream);
-  }
-  if (type == kCacheFp16) return wide_rows<64, kCacheFp16>(p, sms, stream);
-  if (type == kCacheE4m3) return wide_rows<64, kCacheE4m3>(p, sms, stream);
-  return wide_rows<64, kCacheInt8>(p, sms, stream);
-}
-
+template <int TYPE>
 cudaError_t read_attend_wait_timeouts(unsigned long long* count, int reset) {
   return read_local_wait_timeouts(count, reset);
 }

@@ -71,11 +71,11 @@ size_t attend_workspace_bytes(int64_t seqs, int q_heads, int kv_heads, int head_
 cudaError_t launch_attend(const AttendParams& p, int head_dim, int type, int sms,
                           cudaStream_t stream);
 
-// Many rows per key head (attend_wide.cu).
-size_t attend_wide_workspace_bytes(int64_t seqs, int kv_heads, int rows, int head_dim, int sms);
-cudaError_t launch_attend_wide(const AttendParams& p, int head_dim, int type, int sms,
-                               cudaStream_t stream);
+// Many rows per key head (attend_wide.cuh).
+template <int TYPE>
+cudaError_t launch_attend_wide(const AttendParams& p, int head_dim, int sms, cudaStream_t stream);
 // Its bounded waits that gave up since the last reset.
+template <int TYPE>
 cudaError_t read_attend_wait_timeouts(unsigned long long* count, int reset);
 
 // ---- verification of drafted tokens (verify.cu) --------------------------------
