@@ -46,7 +46,8 @@ namespace {
 
 constexpr int kRows = 128, kKeys = 128;
 constexpr int kSoftWarps = 8, kMmaWarp = 8, kLoadWarp = 9;
-constexpr int kMeta = 8;    // tiles whose scales and pages are kept
+constexpr int kMeta = 8;    // tiles of which it is kept which pages are there
+constexpr int kScales = 4;  // tiles whose scales are kept
 constexpr int kBad = 16;    // items whose spoilt nodes are kept
 constexpr int kCopyPitch = 20;  // floats: 16 columns of a row, and its banks moved on by 20
 constexpr float kGrow = 8.0f;
@@ -55,7 +56,9 @@ constexpr float kTinyScale = 7.888609052210118e-31f;  // 2^-100: a smaller scale
 // A slot of a tile (item) is written again kMeta (kBad) tiles (items) on.  A
 // loader is at most NS + RS <= 10 positions of the ring ahead of the MMAs, and
 // a tile's softmax is over when its V tile is consumed: 13 positions before
-// the slot's next K tile at least; an item takes two positions or more.
+// the slot's next K tile at least; an item takes two positions or more.  Scales
+// are written at most NS <= 4 positions ahead, their slot's next K tile 5 after
+// the V tile.
 template <int D, int TYPE, int MODE>
 struct Wide {
   static constexpr bool PAIR = MODE == 0;
@@ -76,13 +79,13 @@ struct Wide {
   static constexpr int TILE = kKeys * D * 2;  // bytes of a stage
   static constexpr int HALF = kKeys * 128;    // 64 elements of every row
   static constexpr int NS = F16 ? (D == 128 ? (PAIR ? 4 : 5) : 8) : (D == 128 ? 2 : 4);
-  static constexpr int RS = F16 ? 0 : (D == 128 && MODE != 1 ? 4 : 6);  // raw tiles
+  static constexpr int RS = F16 ? 0 : (D == 128 && PAIR ? 4 : 6);  // raw tiles
   static constexpr int RAW = kKeys * D;
   static constexpr int Q_OFF = 0;
   static constexpr int ST_OFF = Q_OFF + QT * kRows * D * 2;
   static constexpr int RAW_OFF = ST_OFF + NS * TILE;
   static constexpr int SC_OFF = RAW_OFF + RS * RAW;  // 8-bit: k scale', log2 v, 1 / v
-  static constexpr int CB_OFF = SC_OFF + (F16 ? 0 : 3 * kMeta * kKeys * 4);
+  static constexpr int CB_OFF = SC_OFF + (F16 ? 0 : 3 * kScales * kKeys * 4);
   static constexpr int BYTES = CB_OFF + (SPLIT > 1 ? 2 * kRows * kCopyPitch * 4 : 0);  // rows' copies added
   static constexpr int SMEM = BYTES + 1024;   // room to align the base
   static_assert(SMEM <= 227 * 1024 - 4096, "static shared memory needs room too");
@@ -416,10 +419,10 @@ __global__ void __launch_bounds__(Wide<D, TYPE, MODE>::THREADS, 1)
           lv = 0.0f, rv = 1.0f;
           atomicOr(&bad_of[t.bad][(j >> 5) & 1], 1u << (j & 31));
         }
-        float* f = scales + t.meta * kKeys + ct;
+        float* f = scales + t.meta % kScales * kKeys + ct;
         f[0] = sc[0] * cs;
-        f[kMeta * kKeys] = lv;
-        f[2 * kMeta * kKeys] = rv;
+        f[kScales * kKeys] = lv;
+        f[2 * kScales * kKeys] = rv;
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -695,9 +698,9 @@ __global__ void __launch_bounds__(Wide<D, TYPE, MODE>::THREADS, 1)
           const int64_t pos0 = (int64_t)(w.u0 + i) * kKeys;
           const uint32_t there = *(volatile uint32_t*)&there_of[slot];
           const bool edge = pos0 + kKeys > si.ctx || there != 0xFFFFu;
-          const float4* ksc = reinterpret_cast<const float4*>(scales + slot * kKeys);
-          const float4* lvs = ksc + kMeta * kKeys / 4;
-          const float4* rvs = lvs + kMeta * kKeys / 4;
+          const float4* ksc = reinterpret_cast<const float4*>(scales + slot % kScales * kKeys);
+          const float4* lvs = ksc + kScales * kKeys / 4;
+          const float4* rvs = lvs + kScales * kKeys / 4;
           // what the row sees of positions 32 y .. of an edge tile
           auto sees = [&](int y) {
             const int64_t f = pos0 - si.ctx + 32 * y;  // node number of the first
