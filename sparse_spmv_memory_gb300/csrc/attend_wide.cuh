@@ -237,20 +237,20 @@ __global__ void __launch_bounds__(Wide<D, TYPE, MODE>::THREADS, 1)
     regs_down<W::OTHER_REGS>();
     const int lw = warp - kLoadWarp, lt = lw * 32 + lane;
     constexpr int LT = W::LW * 32;
-    const int page_rows = min(1 << p.c.page_shift, kKeys);  // rows of a box
-    const int boxes = kKeys / page_rows;                    // of a tile
+    const int box_shift = min(p.c.page_shift, 7);  // a box: a page's rows, at most a tile's
+    const int page_rows = 1 << box_shift, boxes = kKeys >> box_shift;
     int c = 0;  // positions of the ring so far
-    int item_no = 0, looked = 0;
+    int item_no = 0, tile_no = 0, looked = 0;
     bool ok = true;
-    struct Tile {     // what the ring's position c holds
-      int64_t pos0;   // its first position
-      RowAt at;       // lane l < 16: its l-th group of 8 rows,
-      int page, row;  // in this page at this row (of all heads')
-      uint32_t there; // groups that are there
-      int left;       // rows before the sequence's end
-      bool edge;      // has nodes, or absent rows
-      int node0;      // node number of its first row (far below 0: none near)
-      int bad, meta;  // slots
+    struct Tile {      // a tile of an item; lane l has box l
+      int page, row;   // the box's page and first row in it (of all heads')
+      bool on;         // it is there
+      int have;        // boxes that are
+      uint32_t there;  // groups of 8 rows that are there
+      int left;        // rows before the sequence's end
+      bool edge;       // has nodes, or absent rows
+      int node0;       // node number of its first row (far below 0: none near)
+      int bad, meta;   // slots
     };
     auto note = [&](const Tile& t, bool first) {  // a K tile's slots (one warp)
       if (lane == 0) {
@@ -277,28 +277,23 @@ __global__ void __launch_bounds__(Wide<D, TYPE, MODE>::THREADS, 1)
       if (c >= W::NS && !wait_warp(empty(st), (c / W::NS - 1) & 1)) return false;
       const uint32_t dst = sT + st * W::TILE;
       if (!v && lw == 0) note(t, first);
-      // box l: the page rows of group l * page_rows / 8, for lane l < boxes
-      const int group = (lane * page_rows >> 3) & 15;
-      const int page = __shfl_sync(0xFFFFFFFFu, t.page, group), row = __shfl_sync(0xFFFFFFFFu, t.row, group);
-      const bool on = lane < boxes && ((t.there >> group) & 1u);
-      const int have = __popc(__ballot_sync(0xFFFFFFFFu, on));
       const bool look = v && t.edge;  // absent rows are to be zeros, nodes' rows are looked at
       const uint32_t bar = look ? rfull(0) : full(st);
       if (lw == 0) {
-        if (lane == 0 && (have || !look)) mbar_arrive_expect_tx(bar, have * page_rows * D * 2);
+        if (lane == 0 && (t.have || !look)) mbar_arrive_expect_tx(bar, t.have * page_rows * D * 2);
         __syncwarp();
-        if (on) {
+        if (t.on) {
 #pragma unroll
           for (int hf = 0; hf < D / 64; ++hf)
-            tma_load_3d(dst + hf * W::HALF + lane * page_rows * 128, v ? &tm_v : &tm_k, hf * 64, row, page,
-                        bar);
+            tma_load_3d(dst + hf * W::HALF + lane * page_rows * 128, v ? &tm_v : &tm_k, hf * 64, t.row,
+                        t.page, bar);
         }
         __syncwarp();
       } else if (!look && lane == 0) {
         mbar_arrive(full(st));
       }
       if (look) {
-        if (have && !wait_warp(bar, looked++ & 1)) return false;
+        if (t.have && !wait_warp(bar, looked++ & 1)) return false;
         constexpr int PR = D / 8;
         for (int id = lt; id < kKeys * PR; id += LT) {
           const int r = id / PR, ch = id % PR;
@@ -338,18 +333,20 @@ __global__ void __launch_bounds__(Wide<D, TYPE, MODE>::THREADS, 1)
         return true;
       }
       if (!v) note(*t, first);
-      const int group = (lane * page_rows >> 3) & 15;
-      const int64_t code = __shfl_sync(0xFFFFFFFFu, t->at.code, group);
-      const bool on = lane < boxes && code >= 0;
-      const int have = __popc(__ballot_sync(0xFFFFFFFFu, on));
-      if (lane < 16) raw_scales[st][lane] = t->at.scale;
+      if (!v) {  // where the scales of lane l's group of 8 rows are
+        const int box = (lane * 8 >> box_shift) & 15, in = (lane * 8) & (page_rows - 1);
+        const int page = __shfl_sync(0xFFFFFFFFu, t->page, box), row = __shfl_sync(0xFFFFFFFFu, t->row, box);
+        if (lane < 16)
+          raw_scales[st][lane] = (t->there >> lane) & 1u ? page * p.c.scale_page_stride + row + in : -1;
+      }
       if (lane == 0) raw_of[st] = RawTile{v, t->edge, 0, t->left, t->node0, t->there, t->bad, t->meta};
       __syncwarp();
-      if (lane == 0) mbar_arrive_expect_tx(rfull(st), have * page_rows * D);
+      if (lane == 0) mbar_arrive_expect_tx(rfull(st), t->have * page_rows * D);
       __syncwarp();
-      if (on)
-        bulk_load(base + W::RAW_OFF + st * W::RAW + lane * page_rows * D, (v ? p.c.v : p.c.k) + code,
-                  page_rows * D, rfull(st));
+      if (t->on)
+        bulk_load(base + W::RAW_OFF + st * W::RAW + lane * page_rows * D,
+                  (v ? p.c.v : p.c.k) + t->page * p.c.page_stride + (int64_t)t->row * D, page_rows * D,
+                  rfull(st));
       __syncwarp();
       return true;
     };
@@ -434,77 +431,50 @@ __global__ void __launch_bounds__(Wide<D, TYPE, MODE>::THREADS, 1)
     };
 
     // The positions of the ring in order: K0, V0, K1, V1, ... for PAIR, else
-    // K0, K1, V0, K2, V1, ..., as the MMA thread takes them.  `Walk` yields them
-    // one by one.
-    struct Walk {
-      Sched sched;
+    // K0, K1, V0, K2, V1, ..., as the MMA thread takes them.
+    if (F16 || lw == 0) {
       Span w;
       SeqInfo si;
-      int i, n;       // next K tile
-      int vi;         // next V tile
-      int32_t entry;  // the next K tile's page, of the lane's group
-      Tile k, last;   // tiles whose V is still to come: k the newer
-      int tiles, items;
-      bool open;
-    };
-    auto look_up = [&](const Walk& x, int i) {
-      const int64_t pos = (int64_t)(x.w.u0 + i) * kKeys + 8 * lane;
-      return i < x.n && lane < 16 && pos < x.si.len
-                 ? p.table[(int64_t)x.w.s * p.ld_table + (pos >> p.c.page_shift)]
-                 : -1;
-    };
-    auto start = [&](Walk& x) {
-      x.open = x.sched.next(p, x.w, x.si);
-      if (!x.open) return;
-      x.n = x.w.u1 - x.w.u0;
-      x.i = x.vi = 0;
-      x.entry = look_up(x, 0);
-    };
-    // The next position: false when there is none.  first: an item's first.
-    auto step = [&](Walk& x, bool& v, bool& first) {
-      if (x.open && x.i == x.n && x.vi == x.n) {
-        ++x.items;
-        start(x);
-      }
-      if (!x.open) return false;
-      const int lead = PAIR ? 0 : 1;
-      v = x.i == x.n || x.i - x.vi > lead;
-      first = !v && x.i == 0;
-      if (v) {
-        ++x.vi;
-        return true;
-      }
-      x.last = x.k;
-      Tile& t = x.k;
-      t.pos0 = (int64_t)(x.w.u0 + x.i) * kKeys;
-      t.at = group_at<D>(p, x.entry, x.w.h, t.pos0 + 8 * (lane & 15));
-      t.page = x.entry;
-      t.row = (x.w.h << p.c.page_shift) + (int)((t.pos0 + 8 * (lane & 15)) & ((1 << p.c.page_shift) - 1));
-      t.there = __ballot_sync(0xFFFFFFFFu, lane < 16 && t.at.code >= 0);
-      t.left = (int)min((int64_t)kKeys, x.si.len - t.pos0);
-      t.edge = t.pos0 + kKeys > x.si.ctx || t.there != 0xFFFFu;
-      t.node0 = (int)max(t.pos0 - x.si.ctx, (int64_t)-(1 << 20));
-      t.bad = x.items % kBad;
-      t.meta = x.tiles++ % kMeta;
-      ++x.i;
-      x.entry = look_up(x, x.i);
-      return true;
-    };
-    // which tile a V position belongs to: the newest K tile, or the one before
-    auto v_tile = [&](const Walk& x) -> const Tile& { return x.vi == x.i ? x.k : x.last; };
-
-    if (F16 || lw == 0) {
-      Walk x;
-      x.sched = sched;
-      x.tiles = x.items = 0;
-      start(x);
-      bool v, first;
-      while (ok && step(x, v, first)) {
-        item_no = x.items;
-        if constexpr (F16)
-          ok = emit16(v, v ? v_tile(x) : x.k, first);
-        else
-          ok = fetch8(v, v ? &v_tile(x) : &x.k, first);
+      while (ok && sched.next(p, w, si)) {
+        const int n = w.u1 - w.u0;
+        const int32_t* table = p.table + (int64_t)w.s * p.ld_table;
+        auto look_up = [&](int i) {  // the page of the lane's box
+          const int64_t pos = (int64_t)(w.u0 + i) * kKeys + (lane << box_shift);
+          return i < n && lane < boxes && pos < si.len ? table[pos >> p.c.page_shift] : -1;
+        };
+        int32_t entry = look_up(0);
+        Tile now, last;
+        for (int i = 0; i <= n && ok; ++i) {
+          if (i < n) {
+            const int64_t pos0 = (int64_t)(w.u0 + i) * kKeys;
+            now.page = entry;
+            now.on = entry >= 0 && entry < p.c.pages;
+            now.row = (w.h << p.c.page_shift) +
+                      (int)((pos0 + (lane << box_shift)) & ((1 << p.c.page_shift) - 1));
+            entry = look_up(i + 1);
+            const uint32_t on = __ballot_sync(0xFFFFFFFFu, now.on);
+            now.have = __popc(on);
+            now.there = __ballot_sync(0xFFFFFFFFu, lane < 16 && ((on >> (lane * 8 >> box_shift)) & 1u));
+            now.left = (int)min((int64_t)kKeys, si.len - pos0);
+            now.edge = pos0 + kKeys > si.ctx || now.there != 0xFFFFu;
+            now.node0 = (int)max(pos0 - si.ctx, (int64_t)-(1 << 20));
+            now.bad = item_no % kBad;
+            now.meta = tile_no++ % kMeta;
+            if constexpr (F16)
+              ok = emit16(false, now, i == 0);
+            else
+              ok = fetch8(false, &now, i == 0);
+            if (PAIR) last = now;
+          }
+          if (ok && (PAIR ? i < n : i > 0)) {
+            if constexpr (F16)
+              ok = emit16(true, last, false);
+            else
+              ok = fetch8(true, &last, false);
+          }
+          if (!PAIR) last = now;
+        }
+        ++item_no;
       }
       if (!F16)  // a last position for each group
         for (int i = 0; i < 2 && ok; ++i) ok = fetch8(false, nullptr, false);
