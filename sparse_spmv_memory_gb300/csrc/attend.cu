@@ -395,6 +395,7 @@ __global__ void __launch_bounds__(NW * 32, 1) attend_narrow_kernel(AttendParams 
           sm[warp][r] = m[mt][k];
           sl[warp][r] = sum;
         }
+        if (r >= rows) continue;
         float* dst = so + ((size_t)warp * ROWS + r) * PITCH;
         // n-tile t, columns 2q, 2q+1 are elements (D/8) 2q + t and (D/8)(2q+1) + t
 #pragma unroll

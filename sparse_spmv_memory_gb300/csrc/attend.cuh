@@ -7,7 +7,9 @@
 // units of all items, one after the other, are cut evenly over the blocks
 // (lengths are known on the device only, and the longest sequence must not
 // decide).  So a block has some items whole, and at its range's two ends parts
-// of items.  A part is stored as unnormalised sums with their maxima in the
+// of items.  Where there are at least two blocks an item, an item's last block is
+// left short instead, so that no block has two items (a second one costs a block
+// its start-up again: 3 to 5 us).  A part is stored as unnormalised sums with their maxima in the
 // block's slot, and the block that completes an item's count of parts joins
 // them in block order: the result does not depend on which block that is.
 #pragma once
@@ -79,6 +81,7 @@ __device__ __forceinline__ int64_t div_units(int64_t a, int64_t b) {
 template <int ROWS, int UK, int NT>
 struct Schedule {
   int64_t per;         // units of a block (the last one's may be fewer)
+  bool padded;         // items begin at multiples of it
   int64_t begin, end;  // this block's
   int64_t at;          // where the walk is
   int64_t s_start;     // first unit of sequence s
@@ -97,26 +100,56 @@ struct Schedule {
     const SeqInfo q = seq_info(p, i);
     return (int64_t)units_of(q) * tiles_of(p, q) * p.c.kv_heads;
   }
-  __device__ __forceinline__ bool take(int64_t total, int min_units) {
-    per = max(div_units(total + gridDim.x - 1, gridDim.x), (int64_t)min_units);
+  __device__ __forceinline__ int64_t per_of(int64_t total, int min_units) const {
+    return max(div_units(total + gridDim.x - 1, gridDim.x), (int64_t)min_units);
+  }
+  __device__ __forceinline__ bool take(int64_t total) {
     begin = at = per * blockIdx.x;
     end = min(begin + per, total);
     return begin < end;
+  }
+  static __device__ __forceinline__ int64_t warp_total(int64_t v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
   }
 
   // All threads of the block; false: nothing to do.
   __device__ __forceinline__ bool init(const AttendParams& p, int min_units) {
     rt_max = (p.max_nodes * (p.q_heads / p.c.kv_heads) + ROWS - 1) / ROWS;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    padded = false;
     if (p.seqs <= 32) {  // every warp by itself: no barrier
-      const int64_t v = seq_units(p, lane);
+      int nu = 0, items = 0;
+      if (lane < p.seqs) {
+        const SeqInfo q = seq_info(p, lane);
+        nu = units_of(q);
+        items = tiles_of(p, q) * p.c.kv_heads;
+      }
+      const int64_t all = warp_total((int64_t)nu * items), n_items = warp_total(items);
+      per = per_of(all, min_units);
+      if (2 * n_items <= gridDim.x && all > 0) {
+        // the fewest units with which every item has blocks of its own
+        auto blocks = [&](int64_t u) { return warp_total((int64_t)items * (int)div_units(nu + u - 1, u)); };
+        padded = true;
+        if (blocks(per) > gridDim.x) {
+          int64_t lo = per + 1, hi = max(lo, div_units(all + gridDim.x - n_items - 1, gridDim.x - n_items));
+          while (lo < hi) {
+            const int64_t mid = (lo + hi) >> 1;
+            if (blocks(mid) <= gridDim.x) hi = mid;
+            else lo = mid + 1;
+          }
+          per = hi;
+        }
+      }
+      const int64_t v = (padded ? div_units(nu + per - 1, per) * per : (int64_t)nu) * items;
       int64_t x = v;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
         if (lane >= o) x += y;
       }
-      if (!take(__shfl_sync(0xFFFFFFFFu, x, 31), min_units)) return false;
+      if (!take(__shfl_sync(0xFFFFFFFFu, x, 31))) return false;
       const uint32_t mine = __ballot_sync(0xFFFFFFFFu, x > begin);
       s = __ffs(mine) - 1;
       s_start = __shfl_sync(0xFFFFFFFFu, x - v, s);
@@ -133,7 +166,8 @@ struct Schedule {
     __syncthreads();
     int64_t total = 0;
     for (int w = 0; w < NT / 32; ++w) total += sums[w];
-    if (!take(total, min_units)) return false;
+    per = per_of(total, min_units);
+    if (!take(total)) return false;
     if (warp == 0) {  // the sequence that has unit `begin`
       int64_t before = 0;
       for (int c = 0; c < p.seqs; c += 32) {
@@ -165,25 +199,27 @@ struct Schedule {
   __device__ __forceinline__ bool next(const AttendParams& p, Span& w, SeqInfo& q) {
     if (at >= end) return false;
     int nu, tiles;
+    int64_t step;  // from an item's first unit to the next one's
     for (;;) {
       q = seq_info(p, s);
       nu = units_of(q);
       tiles = tiles_of(p, q);
-      const int64_t all = (int64_t)nu * tiles * p.c.kv_heads;
+      step = padded ? div_units(nu + per - 1, per) * per : nu;
+      const int64_t all = step * tiles * p.c.kv_heads;
       if (at < s_start + all) break;
       s_start += all;
       ++s;
     }
-    const int in = (int)div_units(at - s_start, nu);  // item of the sequence
+    const int in = (int)div_units(at - s_start, step);  // item of the sequence
     w.s = s;
     w.h = in / tiles;
     w.rt = in % tiles;
     w.nu = nu;
-    w.start = s_start + (int64_t)in * nu;
+    w.start = s_start + in * step;
     w.u0 = (int)(at - w.start);
     w.u1 = (int)min((int64_t)nu, end - w.start);
     w.item = ((int64_t)s * p.c.kv_heads + w.h) * rt_max + w.rt;
-    at = w.start + w.u1;
+    at = padded ? end : w.start + w.u1;
     return true;
   }
 };
