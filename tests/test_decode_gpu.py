@@ -617,3 +617,142 @@ def test_verify_keeps_the_targets_distribution(nm, drafted):
     f = np.bincount(kept, minlength=V) / S
     assert (np.abs(f - p) < 5 * np.sqrt(p * (1 - p) / S)).all(), (f, p)
     assert 0.2 < (count > 1).mean() < 0.95
+
+
+# ---- wide batches, long vocabularies, the calls' own refusals -------------------------
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("nodes,q_heads", [(1, 8), (6, 8), (14, 8), (20, 16), (40, 16)])
+def test_attention_many_sequences(nm, kind, nodes, q_heads):
+    """More sequences than a warp's lanes, all of their own length, one long, some
+    without nodes: rows 4 .. 320 of 2 key heads, every kernel."""
+    rnd = random.Random(nodes)
+    ctx = [rnd.choice([0, 1, 17, 64, 127, 130]) for _ in range(45)] + [900]
+    ns = [rnd.randint(0, nodes) for _ in range(45)] + [nodes]
+    Batch(kind, ctx, ns, q_heads, 2, 64, 8, seed=nodes).check(nm, f"{kind} 46 sequences")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("nodes", [3, 5, 9, 17, 33, 64])
+def test_attention_rows_of_every_tile(nm, kind, nodes):
+    """Rows just above 16, 32, 64, 128, 256 a key head: every row tile and its last
+    rows; the maximum grows over the positions, so that sums are rescaled."""
+    b = Batch(kind, [1300], [nodes], 7, 1, 128, 32, seed=nodes)
+    order = torch.zeros(b.k.shape[0], dtype=torch.int64)
+    order[b.table[0].clamp_min(0).long()] = torch.arange(b.table.shape[1])
+    grow = (0.2 + 0.15 * order.float())[:, None, None]
+    if b.ks is None:
+        b.k = (b.k.float() * grow[..., None]).half()
+    else:
+        b.ks = b.ks * grow
+    b.check(nm, f"{kind} {7 * nodes} rows")
+    b.scale = -b.scale
+    b.check(nm, f"{kind} {7 * nodes} rows, negative scale")
+
+
+@pytest.mark.parametrize("drafted", [True, False])
+@pytest.mark.parametrize("vocab", [131073, 140001, 300007])
+def test_verify_long_vocabularies(nm, drafted, vocab):
+    """Beyond what a cluster's threads hold with 16 elements each, and with 32."""
+    case = verify_case(vocab, 2, 6, vocab, drafted, 0.8, False)
+    same(run_verify(nm, case, 6, 0.8), case[7])
+    case = verify_case(vocab, 2, 6, vocab, drafted, 0.0, True)
+    same(run_verify(nm, case, 6, 0.0), case[7])
+
+
+def test_verify_many_sequences(nm):
+    """More sequences than run at the same time, every one as in the reference."""
+    case = verify_case(9, 200, 5, 33000, True, 0.9, False)
+    same(run_verify(nm, case, 5, 0.9), case[7])
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_append_and_read_interleaved_pages(nm, kind):
+    """K and V pages side by side in one buffer, written on a stream of its own."""
+    x, pos, slots, k, v, ks, vs = append_case(kind, 21, 4, 2, 64, 8, seed=8)
+    raw = torch.zeros((k.shape[0], 2) + k.shape[1:], dtype=torch.uint8 if ks is not None else k.dtype,
+                      device="cuda").view(k.dtype)
+    k2, v2 = raw[:, 0], raw[:, 1]
+    ks2 = vs2 = None
+    if ks is not None:
+        sc = torch.zeros((k.shape[0], 2) + ks.shape[1:], device="cuda")
+        ks2, vs2 = sc[:, 0], sc[:, 1]
+    freq = nm.nm_rope_inv_freq(64)
+    dx, dp, ds = x.view(21, -1).cuda(), pos.cuda(), slots.cuda()
+    nm.nm_rope_append(dx, k, v, dp, ds, freq, 4, k_scale=ks, v_scale=vs)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    nm.nm_rope_append(dx, k2, v2, dp, ds, freq, 4, k_scale=ks2, v_scale=vs2, stream=side)
+    got = nm.nm_cache_read(k2, v2, ds, k_scale=ks2, v_scale=vs2, stream=side)
+    side.synchronize()
+    want = nm.nm_cache_read(k, v, ds, k_scale=ks, v_scale=vs)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert torch.equal(k2.contiguous().view(torch.uint8), k.view(torch.uint8))
+
+
+def test_binding_refusals(nm):
+    """Types, shapes and layouts that the marshalling refuses, and a status of the
+    library as its exception."""
+    b = Batch("e4m3", [40], [3], 8, 2, 64, 16)
+    k, v, ks, vs, q = cuda(b.k, b.v, b.ks, b.vs, b.q)
+    table, ctx, start = b.table.cuda(), torch.tensor([40], dtype=torch.int32).cuda(), \
+        torch.tensor([0, 3], dtype=torch.int32).cuda()
+
+    def attend(q=q, k=k, v=v, table=table, ctx=ctx, start=start, n=3, **kw):
+        kw = dict(dict(k_scale=ks, v_scale=vs), **kw)
+        return nm.nm_tree_attention(q, k, v, table, ctx, start, n, **kw)
+    attend()
+    for bad in (dict(q=q.float()), dict(q=q.transpose(0, 1)), dict(k=k.view(torch.uint8)),
+                dict(k=k[:, :, ::2]), dict(table=table.long()), dict(ctx=ctx.long()),
+                dict(start=start[:1]), dict(k_scale=None), dict(v_scale=vs.half()),
+                dict(tree_mask=torch.zeros(2, dtype=torch.int64, device="cuda")),
+                dict(out=torch.empty((3, 4, 64), dtype=torch.float16, device="cuda")),
+                dict(lse=torch.empty(7, device="cuda")), dict(q=q.cpu())):
+        with pytest.raises(ValueError):
+            attend(**bad)
+    with pytest.raises(TypeError):
+        attend(q=None)
+    with pytest.raises(nm.NMError) as e:
+        attend(n=65)
+    assert e.value.status == 2
+    with pytest.raises(nm.NMError) as e:
+        attend(workspace=torch.zeros(16, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == 5
+    with pytest.raises(nm.NMError) as e:
+        attend(scale=float("inf"))
+    assert e.value.status == 2
+    slots = torch.zeros(3, dtype=torch.int64, device="cuda")
+    with pytest.raises(ValueError):
+        nm.nm_cache_read(k, v, slots.int(), ks, vs)
+    with pytest.raises(ValueError):
+        nm.nm_rope_append(q.view(3, -1)[:, :-64], k, v, start, slots, ctx.float(), 8, ks, vs)
+    logits = torch.zeros((3, 10), device="cuda")
+    ids = torch.zeros(3, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        nm.nm_tree_verify(logits.double(), ids, ids, start, 3)
+    with pytest.raises(ValueError):
+        nm.nm_tree_verify(logits, ids, ids, start, 3, draft=logits[:, :5])
+    with pytest.raises(nm.NMError) as e:  # sampling without random numbers
+        nm.nm_tree_verify(logits, ids, ids, start, 3)
+    assert e.value.status == 1
+
+
+@pytest.mark.parametrize("cache", KINDS)
+def test_example_decodes_as_one_token_at_a_time(nm, cache):
+    """Speculative decoding at temperature 0 gives the tokens of plain decoding, and
+    some drafted tokens are accepted; at a temperature it runs."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "speculative_decode.py")
+    spec = importlib.util.spec_from_file_location("speculative_decode", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    plain, none = ex.decode(2, cache, 20, 0.0, 3)
+    out, accepted = ex.decode(2, cache, 20, 0.0, 3, plain)
+    assert out == plain and none == 0 and accepted > 5
+    warm, _ = ex.decode(2, cache, 12, 1.0, 3, plain)
+    assert len(warm) == 12 and all(0 <= t < ex.VOCAB for t in warm)
+
+
+def test_no_bounded_wait_gave_up(nm):
+    assert nm.nm_wait_timeouts() == 0
