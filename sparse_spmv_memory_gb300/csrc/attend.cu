@@ -67,10 +67,12 @@ __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
 //     column t of MMA n-tile t.  Two rows' halves are paired by byte permutes.
 // No shared memory, no barrier, until a block's warps join their sums.  A warp
 // takes every NW-th unit of the block's part.
-template <int D, int TYPE, int MT>
+constexpr int kNarrowRows = 16, kNarrowWarps = 8;
+
+template <int D, int TYPE>
 struct Narrow {
   static constexpr bool F16 = TYPE == kCacheFp16;
-  static constexpr int NG = F16 || MT > 1 ? 2 : 4;      // groups of 8 positions in a unit
+  static constexpr int NG = F16 ? 2 : 4;      // groups of 8 positions in a unit
   static constexpr int UK = 8 * NG;           // positions of a unit
   static constexpr int KS = D / 16;           // MMA k steps of a score
   static constexpr int NT = D / 8;            // n-tiles of an output row
@@ -82,15 +84,15 @@ struct Narrow {
   }
 };
 
-template <int D, int TYPE, int MT, int NW>
-__global__ void __launch_bounds__(NW * 32, 1) attend_narrow_kernel(AttendParams p) {
-  using N = Narrow<D, TYPE, MT>;
+template <int D, int TYPE>
+__global__ void __launch_bounds__(kNarrowWarps * 32, 1) attend_narrow_kernel(AttendParams p) {
+  using N = Narrow<D, TYPE>;
   constexpr bool F16 = N::F16;
-  constexpr int ROWS = 16 * MT, NTH = NW * 32, PITCH = D + 4;
+  constexpr int ROWS = kNarrowRows, NW = kNarrowWarps, NTH = NW * 32, PITCH = D + 4;
   using Sched = Schedule<ROWS, N::UK, NTH>;
   extern __shared__ __align__(16) uint8_t dyn[];
   float* so = reinterpret_cast<float*>(dyn);                     // [NW][ROWS][PITCH]
-  __shared__ uint4 sq[MT][N::KS][32];                            // A fragments of the queries
+  __shared__ uint4 sq[N::KS][32];                            // A fragments of the queries
   __shared__ uint64_t smask[ROWS];
   __shared__ float sm[NW][ROWS], sl[NW][ROWS], sf[NW][ROWS];
   __shared__ float row_m[ROWS], row_l[ROWS];
@@ -103,27 +105,26 @@ __global__ void __launch_bounds__(NW * 32, 1) attend_narrow_kernel(AttendParams 
   const Heads heads(G);
   const float cs = p.scale * kLog2e;
   int* counters = reinterpret_cast<int*>(p.workspace);
-  float* slots = reinterpret_cast<float*>(
-      p.workspace + attend_counter_bytes((int64_t)p.seqs * p.c.kv_heads * sched.rt_max));
+  float* slots = reinterpret_cast<float*>(p.workspace + attend_counter_bytes(gridDim.x));
 
   Span w;
   SeqInfo si;
   while (sched.next(p, w, si)) {
     const int rows = min(ROWS, si.n * G - w.rt * ROWS);
     __syncthreads();  // the shared arrays of the last item are free
-    for (int i = threadIdx.x; i < MT * N::KS * 32; i += NTH) {
-      const int mt = i / (N::KS * 32), ks = i / 32 % N::KS, ln = i % 32;
+    for (int i = threadIdx.x; i < N::KS * 32; i += NTH) {
+      const int ks = i / 32, ln = i % 32;
       const int e = N::k_elem(ks, ln & 3);
       uint2 v[2];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const int r = 16 * mt + (ln >> 2) + 8 * k, rr = w.rt * ROWS + r;
+        const int r = (ln >> 2) + 8 * k, rr = w.rt * ROWS + r;
         v[k] = make_uint2(0, 0);
         if (r < rows)
           v[k] = *reinterpret_cast<const uint2*>(p.q + (int64_t)(si.first + heads.node(rr)) * p.ldq +
                                                  (w.h * G + heads.head(rr)) * D + e);
       }
-      sq[mt][ks][ln] = make_uint4(v[0].x, v[1].x, v[0].y, v[1].y);
+      sq[ks][ln] = make_uint4(v[0].x, v[1].x, v[0].y, v[1].y);
     }
     for (int r = threadIdx.x; r < ROWS; r += NTH) {
       const int node = heads.node(w.rt * ROWS + r);
@@ -131,16 +132,13 @@ __global__ void __launch_bounds__(NW * 32, 1) attend_narrow_kernel(AttendParams 
     }
     __syncthreads();
 
-    float o[MT][N::NT][4], m[MT][2], l[MT][2];
+    float o[N::NT][4], m[2], l[2];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+    for (int t = 0; t < N::NT; ++t)
 #pragma unroll
-      for (int t = 0; t < N::NT; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[mt][t][i] = 0.0f;
-      m[mt][0] = m[mt][1] = -INFINITY;
-      l[mt][0] = l[mt][1] = 0.0f;
-    }
+      for (int i = 0; i < 4; ++i) o[t][i] = 0.0f;
+    m[0] = m[1] = -INFINITY;
+    l[0] = l[1] = 0.0f;
     const int32_t* table = p.table + (int64_t)w.s * p.ld_table;
     uint32_t kr[N::NG][N::KW], vr[N::NG][2][N::VW];
     float ksc[N::NG][2], vsc[N::NG][2];
@@ -206,31 +204,25 @@ __global__ void __launch_bounds__(NW * 32, 1) attend_narrow_kernel(AttendParams 
 #pragma unroll
       for (int c = 0; c < N::NG; ++c) there |= at[c].code >= 0 ? 1u << c : 0u;
       // ---- scores: row g (i = 0, 1) and g + 8 (2, 3) of positions 8c + 2q, + 1
-      float s[MT][N::NG][4];
+      float s[N::NG][4];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int c = 0; c < N::NG; ++c)
 #pragma unroll
-        for (int c = 0; c < N::NG; ++c)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[mt][c][i] = 0.0f;
+        for (int i = 0; i < 4; ++i) s[c][i] = 0.0f;
 #pragma unroll
       for (int ks = 0; ks < N::KS; ++ks) {
-        uint32_t b[N::NG][2];
+        const uint4 f = sq[ks][lane];
+        const uint32_t a[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
         for (int c = 0; c < N::NG; ++c) {
+          uint32_t b0, b1;
           if (F16) {
-            b[c][0] = kr[c][2 * ks];
-            b[c][1] = kr[c][2 * ks + 1];
+            b0 = kr[c][2 * ks];
+            b1 = kr[c][2 * ks + 1];
           } else {
-            widen4<TYPE>(kr[c][ks], b[c][0], b[c][1]);
+            widen4<TYPE>(kr[c][ks], b0, b1);
           }
-        }
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          const uint4 f = sq[mt][ks][lane];
-          const uint32_t a[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-          for (int c = 0; c < N::NG; ++c) mma16816(s[mt][c], a, b[c][0], b[c][1]);
+          mma16816(s[c], a, b0, b1);
         }
       }
       float vs[N::NG][2], lv[N::NG][2];
@@ -239,11 +231,8 @@ __global__ void __launch_bounds__(NW * 32, 1) attend_narrow_kernel(AttendParams 
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const float f = F16 ? cs : cs * ksc[c][i];
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            s[mt][c][i] *= f;
-            s[mt][c][2 + i] *= f;
-          }
+          s[c][i] *= f;
+          s[c][2 + i] *= f;
           if (!F16) {
             vs[c][i] = vsc[c][i];
             lv[c][i] = fmaxf(log2_fast(vsc[c][i]), -40.0f);
@@ -256,72 +245,63 @@ __global__ void __launch_bounds__(NW * 32, 1) attend_narrow_kernel(AttendParams 
       }
       // ---- masks: the last units have the nodes, or end
       const bool edge = pos0 + N::UK > si.ctx || there != (1u << N::NG) - 1u;
-      uint32_t seen[MT][2];  // bit 2c + i: row sees position 8c + 2q + i
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) seen[mt][0] = seen[mt][1] = ~0u;
+      uint32_t seen[2] = {~0u, ~0u};  // bit 2c + i: row sees position 8c + 2q + i
       if (edge) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const uint64_t bits = smask[16 * mt + g + 8 * k];
-            uint32_t see = 0;
-#pragma unroll
-            for (int c = 0; c < N::NG; ++c)
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const int64_t pos = pos0 + 8 * c + 2 * q + i, j = pos - si.ctx;
-                const bool on = ((there >> c) & 1u) && pos < si.len &&
-                                (j < 0 || ((bits >> (j & 63)) & 1ull));
-                see |= on ? 1u << (2 * c + i) : 0u;
-                if (!on) s[mt][c][2 * k + i] = -INFINITY;
-              }
-            seen[mt][k] = see;
-          }
-      }
-      // ---- weights
-      uint32_t a[MT][N::NG / 2][4];
-      float keep[MT][2];
-      bool grew = false;
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
         for (int k = 0; k < 2; ++k) {
-          float top = m[mt][k];
+          const uint64_t bits = smask[g + 8 * k];
+          uint32_t see = 0;
 #pragma unroll
           for (int c = 0; c < N::NG; ++c)
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-              top = fmaxf(top, F16 ? s[mt][c][2 * k + i] : s[mt][c][2 * k + i] + lv[c][i]);
-          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-          keep[mt][k] = m[mt][k] == -INFINITY ? 0.0f : exp2_fast(m[mt][k] - top);
-          grew |= top != m[mt][k];
-          l[mt][k] *= keep[mt][k];
-          m[mt][k] = top;
-          const float base = top == -INFINITY ? 0.0f : top;
-#pragma unroll
-          for (int c = 0; c < N::NG; ++c) {
-            float e[2];
-#pragma unroll
             for (int i = 0; i < 2; ++i) {
-              e[i] = exp2_fast(s[mt][c][2 * k + i] - base);
-              l[mt][k] += e[i];
-              if (!F16) e[i] = (seen[mt][k] >> (2 * c + i)) & 1u ? e[i] * vs[c][i] : 0.0f;
+              const int64_t pos = pos0 + 8 * c + 2 * q + i, j = pos - si.ctx;
+              const bool on =
+                  ((there >> c) & 1u) && pos < si.len && (j < 0 || ((bits >> (j & 63)) & 1ull));
+              see |= on ? 1u << (2 * c + i) : 0u;
+              if (!on) s[c][2 * k + i] = -INFINITY;
             }
-            a[mt][c / 2][(c & 1) * 2 + k] = pack_half2(e[0], e[1]);
-          }
+          seen[k] = see;
         }
+      }
+      // ---- weights
+      uint32_t a[N::NG / 2][4];
+      float keep[2];
+      bool grew = false;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float top = m[k];
+#pragma unroll
+        for (int c = 0; c < N::NG; ++c)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) top = fmaxf(top, F16 ? s[c][2 * k + i] : s[c][2 * k + i] + lv[c][i]);
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+        keep[k] = m[k] == -INFINITY ? 0.0f : exp2_fast(m[k] - top);
+        grew |= top != m[k];
+        l[k] *= keep[k];
+        m[k] = top;
+        const float base = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+        for (int c = 0; c < N::NG; ++c) {
+          float e[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            e[i] = exp2_fast(s[c][2 * k + i] - base);
+            l[k] += e[i];
+            if (!F16) e[i] = (seen[k] >> (2 * c + i)) & 1u ? e[i] * vs[c][i] : 0.0f;
+          }
+          a[c / 2][(c & 1) * 2 + k] = pack_half2(e[0], e[1]);
+        }
+      }
       if (__any_sync(0xFFFFFFFFu, grew)) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int k = 0; k < 2; ++k)
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int t = 0; t < N::NT; ++t) {
-              o[mt][t][2 * k] *= keep[mt][k];
-              o[mt][t][2 * k + 1] *= keep[mt][k];
-            }
+          for (int t = 0; t < N::NT; ++t) {
+            o[t][2 * k] *= keep[k];
+            o[t][2 * k + 1] *= keep[k];
+          }
       }
       // ---- sums
       uint32_t bad = 0;  // bit 2c + i: the value row of position 8c + 2q + i is not finite
@@ -354,9 +334,7 @@ __global__ void __launch_bounds__(NW * 32, 1) attend_narrow_kernel(AttendParams 
           }
 #pragma unroll
           for (int x = 0; x < (F16 ? 2 : 4); ++x)
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-              mma16816(o[mt][j * (F16 ? 2 : 4) + x], a[mt][c2], b[x][0], b[x][1]);
+            mma16816(o[j * (F16 ? 2 : 4) + x], a[c2], b[x][0], b[x][1]);
         }
       }
       if (u + NW < w.u1) load_v(u + NW);
@@ -367,43 +345,38 @@ __global__ void __launch_bounds__(NW * 32, 1) attend_narrow_kernel(AttendParams 
         bad |= __shfl_xor_sync(0xFFFFFFFFu, bad, 8);
         bad |= __shfl_xor_sync(0xFFFFFFFFu, bad, 16);
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int k = 0; k < 2; ++k) {
+          uint32_t hit = bad & seen[k];
+          hit |= __shfl_xor_sync(0xFFFFFFFFu, hit, 1);
+          hit |= __shfl_xor_sync(0xFFFFFFFFu, hit, 2);
+          if (hit) {
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            uint32_t hit = bad & seen[mt][k];
-            hit |= __shfl_xor_sync(0xFFFFFFFFu, hit, 1);
-            hit |= __shfl_xor_sync(0xFFFFFFFFu, hit, 2);
-            if (hit) {
-#pragma unroll
-              for (int t = 0; t < N::NT; ++t)
-                o[mt][t][2 * k] = o[mt][t][2 * k + 1] = __uint_as_float(0x7FC00000u);
-            }
+            for (int t = 0; t < N::NT; ++t) o[t][2 * k] = o[t][2 * k + 1] = __uint_as_float(0x7FC00000u);
           }
+        }
       }
     }
 
     // ---- join the warps: every warp's sums, maxima and weights to shared memory
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float sum = l[mt][k];
-        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
-        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
-        const int r = 16 * mt + g + 8 * k;
-        if (q == 0) {
-          sm[warp][r] = m[mt][k];
-          sl[warp][r] = sum;
-        }
-        if (r >= rows) continue;
-        float* dst = so + ((size_t)warp * ROWS + r) * PITCH;
-        // n-tile t, columns 2q, 2q+1 are elements (D/8) 2q + t and (D/8)(2q+1) + t
-#pragma unroll
-        for (int t = 0; t < N::NT; ++t) {
-          dst[(D / 8) * 2 * q + t] = o[mt][t][2 * k];
-          dst[(D / 8) * (2 * q + 1) + t] = o[mt][t][2 * k + 1];
-        }
+    for (int k = 0; k < 2; ++k) {
+      float sum = l[k];
+      sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+      sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+      const int r = g + 8 * k;
+      if (q == 0) {
+        sm[warp][r] = m[k];
+        sl[warp][r] = sum;
       }
+      if (r >= rows) continue;
+      float* dst = so + ((size_t)warp * ROWS + r) * PITCH;
+      // n-tile t, columns 2q, 2q+1 are elements (D/8) 2q + t and (D/8)(2q+1) + t
+#pragma unroll
+      for (int t = 0; t < N::NT; ++t) {
+        dst[(D / 8) * 2 * q + t] = o[t][2 * k];
+        dst[(D / 8) * (2 * q + 1) + t] = o[t][2 * k + 1];
+      }
+    }
     __syncthreads();
     for (int r = threadIdx.x; r < ROWS; r += NTH) {
       float M = -INFINITY, tot = 0.0f;
@@ -455,7 +428,7 @@ __global__ void __launch_bounds__(NW * 32, 1) attend_narrow_kernel(AttendParams 
     // ---- join the blocks: the last one to store its part adds all of them
     const int64_t b0 = sched.block_of(w.start), b1 = sched.block_of(w.start + w.nu - 1);
     const int parts = (int)(b1 - b0 + 1);
-    if (!last_of_item(counters + w.item, parts)) continue;
+    if (!last_of_item(counters + b0, parts)) continue;
     float* factor = so;  // [parts][ROWS]
     auto part = [&](int y) {
       return slots + part_slot(b0 + y, sched.per, w.start) * attend_slot_floats(ROWS, D);
@@ -497,13 +470,10 @@ __global__ void __launch_bounds__(NW * 32, 1) attend_narrow_kernel(AttendParams 
   }
 }
 
-constexpr int narrow_warps(int) { return 8; }
-
-template <int D, int TYPE, int MT>
-cudaError_t narrow_one(const AttendParams& p, int sms, cudaStream_t stream) {
-  constexpr int NW = narrow_warps(MT);
-  constexpr size_t smem = (size_t)NW * 16 * MT * (D + 4) * sizeof(float);
-  auto* k = attend_narrow_kernel<D, TYPE, MT, NW>;
+template <int D, int TYPE>
+cudaError_t launch_narrow(const AttendParams& p, int sms, cudaStream_t stream) {
+  constexpr size_t smem = (size_t)kNarrowWarps * kNarrowRows * (D + 4) * sizeof(float);
+  auto* k = attend_narrow_kernel<D, TYPE>;
   static int done[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -513,47 +483,39 @@ cudaError_t narrow_one(const AttendParams& p, int sms, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     if (dev < 64) __atomic_store_n(&done[dev], 1, __ATOMIC_RELEASE);
   }
-  return launch_kernel(k, sms, NW * 32, smem, stream, kFlagPdl, p);
-}
-
-template <int D, int TYPE>
-cudaError_t narrow_mt(const AttendParams& p, int sms, cudaStream_t stream) {
-  const int rows = p.max_nodes * (p.q_heads / p.c.kv_heads);
-  return rows > 16 ? narrow_one<D, TYPE, 2>(p, sms, stream) : narrow_one<D, TYPE, 1>(p, sms, stream);
+  return launch_kernel(k, sms, kNarrowWarps * 32, smem, stream, kFlagPdl, p);
 }
 
 }  // namespace
 
-// Rows of a sequence and key head from which the tcgen05 kernel takes over.
-constexpr int kWideRows = 17;
-
 size_t attend_workspace_bytes(int64_t seqs, int q_heads, int kv_heads, int head_dim, int max_nodes,
                               int sms) {
   const int rows = max_nodes * (q_heads / kv_heads);
-  if (rows >= kWideRows) {
-    const int wide = wide_item_rows(wide_mode(rows));
-    return join_head_bytes(seqs * kv_heads * ((rows + wide - 1) / wide)) +
-           (size_t)sms * 2 * attend_slot_floats(wide, head_dim) * sizeof(float);
-  }
-  const int tile = rows > 16 ? 32 : 16;
-  return attend_counter_bytes(seqs * kv_heads * ((rows + tile - 1) / tile)) +
-         (size_t)sms * 2 * attend_slot_floats(tile, head_dim) * sizeof(float);
+  const int wide = wide_item_rows(wide_mode(rows));
+  return attend_counter_bytes(sms) +
+         (rows <= kNarrowRows ? 0 : join_head_bytes(seqs * kv_heads * ((rows + wide - 1) / wide))) +
+         (size_t)sms * 2 * attend_slot_floats(rows <= kNarrowRows ? kNarrowRows : wide, head_dim) * sizeof(float);
 }
 
+// The narrow kernel has 16 rows of an item, so from 17 on it would read K and V
+// a second time, or hold two row tiles in registers.  The latter, with 32 rows:
+// 103.5, 102 and 105 us (fp16, e4m3, int8) over 100000 positions, and 35.9 us
+// (fp16) over 32 sequences of 200, where the wide kernel takes 77.8, 95, 83.5
+// and 25.5; over one of 500 (fp16) 13.3 and 15.5, the one case that it loses.
 cudaError_t launch_attend(const AttendParams& p, int head_dim, int type, int sms,
                           cudaStream_t stream) {
-  if (p.max_nodes * (p.q_heads / p.c.kv_heads) >= kWideRows)
+  if (p.max_nodes * (p.q_heads / p.c.kv_heads) > kNarrowRows)
     return type == kCacheFp16   ? launch_attend_wide<kCacheFp16>(p, head_dim, sms, stream)
            : type == kCacheE4m3 ? launch_attend_wide<kCacheE4m3>(p, head_dim, sms, stream)
                                 : launch_attend_wide<kCacheInt8>(p, head_dim, sms, stream);
   if (head_dim == 128) {
-    if (type == kCacheFp16) return narrow_mt<128, kCacheFp16>(p, sms, stream);
-    if (type == kCacheE4m3) return narrow_mt<128, kCacheE4m3>(p, sms, stream);
-    return narrow_mt<128, kCacheInt8>(p, sms, stream);
+    if (type == kCacheFp16) return launch_narrow<128, kCacheFp16>(p, sms, stream);
+    if (type == kCacheE4m3) return launch_narrow<128, kCacheE4m3>(p, sms, stream);
+    return launch_narrow<128, kCacheInt8>(p, sms, stream);
   }
-  if (type == kCacheFp16) return narrow_mt<64, kCacheFp16>(p, sms, stream);
-  if (type == kCacheE4m3) return narrow_mt<64, kCacheE4m3>(p, sms, stream);
-  return narrow_mt<64, kCacheInt8>(p, sms, stream);
+  if (type == kCacheFp16) return launch_narrow<64, kCacheFp16>(p, sms, stream);
+  if (type == kCacheE4m3) return launch_narrow<64, kCacheE4m3>(p, sms, stream);
+  return launch_narrow<64, kCacheInt8>(p, sms, stream);
 }
 
 }  // namespace nmk

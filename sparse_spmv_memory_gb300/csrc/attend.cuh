@@ -224,9 +224,13 @@ struct Schedule {
   }
 };
 
-// Workspace: a counter per item, then two slots per block of ROWS rows x (D
-// sums, maximum, sum of weights).
-__host__ __device__ constexpr size_t attend_counter_bytes(int64_t items) { return (size_t)(items + 3) / 4 * 16; }
+// Workspace: a counter for each block, of the narrow kernel's parts of the item
+// that goes on past the block's range (an item has one block where it begins, a
+// block at most one item that it does not end); what a call needs besides; two
+// slots per block of ROWS rows x (D sums, maximum, sum of weights).  The counters
+// are at the same place whatever the call's shape and kernel, and nothing else is
+// ever written there: they are zeros between calls.
+__host__ __device__ constexpr size_t attend_counter_bytes(int blocks) { return (size_t)(blocks + 3) / 4 * 16; }
 __host__ __device__ constexpr size_t attend_slot_floats(int rows, int d) { return (size_t)rows * (d + 2); }
 
 // The many-row kernel (attend_wide.cuh) by the rows of a sequence and key head:
@@ -235,7 +239,7 @@ __host__ __device__ constexpr int wide_mode(int rows) {
   return rows <= 32 ? 4 : rows <= 64 ? 2 : rows <= 128 ? 1 : 0;
 }
 __host__ __device__ constexpr int wide_item_rows(int mode) { return mode == 0 ? 256 : 128 / mode; }
-// Its workspace: 16 bytes for each item (where its parts are), then two slots a block.
+// Behind the counters it has 16 bytes for each item: where its parts are.
 __host__ __device__ constexpr size_t join_head_bytes(int64_t items) { return (size_t)items * 16; }
 
 // The slot that block b has an item's part in: its first where its range begins

@@ -605,9 +605,9 @@ __global__ void __launch_bounds__(Wide<D, TYPE, MODE>::THREADS, 1)
       if (lane == 0) mbar_arrive(soft);
       return wait_warp(soft, phase++ & 1);
     };
-    int4* heads_of_items = reinterpret_cast<int4*>(p.workspace);
-    float* slots = reinterpret_cast<float*>(
-        p.workspace + join_head_bytes((int64_t)p.seqs * p.c.kv_heads * sched.rt_max));
+    uint8_t* ws = p.workspace + attend_counter_bytes(gridDim.x);
+    int4* heads_of_items = reinterpret_cast<int4*>(ws);
+    float* slots = reinterpret_cast<float*>(ws + join_head_bytes((int64_t)p.seqs * p.c.kv_heads * sched.rt_max));
     bool ok = true;
     // An item's queries (of this stream's rows), by this warpgroup: asked for when
     // the last product that reads the ones before is done, announced when they
@@ -960,14 +960,15 @@ __global__ void __launch_bounds__(256) attend_join_kernel(AttendParams p, int rt
   const int rows = min(IROWS, si.n * G - rt * IROWS);
   const int r = blockIdx.y * 32 + (threadIdx.x & 31), warp = threadIdx.x >> 5;
   if ((int)blockIdx.y * 32 >= rows) return;
-  const int4 head = reinterpret_cast<const int4*>(p.workspace)[item];
+  const uint8_t* ws = p.workspace + attend_counter_bytes(blocks);
+  const int4 head = reinterpret_cast<const int4*>(ws)[item];
   const int parts = head.z;
   // (an item without an entry, after a wait that gave up, reads in bounds)
   if (parts < 2 || parts > blocks || (uint32_t)head.x >= 2u * blocks || head.y < 0 || head.y > blocks - parts ||
       r >= rows)
     return;
-  const float* slots = reinterpret_cast<const float*>(
-      p.workspace + join_head_bytes((int64_t)p.seqs * p.c.kv_heads * rt_max));
+  const float* slots =
+      reinterpret_cast<const float*>(ws + join_head_bytes((int64_t)p.seqs * p.c.kv_heads * rt_max));
   // after the first, an item's part begins its block's range
   auto part = [&](int y) {
     return slots + (size_t)(y == 0 ? head.x : (head.y + y) * 2) * attend_slot_floats(IROWS, D);

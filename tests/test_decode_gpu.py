@@ -283,6 +283,23 @@ def test_attention_workspace_and_repeats(nm, kind, nodes):
     assert torch.equal(first[0], second[0]) and torch.equal(first[1], second[1])
 
 
+@pytest.mark.parametrize("kind", KINDS)
+def test_attention_workspace_of_other_shapes(nm, kind):
+    """Calls of different shapes through one workspace, zero-filled once: few and
+    many items, cut and whole, few and many rows."""
+    calls = [Batch(kind, [6000], [1], 8, 1, 128, 64, seed=30),
+             Batch(kind, [700 + 61 * i for i in range(25)], [2] * 25, 8, 4, 128, 64, seed=31),
+             Batch(kind, [900, 2500, 40], [32, 5, 17], 8, 2, 128, 64, seed=32),
+             Batch(kind, [5000, 30], [4, 3], 8, 2, 64, 16, seed=33),
+             Batch(kind, [300 + 97 * i for i in range(40)], [12] * 40, 8, 2, 64, 16, seed=34)]
+    need = max(nm.nm_tree_attention_workspace_bytes(len(b.nodes), b.q.shape[1], b.k.shape[1], b.q.shape[2], max(b.nodes))
+               for b in calls)
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    for turn in range(2):
+        for i in (0, 1, 2, 3, 1, 4, 0, 3, 2):
+            calls[i].check(nm, f"turn {turn}, call {i}", workspace=ws)
+
+
 def test_attention_long_offsets(nm):
     """A cache whose byte and element offsets pass 2^32: the sequence's pages lie
     at both of its ends."""
