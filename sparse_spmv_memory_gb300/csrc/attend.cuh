@@ -230,7 +230,7 @@ struct Schedule {
 // slots per block of ROWS rows x (D sums, maximum, sum of weights).  The counters
 // are at the same place whatever the call's shape and kernel, and nothing else is
 // ever written there: they are zeros between calls.
-__host__ __device__ constexpr size_t attend_counter_bytes(int blocks) { return (size_t)(blocks + 3) / 4 * 16; }
+__host__ __device__ constexpr size_t attend_counter_bytes(int blocks) { return (size_t)(blocks + 31) / 32 * 128; }
 __host__ __device__ constexpr size_t attend_slot_floats(int rows, int d) { return (size_t)rows * (d + 2); }
 
 // The many-row kernel (attend_wide.cuh) by the rows of a sequence and key head:
@@ -240,7 +240,7 @@ __host__ __device__ constexpr int wide_mode(int rows) {
 }
 __host__ __device__ constexpr int wide_item_rows(int mode) { return mode == 0 ? 256 : 128 / mode; }
 // Behind the counters it has 16 bytes for each item: where its parts are.
-__host__ __device__ constexpr size_t join_head_bytes(int64_t items) { return (size_t)items * 16; }
+__host__ __device__ constexpr size_t join_head_bytes(int64_t items) { return (size_t)(items + 7) / 8 * 128; }
 
 // The slot that block b has an item's part in: its first where its range begins
 // inside the item (or with it), else its second.
