@@ -12,8 +12,7 @@
 //   MMA      one thread: S = Q K^T into TMEM; O += P V with P from TMEM and V
 //            as the MN-major operand (its rows are the reduction's).
 //   softmax  two warpgroups, a query row per thread: scores from TMEM, weights
-//            back over them as fp16, 32 positions at a time.  The maximum that
-//            scales a row moves only when a score exceeds it by 2^8 (fp16 weights
+//            back over them as fp16.  The maximum that scales a row moves only when a score exceeds it by 2^8 (fp16 weights
 //            reach 2^8 then, at the same relative rounding), so the sums in TMEM
 //            are seldom rescaled.
 // With at most 64 (32) rows, the tile's 128 rows are two (four) copies of them,
@@ -71,9 +70,10 @@ struct Wide {
   static constexpr int THREADS = 32 * (kLoadWarp + LW);
   // Registers of a thread: the launch gives every warpgroup (65536 / THREADS,
   // rounded down to 8) of them, the softmax warpgroups take some of the others'.
-  static constexpr int REGS = F16 ? 168 : 96, SOFT_REGS = F16 ? 200 : 144, OTHER_REGS = F16 ? 104 : 64;
+  static constexpr int REGS = F16 ? 168 : 96, SOFT_REGS = F16 ? 208 : 144, OTHER_REGS = F16 ? 88 : 64;
   static_assert(2 * SOFT_REGS + (THREADS / 128 - 2) * OTHER_REGS <= THREADS / 128 * REGS,
                 "the split fits the launch");
+  static constexpr int CH = F16 ? kKeys / SPLIT : 32;  // positions a softmax thread holds
   static constexpr int QT = PAIR ? 2 : 1;     // row tiles of an item
   static constexpr int IROWS = QT * kRows / SPLIT;  // rows of an item
   static constexpr int TILE = kKeys * D * 2;  // bytes of a stage
@@ -600,6 +600,9 @@ __global__ void __launch_bounds__(Wide<D, TYPE, MODE>::THREADS, 1)
     const uint32_t tS = tlane + (b ? kS1 : kS0), tO = tlane + (b ? kO1 : kO0);
     const int step = PAIR ? 1 : 2, off0 = PAIR ? 0 : b;  // tiles of this stream
     int tile_no = 0, item_no = 0, ns = 0, no = 0, phase = 0;
+    // A score's step in powers of 2 (fp16).  Not 0, so that a masked -infinity stays
+    // one; no score is large enough to tell 1e-30 from 0.
+    const float step2 = fmaxf(fabsf(cs), 1e-30f);
     auto soft_sync = [&]() {  // all softmax warps
       __syncwarp();
       if (lane == 0) mbar_arrive(soft);
@@ -687,39 +690,51 @@ __global__ void __launch_bounds__(Wide<D, TYPE, MODE>::THREADS, 1)
             if (rest < 32) x &= rest <= 0 ? 0u : (1u << rest) - 1u;
             return x;
           };
-          // 32 positions at a time, in one reading of the scores.
-          const int y0 = copy * (4 / SPLIT), y1 = y0 + 4 / SPLIT;
+          // CH positions at a time, in one reading of the scores: all maxima first,
+          // then the weights, which pass through the MUFU at its rate.
+          constexpr int CH = W::CH;
+          const int y0 = copy * (4 / SPLIT), y1 = y0 + 4 / SPLIT;  // of 32 positions
 #pragma unroll 1
-          for (int y = y0; y < y1; ++y) {
-            uint32_t v[32], h[16];
-            tmem_ld_32(tS + 32 * y, v);
-            tmem_ld_wait();
-            // exponents, in powers of 2
+          for (int y = y0; y < y1; y += CH / 32) {
+            uint32_t v[CH / 32][32];
 #pragma unroll
-            for (int x = 0; x < 32; x += 4) {
-              float2 e0 = make_float2(__uint_as_float(v[x]), __uint_as_float(v[x + 1]));
-              float2 e1 = make_float2(__uint_as_float(v[x + 2]), __uint_as_float(v[x + 3]));
-              if (F16) {
-                e0 = mul2(e0, make_float2(cs, cs));
-                e1 = mul2(e1, make_float2(cs, cs));
-              } else {
-                const float4 a = ksc[8 * y + x / 4], d = lvs[8 * y + x / 4];
-                e0 = fma2(e0, make_float2(a.x, a.y), make_float2(d.x, d.y));
-                e1 = fma2(e1, make_float2(a.z, a.w), make_float2(d.z, d.w));
+            for (int z = 0; z < CH / 32; ++z) tmem_ld_32(tS + 32 * (y + z), v[z]);
+            tmem_ld_wait();
+            // exponents in powers of 2 are v step - m
+            if (F16) {
+              if (cs < 0.0f) {
+#pragma unroll
+                for (int x = 0; x < CH; ++x) v[x / 32][x % 32] ^= 0x80000000u;
               }
-              v[x] = __float_as_uint(e0.x), v[x + 1] = __float_as_uint(e0.y);
-              v[x + 2] = __float_as_uint(e1.x), v[x + 3] = __float_as_uint(e1.y);
+            } else {
+#pragma unroll
+              for (int x = 0; x < CH; x += 4) {
+                const float4 a = ksc[8 * y + x / 4], d = lvs[8 * y + x / 4];
+                const float2 e0 = fma2(make_float2(__uint_as_float(v[x / 32][x % 32]), __uint_as_float(v[x / 32][x % 32 + 1])),
+                                       make_float2(a.x, a.y), make_float2(d.x, d.y));
+                const float2 e1 = fma2(make_float2(__uint_as_float(v[x / 32][x % 32 + 2]), __uint_as_float(v[x / 32][x % 32 + 3])),
+                                       make_float2(a.z, a.w), make_float2(d.z, d.w));
+                v[x / 32][x % 32] = __float_as_uint(e0.x), v[x / 32][x % 32 + 1] = __float_as_uint(e0.y);
+                v[x / 32][x % 32 + 2] = __float_as_uint(e1.x), v[x / 32][x % 32 + 3] = __float_as_uint(e1.y);
+              }
             }
             if (edge) {
-              const uint32_t see = sees(y);
 #pragma unroll
-              for (int x = 0; x < 32; ++x)
-                if (!((see >> x) & 1u)) v[x] = 0xFF800000u;  // -inf
+              for (int z = 0; z < CH / 32; ++z) {
+                const uint32_t see = sees(y + z);
+#pragma unroll
+                for (int x = 0; x < 32; ++x)
+                  if (!((see >> x) & 1u)) v[z][x] = 0xFF800000u;  // -inf
+              }
             }
             float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int x = 0; x < 32; ++x) t[x & 3] = fmaxf(t[x & 3], __uint_as_float(v[x]));
-            const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+            for (int x = 0; x < CH; x += 8) {
+#pragma unroll
+              for (int z = 0; z < 4; ++z)
+                t[z] = fmaxf(fmaxf(t[z], __uint_as_float(v[x / 32][x % 32 + z])), __uint_as_float(v[x / 32][x % 32 + z + 4]));
+            }
+            const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * (F16 ? step2 : 1.0f);
             const bool grow = top > m + kGrow || (m == -INFINITY && top > -INFINITY);
             if (__any_sync(0xFFFFFFFFu, grow)) {
               // seldom (but for an item's first positions): the sums so far, and
@@ -727,29 +742,30 @@ __global__ void __launch_bounds__(Wide<D, TYPE, MODE>::THREADS, 1)
               const float keep = !grow ? 1.0f : m == -INFINITY ? 0.0f : exp2_fast(m - top);
               if (k > 0) {
 #pragma unroll 1
-                for (int d = 0; d < D; d += 32) {
-                  uint32_t o[32];
-                  tmem_ld_32(tO + d, o);
+                for (int d = 0; d < D; d += 16) {
+                  uint32_t o[16];
+                  tmem_ld_16(tO + d, o);
                   tmem_ld_wait();
 #pragma unroll
-                  for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * keep);
-                  tmem_st_32(tO + d, o);
+                  for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * keep);
+                  tmem_st_16(tO + d, o);
                 }
               }
+              if (CH < kKeys / SPLIT) {
 #pragma unroll 1
-              for (int z = y0; z < y; z += 2) {  // two chunks' weights (one may be to come)
-                uint32_t o[32];
-                tmem_st_wait();
-                tmem_ld_32(tS + 16 * z, o);
-                tmem_ld_wait();
-                // (rounded a second time, in the few tiles where a maximum moves)
+                for (int z = y0; z < y; ++z) {
+                  uint32_t o[16];
+                  tmem_st_wait();
+                  tmem_ld_16(tS + 16 * z, o);
+                  tmem_ld_wait();
+                  // (rounded a second time, in the few tiles where a maximum moves)
 #pragma unroll
-                for (int x = 0; x < 32; ++x) {
-                  const float2 f = half2_bits_to_float2(o[x]);
-                  o[x] = half2_of(f.x * keep, f.y * keep);
+                  for (int x = 0; x < 16; ++x) {
+                    const float2 f = half2_bits_to_float2(o[x]);
+                    o[x] = half2_of(f.x * keep, f.y * keep);
+                  }
+                  tmem_st_16(tS + 16 * z, o);
                 }
-                tmem_st_16(tS + 16 * z, o);
-                if (z + 1 < y) tmem_st_16(tS + 16 * z + 16, o + 16);
               }
               l *= keep;
               if (grow) m = top;
@@ -757,24 +773,36 @@ __global__ void __launch_bounds__(Wide<D, TYPE, MODE>::THREADS, 1)
             const float off = m == -INFINITY ? 0.0f : -m;
             float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-            for (int x = 0; x < 32; x += 4) {
-              float2 e0 = add2(make_float2(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), make_float2(off, off));
-              float2 e1 = add2(make_float2(__uint_as_float(v[x + 2]), __uint_as_float(v[x + 3])), make_float2(off, off));
-              e0 = make_float2(exp2_fast(e0.x), exp2_fast(e0.y));
-              e1 = make_float2(exp2_fast(e1.x), exp2_fast(e1.y));
-              if (F16) {
-                sum[0] = add2(sum[0], e0);
-                sum[1] = add2(sum[1], e1);
-              } else {
-                const float4 r = rvs[8 * y + x / 4];
-                sum[0] = fma2(e0, make_float2(r.x, r.y), sum[0]);
-                sum[1] = fma2(e1, make_float2(r.z, r.w), sum[1]);
+            for (int z = 0; z < CH / 32; ++z) {
+              uint32_t h[16];
+#pragma unroll
+              for (int x = 0; x < 32; x += 4) {
+                const uint32_t* u = &v[z][x];
+                float2 e0 = make_float2(__uint_as_float(u[0]), __uint_as_float(u[1]));
+                float2 e1 = make_float2(__uint_as_float(u[2]), __uint_as_float(u[3]));
+                if (F16) {
+                  e0 = fma2(e0, make_float2(step2, step2), make_float2(off, off));
+                  e1 = fma2(e1, make_float2(step2, step2), make_float2(off, off));
+                } else {
+                  e0 = add2(e0, make_float2(off, off));
+                  e1 = add2(e1, make_float2(off, off));
+                }
+                e0 = make_float2(exp2_fast(e0.x), exp2_fast(e0.y));
+                e1 = make_float2(exp2_fast(e1.x), exp2_fast(e1.y));
+                if (F16) {
+                  sum[0] = add2(sum[0], e0);
+                  sum[1] = add2(sum[1], e1);
+                } else {
+                  const float4 r = rvs[8 * (y + z) + x / 4];
+                  sum[0] = fma2(e0, make_float2(r.x, r.y), sum[0]);
+                  sum[1] = fma2(e1, make_float2(r.z, r.w), sum[1]);
+                }
+                h[x / 2] = half2_of(e0.x, e0.y);
+                h[x / 2 + 1] = half2_of(e1.x, e1.y);
               }
-              h[x / 2] = half2_of(e0.x, e0.y);
-              h[x / 2 + 1] = half2_of(e1.x, e1.y);
+              tmem_st_16(tS + 16 * (y + z), h);
             }
             l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-            tmem_st_16(tS + 16 * y, h);
           }
           if (SPLIT > 1) {  // no weight on the other copies' positions
             const uint32_t zero[16] = {};
