@@ -74,6 +74,8 @@ struct Wide {
   static_assert(2 * SOFT_REGS + (THREADS / 128 - 2) * OTHER_REGS <= THREADS / 128 * REGS,
                 "the split fits the launch");
   static constexpr int CH = F16 ? kKeys / SPLIT : 32;  // positions a softmax thread holds
+  // The product with V begins when half of the weights are there.
+  static constexpr int PARTS = CH == kKeys ? 2 : 1;
   static constexpr int QT = PAIR ? 2 : 1;     // row tiles of an item
   static constexpr int IROWS = QT * kRows / SPLIT;  // rows of an item
   static constexpr int TILE = kKeys * D * 2;  // bytes of a stage
@@ -163,7 +165,7 @@ __global__ void __launch_bounds__(Wide<D, TYPE, MODE>::THREADS, 1)
   constexpr int IROWS = W::IROWS;
   using Sched = Schedule<IROWS, kKeys, W::THREADS>;
   extern __shared__ uint8_t raw_smem[];
-  __shared__ uint64_t bar_mem[2 * W::NS + 8 + 2 * RS];
+  __shared__ uint64_t bar_mem[2 * W::NS + 8 + 2 * RS + 2];
   __shared__ uint32_t tmem_slot;
   __shared__ uint32_t there_of[kMeta];
   __shared__ uint32_t bad_of[kBad][2];
@@ -185,6 +187,7 @@ __global__ void __launch_bounds__(Wide<D, TYPE, MODE>::THREADS, 1)
   const uint32_t qfull = bars + 8u * (2 * W::NS + 6), soft = bars + 8u * (2 * W::NS + 7);
   auto rfull = [&](int s) { return bars + 8u * (2 * W::NS + 8 + s); };        // raw tile landed
   auto rfree = [&](int s) { return bars + 8u * (2 * W::NS + 8 + RS + s); };   // ... and read
+  auto phalf = [&](int b) { return bars + 8u * (2 * W::NS + 8 + 2 * RS + b); };  // PARTS == 2: the first half of the weights
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_launch_dependents();
@@ -202,6 +205,7 @@ __global__ void __launch_bounds__(Wide<D, TYPE, MODE>::THREADS, 1)
     for (int b = 0; b < 2; ++b) {
       mbar_init(sfull(b), 1);
       mbar_init(pfull(b), 4);
+      mbar_init(phalf(b), 4);
       mbar_init(ofull(b), 1);
     }
     mbar_init(qfull, PAIR ? kSoftWarps : kSoftWarps / 2);
@@ -528,18 +532,23 @@ __global__ void __launch_bounds__(Wide<D, TYPE, MODE>::THREADS, 1)
       __syncwarp();
     };
     auto sums = [&](int pos, int b, bool add) {
-      if (!wait_warp(pfull(b), np[b]++ & 1)) return false;
-      tc_fence_after_sync();
       const uint32_t d = tmem + (b ? kO1 : kO0), a = tmem + (b ? kS1 : kS0);
       const uint32_t v = v_lo + pos % W::NS * (W::TILE >> 4);
-      if (lead) {
+      constexpr int STEPS = kKeys / 16 / W::PARTS;
 #pragma unroll
-        for (int ks = 0; ks < kKeys / 16; ++ks)
-          mma_f16_ts(d, a + ks * 8, desc_of(v + ks * (2048 >> 4), kDescSw128Hi), id_o,
-                     ks != 0 ? 1u : add ? 1u : 0u);
-        mma_commit(ofull(b));
+      for (int part = 0; part < W::PARTS; ++part) {
+        if (!wait_warp(part == W::PARTS - 1 ? pfull(b) : phalf(b), np[b] & 1)) return false;
+        tc_fence_after_sync();
+        if (lead) {
+#pragma unroll
+          for (int ks = part * STEPS; ks < (part + 1) * STEPS; ++ks)
+            mma_f16_ts(d, a + ks * 8, desc_of(v + ks * (2048 >> 4), kDescSw128Hi), id_o,
+                       ks != 0 ? 1u : add ? 1u : 0u);
+          if (part == W::PARTS - 1) mma_commit(ofull(b));
+        }
+        __syncwarp();
       }
-      __syncwarp();
+      ++np[b];
       return true;
     };
     auto release = [&](int pos) {
@@ -611,6 +620,12 @@ __global__ void __launch_bounds__(Wide<D, TYPE, MODE>::THREADS, 1)
     uint8_t* ws = p.workspace + attend_counter_bytes(gridDim.x);
     int4* heads_of_items = reinterpret_cast<int4*>(ws);
     float* slots = reinterpret_cast<float*>(ws + join_head_bytes((int64_t)p.seqs * p.c.kv_heads * sched.rt_max));
+    auto give_weights = [&](uint32_t bar) {
+      tmem_st_wait();
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
     bool ok = true;
     // An item's queries (of this stream's rows), by this warpgroup: asked for when
     // the last product that reads the ones before is done, announced when they
@@ -801,6 +816,7 @@ __global__ void __launch_bounds__(Wide<D, TYPE, MODE>::THREADS, 1)
                 h[x / 2 + 1] = half2_of(e1.x, e1.y);
               }
               tmem_st_16(tS + 16 * (y + z), h);
+              if (W::PARTS == 2 && z == 1) give_weights(phalf(b));
             }
             l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
           }
@@ -810,11 +826,10 @@ __global__ void __launch_bounds__(Wide<D, TYPE, MODE>::THREADS, 1)
             for (int y = 0; y < 4; ++y)
               if (y < y0 || y >= y1) tmem_st_16(tS + 16 * y, zero);
           }
-          tmem_st_wait();
+        } else if (W::PARTS == 2) {
+          give_weights(phalf(b));
         }
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(pfull(b));
+        give_weights(pfull(b));
       }
       if (ok && asks) announce_q();
       if (ok && tiles > 0) ok = wait_warp(ofull(b), (no + tiles - 1) & 1);
