@@ -243,6 +243,9 @@ __global__ void __launch_bounds__(Wide<D, TYPE, MODE>::THREADS, 1)
     constexpr int LT = W::LW * 32;
     const int box_shift = min(p.c.page_shift, 7);  // a box: a page's rows, at most a tile's
     const int page_rows = 1 << box_shift, boxes = kKeys >> box_shift;
+    // (16 x 8000 positions: 100 us without, 95 with; what else is in L2, the
+    // blocks' parts and the code among it, stays there)
+    const uint64_t once = l2_evict_first();
     int c = 0;  // positions of the ring so far
     int item_no = 0, tile_no = 0, looked = 0;
     bool ok = true;
@@ -290,7 +293,7 @@ __global__ void __launch_bounds__(Wide<D, TYPE, MODE>::THREADS, 1)
 #pragma unroll
           for (int hf = 0; hf < D / 64; ++hf)
             tma_load_3d(dst + hf * W::HALF + lane * page_rows * 128, v ? &tm_v : &tm_k, hf * 64, t.row,
-                        t.page, bar);
+                        t.page, bar, once);
         }
         __syncwarp();
       } else if (!look && lane == 0) {
@@ -350,7 +353,7 @@ __global__ void __launch_bounds__(Wide<D, TYPE, MODE>::THREADS, 1)
       if (t->on)
         bulk_load(base + W::RAW_OFF + st * W::RAW + lane * page_rows * D,
                   (v ? p.c.v : p.c.k) + t->page * p.c.page_stride + (int64_t)t->row * D, page_rows * D,
-                  rfull(st));
+                  rfull(st), once);
       __syncwarp();
       return true;
     };
@@ -988,11 +991,13 @@ __global__ void __launch_bounds__(Wide<D, TYPE, MODE>::THREADS, 1)
   }
 }
 
-// Adds the parts of the items that several blocks had: a block takes 32 rows of
-// an item, a thread a row and 4 or 8 columns (warps side by side), every part's
-// loads in flight together.  A launch of its own: one block that added its item
-// in the kernel above had 10 to 40 us of it, a whole grid has 2 to 3.
-template <int D, int IROWS>
+// Adds the parts of the items that several blocks had: a block takes 32 rows and
+// 32 C columns of an item, a thread a row and 4 C columns (warps side by side),
+// B parts' loads in flight together.  A launch of its own: one block that added
+// its item in the kernel above had 10 to 40 us of it.  Whole rows (C = D / 32)
+// where the blocks then fill the device, else a quarter (half) of them: 128 items
+// of 256 rows take 7 us more with C = 1, 8 of 32 rows 3 us more with C = 4.
+template <int D, int IROWS, int C>
 __global__ void __launch_bounds__(256) attend_join_kernel(AttendParams p, int rt_max, int blocks) {
   pdl_launch_dependents();
   pdl_wait_previous();
@@ -1012,11 +1017,12 @@ __global__ void __launch_bounds__(256) attend_join_kernel(AttendParams p, int rt
     return;
   const float* slots =
       reinterpret_cast<const float*>(ws + join_head_bytes((int64_t)p.seqs * p.c.kv_heads * rt_max));
+  const int c0 = ((int)blockIdx.z * 8 + warp) * C;  // the thread's first 16 bytes of a row
+  constexpr int B = C == 4 ? 2 : 8;  // parts in flight
   // after the first, an item's part begins its block's range
   auto part = [&](int y) {
     return slots + (size_t)(y == 0 ? head.x : (head.y + y) * 2) * attend_slot_floats(IROWS, D);
   };
-  constexpr int C = D / 32, B = 16 / C;  // 16-byte columns of a thread, parts at a time
   float4 x[C], v[B][C];
   float pm[B];
   auto fetch = [&](int y0) {
@@ -1025,8 +1031,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(AttendParams p, int rt
       const float* f = part(min(y0 + j, parts - 1));
       pm[j] = __ldcg(f + IROWS * D + r);
 #pragma unroll
-      for (int k = 0; k < C; ++k)
-        v[j][k] = __ldcg(reinterpret_cast<const float4*>(f) + (warp * C + k) * IROWS + r);
+      for (int k = 0; k < C; ++k) v[j][k] = __ldcg(reinterpret_cast<const float4*>(f) + (c0 + k) * IROWS + r);
     }
   };
   fetch(0);
@@ -1048,13 +1053,19 @@ __global__ void __launch_bounds__(256) attend_join_kernel(AttendParams p, int rt
   const float inv = tot == 0.0f ? 0.0f : 1.0f / tot;
   const Heads heads(G);
   const int rr = rt * IROWS + r, node = heads.node(rr), hq = h * G + heads.head(rr);
-  __half* dst = p.out + (int64_t)(si.first + node) * p.ldo + hq * D + warp * C * 4;
+  __half* dst = p.out + (int64_t)(si.first + node) * p.ldo + hq * D + c0 * 4;
+  uint2 y[C];
 #pragma unroll
-  for (int k = 0; k < C; k += 2)
-    *reinterpret_cast<uint4*>(dst + 4 * k) =
-        make_uint4(half2_of(x[k].x * inv, x[k].y * inv), half2_of(x[k].z * inv, x[k].w * inv),
-                   half2_of(x[k + 1].x * inv, x[k + 1].y * inv), half2_of(x[k + 1].z * inv, x[k + 1].w * inv));
-  if (warp == 0 && p.lse)
+  for (int k = 0; k < C; ++k)
+    y[k] = make_uint2(half2_of(x[k].x * inv, x[k].y * inv), half2_of(x[k].z * inv, x[k].w * inv));
+  if (C == 1) {
+    *reinterpret_cast<uint2*>(dst) = y[0];
+  } else {
+#pragma unroll
+    for (int k = 0; k < C; k += 2)
+      *reinterpret_cast<uint4*>(dst + 4 * k) = make_uint4(y[k].x, y[k].y, y[k + 1 < C ? k + 1 : k].x, y[k + 1 < C ? k + 1 : k].y);
+  }
+  if (c0 == 0 && p.lse)
     p.lse[(int64_t)(si.first + node) * p.q_heads + hq] = tot == 0.0f ? -INFINITY : (M + log2f(tot)) * kLn2;
 }
 
@@ -1092,10 +1103,12 @@ cudaError_t wide_one(const AttendParams& p, int sms, cudaStream_t stream) {
   e = launch_kernel(k, sms, W::THREADS, W::SMEM, stream, kFlagPdl, p, tk, tv);
   if (e != cudaSuccess) return e;
   constexpr int IROWS = W::IROWS;
-  const int rt_max = (p.max_nodes * (p.q_heads / p.c.kv_heads) + IROWS - 1) / IROWS;
+  const int rows = p.max_nodes * (p.q_heads / p.c.kv_heads), rt_max = (rows + IROWS - 1) / IROWS;
+  const dim3 grid((unsigned)(p.seqs * p.c.kv_heads * rt_max), (unsigned)((rows < IROWS ? rows : IROWS) + 31) / 32);
+  // whole rows of threads where that fills the device, else a quarter (half)
   cudaLaunchConfig_t cfg = {};
-  const int rows = p.max_nodes * (p.q_heads / p.c.kv_heads);
-  cfg.gridDim = dim3((unsigned)(p.seqs * p.c.kv_heads * rt_max), (unsigned)((rows < IROWS ? rows : IROWS) + 31) / 32);
+  const bool narrow = grid.x * grid.y < (unsigned)sms;
+  cfg.gridDim = dim3(grid.x, grid.y, narrow ? D / 32 : 1);
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -1103,7 +1116,8 @@ cudaError_t wide_one(const AttendParams& p, int sms, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attend_join_kernel<D, IROWS>, p, rt_max, sms);
+  return narrow ? cudaLaunchKernelEx(&cfg, attend_join_kernel<D, IROWS, 1>, p, rt_max, sms)
+                : cudaLaunchKernelEx(&cfg, attend_join_kernel<D, IROWS, D / 32>, p, rt_max, sms);
 }
 
 template <int D, int TYPE>
