@@ -388,7 +388,12 @@ __global__ void __launch_bounds__(Wide<D, TYPE, MODE>::THREADS, 1)
       static_assert(STEP % 4 == 0, "see above");
       const int ch = ct % PR, r0 = ct / PR;
       const uint32_t from = src + ct * 16;
-      const uint32_t to = dst + (ch >> 2) * W::HALF + r0 * 128 + ((((ch & 3) * 2) ^ (r0 & 7)) << 4);
+      // Eight threads store 16 bytes at a time, of one row's two halves (D = 128),
+      // which are in the same banks: those of the second half take the upper 8
+      // codes of their piece first.
+      const bool upper = (ch >> 2) != 0;
+      const uint32_t to =
+          (dst + (ch >> 2) * W::HALF + r0 * 128 + ((((ch & 3) * 2) ^ (r0 & 7)) << 4)) ^ (upper ? 16u : 0u);
       constexpr uint32_t kTurn = STEP % 8 ? 64u : 0u;
       const bool look = v && t.edge;
       constexpr int ALL = (kKeys + STEP - 1) / STEP, B = 4;
@@ -408,7 +413,8 @@ __global__ void __launch_bounds__(Wide<D, TYPE, MODE>::THREADS, 1)
           if (look && !(r < t.left && ((t.there >> (r >> 3)) & 1u))) w[i][0] = w[i][1] = w[i][2] = w[i][3] = 0;
           uint32_t h[8];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) widen4<F16 ? kCacheE4m3 : TYPE>(w[i][k], h[2 * k], h[2 * k + 1]);
+          for (int k = 0; k < 4; ++k)
+            widen4<F16 ? kCacheE4m3 : TYPE>(D == 128 && upper ? w[i][k ^ 2] : w[i][k], h[2 * k], h[2 * k + 1]);
           if (TYPE == kCacheE4m3 && look && t.node0 + r >= 0) clean(h, 8, t.node0 + r, t.bad);
           const uint32_t at = (to + (i0 + i) * STEP * 128) ^ ((i0 + i) & 1 ? kTurn : 0u);
           sts_v4(at, h[0], h[1], h[2], h[3]);
