@@ -30,7 +30,9 @@
  * call says, and never read or written through.  Launches use programmatic
  * dependent launch; every kernel waits for the previous one on the stream
  * before it touches any buffer.  No call uses floating-point atomics: the
- * same inputs give the same bits.
+ * same inputs give the same bits.  nm_tree_attention's and nm_tree_verify's
+ * kernels wait on barriers of their own with a limit: nm_wait_timeouts
+ * (nm_spmv.h) counts the waits that gave up, after which outputs are undefined.
  */
 #ifndef NM_DECODE_H
 #define NM_DECODE_H
@@ -56,7 +58,8 @@ extern "C" {
  * (or v), and its scale at p * scale_page_stride + h * page_size + offset.
  * A slot is p * page_size + offset.
  *   k, v      : device, 32-byte aligned.
- *   *_scale   : device fp32, 4-byte aligned; NULL for NM_CACHE_FP16.
+ *   *_scale   : device fp32, 4-byte aligned; NULL for NM_CACHE_FP16.  Scales are
+ *               not negative (nm_rope_append writes none that is).
  *   page_size : a power of two, 8 .. 2^20;  head_dim : 64 or 128;
  *   pages >= 1, kv_heads 1 .. 1024;
  *   page_stride >= kv_heads * page_size * head_dim elements, a multiple of
@@ -157,14 +160,15 @@ int nm_cache_read(const nm_cache *cache, const int64_t *slots, int64_t rows, voi
  * and a non-finite row of the context all nodes of its sequence.
  * Scores, maxima and sums are fp32.  The weights exp(score - max) are rounded
  * to fp16 for the tensor cores' product with the values (times the row's
- * scale where the cache has one); products are accumulated in fp32 and out is
+ * scale where the cache has one; one below 2^-100 counts as 2^-100); products are accumulated in fp32 and out is
  * rounded once.  The split of the positions over the blocks depends on the
  * lengths, and every part is joined in a fixed order.
  *   workspace : device scratch, 16-byte aligned, of at least
- *       nm_tree_attention_workspace_bytes(...) bytes (partial sums of rows cut
- *       between blocks, and counters), ZERO-FILLED before its first use; every
- *       call leaves the counters zero again, so it can be used by any later
- *       call on the same stream.
+ *       nm_tree_attention_workspace_bytes(...) bytes (counters, then partial
+ *       sums of rows cut between blocks), ZERO-FILLED before its first use.  The
+ *       counters are at its start whatever the call's shape, nothing else is
+ *       written there, and every call leaves them zero: later calls of any shape
+ *       on the same device, ordered after this one, can use it as it is.
  * seqs == 0 or tokens == 0 is a no-op; seqs < 65536, tokens < 2^31, q_heads
  * 1 .. 1024, q_heads / kv_heads <= 64.
  * ------------------------------------------------------------------------- */

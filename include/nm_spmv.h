@@ -371,7 +371,8 @@ int nm_spmm_prefill_plan(int64_t rows, int64_t cols, int64_t T, int sms, int *va
  * set return without doing anything, so their Y is left unwritten.  Zero in
  * every correct run; `reset` != 0 resets the count to zero and clears the
  * abort flag.  After a nonzero count, treat the outputs of the tensor-core
- * calls since the last reset as undefined.
+ * calls since the last reset as undefined.  The attention and verification
+ * kernels of nm_decode.h count here too.
  * Host-synchronous (reads a device counter); negative nm_status on error. */
 int64_t nm_wait_timeouts(int reset);
 

@@ -142,6 +142,16 @@ def test_attention_heads(nm, kind, q_heads, kv_heads, dim, nodes):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("nodes", [3, 9, 18, 33, 64])
+@pytest.mark.parametrize("scale", [-0.07, 0.0, 1e-20])
+def test_attention_scales(nm, kind, nodes, scale):
+    """A scale of any sign, and ones under which every row is averaged."""
+    b = Batch(kind, [300, 0], [nodes, 2], 8, 2, 128, 64, seed=41)
+    b.scale = scale
+    b.check(nm, f"{kind} nodes {nodes} scale {scale}")
+
+
+@pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("page", [8, 64, 128, 1024])
 @pytest.mark.parametrize("nodes", [2, 40])
 def test_attention_pages_and_causal(nm, kind, page, nodes):
