@@ -67,12 +67,22 @@ __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
 //     column t of MMA n-tile t.  Two rows' halves are paired by byte permutes.
 // No shared memory, no barrier, until a block's warps join their sums.  A warp
 // takes every NW-th unit of the block's part.
-constexpr int kNarrowRows = 16, kNarrowWarps = 8;
+//
+// What bounds it: the bytes that a warp's registers have in flight, and with codes
+// the chain load, widen, product, weight, permute, product, which two or three
+// warps a scheduler do not cover (35 % of issue slots, 16 % of the tensor pipe).
+// Hence 12 warps of 16 positions for codes (8 rows over 100000 positions, e4m3:
+// 69.0 us; 8 warps of 32: 72.4, 10: 73.4, 14: 92.4 and 16: 94.9, which spill),
+// and 8 warps for fp16, whose rows take twice the registers.  1 token over 500
+// positions: 9.3 us, of which launch, lengths and the table's look-up some 3, the
+// loads 1.5, and joining warps, then blocks, 3.
+constexpr int kNarrowRows = 16;
 
 template <int D, int TYPE>
 struct Narrow {
   static constexpr bool F16 = TYPE == kCacheFp16;
-  static constexpr int NG = F16 ? 2 : 4;      // groups of 8 positions in a unit
+  static constexpr int NW = F16 ? 8 : 12;       // warps
+  static constexpr int NG = F16 ? 2 : 2;       // groups of 8 positions in a unit
   static constexpr int UK = 8 * NG;           // positions of a unit
   static constexpr int KS = D / 16;           // MMA k steps of a score
   static constexpr int NT = D / 8;            // n-tiles of an output row
@@ -85,10 +95,10 @@ struct Narrow {
 };
 
 template <int D, int TYPE>
-__global__ void __launch_bounds__(kNarrowWarps * 32, 1) attend_narrow_kernel(AttendParams p) {
+__global__ void __launch_bounds__(Narrow<D, TYPE>::NW * 32, 1) attend_narrow_kernel(AttendParams p) {
   using N = Narrow<D, TYPE>;
   constexpr bool F16 = N::F16;
-  constexpr int ROWS = kNarrowRows, NW = kNarrowWarps, NTH = NW * 32, PITCH = D + 4;
+  constexpr int ROWS = kNarrowRows, NW = N::NW, NTH = NW * 32, PITCH = D + 4;
   using Sched = Schedule<ROWS, N::UK, NTH>;
   extern __shared__ __align__(16) uint8_t dyn[];
   float* so = reinterpret_cast<float*>(dyn);                     // [NW][ROWS][PITCH]
@@ -472,7 +482,7 @@ __global__ void __launch_bounds__(kNarrowWarps * 32, 1) attend_narrow_kernel(Att
 
 template <int D, int TYPE>
 cudaError_t launch_narrow(const AttendParams& p, int sms, cudaStream_t stream) {
-  constexpr size_t smem = (size_t)kNarrowWarps * kNarrowRows * (D + 4) * sizeof(float);
+  constexpr size_t smem = (size_t)Narrow<D, TYPE>::NW * kNarrowRows * (D + 4) * sizeof(float);
   auto* k = attend_narrow_kernel<D, TYPE>;
   static int done[64];
   int dev = 0;
@@ -483,28 +493,35 @@ cudaError_t launch_narrow(const AttendParams& p, int sms, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     if (dev < 64) __atomic_store_n(&done[dev], 1, __ATOMIC_RELEASE);
   }
-  return launch_kernel(k, sms, kNarrowWarps * 32, smem, stream, kFlagPdl, p);
+  return launch_kernel(k, sms, Narrow<D, TYPE>::NW * 32, smem, stream, kFlagPdl, p);
 }
 
 }  // namespace
 
 size_t attend_workspace_bytes(int64_t seqs, int q_heads, int kv_heads, int head_dim, int max_nodes,
                               int sms) {
-  const int rows = max_nodes * (q_heads / kv_heads);
-  const int wide = wide_item_rows(wide_mode(rows));
-  return attend_counter_bytes(sms) +
-         (rows <= kNarrowRows ? 0 : join_head_bytes(seqs * kv_heads * ((rows + wide - 1) / wide))) +
-         (size_t)sms * 2 * attend_slot_floats(rows <= kNarrowRows ? kNarrowRows : wide, head_dim) * sizeof(float);
+  // (the narrow kernel's parts are smaller, and it has no heads of items)
+  const int rows = max_nodes * (q_heads / kv_heads), wide = wide_item_rows(wide_mode(rows));
+  return attend_counter_bytes(sms) + join_head_bytes(seqs * kv_heads * ((rows + wide - 1) / wide)) +
+         (size_t)sms * 2 * attend_slot_floats(wide, head_dim) * sizeof(float);
 }
 
 // The narrow kernel has 16 rows of an item, so from 17 on it would read K and V
 // a second time, or hold two row tiles in registers.  The latter, with 32 rows:
 // 103.5, 102 and 105 us (fp16, e4m3, int8) over 100000 positions, and 35.9 us
-// (fp16) over 32 sequences of 200, where the wide kernel takes 77.8, 95, 83.5
+// (fp16) over 32 sequences of 200, where the wide kernel takes 72.9, 84.6, 75.4
 // and 25.5; over one of 500 (fp16) 13.3 and 15.5, the one case that it loses.
+// With up to 16 rows the narrow kernel begins and ends 2 to 4 us sooner, but has
+// fewer bytes of an fp16 cache in flight than the wide one's ring.  Of 8 rows and
+// 8 key heads (narrow, wide): 500 positions 9.3, 13.1 us; 4000 14.0, 16.8; 16000
+// 23.0, 25.3; 32000 35.0, 33.2; 100000 82.3, 70.4; 16 sequences of 4000 49.5,
+// 45.6; 64 of 1500 79.0, 66.9: even at 64 to 130 MB, taken by what the tables can
+// hold, since the lengths are on the device.  Codes: 8 rows over 100000 positions
+// 69.2, 84 (e4m3) and 70.1, 72.9 (int8): the wide kernel's widening costs more.
 cudaError_t launch_attend(const AttendParams& p, int head_dim, int type, int sms,
                           cudaStream_t stream) {
-  if (p.max_nodes * (p.q_heads / p.c.kv_heads) > kNarrowRows)
+  const double held = (double)p.seqs * (double)p.table_cols * (double)(1 << p.c.page_shift) * p.c.kv_heads * head_dim * 4;
+  if (p.max_nodes * (p.q_heads / p.c.kv_heads) > kNarrowRows || (type == kCacheFp16 && held >= sms * 655360.0))
     return type == kCacheFp16   ? launch_attend_wide<kCacheFp16>(p, head_dim, sms, stream)
            : type == kCacheE4m3 ? launch_attend_wide<kCacheE4m3>(p, head_dim, sms, stream)
                                 : launch_attend_wide<kCacheInt8>(p, head_dim, sms, stream);

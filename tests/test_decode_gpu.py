@@ -152,6 +152,19 @@ def test_attention_scales(nm, kind, nodes, scale):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dim,q_heads", [(128, 8), (64, 56)])
+@pytest.mark.parametrize("ctx,nodes", [([300, 0, 77], [1, 2, 1]), ([2500], [2]), ([40] * 40, [1] * 40)])
+def test_attention_few_rows_of_wide_tables(nm, kind, dim, q_heads, ctx, nodes):
+    """Few query rows, and tables that could hold far more than the sequences do."""
+    b = Batch(kind, ctx, nodes, q_heads, 8, dim, 64, seed=43)
+    wide = torch.full((len(ctx), -(-220 * 2 ** 20 // (len(ctx) * 64 * 8 * dim * 4))), -1, dtype=torch.int32)
+    cols = min(wide.shape[1], b.table.shape[1])
+    wide[:, :cols] = b.table[:, :cols]
+    b.table = wide
+    b.check(nm, f"{kind} {q_heads}x{dim} ctx {ctx}")
+
+
+@pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("page", [8, 64, 128, 1024])
 @pytest.mark.parametrize("nodes", [2, 40])
 def test_attention_pages_and_causal(nm, kind, page, nodes):
