@@ -22,13 +22,7 @@
 
 namespace nmk {
 
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-
-__device__ __forceinline__ float exp2_fast(float x) {  // 2^x, 2^-22 relative, 0 for -inf
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
+constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float log2_fast(float x) {
   float y;

@@ -6,6 +6,14 @@
 
 namespace nmk {
 
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float exp2_fast(float x) {  // 2^x, 2^-22 relative, 0 for -inf
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // 256-bit read-only streaming load (one mask word's 16 fp16 values).
 // Weights are read exactly once per call, so they bypass L1 and are marked
 // evict-first in L2 to leave room for x and y (PTX accepts the L2 eviction

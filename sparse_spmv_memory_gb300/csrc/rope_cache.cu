@@ -68,6 +68,9 @@ __device__ __forceinline__ void turn_of(float p, float f, float m, float& c, flo
 // to `turns` times.  Its lanes compute the token's cos and sin once, two angles
 // each, and hand them round by shuffles; a pair's other half comes from the lane
 // that has it.  No shared memory, no barrier, the next turn's load in flight.
+// What bounds it: latency for few tokens (one token of 48 heads 2.3 us), for many
+// the instructions of angles, shuffles and the codes' divisions (512 tokens of 80
+// heads to e4m3 9.7 us where its 23 MB take 3.4; 2.3 instructions a cycle and SM).
 template <int D, int TYPE>
 __global__ void __launch_bounds__(128) append_kernel(AppendParams p, int turns) {
   constexpr int L = D / 8, HEADS = 32 / L;  // lanes of a head, heads of a turn
@@ -181,7 +184,9 @@ __global__ void __launch_bounds__(128) append_kernel(AppendParams p, int turns) 
 }
 
 // A warp takes a slot: its rows are one 16-byte piece a lane, 32 lanes at a time
-// over the heads, K and V side by side, and both outputs are contiguous.
+// over the heads, K and V side by side, and both outputs are contiguous.  Bound
+// by HBM: 65536 rows of 8 heads from e4m3, a third of the bytes read and two
+// written, take 71 us, 5.7 TB/s.
 template <int D, int TYPE>
 __global__ void __launch_bounds__(256) read_kernel(ReadParams p) {
   constexpr bool F16 = TYPE == kCacheFp16;
@@ -246,8 +251,8 @@ template <int D, int TYPE>
 static cudaError_t append_one(const AppendParams& p, int sms, cudaStream_t stream) {
   const int heads = (p.q_out ? p.q_heads : 0) + 2 * p.c.kv_heads;
   constexpr int kPer = 32 / (D / 8) * 4;  // heads of a block's turn
-  // As many turns as leave every SM 24 warps: the angles are worth more of them,
-  // a single token's latency one.
+  // As many turns as leave every SM 24 warps: a turn more spares a warp its angles
+  // (some 60 instructions a lane), but one token's heads go side by side.
   const int all = (heads + kPer - 1) / kPer;
   int64_t turns = (int64_t)p.tokens * all / (6 * sms);
   turns = turns < 1 ? 1 : turns > all ? all : turns;
