@@ -30,7 +30,7 @@
 //     with 160 KB in flight an SM; of the rest 10 us are start, end and join.
 //   fp16, 256 rows: a stream's chain scores -> softmax -> product.  A tile takes
 //     1.6 us (0.77 softmax, 4 x 0.27 MMAs, two streams in turn), 53 % of the tensor
-//     pipe; 16 sequences of 32 nodes over 8000 positions 96 us, 0.93 PFLOP/s.
+//     pipe; 16 sequences of 32 nodes over 8000 positions 98 us, 0.91 PFLOP/s.
 //     Threads that held 32 scores at a time, with a branch between: 116 us.
 //   codes: the chain raw tile -> widened stage -> MMA -> free stage, 1.6 to 1.9 us a
 //     tile, since two stages of fp16 and six raw tiles fill the shared memory.
