@@ -7,6 +7,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <ATen/ops/zeros.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -74,10 +75,20 @@ bool truth(PyObject* o) {
   return v != 0;
 }
 
-void* stream_of(PyObject* o) {
-  if (o != Py_None) return reinterpret_cast<void*>(static_cast<uintptr_t>(PyLong_AsUnsignedLongLong(o)));
-  return c10::cuda::getCurrentCUDAStream().stream();
-}
+// The stream that a call was given (None: the current one), which is the current
+// one meanwhile: what the call allocates, and the zeros of a workspace, are ordered
+// with its kernels.
+struct OnStream {
+  c10::cuda::OptionalCUDAStreamGuard guard;
+  OnStream(PyObject* o, const Tensor& t) {
+    if (o == Py_None) return;
+    const unsigned long long v = PyLong_AsUnsignedLongLong(o);
+    if (v == (unsigned long long)-1 && PyErr_Occurred()) throw PythonError{};
+    guard.reset_stream(c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(static_cast<uintptr_t>(v)),
+                                                        t.device().index()));
+  }
+  void* stream() const { return c10::cuda::getCurrentCUDAStream().stream(); }
+};
 
 // Whether the dimensions from `first` on are laid out densely.
 bool dense_from(const Tensor& t, int first) {
@@ -193,6 +204,7 @@ PyObject* rope_append(PyObject* const* a) {
   const Tensor* q = tensor(a[11], "q", true);
   const bool want = q || truth(a[12]);
   Tensor made;
+  const OnStream on(a[13], qkv);
   if (want && !q) made = at::empty({tokens, q_heads, c.head_dim}, qkv.options());
   const Tensor* out = q ? q : want ? &made : nullptr;
   if (out && out->dim() == 3 && out->size(1) != q_heads) refuse("q must have q_heads heads");
@@ -200,7 +212,7 @@ PyObject* rope_append(PyObject* const* a) {
                        pointer<int32_t>(&pos), pointer<int64_t>(&slots), pointer<float>(&freq),
                        (int)std::min<int64_t>(2 * freq.numel(), 1 << 20), truth(a[9]) ? 1 : 0,
                        (float)real(a[10]), pointer(out),
-                       out ? head_stride(*out, tokens, c.head_dim, "q") : 0, &c, stream_of(a[13])),
+                       out ? head_stride(*out, tokens, c.head_dim, "q") : 0, &c, on.stream()),
         "nm_rope_append");
   if (!out) Py_RETURN_NONE;
   return wrapped(q, a[11], made);
@@ -219,10 +231,11 @@ PyObject* cache_read(PyObject* const* a) {
       refuse("k and v must be contiguous float16 [rows][kv_heads][head_dim]");
   Tensor mk, mv;
   const auto half = slots.options().dtype(at::kHalf);
+  const OnStream on(a[7], slots);
   if (!k) mk = at::empty({rows, c.kv_heads, c.head_dim}, half);
   if (!v) mv = at::empty({rows, c.kv_heads, c.head_dim}, half);
   check(nm_cache_read(&c, pointer<int64_t>(&slots), rows, pointer(k ? k : &mk), pointer(v ? v : &mv),
-                      stream_of(a[7])),
+                      on.stream()),
         "nm_cache_read");
   return tuple_of({wrapped(k, a[5], mk), wrapped(v, a[6], mv)});
 }
@@ -246,6 +259,7 @@ PyObject* tree_attention(PyObject* const* a) {
     refuse("block_table must be int32 [seqs][entries]");
   if (q_heads > INT32_MAX) refuse("q is too large");
   Tensor mo, ml, mw;
+  const OnStream on(a[14], q);
   if (!out) mo = at::empty({tokens, q_heads, c.head_dim}, q.options());
   const Tensor& o = out ? *out : mo;
   const int64_t ldo = head_stride(o, tokens, c.head_dim, "out");
@@ -265,7 +279,7 @@ PyObject* tree_attention(PyObject* const* a) {
                           pointer<int32_t>(&ctx), pointer<uint64_t>(mask),
                           a[10] == Py_None ? 1.0f / std::sqrt((float)c.head_dim) : (float)real(a[10]),
                           pointer(&o), ldo, pointer<float>(&l), pointer(&work), work.nbytes(),
-                          stream_of(a[14])),
+                          on.stream()),
         "nm_tree_attention");
   return tuple_of({wrapped(out, a[11], mo), wrapped(lse, a[12], ml)});
 }
@@ -297,6 +311,7 @@ PyObject* tree_verify(PyObject* const* a) {
   const int64_t ldd = rows(draft, n, "draft"), ldr = rows(race, seqs, "race");
   const auto i32 = logits.options().dtype(at::kInt);
   Tensor mp, mc, mt;
+  const OnStream on(a[12], logits);
   if (!path) mp = at::empty({seqs, std::max(0, max_nodes)}, i32);
   if (!count) mc = at::empty({seqs}, i32);
   if (!token) mt = at::empty({seqs}, i32);
@@ -308,7 +323,7 @@ PyObject* tree_verify(PyObject* const* a) {
                        seqs, max_nodes, pointer<float>(accept), pointer<float>(race), ldr,
                        (float)real(a[8]), pointer<int32_t>(path ? path : &mp),
                        pointer<int32_t>(count ? count : &mc), pointer<int32_t>(token ? token : &mt),
-                       stream_of(a[12])),
+                       on.stream()),
         "nm_tree_verify");
   return tuple_of({wrapped(path, a[9], mp), wrapped(count, a[10], mc), wrapped(token, a[11], mt)});
 }

@@ -323,6 +323,33 @@ def test_attention_workspace_of_other_shapes(nm, kind):
             calls[i].check(nm, f"turn {turn}, call {i}", workspace=ws)
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("nodes", [1, 24])
+def test_attention_workspace_of_a_given_stream(nm, kind, nodes):
+    """The zeros of a workspace that a call makes for itself are there before its
+    kernels on the stream that it was given, however busy the current one is."""
+    b = Batch(kind, [9000, 400], [nodes, nodes], 8, 2, 128, 64, seed=35)
+    want = b.check(nm, "on the current stream")
+    need = nm.nm_tree_attention_workspace_bytes(2, 8, 2, 128, nodes)
+    args = cuda(b.q, b.k, b.v, b.table, torch.tensor(b.ctx, dtype=torch.int32),
+                torch.tensor(b.start, dtype=torch.int32))
+    ks, vs = cuda(b.ks, b.vs)
+    mask = signed(b.masks).cuda()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        used = torch.full((need,), 255, dtype=torch.uint8, device="cuda")  # what the allocator gives next
+        torch.cuda.synchronize()
+        del used
+        torch.cuda._sleep(100_000_000)
+        out, lse = nm.nm_tree_attention(*args, nodes, tree_mask=mask, k_scale=ks, v_scale=vs, stream=side)
+        side.synchronize()
+        with torch.cuda.stream(side):
+            same = bool((out == want[0]).all()) and bool((lse == want[1]).all())
+        torch.cuda.synchronize()
+        assert same
+
+
 def test_attention_long_offsets(nm):
     """A cache whose byte and element offsets pass 2^32: the sequence's pages lie
     at both of its ends."""
