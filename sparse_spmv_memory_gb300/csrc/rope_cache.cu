@@ -70,7 +70,7 @@ __device__ __forceinline__ void turn_of(float p, float f, float m, float& c, flo
 // that has it.  No shared memory, no barrier, the next turn's load in flight.
 // What bounds it: latency for few tokens (one token of 48 heads 2.3 us), for many
 // the instructions of angles, shuffles and the codes' divisions (512 tokens of 80
-// heads to e4m3 9.7 us where its 23 MB take 3.4; 2.3 instructions a cycle and SM).
+// heads to e4m3 6.5 us where its bytes take 3).
 template <int D, int TYPE>
 __global__ void __launch_bounds__(128) append_kernel(AppendParams p, int turns) {
   constexpr int L = D / 8, HEADS = 32 / L;  // lanes of a head, heads of a turn
@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(128) append_kernel(AppendParams p, int turns) 
 // A warp takes a slot: its rows are one 16-byte piece a lane, 32 lanes at a time
 // over the heads, K and V side by side, and both outputs are contiguous.  Bound
 // by HBM: 65536 rows of 8 heads from e4m3, a third of the bytes read and two
-// written, take 71 us, 5.7 TB/s.
+// written, take 64 us, 6.4 TB/s.
 template <int D, int TYPE>
 __global__ void __launch_bounds__(256) read_kernel(ReadParams p) {
   constexpr bool F16 = TYPE == kCacheFp16;
@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(256) read_kernel(ReadParams p) {
     const int64_t slot = p.slots[r];
     const bool there = slot >= 0 && slot < (p.c.pages << p.c.page_shift);
     const int64_t page = slot >> p.c.page_shift, off = slot & ((1 << p.c.page_shift) - 1);
-#pragma unroll 2
+#pragma unroll 4
     for (int h = lane / L; h < H; h += HEADS) {
       const int64_t in_page = ((int64_t)h << p.c.page_shift) + off;
       const int64_t at = page * p.c.page_stride + in_page * D + piece * E;
@@ -251,10 +251,11 @@ template <int D, int TYPE>
 static cudaError_t append_one(const AppendParams& p, int sms, cudaStream_t stream) {
   const int heads = (p.q_out ? p.q_heads : 0) + 2 * p.c.kv_heads;
   constexpr int kPer = 32 / (D / 8) * 4;  // heads of a block's turn
-  // As many turns as leave every SM 24 warps: a turn more spares a warp its angles
-  // (some 60 instructions a lane), but one token's heads go side by side.
+  // As many turns as leave every SM 44 warps: a turn more spares a warp its angles
+  // (some 60 instructions a lane), but one token's heads go side by side.  512
+  // tokens of 80 heads: 3 turns 6.4 us, 4 7.4, 5 (24 warps) 9.6, 2 7.0.
   const int all = (heads + kPer - 1) / kPer;
-  int64_t turns = (int64_t)p.tokens * all / (6 * sms);
+  int64_t turns = ((int64_t)p.tokens * all + 11 * sms / 2) / (11 * sms);
   turns = turns < 1 ? 1 : turns > all ? all : turns;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.tokens, (unsigned)((all + turns - 1) / turns));
@@ -282,9 +283,12 @@ cudaError_t launch_rope_append(const AppendParams& p, int head_dim, int type, in
 
 template <int D, int TYPE>
 static cudaError_t read_one(const ReadParams& p, int sms, cudaStream_t stream) {
-  // eight blocks' warps fill an SM; a long read's warps take several rows each
+  // Several times the blocks that fit at once, so that those that end early make
+  // room for others; a long read's warps take several rows each.  65536 rows of 8
+  // heads, fp16, e4m3 and int8: 79.8, 63.8 and 62.8 us; 20 blocks an SM 81.9, 64.3
+  // and 65.5; 8 83.7, 71.1 and 76.3; 5 92.6, 85.0 and 72.7.
   const int64_t blocks = ((int64_t)p.rows + 7) / 8;
-  return launch_kernel(read_kernel<D, TYPE>, (int)(blocks < 8 * sms ? blocks : 8 * sms), 256, 0, stream,
+  return launch_kernel(read_kernel<D, TYPE>, (int)(blocks < 32 * sms ? blocks : 32 * sms), 256, 0, stream,
                        kFlagPdl, p);
 }
 

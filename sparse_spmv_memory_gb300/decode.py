@@ -10,6 +10,9 @@ float16, float8_e4m3fn or int8 (the dtype names what it holds; any page stride,
 the inner three dimensions contiguous), and for the 8-bit types ``k_scale`` and
 ``v_scale`` float32 [pages][kv_heads][page_size].  A slot is
 page * page_size + offset.
+
+``stream`` is a torch.cuda.Stream or a raw cudaStream_t (None: the current one);
+outputs and workspaces that a call makes itself are allocated on that stream.
 """
 from __future__ import annotations
 
