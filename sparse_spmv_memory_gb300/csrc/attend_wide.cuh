@@ -693,7 +693,13 @@ __global__ void __launch_bounds__(Wide<D, TYPE, MODE>::THREADS, 1)
       const int tiles = PAIR && rows == 0 ? 0 : (n - off0 + step - 1) / step;
       // this stream has the item's last scores (or reads none of its queries)
       const bool asks = have && (PAIR || b == ((n - 1) & 1));
-      if (PAIR && asks && tiles == 0) ask_q(w2, si2);
+      if (PAIR && asks && tiles == 0) {
+        // A stream without rows waits for no scores.  It waits here until both
+        // have announced this item's queries: an arrival for the next item before
+        // the other stream's would complete this item's phase in its place.
+        ask_q(w2, si2);
+        ok = wait_warp(qfull, item_no & 1);
+      }
       for (int k = 0; k < tiles; ++k) {
         const int i = off0 + k * step;
         ok = wait_warp(sfull(b), ns++ & 1);

@@ -716,6 +716,26 @@ def test_attention_rows_of_every_tile(nm, kind, nodes):
     b.check(nm, f"{kind} {7 * nodes} rows, negative scale")
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("q_heads,kv_heads,nodes,ns", [
+    (64, 8, 33, [1, 33, 3, 1, 2, 1, 5, 4] * 2),      # most sequences have one of two row tiles
+    (16, 2, 64, [64, 7, 1, 12, 0, 16, 30, 1] * 2),
+    (28, 4, 40, [40, 18, 19, 3] * 2),                # 280, 126, 133, 21 rows: last tiles of 24 and 133
+    (64, 1, 6, [6] * 12)])                           # 384: every sequence's second tile has 128
+def test_attention_batches_with_one_of_two_row_tiles(nm, kind, q_heads, kv_heads, nodes, ns):
+    """More than 128 rows a key head at most, but items that have no more than 128,
+    and many of them in a block (a long sequence makes the blocks' ranges long): one
+    of the block's two streams is idle."""
+    rnd = random.Random(q_heads + nodes)
+    ctx = [60000 if kv_heads < 4 else 30000] + [rnd.choice([0, 5, 100, 127, 128, 250]) for _ in ns]
+    b = Batch(kind, ctx, [1] + ns, q_heads, kv_heads, 64, 16, seed=nodes)
+    first = b.check(nm, f"{kind} {q_heads}/{kv_heads}")
+    for _ in range(20):
+        out, lse = b.run(nm)
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    assert nm.nm_wait_timeouts() == 0
+
+
 @pytest.mark.parametrize("drafted", [True, False])
 @pytest.mark.parametrize("vocab", [131073, 140001, 300007])
 def test_verify_long_vocabularies(nm, drafted, vocab):
