@@ -175,10 +175,11 @@ __global__ void __launch_bounds__(Wide<D, TYPE, MODE>::THREADS, 1)
   using W = Wide<D, TYPE, MODE>;
   constexpr bool F16 = W::F16, PAIR = W::PAIR;
   constexpr int RS = F16 ? 1 : W::RS, SPLIT = W::SPLIT;
+  constexpr int RB = F16 ? W::NS : RS;  // barriers of tiles that landed
   constexpr int IROWS = W::IROWS;
   using Sched = Schedule<IROWS, kKeys, W::THREADS>;
   extern __shared__ uint8_t raw_smem[];
-  __shared__ uint64_t bar_mem[2 * W::NS + 8 + 2 * RS + 2];
+  __shared__ uint64_t bar_mem[2 * W::NS + 8 + RB + RS + 2];
   __shared__ uint32_t tmem_slot;
   __shared__ uint32_t there_of[kMeta];
   __shared__ uint32_t bad_of[kBad][2];
@@ -198,9 +199,10 @@ __global__ void __launch_bounds__(Wide<D, TYPE, MODE>::THREADS, 1)
   auto pfull = [&](int b) { return bars + 8u * (2 * W::NS + 2 + b); };  // weights ready
   auto ofull = [&](int b) { return bars + 8u * (2 * W::NS + 4 + b); };  // sums ready
   const uint32_t qfull = bars + 8u * (2 * W::NS + 6), soft = bars + 8u * (2 * W::NS + 7);
-  auto rfull = [&](int s) { return bars + 8u * (2 * W::NS + 8 + s); };        // raw tile landed
-  auto rfree = [&](int s) { return bars + 8u * (2 * W::NS + 8 + RS + s); };   // ... and read
-  auto phalf = [&](int b) { return bars + 8u * (2 * W::NS + 8 + 2 * RS + b); };  // PARTS == 2: the first half of the weights
+  // a raw tile landed; fp16: a stage that the loaders look at before it is full
+  auto rfull = [&](int s) { return bars + 8u * (2 * W::NS + 8 + s); };
+  auto rfree = [&](int s) { return bars + 8u * (2 * W::NS + 8 + RB + s); };   // 8-bit: ... and read
+  auto phalf = [&](int b) { return bars + 8u * (2 * W::NS + 8 + RB + RS + b); };  // PARTS == 2: the first half of the weights
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_launch_dependents();
@@ -211,10 +213,8 @@ __global__ void __launch_bounds__(Wide<D, TYPE, MODE>::THREADS, 1)
       mbar_init(full(s), F16 ? W::LW : W::CW);
       mbar_init(empty(s), 1);
     }
-    for (int s = 0; s < RS; ++s) {
-      mbar_init(rfull(s), 1);
-      mbar_init(rfree(s), W::CW);
-    }
+    for (int s = 0; s < RB; ++s) mbar_init(rfull(s), 1);
+    for (int s = 0; s < RS; ++s) mbar_init(rfree(s), W::CW);
     for (int b = 0; b < 2; ++b) {
       mbar_init(sfull(b), 1);
       mbar_init(pfull(b), 4);
@@ -260,7 +260,8 @@ __global__ void __launch_bounds__(Wide<D, TYPE, MODE>::THREADS, 1)
     // blocks' parts and the code among it, stays there)
     const uint64_t once = l2_evict_first();
     int c = 0;  // positions of the ring so far
-    int item_no = 0, tile_no = 0, looked = 0;
+    int item_no = 0, tile_no = 0;
+    uint32_t looked = 0;  // fp16: parity of each stage's looks so far
     bool ok = true;
     struct Tile {      // a tile of an item; lane l has box l
       int page, row;   // the box's page and first row in it (of all heads')
@@ -298,7 +299,10 @@ __global__ void __launch_bounds__(Wide<D, TYPE, MODE>::THREADS, 1)
       const uint32_t dst = sT + st * W::TILE;
       if (!v && lw == 0) note(t, first);
       const bool look = v && t.edge;  // absent rows are to be zeros, nodes' rows are looked at
-      const uint32_t bar = look ? rfull(0) : full(st);
+      // The look has a barrier of the stage's own: no warp can be a look of this
+      // stage ahead of another, since the stage is not empty again before all have
+      // arrived on `full`.
+      const uint32_t bar = look ? rfull(st) : full(st);
       if (lw == 0) {
         if (lane == 0 && (t.have || !look)) mbar_arrive_expect_tx(bar, t.have * page_rows * D * 2);
         __syncwarp();
@@ -313,7 +317,10 @@ __global__ void __launch_bounds__(Wide<D, TYPE, MODE>::THREADS, 1)
         mbar_arrive(full(st));
       }
       if (look) {
-        if (t.have && !wait_warp(bar, looked++ & 1)) return false;
+        if (t.have) {
+          if (!wait_warp(bar, (looked >> st) & 1u)) return false;
+          looked ^= 1u << st;
+        }
         constexpr int PR = D / 8;
         for (int id = lt; id < kKeys * PR; id += LT) {
           const int r = id / PR, ch = id % PR;

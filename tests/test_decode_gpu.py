@@ -736,6 +736,24 @@ def test_attention_batches_with_one_of_two_row_tiles(nm, kind, q_heads, kv_heads
     assert nm.nm_wait_timeouts() == 0
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("q_heads,nodes", [(8, 3), (16, 5), (64, 3)])
+def test_attention_batches_of_edge_tiles(nm, dim, q_heads, nodes):
+    """Every value tile of an fp16 cache has nodes or absent rows in it, so that each
+    is looked at before the product; many such items follow one another in a block,
+    and a page that is missing altogether now and then."""
+    rnd = random.Random(q_heads)
+    ctx = [rnd.randrange(100) for _ in range(160)] + [40000]
+    b = Batch("fp16", ctx, [rnd.randint(1, nodes) for _ in range(160)] + [1], q_heads, 1, dim, 16, seed=q_heads)
+    for s in range(0, 160, 7):
+        b.table[s, 0] = -1
+    first = b.check(nm, f"{q_heads}x{dim}")
+    for _ in range(20):
+        out, lse = b.run(nm)
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    assert nm.nm_wait_timeouts() == 0
+
+
 @pytest.mark.parametrize("drafted", [True, False])
 @pytest.mark.parametrize("vocab", [131073, 140001, 300007])
 def test_verify_long_vocabularies(nm, drafted, vocab):
