@@ -222,6 +222,34 @@ int nm_tree_verify(const void *logits, int logits_fp32, int64_t ld_logits, int64
                    int64_t ld_race, float temperature, int32_t *path, int32_t *count,
                    int32_t *token, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * nm_tree_attention_stall_selftest, nm_tree_verify_stall_selftest -- exercise
+ * the bounded waits (self-tests): the calls above with every wait limited to
+ * wait_limit_us (1 .. 2,000,000) and an arrival that never comes.  The many-row
+ * attention kernel's loaders issue nothing (a call that goes to the few-row
+ * kernel runs as usual: that one has no waits); of each sequence's blocks in
+ * nm_tree_verify the last sends nothing to the first.  The waits run out or give
+ * up after the first that did, are counted in nm_wait_timeouts(), and the kernel
+ * returns with its outputs undefined (verify: not written); the device stays
+ * usable.  Until nm_wait_timeouts(1) these kernels' calls do nothing.
+ * Asynchronous; NM_OK once launched.
+ * ------------------------------------------------------------------------- */
+int nm_tree_attention_stall_selftest(const void *q, int64_t ldq, int64_t tokens, int q_heads,
+                                     int64_t seqs, const int32_t *q_start, int max_nodes,
+                                     const nm_cache *cache, const int32_t *block_table,
+                                     int64_t ld_table, int64_t table_cols, const int32_t *ctx_len,
+                                     const uint64_t *tree_mask, float scale, void *out,
+                                     int64_t ldo, float *lse, void *workspace,
+                                     size_t workspace_bytes, int64_t wait_limit_us, void *stream);
+int nm_tree_verify_stall_selftest(const void *logits, int logits_fp32, int64_t ld_logits,
+                                  int64_t vocab, const float *draft, int64_t ld_draft,
+                                  const int32_t *ids, const int32_t *parents,
+                                  const int32_t *node_start, int64_t tokens, int64_t seqs,
+                                  int max_nodes, const float *accept, const float *race,
+                                  int64_t ld_race, float temperature, int32_t *path,
+                                  int32_t *count, int32_t *token, int64_t wait_limit_us,
+                                  void *stream);
+
 #ifdef __cplusplus
 }
 #endif

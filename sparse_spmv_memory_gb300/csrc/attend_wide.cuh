@@ -206,7 +206,10 @@ __global__ void __launch_bounds__(Wide<D, TYPE, MODE>::THREADS, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_launch_dependents();
-  if (__syncthreads_or(threadIdx.x == 0 && wait_aborted())) return;
+  if (__syncthreads_or(threadIdx.x == 0 && wait_aborted())) {
+    pdl_wait_previous();  // what follows on the stream is after the kernels before this one
+    return;
+  }
   // what touches no caller's memory comes before the wait for the last kernel
   if (warp == 0 && lane == 0) {
     for (int s = 0; s < W::NS; ++s) {
@@ -245,7 +248,7 @@ __global__ void __launch_bounds__(Wide<D, TYPE, MODE>::THREADS, 1)
   const Heads heads(G);
   const float cs = p.scale * kLog2e;
   auto wait_warp = [&](uint32_t bar, uint32_t par) {
-    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, par)) != 0;
+    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, par, p.wait_limit_ns)) != 0;
   };
 
   if (!work) {
@@ -262,7 +265,7 @@ __global__ void __launch_bounds__(Wide<D, TYPE, MODE>::THREADS, 1)
     int c = 0;  // positions of the ring so far
     int item_no = 0, tile_no = 0;
     uint32_t looked = 0;  // fp16: parity of each stage's looks so far
-    bool ok = true;
+    bool ok = !p.stall;
     struct Tile {      // a tile of an item; lane l has box l
       int page, row;   // the box's page and first row in it (of all heads')
       bool on;         // it is there
@@ -999,6 +1002,7 @@ __global__ void __launch_bounds__(Wide<D, TYPE, MODE>::THREADS, 1)
       tc_fence_before_sync();
       if (!PAIR) ok = soft_sync();  // nobody reads the other stream's sums any more
     }
+    cp_async_wait_all();  // (queries asked for before a wait gave up)
   }
 
   // ---- teardown: MMAs that were issued are done before TMEM is freed

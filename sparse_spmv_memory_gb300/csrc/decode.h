@@ -12,6 +12,7 @@ namespace nmk {
 constexpr int kCacheFp16 = 0, kCacheE4m3 = 1, kCacheInt8 = 2;
 
 constexpr int kMaxNodes = 64;  // nodes of a tree: the bits of a mask word
+constexpr uint64_t kDecodeWaitNs = 2000000000ull;  // the kernels' waits give up after this
 
 struct CacheView {
   uint8_t *k, *v;           // codes or fp16
@@ -65,6 +66,8 @@ struct AttendParams {
   int64_t ldo;
   float* lse;  // may be null
   uint8_t* workspace;
+  uint64_t wait_limit_ns;  // bound of every wait in the many-row kernel
+  int stall;               // self-test: its loaders issue nothing
 };
 size_t attend_workspace_bytes(int64_t seqs, int q_heads, int kv_heads, int head_dim, int max_nodes,
                               int sms);
@@ -92,6 +95,8 @@ struct VerifyParams {
   int64_t ld_race;
   float temperature;
   int32_t *path, *count, *token;
+  uint64_t wait_limit_ns;  // bound of every wait
+  int stall;               // self-test: a cluster's last block sends nothing to its first
 };
 cudaError_t launch_verify(const VerifyParams& p, int logits_fp32, int sms, cudaStream_t stream);
 cudaError_t read_verify_wait_timeouts(unsigned long long* count, int reset);

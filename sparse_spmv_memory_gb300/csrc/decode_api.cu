@@ -183,12 +183,12 @@ size_t nm_tree_attention_workspace_bytes(int64_t seqs, int q_heads, int kv_heads
   return attend_workspace_bytes(seqs, q_heads, kv_heads, head_dim, max_nodes, sms);
 }
 
-int nm_tree_attention(const void* q, int64_t ldq, int64_t tokens, int q_heads, int64_t seqs,
-                      const int32_t* q_start, int max_nodes, const nm_cache* cache,
-                      const int32_t* block_table, int64_t ld_table, int64_t table_cols,
-                      const int32_t* ctx_len, const uint64_t* tree_mask, float scale, void* out,
-                      int64_t ldo, float* lse, void* workspace, size_t workspace_bytes,
-                      void* stream) {
+static int tree_attention(const void* q, int64_t ldq, int64_t tokens, int q_heads, int64_t seqs,
+                          const int32_t* q_start, int max_nodes, const nm_cache* cache,
+                          const int32_t* block_table, int64_t ld_table, int64_t table_cols,
+                          const int32_t* ctx_len, const uint64_t* tree_mask, float scale, void* out,
+                          int64_t ldo, float* lse, void* workspace, size_t workspace_bytes,
+                          void* stream, uint64_t wait_limit_ns, int stall) {
   if (!q || !q_start || !block_table || !ctx_len || !out) return NM_ERR_NULL;
   AttendParams p;
   const int st = check_cache(cache, &p.c);
@@ -233,16 +233,42 @@ int nm_tree_attention(const void* q, int64_t ldq, int64_t tokens, int q_heads, i
   p.ldo = ldo;
   p.lse = lse;
   p.workspace = static_cast<uint8_t*>(workspace);
+  p.wait_limit_ns = wait_limit_ns;
+  p.stall = stall;
   return status(launch_attend(p, cache->head_dim, cache->type, sms,
                               static_cast<cudaStream_t>(stream)));
 }
 
-int nm_tree_verify(const void* logits, int logits_fp32, int64_t ld_logits, int64_t vocab,
-                   const float* draft, int64_t ld_draft, const int32_t* ids,
-                   const int32_t* parents, const int32_t* node_start, int64_t tokens,
-                   int64_t seqs, int max_nodes, const float* accept, const float* race,
-                   int64_t ld_race, float temperature, int32_t* path, int32_t* count,
-                   int32_t* token, void* stream) {
+int nm_tree_attention(const void* q, int64_t ldq, int64_t tokens, int q_heads, int64_t seqs,
+                      const int32_t* q_start, int max_nodes, const nm_cache* cache,
+                      const int32_t* block_table, int64_t ld_table, int64_t table_cols,
+                      const int32_t* ctx_len, const uint64_t* tree_mask, float scale, void* out,
+                      int64_t ldo, float* lse, void* workspace, size_t workspace_bytes,
+                      void* stream) {
+  return tree_attention(q, ldq, tokens, q_heads, seqs, q_start, max_nodes, cache, block_table,
+                        ld_table, table_cols, ctx_len, tree_mask, scale, out, ldo, lse, workspace,
+                        workspace_bytes, stream, kDecodeWaitNs, 0);
+}
+
+int nm_tree_attention_stall_selftest(const void* q, int64_t ldq, int64_t tokens, int q_heads,
+                                     int64_t seqs, const int32_t* q_start, int max_nodes,
+                                     const nm_cache* cache, const int32_t* block_table,
+                                     int64_t ld_table, int64_t table_cols, const int32_t* ctx_len,
+                                     const uint64_t* tree_mask, float scale, void* out, int64_t ldo,
+                                     float* lse, void* workspace, size_t workspace_bytes,
+                                     int64_t wait_limit_us, void* stream) {
+  if (wait_limit_us < 1 || wait_limit_us > 2000000) return NM_ERR_SHAPE;
+  return tree_attention(q, ldq, tokens, q_heads, seqs, q_start, max_nodes, cache, block_table,
+                        ld_table, table_cols, ctx_len, tree_mask, scale, out, ldo, lse, workspace,
+                        workspace_bytes, stream, (uint64_t)wait_limit_us * 1000u, 1);
+}
+
+static int tree_verify(const void* logits, int logits_fp32, int64_t ld_logits, int64_t vocab,
+                       const float* draft, int64_t ld_draft, const int32_t* ids,
+                       const int32_t* parents, const int32_t* node_start, int64_t tokens,
+                       int64_t seqs, int max_nodes, const float* accept, const float* race,
+                       int64_t ld_race, float temperature, int32_t* path, int32_t* count,
+                       int32_t* token, void* stream, uint64_t wait_limit_ns, int stall) {
   if (!logits || !ids || !parents || !node_start || !path || !count || !token) return NM_ERR_NULL;
   if (!(temperature >= 0.0f) || !isfinite(temperature)) return NM_ERR_SHAPE;
   if (temperature > 0.0f && (!accept || !race)) return NM_ERR_NULL;
@@ -283,7 +309,34 @@ int nm_tree_verify(const void* logits, int logits_fp32, int64_t ld_logits, int64
   p.path = path;
   p.count = count;
   p.token = token;
+  p.wait_limit_ns = wait_limit_ns;
+  p.stall = stall;
   return status(launch_verify(p, logits_fp32, sms, static_cast<cudaStream_t>(stream)));
+}
+
+int nm_tree_verify(const void* logits, int logits_fp32, int64_t ld_logits, int64_t vocab,
+                   const float* draft, int64_t ld_draft, const int32_t* ids,
+                   const int32_t* parents, const int32_t* node_start, int64_t tokens,
+                   int64_t seqs, int max_nodes, const float* accept, const float* race,
+                   int64_t ld_race, float temperature, int32_t* path, int32_t* count,
+                   int32_t* token, void* stream) {
+  return tree_verify(logits, logits_fp32, ld_logits, vocab, draft, ld_draft, ids, parents,
+                     node_start, tokens, seqs, max_nodes, accept, race, ld_race, temperature, path,
+                     count, token, stream, kDecodeWaitNs, 0);
+}
+
+int nm_tree_verify_stall_selftest(const void* logits, int logits_fp32, int64_t ld_logits,
+                                  int64_t vocab, const float* draft, int64_t ld_draft,
+                                  const int32_t* ids, const int32_t* parents,
+                                  const int32_t* node_start, int64_t tokens, int64_t seqs,
+                                  int max_nodes, const float* accept, const float* race,
+                                  int64_t ld_race, float temperature, int32_t* path,
+                                  int32_t* count, int32_t* token, int64_t wait_limit_us,
+                                  void* stream) {
+  if (wait_limit_us < 1 || wait_limit_us > 2000000) return NM_ERR_SHAPE;
+  return tree_verify(logits, logits_fp32, ld_logits, vocab, draft, ld_draft, ids, parents,
+                     node_start, tokens, seqs, max_nodes, accept, race, ld_race, temperature, path,
+                     count, token, stream, (uint64_t)wait_limit_us * 1000u, 1);
 }
 
 }  // extern "C"

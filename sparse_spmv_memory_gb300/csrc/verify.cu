@@ -182,6 +182,11 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(VerifyParams p, int
     mbar_init(bars + 8, 1);
     fence_mbar_init();
   }
+  // No wait of the block's gave up, and none of another's before it began.  It is
+  // one value for the whole block, so that its warps leave the walk together: a
+  // block that leaves keeps its shared memory until the cluster ends, and the
+  // others' next wait, for what it does not send any more, has its limit too.
+  bool ok = !__syncthreads_or(threadIdx.x == 0 && wait_aborted());
   // every block's barriers are there before another's store can arrive
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -191,7 +196,6 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(VerifyParams p, int
   const int groups = (V + 7) / 8;
   const bool more = HELD * stride < groups;  // a longer vocabulary than the cluster holds
   int round = 0;
-  bool ok = true;  // no wait gave up
 
   // The values of all threads of the cluster, joined (the same in every thread);
   // none: op's neutral value.  A box is written again two exchanges on: a block
@@ -205,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(VerifyParams p, int
     if (warp == 0) {
       v = lanes_join<kWarps>(warps[lane & (kWarps - 1)], op);
       if (lane == 0) mbar_arrive_expect_tx(bar, cl * 8);
-      if (lane < (int)cl) {
+      if (lane < (int)cl && !(p.stall && rank == cl - 1 && lane == 0)) {
         uint32_t at, rbar;
         asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(&box[r][rank])), "r"(lane));
         asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(rbar) : "r"(bar), "r"(lane));
@@ -214,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(VerifyParams p, int
                      : "memory");
       }
     }
-    ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar, (round >> 1) & 1)) && ok;
+    ok = __syncthreads_and(warp != 0 || mbar_wait(bar, (round >> 1) & 1, p.wait_limit_ns));
     ++round;
     return lanes_join<kMaxCluster>((lane & (kMaxCluster - 1)) < (int)cl ? box[r][lane & (kMaxCluster - 1)] : none, op);
   };
@@ -283,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(VerifyParams p, int
   };
 
   int cur = 0, len = 0, token = -1;
-  if (n > 0) {
+  if (n > 0 && ok) {
     // lane l has the nodes l and l + 32
     int par[2], id[2];
     float u[2];

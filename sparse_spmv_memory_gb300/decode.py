@@ -51,6 +51,9 @@ def declare(L) -> None:
         "nm_tree_verify": ([P, I32, I64, I64, P, I64, P, P, P, I64, I64, I32, P, P, I64, F32, P,
                             P, P, P], I32),
     }
+    for name in ("nm_tree_attention", "nm_tree_verify"):  # the same and a limit, before the stream
+        args, res = sig[name]
+        sig[name + "_stall_selftest"] = (args[:-1] + [I64, P], res)
     for name, (args, res) in sig.items():
         f = getattr(L, name)
         f.argtypes = args

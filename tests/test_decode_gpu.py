@@ -859,5 +859,75 @@ def test_example_decodes_as_one_token_at_a_time(nm, cache):
     assert len(warm) == 12 and all(0 <= t < ex.VOCAB for t in warm)
 
 
+# ---- waits that give up -----------------------------------------------------------------
+def stalled(nm, call, limit_s=2.0):
+    """Runs a call whose arrival never comes: it ends after about its limit (20 ms)
+    and is counted, the next call of its kind does nothing, and after a reset the
+    count is zero again."""
+    import time
+    torch.cuda.synchronize()
+    nm.nm_wait_timeouts(reset=True)
+    t0 = time.time()
+    assert call() == 0
+    torch.cuda.synchronize()
+    assert time.time() - t0 < limit_s
+    assert nm.nm_wait_timeouts() > 0
+
+
+@pytest.mark.parametrize("drafted", [True, False])
+@pytest.mark.parametrize("vocab", [300, 20000, 128256])
+@pytest.mark.parametrize("temperature", [0.0, 0.9])
+def test_verify_wait_that_gives_up(nm, drafted, vocab, temperature):
+    """One block of a sequence never hears of another (or of itself): it gives up,
+    the others at their next exchange, in every sequence; the kernel ends."""
+    case = verify_case(vocab, 5, 9, vocab, drafted, temperature, False)
+    logits, ids, parents, start, accept, race, q = cuda(*(None if a is None else torch.from_numpy(a)
+                                                          for a in case[:7]))
+    path = torch.full((5, 9), -7, dtype=torch.int32, device="cuda")
+    count, token = (torch.full((5,), -7, dtype=torch.int32, device="cuda") for _ in range(2))
+    P = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    stalled(nm, lambda: nm.lib().nm_tree_verify_stall_selftest(
+        P(logits), 0, vocab, vocab, P(q), vocab, P(ids), P(parents), P(start), len(ids), 5, 9, P(accept),
+        P(race), vocab, temperature, P(path), P(count), P(token), 20000, torch.cuda.current_stream().cuda_stream))
+    # until the reset calls return without an answer, all blocks of a cluster alike
+    count.fill_(-9)
+    token.fill_(-9)
+    run_verify(nm, case, 9, temperature, count=count, token=token)
+    torch.cuda.synchronize()
+    assert (count == -9).all() and (token == -9).all()
+    nm.nm_wait_timeouts(reset=True)
+    same(run_verify(nm, case, 9, temperature), case[7])
+    assert nm.nm_wait_timeouts() == 0
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("nodes", [3, 6, 12, 40])
+def test_attention_wait_that_gives_up(nm, kind, nodes):
+    """The loaders of the many-row kernel bring nothing: every role gives up, tensor
+    memory is freed, and the call after a reset is right."""
+    from sparse_spmv_memory_gb300.decode import _Cache
+    import ctypes
+    b = Batch(kind, [700, 90, 1500], [nodes, 1, nodes], 16, 2, 128, 16, seed=51)
+    k, v, ks, vs, q = cuda(b.k, b.v, b.ks, b.vs, b.q)
+    table, ctx, start = cuda(b.table, torch.tensor(b.ctx, dtype=torch.int32), torch.tensor(b.start, dtype=torch.int32))
+    mask = signed(b.masks).cuda()
+    T = q.shape[0]
+    out, lse = torch.zeros_like(q), torch.zeros((T, 16), device="cuda")
+    need = nm.nm_tree_attention_workspace_bytes(3, 16, 2, 128, nodes)
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    P = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    c = _Cache(k=P(k), v=P(v), k_scale=P(ks), v_scale=P(vs), pages=k.shape[0], page_stride=2 * 16 * 128,
+               scale_page_stride=32, kv_heads=2, page_size=16, head_dim=128, type=KINDS.index(kind))
+    stalled(nm, lambda: nm.lib().nm_tree_attention_stall_selftest(
+        P(q), 16 * 128, T, 16, 3, P(start), nodes, ctypes.byref(c), P(table), table.shape[1], table.shape[1],
+        P(ctx), P(mask), b.scale, P(out), 16 * 128, P(lse), P(ws), need, 20000,
+        torch.cuda.current_stream().cuda_stream))
+    b.run(nm, workspace=ws)  # returns without an answer
+    torch.cuda.synchronize()
+    nm.nm_wait_timeouts(reset=True)
+    b.check(nm, f"{kind} after a reset", workspace=ws)
+    assert nm.nm_wait_timeouts() == 0
+
+
 def test_no_bounded_wait_gave_up(nm):
     assert nm.nm_wait_timeouts() == 0

@@ -175,6 +175,16 @@ def test_verify_refused(nm):
     assert call(t=0.0, acc=None, race=None, draft=None, seqs=0) == 0
 
 
+def test_stall_selftests_refuse_a_limit_out_of_range(nm):
+    L, c = nm.lib(), cache()
+    o = 0x500000000
+    for limit in (0, -5, 2000001):
+        assert L.nm_tree_verify_stall_selftest(o, 0, 8, 8, None, 0, o, o, o, 4, 0, 4, None, None, 0, 0.0,
+                                               o, o, o, limit, None) == 2
+        assert L.nm_tree_attention_stall_selftest(o, 256, 8, 4, 0, o, 4, ref(c), o, 4, 4, o, None, 1.0,
+                                                  o, 256, None, None, 0, limit, None) == 2
+
+
 def test_binding_refuses_cpu_tensors_and_wrong_types(nm):
     k = torch.zeros((2, 1, 8, 64), dtype=torch.float16)
     with pytest.raises(ValueError, match="CUDA"):
