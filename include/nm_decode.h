@@ -140,7 +140,9 @@ int nm_cache_read(const nm_cache *cache, const int64_t *slots, int64_t rows, voi
  *               h / (q_heads / kv_heads).
  *   q_start   : device int32 [seqs + 1], ascending: sequence s has the tokens
  *               q_start[s] .. q_start[s+1] - 1 of q, its nodes 0 .. n - 1.
- *               Nodes beyond max_nodes (1 .. 64) or `tokens` are not computed.
+ *               Nodes beyond max_nodes (1 .. 64) or `tokens` are not computed;
+ *               an entry below 0 counts as 0, and a sequence that ends before
+ *               it begins has no nodes.
  *   block_table: device int32 [seqs][ld_table], table_cols >= 1 entries used;
  *               entry i of sequence s is the page of its positions
  *               i * page_size ..; positions in a page out of range or beyond

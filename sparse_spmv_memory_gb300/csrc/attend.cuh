@@ -49,7 +49,7 @@ struct SeqInfo {
 __device__ __forceinline__ SeqInfo seq_info(const AttendParams& p, int s) {
   SeqInfo i;
   i.first = max(p.q_start[s], 0);
-  i.n = max(0, min(min(p.q_start[s + 1], p.tokens) - i.first, p.max_nodes));
+  i.n = max(0, min(min(max(p.q_start[s + 1], 0), p.tokens) - i.first, p.max_nodes));
   i.ctx = max(p.ctx_len[s], 0);
   i.len = min(i.ctx + i.n, p.table_cols << p.c.page_shift);
   return i;

@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(VerifyParams p, int
   };
 
   const int first = min(max(p.node_start[s], 0), p.tokens);
-  const int n = min(min(p.node_start[s + 1], p.tokens) - first, p.max_nodes);
+  const int n = min(min(max(p.node_start[s + 1], 0), p.tokens) - first, p.max_nodes);
   int32_t* path = p.path + (int64_t)s * p.max_nodes;
   const bool writer = rank == 0 && warp == 0;
   const bool greedy = p.temperature == 0.0f, drafted = p.draft != nullptr;

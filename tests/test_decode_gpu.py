@@ -286,6 +286,41 @@ def test_attention_ragged_bounds(nm):
     assert (out[7:] == 5).all() and (lse[7:] == 5).all()
 
 
+INT_MIN = -2 ** 31
+
+
+@pytest.mark.parametrize("nodes", [2, 7])
+@pytest.mark.parametrize("start,rows", [([0, 3, INT_MIN, 7], [3, 0, 7]), ([0, 3, -5, 7], [3, 0, 7]),
+                                        ([INT_MIN, 3, 2 ** 31 - 1, INT_MIN], [3, 9, 0])])
+def test_starts_out_of_range(nm, nodes, start, rows):
+    """Starts below 0, beyond the tokens or before the last one: the other sequences
+    are as ever, and nothing beyond the tokens is read or written."""
+    b = Batch("fp16", [50, 60, 70], [3, 0, 9], 8, 2, 64, 16, seed=17, spoil=False)
+    T = 12
+    k, v, q = cuda(b.k, b.v, b.q)
+    st = torch.tensor(start, dtype=torch.int32).cuda()
+    ctx = torch.tensor(b.ctx, dtype=torch.int32).cuda()
+    wide = torch.full((T + 70, 8, 64), 5.0, dtype=torch.float16, device="cuda")
+    lse = torch.full((T + 70, 8), 5.0, device="cuda")
+    nm.nm_tree_attention(q, k, v, b.table.cuda(), ctx, st, nodes, out=wide[:T], lse=lse[:T])
+    done = set()
+    for s in range(3):
+        first = max(start[s], 0)
+        n = min(nodes, rows[s])
+        if n:
+            done |= set(range(first, first + n))
+    left = [t for t in range(T + 70) if t not in done]
+    assert (wide[left] == 5).all() and (lse[left] == 5).all()
+    assert (lse[sorted(done)] != 5).all()
+    V = 40
+    logits = torch.zeros((T, V), device="cuda")
+    logits[:, 9] = 30.0
+    zero = torch.zeros(T, dtype=torch.int32, device="cuda")
+    path, count, token = nm.nm_tree_verify(logits, zero, zero - 1, st, nodes, temperature=0.0)
+    assert count.tolist() == [min(1, r) for r in rows]
+    assert token.tolist() == [9 if r else -1 for r in rows]
+
+
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("nodes", [1, 4, 32])
 def test_attention_workspace_and_repeats(nm, kind, nodes):
