@@ -114,8 +114,8 @@ int nm_rope_inv_freq(float *inv_freq, int rot_dim, double base, int scaling, dou
  * to the nearest (ties to even); a row of zeros has scale 0; a row with a
  * non-finite element has scale NaN (it reads back as NaN).  fp16 rows are
  * rounded once (RNE).  qkv must not overlap q_out or the cache.
- * tokens == 0 is a no-op.  tokens < 2^31, q_heads 1 .. 1024, rot_dim even,
- * 0 .. head_dim, else NM_ERR_SHAPE.
+ * tokens == 0 is a no-op (the tokens' arrays may be NULL then).  tokens < 2^31,
+ * q_heads 1 .. 1024, rot_dim even, 0 .. head_dim, else NM_ERR_SHAPE.
  * ------------------------------------------------------------------------- */
 int nm_rope_append(const void *qkv, int64_t ldqkv, int64_t tokens, int q_heads,
                    const int32_t *positions, const int64_t *slots, const float *inv_freq,
@@ -126,7 +126,8 @@ int nm_rope_append(const void *qkv, int64_t ldqkv, int64_t tokens, int q_heads,
  * nm_cache_read -- rows of the cache as fp16 (code * scale, rounded once).
  *   slots : device int64 [rows]; a slot outside the cache reads as zeros.
  *   k_out, v_out : device fp16 [rows][kv_heads][head_dim], 16-byte aligned;
- *           either may be NULL.  rows == 0 is a no-op; rows < 2^31.
+ *           either may be NULL.  rows == 0 is a no-op (slots may be NULL
+ *           then); rows < 2^31.
  * ------------------------------------------------------------------------- */
 int nm_cache_read(const nm_cache *cache, const int64_t *slots, int64_t rows, void *k_out,
                   void *v_out, void *stream);
@@ -171,8 +172,8 @@ int nm_cache_read(const nm_cache *cache, const int64_t *slots, int64_t rows, voi
  *       counters are at its start whatever the call's shape, nothing else is
  *       written there, and every call leaves them zero: later calls of any shape
  *       on the same device, ordered after this one, can use it as it is.
- * seqs == 0 or tokens == 0 is a no-op; seqs < 65536, tokens < 2^31, q_heads
- * 1 .. 1024, q_heads / kv_heads <= 64.
+ * seqs == 0 or tokens == 0 is a no-op (all arrays but the cache's may be NULL
+ * then); seqs < 65536, tokens < 2^31, q_heads 1 .. 1024, q_heads / kv_heads <= 64.
  * ------------------------------------------------------------------------- */
 size_t nm_tree_attention_workspace_bytes(int64_t seqs, int q_heads, int kv_heads, int head_dim,
                                          int max_nodes);
@@ -215,6 +216,9 @@ int nm_tree_attention(const void *q, int64_t ldq, int64_t tokens, int q_heads, i
  *             then -1;  count : device int32 [seqs]: how many (0 for a sequence
  *             without nodes);  token : device int32 [seqs]: the next token.
  * Sums are fp32 over fixed parts of the vocabulary, added in a fixed order.
+ * seqs == 0 is a no-op (all arrays may be NULL then).  With tokens == 0 no
+ * sequence has nodes; path, count and token are written, and the nodes' arrays may
+ * be NULL.
  * vocab 1 .. 2^24, seqs < 65536, temperature >= 0 and finite.
  * ------------------------------------------------------------------------- */
 int nm_tree_verify(const void *logits, int logits_fp32, int64_t ld_logits, int64_t vocab,

@@ -110,7 +110,8 @@ int nm_rope_append(const void* qkv, int64_t ldqkv, int64_t tokens, int q_heads,
                    const int32_t* positions, const int64_t* slots, const float* inv_freq,
                    int rot_dim, int interleaved, float mscale, void* q_out, int64_t ldq,
                    const nm_cache* cache, void* stream) {
-  if (!qkv || !positions || !slots || (!inv_freq && rot_dim != 0)) return NM_ERR_NULL;
+  // (an empty array's address may be NULL: there is nothing to read or write)
+  if (tokens != 0 && (!qkv || !positions || !slots || (!inv_freq && rot_dim != 0))) return NM_ERR_NULL;
   AppendParams p;
   const int st = check_cache(cache, &p.c);
   if (st != NM_OK) return st;
@@ -148,7 +149,7 @@ int nm_rope_append(const void* qkv, int64_t ldqkv, int64_t tokens, int q_heads,
 
 int nm_cache_read(const nm_cache* cache, const int64_t* slots, int64_t rows, void* k_out,
                   void* v_out, void* stream) {
-  if (!slots) return NM_ERR_NULL;
+  if (!slots && rows != 0) return NM_ERR_NULL;
   ReadParams p;
   const int st = check_cache(cache, &p.c);
   if (st != NM_OK) return st;
@@ -189,7 +190,8 @@ static int tree_attention(const void* q, int64_t ldq, int64_t tokens, int q_head
                           const int32_t* ctx_len, const uint64_t* tree_mask, float scale, void* out,
                           int64_t ldo, float* lse, void* workspace, size_t workspace_bytes,
                           void* stream, uint64_t wait_limit_ns, int stall) {
-  if (!q || !q_start || !block_table || !ctx_len || !out) return NM_ERR_NULL;
+  if (tokens != 0 && seqs != 0 && (!q || !q_start || !block_table || !ctx_len || !out))
+    return NM_ERR_NULL;
   AttendParams p;
   const int st = check_cache(cache, &p.c);
   if (st != NM_OK) return st;
@@ -269,9 +271,10 @@ static int tree_verify(const void* logits, int logits_fp32, int64_t ld_logits, i
                        int64_t seqs, int max_nodes, const float* accept, const float* race,
                        int64_t ld_race, float temperature, int32_t* path, int32_t* count,
                        int32_t* token, void* stream, uint64_t wait_limit_ns, int stall) {
-  if (!logits || !ids || !parents || !node_start || !path || !count || !token) return NM_ERR_NULL;
+  if (seqs != 0 && (!node_start || !path || !count || !token)) return NM_ERR_NULL;
+  if (seqs != 0 && tokens != 0 && (!logits || !ids || !parents)) return NM_ERR_NULL;
   if (!(temperature >= 0.0f) || !isfinite(temperature)) return NM_ERR_SHAPE;
-  if (temperature > 0.0f && (!accept || !race)) return NM_ERR_NULL;
+  if (seqs != 0 && tokens != 0 && temperature > 0.0f && (!accept || !race)) return NM_ERR_NULL;
   if (vocab < 1 || vocab > (1 << 24) || tokens < 0 || tokens >= kMax31 || seqs < 0 ||
       seqs >= 65536 || max_nodes < 1 || max_nodes > kMaxNodes || ld_logits < vocab ||
       ld_logits >= kMax31 || (temperature > 0.0f && (ld_race < vocab || ld_race >= kMax31)) ||

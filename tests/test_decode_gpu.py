@@ -876,6 +876,48 @@ def test_binding_refusals(nm):
     assert e.value.status == 1
 
 
+# ---- nothing to do -------------------------------------------------------------------
+def test_empty_calls(nm):
+    """No tokens, rows or sequences, with tensors that are really empty (their
+    address is NULL): no-ops, and a batch whose sequences all have no nodes is
+    answered."""
+    i32, dev = torch.int32, "cuda"
+    for kind in KINDS:
+        shape = (4, 2, 8, 64)
+        k, v = (torch.zeros(shape, dtype=ref.DTYPES[kind], device=dev) for _ in range(2))
+        ks, vs = (None, None) if kind == "fp16" else (torch.zeros(shape[:3], device=dev) for _ in range(2))
+        no = torch.zeros(0, dtype=torch.int64, device=dev)
+        empty = torch.zeros(0, dtype=i32, device=dev)
+        assert no.data_ptr() == 0
+        qkv = torch.zeros((0, 8 * 64), dtype=torch.float16, device=dev)
+        q = nm.nm_rope_append(qkv, k, v, empty, no, nm.nm_rope_inv_freq(64), 4, k_scale=ks, v_scale=vs)
+        assert q.shape == (0, 4, 64)
+        assert nm.nm_rope_append(qkv, k, v, empty, no, nm.nm_rope_inv_freq(64), 4, k_scale=ks, v_scale=vs,
+                                 want_q=False) is None
+        rk, rv = nm.nm_cache_read(k, v, no, ks, vs)
+        assert rk.shape == rv.shape == (0, 2, 64)
+        for seqs in (0, 3):
+            start = torch.zeros(seqs + 1, dtype=i32, device=dev)
+            table, ctx = torch.zeros((seqs, 4), dtype=i32, device=dev), torch.full((seqs,), 20, dtype=i32, device=dev)
+            mask = no if seqs else None
+            out, lse = nm.nm_tree_attention(q, k, v, table, ctx, start, 4, tree_mask=mask, k_scale=ks, v_scale=vs)
+            assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
+        some = torch.ones((5, 4, 64), dtype=torch.float16, device=dev)
+        out, lse = nm.nm_tree_attention(some, k, v, torch.zeros((0, 4), dtype=i32, device=dev), empty,
+                                        torch.zeros(1, dtype=i32, device=dev), 4, k_scale=ks, v_scale=vs)
+        assert out.shape == (5, 4, 64)
+    for seqs in (0, 3):
+        for dtype in (torch.float16, torch.float32):
+            logits = torch.zeros((0, 33), dtype=dtype, device=dev)
+            start = torch.zeros(seqs + 1, dtype=i32, device=dev)
+            for kw in (dict(temperature=0.0), dict(accept=logits.float()[:, 0], race=torch.ones((seqs, 33), device=dev)),
+                       dict(accept=logits.float()[:, 0], race=torch.ones((seqs, 33), device=dev), draft=logits.float())):
+                path, count, token = nm.nm_tree_verify(logits, empty, empty, start, 4, **kw)
+                assert path.tolist() == [[-1] * 4] * seqs
+                assert count.tolist() == [0] * seqs and token.tolist() == [-1] * seqs
+    torch.cuda.synchronize()
+
+
 @pytest.mark.parametrize("cache", KINDS)
 def test_example_decodes_as_one_token_at_a_time(nm, cache):
     """Speculative decoding at temperature 0 gives the tokens of plain decoding, and

@@ -175,6 +175,21 @@ def test_verify_refused(nm):
     assert call(t=0.0, acc=None, race=None, draft=None, seqs=0) == 0
 
 
+def test_empty_calls_take_no_addresses(nm):
+    """Arrays without elements: NULL is what an empty tensor has."""
+    L, c, N = nm.lib(), cache(), None
+    assert L.nm_rope_append(N, 512, 0, 4, N, N, N, 64, 0, 1.0, N, 0, ref(c), N) == 0
+    assert L.nm_rope_append(N, 512, 1, 4, N, N, N, 64, 0, 1.0, N, 0, ref(c), N) == 1
+    assert L.nm_rope_append(N, 504, 0, 4, N, N, N, 64, 0, 1.0, N, 0, ref(c), N) == 2
+    assert L.nm_rope_append(N, 512, 0, 4, N, N, N, 64, 0, 1.0, N, 0, N, N) == 1
+    assert L.nm_cache_read(ref(c), N, 0, N, N, N) == 0 and L.nm_cache_read(ref(c), N, 1, N, N, N) == 1
+    for tokens, seqs, code in ((0, 0, 0), (0, 3, 0), (5, 0, 0), (5, 3, 1), (-1, 0, 2), (0, -1, 2)):
+        assert L.nm_tree_attention(N, 256, tokens, 4, seqs, N, 4, ref(c), N, 4, 4, N, N, 1.0, N, 256, N, N, 0,
+                                   N) == code
+    for tokens, seqs, t, code in ((0, 0, 0.0, 0), (0, 0, 1.0, 0), (7, 0, 1.0, 0), (0, 2, 1.0, 1), (-1, 0, 1.0, 2)):
+        assert L.nm_tree_verify(N, 0, 8, 8, N, 0, N, N, N, tokens, seqs, 4, N, N, 8, t, N, N, N, N) == code
+
+
 def test_stall_selftests_refuse_a_limit_out_of_range(nm):
     L, c = nm.lib(), cache()
     o = 0x500000000
