@@ -161,10 +161,12 @@ int nm_cache_read(const nm_cache *cache, const int64_t *slots, int64_t rows, voi
  * positions beyond a sequence's last node are never used, whatever they hold;
  * a non-finite key or value row of a node spoils only the nodes that see it,
  * and a non-finite row of the context all nodes of its sequence.
- * Scores, maxima and sums are fp32.  The weights exp(score - max) are rounded
- * to fp16 for the tensor cores' product with the values (times the row's
- * scale where the cache has one; one below 2^-100 counts as 2^-100); products are accumulated in fp32 and out is
- * rounded once.  The split of the positions over the blocks depends on the
+ * Scores, maxima and sums are fp32.  The weights exp(score - max), times the
+ * value row's scale where the cache has one, are rounded to fp16 for the tensor
+ * cores' product with the values: by at most 2^-11 of a weight, or 2^-34 of the
+ * largest so far where that is more.  (A scale below 2^-64 may count as less or
+ * as 2^-80: such values are 0 in fp16.)  Products are accumulated in fp32 and out
+ * is rounded once.  The split of the positions over the blocks depends on the
  * lengths, and every part is joined in a fixed order.
  *   workspace : device scratch, 16-byte aligned, of at least
  *       nm_tree_attention_workspace_bytes(...) bytes (counters, then partial

@@ -77,6 +77,7 @@ __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
 // positions: 9.3 us, of which launch, lengths and the table's look-up some 3, the
 // loads 1.5, and joining warps, then blocks, 3.
 constexpr int kNarrowRows = 16;
+constexpr float kLift = 14.0f;
 
 template <int D, int TYPE>
 struct Narrow {
@@ -274,24 +275,26 @@ __global__ void __launch_bounds__(Narrow<D, TYPE>::NW * 32, 1) attend_narrow_ker
           seen[k] = see;
         }
       }
-      // ---- weights
+      // ---- weights: the largest is 2^kLift, so that they are fp16 at its full
+      // precision down to 2^-28 of it: many small ones add up
       uint32_t a[N::NG / 2][4];
       float keep[2];
       bool grew = false;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        float top = m[k];
+        float top = -INFINITY;
 #pragma unroll
         for (int c = 0; c < N::NG; ++c)
 #pragma unroll
           for (int i = 0; i < 2; ++i) top = fmaxf(top, F16 ? s[c][2 * k + i] : s[c][2 * k + i] + lv[c][i]);
         top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-        keep[k] = m[k] == -INFINITY ? 0.0f : exp2_fast(m[k] - top);
-        grew |= top != m[k];
+        const float next = fmaxf(m[k], top - kLift);
+        keep[k] = m[k] == -INFINITY ? 0.0f : exp2_fast(m[k] - next);
+        grew |= next != m[k];
         l[k] *= keep[k];
-        m[k] = top;
-        const float base = top == -INFINITY ? 0.0f : top;
+        m[k] = next;
+        const float base = next == -INFINITY ? 0.0f : next;
 #pragma unroll
         for (int c = 0; c < N::NG; ++c) {
           float e[2];

@@ -13,8 +13,11 @@
 //            as the MN-major operand (its rows are the reduction's).
 //   softmax  two warpgroups, a query row per thread: scores from TMEM, weights
 //            back over them as fp16.  The maximum that scales a row moves only
-//            when a score exceeds it by 2^8 (fp16 weights reach 2^8 then, at the
-//            same relative rounding), so the sums in TMEM are seldom rescaled.
+//            when a score exceeds it by 2^6.9, so the sums in TMEM are seldom
+//            rescaled.  The weight at that maximum is 2^9: none passes 2^15.9, and
+//            all are fp16 at its full precision down to 2^-23 of the largest, since
+//            many small ones add up.  (2^11 and 2^4: 16 sequences of 32 nodes over
+//            8000 positions 110 us for 104, as scores that pass 2^4 are not seldom.)
 // With at most 64 (32) rows, the tile's 128 rows are two (four) copies of them,
 // and copy c weighs only the c-th half (quarter) of a tile's positions: a warp can
 // read no other lanes of TMEM than its own, so without copies half of the softmax
@@ -62,8 +65,10 @@ constexpr int kMeta = 8;    // tiles of which it is kept which pages are there
 constexpr int kScales = 4;  // tiles whose scales are kept
 constexpr int kBad = 16;    // items whose spoilt nodes are kept
 constexpr int kCopyPitch = 20;  // floats: 16 columns of a row, and its banks moved on by 20
-constexpr float kGrow = 8.0f;
-constexpr float kTinyScale = 7.888609052210118e-31f;  // 2^-100: a smaller scale counts as this
+constexpr float kLift = 9.0f, kGrow = 6.9f;
+// 2^-80: a smaller scale counts as this, and no value times it is an fp16 number but
+// 0.  (So a weight over its scale is at most 2^95, and 2^31 of them add up.)
+constexpr float kTinyScale = 8.271806125530277e-25f;
 
 // A slot of a tile (item) is written again kMeta (kBad) tiles (items) on.  A
 // loader is at most NS + RS <= 10 positions of the ring ahead of the MMAs, and
@@ -447,7 +452,7 @@ __global__ void __launch_bounds__(Wide<D, TYPE, MODE>::THREADS, 1)
       if (!v && ct < kKeys) {
         const int j = t.node0 + ct;
         float lv = log2f(sc[1]), rv = 1.0f / sc[1];
-        if (sc[1] < kTinyScale) lv = -100.0f, rv = 1.0f / kTinyScale;
+        if (sc[1] < kTinyScale) lv = -80.0f, rv = 1.0f / kTinyScale;
         if (t.edge && j >= 0 && !(sc[1] < INFINITY)) {  // a node's row whose scale is not finite
           lv = 0.0f, rv = 1.0f;
           atomicOr(&bad_of[t.bad][(j >> 5) & 1], 1u << (j & 31));
@@ -788,11 +793,12 @@ __global__ void __launch_bounds__(Wide<D, TYPE, MODE>::THREADS, 1)
                 t[z] = fmaxf(fmaxf(t[z], __uint_as_float(v[x / 32][x % 32 + z])), __uint_as_float(v[x / 32][x % 32 + z + 4]));
             }
             const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * (F16 ? step2 : 1.0f);
-            const bool grow = top > m + kGrow || (m == -INFINITY && top > -INFINITY);
+            const float next = top - kLift;
+            const bool grow = next > m + kGrow || (m == -INFINITY && next > -INFINITY);
             if (__any_sync(0xFFFFFFFFu, grow)) {
               // seldom (but for an item's first positions): the sums so far, and
               // the weights of this tile so far, move to the new maximum
-              const float keep = !grow ? 1.0f : m == -INFINITY ? 0.0f : exp2_fast(m - top);
+              const float keep = !grow ? 1.0f : m == -INFINITY ? 0.0f : exp2_fast(m - next);
               if (k > 0) {
 #pragma unroll 1
                 for (int d = 0; d < D; d += 16) {
@@ -821,7 +827,7 @@ __global__ void __launch_bounds__(Wide<D, TYPE, MODE>::THREADS, 1)
                 }
               }
               l *= keep;
-              if (grow) m = top;
+              if (grow) m = next;
             }
             const float off = m == -INFINITY ? 0.0f : -m;
             float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};

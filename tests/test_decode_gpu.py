@@ -222,6 +222,57 @@ def test_attention_large_scores_and_outliers(nm, kind, nodes):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("nodes,group", [(1, 2), (5, 2), (5, 4), (9, 7), (20, 5), (64, 4)])
+@pytest.mark.parametrize("small", [-25.5, -27, -29])
+def test_attention_one_dominant_position(nm, kind, nodes, group, small):
+    """Nearly all the weight on an early position, whose values are 0 in most columns;
+    1023 others of 2^small of its weight make those columns.  Enough sequences, all of
+    the same pages, for items that one block has whole.  Tolerance: weights of down to
+    2^-24 of the largest are rounded by 2^-11 (below: 2^-35 of it each), A = sum p|v|; a
+    score by e_s = 2 (D + 8) 2^-24 scale |q k|; sums are fp32 over at most 2^10 terms;
+    the output's rounding."""
+    L, D, H, page, S = 1024, 64, 8, 64, 38
+    gen = torch.Generator().manual_seed(nodes)
+    k = torch.randn((H, L, D), generator=gen)
+    v = 64 * (1 + 0.5 * torch.randn((H, L, D), generator=gen))
+    at = 5
+    k[..., 0] = 0.0
+    k[:, at], v[:, at] = 0.0, 0.0
+    k[:, at, 0], v[:, at, 5] = 16.0, 200.0
+
+    def stored(x):  # [pages][heads][page][dim], and scales
+        x = x.view(H, L // page, page, D).transpose(0, 1).contiguous()
+        if kind == "fp16":
+            return x.half(), None
+        s = x.abs().amax(-1) / ref.CODE_MAX[kind]
+        y = x / s[..., None]
+        return (y.round().to(torch.int8) if kind == "int8" else y.to(ref.DTYPES[kind])), s
+    (kc, ks), (vc, vs) = stored(k), stored(v)
+    kd, vd = (ref.values(c, s).transpose(0, 1).reshape(H, L, D) for c, s in ((kc, ks), (vc, vs)))
+    T, Q = S * nodes, H * group
+    q = torch.zeros((T, Q, D), dtype=torch.float16)
+    q[..., 0] = 8.0
+    scale = float(np.float32(-small * np.log(2.0) / (8.0 * float(kd[0, at, 0]))))
+    table = torch.arange(L // page, dtype=torch.int32).expand(S, -1).contiguous()
+    out, lse = nm.nm_tree_attention(
+        *cuda(q, kc, vc, table), torch.full((S,), L, dtype=torch.int32).cuda(),
+        (torch.arange(S + 1) * nodes).to(torch.int32).cuda(), nodes,
+        tree_mask=torch.zeros(T, dtype=torch.int64).cuda(), k_scale=cuda(ks), v_scale=cuda(vs), scale=scale)
+    s = kd[..., 0] * 8.0 * scale
+    p = torch.softmax(s, -1)[:, None]
+    o, A = (p @ vd)[:, 0], (p @ vd.abs())[:, 0]
+    es = 2 * (D + 8) * 2.0 ** -24 * float(s.abs().max())
+    tol = (2.0 ** -11 + 2 * es + 2.0 ** -14) * A + L * 2.0 ** -35 * vd.abs().max() + 2.0 ** -11 * o.abs() + 2.0 ** -25
+    assert (tol[:, 6:] < 0.15 * o[:, 6:]).all()
+
+    def rows(x):  # of every key head, for its query heads and all tokens
+        return x.repeat_interleave(group, 0).expand((T,) + (Q,) + x.shape[1:])
+    within(out, rows(o), rows(tol), f"{kind} out")
+    want = torch.logsumexp(s, -1)
+    within(lse, rows(want), rows(es + 2.0 ** -14 + 2.0 ** -22 * want), f"{kind} lse")
+
+
+@pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("nodes", [1, 20])
 def test_attention_absent_pages(nm, kind, nodes):
     """Entries out of range, and positions beyond the table, are seen by no node."""
