@@ -163,7 +163,7 @@ int nm_cache_read(const nm_cache *cache, const int64_t *slots, int64_t rows, voi
  * and a non-finite row of the context all nodes of its sequence.
  * Scores, maxima and sums are fp32.  The weights exp(score - max), times the
  * value row's scale where the cache has one, are rounded to fp16 for the tensor
- * cores' product with the values: by at most 2^-11 of a weight, or 2^-34 of the
+ * cores' product with the values: by at most 2^-11 of a weight, or 2^-33 of the
  * largest so far where that is more.  (A scale below 2^-64 may count as less or
  * as 2^-80: such values are 0 in fp16.)  Products are accumulated in fp32 and out
  * is rounded once.  The split of the positions over the blocks depends on the

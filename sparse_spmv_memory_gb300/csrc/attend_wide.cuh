@@ -14,8 +14,8 @@
 //   softmax  two warpgroups, a query row per thread: scores from TMEM, weights
 //            back over them as fp16.  The maximum that scales a row moves only
 //            when a score exceeds it by 2^6.9, so the sums in TMEM are seldom
-//            rescaled.  The weight at that maximum is 2^9: none passes 2^15.9, and
-//            all are fp16 at its full precision down to 2^-23 of the largest, since
+//            rescaled.  The weight at that maximum is 2^8 to 2^9: none passes 2^15.9, and
+//            all are fp16 at its full precision down to 2^-22 of the largest, since
 //            many small ones add up.  (2^11 and 2^4: 16 sequences of 32 nodes over
 //            8000 positions 110 us for 104, as scores that pass 2^4 are not seldom.)
 // With at most 64 (32) rows, the tile's 128 rows are two (four) copies of them,
@@ -793,11 +793,12 @@ __global__ void __launch_bounds__(Wide<D, TYPE, MODE>::THREADS, 1)
                 t[z] = fmaxf(fmaxf(t[z], __uint_as_float(v[x / 32][x % 32 + z])), __uint_as_float(v[x / 32][x % 32 + z + 4]));
             }
             const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * (F16 ? step2 : 1.0f);
-            const float next = top - kLift;
-            const bool grow = next > m + kGrow || (m == -INFINITY && next > -INFINITY);
+            const bool grow = top > m + (kGrow + kLift) || (m == -INFINITY && top > -INFINITY);
             if (__any_sync(0xFFFFFFFFu, grow)) {
               // seldom (but for an item's first positions): the sums so far, and
-              // the weights of this tile so far, move to the new maximum
+              // the weights of this tile so far, move to the new maximum.  A maximum
+              // is a whole power of 2, so that a weight times `keep` is exact.
+              const float next = ceilf(top) - kLift;
               const float keep = !grow ? 1.0f : m == -INFINITY ? 0.0f : exp2_fast(m - next);
               if (k > 0) {
 #pragma unroll 1
@@ -817,7 +818,6 @@ __global__ void __launch_bounds__(Wide<D, TYPE, MODE>::THREADS, 1)
                   tmem_st_wait();
                   tmem_ld_16(tS + 16 * z, o);
                   tmem_ld_wait();
-                  // (rounded a second time, in the few tiles where a maximum moves)
 #pragma unroll
                   for (int x = 0; x < 16; ++x) {
                     const float2 f = half2_bits_to_float2(o[x]);

@@ -272,6 +272,56 @@ def test_attention_one_dominant_position(nm, kind, nodes, group, small):
     within(lse, rows(want), rows(es + 2.0 ** -14 + 2.0 ** -22 * want), f"{kind} lse")
 
 
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("nodes,q_heads", [(50, 1), (64, 2), (64, 5)])
+def test_attention_weights_are_rounded_once(nm, kind, nodes, q_heads):
+    """The largest score so far grows by 2^9 to 2^11 inside a tile of 128 positions, at
+    one whose value row is 0 in all columns but one, as is that of the largest before:
+    the other columns show the weight of one that is neither.  One rounding of it to fp16, one of the output, 2^-11 each, and
+    2^-15 for scores, scales and exponentials: two products at most that are not 0,
+    exact, then four roundings of numbers up to 42, 2^-24 of them each."""
+    D, page = 128, 16
+    gen = torch.Generator().manual_seed(nodes)
+    L = 100
+    k, v = torch.zeros((L, D)), torch.zeros((L, D))
+    other = [i for i in range(L) if i not in (3, 7, 45)]
+    k[other, 0], v[other] = -1.0, 1e-3
+    k[[3, 7, 45], 0] = 1.0
+    k[[7, 45], 2] = 1.0
+    k[45, 1] = 1.0
+    v[3] = 1.0 + torch.rand(D, generator=gen)
+    v[[7, 45], 0] = 2.0
+    out = []
+    for x in (k, v):
+        s = x.abs().amax(-1) / ref.CODE_MAX[kind]
+        y = x / torch.where(s > 0, s, 1.0)[:, None]
+        out += [y.round().to(torch.int8) if kind == "int8" else y.to(ref.DTYPES[kind]), s]
+    kc, ks, vc, vs = out
+    kd, vd = ref.values(kc, ks), ref.values(vc, vs)
+    q = torch.zeros((nodes, q_heads, D))
+    q[..., 0] = 20.0
+    q[..., 1] = (9 + 2 * torch.rand((nodes, q_heads), generator=gen)) * 0.6931
+    q[..., 2] = torch.rand((nodes, q_heads), generator=gen) * 0.6931
+    q = q.half()
+    pages = -(-(L + nodes) // page)
+
+    def paged(x, shape):
+        raw = x.view(torch.uint8) if x.dim() == 2 else x
+        y = torch.zeros((pages * page,) + raw.shape[1:], dtype=raw.dtype)
+        y[:L] = raw
+        return y.view(x.dtype).view(shape).cuda()
+    one = (pages, 1, page)
+    got, _ = nm.nm_tree_attention(
+        q.cuda(), paged(kc, one + (D,)), paged(vc, one + (D,)), torch.arange(pages, dtype=torch.int32)[None].cuda(),
+        torch.tensor([L], dtype=torch.int32).cuda(), torch.tensor([0, nodes], dtype=torch.int32).cuda(), nodes,
+        tree_mask=torch.zeros(nodes, dtype=torch.int64).cuda(), k_scale=paged(ks, one), v_scale=paged(vs, one),
+        scale=1.0)
+    s = q.double() @ kd.T
+    p = torch.softmax(s, -1)
+    o, A = p @ vd, p @ vd.abs()
+    within(got, o, 2.0 ** -11 * (A + o.abs()) + 2.0 ** -15 * A + 2.0 ** -25, f"{kind} out")
+
+
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("nodes", [1, 20])
 def test_attention_absent_pages(nm, kind, nodes):
