@@ -7,7 +7,8 @@
 // (b + 1) / Z), since relu(relu(x) - q) = relu(x - q) for q >= 0.  So a
 // rejection costs one sum over the vocabulary and nothing is written.  Without
 // draft probabilities w_r is p without the rejected tokens over what is left
-// of its sum.
+// of its sum: a difference while that is a quarter of p at least, whose rounding
+// is then 2^-22 of it a rejection, and else summed anew.
 //
 // The walk is sequential: what bounds it is the time from one node's row to
 // the next decision, not bandwidth.  One cluster of blocks takes a sequence;
@@ -286,6 +287,13 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(VerifyParams p, int
     }
   };
 
+  // whether token t is that of one of the nodes `set`
+  auto rejected = [&](uint64_t set, int t) {
+    for (; set; set &= set - 1)
+      if (p.ids[first + __ffsll(set) - 1] == t) return true;
+    return false;
+  };
+
   int cur = 0, len = 0, token = -1;
   if (n > 0 && ok) {
     // lane l has the nodes l and l + 32
@@ -438,9 +446,29 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(VerifyParams p, int
             break;
           }
           if (later) fetch(__ffsll(later) - 1);
-          if (!again && left - pt > 0.0f) {
+          if (again) continue;  // its weight is 0 already
+          float now = left - pt;
+          if (now < 0.25f) {
+            float z = 0.0f;
+#pragma unroll
+            for (int k = 0; k < HELD; ++k)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) z += (gt + k * stride) * 8 + i == t ? 0.0f : x[k][i];
+            rest_of(row, [&](int e, const float (&v)[8]) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) z += e + i == t || rejected(gone, e + i) ? 0.0f : prob(v[i]);
+            });
+            now = sum_of(z);
+            if (!ok) break;
+          }
+          if (now > 0.0f) {
             gone |= 1ull << c;
-            left -= pt;
+            left = now;
+#pragma unroll
+            for (int k = 0; k < HELD; ++k)
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if ((gt + k * stride) * 8 + i == t) x[k][i] = 0.0f;
           }
         }
       }
@@ -458,14 +486,6 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(VerifyParams p, int
 #pragma unroll
           for (int i = 0; i < 8; ++i) x[k][i] = fmaxf(a * x[k][i] - b * q[i], 0.0f);
         }
-      }
-      for (uint64_t g = gone; g; g &= g - 1) {  // rejected without draft
-        const int c = __ffsll(g) - 1, t = __shfl_sync(0xFFFFFFFFu, c < 32 ? id[0] : id[1], c & 31);
-#pragma unroll
-        for (int k = 0; k < HELD; ++k)
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if ((gt + k * stride) * 8 + i == t) x[k][i] = 0.0f;
       }
       Best t{-1.0f, -1};
       auto run = [&](int e, const float (&w)[8], const float (&r)[8]) {
@@ -491,10 +511,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(VerifyParams p, int
           for (int i = 0; i < 8; ++i) {
             w[0][i] = prob(w[0][i]);
             if (drafted && g * 8 + i < V) w[0][i] = fmaxf(a * w[0][i] - b * qrow[g * 8 + i], 0.0f);
-            for (uint64_t o = gone; o; o &= o - 1) {
-              const int c = __ffsll(o) - 1;
-              if (p.ids[first + c] == g * 8 + i) w[0][i] = 0.0f;
-            }
+            if (rejected(gone, g * 8 + i)) w[0][i] = 0.0f;
           }
           run(g * 8, w[0], r[0]);
         }

@@ -822,6 +822,44 @@ def test_verify_keeps_the_targets_distribution(nm, drafted):
     assert 0.2 < (count > 1).mean() < 0.95
 
 
+@pytest.mark.parametrize("vocab", [1000, 300007])
+@pytest.mark.parametrize("fp32", [True, False])
+def test_verify_little_mass_left(nm, vocab, fp32):
+    """Without draft, after a rejection of a token of probability 1 - d: what is left, d
+    = 2e-6 to 3e-2, is a sum as exact as its terms.  The second child is tried at 0.5 %
+    to either side of its share, the race is decided by far: fp32 sums and
+    exponentials are good to 1e-5 here."""
+    rng = np.random.default_rng(vocab)
+    S = 48 if vocab < 10000 else 6
+    N = 4 * S
+    logits = np.zeros((N, vocab), np.float32)
+    ids = np.tile(np.array([0, 3, 8, vocab - 1], np.int32), S)       # node 0 has the children 1, 2, 3
+    parents = np.tile(np.array([-1, 0, 0, 0], np.int32), S)
+    start = np.arange(0, N + 1, 4, dtype=np.int32)
+    accept = np.full(N, 1 - 2.0 ** -24, np.float32)
+    race = np.ones((S, vocab), np.float32)
+    race[:, 11] = 1e-9
+    for s in range(S):
+        x = rng.normal(size=vocab) * 0.5
+        x[3] = x[8] = x[-1] = -np.inf
+        rest = np.exp(x).sum()
+        share2, share3 = rng.uniform(0.2, 0.5), rng.uniform(0.2, 0.4)
+        x[8], x[-1] = np.log(rest * share2 / (1 - share2 - share3)), np.log(rest * share3 / (1 - share2 - share3))
+        x[3] = np.log(np.exp(x).sum()) + np.log(1 / 10 ** rng.uniform(-5.7, -1.5))
+        logits[4 * s] = x
+    if not fp32:
+        logits = logits.astype(np.float16)
+    for s in range(S):
+        w = np.exp(logits[4 * s].astype(np.float64) - logits[4 * s].max())
+        w[3] = 0
+        accept[4 * s + 2] = w[8] / w.sum() * (1 + rng.choice([-1, 1]) * 0.005)
+        w[8] = 0
+        accept[4 * s + 3] = w[-1] / w.sum() * (1 + rng.choice([-1, 1]) * 0.005)
+    want = ref.verify(logits, ids, parents, start, accept, race, None, 1.0, 4)
+    assert len(set(want[0][:, 1])) == 3 or vocab > 10000
+    same(run_verify(nm, (logits, ids, parents, start, accept, race, None), 4, 1.0), want[:3])
+
+
 # ---- wide batches, long vocabularies, the calls' own refusals -------------------------
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("nodes,q_heads", [(1, 8), (6, 8), (14, 8), (20, 16), (40, 16)])
