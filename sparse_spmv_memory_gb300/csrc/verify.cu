@@ -241,7 +241,8 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(VerifyParams p, int
   int32_t* path = p.path + (int64_t)s * p.max_nodes;
   const bool writer = rank == 0 && warp == 0;
   const bool greedy = p.temperature == 0.0f, drafted = p.draft != nullptr;
-  const float scale = greedy ? 1.0f : kLog2e / p.temperature;
+  // (finite at the smallest temperatures too: the largest logit's exponent is 0 times it)
+  const float scale = greedy ? 1.0f : fminf(kLog2e / p.temperature, 3.4e38f);
   const float* race = p.race + (int64_t)s * p.ld_race;
   auto row_of = [&](int node) { return static_cast<const T*>(p.logits) + (int64_t)(first + node) * p.ld_logits; };
   auto draft_of = [&](int node) { return p.draft + (int64_t)(first + node) * p.ld_draft; };

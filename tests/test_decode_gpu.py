@@ -860,6 +860,19 @@ def test_verify_little_mass_left(nm, vocab, fp32):
     same(run_verify(nm, (logits, ids, parents, start, accept, race, None), 4, 1.0), want[:3])
 
 
+@pytest.mark.parametrize("temperature", [1e-45, 1e-40, 1e-30])
+@pytest.mark.parametrize("drafted", [True, False])
+def test_verify_smallest_temperatures(nm, temperature, drafted):
+    """Temperatures down to the smallest number above 0: all the weight is on the
+    largest logit (one that no other equals)."""
+    case = verify_case(31, 6, 9, 500, drafted, 0.0, True)
+    logits, ids, parents, start, accept, race, q, _ = case
+    assert all(np.sort(r)[-1] > np.sort(r)[-2] for r in logits)
+    got = run_verify(nm, case, 9, temperature)
+    want = ref.verify(logits, ids, parents, start, accept, race, q, max(temperature, 1e-12), 9)
+    same(got, want[:3])
+
+
 # ---- wide batches, long vocabularies, the calls' own refusals -------------------------
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("nodes,q_heads", [(1, 8), (6, 8), (14, 8), (20, 16), (40, 16)])
