@@ -108,8 +108,10 @@ int nm_rope_inv_freq(float *inv_freq, int rot_dim, double base, int scaling, dou
  *               a long-context scheme scales its attention).
  *   q_out     : device fp16 [tokens][ldq], 16-byte aligned, ldq % 8 == 0; NULL:
  *               the query heads are skipped.
- * Angles, products and the scales' divisions are fp32; the angle's rounding
- * error is carried along, so that long positions keep fp32 accuracy.  A row's
+ * Angles, products and the scales' divisions are fp32; the roundings of the
+ * position and of the angle are carried along, so that all positions keep fp32
+ * accuracy (2^-21 of |a| + |b| where position * inv_freq's rounding is below 2^-7,
+ * positions below 131072 times inv_freq of 1; 2^-20 beyond).  A row's
  * scale is max|x| / 448 (e4m3) or / 127 (int8) and its codes are x / scale,
  * to the nearest (ties to even); a row of zeros has scale 0; a row with a
  * non-finite element has scale NaN (it reads back as NaN).  fp16 rows are

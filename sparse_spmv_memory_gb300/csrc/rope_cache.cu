@@ -51,15 +51,30 @@ __device__ __forceinline__ uint2 encode8(const float (&x)[8], float scale) {
                     b[4] | b[5] << 8 | b[6] << 16 | b[7] << 24);
 }
 
-// cos and sin of p * f for a position p, times m.  The product's rounding
-// error e (exact by fma) turns the rounded angle's pair by e: at position
-// 131071 it reaches 2^-8 of a radian, which would be the largest error by far.
-__device__ __forceinline__ void turn_of(float p, float f, float m, float& c, float& s) {
+// cos and sin of pos * f, times m.  The product's rounding error e (exact by fma)
+// turns the rounded angle's pair by e: at position 131071 and f = 1 it reaches 2^-8
+// of a radian, which would be the largest error by far.
+__device__ __forceinline__ void turn_of(int pos, float f, float m, float& c, float& s) {
+  const float p = (float)pos;
   const float a = __fmul_rn(p, f);
-  const float e = __fmaf_rn(p, f, -a);
+  float e = __fmaf_rn(p, f, -a);
   float s0, c0;
   sincosf(a, &s0, &c0);
-  const float d = 1.0f - 0.5f * e * e;  // |e| <= 2^-7 for p < 2^17: e^4 / 24 is below fp32
+  if (fabsf(e) > 0.0078125f || (uint32_t)pos + (1u << 24) > (2u << 24)) {
+    // Far positions: e is an angle of its own, and above 2^24 the position's rounding
+    // times f joins it.  The sum's two parts: the first turns by its cosine and sine,
+    // the second (2^-16 for f of 1) is the new e.
+    const float rest = (float)(int)((int64_t)pos - (int64_t)p);
+    const float h = __fmul_rn(rest, f), l = __fmaf_rn(rest, f, -h);
+    const float t = __fadd_rn(e, h), b = __fsub_rn(t, e);
+    e = __fadd_rn(__fadd_rn(__fsub_rn(e, __fsub_rn(t, b)), __fsub_rn(h, b)), l);
+    float s1, c1;
+    sincosf(t, &s1, &c1);
+    const float c2 = c0 * c1 - s0 * s1;
+    s0 = s0 * c1 + c0 * s1;
+    c0 = c2;
+  }
+  const float d = 1.0f - 0.5f * e * e;  // |e| <= 2^-7: e^3 / 6 is 2^-23.6, below fp32
   c = m * fmaf(-s0, e, c0 * d);
   s = m * fmaf(c0, e, s0 * d);
 }
@@ -92,7 +107,7 @@ __global__ void __launch_bounds__(128) append_kernel(AppendParams p, int turns) 
 
   // angles 2 lane and 2 lane + 1, and from them the lane's own
   float ac[2] = {1.0f, 1.0f}, as[2] = {0.0f, 0.0f}, c[8], s[8];
-  const float pos = (float)p.positions[t];
+  const int pos = p.positions[t];
 #pragma unroll
   for (int k = 0; k < 2; ++k)
     if (2 * lane + k < half) turn_of(pos, p.inv_freq[2 * lane + k], p.mscale, ac[k], as[k]);

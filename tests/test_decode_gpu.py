@@ -640,6 +640,36 @@ def test_append_again_commits_the_same_rows(nm, kind):
     assert q.shape == (9, 4, 128)
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("lo,hi", [(2 ** 17, 2 ** 18), (2 ** 20, 2 ** 21), (2 ** 23, 2 ** 24 + 99),
+                                   (2 ** 27, 2 ** 28), (2 ** 31 - 5000, 2 ** 31 - 1)])
+def test_append_far_positions(nm, interleaved, lo, hi):
+    """Positions up to the largest int32, above 2^24 too, where they are no fp32
+    numbers.  Tolerance: two pairs of cosine and sine, 2^-23 each, make one, 2^-21.4
+    with the roundings; two products and a sum; q and fp16 rows are rounded once."""
+    T, Q, H, D = 150, 4, 2, 128
+    x, pos, slots, k, v, _, _ = append_case("fp16", T, Q, H, D, 16, seed=lo % 1000)
+    gen = torch.Generator().manual_seed(lo % 997)
+    pos = torch.randint(lo, hi, (T,), generator=gen).to(torch.int32)
+    pos[-1] = hi
+    freq = nm.nm_rope_inv_freq(D, 10000.0, device="cpu")
+    freq[3] = 1.75  # a frequency may be above 1
+    q = nm.nm_rope_append(x.view(T, -1).cuda(), k, v, pos.cuda(), slots.cuda(), freq.cuda(), Q, interleaved=interleaved)
+    # the product of 31 and 24 bits does not fit a double
+    angle = pos.numpy().astype(np.longdouble)[:, None] * freq.numpy().astype(np.longdouble)
+    c, s = (torch.from_numpy(f(angle).astype(np.float64))[:, None] for f in (np.cos, np.sin))
+    h = D // 2
+    ia = torch.arange(0, D, 2) if interleaved else torch.arange(h)
+    ib = ia + 1 if interleaved else ia + h
+    y, size = x[:, :Q + H].double(), x[:, :Q + H].double()
+    a, b = x[:, :Q + H, ia].double(), x[:, :Q + H, ib].double()
+    y[..., ia], y[..., ib] = a * c - b * s, b * c + a * s
+    size[..., ia] = size[..., ib] = a.abs() + b.abs()
+    tol = 2.0 ** -11 * y.abs() + 2.0 ** -20 * size + 2.0 ** -25
+    within(q, y[:, :Q], tol[:, :Q], "q")
+    within(k.cpu()[slots // 16, :, slots % 16], y[:, Q:], tol[:, Q:], "k")
+
+
 @pytest.mark.parametrize("kind", ["e4m3", "int8"])
 def test_append_zero_and_non_finite_rows(nm, kind):
     x, pos, slots, k, v, ks, vs = append_case(kind, 4, 2, 1, 64, 8, seed=5)
