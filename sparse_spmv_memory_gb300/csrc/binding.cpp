@@ -34,17 +34,25 @@ struct PythonError {};  // already set
 
 [[noreturn]] void refuse(const std::string& why) { throw Refused(why); }
 
-// An argument that is a CUDA tensor, or (optional) None.
-const Tensor* tensor(PyObject* o, const char* what, bool optional = false) {
-  if (o == Py_None && optional) return nullptr;
-  if (!THPVariable_Check(o)) {
-    PyErr_Format(PyExc_TypeError, "%s must be a tensor", what);
-    throw PythonError{};
+// The tensors of a call, all on the device of the first.
+struct Tensors {
+  int device = -1;
+
+  // An argument that is a CUDA tensor, or (optional) None.
+  const Tensor* operator()(PyObject* o, const char* what, bool optional = false) {
+    if (o == Py_None && optional) return nullptr;
+    if (!THPVariable_Check(o)) {
+      PyErr_Format(PyExc_TypeError, "%s must be a tensor", what);
+      throw PythonError{};
+    }
+    const Tensor& t = THPVariable_Unpack(o);
+    if (!t.is_cuda()) refuse("nm_* calls take CUDA tensors (there is no CPU path)");
+    const int on = (int)t.get_device();
+    if (device < 0) device = on;
+    if (on != device) refuse(std::string(what) + " is on another device than the call's first tensor");
+    return &t;
   }
-  const Tensor& t = THPVariable_Unpack(o);
-  if (!t.is_cuda()) refuse("nm_* calls take CUDA tensors (there is no CPU path)");
-  return &t;
-}
+};
 
 template <typename T = void>
 T* pointer(const Tensor* t) {
@@ -75,17 +83,18 @@ bool truth(PyObject* o) {
   return v != 0;
 }
 
-// The stream that a call was given (None: the current one), which is the current
-// one meanwhile: what the call allocates, and the zeros of a workspace, are ordered
-// with its kernels.
+// The tensors' device, and the stream that a call was given (None: that device's
+// current one): both are the current ones meanwhile, so that what the call
+// allocates, and the zeros of a workspace, are ordered with its kernels.
 struct OnStream {
+  c10::cuda::CUDAGuard device;
   c10::cuda::OptionalCUDAStreamGuard guard;
-  OnStream(PyObject* o, const Tensor& t) {
+  OnStream(PyObject* o, const Tensors& in) : device((c10::DeviceIndex)in.device) {
     if (o == Py_None) return;
     const unsigned long long v = PyLong_AsUnsignedLongLong(o);
     if (v == (unsigned long long)-1 && PyErr_Occurred()) throw PythonError{};
     guard.reset_stream(c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(static_cast<uintptr_t>(v)),
-                                                        t.device().index()));
+                                                        (c10::DeviceIndex)in.device));
   }
   void* stream() const { return c10::cuda::getCurrentCUDAStream().stream(); }
 };
@@ -122,7 +131,7 @@ int64_t head_stride(const Tensor& t, int64_t tokens, int64_t dim, const char* wh
   return tokens > 1 ? t.stride(0) : t.size(1) * t.size(2);
 }
 
-nm_cache cache_of(PyObject* k_, PyObject* v_, PyObject* ks_, PyObject* vs_) {
+nm_cache cache_of(Tensors& tensor, PyObject* k_, PyObject* v_, PyObject* ks_, PyObject* vs_) {
   const Tensor &k = *tensor(k_, "k_cache"), &v = *tensor(v_, "v_cache");
   const Tensor *ks = tensor(ks_, "k_scale", true), *vs = tensor(vs_, "v_scale", true);
   nm_cache c;
@@ -190,7 +199,8 @@ PyObject* tuple_of(std::initializer_list<PyObject*> items) {
 // (qkv, k_cache, v_cache, positions, slots, inv_freq, q_heads, k_scale, v_scale,
 //  interleaved, mscale, q, want_q, stream)
 PyObject* rope_append(PyObject* const* a) {
-  const nm_cache c = cache_of(a[1], a[2], a[7], a[8]);
+  Tensors tensor;
+  const nm_cache c = cache_of(tensor, a[1], a[2], a[7], a[8]);
   const Tensor &qkv = *tensor(a[0], "qkv"), &pos = *tensor(a[3], "positions"),
                &slots = *tensor(a[4], "slots"), &freq = *tensor(a[5], "inv_freq");
   const int64_t q_heads = integer(a[6]);
@@ -204,7 +214,7 @@ PyObject* rope_append(PyObject* const* a) {
   const Tensor* q = tensor(a[11], "q", true);
   const bool want = q || truth(a[12]);
   Tensor made;
-  const OnStream on(a[13], qkv);
+  const OnStream on(a[13], tensor);
   if (want && !q) made = at::empty({tokens, q_heads, c.head_dim}, qkv.options());
   const Tensor* out = q ? q : want ? &made : nullptr;
   if (out && out->dim() == 3 && out->size(1) != q_heads) refuse("q must have q_heads heads");
@@ -220,7 +230,8 @@ PyObject* rope_append(PyObject* const* a) {
 
 // (k_cache, v_cache, slots, k_scale, v_scale, k, v, stream)
 PyObject* cache_read(PyObject* const* a) {
-  const nm_cache c = cache_of(a[0], a[1], a[3], a[4]);
+  Tensors tensor;
+  const nm_cache c = cache_of(tensor, a[0], a[1], a[3], a[4]);
   const Tensor& slots = *tensor(a[2], "slots");
   const int64_t rows = slots.numel();
   vector(&slots, at::kLong, rows, "slots");
@@ -231,7 +242,7 @@ PyObject* cache_read(PyObject* const* a) {
       refuse("k and v must be contiguous float16 [rows][kv_heads][head_dim]");
   Tensor mk, mv;
   const auto half = slots.options().dtype(at::kHalf);
-  const OnStream on(a[7], slots);
+  const OnStream on(a[7], tensor);
   if (!k) mk = at::empty({rows, c.kv_heads, c.head_dim}, half);
   if (!v) mv = at::empty({rows, c.kv_heads, c.head_dim}, half);
   check(nm_cache_read(&c, pointer<int64_t>(&slots), rows, pointer(k ? k : &mk), pointer(v ? v : &mv),
@@ -243,7 +254,8 @@ PyObject* cache_read(PyObject* const* a) {
 // (q, k_cache, v_cache, block_table, ctx_len, q_start, max_nodes, tree_mask,
 //  k_scale, v_scale, scale, out, lse, workspace, stream)
 PyObject* tree_attention(PyObject* const* a) {
-  const nm_cache c = cache_of(a[1], a[2], a[8], a[9]);
+  Tensors tensor;
+  const nm_cache c = cache_of(tensor, a[1], a[2], a[8], a[9]);
   const Tensor &q = *tensor(a[0], "q"), &table = *tensor(a[3], "block_table"),
                &ctx = *tensor(a[4], "ctx_len"), &start = *tensor(a[5], "q_start");
   const Tensor *mask = tensor(a[7], "tree_mask", true), *out = tensor(a[11], "out", true),
@@ -259,7 +271,7 @@ PyObject* tree_attention(PyObject* const* a) {
     refuse("block_table must be int32 [seqs][entries]");
   if (q_heads > INT32_MAX) refuse("q is too large");
   Tensor mo, ml, mw;
-  const OnStream on(a[14], q);
+  const OnStream on(a[14], tensor);
   if (!out) mo = at::empty({tokens, q_heads, c.head_dim}, q.options());
   const Tensor& o = out ? *out : mo;
   const int64_t ldo = head_stride(o, tokens, c.head_dim, "out");
@@ -287,6 +299,7 @@ PyObject* tree_attention(PyObject* const* a) {
 // (logits, tokens, parents, node_start, max_nodes, draft, accept, race,
 //  temperature, path, count, token, stream)
 PyObject* tree_verify(PyObject* const* a) {
+  Tensors tensor;
   const Tensor &logits = *tensor(a[0], "logits"), &ids = *tensor(a[1], "tokens"),
                &parents = *tensor(a[2], "parents"), &start = *tensor(a[3], "node_start");
   const Tensor *draft = tensor(a[5], "draft", true), *accept = tensor(a[6], "accept", true),
@@ -311,7 +324,7 @@ PyObject* tree_verify(PyObject* const* a) {
   const int64_t ldd = rows(draft, n, "draft"), ldr = rows(race, seqs, "race");
   const auto i32 = logits.options().dtype(at::kInt);
   Tensor mp, mc, mt;
-  const OnStream on(a[12], logits);
+  const OnStream on(a[12], tensor);
   if (!path) mp = at::empty({seqs, std::max(0, max_nodes)}, i32);
   if (!count) mc = at::empty({seqs}, i32);
   if (!token) mt = at::empty({seqs}, i32);

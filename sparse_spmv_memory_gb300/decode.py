@@ -11,8 +11,9 @@ the inner three dimensions contiguous), and for the 8-bit types ``k_scale`` and
 ``v_scale`` float32 [pages][kv_heads][page_size].  A slot is
 page * page_size + offset.
 
-``stream`` is a torch.cuda.Stream or a raw cudaStream_t (None: the current one);
-outputs and workspaces that a call makes itself are allocated on that stream.
+All tensors of a call are on one device, current or not.  ``stream`` is a
+torch.cuda.Stream or a raw cudaStream_t (None: that device's current one); outputs
+and workspaces that a call makes itself are allocated on that stream.
 """
 from __future__ import annotations
 

@@ -204,3 +204,27 @@ def test_binding_refuses_cpu_tensors_and_wrong_types(nm):
     k = torch.zeros((2, 1, 8, 64), dtype=torch.float16)
     with pytest.raises(ValueError, match="CUDA"):
         nm.nm_cache_read(k, k, torch.zeros(1, dtype=torch.int64))
+
+
+@pytest.mark.filterwarnings("ignore")
+def test_binding_refuses_tensors_of_two_devices(nm):
+    """Tensors that only say which device they are on, and have no memory: the refusal
+    comes before anything else is asked of them."""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    with FakeTensorMode():
+        def t(*shape, dtype=torch.int32, on=0):
+            return torch.empty(shape, dtype=dtype, device=f"cuda:{on}")
+        h, f, i64 = torch.float16, torch.float32, torch.int64
+        k, v = t(4, 1, 8, 64, dtype=h), t(4, 1, 8, 64, dtype=h)
+        other = "another device"
+        with pytest.raises(ValueError, match=other):
+            nm.nm_cache_read(k, v, t(3, dtype=i64, on=1))
+        with pytest.raises(ValueError, match=other):
+            nm.nm_cache_read(k, t(4, 1, 8, 64, dtype=h, on=1), t(3, dtype=i64))
+        with pytest.raises(ValueError, match=other):
+            nm.nm_rope_append(t(3, 256, dtype=h), k, v, t(3), t(3, dtype=i64, on=1), t(32, dtype=f), 2)
+        with pytest.raises(ValueError, match=other):
+            nm.nm_tree_attention(t(3, 2, 64, dtype=h), k, v, t(1, 4), t(1), t(2), 3,
+                                 workspace=t(64, dtype=torch.uint8, on=1))
+        with pytest.raises(ValueError, match=other):
+            nm.nm_tree_verify(t(3, 9, dtype=h), t(3), t(3), t(2), 3, temperature=0.0, token=t(1, on=2))
