@@ -1,14 +1,18 @@
 """Build step of the CUDA library: compiles csrc/*.cu for sm_103a with nvcc and
 links them into ``libnmspmv.so`` next to this file (in-tree, never installed),
-and builds the compiled half of decode.py against it.
+and, where PyTorch is installed, builds the compiled half of decode.py against it.
 
 The translation units are compiled in parallel; nothing is rebuilt when the
-library is newer than every source and header.
+library is newer than every source and header, and the binding newer than its own
+and built for the running Python and PyTorch.
 """
 from __future__ import annotations
 
 import glob
+import importlib.metadata
+import importlib.util
 import os
+import platform
 import shutil
 import subprocess
 import sys
@@ -38,18 +42,55 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found (set NVCC or put the CUDA toolkit on PATH)")
 
 
-def _inputs() -> list[str]:
-    files = [os.path.join(CSRC, s) for s in SOURCES] + [EXT_SOURCE]
+def _library_inputs() -> list[str]:
+    files = [os.path.join(CSRC, s) for s in SOURCES]
     files += glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
     files += glob.glob(os.path.join(INCLUDE, "*.h"))
     return files
 
 
+def _inputs() -> list[str]:
+    return _library_inputs() + [EXT_SOURCE]
+
+
+def _newer(made: str, files: list[str]) -> bool:
+    return os.path.exists(made) and all(os.path.getmtime(f) <= os.path.getmtime(made) for f in files)
+
+
+def _python() -> str | None:
+    """What the binding is built for, this Python and PyTorch; None without PyTorch,
+    which the library itself does not need."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return None
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:  # not installed as a package
+        version = spec.origin
+    return f"{sys.implementation.cache_tag} {platform.machine()} torch {version}"
+
+
+def _stamp() -> str:
+    path = os.path.join(BUILD_DIR, "binding.for")
+    if not os.path.exists(path):
+        return ""
+    with open(path) as f:
+        return f.read()
+
+
+def library_up_to_date() -> bool:
+    return _newer(LIB_PATH, _library_inputs())
+
+
+def binding_up_to_date() -> bool:
+    """Whether there is a binding for this Python and PyTorch (or nothing to build one for)."""
+    want = _python()
+    return want is None or (_newer(EXT_PATH, [EXT_SOURCE] + glob.glob(os.path.join(INCLUDE, "*.h")))
+                            and _stamp() == want)
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(EXT_PATH):
-        return False
-    made = min(os.path.getmtime(LIB_PATH), os.path.getmtime(EXT_PATH))
-    return all(os.path.getmtime(f) <= made for f in _inputs())
+    return library_up_to_date() and binding_up_to_date()
 
 
 def _ext_command(out: str) -> tuple[list[str], list[str]]:
@@ -69,28 +110,43 @@ def _ext_command(out: str) -> tuple[list[str], list[str]]:
                 "-isystem", sysconfig.get_paths()["include"],
                 f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
                 "-c", EXT_SOURCE, "-o", obj]
-    link = [cxx, "-shared", "-o", out, obj, f"-L{HERE}", "-l:" + os.path.basename(LIB_PATH),
-            "-Wl,-rpath,$ORIGIN",
+    link = [cxx, "-shared", "-o", out, obj, f"-L{os.path.dirname(LIB_PATH)}",
+            "-l:" + os.path.basename(LIB_PATH), "-Wl,-rpath,$ORIGIN",
             f"-L{os.path.join(root, 'lib')}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
     return compile_, link
 
 
+def _started(cmd: list[str]) -> subprocess.Popen:
+    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+
+
+def _linked(cmd: list[str], tmp: str, path: str) -> None:
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("link failed:\n" + res.stdout + res.stderr)
+    os.replace(tmp, path)
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    """Compile and link the library; returns its path.  Raises on failure."""
-    if not force and up_to_date():
+    """Compile and link if needed, the binding too where PyTorch is there; returns the
+    library path."""
+    library = force or not library_up_to_date()
+    binding = _python() is not None and (force or not binding_up_to_date())
+    if not library and not binding:
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
     exe = nvcc()
     extra = ["-Xptxas", "-v"] if ptxas_info else []
-    procs = []
     ext_tmp = EXT_PATH + ".tmp"
-    ext_compile, ext_link = _ext_command(ext_tmp)
-    for src in SOURCES:
+    ext = None
+    procs = []
+    for src in SOURCES if library else []:
         obj = os.path.join(BUILD_DIR, src.replace(".cu", ".o"))
         cmd = [exe, *NVCC_FLAGS, *extra, "-c", os.path.join(CSRC, src), "-o", obj]
-        procs.append((src, obj, subprocess.Popen(cmd, stdout=subprocess.PIPE,
-                                                 stderr=subprocess.STDOUT, text=True)))
-    ext = subprocess.Popen(ext_compile, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+        procs.append((src, obj, _started(cmd)))
+    if binding:
+        ext_compile, ext_link = _ext_command(ext_tmp)
+        ext = _started(ext_compile)
     objs, errors = [], []
     for src, obj, p in procs:
         out, _ = p.communicate()
@@ -99,21 +155,19 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         elif verbose or ptxas_info:
             sys.stdout.write(out)
         objs.append(obj)
-    out, _ = ext.communicate()
-    if ext.returncode != 0:
-        errors.append(f"--- {os.path.basename(EXT_SOURCE)} ---\n{out}")
+    if ext:
+        out, _ = ext.communicate()
+        if ext.returncode != 0:
+            errors.append(f"--- {os.path.basename(EXT_SOURCE)} ---\n{out}")
     if errors:
         raise RuntimeError("compilation failed:\n" + "\n".join(errors))
-    tmp = LIB_PATH + ".tmp"
-    cmd = [exe, *ARCH, "-shared", "-o", tmp, *objs]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError("link failed:\n" + res.stdout + res.stderr)
-    os.replace(tmp, LIB_PATH)
-    res = subprocess.run(ext_link, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError("link failed:\n" + res.stdout + res.stderr)
-    os.replace(ext_tmp, EXT_PATH)
+    if library:
+        tmp = LIB_PATH + ".tmp"
+        _linked([exe, *ARCH, "-shared", "-o", tmp, *objs], tmp, LIB_PATH)
+    if binding:
+        _linked(ext_link, ext_tmp, EXT_PATH)
+        with open(os.path.join(BUILD_DIR, "binding.for"), "w") as f:
+            f.write(_python())
     return LIB_PATH
 
 
