@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(256) read_kernel(ReadParams p) {
       for (int k = 0; k < 2; ++k) {
         raw[k] = make_uint4(0, 0, 0, 0);
         scale[k] = 0.0f;
-        if (there) {
+        if (there && (k ? p.v_out : p.k_out)) {
           raw[k] = ld_stream_v4((k ? p.c.v : p.c.k) + at * (F16 ? 2 : 1));
           if (!F16) scale[k] = (k ? p.c.v_scale : p.c.k_scale)[sat];
         }

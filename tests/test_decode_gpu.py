@@ -706,6 +706,26 @@ def test_read_bits(nm, kind, rows, heads, dim, page):
         assert torch.equal(got.cpu(), want)
 
 
+@pytest.mark.parametrize("kind", KINDS)
+def test_read_of_one_half(nm, kind):
+    """Only k or only v asked for: the same rows, and the other half is not read (its
+    scales and codes do not matter)."""
+    from sparse_spmv_memory_gb300.decode import _Cache
+    import ctypes
+    gen = torch.Generator().manual_seed(2)
+    k, v, ks, vs = cuda(*ref.random_cache(kind, 9, 3, 16, 64, gen))
+    slots = torch.randint(0, 9 * 16, (50,), generator=gen).cuda()
+    rk, rv = nm.nm_cache_read(k, v, slots, ks, vs)
+    P = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    c = _Cache(k=P(k), v=P(v), k_scale=P(ks), v_scale=P(vs), pages=9, page_stride=3 * 16 * 64,
+               scale_page_stride=48, kv_heads=3, page_size=16, head_dim=64, type=KINDS.index(kind))
+    for want, which in ((rk, 0), (rv, 1)):
+        out = torch.zeros_like(want)
+        assert nm.lib().nm_cache_read(ctypes.byref(c), P(slots), 50, None if which else P(out),
+                                      P(out) if which else None, torch.cuda.current_stream().cuda_stream) == 0
+        assert torch.equal(out, want)
+
+
 # ---- verification --------------------------------------------------------------------
 def verify_case(seed, seqs, nodes, vocab, drafted, temperature, fp32, closeness=0.7, fan=3):
     """Inputs of a walk whose decisions all lie 1e-4 off their boundaries: fp32
