@@ -325,7 +325,8 @@ PyObject* tree_verify(PyObject* const* a) {
   const auto i32 = logits.options().dtype(at::kInt);
   Tensor mp, mc, mt;
   const OnStream on(a[12], tensor);
-  if (!path) mp = at::empty({seqs, std::max(0, max_nodes)}, i32);
+  // (the call refuses any other number of nodes, and nothing is allocated for it)
+  if (!path) mp = at::empty({seqs, std::min(std::max(1, max_nodes), 64)}, i32);
   if (!count) mc = at::empty({seqs}, i32);
   if (!token) mt = at::empty({seqs}, i32);
   vector(path, at::kInt, seqs * max_nodes, "path");

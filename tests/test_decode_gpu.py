@@ -1120,6 +1120,18 @@ def test_empty_calls(nm):
     torch.cuda.synchronize()
 
 
+def test_verify_refuses_any_number_of_nodes(nm):
+    """More nodes than a tree may have, however many: the status of the library, and no
+    path of that length is allocated first."""
+    logits = torch.zeros((3, 10), device="cuda")
+    ids = torch.zeros(3, dtype=torch.int32, device="cuda")
+    start = torch.zeros(60001, dtype=torch.int32, device="cuda")
+    for n in (65, 10 ** 6, 2 ** 31 - 1, 0, -1, -2 ** 31):
+        with pytest.raises(nm.NMError) as e:
+            nm.nm_tree_verify(logits, ids, ids, start, n, temperature=0.0)
+        assert e.value.status == 2
+
+
 @pytest.mark.parametrize("cache", KINDS)
 def test_example_decodes_as_one_token_at_a_time(nm, cache):
     """Speculative decoding at temperature 0 gives the tokens of plain decoding, and
