@@ -235,8 +235,8 @@ int nm_tree_verify(const void *logits, int logits_fp32, int64_t ld_logits, int64
 /* ---------------------------------------------------------------------------
  * nm_tree_attention_stall_selftest, nm_tree_verify_stall_selftest -- exercise
  * the bounded waits (self-tests): the calls above with every wait limited to
- * wait_limit_us (1 .. 2,000,000) and an arrival that never comes.  The many-row
- * attention kernel's loaders issue nothing (a call that goes to the few-row
+ * wait_limit_us (1 .. 2,000,000) and an arrival that never comes.  In every other
+ * block of the many-row attention kernel the loaders issue nothing (a call that goes to the few-row
  * kernel runs as usual: that one has no waits); of each sequence's blocks in
  * nm_tree_verify the last sends nothing to the first.  The waits run out or give
  * up after the first that did, are counted in nm_wait_timeouts(), and the kernel

@@ -63,6 +63,7 @@ constexpr int kRows = 128, kKeys = 128;
 constexpr int kSoftWarps = 8, kMmaWarp = 8, kLoadWarp = 9;
 constexpr int kMeta = 8;    // tiles of which it is kept which pages are there
 constexpr int kScales = 4;  // tiles whose scales are kept
+constexpr uint64_t kDrainNs = 100000000ull;  // copies in flight land long before
 constexpr int kBad = 16;    // items whose spoilt nodes are kept
 constexpr int kCopyPitch = 20;  // floats: 16 columns of a row, and its banks moved on by 20
 constexpr float kLift = 9.0f, kGrow = 6.9f;
@@ -270,7 +271,7 @@ __global__ void __launch_bounds__(Wide<D, TYPE, MODE>::THREADS, 1)
     int c = 0;  // positions of the ring so far
     int item_no = 0, tile_no = 0;
     uint32_t looked = 0;  // fp16: parity of each stage's looks so far
-    bool ok = !p.stall;
+    bool ok = !(p.stall && blockIdx.x % 2 == 0);
     struct Tile {      // a tile of an item; lane l has box l
       int page, row;   // the box's page and first row in it (of all heads')
       bool on;         // it is there
@@ -326,7 +327,10 @@ __global__ void __launch_bounds__(Wide<D, TYPE, MODE>::THREADS, 1)
       }
       if (look) {
         if (t.have) {
-          if (!wait_warp(bar, (looked >> st) & 1u)) return false;
+          if (!wait_warp(bar, (looked >> st) & 1u)) {
+            mbar_wait(bar, (looked >> st) & 1u, kDrainNs, false);  // the copies that it is for land
+            return false;
+          }
           looked ^= 1u << st;
         }
         constexpr int PR = D / 8;
@@ -519,10 +523,12 @@ __global__ void __launch_bounds__(Wide<D, TYPE, MODE>::THREADS, 1)
       }
       if (!F16)  // a last position for each group
         for (int i = 0; i < 2 && ok; ++i) ok = fetch8(false, nullptr, false);
-      // Before the block ends its copies have landed ...
+      // Before the block ends its copies have landed, whatever else failed (an fp16
+      // stage's barrier also has the loaders' arrivals, which may be missing then) ...
       constexpr int NC = F16 ? W::NS : RS;
       for (int pos = max(0, c - NC); pos < c; ++pos)
-        mbar_wait(F16 ? full(pos % W::NS) : rfull(pos % RS), (pos / NC) & 1, kWaitLimitNs, ok);
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(F16 ? full(pos % W::NS) : rfull(pos % RS), (pos / NC) & 1,
+                                               ok ? kWaitLimitNs : kDrainNs, false)) && ok;
       // ... and every release of a stage has arrived.
       if (F16)
         for (int pos = max(0, c - W::NS); ok && pos < c; ++pos)

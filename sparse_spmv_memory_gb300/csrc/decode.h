@@ -67,7 +67,7 @@ struct AttendParams {
   float* lse;  // may be null
   uint8_t* workspace;
   uint64_t wait_limit_ns;  // bound of every wait in the many-row kernel
-  int stall;               // self-test: its loaders issue nothing
+  int stall;               // self-test: the loaders of every other block issue nothing
 };
 size_t attend_workspace_bytes(int64_t seqs, int q_heads, int kv_heads, int head_dim, int max_nodes,
                               int sms);

@@ -533,6 +533,10 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(VerifyParams p, int
   __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  // All stores have been issued.  A block whose waits did not give up has received
+  // its own; for another they land within microseconds.
+  if (!ok)
+    for (int i = 0; i < 50; ++i) __nanosleep(1000);
 }
 
 bool rows_aligned(const void* p, int64_t ld, size_t size) {

@@ -1220,5 +1220,45 @@ def test_attention_wait_that_gives_up(nm, kind, nodes):
     assert nm.nm_wait_timeouts() == 0
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("nodes", [3, 6, 12, 24])
+def test_attention_gives_up_with_copies_in_flight(nm, kind, nodes):
+    """Half of the blocks give up soon; the others, with milliseconds of work before
+    them, then give up in the midst of it, copies and products in flight: they end as
+    well, and the next call is right."""
+    from sparse_spmv_memory_gb300.decode import _Cache
+    import ctypes
+    S, H, G, D, page, L = 128, 8, 8, 64, 64, 65536
+    gen = torch.Generator("cuda").manual_seed(nodes)
+    pages = L // page + 1
+    k, v = (torch.randn((pages, H, page, D), generator=gen, device="cuda") for _ in range(2))
+    ks = vs = None
+    if kind == "fp16":
+        k, v = k.half(), v.half()
+    else:
+        k, v = (x.clamp(-4, 4).mul(30).to(ref.DTYPES[kind]) for x in (k, v))
+        ks, vs = (torch.full((pages, H, page), 1 / 30, device="cuda") for _ in range(2))
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").expand(S, -1).contiguous()  # all of one text
+    ctx = torch.full((S,), L, dtype=torch.int32, device="cuda")
+    start = (torch.arange(S + 1, device="cuda") * nodes).to(torch.int32)
+    T = S * nodes
+    q = torch.randn((T, H * G, D), generator=gen, device="cuda").half()
+    need = nm.nm_tree_attention_workspace_bytes(S, H * G, H, D, nodes)
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    out, lse = torch.zeros_like(q), torch.zeros((T, H * G), device="cuda")
+    P = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    c = _Cache(k=P(k), v=P(v), k_scale=P(ks), v_scale=P(vs), pages=pages, page_stride=H * page * D,
+               scale_page_stride=H * page, kv_heads=H, page_size=page, head_dim=D, type=KINDS.index(kind))
+    good = nm.nm_tree_attention(q, k, v, table, ctx, start, nodes, k_scale=ks, v_scale=vs, workspace=ws)
+    for limit in (1, 500, 3000):
+        stalled(nm, lambda: nm.lib().nm_tree_attention_stall_selftest(
+            P(q), H * G * D, T, H * G, S, P(start), nodes, ctypes.byref(c), P(table), pages, pages, P(ctx), None,
+            D ** -0.5, P(out), H * G * D, P(lse), P(ws), need, limit, torch.cuda.current_stream().cuda_stream), 6.0)
+        nm.nm_wait_timeouts(reset=True)
+        again = nm.nm_tree_attention(q, k, v, table, ctx, start, nodes, k_scale=ks, v_scale=vs, workspace=ws)
+        assert torch.equal(again[0], good[0]) and torch.equal(again[1], good[1])
+        assert nm.nm_wait_timeouts() == 0
+
+
 def test_no_bounded_wait_gave_up(nm):
     assert nm.nm_wait_timeouts() == 0
