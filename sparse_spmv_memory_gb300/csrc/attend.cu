@@ -83,7 +83,7 @@ template <int D, int TYPE>
 struct Narrow {
   static constexpr bool F16 = TYPE == kCacheFp16;
   static constexpr int NW = F16 ? 8 : 12;       // warps
-  static constexpr int NG = F16 ? 2 : 2;       // groups of 8 positions in a unit
+  static constexpr int NG = 2;                // groups of 8 positions in a unit
   static constexpr int UK = 8 * NG;           // positions of a unit
   static constexpr int KS = D / 16;           // MMA k steps of a score
   static constexpr int NT = D / 8;            // n-tiles of an output row

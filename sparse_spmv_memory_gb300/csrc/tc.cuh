@@ -10,8 +10,8 @@ namespace nmk {
 
 // Number of mbarrier waits that gave up (see mbar_wait); read and reset by
 // nm_wait_timeouts().  Zero in every correct run.  Each translation unit that
-// includes this header (prefill.cu, attend_wide.cu) has a counter and a flag of
-// its own; nm_wait_timeouts adds the counters and clears the flags.
+// includes this header (prefill.cu, attend_wide_*.cu, verify.cu) has a counter and
+// a flag of its own; nm_wait_timeouts adds the counters and clears the flags.
 static __device__ unsigned long long g_wait_timeouts = 0;
 
 // Set by the first wait that gives up; every later abortable wait (in any
@@ -306,7 +306,7 @@ __device__ __forceinline__ void tmem_ld_16(uint32_t taddr, uint32_t (&v)[16]) {
       : "memory");
 }
 
-// 16 and 32 columns of this warp's 32 TMEM lanes, stored.
+// 16 columns of this warp's 32 TMEM lanes, stored.
 __device__ __forceinline__ void tmem_st_16(uint32_t taddr, const uint32_t* v) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
@@ -314,11 +314,6 @@ __device__ __forceinline__ void tmem_st_16(uint32_t taddr, const uint32_t* v) {
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
       "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
-}
-
-__device__ __forceinline__ void tmem_st_32(uint32_t taddr, const uint32_t (&v)[32]) {
-  tmem_st_16(taddr, v);
-  tmem_st_16(taddr + 16, v + 16);
 }
 
 __device__ __forceinline__ void tmem_st_wait() {
