@@ -74,7 +74,7 @@ __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
 // Hence 12 warps of 16 positions for codes (8 rows over 100000 positions, e4m3:
 // 69.0 us; 8 warps of 32: 72.4, 10: 73.4, 14: 92.4 and 16: 94.9, which spill),
 // and 8 warps for fp16, whose rows take twice the registers.  1 token over 500
-// positions: 9.3 us, of which launch, lengths and the table's look-up some 3, the
+// positions: 9.1 us, of which launch, lengths and the table's look-up some 3, the
 // loads 1.5, and joining warps, then blocks, 3.
 constexpr int kNarrowRows = 16;
 constexpr float kLift = 14.0f;
@@ -516,11 +516,11 @@ size_t attend_workspace_bytes(int64_t seqs, int q_heads, int kv_heads, int head_
 // and 25.5; over one of 500 (fp16) 13.3 and 15.5, the one case that it loses.
 // With up to 16 rows the narrow kernel begins and ends 2 to 4 us sooner, but has
 // fewer bytes of an fp16 cache in flight than the wide one's ring.  Of 8 rows and
-// 8 key heads (narrow, wide): 500 positions 9.3, 13.1 us; 4000 14.0, 16.8; 16000
-// 23.0, 25.3; 32000 35.0, 33.2; 100000 82.3, 70.4; 16 sequences of 4000 49.5,
-// 45.6; 64 of 1500 79.0, 66.9: even at 64 to 130 MB, taken by what the tables can
+// 8 key heads (narrow, wide): 500 positions 9.3, 13.1 us; 4000 14.3, 16.8; 16000
+// 23.1, 25.3; 32000 35.0, 33.6; 100000 82.3, 70.8; 16 sequences of 4000 49.5,
+// 46.1; 64 of 1500 79.0, 67.0: even at 64 to 130 MB, taken by what the tables can
 // hold, since the lengths are on the device.  Codes: 8 rows over 100000 positions
-// 69.2, 84 (e4m3) and 70.1, 72.9 (int8): the wide kernel's widening costs more.
+// 69.3, 84 (e4m3) and 70.4, 72.9 (int8): the wide kernel's widening costs more.
 cudaError_t launch_attend(const AttendParams& p, int head_dim, int type, int sms,
                           cudaStream_t stream) {
   const double held = (double)p.seqs * (double)p.table_cols * (double)(1 << p.c.page_shift) * p.c.kv_heads * head_dim * 4;

@@ -33,11 +33,11 @@
 //     with 160 KB in flight an SM; of the rest 10 us are start, end and join.
 //   fp16, 256 rows: a stream's chain scores -> softmax -> product.  A tile takes
 //     1.6 us (0.77 softmax, 4 x 0.27 MMAs, two streams in turn), 53 % of the tensor
-//     pipe; 16 sequences of 32 nodes over 8000 positions 98 us, 0.91 PFLOP/s.
-//     Threads that held 32 scores at a time, with a branch between: 116 us.
+//     pipe; 16 sequences of 32 nodes over 8000 positions 104 us, 0.86 PFLOP/s.
+//     Threads that held 32 scores at a time, with a branch between: 116 us (for 98 then).
 //   codes: the chain raw tile -> widened stage -> MMA -> free stage, 1.6 to 1.9 us a
 //     tile, since two stages of fp16 and six raw tiles fill the shared memory.
-//     64 rows over 100000 positions: int8 79.6 us, e4m3 91.  One group of ten
+//     64 rows over 100000 positions: int8 81.8 us, e4m3 90.8.  One group of ten
 //     widening warps in place of two of five: 89.7 and 97.5, with a third stage
 //     91.6 and 97.0.
 #pragma once

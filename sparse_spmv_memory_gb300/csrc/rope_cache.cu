@@ -83,9 +83,10 @@ __device__ __forceinline__ void turn_of(int pos, float f, float m, float& c, flo
 // to `turns` times.  Its lanes compute the token's cos and sin once, two angles
 // each, and hand them round by shuffles; a pair's other half comes from the lane
 // that has it.  No shared memory, no barrier, the next turn's load in flight.
-// What bounds it: latency for few tokens (one token of 48 heads 2.3 us), for many
-// the instructions of angles, shuffles and the codes' divisions (512 tokens of 80
-// heads to e4m3 6.5 us where its bytes take 3).
+// What bounds it: latency for few tokens (one token of 48 heads 1.8 us in a graph),
+// for many the issue of angles, shuffles and conversions, 2.5 instructions a clock,
+// and the waits between slot, position, frequencies and row (512 tokens of 80 heads
+// to e4m3 6.5 us with its inputs in L2, 8.5 from HBM, where its bytes take 3).
 template <int D, int TYPE>
 __global__ void __launch_bounds__(128) append_kernel(AppendParams p, int turns) {
   constexpr int L = D / 8, HEADS = 32 / L;  // lanes of a head, heads of a turn

@@ -21,8 +21,8 @@
 // to L2 meanwhile.
 //
 // Measured: a node costs 2 us to load and weigh and an exchange 1.1; 5 nodes of
-// one sequence over a vocabulary of 128256 take 12 us, 16 sequences of 32 nodes 38
-// (17 % of HBM's rate), 32 of 8 without draft over 50257 18.5.
+// one sequence over a vocabulary of 128256 take 12 us, 16 sequences of 32 nodes 39
+// (17 % of HBM's rate), 32 of 8 without draft over 50257 19.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -492,6 +492,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(VerifyParams p, int
       auto run = [&](int e, const float (&w)[8], const float (&r)[8]) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
+          // (2 units in the last place off at most: less than the weights themselves are)
           const float v = w[i] > 0.0f ? __fdividef(w[i], r[i]) : 0.0f;
           if (v > t.w && e + i < V) t = Best{v, e + i};  // ascending: the lowest of equals
         }
