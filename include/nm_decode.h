@@ -24,7 +24,8 @@
  *
  * Conventions, status codes and stream behaviour are nm_spmv.h's: the caller
  * owns every buffer, nothing is allocated, calls enqueue on `stream` and
- * return; arguments are checked on the host before anything is launched.
+ * return; arguments are checked on the host before anything is launched, among
+ * them that what a call writes meets nothing that it reads (NM_ERR_ALIAS).
  * Values that lie on the device (slots, page numbers, lengths, parents) are
  * checked by the kernels: an entry out of range is treated as absent, as each
  * call says, and never read or written through.  Launches use programmatic

@@ -5,6 +5,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "../../include/nm_decode.h"
 #include "decode.h"
 #include "kernels.h"
@@ -20,6 +22,19 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
   return a && b && na && nb && a0 < b0 + nb && b0 < a0 + na;
+}
+
+// An array that a call reads, in bytes.
+struct Input {
+  const void* at;
+  size_t bytes;
+};
+
+// Whether [b, b + nb) meets any of them.
+bool overlaps_any(const void* b, size_t nb, std::initializer_list<Input> inputs) {
+  for (const Input& i : inputs)
+    if (overlap(b, nb, i.at, i.bytes)) return true;
+  return false;
 }
 
 // Bytes from the first to the last element of `rows` rows of `width`, `ld` apart.
@@ -126,8 +141,11 @@ int nm_rope_append(const void* qkv, int64_t ldqkv, int64_t tokens, int q_heads,
     return NM_ERR_ALIGN;
   if (tokens == 0) return NM_OK;
   const size_t in = span(tokens, ldqkv, width, 2), out = span(tokens, ldq, qwidth, 2);
-  if (overlap(qkv, in, q_out, out) || overlaps_cache(cache, qkv, in) ||
-      (q_out && overlaps_cache(cache, q_out, out)))
+  const size_t pos = (size_t)tokens * 4, sb = (size_t)tokens * 8, fb = (size_t)(rot_dim / 2) * 4;
+  if (overlaps_any(q_out, out, {{qkv, in}, {positions, pos}, {slots, sb}, {inv_freq, fb}}) ||
+      overlaps_cache(cache, qkv, in) || (q_out && overlaps_cache(cache, q_out, out)) ||
+      overlaps_cache(cache, positions, pos) || overlaps_cache(cache, slots, sb) ||
+      overlaps_cache(cache, inv_freq, fb))
     return NM_ERR_ALIAS;
   int sms;
   if (sm_count(&sms) != NM_OK) return NM_ERR_CUDA;
@@ -158,7 +176,8 @@ int nm_cache_read(const nm_cache* cache, const int64_t* slots, int64_t rows, voi
   if (rows == 0 || (!k_out && !v_out)) return NM_OK;
   const size_t out = (size_t)rows * cache->kv_heads * cache->head_dim * 2;
   if (overlap(k_out, out, v_out, out) || overlaps_cache(cache, k_out, k_out ? out : 0) ||
-      overlaps_cache(cache, v_out, v_out ? out : 0))
+      overlaps_cache(cache, v_out, v_out ? out : 0) || overlap(k_out, out, slots, (size_t)rows * 8) ||
+      overlap(v_out, out, slots, (size_t)rows * 8))
     return NM_ERR_ALIAS;
   int sms;
   if (sm_count(&sms) != NM_OK) return NM_ERR_CUDA;
@@ -206,17 +225,21 @@ static int tree_attention(const void* q, int64_t ldq, int64_t tokens, int q_head
       !aligned(lse, 4) || !aligned(workspace, 16))
     return NM_ERR_ALIGN;
   if (seqs == 0 || tokens == 0) return NM_OK;
+  const size_t ob = span(tokens, ldo, width, 2), qb = span(tokens, ldq, width, 2);
+  const size_t lb = (size_t)tokens * q_heads * 4;
+  auto meets_input = [&](const void* at, size_t n) {
+    return overlaps_cache(cache, at, n) ||
+           overlaps_any(at, n, {{q, qb}, {q_start, (size_t)(seqs + 1) * 4}, {ctx_len, (size_t)seqs * 4},
+                                {block_table, span(seqs, ld_table, table_cols, 4)},
+                                {tree_mask, (size_t)tokens * 8}});
+  };
+  if (meets_input(out, ob) || (lse && meets_input(lse, lb)) || overlap(lse, lb, out, ob)) return NM_ERR_ALIAS;
   int sms;
   if (sm_count(&sms) != NM_OK) return NM_ERR_CUDA;
   const size_t need =
       attend_workspace_bytes(seqs, q_heads, cache->kv_heads, cache->head_dim, max_nodes, sms);
   if (need > 0 && (!workspace || workspace_bytes < need)) return NM_ERR_WORKSPACE;
-  const size_t ob = span(tokens, ldo, width, 2), qb = span(tokens, ldq, width, 2);
-  const size_t lb = (size_t)tokens * q_heads * 4;
-  if (overlap(out, ob, q, qb) || overlaps_cache(cache, out, ob) || overlap(lse, lb, q, qb) ||
-      overlap(lse, lb, out, ob) || overlaps_cache(cache, lse, lse ? lb : 0) ||
-      overlap(workspace, need, q, qb) || overlap(workspace, need, out, ob) ||
-      overlap(workspace, need, lse, lb) || overlaps_cache(cache, workspace, need))
+  if (meets_input(workspace, need) || overlap(workspace, need, out, ob) || overlap(workspace, need, lse, lb))
     return NM_ERR_ALIAS;
   p.q = static_cast<const __half*>(q);
   p.ldq = ldq;
@@ -287,9 +310,17 @@ static int tree_verify(const void* logits, int logits_fp32, int64_t ld_logits, i
   if (seqs == 0) return NM_OK;
   const size_t pb = (size_t)seqs * max_nodes * 4, cb = (size_t)seqs * 4;
   const size_t lb = span(tokens, ld_logits, vocab, logits_fp32 ? 4 : 2);
-  if (overlap(path, pb, count, cb) || overlap(path, pb, token, cb) ||
-      overlap(count, cb, token, cb) || overlap(path, pb, logits, lb) ||
-      overlap(count, cb, logits, lb) || overlap(token, cb, logits, lb))
+  const bool sampled = temperature > 0.0f;
+  const Input written[] = {{path, pb}, {count, cb}, {token, cb}};
+  for (const Input& w : written)
+    if (overlaps_any(w.at, w.bytes,
+                     {{logits, lb}, {ids, (size_t)tokens * 4}, {parents, (size_t)tokens * 4},
+                      {node_start, (size_t)(seqs + 1) * 4},
+                      {draft, sampled ? span(tokens, ld_draft, vocab, 4) : 0},
+                      {accept, sampled ? (size_t)tokens * 4 : 0},
+                      {race, sampled ? span(seqs, ld_race, vocab, 4) : 0}}))
+      return NM_ERR_ALIAS;
+  if (overlap(path, pb, count, cb) || overlap(path, pb, token, cb) || overlap(count, cb, token, cb))
     return NM_ERR_ALIAS;
   int sms;
   if (sm_count(&sms) != NM_OK) return NM_ERR_CUDA;

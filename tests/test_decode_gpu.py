@@ -1132,6 +1132,27 @@ def test_verify_refuses_any_number_of_nodes(nm):
         assert e.value.status == 2
 
 
+@pytest.mark.parametrize("nodes", [1, 9])
+def test_attention_workspace_over_an_input_refused(nm, nodes):
+    """A workspace that meets any array that the call reads or writes."""
+    b = Batch("int8", [40, 3], [nodes, 1], 8, 2, 64, 16, seed=2, spoil=False)
+    need = nm.nm_tree_attention_workspace_bytes(2, 8, 2, 64, nodes)
+    k, v, ks, vs = cuda(b.k, b.v, b.ks, b.vs)
+    args = dict(q=b.q.cuda(), block_table=b.table.cuda(), ctx_len=torch.tensor(b.ctx, dtype=torch.int32).cuda(),
+                q_start=torch.tensor(b.start, dtype=torch.int32).cuda(), tree_mask=signed(b.masks).cuda(),
+                out=torch.empty_like(b.q.cuda()), lse=torch.empty(b.q.shape[:2], device="cuda"))
+    ws = torch.zeros(need + (1 << 20), dtype=torch.uint8, device="cuda")
+    for name, t in args.items():
+        inside = ws[need - 64:].view(t.dtype)[:t.numel()].view(t.shape)
+        inside.copy_(t)
+        with pytest.raises(nm.NMError) as e:
+            nm.nm_tree_attention(k_cache=k, v_cache=v, max_nodes=nodes, k_scale=ks, v_scale=vs, workspace=ws[:need],
+                                 **dict(args, **{name: inside}))
+        assert e.value.status == 7, name
+        ws.zero_()
+    nm.nm_tree_attention(k_cache=k, v_cache=v, max_nodes=nodes, k_scale=ks, v_scale=vs, workspace=ws[:need], **args)
+
+
 @pytest.mark.parametrize("cache", KINDS)
 def test_example_decodes_as_one_token_at_a_time(nm, cache):
     """Speculative decoding at temperature 0 gives the tokens of plain decoding, and

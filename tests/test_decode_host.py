@@ -190,6 +190,44 @@ def test_empty_calls_take_no_addresses(nm):
         assert L.nm_tree_verify(N, 0, 8, 8, N, 0, N, N, N, tokens, seqs, 4, N, N, 8, t, N, N, N, N) == code
 
 
+def test_outputs_over_any_input_refused(nm):
+    """What a call writes may not meet anything that it reads."""
+    L, c = nm.lib(), cache()
+    qkv, pos, slots, freq, q = 0x400000000, 0x500000000, 0x510000000, 0x520000000, 0x600000000
+
+    def append(q=q, pos=pos, slots=slots, freq=freq):
+        return L.nm_rope_append(qkv, 512, 4, 4, pos, slots, freq, 64, 0, 1.0, q, 256, ref(c), None)
+    for over in (dict(pos=q + 16), dict(slots=q + 1024), dict(freq=q + 2040), dict(pos=0x100000000 + 64),
+                 dict(slots=0x200000000 + 8), dict(freq=0x310000000 + 4)):
+        assert append(**over) == 7, over
+    for k, v in ((slots, None), (None, slots + 16), (slots - 64, None)):
+        assert L.nm_cache_read(ref(c), slots, 4, k, v, None) == 7
+
+    base = dict(q=0x400000000, start=0x500000000, table=0x510000000, ctx=0x520000000, mask=0x530000000,
+                out=0x600000000, lse=0x610000000, ws=0x620000000)
+
+    def attend(**kw):
+        a = dict(base, **kw)
+        return L.nm_tree_attention(a["q"], 256, 8, 4, 2, a["start"], 4, ref(c), a["table"], 6, 6, a["ctx"],
+                                   a["mask"], 0.1, a["out"], 256, a["lse"], a["ws"], 1 << 40, None)
+    for written in ("out", "lse"):
+        for read in ("q", "start", "table", "ctx", "mask"):
+            assert attend(**{read: base[written] + 16}) == 7, (written, read)
+
+    base = dict(logits=0x400000000, draft=0x500000000, ids=0x600000000, par=0x601000000, start=0x602000000,
+                acc=0x603000000, race=0x604000000, path=0x700000000, count=0x701000000, token=0x702000000)
+
+    def verify(t=1.0, **kw):
+        a = dict(base, **kw)
+        return L.nm_tree_verify(a["logits"], 0, 1000, 1000, a["draft"], 1000, a["ids"], a["par"], a["start"], 8, 2,
+                                4, a["acc"], a["race"], 1000, t, a["path"], a["count"], a["token"], None)
+    for written in ("path", "count", "token"):
+        for read in ("logits", "draft", "ids", "par", "start", "acc", "race"):
+            assert verify(**{read: base[written]}) == 7, (written, read)
+            if read not in ("draft", "acc", "race"):  # not read at temperature 0
+                assert verify(t=0.0, **{read: base[written]}) == 7
+
+
 def test_stall_selftests_refuse_a_limit_out_of_range(nm):
     L, c = nm.lib(), cache()
     o = 0x500000000
