@@ -13,7 +13,8 @@ The operation (SparseDecoding, aimodeling.com article, "The Kernel Is the
 Other Half of the Answer"): y = W x for one token, with W kept N:M-sparse
 (2:4, 4:8, 8:16, 16:32) and stored as compact fp16 values plus one 32-bit
 mask word per 32 input columns.  ``decode`` adds the operators around those
-products in a step of speculative decoding (``include/nm_decode.h``).
+products in a step of speculative decoding (``include/nm_decode.h``), ``layer``
+those between them in a layer and at its answer (``include/nm_layer.h``).
 """
 from __future__ import annotations
 
@@ -34,6 +35,7 @@ __all__ = [
     "nm_prefill_stall_selftest",
     "nm_rope_inv_freq", "nm_rope_append", "nm_cache_read", "nm_tree_attention",
     "nm_tree_attention_workspace_bytes", "nm_tree_verify",
+    "nm_linear", "nm_linear_workspace_bytes", "nm_residual_norm", "nm_token_logprobs",
 ]
 
 NM_OK = 0
@@ -115,6 +117,7 @@ def _declare(L: ctypes.CDLL) -> ctypes.CDLL:
         f.argtypes = args
         f.restype = res
     decode.declare(L)
+    layer.declare(L)
     return L
 
 
@@ -484,3 +487,8 @@ from . import decode  # noqa: E402
 from .decode import (  # noqa: E402
     nm_cache_read, nm_rope_append, nm_rope_inv_freq, nm_tree_attention,
     nm_tree_attention_workspace_bytes, nm_tree_verify)
+
+# The operators between the products of a layer and at its answer.
+from . import layer  # noqa: E402
+from .layer import (  # noqa: E402
+    nm_linear, nm_linear_workspace_bytes, nm_residual_norm, nm_token_logprobs)

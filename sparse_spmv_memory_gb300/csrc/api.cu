@@ -52,77 +52,25 @@ cudaError_t ensure_max_smem(const void* func, int* done_flags, int max_devices) 
   return e;
 }
 
-}  // namespace nmk
+// ---- launch plans ------------------------------------------------------------
+static int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 
-using namespace nmk;
+static int spmv_pitch(int64_t words) { return (int)round_up(words, 32); }
 
-namespace {
-
-constexpr int64_t kMaxRows = (int64_t)1 << 31;
-constexpr int64_t kMaxCols = (int64_t)1 << 31;  // words per row then fit an int
-constexpr int kPrefillMaxSplits = 8;   // K slices the prefill plan considers
-constexpr int kPrefillMaxSlices = 64;  // K slices a caller may ask for
-constexpr int kMaxGrid24 = 65536;      // blocks an explicit 2:4 SpMM plan may ask for
-constexpr int kDefaultVariant24 = 1;  // 20 warps x 1 unit, 4 accumulator chains
-
-// nm_spmm24 indexes its 16-row x 128-column units in 32 bits.
-bool spmm24_fits(int64_t rows, int64_t cols) {
-  return (rows + 15) / 16 * (cols / 128) < ((int64_t)1 << 31);
-}
-
-// nm_spmm24's plan: variant, column slices (the fewest whose x fits a block's
-// shared memory; cs units each, the last slice the rest) and a grid of whole
-// slices (one block per SM by default, rounded down to a multiple of the
-// slices; an explicit grid likewise).
-struct Spmm24Plan {
-  int variant, slices, cs, grid;
-};
-
-bool make_spmm24_plan(int64_t cols, int variant, int grid, const DeviceInfo& d, Spmm24Plan* pl) {
-  const int units = (int)(cols / 128);
-  int S = spmm24_slices(units, (size_t)d.smem_optin);
-  if (S < 1) return false;
-  const int cs = (units + S - 1) / S;
-  S = (units + cs - 1) / cs;  // every slice non-empty
-  if (grid <= 0) grid = d.sms;
-  grid = grid / S * S;
-  if (grid < S) grid = S;
-  pl->variant = variant < 0 ? kDefaultVariant24 : variant;
-  pl->slices = S;
-  pl->cs = cs;
-  pl->grid = grid;
-  return true;
-}
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-  return na && nb && a0 < b0 + nb && b0 < a0 + na;
-}
-
-bool valid_pattern(int N, int M) {
-  return (N == 2 && M == 4) || (N == 4 && M == 8) || (N == 8 && M == 16) || (N == 16 && M == 32);
-}
-
-int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
-
-int spmv_pitch(int64_t words) { return (int)round_up(words, 32); }
-
-int64_t gemv_steps(int64_t cols) { return (cols + 511) / 512; }
+static int64_t gemv_steps(int64_t cols) { return (cols + 511) / 512; }
 
 // Measured on GB300 over the decode-layer shapes: the {20 warps, 3 steps in
 // flight, fp16 x} variant streams large matrices fastest; below ~134M weight
 // positions (where the launch's fixed start-up cost weighs more) the
 // {24 warps, 2 steps, fp32 x} variant is ahead, and up to 4096x4096 (2^24)
 // the {28 warps, 1 step, fp32 x} one.
-int default_spmv_variant(int64_t rows = 0, int64_t cols = 0) {
+static int default_spmv_variant(int64_t rows = 0, int64_t cols = 0) {
   const int64_t n = rows * cols;
   return n >= ((int64_t)1 << 27) ? 1 : (n > ((int64_t)1 << 24) ? 0 : 6);
 }
 
 // The dense baseline's fastest variant on every decode-layer shape measured.
-int default_gemv_variant() { return 0; }
+static int default_gemv_variant() { return 0; }
 
 // Builds the sparse launch plan; returns NM_OK or a status.
 int make_spmv_plan(int64_t rows, int64_t cols, int variant, int grid, SpmvPlan* plan,
@@ -148,7 +96,7 @@ int make_spmv_plan(int64_t rows, int64_t cols, int variant, int grid, SpmvPlan* 
   return NM_OK;
 }
 
-int make_gemv_plan(int64_t rows, int64_t cols, int variant, int grid, GemvPlan* plan,
+static int make_gemv_plan(int64_t rows, int64_t cols, int variant, int grid, GemvPlan* plan,
                    GemvParams* p) {
   DeviceInfo d;
   if (device_info(&d) != cudaSuccess) return NM_ERR_CUDA;
@@ -221,6 +169,58 @@ int make_spmm_plan(int64_t rows, int64_t cols, int batch, int variant, int grid,
 
 size_t spmm_workspace_for(const SpmmParams& p) {
   return p.slices > 1 ? (size_t)p.slices * p.batch * p.rows * sizeof(float) : 0;
+}
+
+}  // namespace nmk
+
+using namespace nmk;
+
+namespace {
+
+constexpr int64_t kMaxRows = (int64_t)1 << 31;
+constexpr int64_t kMaxCols = (int64_t)1 << 31;  // words per row then fit an int
+constexpr int kPrefillMaxSlices = 64;  // K slices a caller may ask for
+constexpr int kMaxGrid24 = 65536;      // blocks an explicit 2:4 SpMM plan may ask for
+constexpr int kDefaultVariant24 = 1;  // 20 warps x 1 unit, 4 accumulator chains
+
+// nm_spmm24 indexes its 16-row x 128-column units in 32 bits.
+bool spmm24_fits(int64_t rows, int64_t cols) {
+  return (rows + 15) / 16 * (cols / 128) < ((int64_t)1 << 31);
+}
+
+// nm_spmm24's plan: variant, column slices (the fewest whose x fits a block's
+// shared memory; cs units each, the last slice the rest) and a grid of whole
+// slices (one block per SM by default, rounded down to a multiple of the
+// slices; an explicit grid likewise).
+struct Spmm24Plan {
+  int variant, slices, cs, grid;
+};
+
+bool make_spmm24_plan(int64_t cols, int variant, int grid, const DeviceInfo& d, Spmm24Plan* pl) {
+  const int units = (int)(cols / 128);
+  int S = spmm24_slices(units, (size_t)d.smem_optin);
+  if (S < 1) return false;
+  const int cs = (units + S - 1) / S;
+  S = (units + cs - 1) / cs;  // every slice non-empty
+  if (grid <= 0) grid = d.sms;
+  grid = grid / S * S;
+  if (grid < S) grid = S;
+  pl->variant = variant < 0 ? kDefaultVariant24 : variant;
+  pl->slices = S;
+  pl->cs = cs;
+  pl->grid = grid;
+  return true;
+}
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+  return na && nb && a0 < b0 + nb && b0 < a0 + na;
+}
+
+bool valid_pattern(int N, int M) {
+  return (N == 2 && M == 4) || (N == 4 && M == 8) || (N == 8 && M == 16) || (N == 16 && M == 32);
 }
 
 int check_spmv_args(const void* values, const uint32_t* masks, int64_t rows, int64_t cols,
@@ -732,14 +732,15 @@ int nm_prefill_stall_selftest(const void* values, const uint32_t* masks, int64_t
 }
 
 int64_t nm_wait_timeouts(int reset) {
-  unsigned long long n[5] = {0};
+  unsigned long long n[6] = {0};
   if (read_wait_timeouts(&n[0], reset) != cudaSuccess ||
       read_attend_wait_timeouts<kCacheFp16>(&n[1], reset) != cudaSuccess ||
       read_attend_wait_timeouts<kCacheE4m3>(&n[2], reset) != cudaSuccess ||
       read_attend_wait_timeouts<kCacheInt8>(&n[3], reset) != cudaSuccess ||
-      read_verify_wait_timeouts(&n[4], reset) != cudaSuccess)
+      read_verify_wait_timeouts(&n[4], reset) != cudaSuccess ||
+      read_linear_wait_timeouts(&n[5], reset) != cudaSuccess)
     return -NM_ERR_CUDA;
-  return (int64_t)(n[0] + n[1] + n[2] + n[3] + n[4]);
+  return (int64_t)(n[0] + n[1] + n[2] + n[3] + n[4] + n[5]);
 }
 
 int64_t nm_check_masks(const uint32_t* masks, int64_t rows, int64_t cols, void* stream) {

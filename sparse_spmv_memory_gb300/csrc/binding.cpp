@@ -1,9 +1,9 @@
-// binding.cpp -- the Python side of nm_decode.h: tensors to pointers, sizes and
-// strides, checked.  The operators of a decoding step run for a few
+// binding.cpp -- the Python side of nm_decode.h and nm_layer.h: tensors to pointers,
+// sizes and strides, checked.  The operators of a decoding step run for a few
 // microseconds each, about what a handful of attribute reads of a tensor costs
 // in Python (a ctypes call of one of them took 25 us and more on the GB300's
-// host, this 4), so these calls are marshalled in C++; decode.py has their
-// signatures and documentation.
+// host, this 4), so these calls are marshalled in C++; decode.py and layer.py
+// have their signatures and documentation.
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <ATen/ops/zeros.h>
@@ -18,6 +18,7 @@
 #include <string>
 
 #include "../../include/nm_decode.h"
+#include "../../include/nm_layer.h"
 
 namespace {
 
@@ -342,6 +343,161 @@ PyObject* tree_verify(PyObject* const* a) {
   return tuple_of({wrapped(path, a[9], mp), wrapped(count, a[10], mc), wrapped(token, a[11], mt)});
 }
 
+// A float16 matrix of rows x cols with unit column stride; its row stride.
+int64_t half_rows(const Tensor& t, int64_t rows, int64_t cols, const char* what) {
+  if (t.scalar_type() != at::kHalf || t.dim() != 2 || t.size(0) != rows || t.size(1) != cols)
+    refuse(std::string(what) + " must be float16 [" + std::to_string(rows) + "][" + std::to_string(cols) + "]");
+  return row_stride(t, what);
+}
+
+// (values, masks, X, bias, activation, gated, scale, residual, Y, workspace, stream, cols)
+PyObject* linear(PyObject* const* a) {
+  Tensors tensor;
+  const Tensor &values = *tensor(a[0], "values"), &masks = *tensor(a[1], "masks"), &x = *tensor(a[2], "X");
+  const Tensor *bias = tensor(a[3], "bias", true), *residual = tensor(a[7], "residual", true),
+               *y = tensor(a[8], "Y", true), *ws = tensor(a[9], "workspace", true);
+  if (x.scalar_type() != at::kHalf || x.dim() != 2) refuse("X must be float16 [tokens][cols]");
+  const int64_t tokens = x.size(0), cols = a[11] == Py_None ? x.size(1) : integer(a[11]);
+  if (cols < 1 || cols > x.size(1)) refuse("cols must be 1 .. the width of X");
+  if (masks.scalar_type() != at::kInt || masks.dim() != 2 || !masks.is_contiguous() ||
+      masks.size(1) * 32 != cols)
+    refuse("masks must be contiguous int32 [rows][cols / 32]");
+  const int64_t rows = masks.size(0);
+  if (values.scalar_type() != at::kHalf || !values.is_contiguous() || values.numel() != rows * (cols / 2))
+    refuse("values must be contiguous float16 [rows][cols / 2]");
+  nm_epilogue e;
+  e.activation = int32(a[4], "activation");
+  e.gated = truth(a[5]) ? 1 : 0;
+  if (e.gated && rows % 2) refuse("a gated product needs an even number of rows");
+  const int64_t n = e.gated ? rows / 2 : rows;
+  vector(bias, at::kHalf, rows, "bias");
+  e.bias = pointer(bias);
+  e.residual = pointer(residual);
+  e.ldres = residual ? half_rows(*residual, tokens, n, "residual") : 0;
+  e.scale = (float)real(a[6]);
+  Tensor my, mw;
+  const OnStream on(a[10], tensor);
+  if (!y) my = at::empty({tokens, n}, x.options());
+  const Tensor& out = y ? *y : my;
+  const int64_t ldy = half_rows(out, tokens, n, "Y");
+  if (!ws) {
+    const size_t need = nm_linear_workspace_bytes(rows, cols, tokens);
+    if (need) mw = at::empty({(int64_t)need}, x.options().dtype(at::kByte));
+  } else if (!ws->is_contiguous()) {
+    refuse("workspace must be contiguous");
+  }
+  check(nm_linear(pointer(&values), pointer<uint32_t>(&masks), rows, cols, pointer(&x),
+                  tokens > 1 ? row_stride(x, "X") : (row_stride(x, "X") + 7) / 8 * 8, tokens, &e,
+                  pointer(&out), ldy, ws ? pointer(ws) : mw.defined() ? mw.data_ptr() : nullptr,
+                  ws ? ws->nbytes() : mw.defined() ? mw.nbytes() : 0, on.stream()),
+        "nm_linear");
+  return wrapped(y, a[8], my);
+}
+
+// A norm's weight and bias: float16 or float32 alike, [width] each.
+nm_norm norm_of(Tensors& tensor, PyObject* kind, PyObject* weight_, PyObject* bias_, int64_t width,
+                float offset, float eps, const char* what) {
+  const Tensor *w = tensor(weight_, what, true), *b = tensor(bias_, what, true);
+  nm_norm n;
+  n.kind = int32(kind, what);
+  n.offset = offset;
+  n.eps = eps;
+  const at::ScalarType type = w ? w->scalar_type() : b ? b->scalar_type() : at::kHalf;
+  if (type != at::kHalf && type != at::kFloat)
+    refuse(std::string("the weight and bias of ") + what + " must be float16 or float32");
+  n.params_fp32 = type == at::kFloat;
+  vector(w, type, width, what);
+  vector(b, type, width, what);
+  n.weight = pointer(w);
+  n.bias = pointer(b);
+  return n;
+}
+
+// (residual, block, norm, weight, bias, post_norm, post_weight, post_bias, gate, scale,
+//  residual_scale, weight_offset, eps, residual_out, out, stream)
+PyObject* residual_norm(PyObject* const* a) {
+  Tensors tensor;
+  const Tensor& r = *tensor(a[0], "residual");
+  const Tensor *block = tensor(a[1], "block", true), *gate = tensor(a[8], "gate", true),
+               *given_r = tensor(a[13], "residual_out", true), *given_o = tensor(a[14], "out", true);
+  const bool fp32 = r.scalar_type() == at::kFloat;
+  if ((!fp32 && r.scalar_type() != at::kHalf) || r.dim() != 2)
+    refuse("residual must be float16 or float32 [tokens][width]");
+  const int64_t tokens = r.size(0), width = r.size(1);
+  const float offset = (float)real(a[11]), eps = (float)real(a[12]);
+  const nm_norm pre = norm_of(tensor, a[2], a[3], a[4], width, offset, eps, "norm");
+  const nm_norm post = norm_of(tensor, a[5], a[6], a[7], width, offset, eps, "post_norm");
+  const double scale = real(a[9]), residual_scale = real(a[10]);
+  if (!block && (gate || post.kind != NM_NORM_NONE)) refuse("a gate or a norm after the block needs the block");
+  const int64_t ldr = row_stride(r, "residual");
+  const int64_t ldb = block ? half_rows(*block, tokens, width, "block") : 0;
+  int64_t ldg = 0;
+  if (gate) {
+    if (gate->dim() == 1 || gate->size(0) != tokens || tokens == 1)
+      vector(gate, at::kHalf, width, "gate");  // one for all tokens
+    else
+      ldg = half_rows(*gate, tokens, width, "gate");
+  }
+  if (pre.kind == NM_NORM_NONE && given_o) refuse("out needs a norm");
+  Tensor mr, mo;
+  const OnStream on(a[15], tensor);
+  // without a block and a factor the stream stays what it is
+  const bool same = !block && residual_scale == 1.0 && !given_r;
+  if (!given_r && !same) mr = at::empty({tokens, width}, r.options());
+  if (pre.kind != NM_NORM_NONE && !given_o) mo = at::empty({tokens, width}, r.options().dtype(at::kHalf));
+  const Tensor* to = given_r ? given_r : same ? nullptr : &mr;
+  const Tensor* o = given_o ? given_o : mo.defined() ? &mo : nullptr;
+  if (to && (to->scalar_type() != r.scalar_type() || to->sizes() != r.sizes()))
+    refuse("residual_out must be of residual's type and shape");
+  if (to || o)
+    check(nm_residual_norm(pointer(&r), fp32 ? 1 : 0, ldr, pointer(block), ldb, &post, pointer(gate), ldg,
+                           (float)scale, (float)residual_scale, pointer(to),
+                           to ? row_stride(*to, "residual_out") : 0, &pre, pointer(o),
+                           o ? half_rows(*o, tokens, width, "out") : 0, tokens, width, on.stream()),
+          "nm_residual_norm");
+  PyObject* first = o ? wrapped(given_o, a[14], mo) : Py_NewRef(Py_None);
+  return tuple_of({first, same ? Py_NewRef(a[0]) : wrapped(given_r, a[13], mr)});
+}
+
+// (logits, tokens, top, temperature, logprob, entropy, top_ids, top_logprob, stream)
+PyObject* token_logprobs(PyObject* const* a) {
+  Tensors tensor;
+  const Tensor& logits = *tensor(a[0], "logits");
+  const Tensor *ids = tensor(a[1], "tokens", true), *lp = tensor(a[4], "logprob", true),
+               *entropy = tensor(a[5], "entropy", true), *top_ids = tensor(a[6], "top_ids", true),
+               *top_lp = tensor(a[7], "top_logprob", true);
+  const bool fp32 = logits.scalar_type() == at::kFloat;
+  if (!fp32 && logits.scalar_type() != at::kHalf) refuse("logits must be float16 or float32");
+  const int64_t ld = row_stride(logits, "logits"), rows = logits.size(0), vocab = logits.size(1);
+  const int top = int32(a[2], "top");
+  if (ids && (ids->scalar_type() != at::kInt || ids->dim() < 1 || ids->dim() > 2 || ids->size(0) != rows))
+    refuse("tokens must be int32 [rows] or [rows][n]");
+  const bool flat = ids && ids->dim() == 1;
+  const int64_t n = !ids ? 0 : flat ? 1 : ids->size(1);
+  if (n > INT32_MAX) refuse("tokens is too large");
+  const int64_t ld_ids = !ids ? 0 : flat ? (rows > 1 ? ids->stride(0) : 1) : n ? row_stride(*ids, "tokens") : 0;
+  const auto f32 = logits.options().dtype(at::kFloat);
+  Tensor ml, me, mi, mt;
+  const OnStream on(a[8], tensor);
+  // (the call refuses any other number, and nothing is allocated for it)
+  const int64_t k = std::min(std::max(0, top), 32);
+  if (!lp) ml = flat ? at::empty({rows}, f32) : at::empty({rows, n}, f32);
+  if (!entropy) me = at::empty({rows}, f32);
+  if (!top_ids) mi = at::empty({rows, k}, f32.dtype(at::kInt));
+  if (!top_lp) mt = at::empty({rows, k}, f32);
+  vector(lp, at::kFloat, rows * n, "logprob");
+  vector(entropy, at::kFloat, rows, "entropy");
+  vector(top_ids, at::kInt, rows * k, "top_ids");
+  vector(top_lp, at::kFloat, rows * k, "top_logprob");
+  check(nm_token_logprobs(pointer(&logits), fp32 ? 1 : 0, ld, rows, vocab, pointer<int32_t>(ids), ld_ids, (int)n,
+                          (float)real(a[3]), pointer<float>(lp ? lp : &ml), pointer<float>(entropy ? entropy : &me),
+                          top, pointer<int32_t>(top_ids ? top_ids : &mi), pointer<float>(top_lp ? top_lp : &mt),
+                          on.stream()),
+        "nm_token_logprobs");
+  return tuple_of({wrapped(lp, a[4], ml), wrapped(entropy, a[5], me), wrapped(top_ids, a[6], mi),
+                   wrapped(top_lp, a[7], mt)});
+}
+
 // Runs a call, with whatever it throws turned into a Python exception.
 template <PyObject* (*CALL)(PyObject* const*), int ARGS>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -376,6 +532,12 @@ PyMethodDef kMethods[] = {
     {"tree_attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&entry<tree_attention, 15>)),
      METH_FASTCALL, nullptr},
     {"tree_verify", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&entry<tree_verify, 13>)),
+     METH_FASTCALL, nullptr},
+    {"linear", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&entry<linear, 12>)),
+     METH_FASTCALL, nullptr},
+    {"residual_norm", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&entry<residual_norm, 16>)),
+     METH_FASTCALL, nullptr},
+    {"token_logprobs", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&entry<token_logprobs, 9>)),
      METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 

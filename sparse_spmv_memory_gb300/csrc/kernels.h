@@ -8,6 +8,16 @@
 
 namespace nmk {
 
+// ---- the epilogue of nm_linear (epilogue.cuh) --------------------------------
+struct Epilogue {
+  const __half* bias = nullptr;      // [rows]
+  const __half* residual = nullptr;  // [tokens][ldres]
+  int64_t ldres = 0;
+  float scale = 1.f;
+  int act = 0;    // NM_ACT_*
+  int gated = 0;  // rows are (gate, up) pairs
+};
+
 // ---- sparse ----------------------------------------------------------------
 struct SpmvParams {
   const uint32_t* values;  // fp16 pairs, [rows][words*8] uint32
@@ -21,6 +31,7 @@ struct SpmvParams {
   int early_weights;  // 1: load the first weights before waiting on the previous kernel
   int64_t rows_q = 0;  // set by the launcher: rows (or row pairs) per block ...
   int rows_r = 0;      // ... and how many blocks take one more
+  Epilogue epi;        // epilogue 2 only
 };
 
 struct SpmvPlan {
@@ -33,9 +44,12 @@ int spmv_variant_warps(int variant);
 int spmv_variant_count();
 size_t spmv_smem_bytes(int pitch, int nw);
 // epilogue 0: y = W x; 1: rows are interleaved (gate, up) pairs and y receives
-// h = silu(gate) * up, rows/2 values.
+// h = silu(gate) * up, rows/2 values.  (2, nm_linear's: launch_spmv_linear, the
+// default plans' variants only.)
 cudaError_t launch_spmv(const SpmvParams& p, const SpmvPlan& plan, int flags,
                         cudaStream_t stream, int epilogue = 0);
+cudaError_t launch_spmv_linear(const SpmvParams& p, const SpmvPlan& plan, int flags,
+                               cudaStream_t stream);
 
 // ---- dense -----------------------------------------------------------------
 struct GemvParams {
@@ -84,6 +98,8 @@ struct SpmmParams {
   int bps = 1;         // blocks per column slice
   int steps_q = 0;     // steps per slice, and how many slices take one more
   int steps_r = 0;
+  Epilogue epi;        // nm_linear only, as the next
+  int ystride = 0;     // rows a block may have (launch_spmm_linear)
 };
 
 struct SpmmPlan {
@@ -106,6 +122,10 @@ cudaError_t launch_spmm_variant(const SpmmParams& p, int variant, int grid, int 
                                 cudaStream_t stream);
 cudaError_t launch_spmm(const SpmmParams& p, const SpmmPlan& plan, int flags,
                         cudaStream_t stream);
+// nm_linear's (the default plans' variants only): with one column slice the kernel
+// writes Y, with more the fp32 partials alone (then launch_linear_combine).
+cudaError_t launch_spmm_linear(const SpmmParams& p, const SpmmPlan& plan, int flags,
+                               cudaStream_t stream);
 
 // ---- small batches of a 2:4 matrix on the tensor cores (spmm24.cu) ----------
 struct Spmm24Params {
@@ -157,6 +177,7 @@ struct SpmmTcParams {
   float* part = nullptr;    // fp32 [slices][T][rows] when slices > 1
   uint64_t wait_limit_ns = 0;  // bound of every in-kernel wait (0: the default)
   int stall_weights = 0;       // self-test: the weight producer issues nothing
+  Epilogue epi;                // nm_linear only (launch_spmm_tc_linear)
 };
 
 int spmm_tc_variant_count();
@@ -168,6 +189,13 @@ void spmm_tc_default_plan(int64_t rows, int words, int64_t T, int sms, int varia
                           int max_splits, int* variant_out, int* splits_out);
 int spmm_tc_block_tokens(int variant);
 cudaError_t launch_spmm_tc(const SpmmTcParams& p, int variant, cudaStream_t stream);
+// nm_linear's: Y with the epilogue, or (slices > 1) the fp32 partials alone.
+cudaError_t launch_spmm_tc_linear(const SpmmTcParams& p, int variant, cudaStream_t stream);
+cudaError_t read_linear_wait_timeouts(unsigned long long* count, int reset);
+// Y from the fp32 partial sums [slices][tokens][rows], added in slice order.
+cudaError_t launch_linear_combine(const float* part, int slices, int64_t tokens, int64_t rows,
+                                  const Epilogue& epi, __half* Y, int64_t ldy, int sms,
+                                  cudaStream_t stream);
 // Number of bounded mbarrier waits that gave up since the last reset.
 cudaError_t read_wait_timeouts(unsigned long long* count, int reset);
 
@@ -200,6 +228,15 @@ inline cudaError_t launch_kernel(Kernel kernel, int grid, int block, size_t smem
   cfg.numAttrs = (flags & kFlagPdl) ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
+
+// Launch plans (api.cu).  variant < 0, grid <= 0, slices <= 0 ask for the default;
+// they return an nm_status.
+int make_spmv_plan(int64_t rows, int64_t cols, int variant, int grid, SpmvPlan* plan,
+                   SpmvParams* p);
+int make_spmm_plan(int64_t rows, int64_t cols, int batch, int variant, int grid, int slices,
+                   SpmmPlan* plan, SpmmParams* p);
+size_t spmm_workspace_for(const SpmmParams& p);
+constexpr int kPrefillMaxSplits = 8;  // K slices the prefill plan considers
 
 // Per-device attributes, queried once (api.cu).
 struct DeviceInfo {

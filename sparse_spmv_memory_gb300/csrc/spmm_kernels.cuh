@@ -35,6 +35,7 @@
 #include <stdint.h>
 
 #include "device.cuh"
+#include "epilogue.cuh"
 #include "kernels.h"
 #include "spmm_variants.h"
 #include "split.cuh"
@@ -439,7 +440,43 @@ __device__ __forceinline__ float warp_sum_tokens(float (&v)[BP], int lane) {
   return t;
 }
 
-template <int NW, int U, int BP, int XF>
+// EPI (nm_linear), one column slice: a block keeps its rows' fp32 sums in shared
+// memory, token by token, and finishes them after the cut-row combine, a token's
+// outputs side by side; blocks then own whole (gate, up) pairs where rows come in
+// pairs.  With column slices the sums go to the workspace as ever, and the combine
+// (linear.cu) has the epilogue.
+template <int NW, int BP>
+__device__ __forceinline__ void linear_epilogue(const SpmmParams& p, const float* ysm, int ystride,
+                                                int64_t r0, int64_t r1) {
+  __syncthreads();
+  const Epilogue& e = p.epi;
+  const int n = (int)(e.gated ? (r1 - r0) / 2 : r1 - r0);
+  const int64_t o0 = e.gated ? r0 / 2 : r0;
+  for (int k = threadIdx.x; k < n; k += NW * 32) {
+    const int64_t o = o0 + k;
+    float res[BP];
+#pragma unroll
+    for (int j = 0; j < BP; ++j) res[j] = j < p.batch ? residual_at(e, j, o) : 0.f;
+    const float b0 = bias_at(e, e.gated ? 2 * o : o), b1 = e.gated ? bias_at(e, 2 * o + 1) : 0.f;
+#pragma unroll
+    for (int j = 0; j < BP; ++j) {
+      if (j >= p.batch) break;
+      const float* s = ysm + j * ystride;
+      const float v = e.gated ? activate(s[2 * k] + b0, e.act) * (s[2 * k + 1] + b1)
+                              : activate(s[k] + b0, e.act);
+      p.Y[(int64_t)j * p.ldy + o] = __float2half_rn(fmaf(e.scale, v, res[j]));
+    }
+  }
+}
+
+// A block's rows among a slice's blocks: whole pairs where the epilogue wants them.
+template <bool EPI>
+__device__ __forceinline__ BlockRows slice_rows(const SpmmParams& p, int c) {
+  const BlockRows b = split_part(c, p.rows_q, p.rows_r, p.bps);
+  return EPI && p.epi.gated && p.slices == 1 ? BlockRows{2 * b.r0, 2 * b.r1} : b;
+}
+
+template <int NW, int U, int BP, int XF, bool EPI>
 __global__ void __launch_bounds__(NW * 32, 1) spmm_kernel(const SpmmParams p) {
   extern __shared__ __align__(16) float smem[];
   const int P = p.pitch;
@@ -449,10 +486,11 @@ __global__ void __launch_bounds__(NW * 32, 1) spmm_kernel(const SpmmParams p) {
   float* pf = smem + 34 * P * kSlotWords;               // [NW][BP]
   float* pl = pf + NW * BP;                             // [NW][BP]
   int* rinfo = reinterpret_cast<int*>(pl + NW * BP);    // [NW][4]
+  float* ysm = reinterpret_cast<float*>(rinfo + 4 * NW);  // EPI: [BP][ystride] sums of the block's rows
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sl = (int)(blockIdx.x / (unsigned)p.bps), c = blockIdx.x - sl * p.bps;  // slice, block in it
-  const BlockRows br = split_part(c, p.rows_q, p.rows_r, p.bps);
+  const BlockRows br = slice_rows<EPI>(p, c);
   const int64_t r0 = br.r0, r1 = br.r1;
   const BlockRows sr = split_part(sl, p.steps_q, p.steps_r, p.slices);
   const int ts0 = (int)sr.r0, ts1 = (int)sr.r1;
@@ -479,7 +517,11 @@ __global__ void __launch_bounds__(NW * 32, 1) spmm_kernel(const SpmmParams p) {
   const uint32_t tile_base = smem_addr(tile) + row_bytes;  // row b = 0
   auto store = [&](int row, const float (&v)[BP]) {
     const int64_t gr = r0 + row;
-    if (p.slices == 1) {
+    if (EPI && p.slices == 1) {
+#pragma unroll
+      for (int j = 0; j < BP; ++j)
+        if (j < p.batch) ysm[j * p.ystride + row] = v[j];
+    } else if (p.slices == 1) {
 #pragma unroll
       for (int j = 0; j < BP; ++j)
         if (j < p.batch) p.Y[(int64_t)j * p.ldy + gr] = __float2half_rn(v[j]);
@@ -545,6 +587,7 @@ __global__ void __launch_bounds__(NW * 32, 1) spmm_kernel(const SpmmParams p) {
 
   __syncthreads();
   combine_cut_rows_n<NW, BP>(rinfo, pf, pl, store);
+  if (EPI && p.slices == 1) linear_epilogue<NW, BP>(p, ysm, p.ystride, r0, r1);
 }
 
 // Whole-step kernel (cols % 1024 == 0, so every step of every slice is 32
@@ -574,7 +617,7 @@ __device__ __forceinline__ void load_steps_batch(SpmmBatch<U>& bt, const uint32_
   }
 }
 
-template <int NW, int U, int BP, int XF, bool SLICED>
+template <int NW, int U, int BP, int XF, bool SLICED, bool EPI>
 __global__ void __launch_bounds__(NW * 32, 1) spmm_full_kernel(const SpmmParams p) {
   extern __shared__ __align__(16) float smem[];
   const int P = p.pitch;
@@ -586,6 +629,7 @@ __global__ void __launch_bounds__(NW * 32, 1) spmm_full_kernel(const SpmmParams 
   float* pf = smem + 34 * P * kSlotWords;               // [NW][BP]
   float* pl = pf + NW * BP;                             // [NW][BP]
   int* rinfo = reinterpret_cast<int*>(pl + NW * BP);    // [NW][4]
+  float* ysm = reinterpret_cast<float*>(rinfo + 4 * NW);  // EPI: [BP][ystride] sums of the block's rows
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int sl = 0, ts0 = 0, Ts = p.steps;  // slice, its first step and steps of a row
@@ -598,7 +642,7 @@ __global__ void __launch_bounds__(NW * 32, 1) spmm_full_kernel(const SpmmParams 
     ts0 = (int)sr.r0;
     Ts = (int)(sr.r1 - sr.r0);
   } else {
-    br = block_rows(p.rows_q, p.rows_r);
+    br = EPI ? slice_rows<EPI>(p, blockIdx.x) : block_rows(p.rows_q, p.rows_r);
   }
   const int skip = p.steps - Ts;  // the other slices' steps
   const int F = (int)((br.r1 - br.r0) * Ts);
@@ -627,7 +671,9 @@ __global__ void __launch_bounds__(NW * 32, 1) spmm_full_kernel(const SpmmParams 
   // one token's sum of local row `row`: Y, or this slice's fp32 partial
   auto put = [&](int row, int j, float v) {
     const int64_t gr = br.r0 + row;
-    if (!SLICED)
+    if (EPI && !SLICED)
+      ysm[j * p.ystride + row] = v;
+    else if (!SLICED)
       p.Y[(int64_t)j * p.ldy + gr] = __float2half_rn(v);
     else
       p.partial[((int64_t)sl * p.batch + j) * p.rows + gr] = v;
@@ -710,22 +756,24 @@ __global__ void __launch_bounds__(NW * 32, 1) spmm_full_kernel(const SpmmParams 
 
   __syncthreads();
   combine_cut_rows_n<NW, BP>(rinfo, pf, pl, store);
+  if (EPI && !SLICED) linear_epilogue<NW, BP>(p, ysm, p.ystride, br.r0, br.r1);
 }
 
-template <int NW, int U, int BP, int XF>
+template <int NW, int U, int BP, int XF, bool EPI>
 cudaError_t launch_spmm_t(const SpmmParams& p, int grid, int flags, cudaStream_t stream) {
   static int smem_set[64] = {0}, smem_full[64] = {0}, smem_sliced[64] = {0};
-  const size_t smem = spmm_smem_bytes(p.pitch, NW, BP, XF);
-  const int64_t block_steps = (p.rows_q + 2) * (int64_t)p.steps;
+  const size_t smem = spmm_smem_bytes(p.pitch, NW, BP, XF) +
+                      (EPI && p.slices == 1 ? (size_t)BP * p.ystride * sizeof(float) : 0);
+  const int64_t block_steps = (EPI && p.epi.gated ? 2 : 1) * (p.rows_q + 2) * (int64_t)p.steps;
   if (p.words % 32 == 0 && block_steps < (int64_t)0x7FFFFFFF) {
-    auto* k = p.slices == 1 ? spmm_full_kernel<NW, U, BP, XF, false>
-                            : spmm_full_kernel<NW, U, BP, XF, true>;
+    auto* k = p.slices == 1 ? spmm_full_kernel<NW, U, BP, XF, false, EPI>
+                            : spmm_full_kernel<NW, U, BP, XF, true, EPI>;
     cudaError_t e = ensure_max_smem(reinterpret_cast<const void*>(k),
                                     p.slices == 1 ? smem_full : smem_sliced, 64);
     if (e != cudaSuccess) return e;
     return launch_kernel(k, grid, NW * 32, smem, stream, flags, p);
   }
-  auto* k = spmm_kernel<NW, U, BP, XF>;
+  auto* k = spmm_kernel<NW, U, BP, XF, EPI>;
   cudaError_t e = ensure_max_smem(reinterpret_cast<const void*>(k), smem_set, 64);
   if (e != cudaSuccess) return e;
   return launch_kernel(k, grid, NW * 32, smem, stream, flags, p);
@@ -741,7 +789,7 @@ cudaError_t launch_spmm_variant(const SpmmParams& p, int variant, int grid, int 
     if constexpr (BP == 6 && kSpmmVariants[i][2] != 0) return cudaErrorInvalidValue; \
     else                                                                            \
       return launch_spmm_t<kSpmmVariants[i][0], kSpmmVariants[i][1], BP,             \
-                           kSpmmVariants[i][2]>(p, grid, flags, stream);
+                           kSpmmVariants[i][2], false>(p, grid, flags, stream);
     NM_SPMM_CASE(0) NM_SPMM_CASE(1) NM_SPMM_CASE(2) NM_SPMM_CASE(3) NM_SPMM_CASE(4)
     NM_SPMM_CASE(5) NM_SPMM_CASE(6) NM_SPMM_CASE(7) NM_SPMM_CASE(8) NM_SPMM_CASE(9)
 #undef NM_SPMM_CASE
