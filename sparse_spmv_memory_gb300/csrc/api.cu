@@ -31,6 +31,8 @@ cudaError_t device_info(DeviceInfo* out) {
   if (e != cudaSuccess) return e;
   e = cudaDeviceGetAttribute(&d.smem_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
   if (e != cudaSuccess) return e;
+  e = cudaDeviceGetAttribute(&d.smem_sm, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev);
+  if (e != cudaSuccess) return e;
   if (dev >= 0 && dev < kMaxDevices) {
     g_info[dev] = d;
     g_info_ready[dev].store(1, std::memory_order_release);
@@ -39,7 +41,7 @@ cudaError_t device_info(DeviceInfo* out) {
   return cudaSuccess;
 }
 
-cudaError_t ensure_max_smem(const void* func, int* done_flags, int max_devices) {
+cudaError_t ensure_max_smem(const void* func, int* done_flags, int max_devices, int own) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -47,7 +49,7 @@ cudaError_t ensure_max_smem(const void* func, int* done_flags, int max_devices) 
   DeviceInfo d;
   e = device_info(&d);
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, d.smem_optin);
+  e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, d.smem_optin - own);
   if (e == cudaSuccess && dev < max_devices) __atomic_store_n(&done_flags[dev], 1, __ATOMIC_RELEASE);
   return e;
 }

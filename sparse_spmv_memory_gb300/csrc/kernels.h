@@ -242,11 +242,12 @@ constexpr int kPrefillMaxSplits = 8;  // K slices the prefill plan considers
 struct DeviceInfo {
   int sms;
   int smem_optin;  // bytes of dynamic shared memory a block may opt into
+  int smem_sm;     // bytes of shared memory of an SM
 };
 cudaError_t device_info(DeviceInfo* out);
 
-// Sets the dynamic shared memory limit of `func` to the device maximum once
-// per device.
-cudaError_t ensure_max_smem(const void* func, int* done_flags, int max_devices);
+// Sets the dynamic shared memory limit of `func` to the device maximum, less what its
+// own static arrays take, once per device.
+cudaError_t ensure_max_smem(const void* func, int* done_flags, int max_devices, int own = 0);
 
 }  // namespace nmk

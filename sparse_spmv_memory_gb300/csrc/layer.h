@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "kernels.h"
+
 namespace nmk {
 
 // ---- the residual stream's update and the norms around it (residual_norm.cu) ----
@@ -32,8 +34,11 @@ struct ResidualNormParams {
   int64_t ldo;
   int64_t tokens;
   int width;
+  // set by the launcher
+  float inv_width = 0.f;
+  int own_gate = 0;  // 1: a gate for every token
 };
-cudaError_t launch_residual_norm(const ResidualNormParams& p, int stream_fp32, int sms,
+cudaError_t launch_residual_norm(const ResidualNormParams& p, int stream_fp32, const DeviceInfo& d,
                                  cudaStream_t stream);
 
 // ---- log probabilities of tokens (logprobs.cu) ----------------------------------

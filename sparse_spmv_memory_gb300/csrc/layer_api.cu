@@ -276,7 +276,7 @@ int nm_residual_norm(const void* residual, int stream_fp32, int64_t ldr, const v
   p.ldo = out ? ldo : 0;
   p.tokens = tokens;
   p.width = (int)width;
-  return status(launch_residual_norm(p, stream_fp32, d.sms, static_cast<cudaStream_t>(stream)));
+  return status(launch_residual_norm(p, stream_fp32, d, static_cast<cudaStream_t>(stream)));
 }
 
 int nm_token_logprobs(const void* logits, int logits_fp32, int64_t ld_logits, int64_t rows,
