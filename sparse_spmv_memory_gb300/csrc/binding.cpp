@@ -181,6 +181,30 @@ PyObject* wrapped(const Tensor* given, PyObject* given_o, Tensor& made) {
   return given_o;
 }
 
+// Several outputs of a call in one allocation, each at a multiple of 256 bytes: an
+// allocation costs about a microsecond on the GB300's host, as much as the rest of a
+// call's marshalling.
+struct Outputs {
+  Tensor whole;
+  int64_t used = 0;
+
+  explicit Outputs(int64_t bytes, const at::TensorOptions& like)
+      : whole(at::empty({bytes}, like.dtype(at::kByte))) {}
+
+  static int64_t room(int64_t bytes) { return (bytes + 255) / 256 * 256; }
+
+  Tensor next(at::IntArrayRef sizes, at::ScalarType type) {
+    const caffe2::TypeMeta meta = c10::scalarTypeToTypeMeta(type);
+    auto impl = c10::make_intrusive<c10::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(), meta);
+    impl->set_storage_offset(used / (int64_t)meta.itemsize());
+    impl->set_sizes_contiguous(sizes);
+    int64_t n = (int64_t)meta.itemsize();
+    for (int64_t d : sizes) n *= d;
+    used += room(n);
+    return Tensor(std::move(impl));
+  }
+};
+
 PyObject* tuple_of(std::initializer_list<PyObject*> items) {
   PyObject* t = PyTuple_New((Py_ssize_t)items.size());
   Py_ssize_t i = 0;
@@ -443,8 +467,17 @@ PyObject* residual_norm(PyObject* const* a) {
   const OnStream on(a[15], tensor);
   // without a block and a factor the stream stays what it is
   const bool same = !block && residual_scale == 1.0 && !given_r;
-  if (!given_r && !same) mr = at::empty({tokens, width}, r.options());
-  if (pre.kind != NM_NORM_NONE && !given_o) mo = at::empty({tokens, width}, r.options().dtype(at::kHalf));
+  const bool make_r = !given_r && !same, make_o = pre.kind != NM_NORM_NONE && !given_o;
+  if (make_r && make_o) {
+    const int64_t n = tokens * width;
+    Outputs both(Outputs::room(n * (fp32 ? 4 : 2)) + n * 2, r.options());
+    mr = both.next({tokens, width}, r.scalar_type());
+    mo = both.next({tokens, width}, at::kHalf);
+  } else if (make_r) {
+    mr = at::empty({tokens, width}, r.options());
+  } else if (make_o) {
+    mo = at::empty({tokens, width}, r.options().dtype(at::kHalf));
+  }
   const Tensor* to = given_r ? given_r : same ? nullptr : &mr;
   const Tensor* o = given_o ? given_o : mo.defined() ? &mo : nullptr;
   if (to && (to->scalar_type() != r.scalar_type() || to->sizes() != r.sizes()))
@@ -481,10 +514,14 @@ PyObject* token_logprobs(PyObject* const* a) {
   const OnStream on(a[8], tensor);
   // (the call refuses any other number, and nothing is allocated for it)
   const int64_t k = std::min(std::max(0, top), 32);
-  if (!lp) ml = flat ? at::empty({rows}, f32) : at::empty({rows, n}, f32);
-  if (!entropy) me = at::empty({rows}, f32);
-  if (!top_ids) mi = at::empty({rows, k}, f32.dtype(at::kInt));
-  if (!top_lp) mt = at::empty({rows, k}, f32);
+  if (!lp || !entropy || !top_ids || !top_lp) {
+    const auto room = [](bool given, int64_t words) { return given ? 0 : Outputs::room(4 * words); };
+    Outputs made(room(lp, rows * n) + room(entropy, rows) + room(top_ids, rows * k) + room(top_lp, rows * k), f32);
+    if (!lp) ml = flat ? made.next({rows}, at::kFloat) : made.next({rows, n}, at::kFloat);
+    if (!entropy) me = made.next({rows}, at::kFloat);
+    if (!top_ids) mi = made.next({rows, k}, at::kInt);
+    if (!top_lp) mt = made.next({rows, k}, at::kFloat);
+  }
   vector(lp, at::kFloat, rows * n, "logprob");
   vector(entropy, at::kFloat, rows, "entropy");
   vector(top_ids, at::kInt, rows * k, "top_ids");
