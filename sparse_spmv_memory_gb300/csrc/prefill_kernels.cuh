@@ -177,36 +177,65 @@ __device__ __forceinline__ void densify_stage(uint32_t sA, uint32_t sV, uint32_t
   }
 }
 
-// The epilogue of nm_linear for 32 tokens (from t0) of the row held by each lane
-// of a warp.  Gated: lanes 2i and 2i + 1 hold a gate row and its up row; they
-// trade halves, so that the even lane finishes the first 16 tokens and the odd
-// lane the last 16, each token's outputs of a warp lying side by side.
+// One output of nm_linear, its bias added already.
+__device__ __forceinline__ __half linear_output(const Epilogue& e, float g, float u, float res) {
+  const float a = activate_fast(g, e.act);
+  return __float2half_rn(fmaf(e.scale, e.gated ? a * u : a, res));
+}
+
+// The epilogue of nm_linear for n <= 32 tokens (from t0) of the row held by each lane
+// of a warp.  Gated: lanes 2i and 2i + 1 hold a gate row and its up row; they trade
+// halves, so that the even lane finishes the first 16 tokens and the odd lane the last
+// 16, each token's outputs of a warp lying side by side.
 __device__ __forceinline__ void linear_store_32(const Epilogue& e, const uint32_t (&v)[32], bool row_ok,
-                                                int64_t r, int64_t t0, int64_t T, __half* Y,
+                                                int64_t r, int64_t t0, int n, __half* Y,
                                                 int64_t ldy, int lane) {
   const float b = row_ok ? bias_at(e, r) : 0.f;
   if (e.gated) {
     const bool odd = lane & 1;
     const float other_b = __shfl_xor_sync(0xFFFFFFFFu, b, 1);
     const int64_t o = r >> 1, first = t0 + (odd ? 16 : 0);
+    const int mine = row_ok ? n - (odd ? 16 : 0) : 0;
+    __half* y = Y + first * ldy + o;
+    const __half* res = e.residual ? e.residual + first * e.ldres + o : nullptr;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const float keep = __uint_as_float(odd ? v[16 + i] : v[i]) + b;
       const float send = __uint_as_float(odd ? v[i] : v[16 + i]);
       const float other = __shfl_xor_sync(0xFFFFFFFFu, send, 1) + other_b;
-      const int64_t t = first + i;
-      if (row_ok && t < T) {
-        const float g = odd ? other : keep, u = odd ? keep : other;
-        Y[t * ldy + o] = __float2half_rn(fmaf(e.scale, activate(g, e.act) * u, residual_at(e, t, o)));
+      if (i < mine) {
+        *y = linear_output(e, odd ? other : keep, odd ? keep : other, res ? __half2float(*res) : 0.f);
+        y += ldy;
+        if (res) res += e.ldres;
       }
     }
   } else if (row_ok) {
+    __half* y = Y + t0 * ldy + r;
+    if (e.residual) {
+      const __half* res = e.residual + t0 * e.ldres + r;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const int64_t t = t0 + i;
-      if (t < T)
-        Y[t * ldy + r] = __float2half_rn(
-            fmaf(e.scale, activate(__uint_as_float(v[i]) + b, e.act), residual_at(e, t, r)));
+      for (int i0 = 0; i0 < 32; i0 += 8) {
+        __half x[8];  // eight on their way at a time
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i0 + i < n) {
+            x[i] = *res;
+            res += e.ldres;
+          }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i0 + i < n) {
+            *y = linear_output(e, __uint_as_float(v[i0 + i]) + b, 0.f, __half2float(x[i]));
+            y += ldy;
+          }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (i < n) {
+          *y = linear_output(e, __uint_as_float(v[i]) + b, 0.f, 0.f);
+          y += ldy;
+        }
     }
   }
 }
@@ -482,7 +511,8 @@ __global__ void __launch_bounds__(threads_for(DW), 1)
           }
         } else if constexpr (EPI) {
           // (under a split, lanes past the last row come here too: the warp stays together)
-          if (!part) linear_store_32(epi, v, row_ok, r, n0 + c0, T, Y, ldy, lane);
+          if (!part && n0 + c0 < T)
+            linear_store_32(epi, v, row_ok, r, n0 + c0, (int)min((int64_t)32, T - n0 - c0), Y, ldy, lane);
         } else if (row_ok) {
 #pragma unroll
           for (int i = 0; i < 32; ++i) {

@@ -58,12 +58,12 @@ __global__ void __launch_bounds__(256) linear_combine_kernel(const float* __rest
 #pragma unroll
         for (int i = 0; i + 1 < V; i += 2) {
           const int64_t o = (r + i) / 2;
-          Y[t * ldy + o] = __float2half_rn(fmaf(e.scale, activate(s[i], e.act) * s[i + 1], residual_at(e, t, o)));
+          Y[t * ldy + o] = __float2half_rn(fmaf(e.scale, activate_fast(s[i], e.act) * s[i + 1], residual_at(e, t, o)));
         }
       } else {
 #pragma unroll
         for (int i = 0; i < V; ++i)
-          Y[t * ldy + r + i] = __float2half_rn(fmaf(e.scale, activate(s[i], e.act), residual_at(e, t, r + i)));
+          Y[t * ldy + r + i] = __float2half_rn(fmaf(e.scale, activate_fast(s[i], e.act), residual_at(e, t, r + i)));
       }
     }
   }
