@@ -177,7 +177,8 @@ struct SpmmTcParams {
   float* part = nullptr;    // fp32 [slices][T][rows] when slices > 1
   uint64_t wait_limit_ns = 0;  // bound of every in-kernel wait (0: the default)
   int stall_weights = 0;       // self-test: the weight producer issues nothing
-  Epilogue epi;                // nm_linear only (launch_spmm_tc_linear)
+  Epilogue epi;                // nm_linear only (launch_spmm_tc_linear), as the next
+  int tile = 0;                // tokens of one MMA: a multiple of 16 up to the variant's
 };
 
 int spmm_tc_variant_count();
@@ -191,6 +192,7 @@ int spmm_tc_block_tokens(int variant);
 cudaError_t launch_spmm_tc(const SpmmTcParams& p, int variant, cudaStream_t stream);
 // nm_linear's: Y with the epilogue, or (slices > 1) the fp32 partials alone.
 cudaError_t launch_spmm_tc_linear(const SpmmTcParams& p, int variant, cudaStream_t stream);
+int linear_tile(int variant, int64_t tokens);
 cudaError_t read_linear_wait_timeouts(unsigned long long* count, int reset);
 // Y from the fp32 partial sums [slices][tokens][rows], added in slice order.
 cudaError_t launch_linear_combine(const float* part, int slices, int64_t tokens, int64_t rows,

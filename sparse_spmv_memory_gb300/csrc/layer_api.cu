@@ -56,7 +56,7 @@ struct LinearPlan {
   SpmvParams vp;
   SpmmPlan spmm;
   SpmmParams mp;
-  int variant, slices;  // prefill
+  int variant, slices, tile;  // prefill
   int sms;
   size_t workspace;
 };
@@ -108,6 +108,7 @@ int linear_plan(int64_t rows, int64_t cols, int64_t tokens, int gated, LinearPla
   const int words = (int)(cols / 32);
   spmm_tc_default_plan(rows, words, tokens, d.sms, -1, 0, kPrefillMaxSplits, &pl->variant, &z);
   pl->slices = z;
+  pl->tile = linear_tile(pl->variant, tokens);
   pl->workspace = spmm_tc_workspace_bytes(rows, words, tokens, z);
   return NM_OK;
 }
@@ -223,6 +224,7 @@ int nm_linear(const void* values, const uint32_t* masks, int64_t rows, int64_t c
   p.wslice = spmm_tc_slice_words(p.words, pl.slices);
   p.part = part;
   p.epi = epi;
+  p.tile = pl.tile;
   const cudaError_t err = launch_spmm_tc_linear(p, pl.variant, s);
   if (err != cudaSuccess || p.slices == 1) return status(err);
   return status(launch_linear_combine(part, p.slices, tokens, rows, epi, out, ldy, pl.sms, s));

@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(threads_for(DW), 1)
                    const __grid_constant__ CUtensorMap tm_m, const uint32_t* __restrict__ masks,
                    __half* __restrict__ Y, float* __restrict__ part, int64_t rows, int words,
                    int wslice, int64_t T, int64_t ldy, uint64_t wait_limit_ns, int stall_weights,
-                   const Epilogue epi) {
+                   const Epilogue epi, int tile) {
   using L = Layout<NMMA, NB, STAGES, DG, MS, MT>;
   static_assert(DG == 1 || G == 1, "waiting on every second stage needs one densify group");
   // G = 2 waits on the odd stages' afull barriers only; with an even ring each
@@ -286,12 +286,15 @@ __global__ void __launch_bounds__(threads_for(DW), 1)
   };
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (EPI) pdl_launch_dependents();
   // After a wait gave up (this launch or an earlier one not yet reset), the
   // block does nothing: the decision is block-uniform, taken before any
   // barrier, copy or tensor-memory allocation.
   if (__syncthreads_or(threadIdx.x == 0 && wait_aborted())) return;
   const int64_t r0 = (int64_t)blockIdx.y * BM;
-  const int64_t n0 = (int64_t)blockIdx.x * L::BN;
+  // Tokens of one MMA: NMMA, or (EPI) what the launcher chose.
+  const int nmma = EPI ? tile : NMMA;
+  const int64_t n0 = (int64_t)blockIdx.x * (EPI ? NB * nmma : L::BN);
   // K split: this block multiplies the mask words w0 .. w0 + nk - 1 (stage
   // kt is word w0 + kt); w0 is a multiple of MW, so mask boxes stay aligned.
   const int w0 = (int)blockIdx.z * wslice;
@@ -322,6 +325,8 @@ __global__ void __launch_bounds__(threads_for(DW), 1)
   uint32_t tmem_base;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem_base) : "r"(slot) : "memory");
 
+  if (EPI) pdl_wait_previous();  // (everything above touches no argument's memory)
+
   // Teardown must not free shared memory under copies still in flight: a
   // producer waits (bounded) for the stages it issued among the last STAGES
   // of the row -- the final use of each slot, so the phase it waits for is
@@ -339,11 +344,11 @@ __global__ void __launch_bounds__(threads_for(DW), 1)
       for (int kt = 0; kt < nk; ++kt) {
         const int s = kt % STAGES, u = kt / STAGES;
         if (u > 0 && !mbar_wait(empty(s), (u - 1) & 1, wait_limit_ns)) break;
-        mbar_arrive_expect_tx(full(kt), L::B_BYTES);
+        mbar_arrive_expect_tx(full(kt), EPI ? NB * nmma * ROW_BYTES : L::B_BYTES);
 #pragma unroll
         for (int j = 0; j < NB; ++j)
           tma_load_2d(sB + s * L::B_BYTES + j * NMMA * ROW_BYTES, &tm_x, (w0 + kt) * BK,
-                      (int)(n0 + j * NMMA), full(kt));
+                      (int)(n0 + j * nmma), full(kt));
         last = kt;
       }
       drain(last);
@@ -418,7 +423,7 @@ __global__ void __launch_bounds__(threads_for(DW), 1)
     // into two accumulators).
     const int role = warp == 1 ? 0 : 1;
     if (lane == 0 && (role == 0 || MS != 0)) {
-      constexpr uint32_t idesc = idesc_f16_f32(BM, NMMA);
+      const uint32_t idesc = EPI ? idesc_f16_f32(BM, nmma) : idesc_f16_f32(BM, NMMA);
       const int k0 = MS ? role : 0, kstep = MS ? 2 : G;
       const uint32_t dacc = tmem_base + (uint32_t)(MS && role ? L::BN : 0);
       for (int kt = k0; kt < nk; kt += kstep) {
@@ -491,6 +496,11 @@ __global__ void __launch_bounds__(threads_for(DW), 1)
       const uint32_t tbase = tmem_base + ((uint32_t)(32 * quad) << 16);
 #pragma unroll 1
       for (int c0 = qi * 32; c0 < L::BN; c0 += QW * 32) {
+        // the chunk's first token and how many it has (EPI; the part of the accumulator
+        // behind an MMA's tokens holds nothing)
+        const int64_t t0 = EPI ? n0 + c0 / NMMA * nmma + c0 % NMMA : n0 + c0;
+        const int64_t left = EPI ? min((int64_t)min(nmma - c0 % NMMA, 32), T - t0) : 32;
+        if (EPI && left <= 0) continue;
         uint32_t v[32];
         tmem_ld_32(tbase + (uint32_t)c0, v);
         tmem_ld_wait();
@@ -506,13 +516,12 @@ __global__ void __launch_bounds__(threads_for(DW), 1)
           float* pz = part + (int64_t)blockIdx.z * T * rows + r;
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            const int64_t t = n0 + c0 + i;
-            if (t < T) pz[t * rows] = __uint_as_float(v[i]);
+            const int64_t t = t0 + i;
+            if (EPI ? i < left : t < T) pz[t * rows] = __uint_as_float(v[i]);
           }
         } else if constexpr (EPI) {
           // (under a split, lanes past the last row come here too: the warp stays together)
-          if (!part && n0 + c0 < T)
-            linear_store_32(epi, v, row_ok, r, n0 + c0, (int)min((int64_t)32, T - n0 - c0), Y, ldy, lane);
+          if (!part) linear_store_32(epi, v, row_ok, r, t0, (int)left, Y, ldy, lane);
         } else if (row_ok) {
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
@@ -553,6 +562,7 @@ static cudaError_t launch_tc_mt(const SpmmTcParams& p, cudaStream_t stream) {
   using L = Layout<NMMA, NB, STAGES, DG, MS, MT>;
   CUtensorMap tm_v, tm_x, tm_m;
   memset(&tm_m, 0, sizeof(tm_m));
+  const int tile = EPI ? p.tile : NMMA;  // tokens of an MMA
   if (MT && !encode_2d(&tm_m, p.masks, (uint64_t)p.words, (uint64_t)p.rows,
                        (uint64_t)p.words * 4, MW, BM, CU_TENSOR_MAP_SWIZZLE_NONE,
                        CU_TENSOR_MAP_DATA_TYPE_UINT32))
@@ -560,7 +570,7 @@ static cudaError_t launch_tc_mt(const SpmmTcParams& p, cudaStream_t stream) {
   if (!encode_2d(&tm_v, p.values, (uint64_t)p.words * 16, (uint64_t)p.rows,
                  (uint64_t)p.words * 32, 16, BM, CU_TENSOR_MAP_SWIZZLE_NONE) ||
       !encode_2d(&tm_x, p.X, (uint64_t)p.words * 32, (uint64_t)p.T, (uint64_t)p.ldx * 2, BK,
-                 NMMA, CU_TENSOR_MAP_SWIZZLE_64B))
+                 tile, CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorInvalidValue;
   auto* k = spmm_tc_kernel<NMMA, NB, STAGES, G, DG, DW, MS, MT, EPI>;
   static int attr_done[64] = {0};
@@ -572,17 +582,22 @@ static cudaError_t launch_tc_mt(const SpmmTcParams& p, cudaStream_t stream) {
     attr_done[dev] = 1;
   }
   const int wslice = p.slices > 1 ? p.wslice : p.words;
-  const dim3 grid((unsigned)((p.T + L::BN - 1) / L::BN), (unsigned)((p.rows + BM - 1) / BM),
+  const dim3 grid((unsigned)((p.T + NB * tile - 1) / (NB * tile)), (unsigned)((p.rows + BM - 1) / BM),
                   (unsigned)(p.slices > 1 ? p.slices : 1));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads_for(DW));
   cfg.dynamicSmemBytes = L::SMEM;
   cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = EPI ? 1 : 0;
   const uint64_t limit = p.wait_limit_ns ? p.wait_limit_ns : kWaitLimitNs;
   float* part = p.slices > 1 ? p.part : nullptr;
   return cudaLaunchKernelEx(&cfg, k, tm_v, tm_x, tm_m, p.masks, p.Y, part, p.rows, p.words,
-                            wslice, p.T, p.ldy, limit, p.stall_weights, p.epi);
+                            wslice, p.T, p.ldy, limit, p.stall_weights, p.epi, tile);
 }
 
 // Mask words by TMA when the mask array allows it (16-byte aligned, row pitch

@@ -20,6 +20,16 @@ cudaError_t launch_spmm_tc_linear(const SpmmTcParams& p, int variant, cudaStream
   }
 }
 
+// Tokens of one MMA: the tokens spread evenly over the blocks that the variant's full
+// tiles would need, and over a block's MMAs, in multiples of 16.  (300 tokens: two of
+// 160 in a block for two of 256.)
+int linear_tile(int variant, int64_t tokens) {
+  constexpr int kMmas[] = {2, 1, 1, 1, 2};
+  const int64_t full = spmm_tc_block_tokens(variant), blocks = (tokens + full - 1) / full;
+  const int64_t each = (tokens + blocks - 1) / blocks, n = kMmas[variant];
+  return (int)(((each + n - 1) / n + 15) / 16 * 16);
+}
+
 cudaError_t read_linear_wait_timeouts(unsigned long long* count, int reset) {
   return read_local_wait_timeouts(count, reset);
 }
