@@ -190,9 +190,12 @@ void spmm_tc_default_plan(int64_t rows, int words, int64_t T, int sms, int varia
                           int max_splits, int* variant_out, int* splits_out);
 int spmm_tc_block_tokens(int variant);
 cudaError_t launch_spmm_tc(const SpmmTcParams& p, int variant, cudaStream_t stream);
-// nm_linear's: Y with the epilogue, or (slices > 1) the fp32 partials alone.
+// nm_linear's: its own plan; the slices of a row tile are a cluster.
+struct LinearTcPlan {
+  int variant, slices, tile;
+};
+LinearTcPlan linear_tc_plan(int64_t rows, int words, int64_t tokens, int sms);
 cudaError_t launch_spmm_tc_linear(const SpmmTcParams& p, int variant, cudaStream_t stream);
-int linear_tile(int variant, int64_t tokens);
 cudaError_t read_linear_wait_timeouts(unsigned long long* count, int reset);
 // Y from the fp32 partial sums [slices][tokens][rows], added in slice order.
 cudaError_t launch_linear_combine(const float* part, int slices, int64_t tokens, int64_t rows,

@@ -56,7 +56,7 @@ struct LinearPlan {
   SpmvParams vp;
   SpmmPlan spmm;
   SpmmParams mp;
-  int variant, slices, tile;  // prefill
+  LinearTcPlan tc;
   int sms;
   size_t workspace;
 };
@@ -104,12 +104,7 @@ int linear_plan(int64_t rows, int64_t cols, int64_t tokens, int gated, LinearPla
   }
   if ((rows + 127) / 128 > 65535) return NM_ERR_SHAPE;
   pl->path = Path::kPrefill;
-  int z;
-  const int words = (int)(cols / 32);
-  spmm_tc_default_plan(rows, words, tokens, d.sms, -1, 0, kPrefillMaxSplits, &pl->variant, &z);
-  pl->slices = z;
-  pl->tile = linear_tile(pl->variant, tokens);
-  pl->workspace = spmm_tc_workspace_bytes(rows, words, tokens, z);
+  pl->tc = linear_tc_plan(rows, (int)(cols / 32), tokens, d.sms);
   return NM_OK;
 }
 
@@ -220,14 +215,11 @@ int nm_linear(const void* values, const uint32_t* masks, int64_t rows, int64_t c
   p.rows = rows;
   p.words = (int)(cols / 32);
   p.T = tokens;
-  p.slices = spmm_tc_slices(p.words, pl.slices);
-  p.wslice = spmm_tc_slice_words(p.words, pl.slices);
-  p.part = part;
+  p.slices = spmm_tc_slices(p.words, pl.tc.slices);
+  p.wslice = spmm_tc_slice_words(p.words, pl.tc.slices);
   p.epi = epi;
-  p.tile = pl.tile;
-  const cudaError_t err = launch_spmm_tc_linear(p, pl.variant, s);
-  if (err != cudaSuccess || p.slices == 1) return status(err);
-  return status(launch_linear_combine(part, p.slices, tokens, rows, epi, out, ldy, pl.sms, s));
+  p.tile = pl.tc.tile;
+  return status(launch_spmm_tc_linear(p, pl.tc.variant, s));
 }
 
 int nm_residual_norm(const void* residual, int stream_fp32, int64_t ldr, const void* block,

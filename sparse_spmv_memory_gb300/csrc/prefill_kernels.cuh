@@ -177,10 +177,51 @@ __device__ __forceinline__ void densify_stage(uint32_t sA, uint32_t sV, uint32_t
   }
 }
 
-// One output of nm_linear, its bias added already.
-__device__ __forceinline__ __half linear_output(const Epilogue& e, float g, float u, float res) {
-  const float a = activate_fast(g, e.act);
-  return __float2half_rn(fmaf(e.scale, e.gated ? a * u : a, res));
+// All threads of the cluster; those that have left count as there.
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// A shared-memory address of this block in block `rank` of the cluster.
+__device__ __forceinline__ uint32_t remote_smem(uint32_t at, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(at), "r"(rank));
+  return r;
+}
+
+// n <= N outputs of a lane, ldy apart: residual + scale * x.
+template <int N>
+__device__ __forceinline__ void store_outputs(const Epilogue& e, const float (&x)[N], int n, int64_t t0, int64_t o,
+                                              __half* Y, int64_t ldy) {
+  __half* y = Y + t0 * ldy + o;
+  if (e.residual) {
+    const __half* res = e.residual + t0 * e.ldres + o;
+#pragma unroll
+    for (int i0 = 0; i0 < N; i0 += 16) {
+      __half h[16];  // on their way at a time
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (i0 + i < n) {
+          h[i] = *res;
+          res += e.ldres;
+        }
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (i0 + i < n) {
+          *y = __float2half_rn(fmaf(e.scale, x[i0 + i], __half2float(h[i])));
+          y += ldy;
+        }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < n) {
+        *y = __float2half_rn(e.scale * x[i]);
+        y += ldy;
+      }
+  }
 }
 
 // The epilogue of nm_linear for n <= 32 tokens (from t0) of the row held by each lane
@@ -193,50 +234,24 @@ __device__ __forceinline__ void linear_store_32(const Epilogue& e, const uint32_
   const float b = row_ok ? bias_at(e, r) : 0.f;
   if (e.gated) {
     const bool odd = lane & 1;
-    const float other_b = __shfl_xor_sync(0xFFFFFFFFu, b, 1);
-    const int64_t o = r >> 1, first = t0 + (odd ? 16 : 0);
-    const int mine = row_ok ? n - (odd ? 16 : 0) : 0;
-    __half* y = Y + first * ldy + o;
-    const __half* res = e.residual ? e.residual + first * e.ldres + o : nullptr;
+    float g[16], u[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const float keep = __uint_as_float(odd ? v[16 + i] : v[i]) + b;
-      const float send = __uint_as_float(odd ? v[i] : v[16 + i]);
-      const float other = __shfl_xor_sync(0xFFFFFFFFu, send, 1) + other_b;
-      if (i < mine) {
-        *y = linear_output(e, odd ? other : keep, odd ? keep : other, res ? __half2float(*res) : 0.f);
-        y += ldy;
-        if (res) res += e.ldres;
-      }
+      const float lo = __uint_as_float(v[i]) + b, hi = __uint_as_float(v[16 + i]) + b;
+      const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? lo : hi, 1);
+      g[i] = odd ? other : lo;
+      u[i] = odd ? hi : other;
     }
-  } else if (row_ok) {
-    __half* y = Y + t0 * ldy + r;
-    if (e.residual) {
-      const __half* res = e.residual + t0 * e.ldres + r;
+    activate_fast(g, e.act);
 #pragma unroll
-      for (int i0 = 0; i0 < 32; i0 += 8) {
-        __half x[8];  // eight on their way at a time
+    for (int i = 0; i < 16; ++i) g[i] *= u[i];
+    store_outputs<16>(e, g, row_ok ? n - (odd ? 16 : 0) : 0, t0 + (odd ? 16 : 0), r >> 1, Y, ldy);
+  } else {
+    float x[32];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (i0 + i < n) {
-            x[i] = *res;
-            res += e.ldres;
-          }
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (i0 + i < n) {
-            *y = linear_output(e, __uint_as_float(v[i0 + i]) + b, 0.f, __half2float(x[i]));
-            y += ldy;
-          }
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (i < n) {
-          *y = linear_output(e, __uint_as_float(v[i]) + b, 0.f, 0.f);
-          y += ldy;
-        }
-    }
+    for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(v[i]) + b;
+    activate_fast(x, e.act);
+    store_outputs<32>(e, x, row_ok ? n : 0, t0, r, Y, ldy);
   }
 }
 
@@ -290,7 +305,9 @@ __global__ void __launch_bounds__(threads_for(DW), 1)
   // After a wait gave up (this launch or an earlier one not yet reset), the
   // block does nothing: the decision is block-uniform, taken before any
   // barrier, copy or tensor-memory allocation.
-  if (__syncthreads_or(threadIdx.x == 0 && wait_aborted())) return;
+  // (A cluster's blocks write each other's shared memory, so none of them leaves before
+  // the others: their waits give up at once instead.)
+  if (!(EPI && gridDim.z > 1) && __syncthreads_or(threadIdx.x == 0 && wait_aborted())) return;
   const int64_t r0 = (int64_t)blockIdx.y * BM;
   // Tokens of one MMA: NMMA, or (EPI) what the launcher chose.
   const int nmma = EPI ? tile : NMMA;
@@ -337,6 +354,7 @@ __global__ void __launch_bounds__(threads_for(DW), 1)
       mbar_wait(full(kt), full_par(kt), wait_limit_ns, false);
   };
 
+  bool fine = false;  // (densify warps) the accumulator is whole
   if (warp == 0) {
     // ---- X producer: the token tile of each stage -------------------------
     if (lane == 0) {
@@ -487,7 +505,8 @@ __global__ void __launch_bounds__(threads_for(DW), 1)
     if (!mbar_wait(accum, 0, wait_limit_ns)) ok = false;
     tc_fence_after_sync();
     // tcgen05.ld is a warp-wide instruction: the whole warp reads or none does.
-    if (__all_sync(0xFFFFFFFFu, ok)) {
+    fine = __all_sync(0xFFFFFFFFu, ok);
+    if (!EPI && fine) {
       const int quad = warp & 3;              // TMEM lanes 32*quad .. +31
       const int qi = dw >> 2;                 // this warp's index among its quadrant's warps
       constexpr int QW = DW / 4;              // warps per quadrant, striding the columns
@@ -496,11 +515,6 @@ __global__ void __launch_bounds__(threads_for(DW), 1)
       const uint32_t tbase = tmem_base + ((uint32_t)(32 * quad) << 16);
 #pragma unroll 1
       for (int c0 = qi * 32; c0 < L::BN; c0 += QW * 32) {
-        // the chunk's first token and how many it has (EPI; the part of the accumulator
-        // behind an MMA's tokens holds nothing)
-        const int64_t t0 = EPI ? n0 + c0 / NMMA * nmma + c0 % NMMA : n0 + c0;
-        const int64_t left = EPI ? min((int64_t)min(nmma - c0 % NMMA, 32), T - t0) : 32;
-        if (EPI && left <= 0) continue;
         uint32_t v[32];
         tmem_ld_32(tbase + (uint32_t)c0, v);
         tmem_ld_wait();
@@ -516,12 +530,9 @@ __global__ void __launch_bounds__(threads_for(DW), 1)
           float* pz = part + (int64_t)blockIdx.z * T * rows + r;
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            const int64_t t = t0 + i;
-            if (EPI ? i < left : t < T) pz[t * rows] = __uint_as_float(v[i]);
+            const int64_t t = n0 + c0 + i;
+            if (t < T) pz[t * rows] = __uint_as_float(v[i]);
           }
-        } else if constexpr (EPI) {
-          // (under a split, lanes past the last row come here too: the warp stays together)
-          if (!part) linear_store_32(epi, v, row_ok, r, t0, (int)left, Y, ldy, lane);
         } else if (row_ok) {
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
@@ -529,6 +540,87 @@ __global__ void __launch_bounds__(threads_for(DW), 1)
             if (t < T) Y[t * ldy + r] = __float2half_rn(__uint_as_float(v[i]));
           }
         }
+      }
+    }
+  }
+
+  if constexpr (EPI) {
+    // ---- nm_linear's epilogue -------------------------------------------------
+    // The accumulator's columns in pieces of 32 (an MMA's tokens may end inside one).
+    // Under a K split the blocks of a row tile's slices are a cluster: piece i is
+    // finished by block i % slices, to which the others send theirs through
+    // distributed shared memory (their rings lie idle by now), and which adds them in
+    // slice order: nothing goes through memory, and no second launch.
+    const int slices = (int)gridDim.z, me = (int)blockIdx.z;
+    const int per = (nmma + 31) / 32, pieces = NB * per;
+    const int dw = warp - FIRST_DENSIFY_WARP, quad = warp & 3, qi = dw >> 2;
+    const bool mine = warp >= FIRST_DENSIFY_WARP && warp < FIRST_DENSIFY_WARP + DW && fine;
+    constexpr int QW = DW / 4;
+    const int64_t r = r0 + 32 * quad + lane;
+    const uint32_t tbase = tmem_base + ((uint32_t)(32 * quad) << 16);
+    auto column = [&](int i) { return i / per * NMMA + i % per * 32; };
+    auto sums = [&](int i, uint32_t (&v)[32]) {
+      tmem_ld_32(tbase + (uint32_t)column(i), v);
+      tmem_ld_wait();
+      if (MS && nk > 1) {  // the odd stages' accumulator (none when nk == 1)
+        uint32_t w[32];
+        tmem_ld_32(tbase + (uint32_t)(L::BN + column(i)), w);
+        tmem_ld_wait();
+#pragma unroll
+        for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) + __uint_as_float(w[k]));
+      }
+    };
+    // its first token, and how many it has
+    auto first = [&](int i) { return n0 + i / per * nmma + i % per * 32; };
+    auto count = [&](int i) { return (int)min((int64_t)min(nmma - i % per * 32, 32), T - first(i)); };
+    // Where block `from`'s piece i lies in the shared memory of the block that finishes it:
+    // [place among the others][its pieces][32 tokens][128 rows] fp32.
+    const int share = (pieces + slices - 1) / slices;
+    auto inbox = [&](int i, int from) {
+      const int to = i % slices, at = (from < to ? from : from - 1) * share + i / slices;
+      return base + (uint32_t)(at * (32 * BM * 4) + (32 * quad + lane) * 4);
+    };
+    if (slices > 1) {
+      cluster_sync();  // every block is done with its ring
+      if (mine) {
+#pragma unroll 1
+        for (int i = qi; i < pieces; i += QW) {
+          if (i % slices == me || count(i) <= 0) continue;
+          uint32_t v[32];
+          sums(i, v);
+          const uint32_t to = remote_smem(inbox(i, me), (uint32_t)(i % slices));
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to + k * (BM * 4)), "r"(v[k]) : "memory");
+        }
+      }
+      cluster_sync();
+    }
+    if (mine) {
+#pragma unroll 1
+      for (int i = me + qi * slices; i < pieces; i += QW * slices) {
+        const int n = count(i);
+        if (n <= 0) continue;
+        uint32_t v[32];
+        sums(i, v);
+        if (slices > 1) {
+          float acc[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) acc[k] = 0.f;
+          for (int z = 0; z < slices; ++z) {
+            if (z == me) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k) acc[k] += __uint_as_float(v[k]);
+            } else {
+              const uint32_t from = inbox(i, z);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) acc[k] += lds_f32(from + k * (BM * 4));
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(acc[k]);
+        }
+        linear_store_32(epi, v, r < rows, r, first(i), n, Y, ldy, lane);
       }
     }
   }
@@ -572,6 +664,10 @@ static cudaError_t launch_tc_mt(const SpmmTcParams& p, cudaStream_t stream) {
       !encode_2d(&tm_x, p.X, (uint64_t)p.words * 32, (uint64_t)p.T, (uint64_t)p.ldx * 2, BK,
                  tile, CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorInvalidValue;
+  if (EPI && p.slices > 1) {  // what a block is sent fits its ring
+    const int pieces = NB * ((tile + 31) / 32), share = (pieces + p.slices - 1) / p.slices;
+    if ((p.slices - 1) * share * 32 * BM * 4 > L::M_OFF) return cudaErrorInvalidValue;
+  }
   auto* k = spmm_tc_kernel<NMMA, NB, STAGES, G, DG, DW, MS, MT, EPI>;
   static int attr_done[64] = {0};
   int dev = 0;
@@ -589,11 +685,14 @@ static cudaError_t launch_tc_mt(const SpmmTcParams& p, cudaStream_t stream) {
   cfg.blockDim = dim3(threads_for(DW));
   cfg.dynamicSmemBytes = L::SMEM;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = grid.z;
   cfg.attrs = attr;
-  cfg.numAttrs = EPI ? 1 : 0;
+  cfg.numAttrs = EPI ? (grid.z > 1 ? 2 : 1) : 0;
   const uint64_t limit = p.wait_limit_ns ? p.wait_limit_ns : kWaitLimitNs;
   float* part = p.slices > 1 ? p.part : nullptr;
   return cudaLaunchKernelEx(&cfg, k, tm_v, tm_x, tm_m, p.masks, p.Y, part, p.rows, p.words,

@@ -113,7 +113,7 @@ def test_linear_long_rows(nm, tokens, rows, cols, gated):
 def test_linear_every_kind_of_plan_is_met(nm):
     need = nm.nm_linear_workspace_bytes
     assert need(20, 53248, 1) > 0 and need(4096, 4096, 1) == 0 and need(40, 28672, 8) > 0
-    assert need(300, 1056, 8) == 0 and need(64, 28672, 16) > 0 and need(57344, 8192, 2048) == 0
+    assert need(300, 1056, 8) == 0 and need(64, 28672, 16) == 0 and need(57344, 8192, 2048) == 0
     assert need(0, 64, 4) == need(4, 64, 0) == need(4, 33, 4) == need(-1, 64, 4) == 0
 
 
@@ -154,10 +154,10 @@ def test_linear_in_place_and_rows_between(nm, tokens, gated):
 
 
 def test_linear_agrees_with_the_products_it_extends(nm):
-    """Without an epilogue the bits are those of nm_spmv, nm_spmm and nm_spmm_prefill;
-    gated SiLU of one token those of nm_spmv_swiglu up to its own rounding."""
+    """Up to 8 tokens, where the plans are the same, the bits without an epilogue are those
+    of nm_spmv and nm_spmm, and gated SiLU of one token has those of nm_spmv_swiglu."""
     for rows, cols in [(300, 1056), (1000, 4096)]:
-        for tokens in (1, 2, 4, 6, 8, 9, 64, 300):
+        for tokens in (1, 2, 4, 6, 8):
             p = Product(nm, rows, cols, tokens, seed=tokens)
             y = p.run(nm)
             if tokens == 1:
