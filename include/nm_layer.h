@@ -49,11 +49,12 @@ extern "C" {
  *              nm_linear_workspace_bytes(rows, cols, tokens) bytes (may be NULL
  *              when that is 0); it needs no initial contents.
  * Sums, bias, activation, scale and residual are fp32, with one rounding to fp16
- * at the end.  1 token runs on nm_spmv's kernels, 2..8 on nm_spmm's, more on
- * nm_spmm_prefill's, each with its arithmetic (up to 8 tokens pruned weights
- * are never multiplied; beyond, a non-finite X[t][c] reaches every row).  The
- * summation order is fixed for a shape and device.  The tensor-core kernels'
- * bounded waits count in nm_wait_timeouts.
+ * at the end.  1 token runs on nm_spmv's kernels, 2..8 on nm_spmm's, each with its
+ * arithmetic, more on a tensor-core kernel of its own (fp16 products, fp32 sums; up
+ * to 8 tokens pruned weights are never multiplied; beyond, a non-finite X[t][c]
+ * reaches every row of its token).  The summation order is fixed for a shape and
+ * device.  Only 2..8 tokens of few rows or long columns need the workspace.  The
+ * tensor-core kernel's bounded waits count in nm_wait_timeouts.
  * rows == 0 or tokens == 0 is a no-op.  tokens < 2^31, rows < 2^31 and beyond 8
  * tokens ceil(rows / 128) <= 65535, else NM_ERR_SHAPE.
  * ------------------------------------------------------------------------- */

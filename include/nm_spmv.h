@@ -372,7 +372,7 @@ int nm_spmm_prefill_plan(int64_t rows, int64_t cols, int64_t T, int sms, int *va
  * every correct run; `reset` != 0 resets the count to zero and clears the
  * abort flag.  After a nonzero count, treat the outputs of the tensor-core
  * calls since the last reset as undefined.  The attention and verification
- * kernels of nm_decode.h count here too.
+ * kernels of nm_decode.h and nm_linear of nm_layer.h count here too.
  * Host-synchronous (reads a device counter); negative nm_status on error. */
 int64_t nm_wait_timeouts(int reset);
 

@@ -178,7 +178,7 @@ struct SpmmTcParams {
   uint64_t wait_limit_ns = 0;  // bound of every in-kernel wait (0: the default)
   int stall_weights = 0;       // self-test: the weight producer issues nothing
   Epilogue epi;                // nm_linear only (launch_spmm_tc_linear), as the next
-  int tile = 0;                // tokens of one MMA: a multiple of 16 up to the variant's
+  int tile = 0;                // tokens of one MMA: a multiple of 16 up to the variant's most
 };
 
 int spmm_tc_variant_count();

@@ -1,0 +1,651 @@
+// linear_tc.cu -- nm_linear for more than 8 tokens: Y = residual + scale * act(W X + bias)
+// on the sm_103a tensor cores, W in the N:M bitmask format.
+//
+// As in prefill.cu a block owns 128 rows of W (the MMA's M, TMEM lanes) and a tile of
+// tokens (its N), K advances by one mask word a stage, producers load a stage's compact
+// values, mask words and token tile by TMA, densify warps expand the weights to a
+// swizzled fp16 tile, one or two threads issue the MMAs, and the accumulator stays in
+// tensor memory.  What is this kernel's own:
+//  * The rings are apart.  A stage's compact values are free again once they are
+//    expanded, its expanded tile and its token tile once its MMAs are done, and the token
+//    tile is the largest by far (32 KB of 512 tokens; an expanded tile has 8 KB, compact
+//    values 4).  One ring of all three has as many stages as token tiles fit, 5 at 512
+//    tokens, and a stage then takes a fifth of the way from an empty slot through the
+//    loads, the expansion and the MMAs: 441 ns at 512 tokens, and still 375 at 32, with the
+//    tensor pipe 53 % busy.  Twelve slots of values, which come from HBM, and four each of
+//    the others take 380 ns at 512 tokens (the MMAs alone 332) and 322 at 32.
+//  * An MMA has as many tokens as there are (a multiple of 16), not a full tile's.
+//  * A K split's blocks are a cluster and trade their sums through distributed shared
+//    memory (see the epilogue): no workspace, no second launch.
+//  * The epilogue, and launches that overlap the previous kernel's end.
+// Every mbarrier wait is bounded as prefill.cu's are (the same limits and counters).
+#include <cuda.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+#include <string.h>
+
+#include "densify.cuh"
+#include "device.cuh"
+#include "epilogue.cuh"
+#include "kernels.h"
+#include "tc.cuh"
+
+namespace nmk {
+namespace tc {
+namespace {
+
+constexpr int DW = 16;  // densify warps
+constexpr int lcm_int(int a, int b) { return a / gcd_int(a, b) * b; }
+
+// NMMA: tokens of an MMA at most; NB MMAs a block and K step; SA, SB, SV: slots of
+// expanded weights, token tiles and compact values; DG densify groups, which take the
+// stages in turn.  Two threads issue MMAs: MS 1, the even and the odd stages into two
+// accumulators; MS 2, the two MMAs of every K step.  MT: masks come by TMA, MW stages a box
+// (the mask array is 16-byte aligned with rows of whole boxes), else by cp.async.
+//
+// Barriers.  A parity wait tells a phase from the one before it only, so it is exact
+// only if the waiter saw the barrier's phase before, or the barrier cannot have gone a
+// phase further.  fullv (values there): a ring of lcm(SV, DG), so that all phases of one
+// belong to one group.  fullb (tokens there) and afull (weights expanded): rings of an
+// even number of slots where two issuers take turns.  done (MMAs complete), by stage: the
+// token producer waits for all of them in order; the densify warps of stage kt wait for
+// stage kt - SA, and RD being a multiple of 2 SA, the stage that would complete the same
+// barrier's next phase needs the slot that they are about to fill.
+template <int NMMA, int NB, int SA, int SB, int SV, int DG, int MS, bool MT>
+struct Shape {
+  static constexpr int BN = NMMA * NB;
+  static constexpr int B_BYTES = BN * ROW_BYTES;
+  static constexpr int A_OFF = 0;
+  static constexpr int B_OFF = A_OFF + SA * A_BYTES;
+  static constexpr int V_OFF = B_OFF + SB * B_BYTES;
+  static constexpr int M_OFF = V_OFF + SV * V_BYTES;
+  static constexpr int MT_SLOTS = 3;  // the groups' stages may lie in two boxes; one on its way
+  static constexpr int BAR_OFF = M_OFF + (MT ? MT_SLOTS * MT_SLOT : SV * M_BYTES);
+  static constexpr int FV = lcm_int(SV, DG);
+  static constexpr int LB = MS == 1 && SB % 2 ? 2 * SB : SB, LA = MS == 1 && SA % 2 ? 2 * SA : SA;
+  static constexpr int RD = lcm_int(2 * SA, DG);
+  // fullv, vfree, fullb, afull, done, accum, mfull, mfree
+  static constexpr int N_BARS = FV + SV + LB + LA + RD + 1 + 2 * MT_SLOTS;
+  static constexpr int SLOT_OFF = BAR_OFF + N_BARS * 8;
+  static constexpr int SMEM = SLOT_OFF + 16 + 1024;  // room to align the base to 1024
+  static constexpr uint32_t TMEM_COLS = tmem_cols_for(MS == 1 ? 2 * BN : BN);
+  static_assert(RD > SB, "a done barrier's next phase waits for the token producer");
+  static_assert(MS == 1 ? NB == 1 && 2 * BN <= 512 : NB == 2, "what two issuers share");
+  static_assert(NMMA % 16 == 0 && NMMA >= 16 && NMMA <= 256, "tcgen05 M=128 needs N in 16..256");
+  static_assert(BN <= 512 && B_OFF % 1024 == 0 && (NMMA * ROW_BYTES) % 1024 == 0, "swizzled tiles 1024-aligned");
+  static_assert(SMEM <= 232448, "a block's shared memory");
+  static_assert(DW % DG == 0 && DG <= MW, "every densify group reads every mask box, in order");
+};
+
+// All threads of the cluster; those that have left count as there.
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// A shared-memory address of this block in block `rank` of the cluster.
+__device__ __forceinline__ uint32_t remote_smem(uint32_t at, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(at), "r"(rank));
+  return r;
+}
+
+// n <= N outputs of a lane, ldy apart: residual + scale * x.
+template <int N>
+__device__ __forceinline__ void store_outputs(const Epilogue& e, const float (&x)[N], int n, int64_t t0, int64_t o,
+                                              __half* Y, int64_t ldy) {
+  __half* y = Y + t0 * ldy + o;
+  if (e.residual) {
+    const __half* res = e.residual + t0 * e.ldres + o;
+#pragma unroll
+    for (int i0 = 0; i0 < N; i0 += 16) {
+      __half h[16];  // on their way at a time
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (i0 + i < n) {
+          h[i] = *res;
+          res += e.ldres;
+        }
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (i0 + i < n) {
+          *y = __float2half_rn(fmaf(e.scale, x[i0 + i], __half2float(h[i])));
+          y += ldy;
+        }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < n) {
+        *y = __float2half_rn(e.scale * x[i]);
+        y += ldy;
+      }
+  }
+}
+
+// The epilogue of nm_linear for n <= 32 tokens (from t0) of the row held by each lane
+// of a warp.  Gated: lanes 2i and 2i + 1 hold a gate row and its up row; they trade
+// halves, so that the even lane finishes the first 16 tokens and the odd lane the last
+// 16, each token's outputs of a warp lying side by side.
+__device__ __forceinline__ void linear_store_32(const Epilogue& e, const uint32_t (&v)[32], bool row_ok,
+                                                int64_t r, int64_t t0, int n, __half* Y,
+                                                int64_t ldy, int lane) {
+  const float b = row_ok ? bias_at(e, r) : 0.f;
+  if (e.gated) {
+    const bool odd = lane & 1;
+    float g[16], u[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float lo = __uint_as_float(v[i]) + b, hi = __uint_as_float(v[16 + i]) + b;
+      const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? lo : hi, 1);
+      g[i] = odd ? other : lo;
+      u[i] = odd ? hi : other;
+    }
+    activate_fast(g, e.act);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) g[i] *= u[i];
+    store_outputs<16>(e, g, row_ok ? n - (odd ? 16 : 0) : 0, t0 + (odd ? 16 : 0), r >> 1, Y, ldy);
+  } else {
+    float x[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(v[i]) + b;
+    activate_fast(x, e.act);
+    store_outputs<32>(e, x, row_ok ? n : 0, t0, r, Y, ldy);
+  }
+}
+
+template <int NMMA, int NB, int SA, int SB, int SV, int DG, int MS, bool MT>
+__global__ void __launch_bounds__(threads_for(DW), 1)
+    linear_tc_kernel(const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_x,
+                     const __grid_constant__ CUtensorMap tm_m, const uint32_t* __restrict__ masks, __half* Y,
+                     int64_t rows, int words, int wslice, int64_t T, int64_t ldy, uint64_t wait_limit_ns,
+                     const Epilogue e, int nmma) {
+  using L = Shape<NMMA, NB, SA, SB, SV, DG, MS, MT>;
+  constexpr int WPG = DW / DG;  // warps per densify group
+  constexpr int RPW = BM / WPG;  // rows per warp and stage
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  const uint32_t sA = base + L::A_OFF, sB = base + L::B_OFF, sV = base + L::V_OFF, sM = base + L::M_OFF,
+                 bars = base + L::BAR_OFF, slot = base + L::SLOT_OFF;
+  auto fullv = [&](int kt) { return bars + 8u * (kt % L::FV); };
+  auto vfree = [&](int kt) { return bars + 8u * (L::FV + kt % SV); };
+  auto fullb = [&](int kt) { return bars + 8u * (L::FV + SV + kt % L::LB); };
+  auto afull = [&](int kt) { return bars + 8u * (L::FV + SV + L::LB + kt % L::LA); };
+  auto done = [&](int kt) { return bars + 8u * (L::FV + SV + L::LB + L::LA + kt % L::RD); };
+  constexpr int kAccum = L::FV + SV + L::LB + L::LA + L::RD;
+  const uint32_t accum = bars + 8u * kAccum;
+  auto mfull = [&](int s) { return bars + 8u * (kAccum + 1 + s); };
+  auto mfree = [&](int s) { return bars + 8u * (kAccum + 1 + L::MT_SLOTS + s); };
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_launch_dependents();
+  // After a wait gave up (this launch or an earlier one not yet reset), the block does
+  // nothing: the decision is block-uniform, taken before any barrier, copy or
+  // tensor-memory allocation.  (A cluster's blocks write each other's shared memory, so
+  // none of them leaves before the others: their waits give up at once instead.)
+  if (gridDim.z == 1 && __syncthreads_or(threadIdx.x == 0 && wait_aborted())) return;
+  const int64_t r0 = (int64_t)blockIdx.y * BM;
+  const int64_t n0 = (int64_t)blockIdx.x * (NB * nmma);
+  // K split: this block multiplies the mask words w0 .. w0 + nk - 1 (stage kt is word
+  // w0 + kt); w0 is a multiple of MW, so mask boxes stay aligned.
+  const int w0 = (int)blockIdx.z * wslice;
+  const int nk = min(words - w0, wslice);
+
+  if (warp == 0 && lane == 0) {
+    for (int k = 0; k < L::FV; ++k) mbar_init(fullv(k), MT ? 1 : 1 + 32);  // (+ 32 cp.async arrivals)
+    for (int k = 0; k < SV; ++k) mbar_init(vfree(k), WPG);                 // one arrival per warp of the group
+    for (int k = 0; k < L::LB; ++k) mbar_init(fullb(k), 1);
+    for (int k = 0; k < L::LA; ++k) mbar_init(afull(k), WPG);
+    for (int k = 0; k < L::RD; ++k) mbar_init(done(k), MS == 2 ? 2 : 1);  // tcgen05.commit
+    mbar_init(accum, 2);                                                  // final commit of each issuer
+    for (int m = 0; m < L::MT_SLOTS; ++m) {
+      mbar_init(mfull(m), 1);
+      mbar_init(mfree(m), DW);
+    }
+    fence_mbar_init();
+    prefetch_tmap(&tm_v);
+    prefetch_tmap(&tm_x);
+    if (MT) prefetch_tmap(&tm_m);
+  }
+  if (warp == 1) {
+    tmem_alloc(slot, L::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  uint32_t tmem_base;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem_base) : "r"(slot) : "memory");
+  pdl_wait_previous();  // (everything above touches no argument's memory)
+
+  // Before it ends, a producer waits (bounded) for its copies among a ring's last: shared
+  // memory must not be given up, or written by the cluster, under copies in flight.  Each
+  // is the last use of its slot, whose use before it waited for.
+  bool fine = false;  // (densify warps) the accumulator is whole
+  if (warp == 0) {
+    // ---- token tiles ---------------------------------------------------------
+    if (lane == 0) {
+      int last = -1;
+      for (int kt = 0; kt < nk; ++kt) {
+        if (kt >= SB && !mbar_wait(done(kt - SB), ((kt - SB) / L::RD) & 1, wait_limit_ns)) break;
+        mbar_arrive_expect_tx(fullb(kt), NB * nmma * ROW_BYTES);
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+          tma_load_2d(sB + kt % SB * L::B_BYTES + j * NMMA * ROW_BYTES, &tm_x, (w0 + kt) * BK,
+                      (int)(n0 + j * nmma), fullb(kt));
+        last = kt;
+      }
+      for (int kt = last; kt >= 0 && kt > last - SB; --kt)
+        mbar_wait(fullb(kt), (kt / L::LB) & 1, wait_limit_ns, false);
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ---- compact values (and, without MT, mask words) --------------------------
+    if (!MT || lane == 0) {
+      int last = -1;
+      for (int kt = 0; kt < nk; ++kt) {
+        int ok = 1;
+        if (kt >= SV && lane == 0) ok = mbar_wait(vfree(kt), (kt / SV - 1) & 1, wait_limit_ns);
+        if (!MT) ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(fullv(kt), V_BYTES);
+          tma_load_2d(sV + kt % SV * V_BYTES, &tm_v, (w0 + kt) * 16, (int)r0, fullv(kt));
+        }
+        if (!MT) {
+#pragma unroll
+          for (int i = 0; i < BM / 32; ++i) {
+            const int rr = lane + 32 * i;
+            const int64_t gr = r0 + rr;
+            const bool in = gr < rows;
+            cp_async_4(sM + kt % SV * M_BYTES + 4u * rr, masks + (in ? gr : 0) * words + w0 + kt, in ? 4u : 0u);
+          }
+          cp_async_arrive_noinc(fullv(kt));
+        }
+        last = kt;
+      }
+      if (!MT) cp_async_wait_all();
+      if (lane == 0)
+        for (int kt = last; kt >= 0 && kt > last - SV; --kt)
+          mbar_wait(fullv(kt), (kt / L::FV) & 1, wait_limit_ns, false);
+    }
+    __syncwarp();
+  } else if (warp == mask_warp(DW)) {
+    // ---- mask words (MT), a box of MW stages at a time ---------------------------
+    if (MT && lane == 0) {
+      int nbox = 0;
+      for (int kt = 0; kt < nk; kt += MW) {
+        const int b = kt / MW, ms = b % L::MT_SLOTS;
+        if (b >= L::MT_SLOTS && !mbar_wait(mfree(ms), (b / L::MT_SLOTS - 1) & 1, wait_limit_ns)) break;
+        mbar_arrive_expect_tx(mfull(ms), MT_SLOT);
+        tma_load_2d(sM + ms * MT_SLOT, &tm_m, w0 + kt, (int)r0, mfull(ms));
+        nbox = b + 1;
+      }
+      for (int b = nbox > L::MT_SLOTS ? nbox - L::MT_SLOTS : 0; b < nbox; ++b)
+        mbar_wait(mfull(b % L::MT_SLOTS), (b / L::MT_SLOTS) & 1, wait_limit_ns, false);
+    }
+    __syncwarp();
+  } else if (warp == 1 || warp == mma2_warp(DW)) {
+    // ---- MMAs ----------------------------------------------------------------------
+    // The issuing threads share their schedulers with the densify warps, which keep those
+    // two thirds busy: every instruction of a stage costs them several cycles, a barrier
+    // test 100 to 200 and an MMA 80, so slots and phases are counted and not divided for,
+    // descriptors are sums of 32 bits, and there are two such threads.
+    const int role = warp == 1 ? 0 : 1;
+    if (lane == 0) {
+      const uint32_t idesc = idesc_f16_f32(BM, nmma);
+      const uint64_t a0 = smem_desc_sw64(sA), b0 = smem_desc_sw64(sB + (MS == 2 ? role * NMMA * ROW_BYTES : 0));
+      const uint32_t a_high = (uint32_t)(a0 >> 32), b_high = (uint32_t)(b0 >> 32);
+      const uint32_t a_low = (uint32_t)a0, b_low = (uint32_t)b0;
+      auto desc = [](uint32_t high, uint32_t low) { return ((uint64_t)high << 32) | low; };
+      constexpr int kStep = MS == 1 ? 2 : 1;
+      const int k0 = MS == 1 ? role : 0;
+      const uint32_t dacc = tmem_base + (uint32_t)(role == 0 ? 0 : MS == 1 ? L::BN : NMMA);
+      int ia = k0, ib = k0, id = k0, la = k0, lb = k0;  // slots, and places in the barriers' rings
+      uint32_t pa = 0, pb = 0;                          // phases
+      auto next = [](int& i, int ring) {
+        i += kStep;
+        const bool around = i >= ring;
+        if (around) i -= ring;
+        return around ? 1u : 0u;
+      };
+      for (int kt = k0; kt < nk; kt += kStep) {
+        if (!mbar_wait(fullb(0) + 8u * lb, pb, wait_limit_ns)) break;
+        if (!mbar_wait(afull(0) + 8u * la, pa, wait_limit_ns)) break;
+        tc_fence_after_sync();
+        const uint32_t al = a_low + (uint32_t)ia * (A_BYTES / 16), bl = b_low + (uint32_t)ib * (L::B_BYTES / 16);
+#pragma unroll
+        for (int ks = 0; ks < BK / 16; ++ks)
+          mma_f16(dacc, desc(a_high, al + ks * 2), desc(b_high, bl + ks * 2), idesc, kt != k0 || ks != 0);
+        // Only where someone waits for it: a commit's arrival is not ordered with the
+        // accum commit's, so another could land after this block ended, in the barriers
+        // of the next block on the SM.
+        if (kt + (SA < SB ? SA : SB) < nk) mma_commit(done(0) + 8u * id);
+        next(ia, SA);
+        next(ib, SB);
+        next(id, L::RD);
+        pa ^= next(la, L::LA);
+        pb ^= next(lb, L::LB);
+      }
+      mma_commit(accum);  // also after an early exit: completes once issued MMAs finish
+    }
+    __syncwarp();
+  } else {
+    // ---- expansion of the weights ------------------------------------------------------
+    const int dw = warp - FIRST_DENSIFY_WARP, grp = dw / WPG, wg = dw % WPG;
+    bool ok = true;
+    int box = -1;  // mask box this warp last waited for
+    for (int kt = grp; kt < nk; kt += DG) {
+      bool got = mbar_wait(fullv(kt), (kt / L::FV) & 1, wait_limit_ns);
+      if (MT && kt / MW != box) {
+        // The box's slot is refilled only after every densify warp released it, so the
+        // phase this warp sees here is this box's.
+        box = kt / MW;
+        got = got && mbar_wait(mfull(box % L::MT_SLOTS), (box / L::MT_SLOTS) & 1, wait_limit_ns);
+      }
+      if (kt >= SA) got = got && mbar_wait(done(kt - SA), ((kt - SA) / L::RD) & 1, wait_limit_ns);
+      // The warp decides together, so no lane is left behind at a warp barrier.
+      if (!__all_sync(0xFFFFFFFFu, got)) {
+        ok = false;
+        break;
+      }
+      const uint32_t sMw = MT ? sM + box % L::MT_SLOTS * MT_SLOT + (kt % MW) * 4u : sM + kt % SV * M_BYTES;
+      densify_stage<RPW>(sA + kt % SA * A_BYTES, sV + kt % SV * V_BYTES, sMw, MT ? MW * 4u : 4u, wg, lane);
+      // Each lane orders its tile writes before the tensor core's reads; the warp barrier
+      // then lets one release-arrive publish all 32 lanes' writes and the end of their
+      // reads of the values and the masks.
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(afull(kt));
+        if (kt + SV < nk) mbar_arrive(vfree(kt));
+        if (MT && kt + DG >= MW * (kt / MW + 1)) mbar_arrive(mfree(box % L::MT_SLOTS));  // its last in the box
+      }
+    }
+    if (!mbar_wait(accum, 0, wait_limit_ns)) ok = false;
+    tc_fence_after_sync();
+    // tcgen05.ld is a warp-wide instruction: the whole warp reads or none does.
+    fine = __all_sync(0xFFFFFFFFu, ok);
+  }
+
+  // ---- epilogue --------------------------------------------------------------------------
+  // The accumulator's columns in pieces of 32 (an MMA's tokens may end inside one).  Under
+  // a K split the blocks of a row tile's slices are a cluster: piece i is finished by block
+  // i % slices, to which the others send theirs through distributed shared memory (their
+  // rings lie idle by now), and which adds them in slice order: nothing goes through memory,
+  // and there is no second launch.
+  const int slices = (int)gridDim.z, me = (int)blockIdx.z;
+  const int per = (nmma + 31) / 32, pieces = NB * per;
+  const int dw = warp - FIRST_DENSIFY_WARP, quad = warp & 3, qi = dw >> 2;
+  const bool mine = warp >= FIRST_DENSIFY_WARP && warp < FIRST_DENSIFY_WARP + DW && fine;
+  constexpr int QW = DW / 4;
+  const int64_t r = r0 + 32 * quad + lane;
+  const uint32_t tbase = tmem_base + ((uint32_t)(32 * quad) << 16);
+  auto column = [&](int i) { return i / per * NMMA + i % per * 32; };
+  auto sums = [&](int i, uint32_t (&v)[32]) {
+    tmem_ld_32(tbase + (uint32_t)column(i), v);
+    tmem_ld_wait();
+    if (MS == 1 && nk > 1) {  // the odd stages' accumulator (none when nk == 1)
+      uint32_t w[32];
+      tmem_ld_32(tbase + (uint32_t)(L::BN + column(i)), w);
+      tmem_ld_wait();
+#pragma unroll
+      for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) + __uint_as_float(w[k]));
+    }
+  };
+  // its first token, and how many it has
+  auto first = [&](int i) { return n0 + i / per * nmma + i % per * 32; };
+  auto count = [&](int i) { return (int)min((int64_t)min(nmma - i % per * 32, 32), T - first(i)); };
+  // Where block `from`'s piece i lies in the shared memory of the block that finishes it:
+  // [place among the others][its pieces][32 tokens][128 rows] fp32.
+  const int share = (pieces + slices - 1) / slices;
+  auto inbox = [&](int i, int from) {
+    const int to = i % slices, at = (from < to ? from : from - 1) * share + i / slices;
+    return base + (uint32_t)(at * (32 * BM * 4) + (32 * quad + lane) * 4);
+  };
+  if (slices > 1) {
+    cluster_sync();  // every block is done with its ring
+    if (mine) {
+#pragma unroll 1
+      for (int i = qi; i < pieces; i += QW) {
+        if (i % slices == me || count(i) <= 0) continue;
+        uint32_t v[32];
+        sums(i, v);
+        const uint32_t to = remote_smem(inbox(i, me), (uint32_t)(i % slices));
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+          asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to + k * (BM * 4)), "r"(v[k]) : "memory");
+      }
+    }
+    cluster_sync();
+  }
+  if (mine) {
+#pragma unroll 1
+    for (int i = me + qi * slices; i < pieces; i += QW * slices) {
+      const int n = count(i);
+      if (n <= 0) continue;
+      uint32_t v[32];
+      sums(i, v);
+      if (slices > 1) {
+        float acc[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) acc[k] = 0.f;
+        for (int z = 0; z < slices; ++z) {
+          if (z == me) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) acc[k] += __uint_as_float(v[k]);
+          } else {
+            const uint32_t from = inbox(i, z);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) acc[k] += lds_f32(from + k * (BM * 4));
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(acc[k]);
+      }
+      linear_store_32(e, v, r < rows, r, first(i), n, Y, ldy, lane);
+    }
+  }
+
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    // Tensor memory is freed only after the MMAs that write it have completed: one more
+    // bounded (not abortable) wait on the final commit, which a normal run passed already.
+    mbar_wait(accum, 0, wait_limit_ns, false);
+    tc_fence_after_sync();
+    tmem_dealloc(tmem_base, L::TMEM_COLS);
+  }
+}
+
+template <int NMMA, int NB, int SA, int SB, int SV, int DG, int MS, bool MT>
+cudaError_t launch_mt(const SpmmTcParams& p, cudaStream_t stream) {
+  using L = Shape<NMMA, NB, SA, SB, SV, DG, MS, MT>;
+  CUtensorMap tm_v, tm_x, tm_m;
+  memset(&tm_m, 0, sizeof(tm_m));
+  if (MT && !encode_2d(&tm_m, p.masks, (uint64_t)p.words, (uint64_t)p.rows, (uint64_t)p.words * 4, MW, BM,
+                       CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_DATA_TYPE_UINT32))
+    return cudaErrorInvalidValue;
+  if (!encode_2d(&tm_v, p.values, (uint64_t)p.words * 16, (uint64_t)p.rows, (uint64_t)p.words * 32, 16, BM,
+                 CU_TENSOR_MAP_SWIZZLE_NONE) ||
+      !encode_2d(&tm_x, p.X, (uint64_t)p.words * 32, (uint64_t)p.T, (uint64_t)p.ldx * 2, BK, p.tile,
+                 CU_TENSOR_MAP_SWIZZLE_64B))
+    return cudaErrorInvalidValue;
+  if (p.slices > 1) {  // what a block is sent fits its rings
+    const int pieces = NB * ((p.tile + 31) / 32), share = (pieces + p.slices - 1) / p.slices;
+    if ((p.slices - 1) * share * 32 * BM * 4 > L::M_OFF) return cudaErrorInvalidValue;
+  }
+  auto* k = linear_tc_kernel<NMMA, NB, SA, SB, SV, DG, MS, MT>;
+  static int done[64] = {0};
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev >= 64 || !__atomic_load_n(&done[dev], __ATOMIC_ACQUIRE)) {
+    err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
+    if (err != cudaSuccess) return err;
+    if (dev < 64) __atomic_store_n(&done[dev], 1, __ATOMIC_RELEASE);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((p.T + NB * p.tile - 1) / (NB * p.tile)), (unsigned)((p.rows + BM - 1) / BM),
+                     (unsigned)p.slices);
+  cfg.blockDim = dim3(threads_for(DW));
+  cfg.dynamicSmemBytes = L::SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = (unsigned)p.slices;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.slices > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, k, tm_v, tm_x, tm_m, p.masks, p.Y, p.rows, p.words,
+                            p.slices > 1 ? p.wslice : p.words, p.T, p.ldy, (uint64_t)kWaitLimitNs, p.epi, p.tile);
+}
+
+// Mask words by TMA when the mask array allows it (16-byte aligned, row pitch words * 4 a
+// multiple of 16: every decoder shape), else by cp.async.
+template <int NMMA, int NB, int SA, int SB, int SV, int DG, int MS>
+cudaError_t launch(const SpmmTcParams& p, cudaStream_t stream) {
+  const bool mt = p.words % 4 == 0 && (reinterpret_cast<uintptr_t>(p.masks) & 15) == 0;
+  return mt ? launch_mt<NMMA, NB, SA, SB, SV, DG, MS, true>(p, stream)
+            : launch_mt<NMMA, NB, SA, SB, SV, DG, MS, false>(p, stream);
+}
+
+}  // namespace
+}  // namespace tc
+
+// variant: kCands' index
+cudaError_t launch_spmm_tc_linear(const SpmmTcParams& p, int variant, cudaStream_t stream) {
+  switch (variant) {
+    case 0: return tc::launch<256, 2, 4, 4, 12, 4, 2>(p, stream);
+    case 1: return tc::launch<256, 1, 6, 6, 16, 4, 1>(p, stream);
+    case 2: return tc::launch<128, 1, 8, 8, 20, 4, 1>(p, stream);
+    case 3: return tc::launch<64, 1, 8, 10, 24, 4, 1>(p, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+namespace {
+
+// (variant, MMAs a block, tokens of an MMA at most, ns a stage: base, and by token beyond
+// `flat`).  Measured with 152 row tiles of 8192 columns, one block an SM, at 16 tokens
+// an MMA up to the most: 322 .. 380 ns, 267 .. 288, 262, 266; up to there the expansion of
+// the weights bounds a stage, and beyond the MMAs.
+struct Cand {
+  int variant, mmas, most;
+  double ns, by_token;
+  int flat;
+};
+constexpr Cand kCands[] = {{0, 2, 256, 324.0, 0.2, 288}, {1, 1, 256, 267.0, 0.19, 144},
+                           {2, 1, 128, 262.0, 0.0, 0}, {3, 1, 64, 265.0, 0.0, 0}};
+constexpr double kFixedNs = 4000.0;   // prologue, pipeline fill, teardown
+constexpr double kTokenNs = 10.5;     // the epilogue, a token of the tile
+constexpr double kClusterNs = 2500.0; // the slices' exchange, and
+constexpr double kSentNs = 4.0;       // what a token's share of it takes
+constexpr int kMaxSlices = 8, kMaxSent = 13;  // pieces of 16 KB that a block's rings can take
+
+}  // namespace
+
+// The least time by a model: waves of blocks x (a slice's stages + fixed costs).  Tokens
+// are spread evenly over the blocks that a variant's full tiles would need, and over a
+// block's MMAs, in multiples of 16 (300 tokens: two MMAs of 160 for two of 256).
+LinearTcPlan linear_tc_plan(int64_t rows, int words, int64_t tokens, int sms) {
+  LinearTcPlan best{3, 1, 64};
+  double least = 0.0;
+  for (const Cand& c : kCands) {
+    const int64_t full = (int64_t)c.most * c.mmas, blocks = (tokens + full - 1) / full;
+    const int64_t each = (tokens + blocks - 1) / blocks;
+    const int tile = (int)(((each + c.mmas - 1) / c.mmas + 15) / 16 * 16);
+    const int64_t tiles = (rows + 127) / 128 * ((tokens + tile * c.mmas - 1) / (tile * c.mmas));
+    const int all = tile * c.mmas, pieces = c.mmas * ((tile + 31) / 32);
+    const double stage = c.ns + c.by_token * (all > c.flat ? all - c.flat : 0);
+    for (int z = 1; z <= kMaxSlices; ++z) {
+      if (z > 1 && (spmm_tc_slices(words, z) != z || (z - 1) * ((pieces + z - 1) / z) > kMaxSent)) continue;
+      // clusters of z blocks fill the SMs by groups of 16, and leave the rest of a group empty
+      const int64_t at_once = z == 1 ? sms : (int64_t)sms / 16 * (16 / z) * z + sms % 16 / z * z;
+      const int64_t waves = (tiles * z + at_once - 1) / at_once;
+      const double exchange = z > 1 ? kClusterNs + kSentNs * all : 0.0;
+      const double t = waves * (spmm_tc_slice_words(words, z) * stage + kFixedNs + kTokenNs * all / z + exchange);
+      if (least == 0.0 || t < least * 0.98) {
+        least = t;
+        best = {c.variant, z, tile};
+      }
+    }
+  }
+  return best;
+}
+
+// ---- nm_linear for 2 .. 8 tokens, whose columns are split when the rows are few: the
+// partial sums that nm_spmm's kernel leaves are added and finished here.  V rows a thread
+// (an even number of them where rows come in pairs): V = 4 takes 16-byte loads of the
+// partial sums, which need rows % 4 == 0; V = 2 serves any even number of rows, V = 1 the
+// rest.
+template <int V>
+__global__ void __launch_bounds__(256) linear_combine_kernel(const float* __restrict__ part,
+                                                             int slices, int64_t tokens,
+                                                             int64_t rows, const Epilogue e,
+                                                             __half* Y, int64_t ldy) {
+  pdl_launch_dependents();
+  pdl_wait_previous();
+  const int64_t plane = tokens * rows;
+  for (int64_t t = blockIdx.y; t < tokens; t += gridDim.y) {
+    for (int64_t r = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * V; r < rows;
+         r += (int64_t)gridDim.x * blockDim.x * V) {
+      const float* q = part + t * rows + r;
+      float s[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) s[i] = 0.f;
+#pragma unroll 4
+      for (int z = 0; z < slices; ++z) {
+        if constexpr (V == 4) {
+          const float4 a = *reinterpret_cast<const float4*>(q + z * plane);
+          s[0] += a.x; s[1] += a.y; s[2] += a.z; s[3] += a.w;
+        } else {
+#pragma unroll
+          for (int i = 0; i < V; ++i) s[i] += q[z * plane + i];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) s[i] += bias_at(e, r + i);
+      if (V > 1 && e.gated) {
+#pragma unroll
+        for (int i = 0; i + 1 < V; i += 2) {
+          const int64_t o = (r + i) / 2;
+          Y[t * ldy + o] = __float2half_rn(fmaf(e.scale, activate(s[i], e.act) * s[i + 1], residual_at(e, t, o)));
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          Y[t * ldy + r + i] = __float2half_rn(fmaf(e.scale, activate(s[i], e.act), residual_at(e, t, r + i)));
+      }
+    }
+  }
+}
+
+cudaError_t launch_linear_combine(const float* part, int slices, int64_t tokens, int64_t rows,
+                                  const Epilogue& epi, __half* Y, int64_t ldy, int sms,
+                                  cudaStream_t stream) {
+  const int v = rows % 4 == 0 ? 4 : rows % 2 == 0 ? 2 : 1;
+  const int64_t bx = (rows + 256 * v - 1) / (256 * v);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(bx < 65535 ? bx : 65535), (unsigned)(tokens < 65535 ? tokens : 65535));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  auto* k = v == 4 ? linear_combine_kernel<4> : v == 2 ? linear_combine_kernel<2> : linear_combine_kernel<1>;
+  return cudaLaunchKernelEx(&cfg, k, part, slices, tokens, rows, epi, Y, ldy);
+}
+
+cudaError_t read_linear_wait_timeouts(unsigned long long* count, int reset) {
+  return read_local_wait_timeouts(count, reset);
+}
+
+}  // namespace nmk

@@ -10,7 +10,7 @@ namespace nmk {
 
 // Number of mbarrier waits that gave up (see mbar_wait); read and reset by
 // nm_wait_timeouts().  Zero in every correct run.  Each translation unit that
-// includes this header (prefill.cu, attend_wide_*.cu, verify.cu) has a counter and
+// includes this header (prefill.cu, linear_tc.cu, attend_wide_*.cu, verify.cu) has a counter and
 // a flag of its own; nm_wait_timeouts adds the counters and clears the flags.
 static __device__ unsigned long long g_wait_timeouts = 0;
 
