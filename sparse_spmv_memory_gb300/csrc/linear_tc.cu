@@ -12,8 +12,13 @@
 //    values 4).  One ring of all three has as many stages as token tiles fit, 5 at 512
 //    tokens, and a stage then takes a fifth of the way from an empty slot through the
 //    loads, the expansion and the MMAs: 441 ns at 512 tokens, and still 375 at 32, with the
-//    tensor pipe 53 % busy.  Twelve slots of values, which come from HBM, and four each of
-//    the others take 380 ns at 512 tokens (the MMAs alone 332) and 322 at 32.
+//    tensor pipe 53 % busy.  With twelve stages of values, which come from HBM, and the
+//    others' rings as long as fits it is 355 and 322.
+//  * Few instructions of the threads that feed the rest.  A copy costs its thread 200
+//    cycles and more, a wait 100, an MMA 45 and a commit 55, beside densify warps that keep
+//    the schedulers half busy.  So values and masks come four stages at a time, two warps
+//    load token tiles, and tokens and weights of a stage share a barrier; with the cheaper
+//    expansion of expand_32 320 tokens take 285 ns a stage for 330, 128 take 211 for 262.
 //  * An MMA has as many tokens as there are (a multiple of 16), not a full tile's.
 //  * A K split's blocks are a cluster and trade their sums through distributed shared
 //    memory (see the epilogue): no workspace, no second launch.
@@ -25,58 +30,134 @@
 #include <stdint.h>
 #include <string.h>
 
-#include "densify.cuh"
+#include <type_traits>
+
 #include "device.cuh"
 #include "epilogue.cuh"
 #include "kernels.h"
 #include "tc.cuh"
+#include "tc_tiles.cuh"
 
 namespace nmk {
 namespace tc {
 namespace {
 
 constexpr int DW = 16;  // densify warps
+__host__ __device__ constexpr int tokens2_warp(int dw) { return mask_warp(dw); }  // the second producer of token tiles
 constexpr int lcm_int(int a, int b) { return a / gcd_int(a, b) * b; }
 
-// NMMA: tokens of an MMA at most; NB MMAs a block and K step; SA, SB, SV: slots of
-// expanded weights, token tiles and compact values; DG densify groups, which take the
-// stages in turn.  Two threads issue MMAs: MS 1, the even and the odd stages into two
-// accumulators; MS 2, the two MMAs of every K step.  MT: masks come by TMA, MW stages a box
-// (the mask array is 16-byte aligned with rows of whole boxes), else by cp.async.
+// NMMA: tokens of an MMA at most; NB MMAs a block and K step; S: slots of expanded weights
+// and token tiles, a stage each; SV: slots of compact values and mask words, MW stages (a
+// box) each; DG densify groups, which take the stages in turn.  Two threads issue
+// MMAs: MS 1, the even and the odd stages into two accumulators; MS 2, the two MMAs of
+// every K step.  MT: masks come by TMA (the mask array is 16-byte aligned with rows of
+// whole boxes), else by cp.async.
 //
 // Barriers.  A parity wait tells a phase from the one before it only, so it is exact
 // only if the waiter saw the barrier's phase before, or the barrier cannot have gone a
-// phase further.  fullv (values there): a ring of lcm(SV, DG), so that all phases of one
-// belong to one group.  fullb (tokens there) and afull (weights expanded): rings of an
-// even number of slots where two issuers take turns.  done (MMAs complete), by stage: the
-// token producer waits for all of them in order; the densify warps of stage kt wait for
-// stage kt - SA, and RD being a multiple of 2 SA, the stage that would complete the same
-// barrier's next phase needs the slot that they are about to fill.
-template <int NMMA, int NB, int SA, int SB, int SV, int DG, int MS, bool MT>
+// phase further.  fullv, vfree (a box there, and used up): every densify warp has a stage
+// in every box.  ready (tokens there and weights expanded; one barrier for one wait of the
+// issuers): a ring of an even number of slots, which the producers and issuers of even and
+// odd stages share out.  done (MMAs complete), by stage: a token producer waits for all of
+// its stages in order; the densify warps of stage kt wait for stage kt - S, and RD being a
+// multiple of 2 S, the stage that would complete the same barrier's next phase needs the
+// slot that they are about to fill.
+template <int NMMA, int NB, int S, int SV, int DG, int MS, bool MT>
 struct Shape {
   static constexpr int BN = NMMA * NB;
   static constexpr int B_BYTES = BN * ROW_BYTES;
+  static constexpr int V_SLOT = BM * MW * 32;  // rows of 128 bytes, swizzled
   static constexpr int A_OFF = 0;
-  static constexpr int B_OFF = A_OFF + SA * A_BYTES;
-  static constexpr int V_OFF = B_OFF + SB * B_BYTES;
-  static constexpr int M_OFF = V_OFF + SV * V_BYTES;
-  static constexpr int MT_SLOTS = 3;  // the groups' stages may lie in two boxes; one on its way
-  static constexpr int BAR_OFF = M_OFF + (MT ? MT_SLOTS * MT_SLOT : SV * M_BYTES);
-  static constexpr int FV = lcm_int(SV, DG);
-  static constexpr int LB = MS == 1 && SB % 2 ? 2 * SB : SB, LA = MS == 1 && SA % 2 ? 2 * SA : SA;
-  static constexpr int RD = lcm_int(2 * SA, DG);
-  // fullv, vfree, fullb, afull, done, accum, mfull, mfree
-  static constexpr int N_BARS = FV + SV + LB + LA + RD + 1 + 2 * MT_SLOTS;
+  static constexpr int B_OFF = A_OFF + S * A_BYTES;
+  static constexpr int V_OFF = B_OFF + S * B_BYTES;
+  static constexpr int M_OFF = V_OFF + SV * V_SLOT;
+  static constexpr int BAR_OFF = M_OFF + SV * MT_SLOT;
+  static constexpr int RD = lcm_int(2 * S, DG);
+  static constexpr int N_BARS = 2 * SV + S + RD + 1;  // fullv, vfree, ready, done, accum
   static constexpr int SLOT_OFF = BAR_OFF + N_BARS * 8;
   static constexpr int SMEM = SLOT_OFF + 16 + 1024;  // room to align the base to 1024
   static constexpr uint32_t TMEM_COLS = tmem_cols_for(MS == 1 ? 2 * BN : BN);
-  static_assert(RD > SB, "a done barrier's next phase waits for the token producer");
+  static_assert(S % 2 == 0, "even and odd stages have slots of their own");
   static_assert(MS == 1 ? NB == 1 && 2 * BN <= 512 : NB == 2, "what two issuers share");
   static_assert(NMMA % 16 == 0 && NMMA >= 16 && NMMA <= 256, "tcgen05 M=128 needs N in 16..256");
-  static_assert(BN <= 512 && B_OFF % 1024 == 0 && (NMMA * ROW_BYTES) % 1024 == 0, "swizzled tiles 1024-aligned");
+  static_assert(BN <= 512 && B_OFF % 1024 == 0 && (NMMA * ROW_BYTES) % 1024 == 0 && V_OFF % 1024 == 0,
+                "swizzled tiles 1024-aligned");
   static_assert(SMEM <= 232448, "a block's shared memory");
-  static_assert(DW % DG == 0 && DG <= MW, "every densify group reads every mask box, in order");
+  static_assert(DW % DG == 0 && DG <= MW, "every densify group has a stage in every box");
 };
+
+// Expands 32 rows of a stage, which is word j of its box: sV rows of 128 bytes, their
+// 16-byte chunks at place ^ (row & 7), sM rows of MW mask words, to the stage's swizzled
+// tile at sA (chunk ^= (row >> 1) & 3).
+//
+// Where every byte of the mask words keeps 4 columns (1:2, 2:4, 4:8), which the warp sees
+// for itself (bytes: so far), a byte's values are 8 aligned bytes of the compact row, and a
+// lane takes a byte, four lanes a row: the nibble's bits spread to the bytes of a word, bit
+// i the byte i, times 0x01010100 are the ranks of its columns in it (byte i: how many kept
+// ones lie below), times 0x22 plus 0x10 the prmt selector of that value's two bytes; columns
+// that are not kept become 0 by a mask.  Else a lane takes a nibble, as two column pairs:
+// the rank of a pair's first column, a popcount, finds its values, which one prmt by the
+// pair's mask bits places.  That is twice the instructions: 270 ns a stage for 212 at 128
+// tokens, 300 for 285 at 320.
+__device__ __forceinline__ void expand_32(uint32_t sA, uint32_t sV, uint32_t sM, int j, int row0, int lane,
+                                          bool& bytes) {
+  if (bytes) {
+    const uint32_t m = lds_u32(sM + (uint32_t)(row0 + lane) * (MW * 4u) + 4u * j);
+    uint32_t c = m - ((m >> 1) & 0x55555555u);
+    c = (c & 0x33333333u) + ((c >> 2) & 0x33333333u);
+    c = (c + (c >> 4)) & 0x0F0F0F0Fu;
+    bytes = __all_sync(0xFFFFFFFFu, c == 0x04040404u || m == 0u);  // (0: rows behind the last)
+  }
+  if (bytes) {
+    const uint32_t h = lane >> 2, p = lane & 3, r = (uint32_t)row0 + h;  // rows r + 8 i: r & 7 = h
+    const uint32_t from = sV + 128u * r + (((2u * j + (p >> 1)) ^ h) << 4) + 8u * (p & 1);
+    const uint32_t byte = sM + r * (MW * 4u) + 4u * j + p, to = sA + r * ROW_BYTES + ((p ^ (h >> 1)) << 4);
+    uint32_t b[4], v01[4], v23[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      b[i] = lds_u8_32(byte + 8u * MW * 4u * i);
+      lds_u64(from + 8u * 128u * i, v01[i], v23[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t lo = ((b[i] & 15u) * 0x00204081u) & 0x01010101u, hi = ((b[i] >> 4) * 0x00204081u) & 0x01010101u;
+      const uint32_t s0 = lo * 0x22222200u + 0x10101010u;
+      const uint32_t s1 = hi * 0x22222200u + (__popc(b[i] & 15u) * 0x22222222u + 0x10101010u);
+      const uint32_t k0 = lo * 0xFFu, k1 = hi * 0xFFu;
+      sts_u128(to + 8u * ROW_BYTES * i, prmt(v01[i], v23[i], s0) & prmt(k0, 0u, 0x1100u),
+               prmt(v01[i], v23[i], s0 >> 16) & prmt(k0, 0u, 0x3322u),
+               prmt(v01[i], v23[i], s1) & prmt(k1, 0u, 0x1100u),
+               prmt(v01[i], v23[i], s1 >> 16) & prmt(k1, 0u, 0x3322u));
+    }
+    return;
+  }
+  // (the rank after a row's last value is never selected; it reads the next row or the one before)
+  const uint32_t h = lane >> 3, p = lane & 7, b0 = 4u * p, below = (1u << b0) - 1u, r = (uint32_t)row0 + h;
+  const uint32_t stage = 32u * j;
+  // selectors by q (bit 0: the pair's first column kept, bit 1: the second) for the values v
+  // (rank c) and w (rank c + 1): 0x3232 (0, 0), 0x3210 (v, 0), 0x1032 (0, v), 0x5410 (v, w)
+  constexpr uint32_t kSelLo = 0x32103232u, kSelHi = 0x54101032u;
+  uint32_t nib[8], v[8][4];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) nib[i] = lds_u32(sM + (r + 4u * i) * (MW * 4u) + 4u * j);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {  // rows r + 4 i: row & 7 = h + 4 (i & 1)
+    const uint32_t at = (sV + 128u * r) | ((h + 4u * (i & 1)) << 4), more = 4u * 128u * i;
+    const uint32_t first = stage + 2u * __popc(nib[i] & below);
+    nib[i] = (nib[i] >> b0) & 15u;
+    const uint32_t second = first + 2u * __popc(nib[i] & 3u);
+    v[i][0] = lds_u16_32((first ^ at) + more);
+    v[i][1] = lds_u16_32(((first + 2u) ^ at) + more);
+    v[i][2] = lds_u16_32((second ^ at) + more);
+    v[i][3] = lds_u16_32(((second + 2u) ^ at) + more);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {  // (row >> 1) & 3 = (h >> 1) ^ (2 (i & 1))
+    const uint32_t lo = prmt(v[i][0], v[i][1], prmt(kSelLo, kSelHi, (nib[i] & 3u) * 0x22u + 0x10u));
+    const uint32_t hi = prmt(v[i][2], v[i][3], prmt(kSelLo, kSelHi, (nib[i] >> 2) * 0x22u + 0x10u));
+    sts_u64(sA + (r + 4u * i) * ROW_BYTES + (((p >> 1) ^ (h >> 1) ^ (2u * (i & 1))) << 4) + 8u * (p & 1), lo, hi);
+  }
+}
 
 // All threads of the cluster; those that have left count as there.
 __device__ __forceinline__ void cluster_sync() {
@@ -156,29 +237,26 @@ __device__ __forceinline__ void linear_store_32(const Epilogue& e, const uint32_
   }
 }
 
-template <int NMMA, int NB, int SA, int SB, int SV, int DG, int MS, bool MT>
+template <int NMMA, int NB, int S, int SV, int DG, int MS, bool MT>
 __global__ void __launch_bounds__(threads_for(DW), 1)
     linear_tc_kernel(const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_x,
                      const __grid_constant__ CUtensorMap tm_m, const uint32_t* __restrict__ masks, __half* Y,
                      int64_t rows, int words, int wslice, int64_t T, int64_t ldy, uint64_t wait_limit_ns,
                      const Epilogue e, int nmma) {
-  using L = Shape<NMMA, NB, SA, SB, SV, DG, MS, MT>;
+  using L = Shape<NMMA, NB, S, SV, DG, MS, MT>;
   constexpr int WPG = DW / DG;  // warps per densify group
   constexpr int RPW = BM / WPG;  // rows per warp and stage
+  static_assert(RPW % 32 == 0, "expand_32");
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   const uint32_t sA = base + L::A_OFF, sB = base + L::B_OFF, sV = base + L::V_OFF, sM = base + L::M_OFF,
                  bars = base + L::BAR_OFF, slot = base + L::SLOT_OFF;
-  auto fullv = [&](int kt) { return bars + 8u * (kt % L::FV); };
-  auto vfree = [&](int kt) { return bars + 8u * (L::FV + kt % SV); };
-  auto fullb = [&](int kt) { return bars + 8u * (L::FV + SV + kt % L::LB); };
-  auto afull = [&](int kt) { return bars + 8u * (L::FV + SV + L::LB + kt % L::LA); };
-  auto done = [&](int kt) { return bars + 8u * (L::FV + SV + L::LB + L::LA + kt % L::RD); };
-  constexpr int kAccum = L::FV + SV + L::LB + L::LA + L::RD;
-  const uint32_t accum = bars + 8u * kAccum;
-  auto mfull = [&](int s) { return bars + 8u * (kAccum + 1 + s); };
-  auto mfree = [&](int s) { return bars + 8u * (kAccum + 1 + L::MT_SLOTS + s); };
+  auto fullv = [&](int box) { return bars + 8u * (box % SV); };
+  auto vfree = [&](int box) { return bars + 8u * (SV + box % SV); };
+  auto ready = [&](int kt) { return bars + 8u * (2 * SV + kt % S); };
+  auto done = [&](int kt) { return bars + 8u * (2 * SV + S + kt % L::RD); };
+  const uint32_t accum = bars + 8u * (2 * SV + S + L::RD);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_launch_dependents();
@@ -195,16 +273,13 @@ __global__ void __launch_bounds__(threads_for(DW), 1)
   const int nk = min(words - w0, wslice);
 
   if (warp == 0 && lane == 0) {
-    for (int k = 0; k < L::FV; ++k) mbar_init(fullv(k), MT ? 1 : 1 + 32);  // (+ 32 cp.async arrivals)
-    for (int k = 0; k < SV; ++k) mbar_init(vfree(k), WPG);                 // one arrival per warp of the group
-    for (int k = 0; k < L::LB; ++k) mbar_init(fullb(k), 1);
-    for (int k = 0; k < L::LA; ++k) mbar_init(afull(k), WPG);
+    for (int k = 0; k < SV; ++k) {
+      mbar_init(fullv(k), MT ? 1 : 1 + 32);  // (+ 32 cp.async arrivals)
+      mbar_init(vfree(k), DW);
+    }
+    for (int k = 0; k < S; ++k) mbar_init(ready(k), 1 + WPG);
     for (int k = 0; k < L::RD; ++k) mbar_init(done(k), MS == 2 ? 2 : 1);  // tcgen05.commit
     mbar_init(accum, 2);                                                  // final commit of each issuer
-    for (int m = 0; m < L::MT_SLOTS; ++m) {
-      mbar_init(mfull(m), 1);
-      mbar_init(mfree(m), DW);
-    }
     fence_mbar_init();
     prefetch_tmap(&tm_v);
     prefetch_tmap(&tm_x);
@@ -225,67 +300,56 @@ __global__ void __launch_bounds__(threads_for(DW), 1)
   // memory must not be given up, or written by the cluster, under copies in flight.  Each
   // is the last use of its slot, whose use before it waited for.
   bool fine = false;  // (densify warps) the accumulator is whole
-  if (warp == 0) {
-    // ---- token tiles ---------------------------------------------------------
+  if (warp == 0 || warp == tokens2_warp(DW)) {
+    // ---- token tiles: the even stages, the odd ones --------------------------------
+    // (A copy costs its thread 200 cycles and more: one alone would bound a stage.)
     if (lane == 0) {
       int last = -1;
-      for (int kt = 0; kt < nk; ++kt) {
-        if (kt >= SB && !mbar_wait(done(kt - SB), ((kt - SB) / L::RD) & 1, wait_limit_ns)) break;
-        mbar_arrive_expect_tx(fullb(kt), NB * nmma * ROW_BYTES);
+      for (int kt = warp == 0 ? 0 : 1; kt < nk; kt += 2) {
+        if (kt >= S && !mbar_wait(done(kt - S), ((kt - S) / L::RD) & 1, wait_limit_ns)) break;
+        mbar_arrive_expect_tx(ready(kt), NB * nmma * ROW_BYTES);
 #pragma unroll
         for (int j = 0; j < NB; ++j)
-          tma_load_2d(sB + kt % SB * L::B_BYTES + j * NMMA * ROW_BYTES, &tm_x, (w0 + kt) * BK,
-                      (int)(n0 + j * nmma), fullb(kt));
+          tma_load_2d(sB + kt % S * L::B_BYTES + j * NMMA * ROW_BYTES, &tm_x, (w0 + kt) * BK,
+                      (int)(n0 + j * nmma), ready(kt));
         last = kt;
       }
-      for (int kt = last; kt >= 0 && kt > last - SB; --kt)
-        mbar_wait(fullb(kt), (kt / L::LB) & 1, wait_limit_ns, false);
+      for (int kt = last; kt >= 0 && kt > last - S; kt -= 2)
+        mbar_wait(ready(kt), (kt / S) & 1, wait_limit_ns, false);
     }
     __syncwarp();
   } else if (warp == 2) {
-    // ---- compact values (and, without MT, mask words) --------------------------
+    // ---- compact values and mask words, a box of MW stages at a time ------------------
     if (!MT || lane == 0) {
+      const int boxes = (nk + MW - 1) / MW;
       int last = -1;
-      for (int kt = 0; kt < nk; ++kt) {
+      for (int box = 0; box < boxes; ++box) {
         int ok = 1;
-        if (kt >= SV && lane == 0) ok = mbar_wait(vfree(kt), (kt / SV - 1) & 1, wait_limit_ns);
+        if (box >= SV && lane == 0) ok = mbar_wait(vfree(box), (box / SV - 1) & 1, wait_limit_ns);
         if (!MT) ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
         if (!ok) break;
+        const int at = box % SV, w = w0 + box * MW;
         if (lane == 0) {
-          mbar_arrive_expect_tx(fullv(kt), V_BYTES);
-          tma_load_2d(sV + kt % SV * V_BYTES, &tm_v, (w0 + kt) * 16, (int)r0, fullv(kt));
+          mbar_arrive_expect_tx(fullv(box), L::V_SLOT + (MT ? MT_SLOT : 0));
+          tma_load_2d(sV + at * L::V_SLOT, &tm_v, w * 16, (int)r0, fullv(box));
+          if (MT) tma_load_2d(sM + at * MT_SLOT, &tm_m, w, (int)r0, fullv(box));
         }
         if (!MT) {
 #pragma unroll
-          for (int i = 0; i < BM / 32; ++i) {
-            const int rr = lane + 32 * i;
-            const int64_t gr = r0 + rr;
-            const bool in = gr < rows;
-            cp_async_4(sM + kt % SV * M_BYTES + 4u * rr, masks + (in ? gr : 0) * words + w0 + kt, in ? 4u : 0u);
+          for (int i = 0; i < BM * MW / 32; ++i) {
+            const int e = lane + 32 * i, word = w + e % MW;
+            const int64_t gr = r0 + e / MW;
+            const bool in = gr < rows && word < words;
+            cp_async_4(sM + at * MT_SLOT + 4u * e, masks + (in ? gr * words + word : 0), in ? 4u : 0u);
           }
-          cp_async_arrive_noinc(fullv(kt));
+          cp_async_arrive_noinc(fullv(box));
         }
-        last = kt;
+        last = box;
       }
       if (!MT) cp_async_wait_all();
       if (lane == 0)
-        for (int kt = last; kt >= 0 && kt > last - SV; --kt)
-          mbar_wait(fullv(kt), (kt / L::FV) & 1, wait_limit_ns, false);
-    }
-    __syncwarp();
-  } else if (warp == mask_warp(DW)) {
-    // ---- mask words (MT), a box of MW stages at a time ---------------------------
-    if (MT && lane == 0) {
-      int nbox = 0;
-      for (int kt = 0; kt < nk; kt += MW) {
-        const int b = kt / MW, ms = b % L::MT_SLOTS;
-        if (b >= L::MT_SLOTS && !mbar_wait(mfree(ms), (b / L::MT_SLOTS - 1) & 1, wait_limit_ns)) break;
-        mbar_arrive_expect_tx(mfull(ms), MT_SLOT);
-        tma_load_2d(sM + ms * MT_SLOT, &tm_m, w0 + kt, (int)r0, mfull(ms));
-        nbox = b + 1;
-      }
-      for (int b = nbox > L::MT_SLOTS ? nbox - L::MT_SLOTS : 0; b < nbox; ++b)
-        mbar_wait(mfull(b % L::MT_SLOTS), (b / L::MT_SLOTS) & 1, wait_limit_ns, false);
+        for (int box = last; box >= 0 && box > last - SV; --box)
+          mbar_wait(fullv(box), (box / SV) & 1, wait_limit_ns, false);
     }
     __syncwarp();
   } else if (warp == 1 || warp == mma2_warp(DW)) {
@@ -294,18 +358,18 @@ __global__ void __launch_bounds__(threads_for(DW), 1)
     // two thirds busy: every instruction of a stage costs them several cycles, a barrier
     // test 100 to 200 and an MMA 80, so slots and phases are counted and not divided for,
     // descriptors are sums of 32 bits, and there are two such threads.
-    const int role = warp == 1 ? 0 : 1;
-    if (lane == 0) {
+    auto issue = [&](auto which) {
+      constexpr int role = decltype(which)::value;
       const uint32_t idesc = idesc_f16_f32(BM, nmma);
       const uint64_t a0 = smem_desc_sw64(sA), b0 = smem_desc_sw64(sB + (MS == 2 ? role * NMMA * ROW_BYTES : 0));
       const uint32_t a_high = (uint32_t)(a0 >> 32), b_high = (uint32_t)(b0 >> 32);
       const uint32_t a_low = (uint32_t)a0, b_low = (uint32_t)b0;
       auto desc = [](uint32_t high, uint32_t low) { return ((uint64_t)high << 32) | low; };
       constexpr int kStep = MS == 1 ? 2 : 1;
-      const int k0 = MS == 1 ? role : 0;
+      constexpr int k0 = MS == 1 ? role : 0;
       const uint32_t dacc = tmem_base + (uint32_t)(role == 0 ? 0 : MS == 1 ? L::BN : NMMA);
-      int ia = k0, ib = k0, id = k0, la = k0, lb = k0;  // slots, and places in the barriers' rings
-      uint32_t pa = 0, pb = 0;                          // phases
+      int at = k0, id = k0;  // the slot, and the place in done's ring
+      uint32_t phase = 0;
       auto next = [](int& i, int ring) {
         i += kStep;
         const bool around = i >= ring;
@@ -313,56 +377,53 @@ __global__ void __launch_bounds__(threads_for(DW), 1)
         return around ? 1u : 0u;
       };
       for (int kt = k0; kt < nk; kt += kStep) {
-        if (!mbar_wait(fullb(0) + 8u * lb, pb, wait_limit_ns)) break;
-        if (!mbar_wait(afull(0) + 8u * la, pa, wait_limit_ns)) break;
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(ready(0) + 8u * at, phase, wait_limit_ns))) break;
         tc_fence_after_sync();
-        const uint32_t al = a_low + (uint32_t)ia * (A_BYTES / 16), bl = b_low + (uint32_t)ib * (L::B_BYTES / 16);
+        const uint32_t al = a_low + (uint32_t)at * (A_BYTES / 16), bl = b_low + (uint32_t)at * (L::B_BYTES / 16);
+        if (elect_one()) {
 #pragma unroll
-        for (int ks = 0; ks < BK / 16; ++ks)
-          mma_f16(dacc, desc(a_high, al + ks * 2), desc(b_high, bl + ks * 2), idesc, kt != k0 || ks != 0);
-        // Only where someone waits for it: a commit's arrival is not ordered with the
-        // accum commit's, so another could land after this block ended, in the barriers
-        // of the next block on the SM.
-        if (kt + (SA < SB ? SA : SB) < nk) mma_commit(done(0) + 8u * id);
-        next(ia, SA);
-        next(ib, SB);
+          for (int ks = 0; ks < BK / 16; ++ks)
+            mma_f16(dacc, desc(a_high, al + ks * 2), desc(b_high, bl + ks * 2), idesc, kt != k0 || ks != 0);
+          // Only where someone waits for it: a commit's arrival is not ordered with the
+          // accum commit's, so another could land after this block ended, in the barriers
+          // of the next block on the SM.
+          if (kt + S < nk) mma_commit(done(0) + 8u * id);
+        }
+        __syncwarp();
+        phase ^= next(at, S);
         next(id, L::RD);
-        pa ^= next(la, L::LA);
-        pb ^= next(lb, L::LB);
       }
-      mma_commit(accum);  // also after an early exit: completes once issued MMAs finish
-    }
+      if (elect_one()) mma_commit(accum);  // also after an early exit: completes once issued MMAs finish
+    };
+    if (warp == 1)
+      issue(std::integral_constant<int, 0>());
+    else
+      issue(std::integral_constant<int, 1>());
     __syncwarp();
   } else {
     // ---- expansion of the weights ------------------------------------------------------
     const int dw = warp - FIRST_DENSIFY_WARP, grp = dw / WPG, wg = dw % WPG;
-    bool ok = true;
-    int box = -1;  // mask box this warp last waited for
+    bool ok = true, bytes = true;
     for (int kt = grp; kt < nk; kt += DG) {
-      bool got = mbar_wait(fullv(kt), (kt / L::FV) & 1, wait_limit_ns);
-      if (MT && kt / MW != box) {
-        // The box's slot is refilled only after every densify warp released it, so the
-        // phase this warp sees here is this box's.
-        box = kt / MW;
-        got = got && mbar_wait(mfull(box % L::MT_SLOTS), (box / L::MT_SLOTS) & 1, wait_limit_ns);
-      }
-      if (kt >= SA) got = got && mbar_wait(done(kt - SA), ((kt - SA) / L::RD) & 1, wait_limit_ns);
+      const int box = kt / MW, at = box % SV;
+      bool got = mbar_wait(fullv(box), (box / SV) & 1, wait_limit_ns);
+      if (kt >= S) got = got && mbar_wait(done(kt - S), ((kt - S) / L::RD) & 1, wait_limit_ns);
       // The warp decides together, so no lane is left behind at a warp barrier.
       if (!__all_sync(0xFFFFFFFFu, got)) {
         ok = false;
         break;
       }
-      const uint32_t sMw = MT ? sM + box % L::MT_SLOTS * MT_SLOT + (kt % MW) * 4u : sM + kt % SV * M_BYTES;
-      densify_stage<RPW>(sA + kt % SA * A_BYTES, sV + kt % SV * V_BYTES, sMw, MT ? MW * 4u : 4u, wg, lane);
+#pragma unroll
+      for (int q = 0; q < RPW; q += 32)
+        expand_32(sA + kt % S * A_BYTES, sV + at * L::V_SLOT, sM + at * MT_SLOT, kt % MW, wg * RPW + q, lane, bytes);
       // Each lane orders its tile writes before the tensor core's reads; the warp barrier
       // then lets one release-arrive publish all 32 lanes' writes and the end of their
       // reads of the values and the masks.
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(afull(kt));
-        if (kt + SV < nk) mbar_arrive(vfree(kt));
-        if (MT && kt + DG >= MW * (kt / MW + 1)) mbar_arrive(mfree(box % L::MT_SLOTS));  // its last in the box
+        mbar_arrive(ready(kt));
+        if (kt + DG >= MW * (box + 1)) mbar_arrive(vfree(box));  // its last stage in the box
       }
     }
     if (!mbar_wait(accum, 0, wait_limit_ns)) ok = false;
@@ -461,24 +522,25 @@ __global__ void __launch_bounds__(threads_for(DW), 1)
   }
 }
 
-template <int NMMA, int NB, int SA, int SB, int SV, int DG, int MS, bool MT>
+template <int NMMA, int NB, int S, int SV, int DG, int MS, bool MT>
 cudaError_t launch_mt(const SpmmTcParams& p, cudaStream_t stream) {
-  using L = Shape<NMMA, NB, SA, SB, SV, DG, MS, MT>;
+  using L = Shape<NMMA, NB, S, SV, DG, MS, MT>;
+  if (p.tile < 16 || p.tile > NMMA || p.tile % 16) return cudaErrorInvalidValue;
   CUtensorMap tm_v, tm_x, tm_m;
   memset(&tm_m, 0, sizeof(tm_m));
   if (MT && !encode_2d(&tm_m, p.masks, (uint64_t)p.words, (uint64_t)p.rows, (uint64_t)p.words * 4, MW, BM,
                        CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_DATA_TYPE_UINT32))
     return cudaErrorInvalidValue;
-  if (!encode_2d(&tm_v, p.values, (uint64_t)p.words * 16, (uint64_t)p.rows, (uint64_t)p.words * 32, 16, BM,
-                 CU_TENSOR_MAP_SWIZZLE_NONE) ||
+  if (!encode_2d(&tm_v, p.values, (uint64_t)p.words * 16, (uint64_t)p.rows, (uint64_t)p.words * 32, MW * 16, BM,
+                 CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode_2d(&tm_x, p.X, (uint64_t)p.words * 32, (uint64_t)p.T, (uint64_t)p.ldx * 2, BK, p.tile,
                  CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorInvalidValue;
   if (p.slices > 1) {  // what a block is sent fits its rings
     const int pieces = NB * ((p.tile + 31) / 32), share = (pieces + p.slices - 1) / p.slices;
-    if ((p.slices - 1) * share * 32 * BM * 4 > L::M_OFF) return cudaErrorInvalidValue;
+    if ((p.slices - 1) * share * 32 * BM * 4 > L::BAR_OFF) return cudaErrorInvalidValue;
   }
-  auto* k = linear_tc_kernel<NMMA, NB, SA, SB, SV, DG, MS, MT>;
+  auto* k = linear_tc_kernel<NMMA, NB, S, SV, DG, MS, MT>;
   static int done[64] = {0};
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
@@ -508,11 +570,11 @@ cudaError_t launch_mt(const SpmmTcParams& p, cudaStream_t stream) {
 
 // Mask words by TMA when the mask array allows it (16-byte aligned, row pitch words * 4 a
 // multiple of 16: every decoder shape), else by cp.async.
-template <int NMMA, int NB, int SA, int SB, int SV, int DG, int MS>
+template <int NMMA, int NB, int S, int SV, int DG, int MS>
 cudaError_t launch(const SpmmTcParams& p, cudaStream_t stream) {
   const bool mt = p.words % 4 == 0 && (reinterpret_cast<uintptr_t>(p.masks) & 15) == 0;
-  return mt ? launch_mt<NMMA, NB, SA, SB, SV, DG, MS, true>(p, stream)
-            : launch_mt<NMMA, NB, SA, SB, SV, DG, MS, false>(p, stream);
+  return mt ? launch_mt<NMMA, NB, S, SV, DG, MS, true>(p, stream)
+            : launch_mt<NMMA, NB, S, SV, DG, MS, false>(p, stream);
 }
 
 }  // namespace
@@ -521,10 +583,10 @@ cudaError_t launch(const SpmmTcParams& p, cudaStream_t stream) {
 // variant: kCands' index
 cudaError_t launch_spmm_tc_linear(const SpmmTcParams& p, int variant, cudaStream_t stream) {
   switch (variant) {
-    case 0: return tc::launch<256, 2, 4, 4, 12, 4, 2>(p, stream);
-    case 1: return tc::launch<256, 1, 6, 6, 16, 4, 1>(p, stream);
-    case 2: return tc::launch<128, 1, 8, 8, 20, 4, 1>(p, stream);
-    case 3: return tc::launch<64, 1, 8, 10, 24, 4, 1>(p, stream);
+    case 0: return tc::launch<256, 2, 4, 3, 4, 2>(p, stream);
+    case 1: return tc::launch<256, 1, 6, 4, 4, 1>(p, stream);
+    case 2: return tc::launch<128, 1, 8, 5, 4, 1>(p, stream);
+    case 3: return tc::launch<160, 2, 6, 3, 4, 2>(p, stream);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -532,20 +594,25 @@ cudaError_t launch_spmm_tc_linear(const SpmmTcParams& p, int variant, cudaStream
 namespace {
 
 // (variant, MMAs a block, tokens of an MMA at most, ns a stage: base, and by token beyond
-// `flat`).  Measured with 152 row tiles of 8192 columns, one block an SM, at 16 tokens
-// an MMA up to the most: 322 .. 380 ns, 267 .. 288, 262, 266; up to there the expansion of
-// the weights bounds a stage, and beyond the MMAs.
+// `flat`), measured with 152 row tiles of 8192 columns, 2:4, one block an SM: 296 ns at 128
+// tokens to 425 at 512, 220 to 257 (256 tokens), 211, and 245 to 285 (320).  Up to 128
+// tokens the expansion of the weights bounds a stage, with two MMAs a stage their issue,
+// and at 512 the loads of token tiles (32 KB in 1.3 us, four under way).
 struct Cand {
   int variant, mmas, most;
   double ns, by_token;
   int flat;
 };
-constexpr Cand kCands[] = {{0, 2, 256, 324.0, 0.2, 288}, {1, 1, 256, 267.0, 0.19, 144},
-                           {2, 1, 128, 262.0, 0.0, 0}, {3, 1, 64, 265.0, 0.0, 0}};
+constexpr Cand kCands[] = {{0, 2, 256, 290.0, 0.27, 64}, {1, 1, 256, 222.0, 0.28, 128},
+                           {2, 1, 128, 211.0, 0.0, 0}, {3, 2, 160, 245.0, 0.6, 256}};
 constexpr double kFixedNs = 4000.0;   // prologue, pipeline fill, teardown
 constexpr double kTokenNs = 10.5;     // the epilogue, a token of the tile
-constexpr double kClusterNs = 2500.0; // the slices' exchange, and
+constexpr double kClusterNs = 2500.0; // the slices' exchange,
+constexpr double kSliceNs = 250.0;    // each of them, and
 constexpr double kSentNs = 4.0;       // what a token's share of it takes
+// Clusters of 1 .. 8 such blocks that run at once on 152 SMs (cudaOccupancyMaxActiveClusters):
+// a cluster's SMs belong to one group of them.
+constexpr int kClusters[] = {152, 76, 46, 36, 28, 23, 15, 15};
 constexpr int kMaxSlices = 8, kMaxSent = 13;  // pieces of 16 KB that a block's rings can take
 
 }  // namespace
@@ -554,7 +621,7 @@ constexpr int kMaxSlices = 8, kMaxSent = 13;  // pieces of 16 KB that a block's 
 // are spread evenly over the blocks that a variant's full tiles would need, and over a
 // block's MMAs, in multiples of 16 (300 tokens: two MMAs of 160 for two of 256).
 LinearTcPlan linear_tc_plan(int64_t rows, int words, int64_t tokens, int sms) {
-  LinearTcPlan best{3, 1, 64};
+  LinearTcPlan best{2, 1, 16};
   double least = 0.0;
   for (const Cand& c : kCands) {
     const int64_t full = (int64_t)c.most * c.mmas, blocks = (tokens + full - 1) / full;
@@ -565,10 +632,9 @@ LinearTcPlan linear_tc_plan(int64_t rows, int words, int64_t tokens, int sms) {
     const double stage = c.ns + c.by_token * (all > c.flat ? all - c.flat : 0);
     for (int z = 1; z <= kMaxSlices; ++z) {
       if (z > 1 && (spmm_tc_slices(words, z) != z || (z - 1) * ((pieces + z - 1) / z) > kMaxSent)) continue;
-      // clusters of z blocks fill the SMs by groups of 16, and leave the rest of a group empty
-      const int64_t at_once = z == 1 ? sms : (int64_t)sms / 16 * (16 / z) * z + sms % 16 / z * z;
+      const int64_t at_once = (int64_t)kClusters[z - 1] * sms / 152 * z;
       const int64_t waves = (tiles * z + at_once - 1) / at_once;
-      const double exchange = z > 1 ? kClusterNs + kSentNs * all : 0.0;
+      const double exchange = z > 1 ? kClusterNs + kSliceNs * z + kSentNs * all : 0.0;
       const double t = waves * (spmm_tc_slice_words(words, z) * stage + kFixedNs + kTokenNs * all / z + exchange);
       if (least == 0.0 || t < least * 0.98) {
         least = t;

@@ -136,6 +136,26 @@ def test_linear_many_rows_beside_a_large_tile(nm):
     within(y[:, pick // 2], ref.linear(W, x, bias[pairs], "silu", True, 1.0, None), "gated")
 
 
+@pytest.mark.parametrize("tokens", [16, 100, 200, 330, 512])
+@pytest.mark.parametrize("late", [0, 1, 2, 3, 30])
+def test_linear_words_of_several_patterns(nm, tokens, late):
+    """Mask words that keep 4 columns of every byte, but for one row's from a word on:
+    16 columns at the word's start, its end, spread, or whole bytes."""
+    rows, cols = 200, 64 * 32
+    g = generator(late)
+    even = torch.tensor([0x33333333, 0x55555555, 0x0F0F0F0F, 0x3C5A6996], dtype=torch.int32, device="cuda")
+    odd = torch.tensor([0x0000FFFF, -0x10000, 0x00FF00FF, 0x7F80FF00], dtype=torch.int32, device="cuda")
+    masks = even[torch.randint(0, len(even), (rows, 64), device="cuda", generator=g)]
+    bits = torch.arange(32, dtype=torch.int32, device="cuda")
+    row = 37 * (late + 1) % rows
+    masks[row, late:] = odd[torch.randint(0, len(odd), (64 - late,), device="cuda", generator=g)]
+    assert bool((((masks[..., None] >> bits) & 1).sum(-1) == 16).all())
+    values = torch.randn((rows, cols // 2), dtype=torch.float16, device="cuda", generator=g) * 0.02
+    x = torch.randn((tokens, cols), dtype=torch.float16, device="cuda", generator=g)
+    within(nm.nm_linear(values, masks, x), ref.linear(ref.unpacked(values, masks), x, None, None, False, 1.0, None),
+           "mixed")
+
+
 @pytest.mark.parametrize("tokens", [1, 3, 8, 9, 100])
 @pytest.mark.parametrize("gated", [False, True])
 def test_linear_in_place_and_rows_between(nm, tokens, gated):
