@@ -424,6 +424,7 @@ nm_norm norm_of(Tensors& tensor, PyObject* kind, PyObject* weight_, PyObject* bi
   const Tensor *w = tensor(weight_, what, true), *b = tensor(bias_, what, true);
   nm_norm n;
   n.kind = int32(kind, what);
+  if (n.kind == NM_NORM_NONE && (w || b)) refuse(std::string("a weight or bias needs its ") + what);
   n.offset = offset;
   n.eps = eps;
   const at::ScalarType type = w ? w->scalar_type() : b ? b->scalar_type() : at::kHalf;

@@ -89,8 +89,8 @@ def nm_residual_norm(residual, block=None, norm: str | None = "rms", weight=None
     scaled residual, returned as it is where residual_scale is 1); ``gate`` fp16
     [width] or [tokens][width].  Norms are None, "rms" or "layer", times
     weight_offset + weight (1 without a weight) plus bias, all fp16 or all fp32
-    [width]; without ``norm`` the first result is None.  ``residual_out`` may be
-    ``residual`` itself."""
+    [width] and given with their norm only; without ``norm`` the first result is
+    None.  ``residual_out`` may be ``residual`` itself."""
     return _decode._calls().residual_norm(
         residual, block, _named(NORMS, norm, "norm"), weight, bias, _named(NORMS, post_norm, "post_norm"),
         post_weight, post_bias, gate, scale, residual_scale, weight_offset, eps, residual_out, out,

@@ -375,6 +375,8 @@ def test_norm_refusals(nm):
     refuses(lambda: n.run(nm, residual_out=n.residual.float()))
     refuses(lambda: n.run(nm, norm=None, weight=None, out=torch.empty_like(n.block)))
     refuses(lambda: nm.nm_residual_norm(n.residual, gate=n.kw["gate"]))
+    refuses(lambda: n.run(nm, norm=None))  # (with a weight)
+    refuses(lambda: n.run(nm, post_norm=None))
     refuses(lambda: nm.nm_residual_norm(n.residual.double()))
     refuses(lambda: nm.nm_residual_norm(n.residual, n.block.float()))
     refuses(lambda: nm.nm_residual_norm(torch.zeros((1, 32776), dtype=torch.float16, device="cuda")), 2)
@@ -526,7 +528,7 @@ def test_logprobs_empty_and_refusals(nm):
 def calls(nm):
     g = generator(8)
     out = []
-    for tokens in (1, 6, 8, 40):
+    for tokens in (1, 6, 8, 40, 200, 300, 520):
         p = Product(nm, 130, 2048, tokens, act="silu", gated=True, bias=True, residual=True, seed=tokens)
         out.append((lambda p=p, **kw: [p.run(nm, **kw)]))
     for tokens in (8, 16):
