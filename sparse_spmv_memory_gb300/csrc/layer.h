@@ -41,6 +41,11 @@ struct ResidualNormParams {
 cudaError_t launch_residual_norm(const ResidualNormParams& p, int stream_fp32, const DeviceInfo& d,
                                  cudaStream_t stream);
 
+// rows of any stride and alignment, element by element (residual_norm_any.cu), and
+// whether they are taken: widths up to 8192, or 16384 where all rows are of pairs
+bool takes_any_rows(const ResidualNormParams& p, int stream_fp32);
+cudaError_t launch_any_rows(const ResidualNormParams& p, int stream_fp32, cudaStream_t stream);
+
 // ---- log probabilities of tokens (logprobs.cu) ----------------------------------
 struct LogprobsParams {
   const void* logits;

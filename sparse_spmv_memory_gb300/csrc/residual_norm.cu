@@ -10,17 +10,14 @@
 // the parameters stay there.  Groups of 8 elements are a thread's unit of work.  A layer
 // norm takes its mean first and then the squares about it.
 //
-// Three kernels, by the rows: few rows of whole groups (a row a block, one group a
-// thread: the time to the result counts), many of them (blocks that stay), and any
-// width, stride and alignment.
+// The kernels, by the rows: few rows of whole groups (a row a block, one group a
+// thread: the time to the result counts), many of them (blocks that stay), and long rows
+// of any width, stride and alignment (shorter ones of these: residual_norm_any.cu).
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include "../../include/nm_layer.h"
-#include "device.cuh"
-#include "kernels.h"
-#include "layer.h"
+#include "norm_rows.cuh"
 
 namespace nmk {
 namespace {
@@ -50,14 +47,6 @@ struct Raw {  // a group as it lies in memory
     }
   }
 };
-
-// Two fp32 values, and arithmetic on both at once.
-using Pair = float2;
-
-__device__ __forceinline__ Pair pair(float a, float b) { return make_float2(a, b); }
-__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) { return __ffma2_rn(a, b, c); }
-__device__ __forceinline__ Pair mul2(Pair a, Pair b) { return __fmul2_rn(a, b); }
-__device__ __forceinline__ Pair add2(Pair a, Pair b) { return __fadd2_rn(a, b); }
 
 struct Group {  // 8 elements in fp32
   Pair v[4];
@@ -101,35 +90,6 @@ __device__ __forceinline__ Raw<float> narrow(const Group& x, float) {
   }
   return q;
 }
-
-// Sum over the threads of a row (threadIdx.y's, blockDim.x of them).
-struct RowSum {
-  float (*part)[32];  // [2][warps of the block]
-  int turn = 0;
-  __device__ __forceinline__ float operator()(float v) {
-    v = warp_sum(v);
-    const int warps = blockDim.x >> 5;
-    if (warps == 1) return v;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float* at = part[turn] + threadIdx.y * warps;
-    turn ^= 1;  // the sum after next writes here again, past the next one's barrier
-    if (lane == 0) at[warp] = v;
-    __syncthreads();
-    if (warps <= 8) {
-      v = (lane & 7) < warps ? at[lane & 7] : 0.f;
-#pragma unroll
-      for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-      return v;
-    }
-    if (warps <= 16) {
-      v = (lane & 15) < warps ? at[lane & 15] : 0.f;
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-      return v;
-    }
-    return warp_sum(lane < warps ? at[lane] : 0.f);
-  }
-};
 
 __device__ __forceinline__ void times(Group& x, const Group& y) {
 #pragma unroll
@@ -450,7 +410,7 @@ __global__ void __launch_bounds__(1024) residual_norm_many_kernel(const Residual
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// ---- any rows -------------------------------------------------------------------------
+// ---- long rows of any kind ------------------------------------------------------------
 // Groups are the 16-byte pieces of the stream's row (32 bytes of an fp32 stream), so a
 // row may start and end inside one: group j's elements are at(j) .. at(j) + 7, of
 // which those in 0 .. width - 1 are the row's.  Every array whose row starts at the
@@ -629,7 +589,7 @@ struct Picked {
 // A row on blockDim.x threads, N groups a thread; blockDim.y rows a block.  MAX, MIN:
 // threads a block at most, and blocks an SM at least (what the registers are cut to).
 template <typename S, int N, int MAX, int MIN>
-__global__ void __launch_bounds__(MAX, MIN) residual_norm_any_kernel(const ResidualNormParams p) {
+__global__ void __launch_bounds__(MAX, MIN) residual_norm_long_kernel(const ResidualNormParams p) {
   __shared__ float part[2][32];
   pdl_launch_dependents();
   pdl_wait_previous();
@@ -725,26 +685,10 @@ bool whole_rows(const ResidualNormParams& p) {
          at16(p.out) && p.ldo % 8 == 0;
 }
 
-// A kernel that takes a row on `threads` threads (a multiple of 32).
-template <typename K>
-cudaError_t launch_rows(K* kernel, const ResidualNormParams& p, int threads, cudaStream_t stream) {
-  const int rows = threads >= 256 ? 1 : 256 / threads;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((p.tokens + rows - 1) / rows));
-  cfg.blockDim = dim3((unsigned)threads, (unsigned)rows);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
-}
-
-template <typename S, int N, int MAX, int MIN>
-cudaError_t launch_any(const ResidualNormParams& p, int groups, cudaStream_t stream) {
+template <typename S, int N, int MAX>
+cudaError_t launch_long(const ResidualNormParams& p, int groups, cudaStream_t stream) {
   const int threads = ((groups + N - 1) / N + 31) / 32 * 32;
-  return launch_rows(residual_norm_any_kernel<S, N, MAX, MIN>, p, threads, stream);
+  return launch_rows(residual_norm_long_kernel<S, N, MAX, 1>, p, threads, stream);
 }
 
 template <typename S, int N, bool BIAS>
@@ -802,15 +746,14 @@ cudaError_t launch_stream(const ResidualNormParams& p, const DeviceInfo& d, cuda
     if (groups % 128 == 0)
       return launch_rows(residual_norm_few_kernel<S, 4>, p, groups / 4, stream);
   }
+  // Other rows element by element up to 8192 accesses of a row, else by shifted groups:
+  // 777 rows of 5121 (fp32 stream, layer norms) 22.5 us for 24.8, 16384 of 100 5.8 for
+  // 17.8; 2000 of 30001 180 for 314.
+  if (takes_any_rows(p, sizeof(S) == 4)) return launch_any_rows(p, sizeof(S) == 4, stream);
   const int groups = (p.width + 14) / 8;  // with a start anywhere in a piece
-  if (groups <= 1024 && p.tokens * groups <= (int64_t)d.sms * 1024) return launch_any<S, 1, 1024, 1>(p, groups, stream);
-  // 777 rows of 5121 (fp32 stream, layer norms): 24 us with 80 registers a thread, 27 with
-  // 64, 36 with one group a thread, 28 to 36 with four
-  if (groups <= 768) return launch_any<S, 2, 384, 2>(p, groups, stream);
-  if (groups <= 1024) return launch_any<S, 2, 512, 2>(p, groups, stream);
-  if (groups <= 2048) return launch_any<S, 4, 512, 1>(p, groups, stream);
-  if (groups <= 4096) return launch_any<S, 4, 1024, 1>(p, groups, stream);
-  return launch_any<S, 5, 1024, 1>(p, groups, stream);  // 32768 and a start inside a piece
+  if (groups <= 2048) return launch_long<S, 4, 512>(p, groups, stream);
+  if (groups <= 4096) return launch_long<S, 4, 1024>(p, groups, stream);
+  return launch_long<S, 5, 1024>(p, groups, stream);  // 32768 and a start inside a piece
 }
 
 }  // namespace

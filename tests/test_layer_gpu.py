@@ -281,7 +281,8 @@ class Norm:
             within(out, want_out, what + " out")
 
 
-WIDTHS = [1, 7, 8, 32, 100, 256, 264, 1000, 1024, 2047, 4096, 5121, 8192, 8200, 12288, 16384, 16392, 32761, 32768]
+WIDTHS = [1, 7, 8, 32, 64, 100, 129, 256, 264, 514, 770, 1000, 1024, 1538, 2047, 2050, 4096, 5121, 6146, 8191, 8192, 8193,
+          8200, 12290, 12288, 16384, 16386, 16392, 32761, 32768]
 
 
 @pytest.mark.parametrize("width", WIDTHS)
