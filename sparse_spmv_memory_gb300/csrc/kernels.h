@@ -98,8 +98,11 @@ struct SpmmParams {
   int bps = 1;         // blocks per column slice
   int steps_q = 0;     // steps per slice, and how many slices take one more
   int steps_r = 0;
-  Epilogue epi;        // nm_linear only, as the next
-  int ystride = 0;     // rows a block may have (launch_spmm_linear)
+};
+
+struct SpmmLinearParams : SpmmParams {  // nm_linear's
+  Epilogue epi;
+  int ystride = 0;  // rows a block may have, set by the launcher
 };
 
 struct SpmmPlan {
@@ -124,7 +127,7 @@ cudaError_t launch_spmm(const SpmmParams& p, const SpmmPlan& plan, int flags,
                         cudaStream_t stream);
 // nm_linear's (the default plans' variants only): with one column slice the kernel
 // writes Y, with more the fp32 partials alone (then launch_linear_combine).
-cudaError_t launch_spmm_linear(const SpmmParams& p, const SpmmPlan& plan, int flags,
+cudaError_t launch_spmm_linear(const SpmmLinearParams& p, const SpmmPlan& plan, int flags,
                                cudaStream_t stream);
 
 // ---- small batches of a 2:4 matrix on the tensor cores (spmm24.cu) ----------

@@ -191,7 +191,8 @@ int nm_linear(const void* values, const uint32_t* masks, int64_t rows, int64_t c
     return status(launch_spmv_linear(p, pl.spmv, kFlagPdl, s));
   }
   if (pl.path == Path::kSpmm) {
-    SpmmParams& p = pl.mp;
+    SpmmLinearParams p;
+    static_cast<SpmmParams&>(p) = pl.mp;
     p.values = static_cast<const uint32_t*>(values);
     p.masks = masks;
     p.X = static_cast<const __half*>(X);

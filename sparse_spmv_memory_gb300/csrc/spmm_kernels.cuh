@@ -34,6 +34,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "device.cuh"
 #include "epilogue.cuh"
 #include "kernels.h"
@@ -444,9 +446,10 @@ __device__ __forceinline__ float warp_sum_tokens(float (&v)[BP], int lane) {
 // memory, token by token, and finishes them after the cut-row combine, a token's
 // outputs side by side; blocks then own whole (gate, up) pairs where rows come in
 // pairs.  With column slices the sums go to the workspace as ever, and the combine
-// (linear.cu) has the epilogue.
+// (linear_combine_kernel) has the epilogue.  The parameters are a type of their own: in one
+// struct with nm_spmm's they made its kernels up to 1.7 % slower.
 template <int NW, int BP>
-__device__ __forceinline__ void linear_epilogue(const SpmmParams& p, const float* ysm, int ystride,
+__device__ __forceinline__ void linear_epilogue(const SpmmLinearParams& p, const float* ysm, int ystride,
                                                 int64_t r0, int64_t r1) {
   __syncthreads();
   const Epilogue& e = p.epi;
@@ -469,15 +472,11 @@ __device__ __forceinline__ void linear_epilogue(const SpmmParams& p, const float
   }
 }
 
-// A block's rows among a slice's blocks: whole pairs where the epilogue wants them.
 template <bool EPI>
-__device__ __forceinline__ BlockRows slice_rows(const SpmmParams& p, int c) {
-  const BlockRows b = split_part(c, p.rows_q, p.rows_r, p.bps);
-  return EPI && p.epi.gated && p.slices == 1 ? BlockRows{2 * b.r0, 2 * b.r1} : b;
-}
+using KernelParams = typename std::conditional<EPI, SpmmLinearParams, SpmmParams>::type;
 
 template <int NW, int U, int BP, int XF, bool EPI>
-__global__ void __launch_bounds__(NW * 32, 1) spmm_kernel(const SpmmParams p) {
+__global__ void __launch_bounds__(NW * 32, 1) spmm_kernel(const KernelParams<EPI> p) {
   extern __shared__ __align__(16) float smem[];
   const int P = p.pitch;
   constexpr bool kF32 = XF == 1 || XF == 2;             // fp32 slots
@@ -486,11 +485,13 @@ __global__ void __launch_bounds__(NW * 32, 1) spmm_kernel(const SpmmParams p) {
   float* pf = smem + 34 * P * kSlotWords;               // [NW][BP]
   float* pl = pf + NW * BP;                             // [NW][BP]
   int* rinfo = reinterpret_cast<int*>(pl + NW * BP);    // [NW][4]
-  float* ysm = reinterpret_cast<float*>(rinfo + 4 * NW);  // EPI: [BP][ystride] sums of the block's rows
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sl = (int)(blockIdx.x / (unsigned)p.bps), c = blockIdx.x - sl * p.bps;  // slice, block in it
-  const BlockRows br = slice_rows<EPI>(p, c);
+  BlockRows br = split_part(c, p.rows_q, p.rows_r, p.bps);
+  if constexpr (EPI) {
+    if (p.epi.gated && p.slices == 1) br = BlockRows{2 * br.r0, 2 * br.r1};
+  }
   const int64_t r0 = br.r0, r1 = br.r1;
   const BlockRows sr = split_part(sl, p.steps_q, p.steps_r, p.slices);
   const int ts0 = (int)sr.r0, ts1 = (int)sr.r1;
@@ -517,11 +518,16 @@ __global__ void __launch_bounds__(NW * 32, 1) spmm_kernel(const SpmmParams p) {
   const uint32_t tile_base = smem_addr(tile) + row_bytes;  // row b = 0
   auto store = [&](int row, const float (&v)[BP]) {
     const int64_t gr = r0 + row;
-    if (EPI && p.slices == 1) {
+    if constexpr (EPI) {
+      if (p.slices == 1) {
+        float* ysm = reinterpret_cast<float*>(rinfo + 4 * NW);
 #pragma unroll
-      for (int j = 0; j < BP; ++j)
-        if (j < p.batch) ysm[j * p.ystride + row] = v[j];
-    } else if (p.slices == 1) {
+        for (int j = 0; j < BP; ++j)
+          if (j < p.batch) ysm[j * p.ystride + row] = v[j];
+        return;
+      }
+    }
+    if (p.slices == 1) {
 #pragma unroll
       for (int j = 0; j < BP; ++j)
         if (j < p.batch) p.Y[(int64_t)j * p.ldy + gr] = __float2half_rn(v[j]);
@@ -587,7 +593,9 @@ __global__ void __launch_bounds__(NW * 32, 1) spmm_kernel(const SpmmParams p) {
 
   __syncthreads();
   combine_cut_rows_n<NW, BP>(rinfo, pf, pl, store);
-  if (EPI && p.slices == 1) linear_epilogue<NW, BP>(p, ysm, p.ystride, r0, r1);
+  if constexpr (EPI) {
+    if (p.slices == 1) linear_epilogue<NW, BP>(p, reinterpret_cast<const float*>(rinfo + 4 * NW), p.ystride, r0, r1);
+  }
 }
 
 // Whole-step kernel (cols % 1024 == 0, so every step of every slice is 32
@@ -618,7 +626,7 @@ __device__ __forceinline__ void load_steps_batch(SpmmBatch<U>& bt, const uint32_
 }
 
 template <int NW, int U, int BP, int XF, bool SLICED, bool EPI>
-__global__ void __launch_bounds__(NW * 32, 1) spmm_full_kernel(const SpmmParams p) {
+__global__ void __launch_bounds__(NW * 32, 1) spmm_full_kernel(const KernelParams<EPI> p) {
   extern __shared__ __align__(16) float smem[];
   const int P = p.pitch;
   constexpr bool kF32 = XF == 1 || XF == 2;
@@ -629,7 +637,6 @@ __global__ void __launch_bounds__(NW * 32, 1) spmm_full_kernel(const SpmmParams 
   float* pf = smem + 34 * P * kSlotWords;               // [NW][BP]
   float* pl = pf + NW * BP;                             // [NW][BP]
   int* rinfo = reinterpret_cast<int*>(pl + NW * BP);    // [NW][4]
-  float* ysm = reinterpret_cast<float*>(rinfo + 4 * NW);  // EPI: [BP][ystride] sums of the block's rows
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int sl = 0, ts0 = 0, Ts = p.steps;  // slice, its first step and steps of a row
@@ -642,7 +649,10 @@ __global__ void __launch_bounds__(NW * 32, 1) spmm_full_kernel(const SpmmParams 
     ts0 = (int)sr.r0;
     Ts = (int)(sr.r1 - sr.r0);
   } else {
-    br = EPI ? slice_rows<EPI>(p, blockIdx.x) : block_rows(p.rows_q, p.rows_r);
+    br = block_rows(p.rows_q, p.rows_r);
+    if constexpr (EPI) {
+      if (p.epi.gated) br = BlockRows{2 * br.r0, 2 * br.r1};
+    }
   }
   const int skip = p.steps - Ts;  // the other slices' steps
   const int F = (int)((br.r1 - br.r0) * Ts);
@@ -671,8 +681,8 @@ __global__ void __launch_bounds__(NW * 32, 1) spmm_full_kernel(const SpmmParams 
   // one token's sum of local row `row`: Y, or this slice's fp32 partial
   auto put = [&](int row, int j, float v) {
     const int64_t gr = br.r0 + row;
-    if (EPI && !SLICED)
-      ysm[j * p.ystride + row] = v;
+    if constexpr (EPI && !SLICED)
+      reinterpret_cast<float*>(rinfo + 4 * NW)[j * p.ystride + row] = v;
     else if (!SLICED)
       p.Y[(int64_t)j * p.ldy + gr] = __float2half_rn(v);
     else
@@ -756,15 +766,19 @@ __global__ void __launch_bounds__(NW * 32, 1) spmm_full_kernel(const SpmmParams 
 
   __syncthreads();
   combine_cut_rows_n<NW, BP>(rinfo, pf, pl, store);
-  if (EPI && !SLICED) linear_epilogue<NW, BP>(p, ysm, p.ystride, br.r0, br.r1);
+  if constexpr (EPI && !SLICED)
+    linear_epilogue<NW, BP>(p, reinterpret_cast<const float*>(rinfo + 4 * NW), p.ystride, br.r0, br.r1);
 }
 
 template <int NW, int U, int BP, int XF, bool EPI>
-cudaError_t launch_spmm_t(const SpmmParams& p, int grid, int flags, cudaStream_t stream) {
+cudaError_t launch_spmm_t(const KernelParams<EPI>& p, int grid, int flags, cudaStream_t stream) {
   static int smem_set[64] = {0}, smem_full[64] = {0}, smem_sliced[64] = {0};
-  const size_t smem = spmm_smem_bytes(p.pitch, NW, BP, XF) +
-                      (EPI && p.slices == 1 ? (size_t)BP * p.ystride * sizeof(float) : 0);
-  const int64_t block_steps = (EPI && p.epi.gated ? 2 : 1) * (p.rows_q + 2) * (int64_t)p.steps;
+  size_t smem = spmm_smem_bytes(p.pitch, NW, BP, XF);
+  int64_t block_steps = (p.rows_q + 2) * (int64_t)p.steps;
+  if constexpr (EPI) {
+    if (p.slices == 1) smem += (size_t)BP * p.ystride * sizeof(float);  // the block's rows' sums
+    if (p.epi.gated) block_steps *= 2;
+  }
   if (p.words % 32 == 0 && block_steps < (int64_t)0x7FFFFFFF) {
     auto* k = p.slices == 1 ? spmm_full_kernel<NW, U, BP, XF, false, EPI>
                             : spmm_full_kernel<NW, U, BP, XF, true, EPI>;

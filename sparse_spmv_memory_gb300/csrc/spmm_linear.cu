@@ -6,7 +6,7 @@
 namespace nmk {
 
 template <int BP>
-static cudaError_t launch_bp(const SpmmParams& p, int variant, int grid, cudaStream_t stream, int flags) {
+static cudaError_t launch_bp(const SpmmLinearParams& p, int variant, int grid, cudaStream_t stream, int flags) {
   switch (variant) {
 #define NM_SPMM_LINEAR_CASE(i)                                                                   \
   case i:                                                                                        \
@@ -18,9 +18,9 @@ static cudaError_t launch_bp(const SpmmParams& p, int variant, int grid, cudaStr
   }
 }
 
-cudaError_t launch_spmm_linear(const SpmmParams& p0, const SpmmPlan& plan, int flags,
+cudaError_t launch_spmm_linear(const SpmmLinearParams& p0, const SpmmPlan& plan, int flags,
                                cudaStream_t stream) {
-  SpmmParams p = p0;
+  SpmmLinearParams p = p0;
   p.bps = plan.grid / p.slices;
   // whole pairs in a block where the kernel itself has the epilogue
   const bool by_pairs = p.epi.gated && p.slices == 1;
