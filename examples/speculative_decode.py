@@ -4,8 +4,8 @@
 
 A decoder with random 2:4 weights: per layer the sparse products nm_spmm24
 (QKV, output, gate+up, down) for the drafted nodes of a step as one batch,
-nm_rope_append and nm_tree_attention between them, and after the last layer
-nm_tree_verify.  The accepted path is committed by appending its rows again at
+nm_rope_append, nm_tree_attention and nm_residual_norm between them, and after the
+last layer nm_tree_verify and, for the score of the text, nm_token_logprobs.  The accepted path is committed by appending its rows again at
 their final slots.  In place of a draft model there is a stand-in that has seen
 the text: it proposes the tokens of a plain decoding, three quarters of them
 right, with wrong siblings.  With temperature 0 the tokens are those of decoding
@@ -26,10 +26,6 @@ import sparse_spmv_memory_gb300 as nm
 
 HIDDEN, FFN, Q_HEADS, KV_HEADS, DIM, VOCAB, PAGE = 1024, 2048, 8, 2, 128, 2048, 16
 DTYPES = {"fp16": torch.float16, "e4m3": torch.float8_e4m3fn, "int8": torch.int8}
-
-
-def norm(x):
-    return (x.float() * torch.rsqrt(x.float().square().mean(-1, keepdim=True) + 1e-6)).half()
 
 
 class Matrix:
@@ -88,18 +84,19 @@ class Decoder:
         ctx = torch.tensor([self.len], dtype=torch.int32, device="cuda")
         x = self.embed[torch.tensor(tokens, device="cuda")]
         qkvs, slots = [], self.slots(place)
+        h, _ = nm.nm_residual_norm(x)
         for i, w in enumerate(self.layers):
-            qkv = w["qkv"](norm(x))
+            qkv = w["qkv"](h)
             q = nm.nm_rope_append(qkv, self.k[i], self.v[i], pos, slots, self.freq, Q_HEADS,
                                   k_scale=self.ks[i], v_scale=self.vs[i])
             a, _ = nm.nm_tree_attention(q, self.k[i], self.v[i], self.table, ctx, start, n,
                                         tree_mask=mask, k_scale=self.ks[i], v_scale=self.vs[i],
                                         workspace=self.work if n <= 8 else None)
-            x = x + w["o"](a.view(n, -1))
-            gate, up = w["up"](norm(x)).float().chunk(2, -1)
-            x = x + w["down"]((torch.nn.functional.silu(gate) * up).half())
+            h, x = nm.nm_residual_norm(x, w["o"](a.view(n, -1)))
+            gate, up = w["up"](h).float().chunk(2, -1)
+            h, x = nm.nm_residual_norm(x, w["down"]((torch.nn.functional.silu(gate) * up).half()))
             qkvs.append(qkv)
-        return (norm(x).float() @ self.head.float().T) * 2 * HIDDEN ** -0.5, qkvs, pos
+        return (h.float() @ self.head.float().T) * 2 * HIDDEN ** -0.5, qkvs, pos
 
     def commit(self, path, qkvs, pos):
         """Append the accepted nodes' rows again where they stay: node path[i] at the
@@ -121,9 +118,10 @@ def propose(text, rnd):
     return [guess(0), guess(0), guess(1), guess(1), guess(2), guess(2), guess(3)], [0, 0, 1, 2, 3, 4, 5]
 
 
-def decode(layers, cache, steps, temperature, seed, text=None):
+def decode(layers, cache, steps, temperature, seed, text=None, scores=None):
     """``steps`` tokens, and how many drafted ones were accepted; ``text``: what the
-    draft knows (None: one token at a time)."""
+    draft knows (None: one token at a time); ``scores``: a list that gets their log
+    probabilities."""
     gen, rnd = torch.Generator("cuda").manual_seed(seed + 1), random.Random(seed)
     model = Decoder(layers, cache, 16 + 8 * (steps + 2), seed)
     out, last, accepted = [], 1, 0
@@ -143,7 +141,12 @@ def decode(layers, cache, steps, temperature, seed, text=None):
         model.commit(kept, qkvs, pos)
         accepted += len(kept) - 1
         last = int(token[0])
-        out += [tokens[i] for i in kept[1:]] + [last]
+        more = [tokens[i] for i in kept[1:]] + [last]
+        if scores is not None:  # node kept[i] answered more[i]
+            answered = torch.tensor(more, dtype=torch.int32, device="cuda")
+            scores += nm.nm_token_logprobs(logits[path[0, :len(kept)].long()], answered,
+                                           temperature=temperature or 1.0)[0].tolist()
+        out += more
     return out[:steps], accepted
 
 
@@ -157,9 +160,10 @@ def main(argv=None):
     ap.add_argument("--check", action="store_true", help="compare with one token at a time")
     a = ap.parse_args(argv)
     plain, _ = decode(a.layers, a.cache, a.steps, 0.0, a.seed)
-    out, accepted = decode(a.layers, a.cache, a.steps, a.temperature, a.seed, plain)
+    scores = []
+    out, accepted = decode(a.layers, a.cache, a.steps, a.temperature, a.seed, plain, scores)
     print("tokens:", *out)
-    print(f"{accepted} of the {a.steps} tokens were drafted")
+    print(f"{accepted} of the {a.steps} tokens were drafted; log probability {sum(scores[:a.steps]):.2f}")
     if a.check:
         print("one at a time:", "the same" if plain == out else plain)
         return 0 if plain == out else 1
