@@ -18,6 +18,10 @@
 //    the thread that holds it has its sums taken again without it.  So with R = Z - 1,
 //    log p = (x - max) / T - log1p(R) is accurate where R is tiny.
 // Few rows are cut into a cluster's blocks, whose lists and sums the first block joins.
+// Memory bounds many rows: 2048 of 128256 (fp16, top 5) take 101 us, 5.2 TB/s, where
+// reading them in this order takes 75 to 77 and the sums without the lists 85; 256
+// threads and 64 registers let an SM have four rows, so that one's end is another's
+// loads.  Few rows are a chain of latencies: 7.0 us for one row of 128256 (16 blocks).
 // Elements are taken in chunks of 8 from the 16-byte boundary at or before the row's
 // start, so rows of any alignment are read by whole vectors but for their two ends.
 #include <cuda_fp16.h>

@@ -1,6 +1,7 @@
 // spmm_linear.cu -- nm_linear's products for 2..8 tokens (and for one token with rows
 // too long for nm_spmv): nm_spmm's kernels with the epilogue, in the variants that
-// the default plans take.
+// the default plans take.  The gathers of x in shared memory bound them, as nm_spmm:
+// 10240 x 8192 at 8 tokens 29.0 us (28.2).
 #include "spmm_kernels.cuh"
 
 namespace nmk {
