@@ -298,7 +298,10 @@ __global__ void __launch_bounds__(threads_for(DW), 1)
 
   // Before it ends, a producer waits (bounded) for its copies among a ring's last: shared
   // memory must not be given up, or written by the cluster, under copies in flight.  Each
-  // is the last use of its slot, whose use before it waited for.
+  // is the last use of its slot, whose use before it waited for.  (ready also counts the
+  // densify warps, which do not come any more once a wait has given up: then the copies
+  // have a tenth of a second a slot.)
+  constexpr uint64_t kDrainNs = 100000000;
   bool fine = false;  // (densify warps) the accumulator is whole
   if (warp == 0 || warp == tokens2_warp(DW)) {
     // ---- token tiles: the even stages, the odd ones --------------------------------
@@ -315,7 +318,8 @@ __global__ void __launch_bounds__(threads_for(DW), 1)
         last = kt;
       }
       for (int kt = last; kt >= 0 && kt > last - S; kt -= 2)
-        mbar_wait(ready(kt), (kt / S) & 1, wait_limit_ns, false);
+        if (!mbar_try_wait(ready(kt), (kt / S) & 1))
+          mbar_wait(ready(kt), (kt / S) & 1, wait_aborted() ? min(wait_limit_ns, kDrainNs) : wait_limit_ns, false);
     }
     __syncwarp();
   } else if (warp == 2) {
@@ -632,7 +636,7 @@ LinearTcPlan linear_tc_plan(int64_t rows, int words, int64_t tokens, int sms) {
     const double stage = c.ns + c.by_token * (all > c.flat ? all - c.flat : 0);
     for (int z = 1; z <= kMaxSlices; ++z) {
       if (z > 1 && (spmm_tc_slices(words, z) != z || (z - 1) * ((pieces + z - 1) / z) > kMaxSent)) continue;
-      const int64_t at_once = (int64_t)kClusters[z - 1] * sms / 152 * z;
+      const int64_t clusters = (int64_t)kClusters[z - 1] * sms / 152, at_once = (clusters > 0 ? clusters : 1) * z;
       const int64_t waves = (tiles * z + at_once - 1) / at_once;
       const double exchange = z > 1 ? kClusterNs + kSliceNs * z + kSentNs * all : 0.0;
       const double t = waves * (spmm_tc_slice_words(words, z) * stage + kFixedNs + kTokenNs * all / z + exchange);
