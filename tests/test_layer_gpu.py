@@ -156,6 +156,20 @@ def test_linear_words_of_several_patterns(nm, tokens, late):
            "mixed")
 
 
+@pytest.mark.parametrize("tokens", [1, 8, 20, 200, 300])
+@pytest.mark.parametrize("pattern", [(2, 4), (8, 16)], ids=str)
+def test_linear_masks_and_rows_off_16_bytes(nm, tokens, pattern):
+    """Mask words from any multiple of 4 bytes on, outputs from any multiple of 2."""
+    p = Product(nm, 200, 1024, tokens, pattern, "gelu_tanh", bias=True, residual=True, seed=tokens)
+    want = p.want()
+    moved = torch.zeros(p.masks.numel() + 1, dtype=torch.int32, device="cuda")[1:].view_as(p.masks)
+    p.masks = moved.copy_(p.masks)
+    big = torch.full((tokens, 203), 7.0, device="cuda").half()
+    y = p.run(nm, Y=big[:, 1:201])
+    within(y, want, "moved")
+    assert bool((big[:, 0] == 7).all()) and bool((big[:, 201:] == 7).all())
+
+
 @pytest.mark.parametrize("tokens", [1, 3, 8, 9, 100])
 @pytest.mark.parametrize("gated", [False, True])
 def test_linear_in_place_and_rows_between(nm, tokens, gated):
