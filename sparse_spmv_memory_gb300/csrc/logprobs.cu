@@ -18,7 +18,7 @@
 //    the thread that holds it has its sums taken again without it.  So with R = Z - 1,
 //    log p = (x - max) / T - log1p(R) is accurate where R is tiny.
 // Few rows are cut into a cluster's blocks, whose lists and sums the first block joins.
-// Memory bounds many rows: 2048 of 128256 (fp16, top 5) take 101 us, 5.2 TB/s, where
+// Memory bounds many rows: 2048 of 128256 (fp16, top 5) take 99 us, 5.3 TB/s, where
 // reading them in this order takes 75 to 77 and the sums without the lists 85; 256
 // threads and 64 registers let an SM have four rows, so that one's end is another's
 // loads.  Few rows are a chain of latencies: 7.0 us for one row of 128256 (16 blocks).
@@ -162,41 +162,24 @@ __device__ __forceinline__ float largest(const Raw32& q) {
   return m;
 }
 
-// References are kept as the exponents subtract them: fp16 rows as fl(M c), so that a
-// thread's t = x c - fl(M c) is one fused operation (finite for finite x) and what the
-// rounding of M c adds to every t is taken out at the end; fp32 rows as M, with
-// t = (x - M) c, since their x c may overflow.
-template <typename T>
-__device__ __forceinline__ float reference(float x, float c) {
-  return sizeof(T) == 2 ? __fmul_rn(x, c) : x;  // (not fused into what uses it)
-}
+// t of an element: the difference first, which is exact or rounded once, as at a small
+// temperature x c and M c are far larger than what is left of them (fma(x, c, -fl(M c))
+// is off by half a step of M c, beyond any exponent from |M c| = 2^32 on).
+__device__ __forceinline__ float difference(float x, float ref, float c) { return (x - ref) * c; }
 
-template <typename T>
-__device__ __forceinline__ float difference(float x, float ref, float c) {
-  return sizeof(T) == 2 ? fmaf(x, c, -ref) : (x - ref) * c;
-}
-
-// t of an element, not below kFar; NaN stays.
-template <typename T>
+// The same, not below kFar; NaN stays.
 __device__ __forceinline__ float exponent(float x, float ref, float c) {
-  return max_nan(difference<T>(x, ref, c), kFar);
+  return max_nan(difference(x, ref, c), kFar);
 }
 
 struct Sums {
   float s, a;
 };
 
-// The sums with every t moved by d.
-__device__ __forceinline__ Sums shifted(Sums v, float d) {
-  d = max_nan(d, kFar);
-  const float f = exp2_fast(d);
-  return {v.s * f, f * fmaf(d, v.s, v.a)};
-}
-
 // The sums relative to `to` in place of `from`.
-template <typename T>
 __device__ __forceinline__ Sums moved(Sums v, float from, float to, float c) {
-  return shifted(v, sizeof(T) == 2 ? from - to : (from - to) * c);
+  const float d = exponent(from, to, c), f = exp2_fast(d);
+  return {v.s * f, f * fmaf(d, v.s, v.a)};
 }
 
 // A thread's running sums, of elements 2 i and of elements 2 i + 1.
@@ -213,13 +196,13 @@ __device__ __forceinline__ float2 pair_of(const Raw32& q, int i) {
 }
 
 // A chunk's terms.
-template <typename T, typename Raw>
+template <typename Raw>
 __device__ __forceinline__ void add_chunk(Running& v, const Raw& q, float ref, float c) {
   const float2 c2 = make_float2(c, c), r2 = make_float2(-ref, -ref);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 x = pair_of(q, i);
-    float2 t = sizeof(T) == 2 ? __ffma2_rn(x, c2, r2) : __fmul2_rn(__fadd2_rn(x, r2), c2);
+    float2 t = __fmul2_rn(__fadd2_rn(x, r2), c2);
     t = make_float2(max_nan(t.x, kFar), max_nan(t.y, kFar));
     const float2 e = make_float2(exp2_fast(t.x), exp2_fast(t.y));
     v.s = __fadd2_rn(v.s, e);
@@ -247,14 +230,14 @@ struct Kept {
       }
       all = u == 0 ? top : max_nan(all, top);
     }
-    if (!(difference<T>(all, M, c) <= 4.f)) {  // a far larger element, or NaN
-      const float to = reference<T>(max_nan(all, Lowest<T>::value), c);
-      const Sums x = moved<T>({run.s.x, run.a.x}, M, to, c), y = moved<T>({run.s.y, run.a.y}, M, to, c);
+    if (!(difference(all, M, c) <= 4.f)) {  // a far larger element, or NaN
+      const float to = max_nan(all, Lowest<T>::value);
+      const Sums x = moved({run.s.x, run.a.x}, M, to, c), y = moved({run.s.y, run.a.y}, M, to, c);
       run = {make_float2(x.s, y.s), make_float2(x.a, y.a)};
       M = to;
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) add_chunk<T>(run, q[u], M, c);
+    for (int u = 0; u < U; ++u) add_chunk(run, q[u], M, c);
   }
 };
 
@@ -404,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) logprobs_kernel(const 
     float top = -INFINITY;  // the warp's reference
 #pragma unroll
     for (int u = 0; u < U; ++u) top = fmaxf(top, largest(q[0][u]));
-    kept.M = reference<T>(unordered(__reduce_max_sync(kAll, ordered(fmaxf(top, Lowest<T>::value)))), c);
+    kept.M = unordered(__reduce_max_sync(kAll, ordered(fmaxf(top, Lowest<T>::value))));
     if (starts) {
       Raw one[1];
       load_end(r, c0, one[0]);
@@ -466,12 +449,12 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) logprobs_kernel(const 
   __syncthreads();
   const uint64_t bound = sh.bound, head = sh.head;
   const float top_x = head ? unordered((uint32_t)(head >> 32)) : -INFINITY;
-  const float m = reference<T>(fmaxf(top_x, Lowest<T>::value), c);
+  const float m = fmaxf(top_x, Lowest<T>::value);
   // (a row that has no distribution has no list either)
   const bool hopeless = blocks == 1 && (spoilt || !(fabsf(top_x) < INFINITY));
   int count = 0;
   Sums w = {0.f, 0.f};
-  if (key != head && key != 0) w = moved<T>(v, kept.M, m, c);  // the owner's are taken again without its largest
+  if (key != head && key != 0) w = moved(v, kept.M, m, c);  // the owner's are taken again without its largest
   if (!hopeless) {
     // The owner comes first, so that its sums are always added by the same threads; the
     // others come as they come, which decides nothing.
@@ -512,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) logprobs_kernel(const 
           if (k == owner_chunk && !skipped && x[e] == top_x) {
             skipped = true;  // its largest, once
           } else {
-            const float t = exponent<T>(x[e], m, c), y = exp2_fast(t);
+            const float t = exponent(x[e], m, c), y = exp2_fast(t);
             w.s += y;
             w.a = fmaf(y, t, w.a);
           }
@@ -668,20 +651,15 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) logprobs_kernel(const 
   int holds = 0;
   for (int b = 1; b < blocks; ++b)
     if (sh.best[b][0] > sh.best[holds][0]) holds = b;
-  const float x_max = sh.part[holds].largest, ref = reference<T>(x_max, c);
+  const float x_max = sh.part[holds].largest;
   float R = 0.f, A = 0.f;
   for (int b = 0; b < blocks; ++b) {
     const Part q = sh.part[b];
     Sums z = {q.s, q.a};
     if (b != holds && q.largest != -INFINITY) z.s += 1.f;
-    z = moved<T>(z, reference<T>(fmaxf(q.largest, Lowest<T>::value), c), ref, c);
+    z = moved(z, fmaxf(q.largest, Lowest<T>::value), x_max, c);
     R += z.s;
     A += z.a;
-  }
-  if (sizeof(T) == 2) {  // t relative to max c itself
-    const Sums z = shifted({R, A}, -fmaf(x_max, c, -ref));
-    R = z.s;
-    A = z.a;
   }
   const bool valid = fabsf(x_max) < INFINITY && R == R && !(blocks == 1 && spoilt);
   const float log_z = log1pf(R);

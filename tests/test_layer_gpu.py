@@ -503,6 +503,31 @@ def test_logprobs_temperatures(nm):
         refuses(lambda: nm.nm_token_logprobs(x, ids, temperature=t), 2)
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32], ids=["fp16", "fp32"])
+@pytest.mark.parametrize("rows,vocab", [(1, 128256), (7, 50257), (5, 3000), (200, 5000)])
+@pytest.mark.parametrize("peak", [14.3, 21.6, 3002.0, 4001.0, 30016.0, 65504.0])
+def test_logprobs_large_and_equal_logits_at_small_temperatures(nm, dtype, rows, vocab, peak):
+    """x / T far beyond float32's exact whole numbers: equal largest logits, in different
+    blocks of a row too, share the probability; rows of one value are even (of the type's
+    lowest too), and one step of fp16 below the largest is as far as it is."""
+    g = generator(vocab)
+    x = (torch.randn((rows, vocab), device="cuda", generator=g) * 2).to(dtype)
+    peak = torch.tensor(peak).half()
+    below = float(peak) * (1 - 2.0 ** -10)
+    x[:, [3, vocab - 2]] = peak.to(dtype).cuda()
+    x[:, vocab // 2] = below
+    x[::3, vocab // 3] = float(peak)
+    if rows > 1:
+        x[1] = -float(peak)
+    if rows > 2:
+        x[2] = torch.finfo(dtype).min
+        x[2, 7] = -INF
+    ids = torch.tensor([3, vocab - 2, vocab // 2, 5], dtype=torch.int32, device="cuda").repeat(rows, 1)
+    for t in (2.0 ** -20, 1e-6, 1e-5, 1e-4, 1e-3, 0.01, 0.3):
+        t = float(torch.tensor(t))  # (the call's float32)
+        check_logprobs(nm, x, ids, 4, t, f"{peak} {t}")
+
+
 def test_logprobs_many_ids_and_alignment(nm):
     g = generator(4)
     base = torch.randn(40 * 1001 + 16, device="cuda", generator=g)
