@@ -8,7 +8,7 @@
 // rows, and the instructions: so whatever does not depend on a sum over the row (the
 // norms' parameters, the gate) is asked for before that sum, and rows bypass L1 so that
 // the parameters stay there.  Groups of 8 elements are a thread's unit of work.  A layer
-// norm takes its mean first and then the squares about it.
+// norm takes its mean first, and then the squares about it and what the mean is off by.
 //
 // The kernels, by the rows: few rows of whole groups (a row a block, one group a
 // thread: the time to the result counts), many of them (blocks that stay), and long rows
@@ -101,37 +101,69 @@ __device__ __forceinline__ void times(Group& x, float y) {
   for (int i = 0; i < 4; ++i) x.v[i] = mul2(x.v[i], pair(y, y));
 }
 
-// x - mean (layer norms only), and 1 / sqrt(mean square + eps) of it; 1 without a norm.
-// x is 0 outside the row, and zero(j, x) makes it so again.
+// x - mean (layer norms only, the mean as its sum gives it), and the factor of the norm;
+// r = 1 without a norm.  x is 0 outside the row, and zero(j, x) makes it so again.
 template <int N, typename Zero>
-__device__ __forceinline__ float centred(Group (&x)[N], const NormArgs& a, float inv_width, RowSum& sum,
-                                         Zero&& zero) {
-  if (a.kind == NM_NORM_NONE) return 1.f;
-  Pair t = pair(0.f, 0.f);
-  if (a.kind == NM_NORM_LAYER) {
+__device__ __forceinline__ Factor factor(Group (&x)[N], const NormArgs& a, float inv_width, RowSum& sum, Zero&& zero) {
+  if (a.kind == NM_NORM_NONE) return {1.f, 0.f};
+  auto total = [&]() {
+    Pair t = pair(0.f, 0.f);
 #pragma unroll
     for (int j = 0; j < N; ++j)
       t = add2(t, add2(add2(x[j].v[0], x[j].v[1]), add2(x[j].v[2], x[j].v[3])));
-    const float mean = sum(t.x + t.y) * inv_width;
+    return t.x + t.y;
+  };
+  auto squares = [&]() {
+    Pair t = pair(0.f, 0.f);
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
+    for (int j = 0; j < N; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[j].v[i] = add2(x[j].v[i], pair(-mean, -mean));
-      zero(j, x[j]);
-    }
-    t = pair(0.f, 0.f);
+      for (int i = 0; i < 4; ++i) t = fma2(x[j].v[i], x[j].v[i], t);
+    return t.x + t.y;
+  };
+  if (a.kind != NM_NORM_LAYER) return {1.f / sqrtf(sum(squares()) * inv_width + a.eps), 0.f};
+  const float mean = __fmul_rn(sum(total()), inv_width);  // (equal elements, as a rule: nothing left)
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[j].v[i] = add2(x[j].v[i], pair(-mean, -mean));
+    zero(j, x[j]);
   }
+  return layer_factor(sum(pair(total(), squares())), inv_width, a.eps);
+}
+
+// The same with the rest of the mean taken from x (no longer 0 outside the row): r.
+template <int N, typename Zero>
+__device__ __forceinline__ float centred(Group (&x)[N], const NormArgs& a, float inv_width, RowSum& sum, Zero&& zero) {
+  const Factor f = factor<N>(x, a, inv_width, sum, zero);
+  if (a.kind == NM_NORM_LAYER) {
 #pragma unroll
-  for (int j = 0; j < N; ++j)
+    for (int j = 0; j < N; ++j)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) t = fma2(x[j].v[i], x[j].v[i], t);
-  return 1.f / sqrtf(sum(t.x + t.y) * inv_width + a.eps);
+      for (int i = 0; i < 4; ++i) x[j].v[i] = add2(x[j].v[i], pair(-f.rest, -f.rest));
+  }
+  return f.r;
 }
 
 template <int N>
 __device__ __forceinline__ float centred(Group (&x)[N], const NormArgs& a, float inv_width, RowSum& sum) {
   return centred<N>(x, a, inv_width, sum, [](int, Group&) {});
 }
+
+// For kernels that multiply by r first: x r - rest r in one operation (-0 without a rest,
+// which changes nothing).
+struct Scale {
+  Pair r, shift;
+  __device__ __forceinline__ explicit Scale(const Factor& f) {
+    const float s = -__fmul_rn(f.rest, f.r);
+    r = pair(f.r, f.r);
+    shift = pair(s, s);
+  }
+  __device__ __forceinline__ void operator()(Group& x) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x.v[i] = fma2(x.v[i], r, shift);
+  }
+};
 
 // N groups of a norm's parameters, packed where they are fp16.
 template <int N>
@@ -191,7 +223,7 @@ __device__ __forceinline__ void apply(Group& x, float r, const NormArgs& a, cons
 // 4096: 1.9 us, loads and one sum.
 template <typename S, int N>
 __global__ void __launch_bounds__(1024) residual_norm_few_kernel(const ResidualNormParams p) {
-  __shared__ float part[2][32];
+  __shared__ float part[4][32];
   pdl_launch_dependents();
   pdl_wait_previous();
   const int at = 8 * (int)threadIdx.x, step = 8 * (int)blockDim.x;
@@ -262,8 +294,8 @@ __global__ void __launch_bounds__(1024) residual_norm_few_kernel(const ResidualN
 // row two conversions and about seven operations on both of two elements; and the
 // next rows' stream, block and gate are on their way to shared memory meanwhile, each
 // thread's own groups to slots of its own (no barrier).  4096 rows of 8192 with both
-// norms and a gate: 50 us (5.4 TB/s); a block a row, with the parameters read for every
-// row, took 55, half of it issuing instructions and half waiting for a row's loads.
+// norms and a gate: 49 us (5.5 TB/s), with layer norms 82; a block a row, with the parameters
+// read for every row, took 55 for the 49, half of it issuing instructions and half waiting for a row's loads.
 __device__ __forceinline__ void copy_async(uint4* to, const void* from) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(to)), "l"(from) : "memory");
 }
@@ -296,7 +328,7 @@ __device__ __forceinline__ Group parameters(const void* base, int fp32, float of
 
 template <typename S, int N, bool BIAS>
 __global__ void __launch_bounds__(1024) residual_norm_many_kernel(const ResidualNormParams p, int stages) {
-  __shared__ float part[2][32];
+  __shared__ float part[4][32];
   extern __shared__ uint4 slots[];
   constexpr int kStream = sizeof(S) / 2;  // slots of a group of the stream
   const int threads = blockDim.x * blockDim.y;
@@ -357,11 +389,11 @@ __global__ void __launch_bounds__(1024) residual_norm_many_kernel(const Residual
     if (p.block) {
 #pragma unroll
       for (int j = 0; j < N; ++j) s[j] = widen(staged<__half>(slot(stage, j), threads));
-      const float r = centred<N>(s, p.post, p.inv_width, sum);
+      const Scale scaled(factor<N>(s, p.post, p.inv_width, sum, [](int, Group&) {}));
 #pragma unroll
       for (int j = 0; j < N; ++j) {
         Group x = widen(staged<S>(slot(stage, N + j * kStream), threads));
-        times(s[j], r);
+        scaled(s[j]);
         if (p.own_gate) {
           const Group g = widen(staged<__half>(slot(stage, N * (1 + kStream) + j), threads));
           Group w = P[j];
@@ -394,11 +426,11 @@ __global__ void __launch_bounds__(1024) residual_norm_many_kernel(const Residual
       for (int j = 0; j < N; ++j) put(to + j * step, s[j]);
     }
     if (p.out) {
-      const float r = centred<N>(s, p.pre, p.inv_width, sum);
+      const Scale scaled(factor<N>(s, p.pre, p.inv_width, sum, [](int, Group&) {}));
       __half* to = p.out + row * p.ldo + at;
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        times(s[j], r);
+        scaled(s[j]);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           s[j].v[i] = BIAS ? fma2(s[j].v[i], W[j].v[i], WB[j].v[i]) : mul2(s[j].v[i], W[j].v[i]);
@@ -591,7 +623,7 @@ struct Picked {
 // threads a block at most, and blocks an SM at least (what the registers are cut to).
 template <typename S, int N, int MAX, int MIN>
 __global__ void __launch_bounds__(MAX, MIN) residual_norm_long_kernel(const ResidualNormParams p) {
-  __shared__ float part[2][32];
+  __shared__ float part[4][32];
   pdl_launch_dependents();
   pdl_wait_previous();
   const int64_t mine = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;

@@ -8,7 +8,7 @@
 // A thread has E pairs in fp32 registers; block, stream, gate and the first parameters
 // are asked for before the first sum.  64 registers a thread (40 for pairs): with fewer
 // they are spilled.  777 rows of 5121, fp32 stream, layer norms and a gate for each token:
-// 22.5 us (2.5 TB/s), three rounds of blocks of 7 us each, loads and four sums one after
+// 25.0 us (2.2 TB/s), three rounds of blocks of 8 us each, loads and four sums one after
 // the other; 4096 of 1002, fp16: 8.0 us (4.1 TB/s); 16384 of 100: 5.8.
 #include "norm_rows.cuh"
 
@@ -71,24 +71,32 @@ struct Params {
   }
 };
 
-// x - mean (layer norms only; 0 outside the row again), and 1 / sqrt(mean square + eps)
-// of it; 1 without a norm.
+// x - mean (layer norms only; no longer 0 outside the row), and 1 / sqrt(mean square +
+// eps) of it; 1 without a norm.
 template <int E, typename A>
 __device__ __forceinline__ float centred(Pair (&x)[E], const A& acc, const NormArgs& a, float inv_width, RowSum& sum) {
   if (a.kind == NM_NORM_NONE) return 1.f;
-  Pair t = pair(0.f, 0.f);
-  if (a.kind == NM_NORM_LAYER) {
+  auto total = [&]() {
+    Pair t = pair(0.f, 0.f);
 #pragma unroll
     for (int k = 0; k < E; ++k) t = add2(t, x[k]);
-    const float mean = __fmul_rn(sum(t.x + t.y), inv_width);  // (rounded: equal elements have no deviation)
+    return t.x + t.y;
+  };
+  auto squares = [&]() {
+    Pair t = pair(0.f, 0.f);
 #pragma unroll
-    for (int k = 0; k < E; ++k)
-      x[k] = pair(acc.in(k, 0) ? x[k].x - mean : 0.f, acc.in(k, 1) ? x[k].y - mean : 0.f);
-    t = pair(0.f, 0.f);
-  }
+    for (int k = 0; k < E; ++k) t = fma2(x[k], x[k], t);
+    return t.x + t.y;
+  };
+  if (a.kind != NM_NORM_LAYER) return 1.f / sqrtf(sum(squares()) * inv_width + a.eps);
+  const float mean = __fmul_rn(sum(total()), inv_width);  // (equal elements, as a rule: nothing left)
 #pragma unroll
-  for (int k = 0; k < E; ++k) t = fma2(x[k], x[k], t);
-  return 1.f / sqrtf(sum(t.x + t.y) * inv_width + a.eps);
+  for (int k = 0; k < E; ++k)
+    x[k] = pair(acc.in(k, 0) ? x[k].x - mean : 0.f, acc.in(k, 1) ? x[k].y - mean : 0.f);
+  const Factor f = layer_factor(sum(pair(total(), squares())), inv_width, a.eps);
+#pragma unroll
+  for (int k = 0; k < E; ++k) x[k] = add2(x[k], pair(-f.rest, -f.rest));
+  return f.r;
 }
 
 // x times a norm's r (offset + weight), plus its bias.
@@ -116,7 +124,7 @@ constexpr int block_threads(int t) { return t < 256 ? 256 : t; }
 template <typename S, int V, int T, int E>
 __global__ void __launch_bounds__(block_threads(T), (V == 2 ? 1536 : 1024) / block_threads(T))
     residual_norm_any_kernel(const ResidualNormParams p) {
-  __shared__ float part[2][32];
+  __shared__ float part[4][32];
   pdl_launch_dependents();
   pdl_wait_previous();
   const int64_t mine = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
@@ -167,7 +175,8 @@ __global__ void __launch_bounds__(block_threads(T), (V == 2 ? 1536 : 1024) / blo
   }
   if (!p.out) return;
   if (normed) {
-    if (p.block && p.post.kind != NM_NORM_NONE && p.post.bias) {  // (a bias left the places outside other than 0)
+    if (p.block && (p.post.kind == NM_NORM_LAYER || (p.post.kind == NM_NORM_RMS && p.post.bias))) {
+      // (a mean or a bias left the places outside other than 0)
 #pragma unroll
       for (int k = 0; k < E; ++k) s[k] = pair(acc.in(k, 0) ? s[k].x : 0.f, acc.in(k, 1) ? s[k].y : 0.f);
     }

@@ -364,6 +364,52 @@ def test_norm_rows_of_nothing_and_spoilt_rows(nm):
         assert torch.equal(out[r], clean[r]) and torch.equal(s[r], clean_s[r])
 
 
+# (tokens, width): a row a block, blocks that stay with one and two groups a thread, two and
+# four groups a thread, element by element one and two at a time, shifted groups
+NORM_KERNELS = [(3, 1792), (900, 1792), (1200, 1536), (2, 12288), (2, 24576), (5, 777), (4, 5121), (6, 1002),
+                (3, 13000), (2, 30001), (2, 32767)]
+
+
+@pytest.mark.parametrize("tokens,width", NORM_KERNELS)
+@pytest.mark.parametrize("stream", [torch.float16, torch.float32], ids=["fp16", "fp32"])
+def test_layer_norm_of_equal_elements_is_its_bias(nm, tokens, width, stream):
+    """A row without deviation, at values where a mean that is one rounding off would count
+    against eps.  The mean of x is off by 48 E |x| at most (see layer_ref), the mean of what
+    is left of x by 50 E of that, and 1 / sqrt(var + eps) is at most eps^-1/2."""
+    values = torch.tensor([1000.0, 30016.0, -60000.0, 1001.0, 0.1, 0.0, -3.3], dtype=torch.float16, device="cuda")
+    if stream == torch.float32:
+        values = values.float() * 1.2345678
+    x = values[torch.arange(tokens, device="cuda") % 7]
+    for post in (False, True):
+        n = Norm(tokens, width, None if post else "layer", "layer" if post else None, None, stream, block=post,
+                 bias=True, seed=width)
+        n.residual.copy_(x[:, None].expand(tokens, width) * (0 if post else 1))
+        if post:
+            x = x.clamp(-65504, 65504).half()
+            n.block.copy_(x[:, None].expand(tokens, width))
+        out, s = n.run(nm)
+        w, b = (n.kw["post_weight"], n.kw["post_bias"]) if post else (n.kw["weight"], n.kw["bias"])
+        want = b.double().expand(tokens, width)
+        err = 48 * 50 * ref.E ** 2 * x.double().abs()[:, None] * 1e3 * w.double().abs() + 2 * ref.E * want.abs()
+        within(s if post else out, ref.half(want, err), f"post={post}")
+
+
+@pytest.mark.parametrize("tokens,width", NORM_KERNELS)
+def test_layer_norm_far_from_zero(nm, tokens, width):
+    """Deviations of 1 about a mean of 30000: x - mean is exact, so that the norm is as
+    exact as about 0 (the bound of the test above, and 64 E of the value)."""
+    n = Norm(tokens, width, "layer", None, None, torch.float32, block=False, bias=True, seed=width)
+    n.residual.copy_(torch.randn((tokens, width), device="cuda", generator=generator(3)) + 30000.0)
+    out, _ = n.run(nm)
+    x = n.residual.double()
+    d = x - x.mean(1, keepdim=True)
+    r = torch.rsqrt(d.square().mean(1, keepdim=True) + 1e-6)
+    w = n.kw["weight"].double()
+    want = d * r * w + n.kw["bias"].double()
+    err = 48 * 50 * ref.E ** 2 * 31000 * r * w.abs() + 64 * ref.E * (want.abs() + (d * r * w).abs())
+    within(out, ref.half(want, err), "far")
+
+
 def test_norm_empty_and_alignment(nm):
     n = Norm(0, 64)
     out, s = n.run(nm)
