@@ -264,7 +264,10 @@ __global__ void __launch_bounds__(threads_for(DW), 1)
   // nothing: the decision is block-uniform, taken before any barrier, copy or
   // tensor-memory allocation.  (A cluster's blocks write each other's shared memory, so
   // none of them leaves before the others: their waits give up at once instead.)
-  if (gridDim.z == 1 && __syncthreads_or(threadIdx.x == 0 && wait_aborted())) return;
+  if (gridDim.z == 1 && __syncthreads_or(threadIdx.x == 0 && wait_aborted())) {
+    pdl_wait_previous();  // what follows on the stream is after the kernels before this one
+    return;
+  }
   const int64_t r0 = (int64_t)blockIdx.y * BM;
   const int64_t n0 = (int64_t)blockIdx.x * (NB * nmma);
   // K split: this block multiplies the mask words w0 .. w0 + nk - 1 (stage kt is word

@@ -107,3 +107,21 @@ def test_python_refuses_host_tensors_and_names(nm):
         nm.nm_linear(x, x, x, activation="tanh")
     with pytest.raises(TypeError):
         nm.nm_token_logprobs(7)
+
+
+def test_no_kernel_leaves_before_it_waited_for_the_one_before_it():
+    """A kernel that lets the next one start early and ends without having waited itself
+    would let that one read what the kernel before both still writes."""
+    import glob
+    import os
+    import re
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "sparse_spmv_memory_gb300", "csrc")
+    kernels = 0
+    for path in sorted(glob.glob(os.path.join(csrc, "*.cu*"))):
+        with open(path) as f:
+            code = re.sub(r"//[^\n]*", "", f.read())
+        for part in code.split("pdl_launch_dependents();")[1:]:
+            assert "pdl_wait_previous();" in part, path
+            kernels += 1
+            assert not re.search(r"\breturn\b", re.split(r"pdl_wait_previous\(\);", part)[0]), path
+    assert kernels >= 15
