@@ -78,6 +78,19 @@ int nm_linear(const void *values, const uint32_t *masks, int64_t rows, int64_t c
               int64_t ldx, int64_t tokens, const nm_epilogue *epilogue, void *Y, int64_t ldy,
               void *workspace, size_t workspace_bytes, void *stream);
 
+/* nm_linear_stall_selftest -- exercises the bounded waits of nm_linear's tensor-core
+ * kernel (a self-test, as those of nm_decode.h): nm_linear with every wait limited to
+ * wait_limit_us (1 .. 2,000,000, else NM_ERR_SHAPE), in which the weights of every other
+ * block never come (a call of up to 8 tokens runs as usual: its kernels have no waits).
+ * The waits run out, or give up after the first that did, are counted in
+ * nm_wait_timeouts(), and the kernel returns with Y undefined; the device stays usable.
+ * Until nm_wait_timeouts(1) calls of more than 8 tokens leave Y as it is.  Asynchronous;
+ * NM_OK once launched. */
+int nm_linear_stall_selftest(const void *values, const uint32_t *masks, int64_t rows, int64_t cols,
+                             const void *X, int64_t ldx, int64_t tokens,
+                             const nm_epilogue *epilogue, void *Y, int64_t ldy, void *workspace,
+                             size_t workspace_bytes, int64_t wait_limit_us, void *stream);
+
 /* ---------------------------------------------------------------------------
  * nm_residual_norm -- between two blocks of a layer:
  *     s = residual_scale * residual + scale * gate * post(block)

@@ -179,7 +179,7 @@ struct SpmmTcParams {
   int wslice = 0;           // mask words per slice (spmm_tc_slice_words)
   float* part = nullptr;    // fp32 [slices][T][rows] when slices > 1
   uint64_t wait_limit_ns = 0;  // bound of every in-kernel wait (0: the default)
-  int stall_weights = 0;       // self-test: the weight producer issues nothing
+  int stall_weights = 0;       // self-test: the weight producer (nm_linear: of every other block) issues nothing
   Epilogue epi;                // nm_linear only (launch_spmm_tc_linear), as the next
   int tile = 0;                // tokens of one MMA: a multiple of 16 up to the variant's most
 };

@@ -144,9 +144,10 @@ size_t nm_linear_workspace_bytes(int64_t rows, int64_t cols, int64_t tokens) {
   return pl.workspace;
 }
 
-int nm_linear(const void* values, const uint32_t* masks, int64_t rows, int64_t cols, const void* X,
-              int64_t ldx, int64_t tokens, const nm_epilogue* epilogue, void* Y, int64_t ldy,
-              void* workspace, size_t workspace_bytes, void* stream) {
+// nm_linear with the limit of the tensor-core kernel's waits and the self-test's stall.
+static int linear_call(const void* values, const uint32_t* masks, int64_t rows, int64_t cols, const void* X,
+                       int64_t ldx, int64_t tokens, const nm_epilogue* epilogue, void* Y, int64_t ldy,
+                       void* workspace, size_t workspace_bytes, void* stream, uint64_t wait_limit_ns, int stall) {
   if (!epilogue) return NM_ERR_NULL;
   if (rows != 0 && tokens != 0 && (!values || !masks || !X || !Y)) return NM_ERR_NULL;
   const nm_epilogue& e = *epilogue;
@@ -220,7 +221,24 @@ int nm_linear(const void* values, const uint32_t* masks, int64_t rows, int64_t c
   p.wslice = spmm_tc_slice_words(p.words, pl.tc.slices);
   p.epi = epi;
   p.tile = pl.tc.tile;
+  p.wait_limit_ns = wait_limit_ns;
+  p.stall_weights = stall;
   return status(launch_spmm_tc_linear(p, pl.tc.variant, s));
+}
+
+int nm_linear(const void* values, const uint32_t* masks, int64_t rows, int64_t cols, const void* X,
+              int64_t ldx, int64_t tokens, const nm_epilogue* epilogue, void* Y, int64_t ldy,
+              void* workspace, size_t workspace_bytes, void* stream) {
+  return linear_call(values, masks, rows, cols, X, ldx, tokens, epilogue, Y, ldy, workspace, workspace_bytes, stream,
+                     0, 0);
+}
+
+int nm_linear_stall_selftest(const void* values, const uint32_t* masks, int64_t rows, int64_t cols, const void* X,
+                             int64_t ldx, int64_t tokens, const nm_epilogue* epilogue, void* Y, int64_t ldy,
+                             void* workspace, size_t workspace_bytes, int64_t wait_limit_us, void* stream) {
+  if (wait_limit_us <= 0 || wait_limit_us > 2000000) return NM_ERR_SHAPE;
+  return linear_call(values, masks, rows, cols, X, ldx, tokens, epilogue, Y, ldy, workspace, workspace_bytes, stream,
+                     (uint64_t)wait_limit_us * 1000u, 1);
 }
 
 int nm_residual_norm(const void* residual, int stream_fp32, int64_t ldr, const void* block,

@@ -159,6 +159,33 @@ __device__ __forceinline__ void expand_32(uint32_t sA, uint32_t sV, uint32_t sM,
   }
 }
 
+// Waits of this kernel: mbar_wait with what follows a first test out of line (inlined at
+// each of them it is most of the kernel's code, and a block took 1 us longer).
+__device__ __noinline__ bool wait_late(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+  return mbar_wait(bar, parity, limit_ns);
+}
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+  return mbar_try_wait(bar, parity) || wait_late(bar, parity, limit_ns);
+}
+
+// For copies and MMAs that are on their way: they come, however short the limit of this
+// launch and whatever else gave up, so this has the default limit.  But a barrier of both
+// tokens and weights also counts the densify warps, which do not come any more once a wait
+// has given up: then the copies have a tenth of a second.
+constexpr uint64_t kDrainNs = 100000000;
+__device__ __noinline__ void landed_late(uint32_t bar, uint32_t parity) {
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, parity))
+    if ((int64_t)(global_timer_ns() - t0) > (int64_t)(wait_aborted() ? kDrainNs : kWaitLimitNs)) {
+      atomicAdd(&g_wait_timeouts, 1ull);
+      atomicExch(&g_wait_abort, 1u);
+      break;
+    }
+}
+__device__ __forceinline__ void landed(uint32_t bar, uint32_t parity) {
+  if (!mbar_try_wait(bar, parity)) landed_late(bar, parity);
+}
+
 // All threads of the cluster; those that have left count as there.
 __device__ __forceinline__ void cluster_sync() {
   __syncwarp();
@@ -242,7 +269,7 @@ __global__ void __launch_bounds__(threads_for(DW), 1)
     linear_tc_kernel(const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_x,
                      const __grid_constant__ CUtensorMap tm_m, const uint32_t* __restrict__ masks, __half* Y,
                      int64_t rows, int words, int wslice, int64_t T, int64_t ldy, uint64_t wait_limit_ns,
-                     const Epilogue e, int nmma) {
+                     int stall, const Epilogue e, int nmma) {
   using L = Shape<NMMA, NB, S, SV, DG, MS, MT>;
   constexpr int WPG = DW / DG;  // warps per densify group
   constexpr int RPW = BM / WPG;  // rows per warp and stage
@@ -261,19 +288,13 @@ __global__ void __launch_bounds__(threads_for(DW), 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_launch_dependents();
   // After a wait gave up (this launch or an earlier one not yet reset), the block does
-  // nothing: the decision is block-uniform, taken before any barrier, copy or
-  // tensor-memory allocation.  (A cluster's blocks write each other's shared memory, so
-  // none of them leaves before the others: their waits give up at once instead.)
-  if (gridDim.z == 1 && __syncthreads_or(threadIdx.x == 0 && wait_aborted())) {
-    pdl_wait_previous();  // what follows on the stream is after the kernels before this one
-    return;
-  }
+  // nothing: it has no stages, and no sums to send or to store.  It takes the way to the
+  // end all the same: a cluster's blocks write each other's shared memory, so none leaves
+  // before the others, and what follows on the stream is after the kernels before this
+  // one.  (The flag is there once the setup is done: a wait for it first costs 0.5 us.)
+  const bool aborted = threadIdx.x == 0 && wait_aborted();
   const int64_t r0 = (int64_t)blockIdx.y * BM;
   const int64_t n0 = (int64_t)blockIdx.x * (NB * nmma);
-  // K split: this block multiplies the mask words w0 .. w0 + nk - 1 (stage kt is word
-  // w0 + kt); w0 is a multiple of MW, so mask boxes stay aligned.
-  const int w0 = (int)blockIdx.z * wslice;
-  const int nk = min(words - w0, wslice);
 
   if (warp == 0 && lane == 0) {
     for (int k = 0; k < SV; ++k) {
@@ -293,18 +314,19 @@ __global__ void __launch_bounds__(threads_for(DW), 1)
     tmem_relinquish();
   }
   tc_fence_before_sync();
-  __syncthreads();
+  const bool dead = __syncthreads_or(aborted);
   tc_fence_after_sync();
+  // K split: this block multiplies the mask words w0 .. w0 + nk - 1 (stage kt is word
+  // w0 + kt); w0 is a multiple of MW, so mask boxes stay aligned.
+  const int w0 = (int)blockIdx.z * wslice;
+  const int nk = dead ? 0 : min(words - w0, wslice);
   uint32_t tmem_base;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem_base) : "r"(slot) : "memory");
   pdl_wait_previous();  // (everything above touches no argument's memory)
 
   // Before it ends, a producer waits (bounded) for its copies among a ring's last: shared
   // memory must not be given up, or written by the cluster, under copies in flight.  Each
-  // is the last use of its slot, whose use before it waited for.  (ready also counts the
-  // densify warps, which do not come any more once a wait has given up: then the copies
-  // have a tenth of a second a slot.)
-  constexpr uint64_t kDrainNs = 100000000;
+  // is the last use of its slot, whose use before it waited for.
   bool fine = false;  // (densify warps) the accumulator is whole
   if (warp == 0 || warp == tokens2_warp(DW)) {
     // ---- token tiles: the even stages, the odd ones --------------------------------
@@ -312,7 +334,7 @@ __global__ void __launch_bounds__(threads_for(DW), 1)
     if (lane == 0) {
       int last = -1;
       for (int kt = warp == 0 ? 0 : 1; kt < nk; kt += 2) {
-        if (kt >= S && !mbar_wait(done(kt - S), ((kt - S) / L::RD) & 1, wait_limit_ns)) break;
+        if (kt >= S && !wait(done(kt - S), ((kt - S) / L::RD) & 1, wait_limit_ns)) break;
         mbar_arrive_expect_tx(ready(kt), NB * nmma * ROW_BYTES);
 #pragma unroll
         for (int j = 0; j < NB; ++j)
@@ -320,19 +342,18 @@ __global__ void __launch_bounds__(threads_for(DW), 1)
                       (int)(n0 + j * nmma), ready(kt));
         last = kt;
       }
-      for (int kt = last; kt >= 0 && kt > last - S; kt -= 2)
-        if (!mbar_try_wait(ready(kt), (kt / S) & 1))
-          mbar_wait(ready(kt), (kt / S) & 1, wait_aborted() ? min(wait_limit_ns, kDrainNs) : wait_limit_ns, false);
+      for (int kt = last; kt >= 0 && kt > last - S; kt -= 2) landed(ready(kt), (kt / S) & 1);
     }
     __syncwarp();
   } else if (warp == 2) {
     // ---- compact values and mask words, a box of MW stages at a time ------------------
-    if (!MT || lane == 0) {
+    // (stall, the self-test's: every other block's issue nothing)
+    if ((!MT || lane == 0) && !(stall && (blockIdx.x + blockIdx.y + blockIdx.z) % 2 == 0)) {
       const int boxes = (nk + MW - 1) / MW;
       int last = -1;
       for (int box = 0; box < boxes; ++box) {
         int ok = 1;
-        if (box >= SV && lane == 0) ok = mbar_wait(vfree(box), (box / SV - 1) & 1, wait_limit_ns);
+        if (box >= SV && lane == 0) ok = wait(vfree(box), (box / SV - 1) & 1, wait_limit_ns);
         if (!MT) ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
         if (!ok) break;
         const int at = box % SV, w = w0 + box * MW;
@@ -356,7 +377,7 @@ __global__ void __launch_bounds__(threads_for(DW), 1)
       if (!MT) cp_async_wait_all();
       if (lane == 0)
         for (int box = last; box >= 0 && box > last - SV; --box)
-          mbar_wait(fullv(box), (box / SV) & 1, wait_limit_ns, false);
+          landed(fullv(box), (box / SV) & 1);
     }
     __syncwarp();
   } else if (warp == 1 || warp == mma2_warp(DW)) {
@@ -383,8 +404,12 @@ __global__ void __launch_bounds__(threads_for(DW), 1)
         if (around) i -= ring;
         return around ? 1u : 0u;
       };
+      bool gave_up = false;
       for (int kt = k0; kt < nk; kt += kStep) {
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait(ready(0) + 8u * at, phase, wait_limit_ns))) break;
+        if (!__all_sync(0xFFFFFFFFu, wait(ready(0) + 8u * at, phase, wait_limit_ns))) {
+          gave_up = true;
+          break;
+        }
         tc_fence_after_sync();
         const uint32_t al = a_low + (uint32_t)at * (A_BYTES / 16), bl = b_low + (uint32_t)at * (L::B_BYTES / 16);
         if (elect_one()) {
@@ -401,6 +426,7 @@ __global__ void __launch_bounds__(threads_for(DW), 1)
         next(id, L::RD);
       }
       if (elect_one()) mma_commit(accum);  // also after an early exit: completes once issued MMAs finish
+      if (gave_up) __nanosleep(200000);    // (arrivals in done that nobody waits for any more land meanwhile)
     };
     if (warp == 1)
       issue(std::integral_constant<int, 0>());
@@ -410,11 +436,11 @@ __global__ void __launch_bounds__(threads_for(DW), 1)
   } else {
     // ---- expansion of the weights ------------------------------------------------------
     const int dw = warp - FIRST_DENSIFY_WARP, grp = dw / WPG, wg = dw % WPG;
-    bool ok = true, bytes = true;
+    bool ok = !dead, bytes = true;
     for (int kt = grp; kt < nk; kt += DG) {
       const int box = kt / MW, at = box % SV;
-      bool got = mbar_wait(fullv(box), (box / SV) & 1, wait_limit_ns);
-      if (kt >= S) got = got && mbar_wait(done(kt - S), ((kt - S) / L::RD) & 1, wait_limit_ns);
+      bool got = wait(fullv(box), (box / SV) & 1, wait_limit_ns);
+      if (kt >= S) got = got && wait(done(kt - S), ((kt - S) / L::RD) & 1, wait_limit_ns);
       // The warp decides together, so no lane is left behind at a warp barrier.
       if (!__all_sync(0xFFFFFFFFu, got)) {
         ok = false;
@@ -433,7 +459,7 @@ __global__ void __launch_bounds__(threads_for(DW), 1)
         if (kt + DG >= MW * (box + 1)) mbar_arrive(vfree(box));  // its last stage in the box
       }
     }
-    if (!mbar_wait(accum, 0, wait_limit_ns)) ok = false;
+    if (!wait(accum, 0, wait_limit_ns)) ok = false;
     tc_fence_after_sync();
     // tcgen05.ld is a warp-wide instruction: the whole warp reads or none does.
     fine = __all_sync(0xFFFFFFFFu, ok);
@@ -523,7 +549,7 @@ __global__ void __launch_bounds__(threads_for(DW), 1)
   if (warp == 1) {
     // Tensor memory is freed only after the MMAs that write it have completed: one more
     // bounded (not abortable) wait on the final commit, which a normal run passed already.
-    mbar_wait(accum, 0, wait_limit_ns, false);
+    landed(accum, 0);
     tc_fence_after_sync();
     tmem_dealloc(tmem_base, L::TMEM_COLS);
   }
@@ -572,7 +598,8 @@ cudaError_t launch_mt(const SpmmTcParams& p, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = p.slices > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, k, tm_v, tm_x, tm_m, p.masks, p.Y, p.rows, p.words,
-                            p.slices > 1 ? p.wslice : p.words, p.T, p.ldy, (uint64_t)kWaitLimitNs, p.epi, p.tile);
+                            p.slices > 1 ? p.wslice : p.words, p.T, p.ldy, p.wait_limit_ns ? p.wait_limit_ns : kWaitLimitNs,
+                            p.stall_weights, p.epi, p.tile);
 }
 
 // Mask words by TMA when the mask array allows it (16-byte aligned, row pitch words * 4 a

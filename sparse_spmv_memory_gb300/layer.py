@@ -47,6 +47,8 @@ def declare(L) -> None:
                               I64, P], I32),
         "nm_token_logprobs": ([P, I32, I64, I64, I64, P, I64, I32, F32, P, P, I32, P, P, P], I32),
     }
+    args, res = sig["nm_linear"]  # the same and a limit, before the stream
+    sig["nm_linear_stall_selftest"] = (args[:-1] + [I64, P], res)
     for name, (args, res) in sig.items():
         f = getattr(L, name)
         f.argtypes = args

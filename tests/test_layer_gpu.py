@@ -610,6 +610,89 @@ def test_logprobs_empty_and_refusals(nm):
     refuses(lambda: nm.nm_token_logprobs(x, torch.zeros((4, 1025), dtype=torch.int32, device="cuda")), 2)
 
 
+# ---- waits that give up -------------------------------------------------------------------
+def stalled(nm, p, y, limit_us=20000, limit_s=4.0):
+    """nm_linear's self-test: half of the blocks get no weights; it ends soon and is counted."""
+    import time
+    from sparse_spmv_memory_gb300.layer import _Epilogue, ACTIVATIONS
+    k = p.kw
+    at = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    e = _Epilogue(bias=at(k["bias"]), residual=at(k["residual"]), ldres=p.n, activation=ACTIVATIONS[k["activation"]],
+                  gated=k["gated"], scale=k["scale"])
+    tokens, cols = p.x.shape
+    torch.cuda.synchronize()
+    nm.nm_wait_timeouts(reset=True)
+    t0 = time.time()
+    assert nm.lib().nm_linear_stall_selftest(at(p.values), at(p.masks), p.masks.shape[0], cols, at(p.x), p.x.stride(0),
+                                             tokens, ctypes.byref(e), at(y), y.stride(0), None, 0, limit_us,
+                                             torch.cuda.current_stream().cuda_stream) == 0
+    torch.cuda.synchronize()
+    assert time.time() - t0 < limit_s
+    assert nm.nm_wait_timeouts() > 0
+
+
+# tokens, rows, cols: every size of tile; the masks by TMA and by cp.async; K split over clusters
+STALLS = [(16, 128, 1024), (16, 300, 1056), (100, 1000, 4096), (200, 130, 2048), (300, 300, 1056), (520, 1000, 2080),
+          (16, 64, 28672), (300, 256, 16384), (12, 126, 14336 + 64), (600, 256, 8192)]
+
+
+@pytest.mark.parametrize("tokens,rows,cols", STALLS)
+def test_linear_wait_that_gives_up(nm, tokens, rows, cols):
+    p = Product(nm, rows, cols, tokens, (8, 16), "silu", True, True, True, seed=rows)
+    good = p.run(nm)
+    y = torch.empty_like(good)
+    stalled(nm, p, y)
+    # until the reset calls do nothing, all blocks of a cluster alike
+    y.fill_(7.0)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        p.run(nm, Y=y)
+    torch.cuda.synchronize()
+    assert bool((y == 7).all())
+    nm.nm_wait_timeouts(reset=True)
+    assert torch.equal(p.run(nm, Y=y), good)
+    assert nm.nm_wait_timeouts() == 0
+
+
+@pytest.mark.parametrize("tokens", [16, 128, 256, 300, 512])
+@pytest.mark.parametrize("rows,cols", [(57344, 4096), (256, 65536)])
+def test_linear_gives_up_with_copies_in_flight(nm, tokens, rows, cols):
+    """Half of the blocks give up soon; the others in the midst of their work, copies and
+    products in flight, those of a cluster too: they end as well, and the next call is right."""
+    p = Product(nm, rows, cols, tokens, (2, 4), seed=tokens)
+    good = p.run(nm)
+    y = torch.empty_like(good)
+    for limit in (1, 50, 500):
+        stalled(nm, p, y, limit)
+        nm.nm_wait_timeouts(reset=True)
+        assert torch.equal(p.run(nm, Y=y), good)
+        assert nm.nm_wait_timeouts() == 0
+
+
+@pytest.mark.parametrize("tokens,rows,cols", [(16, 128, 1024), (300, 256, 16384)])
+def test_a_call_that_does_nothing_still_keeps_the_order(nm, tokens, rows, cols):
+    """With the flag set nm_linear's blocks leave at once; what follows on the stream is
+    after what came before all the same: log probabilities from a long row, read by a norm."""
+    p = Product(nm, rows, cols, tokens, seed=1)
+    y = p.run(nm)
+    g = generator(2)
+    x = torch.randn((1, 1 << 24), device="cuda", generator=g)
+    ids = torch.randint(0, 1 << 24, (1, 1024), device="cuda", generator=g).to(torch.int32)
+    want = nm.nm_token_logprobs(x, ids)[0]
+    want_h, _ = nm.nm_residual_norm(want)
+    lp = torch.empty_like(want)
+    stalled(nm, p, y)
+    for _ in range(10):
+        lp.fill_(1.0)
+        nm.nm_token_logprobs(x, ids, logprob=lp)
+        p.run(nm, Y=y)
+        h, _ = nm.nm_residual_norm(lp)
+        assert torch.equal(h, want_h)
+    nm.nm_wait_timeouts(reset=True)
+    p.run(nm, Y=y)
+    assert nm.nm_wait_timeouts() == 0
+
+
 # ---- all of them ------------------------------------------------------------------------
 def calls(nm):
     g = generator(8)

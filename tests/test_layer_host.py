@@ -45,6 +45,13 @@ def test_linear(nm, kw, want):
     assert linear(nm, **kw) == want
 
 
+def test_linear_stall_selftest_refuses_a_limit_out_of_range(nm):
+    from sparse_spmv_memory_gb300.layer import _Epilogue
+    e = ctypes.byref(_Epilogue(bias=None, residual=None, ldres=0, activation=0, gated=0, scale=1.0))
+    for limit, want in ((0, SHAPE), (-1, SHAPE), (2000001, SHAPE), (20000, OK)):
+        assert nm.lib().nm_linear_stall_selftest(V, M, 0, 128, X, 128, 16, e, Y, 64, None, 0, limit, None) == want
+
+
 def norm(nm, pre=True, post=True, **kw):
     from sparse_spmv_memory_gb300.layer import _Norm
     n = dict(kind=1, params_fp32=0, weight=W, bias=None, offset=0.0, eps=1e-6)
