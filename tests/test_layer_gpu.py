@@ -325,6 +325,60 @@ def test_norm_rows_a_block(nm, tokens, width):
     Norm(tokens, width, "rms", "rms", "channel", seed=tokens).check(nm, f"{tokens}x{width}")
 
 
+# rows of whole 16-byte pieces, more than fit the SMs at once, on which blocks stay: one and two
+# groups a thread, one to eight rows a block, two to four stages
+MANY = [(5000, 256), (2600, 512), (1700, 768), (1300, 1024), (700, 1792), (170, 7936), (200, 8192)]
+
+
+@pytest.mark.parametrize("tokens,width", MANY)
+@pytest.mark.parametrize("stream", [torch.float16, torch.float32], ids=["fp16", "fp32"])
+def test_norm_many_rows(nm, tokens, width, stream):
+    assert tokens * (width // 8) > 1024 * torch.cuda.get_device_properties(0).multi_processor_count
+    k = 0
+    for norm in (None, "rms", "layer"):
+        for post in (None, "rms", "layer"):
+            for gate in (None, "channel", "token"):
+                k += 1
+                Norm(tokens, width, norm, post, gate, stream, params=(torch.float16, torch.float32)[k % 2],
+                     bias=k % 3 == 0, weight=k % 4 != 1, scale=(1.0, -0.4)[k // 2 % 2],
+                     residual_scale=(0.8, 1.0)[k // 3 % 2], offset=(0.0, 1.0)[k // 2 % 2], eps=(1e-6, 1e-3)[k % 2],
+                     pad=(0, 8, 24)[k % 3], seed=k).check(nm, f"{norm} {post} {gate} {k}")
+    for norm in ("rms", "layer"):
+        Norm(tokens, width, norm, stream=stream, block=False, bias=True, residual_scale=0.5,
+             seed=1).check(nm, f"{norm} alone, scaled")
+        n = Norm(tokens, width, norm, stream=stream, block=False, bias=norm == "layer", seed=2)
+        n.check(nm, f"{norm} alone")
+        assert n.run(nm)[1] is n.residual
+
+
+@pytest.mark.parametrize("tokens,width", MANY[1::2])
+@pytest.mark.parametrize("stream", [torch.float16, torch.float32], ids=["fp16", "fp32"])
+def test_norm_many_rows_in_place_and_spoilt(nm, tokens, width, stream):
+    n = Norm(tokens, width, "layer", "rms", "token", stream, bias=True, seed=2)
+    big, view = strided((tokens + 2, width), 16, generator(4), stream, spoil=55.0)
+    before = big.clone()
+    n.residual = view[1:tokens + 1].clone()
+    want_out, want = n.want()
+    n.residual = view[1:tokens + 1]
+    out, _ = n.run(nm, residual_out=n.residual)
+    within(n.residual, want, "in place")
+    within(out, want_out, "out")
+    clean, clean_s = out.clone(), n.residual.clone()
+    big[1:tokens + 1, :width] = before[1:tokens + 1, :width]
+    assert torch.equal(big, before)
+    # a row alone is spoilt by what it holds, and rows of nothing have their biases
+    n.residual[tokens // 2, 9] = NAN
+    n.block[tokens - 1, width - 1] = INF
+    n.block[3] = 0
+    out, s = n.run(nm)
+    assert torch.isnan(out[tokens // 2]).all() and torch.isnan(out[tokens - 1]).all()
+    rest = torch.ones(tokens, dtype=torch.bool, device="cuda")
+    rest[[3, tokens // 2, tokens - 1]] = False
+    assert torch.equal(out[rest], clean[rest]) and torch.equal(s[rest], clean_s[rest])
+    w = n.want()
+    within(out[3:4], (w[0][0][3:4], w[0][1][3:4]), "a row of nothing")
+
+
 def test_norm_without_block(nm):
     for stream in (torch.float16, torch.float32):
         n = Norm(7, 1024, stream=stream, block=False)
