@@ -240,7 +240,13 @@ def tensor_peak(seconds_timed: float):
         return FALLBACK_BF16_TFLOPS, "fallback 1900 TFLOP/s"
 
 
-def kernel_source_hash(names=("spmv.cu", "device.cuh", "split.cuh")) -> str:
+SPMV_SOURCES = ("spmv.cu", "spmv_kernels.cuh", "epilogue.cuh", "device.cuh", "split.cuh")
+PREFILL_SOURCES = ("prefill.cu", "tc.cuh", "tc_tiles.cuh", "device.cuh")
+SPMM_SOURCES = ("spmm.cu", "spmm_kernels.cuh", "spmm_variants.h", "spmm_b2.cu", "spmm_b4.cu",
+                "spmm_b6.cu", "spmm_b8.cu", "epilogue.cuh", "device.cuh", "split.cuh")
+
+
+def kernel_source_hash(names=SPMV_SOURCES) -> str:
     """Hash of the files that define a kernel's code (by default the SpMV
     kernels'); a committed ncu traffic record is used only while it matches."""
     h = hashlib.sha256()
@@ -248,11 +254,6 @@ def kernel_source_hash(names=("spmv.cu", "device.cuh", "split.cuh")) -> str:
         with open(os.path.join(ROOT, "sparse_spmv_memory_gb300", "csrc", name), "rb") as f:
             h.update(f.read())
     return h.hexdigest()[:16]
-
-
-PREFILL_SOURCES = ("prefill.cu", "tc.cuh", "device.cuh")
-SPMM_SOURCES = ("spmm.cu", "spmm_kernels.cuh", "spmm_variants.h", "spmm_b2.cu", "spmm_b4.cu",
-                "spmm_b6.cu", "spmm_b8.cu", "device.cuh", "split.cuh")
 
 
 def ncu_traffic(shape_key: str, record="nm_spmv_traffic.json", sources=None):

@@ -164,3 +164,17 @@ def test_clock_record_keeps_the_headline_window_apart(tmp_path):
     assert s["reasons"] == ["sw_power_cap"] and s["samples"] == 20
     h = s["headline_window"]
     assert h["reasons"] == [] and h["samples"] == 10 and h["sm_mhz"] == 2070.0
+
+
+@pytest.mark.parametrize("names", ["SPMV_SOURCES", "SPMM_SOURCES", "PREFILL_SOURCES"])
+def test_traffic_records_hash_all_of_a_kernels_code(names):
+    """The files that a traffic record's validity hangs on are closed under inclusion: the
+    device code of a kernel lies in .cu and .cuh files."""
+    import re
+    csrc = os.path.join(bench.ROOT, "sparse_spmv_memory_gb300", "csrc")
+    listed = getattr(bench, names)
+    for name in listed:
+        with open(os.path.join(csrc, name)) as f:
+            for inner in re.findall(r'#include "([^"/]+\.cuh)"', f.read()):
+                assert inner in listed, f"{name} includes {inner}"
+    assert any("__global__" in open(os.path.join(csrc, name)).read() for name in listed)
