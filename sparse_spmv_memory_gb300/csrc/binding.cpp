@@ -183,17 +183,23 @@ PyObject* wrapped(const Tensor* given, PyObject* given_o, Tensor& made) {
 
 // Several outputs of a call in one allocation, each at a multiple of 256 bytes: an
 // allocation costs about a microsecond on the GB300's host, as much as the rest of a
-// call's marshalling.
+// call's marshalling.  Whoever keeps one output then keeps the memory of all, so from
+// kShared bytes on, where the kernel takes as long as the call (5 us) and hides the
+// microsecond, each has an allocation of its own.
 struct Outputs {
-  Tensor whole;
+  static constexpr int64_t kShared = 16 << 20;
+  Tensor whole;  // (undefined: none)
+  at::TensorOptions like;
   int64_t used = 0;
 
-  explicit Outputs(int64_t bytes, const at::TensorOptions& like)
-      : whole(at::empty({bytes}, like.dtype(at::kByte))) {}
+  explicit Outputs(int64_t bytes, const at::TensorOptions& o) : like(o) {
+    if (bytes < kShared) whole = at::empty({bytes}, like.dtype(at::kByte));
+  }
 
   static int64_t room(int64_t bytes) { return (bytes + 255) / 256 * 256; }
 
   Tensor next(at::IntArrayRef sizes, at::ScalarType type) {
+    if (!whole.defined()) return at::empty(sizes, like.dtype(type));
     const caffe2::TypeMeta meta = c10::scalarTypeToTypeMeta(type);
     auto impl = c10::make_intrusive<c10::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(), meta);
     impl->set_storage_offset(used / (int64_t)meta.itemsize());

@@ -6,8 +6,9 @@ probabilities of tokens.
 As decode.py this is marshalling only, compiled (csrc/binding.cpp).  All tensors of a
 call are on one device, current or not.  ``stream`` is a torch.cuda.Stream or a raw
 cudaStream_t (None: that device's current one); outputs and workspaces that a call
-makes itself are allocated on that stream.  The operators are for inference: they
-have no gradients.
+makes itself are allocated on that stream.  Several outputs of a call that have less
+than 16 MiB together share one allocation (it lives as long as any of them; resizing or
+saving one concerns all).  The operators are for inference: they have no gradients.
 """
 from __future__ import annotations
 

@@ -664,6 +664,23 @@ def test_logprobs_empty_and_refusals(nm):
     refuses(lambda: nm.nm_token_logprobs(x, torch.zeros((4, 1025), dtype=torch.int32, device="cuda")), 2)
 
 
+def test_large_outputs_have_allocations_of_their_own(nm):
+    """Keeping one output of a call does not keep the others' memory, but for small ones."""
+    own = lambda t: t.untyped_storage().nbytes() == t.nbytes  # noqa: E731
+    for tokens, width, apart in ((64, 1024, False), (2048, 4096, True)):
+        for stream in (torch.float16, torch.float32):
+            n = Norm(tokens, width, stream=stream)
+            out, s = n.run(nm)
+            assert own(out) == own(s) == apart
+            n.check(nm, f"{tokens} {stream}")
+    x = torch.randn((4100, 1030), device="cuda")
+    ids = torch.randint(0, 1030, (4100, 1024), device="cuda").to(torch.int32)
+    for rows, apart in ((10, False), (4100, True)):
+        parts = nm.nm_token_logprobs(x[:rows], ids[:rows], top=3)
+        assert all(own(t) == apart for t in parts)
+        check_logprobs(nm, x[:rows], ids[:rows], 3, 1.0, f"{rows}")
+
+
 # ---- waits that give up -------------------------------------------------------------------
 def stalled(nm, p, y, limit_us=20000, limit_s=4.0):
     """nm_linear's self-test: half of the blocks get no weights; it ends soon and is counted."""
