@@ -8,6 +8,8 @@
 // common path has neither a branch nor a rescaling, and a loses no digits to t > 0.
 // Then, in the block:
 //  * the k-th largest (k = top, at least 1) of the warps' four largest thread maxima each
+//    (in rows too short for k of those, of all threads' maxima: 4096 of 1700, top 32, take
+//    64 us, and 315 without a bound, which lists the whole row)
 //    is not above the k-th largest element, and the threads whose maximum reaches it
 //    hold the k largest elements.  Those threads' chunks are read again (from L2), a
 //    chunk a thread; elements that reach it are listed, and an element's place among
@@ -422,9 +424,15 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) logprobs_kernel(const 
   }
   const Sums v = {kept.run.s.x + kept.run.s.y, kept.run.a.x + kept.run.a.y};
 
-  // a lower bound of the K-th largest key: the K-th of the warps' four largest
+  // a lower bound of the K-th largest key: the K-th of the warps' four largest, or of all
+  // threads' where those are fewer than K (short rows)
   const uint64_t key = kept.best_chunk >= 0 ? key_of(kept.best, (uint32_t)kept.best_chunk) : 0;
-  {
+  const int owners = f1 - f0;  // threads that have a whole chunk, and possibly 0 and 32
+  const bool by_threads = K > 4 * (owners / 32) + min(owners % 32, 4);
+  if (by_threads) {
+    sh.listed[threadIdx.x] = key;
+    if (threadIdx.x == 0) sh.bound = 0;
+  } else {
     uint64_t left = key;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -438,7 +446,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM) logprobs_kernel(const 
     sh.count = 0;
   }
   const bool spoilt = __syncthreads_or(v.s != v.s);
-  if (warp == 0) {
+  if (by_threads) {
+    const int place = larger(sh.listed, max(owners + 1, 34) & ~1, key);
+    if (key != 0 && place == K - 1) sh.bound = key;
+    if (key != 0 && place == 0) sh.head = key;
+  } else if (warp == 0) {
     uint64_t kth, head;
     kth_of(sh.top, lane, K, kth, head);
     if (lane == 0) {

@@ -628,6 +628,22 @@ def test_logprobs_large_and_equal_logits_at_small_temperatures(nm, dtype, rows, 
         check_logprobs(nm, x, ids, 4, t, f"{peak} {t}")
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32], ids=["fp16", "fp32"])
+@pytest.mark.parametrize("vocab", [16, 33, 90, 250, 257, 263, 270, 300, 511, 513, 1000, 1023, 1500, 1792, 1801, 2100])
+def test_logprobs_short_rows_with_many_alternatives(nm, vocab, dtype):
+    """Fewer warps than the alternatives need: the bound is then from all threads' largest."""
+    g = generator(vocab)
+    for off in (0, 3):
+        x = torch.randn((5, vocab + 3), device="cuda", generator=g).to(dtype)
+        x[1] = x[1].round()
+        x[2, 10:] = -INF
+        x[3, vocab // 2:] = 9.0
+        x = x[:, off:off + vocab]
+        for top in (1, 4, 5, 8, 12, 16, 20, 31, 32):
+            if top <= vocab:
+                check_logprobs(nm, x, x.argmin(1).to(torch.int32), top, 1.0, f"{vocab} {top} {off}")
+
+
 def test_logprobs_many_ids_and_alignment(nm):
     g = generator(4)
     base = torch.randn(40 * 1001 + 16, device="cuda", generator=g)
