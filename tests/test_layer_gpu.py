@@ -697,6 +697,91 @@ def test_large_outputs_have_allocations_of_their_own(nm):
         check_logprobs(nm, x[:rows], ids[:rows], 3, 1.0, f"{rows}")
 
 
+# ---- calls that the documentation allows ---------------------------------------------------
+@pytest.mark.parametrize("tokens", [1, 2, 8, 9, 40, 300])
+def test_linear_first_columns_of_wider_rows(nm, tokens):
+    """``cols``: X is wider than the matrix; what lies behind is not used."""
+    p = Product(nm, 70, 96, tokens, act="relu", bias=True, seed=tokens)
+    x = torch.full((tokens, 160), NAN, device="cuda").half()
+    x[:, :96] = p.x
+    y = nm.nm_linear(p.values, p.masks, x, cols=96, **p.kw)
+    within(y, p.want(), "wider")
+    if tokens == 1:  # rows of any width, since there is no next one
+        x = torch.full((1, 101), NAN, device="cuda").half()
+        x[:, :96] = p.x
+        within(nm.nm_linear(p.values, p.masks, x, cols=96, **p.kw), p.want(), "odd width")
+
+
+def test_linear_outputs_beyond_32_bits(nm):
+    """Outputs and residuals whose offsets pass 2^31 elements, 9 and more tokens and 8."""
+    g = generator(1)
+    for tokens, rows, ld in ((40000, 57344, 57344), (8, 64, 300000008), (20, 64, 120000008)):
+        p = Product(nm, rows, 32, tokens, (4, 8), bias=True, seed=rows)
+        y = torch.empty((tokens - 1) * ld + rows, dtype=torch.float16, device="cuda").as_strided((tokens, rows), (ld, 1))
+        p.kw["residual"] = torch.randn((tokens, rows), device="cuda", generator=g).half()
+        p.run(nm, Y=y)
+        for a, b in ((0, 4), (tokens // 2, tokens // 2 + 3), (tokens - 5, tokens)):
+            q = Product(nm, 1, 32, 1)
+            q.values, q.masks, q.x = p.values, p.masks, p.x[a:b]
+            q.kw = {**p.kw, "residual": p.kw["residual"][a:b]}
+            within(y[a:b], q.want(), f"{tokens} {a}")
+        del y
+
+
+def test_norm_and_logprobs_beyond_32_bits(nm):
+    for width in (8192, 8190, 30001):
+        tokens = 2 ** 31 // width + 40
+        for stream in (torch.float16, torch.float32):
+            n = Norm(tokens, width, "layer", "rms", "token", stream)
+            out, s = n.run(nm, residual_out=n.residual.clone())
+            for a, b in ((0, 3), (tokens - 70, tokens)):
+                m = Norm(1, 1)
+                m.residual, m.block, m.kw = n.residual[a:b], n.block[a:b], {**n.kw, "gate": n.kw["gate"][a:b]}
+                want_out, want_s = m.want()
+                within(out[a:b], want_out, f"{width} {a} out")
+                within(s[a:b], want_s, f"{width} {a} stream")
+            del n, out, s
+    rows, vocab = 2 ** 31 // 50257 + 30, 50257
+    for dtype in (torch.float16, torch.float32):
+        x = torch.randn((rows, vocab), dtype=dtype, device="cuda", generator=generator(5))
+        ids = torch.arange(rows, device="cuda").to(torch.int32)[:, None] % vocab
+        parts = nm.nm_token_logprobs(x, ids, top=6)
+        for a, b in ((0, 3), (rows - 50, rows)):
+            w = ref.logprobs(x[a:b], ids[a:b], 6, 1.0)
+            assert torch.equal(parts[2][a:b], w[2])
+            for got, want in ((parts[0], w[0]), (parts[1], w[1]), (parts[3], w[3])):
+                within(got[a:b], want, f"{dtype} {a}")
+        del x
+
+
+def test_logprobs_many_ids_of_few_rows_and_the_longest(nm):
+    """Ids beyond a block's threads where a row is split, the same id twice; 2^24 logits."""
+    for rows, vocab in ((1, 128256), (3, 1 << 24)):
+        for dtype in (torch.float16, torch.float32):
+            x = torch.randn((rows, vocab), device="cuda", generator=generator(rows)).to(dtype)
+            ids = torch.randint(-3, vocab + 3, (rows, 1024), device="cuda", generator=generator(7)).to(torch.int32)
+            ids[:, 500:600] = ids[:, :100]
+            check_logprobs(nm, x, ids, 32, 0.5, f"{rows}x{vocab}")
+
+
+def test_calls_under_inference_mode_and_of_parameters(nm):
+    """Outputs of calls in inference mode are usable after it, and gradients are not asked for."""
+    n = Norm(5, 512)
+    out, s = n.run(nm)
+    x = torch.randn((3, 500), device="cuda")
+    want = nm.nm_token_logprobs(x, top=2)
+    with torch.inference_mode():
+        out2, s2 = n.run(nm)
+        got = nm.nm_token_logprobs(x, top=2)
+        assert torch.equal(out2 + 0, out)
+    assert torch.equal(out2, out) and torch.equal(s2, s) and same(got, want)
+    n.kw["weight"] = torch.nn.Parameter(n.kw["weight"])
+    out3, s3 = n.run(nm)
+    assert not out3.requires_grad and torch.equal(out3, out)
+    out3.mul_(2)  # an ordinary tensor, apart from the other output
+    assert torch.equal(s3, s)
+
+
 # ---- waits that give up -------------------------------------------------------------------
 def stalled(nm, p, y, limit_us=20000, limit_s=4.0):
     """nm_linear's self-test: half of the blocks get no weights; it ends soon and is counted."""
