@@ -464,7 +464,7 @@ PyObject* residual_norm(PyObject* const* a) {
   const int64_t ldb = block ? half_rows(*block, tokens, width, "block") : 0;
   int64_t ldg = 0;
   if (gate) {
-    if (gate->dim() == 1 || gate->size(0) != tokens || tokens == 1)
+    if (gate->dim() < 2 || gate->size(0) != tokens || tokens == 1)
       vector(gate, at::kHalf, width, "gate");  // one for all tokens
     else
       ldg = half_rows(*gate, tokens, width, "gate");

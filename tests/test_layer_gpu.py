@@ -475,6 +475,13 @@ def test_norm_empty_and_alignment(nm):
         n.check(nm, f"offset {off}")
 
 
+def test_norm_refuses_a_gate_without_dimensions(nm):
+    n = Norm(4, 64)
+    for gate in (torch.ones((), device="cuda").half(), torch.ones((4, 64, 1), device="cuda").half()):
+        with pytest.raises(ValueError):
+            n.run(nm, gate=gate)
+
+
 def test_norm_refusals(nm):
     n = Norm(4, 64, "rms", "rms", "token")
     refuses(lambda: n.run(nm, norm="group"))
