@@ -11,8 +11,10 @@
  * Conventions, status codes and stream behaviour are nm_spmv.h's: the caller
  * owns every buffer, nothing is allocated, calls enqueue on `stream` and
  * return; arguments are checked on the host before anything is launched, among
- * them that what a call writes meets nothing that it reads (NM_ERR_ALIAS),
- * but for the buffers that a call says may be the same.  Launches use
+ * them that what a call writes meets nothing that it reads (NM_ERR_ALIAS; an array
+ * counts from its first element to its last, with what lies between its rows, so
+ * column blocks of one matrix meet), but for the buffers that a call says may be the
+ * same.  Launches use
  * programmatic dependent launch; every kernel waits for the previous one on
  * the stream before it touches any buffer.  No call uses floating-point atomics:
  * the same inputs give the same bits.  These are inference operators: the
@@ -53,8 +55,9 @@ extern "C" {
  * arithmetic, more on a tensor-core kernel of its own (fp16 products, fp32 sums; up
  * to 8 tokens pruned weights are never multiplied; beyond, a non-finite X[t][c]
  * reaches every row of its token).  The summation order is fixed for a shape and
- * device.  Only 2..8 tokens of few rows or long columns need the workspace.  The
- * tensor-core kernel's bounded waits count in nm_wait_timeouts.
+ * device.  The workspace is needed for 1..8 tokens of rows so long that their x tile,
+ * or what it leaves for the rows' sums, does not fit a block's shared memory: columns
+ * are cut then.  The tensor-core kernel's bounded waits count in nm_wait_timeouts.
  * rows == 0 or tokens == 0 is a no-op.  tokens < 2^31, rows < 2^31 and beyond 8
  * tokens ceil(rows / 128) <= 65535, else NM_ERR_SHAPE.
  * ------------------------------------------------------------------------- */
@@ -110,7 +113,9 @@ int nm_linear_stall_selftest(const void *values, const uint32_t *masks, int64_t 
  *              address and row stride); NULL: not written.
  *   out      : device fp16 [tokens][ldo]; NULL: pre is not computed.
  * All arithmetic is fp32, out is computed from the unrounded s, and each output
- * is rounded once.  Rows are independent: a non-finite value spoils its row alone.
+ * is rounded once.  (Squares are fp32 too: an element beyond 2^63 has an infinite
+ * one.  Where rows are many, weight, gate and scale are multiplied before the block's
+ * values.)  Rows are independent: a non-finite value spoils its row alone.
  * Any strides and alignment of the elements' size; 16-byte aligned rows are
  * fastest.  tokens == 0 is a no-op; tokens < 2^31, width 1 .. 32768, row strides
  * >= width, eps >= 0 and finite; scale, residual_scale and offsets finite, else

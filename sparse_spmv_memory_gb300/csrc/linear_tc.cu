@@ -679,8 +679,8 @@ LinearTcPlan linear_tc_plan(int64_t rows, int words, int64_t tokens, int sms) {
   return best;
 }
 
-// ---- nm_linear for 2 .. 8 tokens, whose columns are split when the rows are few: the
-// partial sums that nm_spmm's kernel leaves are added and finished here.  V rows a thread
+// ---- nm_linear for 1 .. 8 tokens of rows too long for a block's shared memory, whose
+// columns are cut: the partial sums that nm_spmm's kernel leaves are added and finished here.  V rows a thread
 // (an even number of them where rows come in pairs): V = 4 takes 16-byte loads of the
 // partial sums, which need rows % 4 == 0; V = 2 serves any even number of rows, V = 1 the
 // rest.

@@ -294,8 +294,9 @@ __global__ void __launch_bounds__(1024) residual_norm_few_kernel(const ResidualN
 // row two conversions and about seven operations on both of two elements; and the
 // next rows' stream, block and gate are on their way to shared memory meanwhile, each
 // thread's own groups to slots of its own (no barrier).  4096 rows of 8192 with both
-// norms and a gate: 49 us (5.5 TB/s), with layer norms 82; a block a row, with the parameters
-// read for every row, took 55 for the 49, half of it issuing instructions and half waiting for a row's loads.
+// norms and a gate: 49 us (5.5 TB/s), with layer norms 82; a block a row, with the
+// parameters read for every row, took 55 (RMS norms), half of it issuing instructions and
+// half waiting for a row's loads.
 __device__ __forceinline__ void copy_async(uint4* to, const void* from) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(to)), "l"(from) : "memory");
 }
@@ -780,8 +781,8 @@ cudaError_t launch_stream(const ResidualNormParams& p, const DeviceInfo& d, cuda
       return launch_rows(residual_norm_few_kernel<S, 4>, p, groups / 4, stream);
   }
   // Other rows element by element up to 8192 accesses of a row, else by shifted groups:
-  // 777 rows of 5121 (fp32 stream, layer norms) 22.5 us for 24.8, 16384 of 100 5.8 for
-  // 17.8; 2000 of 30001 180 for 314.
+  // 777 rows of 5121 (fp32 stream, layer norms) 22.5 us for 24.8 when it was chosen (25.0
+  // now, with the mean corrected), 16384 of 100 5.8 for 17.8; 2000 of 30001 180 for 314.
   if (takes_any_rows(p, sizeof(S) == 4)) return launch_any_rows(p, sizeof(S) == 4, stream);
   const int groups = (p.width + 14) / 8;  // with a start anywhere in a piece
   if (groups <= 2048) return launch_long<S, 4, 512>(p, groups, stream);

@@ -1,7 +1,7 @@
 // spmv_linear.cu -- nm_linear's one-token products: nm_spmv's kernels with the
 // general epilogue, in the variants that the default plans take.  HBM bounds them:
 // 57344 x 8192 gated 78 to 80 us (the product alone 77 to 79), 4096 x 4096 with a
-// residual 5.4 (4.9: the sums go through shared memory once more).
+// residual 5.4 to 5.9 (4.9: the sums go through shared memory once more).
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
