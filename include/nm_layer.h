@@ -58,6 +58,8 @@ extern "C" {
  * device.  The workspace is needed for 1..8 tokens of rows so long that their x tile,
  * or what it leaves for the rows' sums, does not fit a block's shared memory: columns
  * are cut then.  The tensor-core kernel's bounded waits count in nm_wait_timeouts.
+ * (For 2:4 matrices and 6..8 tokens nm_spmm24 is the faster product, without an
+ * epilogue.)
  * rows == 0 or tokens == 0 is a no-op.  tokens < 2^31, rows < 2^31 and beyond 8
  * tokens ceil(rows / 128) <= 65535, else NM_ERR_SHAPE.
  * ------------------------------------------------------------------------- */
